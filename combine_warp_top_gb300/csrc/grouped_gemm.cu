@@ -512,6 +512,24 @@ bool map_3d(CUtensorMap* m, const void* ptr, uint64_t E, uint64_t rows, uint64_t
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Any tiled map of 2 or 3 dimensions (innermost first) over a dense array.
+bool map_tiled(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, int rank, const void* ptr,
+               const uint64_t* sizes, const uint32_t* boxes, CUtensorMapSwizzle swizzle) {
+    auto enc = encode_fn();
+    if (!enc || rank < 2 || rank > 3) return false;
+    cuuint64_t dims[3], strides[2];
+    cuuint32_t box[3], estr[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        dims[i] = sizes[i];
+        box[i] = boxes[i];
+    }
+    strides[0] = sizes[0] * (uint64_t)elem_bytes;
+    strides[1] = strides[0] * sizes[1];
+    return enc(m, type, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Map over packed weights (E experts x n_blocks n-blocks x ceil(K/64) k-blocks
 // of 256 x 64 bf16) as a [rows, 64] matrix; box = box_rows rows.  *second is
 // set to the same map (the kernels take a second B map for row-major up

@@ -1,0 +1,667 @@
+// Matrix products grouped by expert over ragged row segments, and their
+// gradients (tcgen05 cta_group::2).  With the rows of expert e a segment of R
+// expert-major rows and W[e] its [C_out, C_in] matrix:
+//
+//   forward          out[i, :]   = rows[i, :] W[e]^T          contracts C_in
+//   rows' gradient   drows[i, :] = dout[i, :] W[e]            contracts C_out
+//   weights' grad.   dW[e]       = sum_{i in e} dout[i, :]^T rows[i, :]
+//                                                             contracts the rows
+//
+// One persistent kernel on 256 x 256 output tiles that a CTA pair shares.  All
+// operands stay in their row-major layout: where a contraction runs along the
+// rows of a matrix (W in the rows' gradient, both operands in the weights'
+// gradient) TMA brings boxes of 64 columns x 64 rows and the matrix and
+// instruction descriptors name the operand MN-major, so nothing is transposed
+// or copied.
+//
+// The contraction of a weights' gradient ends inside a 64-row block where the
+// expert's segment ends.  The MMA stops at the next 16 rows, and the rows
+// between the segment's end and there (the next expert's, or anything past the
+// last) are zeroed in shared memory by a warp of its own before the MMA may
+// read the block: for that block the copies complete on a barrier of their
+// CTA, and each CTA's warp arrives on the leader's full barrier in the
+// producer's place.  Both operands are zeroed, so no value of a neighbouring
+// segment, NaN included, reaches a product.  An expert with no rows gets zeros.
+//
+// Precision: the tensor core adds into its fp32 accumulator with truncation,
+// which over a contraction of 4096 random bf16 products is a relative error of
+// 4e-6 (measured; 1e-6 over 1024, 2e-7 over 256; grows with the length), all of it
+// towards zero.  That is far below the rounding of a bf16 output, but not of an
+// fp32 one: fp32 outputs take at most kChainBlocks k-blocks (512 terms) into
+// one accumulator and add those partial sums in fp32 registers, rounding to
+// nearest, in a fixed order.  The epilogue has 8 warps of 128 running sums a
+// thread for it, drawn from the registers that the other warps give up.
+//
+// Roles per CTA (384 threads): warp 0 loads by TMA; warp 1 owns TMEM and, in
+// the leader, issues the MMAs; warp 2 of the leader hands out tiles; warp 3
+// zeroes block ends (weights' gradient); warps 4-11 drain the accumulators,
+// two warps to each 32 rows (128 columns each).  Every wait is bounded.
+#include "../../include/moe_train.h"
+#include "api_checks.cuh"
+#include "moe_internal.cuh"
+#include "pair_queue.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+
+enum Mode { kForward, kRowsGrad, kWeightsGrad };
+
+constexpr int BT = 256;    // rows and columns of a pair's tile
+constexpr int BH = 128;    // rows of A and of B that a CTA of the pair holds
+constexpr int BK = 64;
+constexpr int UMMA_K = 16;
+constexpr int kStages = 6;
+constexpr int kAccs = 2;
+constexpr int kTmemCols = BT * kAccs;
+constexpr int OP_BYTES = BH * BK * 2;   // one operand of one stage in one CTA
+constexpr int BOX_BYTES = OP_BYTES / 2;  // an MN-major box: 64 columns x 64 rows
+constexpr int STAGE_BYTES = 2 * OP_BYTES;
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarps = 8;
+constexpr int kEpilogueCols = BT / 2;  // columns of one epilogue warp
+// Registers a thread: 384 x 168 at launch = 128 x 72 + 256 x 208 + 2048 to spare.
+constexpr int kRegsOther = 72, kRegsEpilogue = 208;
+// Output staging of an epilogue warp: 32 rows of 64 bytes, 64-byte swizzle.
+constexpr int kSliceBytes = 64;
+constexpr int kStagingBytes = 32 * kSliceBytes;
+constexpr int kChainBlocks = 8;  // k-blocks added up in one accumulator (fp32 outputs)
+
+struct Ctl {
+    uint64_t full[kStages];   // leader: both CTAs' operands of a stage are there
+    uint64_t empty[kStages];  // each CTA: its stage may be refilled
+    uint64_t land[kStages];   // each CTA: its copies of a segment's last block have landed
+    uint64_t tfull[kAccs];    // each CTA: accumulator ready
+    uint64_t tempty[kAccs];   // leader: accumulator drained by both CTAs
+    uint64_t done;            // leader: every issued MMA retired
+    uint64_t tq_full[kQ];     // tile queues: pair_queue.cuh
+    uint64_t tq_empty[kQ];
+    int tile_q[kQ];
+    uint64_t tq_taken[kQ];
+    uint64_t lq_full[kQ];
+    uint64_t lq_empty[kQ];
+    int local_q[kQ];
+    uint32_t tmem_base;
+    int abort;
+    int prefix[kMaxE + 1];
+    int offs[kMaxE];
+    int cnts[kMaxE];
+};
+
+constexpr size_t kCtlBytes = (sizeof(Ctl) + 15) & ~size_t(15);
+constexpr size_t kSmemBytes = 1024 + (size_t)kStages * STAGE_BYTES +
+                              (size_t)kEpilogueWarps * kStagingBytes + kCtlBytes;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of one block");
+
+// A tile: its expert, its row and column block, and the k-blocks of its contraction.
+struct Tile {
+    int e, mb, nb, kblocks;
+};
+
+template <int kMode>
+__device__ __forceinline__ Tile tile_of(const Ctl* ctl, int E, int MB, int NB, int KB, int tile) {
+    Tile t;
+    if (kMode == kWeightsGrad) {
+        t.e = tile / (MB * NB);
+        const int local = tile - t.e * MB * NB;
+        t.mb = local / NB;
+        t.nb = local - t.mb * NB;
+        t.kblocks = (ctl->cnts[t.e] + BK - 1) / BK;
+    } else {
+        decode_tile(ctl->prefix, E, NB, BT, BT, tile, t.e, t.mb, t.nb);
+        t.kblocks = KB;
+    }
+    return t;
+}
+
+// kMode, and for kWeightsGrad K unused, m_out x n_out = C_out x C_in; otherwise
+// K the contraction and n_out the columns of out.  chain: k-blocks per
+// accumulator.
+template <int kMode, typename OutT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    grouped_product_kernel(const __grid_constant__ CUtensorMap tmA,
+                           const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmOut,
+                           const int32_t* __restrict__ expert_offsets,
+                           const int32_t* __restrict__ expert_counts, int E, int R, int K,
+                           int m_out, int n_out, OutT* __restrict__ out, int chain,
+                           int accumulate, int* err, int* tile_counter) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t* tiles = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+    const uint32_t tiles_addr = smem_u32(tiles);
+    uint8_t* staging_area = tiles + (size_t)kStages * STAGE_BYTES;
+    Ctl* ctl = reinterpret_cast<Ctl*>(staging_area + (size_t)kEpilogueWarps * kStagingBytes);
+    volatile int* abort_flag = &ctl->abort;
+
+    constexpr bool kW = kMode == kWeightsGrad;
+    constexpr bool kMnA = kW;                 // the contraction runs along A's rows
+    constexpr bool kMnB = kMode != kForward;  // and along B's
+    // readers of a slot of the leader's queue: its producer, MMA thread,
+    // epilogue warps (and block-end warp), and the peer's producer
+    constexpr int kLocalReaders = kEpilogueWarps + (kW ? 1 : 0);
+    constexpr int kQueueReaders = kLocalReaders + 3;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();  // 0 = leader
+    const bool leader = rank == 0;
+    const int MB = (m_out + BT - 1) / BT;
+    const int NB = (n_out + BT - 1) / BT;
+    const int KB = (K + BK - 1) / BK;
+
+    for (int i = threadIdx.x; i < E; i += blockDim.x) {
+        int off = expert_offsets[i], cnt = expert_counts[i];
+        if (off < 0 || cnt < 0 || cnt > R || off > R - cnt) {
+            // a segment outside the rows is reported and left out
+            set_error(err, MOE_ERR_INVALID_ARG);
+            off = cnt = 0;
+        }
+        ctl->offs[i] = off;
+        ctl->cnts[i] = cnt;
+    }
+    __syncthreads();
+    if (!kW && warp == 4) warp_mblk_prefix(ctl->cnts, E, BT, ctl->prefix);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&ctl->full[s]), kW ? 2 : 1);
+            mbar_init(smem_u32(&ctl->empty[s]), 1);
+            mbar_init(smem_u32(&ctl->land[s]), 1);
+        }
+        for (int a = 0; a < kAccs; ++a) {
+            mbar_init(smem_u32(&ctl->tfull[a]), 1);
+            mbar_init(smem_u32(&ctl->tempty[a]), 2 * kEpilogueWarps);
+        }
+        mbar_init(smem_u32(&ctl->done), 1);
+        for (int q = 0; q < kQ; ++q) {
+            mbar_init(smem_u32(&ctl->tq_full[q]), 1);
+            mbar_init(smem_u32(&ctl->tq_empty[q]), kQueueReaders);
+            mbar_init(smem_u32(&ctl->tq_taken[q]), 1);
+            mbar_init(smem_u32(&ctl->lq_full[q]), 1);
+            mbar_init(smem_u32(&ctl->lq_empty[q]), kLocalReaders);
+        }
+        ctl->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_map(&tmA);
+        prefetch_map(&tmB);
+        prefetch_map(&tmOut);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&ctl->tmem_base), kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before any remote signal
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    const int total = kW ? E * MB * NB : ctl->prefix[E] * NB;
+
+    if (warp < 4) {
+        regs_shrink<kRegsOther>();
+        if (warp == 0 && lane == 0) {
+            // ---------------- TMA producer (both CTAs) ----------------
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                int tile = queue_take(ctl, i, leader, abort_flag, err);
+                if (leader && tile != -2) mbar_arrive(smem_u32(&ctl->tq_taken[i % kQ]));
+                if (!leader && tile != -2 && !local_publish(ctl, i, tile, abort_flag, err))
+                    tile = -2;
+                if (tile < 0) break;
+                const Tile t = tile_of<kMode>(ctl, E, MB, NB, KB, tile);
+                const int off = ctl->offs[t.e];
+                const bool ragged = kW && (ctl->cnts[t.e] % UMMA_K) != 0;
+                // this CTA's half of A's rows and of B's
+                const int a0 = t.mb * BT + (int)rank * BH;
+                const int b0 = t.nb * BT + (int)rank * BH;
+                for (int kb = 0; kb < t.kblocks; ++kb) {
+                    if (!wait_bar(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full_local = smem_u32(&ctl->full[stage]);
+                    const uint32_t a_s = tiles_addr + stage * STAGE_BYTES;
+                    const uint32_t b_s = a_s + OP_BYTES;
+                    if (kW) {
+                        const int row = off + kb * BK;
+                        if (ragged && kb == t.kblocks - 1) {
+                            const uint32_t land = smem_u32(&ctl->land[stage]);
+                            mbar_expect_tx(land, STAGE_BYTES);
+                            tma_load_2d(a_s, &tmA, land, a0, row);
+                            tma_load_2d(a_s + BOX_BYTES, &tmA, land, a0 + 64, row);
+                            tma_load_2d(b_s, &tmB, land, b0, row);
+                            tma_load_2d(b_s + BOX_BYTES, &tmB, land, b0 + 64, row);
+                        } else {
+                            const uint32_t full = mapa_shared(full_local, 0);
+                            if (leader) {
+                                mbar_arrive(full_local);
+                                mbar_expect_tx(full_local, 2 * STAGE_BYTES);
+                            }
+                            tma_load_2d_pair(a_s, &tmA, full, a0, row);
+                            tma_load_2d_pair(a_s + BOX_BYTES, &tmA, full, a0 + 64, row);
+                            tma_load_2d_pair(b_s, &tmB, full, b0, row);
+                            tma_load_2d_pair(b_s + BOX_BYTES, &tmB, full, b0 + 64, row);
+                        }
+                    } else {
+                        const uint32_t full = mapa_shared(full_local, 0);
+                        if (leader) mbar_expect_tx(full_local, 2 * STAGE_BYTES);
+                        tma_load_2d_pair(a_s, &tmA, full, kb * BK, off + a0);
+                        if (kMnB) {
+                            tma_load_3d_pair(b_s, &tmB, full, b0, kb * BK, t.e);
+                            tma_load_3d_pair(b_s + BOX_BYTES, &tmB, full, b0 + 64, kb * BK, t.e);
+                        } else {
+                            tma_load_3d_pair(b_s, &tmB, full, kb * BK, b0, t.e);
+                        }
+                    }
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // a wait has given up: let the copies in flight land before the CTA exits
+            if (*abort_flag) spin(4000000);
+        } else if (warp == 1 && leader && lane == 0) {
+            // ---------------- MMA issuer (leader only) ----------------
+            constexpr uint32_t idesc =
+                make_idesc(BT, BT) | (kMnA ? kIdescMnA : 0u) | (kMnB ? kIdescMnB : 0u);
+            // a K step of 16 inside a stage: 32 bytes of a K-major row, or 16 rows
+            constexpr uint64_t kStepA = kMnA ? 16 * 128 / 16 : 2, kStepB = kMnB ? 16 * 128 / 16 : 2;
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                const int tile = queue_take(ctl, i, true, abort_flag, err);
+                if (tile < 0) break;
+                const Tile t = tile_of<kMode>(ctl, E, MB, NB, KB, tile);
+                // K steps of the last block (a segment's end)
+                const int last_steps =
+                    kW ? (ctl->cnts[t.e] - (t.kblocks - 1) * BK + UMMA_K - 1) / UMMA_K
+                       : BK / UMMA_K;
+                int in_chain = 0;
+                for (int kb = 0; kb < t.kblocks; ++kb) {
+                    if (in_chain == 0) {
+                        if (!wait_bar(smem_u32(&ctl->tempty[acc]), acc_phase ^ 1u, abort_flag,
+                                      err)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    // the peer's block-end warp arrives at cluster scope
+                    const uint32_t full = smem_u32(&ctl->full[stage]);
+                    if (!(kW ? wait_bar_cluster(full, phase, abort_flag, err)
+                             : wait_bar(full, phase, abort_flag, err))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + (uint32_t)(acc * BT);
+                    const uint32_t a_s = tiles_addr + stage * STAGE_BYTES;
+                    const uint32_t b_s = a_s + OP_BYTES;
+                    const uint64_t ad = kMnA ? sw128_desc_mn(a_s, BOX_BYTES) : sw128_desc(a_s);
+                    const uint64_t bd = kMnB ? sw128_desc_mn(b_s, BOX_BYTES) : sw128_desc(b_s);
+                    const int steps = kW && kb == t.kblocks - 1 ? last_steps : BK / UMMA_K;
+#pragma unroll
+                    for (int kk = 0; kk < BK / UMMA_K; ++kk) {
+                        if (!kW || kk < steps)
+                            umma_bf16_pair(d, ad + kStepA * kk, bd + kStepB * kk, idesc,
+                                           (in_chain | kk) != 0 ? 1u : 0u);
+                    }
+                    umma_commit_pair_multicast(smem_u32(&ctl->empty[stage]), 0x3);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (++in_chain == chain || kb == t.kblocks - 1) {
+                        umma_commit_pair_multicast(smem_u32(&ctl->tfull[acc]), 0x3);
+                        in_chain = 0;
+                        if (++acc == kAccs) {
+                            acc = 0;
+                            acc_phase ^= 1u;
+                        }
+                    }
+                }
+            }
+            umma_commit_pair_multicast(smem_u32(&ctl->done), 0x1);
+            wait_bar_drain(smem_u32(&ctl->done), 0);
+        } else if (warp == 2 && leader && lane == 0) {
+            // ---------------- tile scheduler (leader) ----------------
+            // index i is published once the producer has taken index i - 1
+            for (int i = 0;; ++i) {
+                if (i > 0) {
+                    const int j = i - 1;
+                    if (!wait_bar(smem_u32(&ctl->tq_taken[j % kQ]), (uint32_t)(j / kQ) & 1u,
+                                  abort_flag, err))
+                        break;
+                }
+                if (queue_publish(ctl, i, tile_counter, total, abort_flag, err) < 0) break;
+            }
+        } else if (kW && warp == 3) {
+            // ---------------- block ends (both CTAs) ----------------
+            const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
+            int stage = 0;
+            uint32_t land_phase = 0;
+            for (int i = 0;; ++i) {
+                int tile = 0;
+                if (lane == 0)
+                    tile = leader ? queue_take(ctl, i, true, abort_flag, err)
+                                  : local_take(ctl, i, abort_flag, err);
+                tile = __shfl_sync(0xffffffffu, tile, 0);
+                if (tile < 0) break;
+                const Tile t = tile_of<kMode>(ctl, E, MB, NB, KB, tile);
+                const int cnt = ctl->cnts[t.e];
+                if (t.kblocks == 0) continue;
+                const int last = (stage + t.kblocks - 1) % kStages;
+                stage = (stage + t.kblocks) % kStages;
+                if (cnt % UMMA_K == 0) continue;
+                int landed = 0;
+                if (lane == 0)
+                    landed = wait_bar(smem_u32(&ctl->land[last]), (land_phase >> last) & 1u,
+                                      abort_flag, err);
+                landed = __shfl_sync(0xffffffffu, landed, 0);
+                if (!landed) break;
+                land_phase ^= 1u << last;
+                // rows [r0, r1) of the 4 boxes of the stage, 8 chunks of 16 bytes each
+                const int r0 = cnt % BK, r1 = (r0 + UMMA_K - 1) / UMMA_K * UMMA_K;
+                uint8_t* st = tiles + (size_t)last * STAGE_BYTES;
+                for (int c = lane; c < (r1 - r0) * 32; c += 32) {
+                    const int box = c & 3, chunk = (c >> 2) & 7, r = r0 + (c >> 5);
+                    *reinterpret_cast<uint4*>(st + box * BOX_BYTES + r * 128 + chunk * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(full0 + (uint32_t)last * 8u);
+            }
+        }
+    } else {
+        // ---------------- epilogue (both CTAs): own 128 rows ----------------
+        regs_grow<kRegsEpilogue>();
+        const int q = warp & 3;               // TMEM lane quadrant
+        const int half = (warp - 4) >> 2;     // 128 columns of the tile
+        uint8_t* staging = staging_area + (size_t)(warp - 4) * kStagingBytes;
+        const uint32_t staging_addr = smem_u32(staging);
+        uint8_t* my_row = staging + lane * kSliceBytes;
+        const int sw = (lane >> 1) & 3;  // 64-byte swizzle of this lane's row
+        const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[0]), 0);
+        constexpr int kSliceCols = kSliceBytes / (int)sizeof(OutT);
+        constexpr int kChunkElems = 16 / (int)sizeof(OutT);
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int i = 0;; ++i) {
+            int tile = 0;
+            if (lane == 0)
+                tile = leader ? queue_take(ctl, i, true, abort_flag, err)
+                              : local_take(ctl, i, abort_flag, err);
+            tile = __shfl_sync(0xffffffffu, tile, 0);
+            if (tile < 0) break;
+            const Tile t = tile_of<kMode>(ctl, E, MB, NB, KB, tile);
+            if (kW && t.kblocks == 0 && accumulate) continue;  // nothing to add
+
+            float sum[kEpilogueCols];
+            bool ok = true;
+            int chains = (t.kblocks + chain - 1) / chain;
+            if (chains == 0) {
+#pragma unroll
+                for (int c = 0; c < kEpilogueCols; ++c) sum[c] = 0.f;
+            }
+            for (int n = 0; n < chains; ++n) {
+                int ready = 0;
+                if (lane == 0)
+                    ready = wait_bar(smem_u32(&ctl->tfull[acc]), acc_phase, abort_flag, err);
+                ready = __shfl_sync(0xffffffffu, ready, 0);
+                if (!ready) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) +
+                                       (uint32_t)(acc * BT + half * kEpilogueCols);
+#pragma unroll
+                for (int c = 0; c < kEpilogueCols; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(tbase + c, v);
+                    tmem_wait_ld();
+                    if (n == 0) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[c + j] = __uint_as_float(v[j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[c + j] += __uint_as_float(v[j]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)acc * 8u);
+                if (++acc == kAccs) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+
+            // first row and column of this warp's part, and how many rows it stores
+            const int row_tile = t.mb * BT + (int)rank * BH + q * 32;
+            const int row0 = kW ? row_tile : ctl->offs[t.e] + row_tile;
+            int rows_valid = (kW ? m_out : ctl->cnts[t.e]) - row_tile;
+            rows_valid = rows_valid < 0 ? 0 : (rows_valid > 32 ? 32 : rows_valid);
+            if (rows_valid == 0) continue;
+            const int col_base = t.nb * BT + half * kEpilogueCols;
+#pragma unroll
+            for (int c = 0; c < kEpilogueCols; c += kSliceCols) {
+                const int col0 = col_base + c;
+                if (col0 < n_out) {
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint4 o;
+                        uint32_t* op = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (sizeof(OutT) == 4)
+                                op[j] = __float_as_uint(sum[c + ch * kChunkElems + j]);
+                            else
+                                op[j] = pack2(sum[c + ch * kChunkElems + 2 * j],
+                                              sum[c + ch * kChunkElems + 2 * j + 1]);
+                        }
+                        *reinterpret_cast<uint4*>(my_row + ((ch ^ sw) << 4)) = o;
+                    }
+                    if (kW || rows_valid == 32) {
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (!kW)
+                                tma_store_2d(&tmOut, staging_addr, col0, row0);
+                            else if (accumulate)
+                                tma_reduce_add_3d(&tmOut, staging_addr, col0, row0, t.e);
+                            else
+                                tma_store_3d(&tmOut, staging_addr, col0, row0, t.e);
+                            bulk_commit();
+                        }
+                    } else {
+                        // the segment ends inside these rows: the rows after it are
+                        // another expert's
+                        __syncwarp();
+                        const int ch = lane & 3, col = col0 + ch * kChunkElems;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int rr = j * 8 + (lane >> 2);
+                            if (rr < rows_valid && col < n_out) {
+                                const uint4 v = *reinterpret_cast<const uint4*>(
+                                    staging + rr * kSliceBytes + ((ch ^ ((rr >> 1) & 3)) << 4));
+                                *reinterpret_cast<uint4*>(out + (size_t)(row0 + rr) * n_out +
+                                                          col) = v;
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while its peer may still signal it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+    // the tile counter returns to zero for the next launch (the last pair out)
+    if (leader && threadIdx.x == 0) {
+        __threadfence();
+        const int before = atomicAdd(tile_counter + 1, 1);
+        if (before == (int)(gridDim.x / 2) - 1) {
+            atomicExch(tile_counter, 0);
+            atomicExch(tile_counter + 1, 0);
+        }
+    }
+}
+
+template <int kMode, typename OutT>
+moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+                  const GemmGroup& g, long long tiles, int K, int m_out, int n_out, void* out,
+                  bool accumulate, cudaStream_t st) {
+    if (tiles >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
+    if (cudaFuncSetAttribute(grouped_product_kernel<kMode, OutT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kSmemBytes) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    const long long pairs_max = sm_count() / 2;
+    const long long pairs = tiles < pairs_max ? tiles : pairs_max;
+    const int chain = sizeof(OutT) == 4 ? kChainBlocks : 1 << 30;
+    grouped_product_kernel<kMode, OutT>
+        <<<(int)(2 * (pairs > 0 ? pairs : 1)), kThreads, kSmemBytes, st>>>(
+            a, b, o, g.offsets, g.counts, g.E, (int)g.R, K, m_out, n_out,
+            reinterpret_cast<OutT*>(out), chain, accumulate ? 1 : 0, g.err, g.prefix + g.E + 1);
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+bool map_bf16(CUtensorMap* m, const void* ptr, long long outer, long long rows, long long cols,
+              uint32_t box_cols, uint32_t box_rows) {
+    const uint64_t sizes[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)outer};
+    const uint32_t box[3] = {box_cols, box_rows, 1};
+    return map_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, outer > 0 ? 3 : 2, ptr, sizes, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool map_out(CUtensorMap* m, const void* ptr, long long outer, long long rows, long long cols,
+             bool f32) {
+    const uint64_t sizes[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)outer};
+    const uint32_t box[3] = {f32 ? 16u : 32u, 32, 1};
+    return map_tiled(m,
+                     f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     f32 ? 4 : 2, outer > 0 ? 3 : 2, ptr, sizes, box, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+moe_status launch_rows(const uint16_t* rows, const GemmGroup& g, int c_in, int c_out,
+                       const uint16_t* w, void* out, bool out_f32, bool input_grad,
+                       cudaStream_t st) {
+    const int K = input_grad ? c_out : c_in, n_out = input_grad ? c_in : c_out;
+    CUtensorMap a, b, o;
+    const bool ok = map_bf16(&a, rows, 0, g.R, K, BK, BH) &&
+                    map_bf16(&b, w, g.E, c_out, c_in, BK, input_grad ? BK : BH) &&
+                    map_out(&o, out, 0, g.R, n_out, out_f32);
+    if (!ok) return MOE_ERR_UNSUPPORTED;
+    const long long tiles = ((g.R + BT - 1) / BT + g.E) * ((n_out + BT - 1LL) / BT);
+    if (input_grad)
+        return out_f32 ? launch<kRowsGrad, float>(a, b, o, g, tiles, K, 0, n_out, out, false, st)
+                       : launch<kRowsGrad, __nv_bfloat16>(a, b, o, g, tiles, K, 0, n_out, out,
+                                                          false, st);
+    return out_f32 ? launch<kForward, float>(a, b, o, g, tiles, K, 0, n_out, out, false, st)
+                   : launch<kForward, __nv_bfloat16>(a, b, o, g, tiles, K, 0, n_out, out, false,
+                                                     st);
+}
+
+moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const GemmGroup& g, int c_in,
+                          int c_out, void* dw, bool out_f32, bool accumulate,
+                          cudaStream_t st) {
+    CUtensorMap a, b, o;
+    const bool ok = map_bf16(&a, dout, 0, g.R, c_out, 64, BK) &&
+                    map_bf16(&b, rows, 0, g.R, c_in, 64, BK) &&
+                    map_out(&o, dw, g.E, c_out, c_in, out_f32);
+    if (!ok) return MOE_ERR_UNSUPPORTED;
+    const long long tiles =
+        (long long)g.E * ((c_out + BT - 1) / BT) * ((c_in + BT - 1LL) / BT);
+    return out_f32 ? launch<kWeightsGrad, float>(a, b, o, g, tiles, 0, c_out, c_in, dw, accumulate,
+                                                 st)
+                   : launch<kWeightsGrad, __nv_bfloat16>(a, b, o, g, tiles, 0, c_out, c_in, dw,
+                                                         accumulate, st);
+}
+
+moe_status check_grouped(const moe_layout* layout, const moe_shape* shape, int32_t C_in,
+                         int32_t C_out, int32_t out_type, void* ws, size_t ws_bytes) {
+    MOE_TRY(check_shape(shape));
+    MOE_TRY(check_layout(layout, shape));
+    MOE_TRY(check_ws(shape, ws, ws_bytes));
+    if (C_in <= 0 || C_out <= 0) return MOE_ERR_INVALID_ARG;
+    if (C_in % 8 != 0 || C_out % 8 != 0) return MOE_ERR_UNSUPPORTED;
+    if (out_type != MOE_TYPE_BF16 && out_type != MOE_TYPE_F32) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_grouped_gemm(const uint16_t* rows, const moe_layout* layout,
+                            const moe_shape* shape, int32_t C_in, int32_t C_out,
+                            const uint16_t* w, void* out, int32_t out_type, void* ws,
+                            size_t ws_bytes, void* stream) {
+    MOE_RANGE();
+    MOE_TRY(check_grouped(layout, shape, C_in, C_out, out_type, ws, ws_bytes));
+    if (shape->N == 0) return MOE_OK;
+    if (!rows || !w || !out) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(rows, w, out)) return MOE_ERR_INVALID_ARG;
+    return launch_rows(rows, routed_group(*layout, *shape, ws), C_in, C_out, w, out,
+                       out_type == MOE_TYPE_F32, false, as_stream(stream));
+}
+
+moe_status moe_grouped_gemm_input_grad(const uint16_t* dout, const moe_layout* layout,
+                                       const moe_shape* shape, int32_t C_in, int32_t C_out,
+                                       const uint16_t* w, void* drows, int32_t out_type, void* ws,
+                                       size_t ws_bytes, void* stream) {
+    MOE_RANGE();
+    MOE_TRY(check_grouped(layout, shape, C_in, C_out, out_type, ws, ws_bytes));
+    if (shape->N == 0) return MOE_OK;
+    if (!dout || !w || !drows) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(dout, w, drows)) return MOE_ERR_INVALID_ARG;
+    return launch_rows(dout, routed_group(*layout, *shape, ws), C_in, C_out, w, drows,
+                       out_type == MOE_TYPE_F32, true, as_stream(stream));
+}
+
+moe_status moe_grouped_gemm_weight_grad(const uint16_t* dout, const uint16_t* rows,
+                                        const moe_layout* layout, const moe_shape* shape,
+                                        int32_t C_in, int32_t C_out, void* dw, int32_t out_type,
+                                        int32_t accumulate, void* ws, size_t ws_bytes,
+                                        void* stream) {
+    MOE_RANGE();
+    MOE_TRY(check_grouped(layout, shape, C_in, C_out, out_type, ws, ws_bytes));
+    if (accumulate && out_type != MOE_TYPE_F32) return MOE_ERR_UNSUPPORTED;
+    if (!dw || !aligned16(dw)) return MOE_ERR_INVALID_ARG;
+    const bool f32 = out_type == MOE_TYPE_F32;
+    if (shape->N == 0) {
+        if (accumulate) return MOE_OK;
+        return cuda_status(cudaMemsetAsync(
+            dw, 0, (size_t)shape->E * C_out * C_in * (f32 ? 4 : 2), as_stream(stream)));
+    }
+    if (!dout || !rows || !aligned16(dout, rows)) return MOE_ERR_INVALID_ARG;
+    return launch_weights(dout, rows, routed_group(*layout, *shape, ws), C_in, C_out, dw, f32,
+                          accumulate != 0, as_stream(stream));
+}
+
+}  // extern "C"

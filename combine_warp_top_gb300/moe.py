@@ -1,4 +1,4 @@
-"""Python binding of libmoe (include/moe.h): argument marshalling only.
+"""Python binding of libmoe (include/moe.h, include/moe_train.h): argument marshalling only.
 
 Every function below has the name of the C entry point it calls and takes
 torch CUDA tensors in place of device pointers.  All arithmetic runs in the
@@ -85,6 +85,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_combine_shared": (I32, [P, P, lay, shp, P, P, P, P, P]),
         "moe_placement_search": (I32, [P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                        ctypes.c_int64, P, P]),
+        "moe_grouped_gemm": (I32, [P, lay, shp, I32, I32, P, P, I32, P, S, P]),
+        "moe_grouped_gemm_input_grad": (I32, [P, lay, shp, I32, I32, P, P, I32, P, S, P]),
+        "moe_grouped_gemm_weight_grad": (I32, [P, P, lay, shp, I32, I32, P, I32, I32, P, S, P]),
         "moe_selftest_wait_timeout": (I32, [P, ctypes.c_int64, P]),
         "moe_get_error": (I32, [P, P]),
         "moe_status_str": (ctypes.c_char_p, [I32]),
@@ -501,6 +504,79 @@ def moe_placement_search(coselect_host, ranks: int, nodes: int = 1, max_swaps: i
                                        ctypes.c_void_p(placement.data_ptr()), ctypes.byref(swaps)),
            "moe_placement_search")
     return placement, int(swaps.value)
+
+
+# ---- training operators (include/moe_train.h) ------------------------------------------
+
+MOE_TYPES = {torch.bfloat16: 0, torch.float32: 1}  # moe_type
+
+
+def _exact(t, dtype, shape, what):
+    """Pointer of a contiguous device tensor of exactly this type and shape
+    (None passes: the C call decides whether NULL is allowed)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _out_type(t, what):
+    """moe_type of an output tensor that may be bf16 or fp32."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch tensor")
+    if t.dtype not in MOE_TYPES:
+        raise ValueError(f"{what}: expected bf16 or fp32, got {t.dtype}")
+    return MOE_TYPES[t.dtype]
+
+
+def _expert_matrices(w, shape: Shape, what):
+    """(C_out, C_in) of per-expert matrices [E, C_out, C_in]."""
+    if not isinstance(w, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch tensor")
+    if w.dim() != 3 or w.shape[0] != shape.E:
+        raise ValueError(f"{what}: expected [E = {shape.E}, C_out, C_in], got {tuple(w.shape)}")
+    return w.shape[1], w.shape[2]
+
+
+def moe_grouped_gemm(rows, layout: Layout, shape: Shape, w, out, ws, stream=None):
+    """out[i] = rows[i] W[e]^T for the N*k expert-major rows; w [E, C_out, C_in]
+    bf16, out [N*k, C_out] bf16 or fp32."""
+    co, ci = _expert_matrices(w, shape, "w")
+    ot, R = _out_type(out, "out"), shape.R
+    _check(load().moe_grouped_gemm(
+        _exact(rows, torch.bfloat16, (R, ci), "rows"), _lay(layout, shape),
+        ctypes.byref(shape.c()), ci, co, _exact(w, torch.bfloat16, w.shape, "w"),
+        _exact(out, out.dtype, (R, co), "out"), ot, *_ws(ws), _stream(stream)),
+        "moe_grouped_gemm")
+
+
+def moe_grouped_gemm_input_grad(dout, layout: Layout, shape: Shape, w, drows, ws, stream=None):
+    """drows[i] = dout[i] W[e]; drows [N*k, C_in] bf16 or fp32."""
+    co, ci = _expert_matrices(w, shape, "w")
+    ot, R = _out_type(drows, "drows"), shape.R
+    _check(load().moe_grouped_gemm_input_grad(
+        _exact(dout, torch.bfloat16, (R, co), "dout"), _lay(layout, shape),
+        ctypes.byref(shape.c()), ci, co, _exact(w, torch.bfloat16, w.shape, "w"),
+        _exact(drows, drows.dtype, (R, ci), "drows"), ot, *_ws(ws), _stream(stream)),
+        "moe_grouped_gemm_input_grad")
+
+
+def moe_grouped_gemm_weight_grad(dout, rows, layout: Layout, shape: Shape, dw, ws,
+                                 accumulate=False, stream=None):
+    """dw[e] (+)= sum of dout[i]^T rows[i] over the expert's rows; dw
+    [E, C_out, C_in] bf16 or fp32 (fp32 to accumulate)."""
+    co, ci = _expert_matrices(dw, shape, "dw")
+    ot, R = _out_type(dw, "dw"), shape.R
+    _check(load().moe_grouped_gemm_weight_grad(
+        _exact(dout, torch.bfloat16, (R, co), "dout"),
+        _exact(rows, torch.bfloat16, (R, ci), "rows"), _lay(layout, shape),
+        ctypes.byref(shape.c()), ci, co, _exact(dw, dw.dtype, dw.shape, "dw"), ot,
+        int(bool(accumulate)), *_ws(ws), _stream(stream)), "moe_grouped_gemm_weight_grad")
 
 
 def moe_selftest_wait_timeout(ws, limit_cycles: int, stream=None):
