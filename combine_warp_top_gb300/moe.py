@@ -37,6 +37,11 @@ class MoeLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in LAYOUT_FIELDS]
 
 
+class MoeNormShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "H", "post", "pre", "gate", "stream_type")] + \
+        [("eps", ctypes.c_float), ("residual_scale", ctypes.c_float)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -56,6 +61,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     P, S, I32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
     shp, lay = ctypes.POINTER(MoeShape), ctypes.POINTER(MoeLayout)
+    nrm = ctypes.POINTER(MoeNormShape)
     sigs = {
         "moe_workspace_bytes": (S, [shp]),
         "moe_packed_gate_up_bytes": (S, [shp]),
@@ -88,6 +94,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_grouped_gemm": (I32, [P, lay, shp, I32, I32, P, P, I32, P, S, P]),
         "moe_grouped_gemm_input_grad": (I32, [P, lay, shp, I32, I32, P, P, I32, P, S, P]),
         "moe_grouped_gemm_weight_grad": (I32, [P, P, lay, shp, I32, I32, P, I32, I32, P, S, P]),
+        "moe_swiglu": (I32, [P, P, lay, shp, P, P]),
+        "moe_swiglu_grad": (I32, [P, P, P, lay, shp, P, P, P]),
+        "moe_route_grad": (I32, [P, P, P, shp, P, P]),
+        "moe_route_full_softmax_grad": (I32, [P, P, P, shp, P, P]),
+        "moe_route_sigmoid_bias_grad": (I32, [P, P, P, shp, P, P]),
+        "moe_norm_workspace_bytes": (S, [nrm]),
+        "moe_block_norm": (I32, [P, P, P, P, P, nrm, P, P, P, P, P]),
+        "moe_block_norm_grad": (I32, [P, P, P, P, P, P, P, P, P, nrm, P, P, P, P, P, I32, P, S,
+                                      P]),
         "moe_selftest_wait_timeout": (I32, [P, ctypes.c_int64, P]),
         "moe_get_error": (I32, [P, P]),
         "moe_status_str": (ctypes.c_char_p, [I32]),
@@ -577,6 +592,135 @@ def moe_grouped_gemm_weight_grad(dout, rows, layout: Layout, shape: Shape, dw, w
         _exact(rows, torch.bfloat16, (R, ci), "rows"), _lay(layout, shape),
         ctypes.byref(shape.c()), ci, co, _exact(dw, dw.dtype, dw.shape, "dw"), ot,
         int(bool(accumulate)), *_ws(ws), _stream(stream)), "moe_grouped_gemm_weight_grad")
+
+
+def moe_swiglu(gu, topk_w, layout: Layout, shape: Shape, h, stream=None):
+    """h[i] = w_i SiLU(g) u for the expert-major rows gu = [g | u] [N*k, 2*I],
+    w_i the routing weight (topk_w fp32 [N, k]; None: ones) of the row's pair."""
+    s = shape
+    _check(load().moe_swiglu(
+        _exact(gu, torch.bfloat16, (s.R, 2 * s.I), "gu"),
+        _exact(topk_w, torch.float32, (s.N, s.k), "topk_w"), _lay(layout, s),
+        ctypes.byref(s.c()), _exact(h, torch.bfloat16, (s.R, s.I), "h"), _stream(stream)),
+        "moe_swiglu")
+
+
+def moe_swiglu_grad(dh, gu, topk_w, layout: Layout, shape: Shape, dgu, dtopk_w, stream=None):
+    """dgu [N*k, 2*I] and dtopk_w fp32 [N, k] (None: not wanted) of moe_swiglu."""
+    s = shape
+    _check(load().moe_swiglu_grad(
+        _exact(dh, torch.bfloat16, (s.R, s.I), "dh"),
+        _exact(gu, torch.bfloat16, (s.R, 2 * s.I), "gu"),
+        _exact(topk_w, torch.float32, (s.N, s.k), "topk_w"), _lay(layout, s),
+        ctypes.byref(s.c()), _exact(dgu, torch.bfloat16, (s.R, 2 * s.I), "dgu"),
+        _exact(dtopk_w, torch.float32, (s.N, s.k), "dtopk_w"), _stream(stream)),
+        "moe_swiglu_grad")
+
+
+def moe_route_grad(topk_ids, topk_w, dtopk_w, shape: Shape, dlogits, stream=None):
+    """dlogits fp32 [N, E] of moe_route (softmax over the selected k)."""
+    s = shape
+    _check(load().moe_route_grad(
+        _exact(topk_ids, torch.int32, (s.N, s.k), "topk_ids"),
+        _exact(topk_w, torch.float32, (s.N, s.k), "topk_w"),
+        _exact(dtopk_w, torch.float32, (s.N, s.k), "dtopk_w"), ctypes.byref(s.c()),
+        _exact(dlogits, torch.float32, (s.N, s.E), "dlogits"), _stream(stream)),
+        "moe_route_grad")
+
+
+def _route_logits_grad(name, logits, topk_ids, dtopk_w, shape, dlogits, stream):
+    s = shape
+    _check(getattr(load(), name)(
+        _exact(logits, torch.float32, (s.N, s.E), "logits"),
+        _exact(topk_ids, torch.int32, (s.N, s.k), "topk_ids"),
+        _exact(dtopk_w, torch.float32, (s.N, s.k), "dtopk_w"), ctypes.byref(s.c()),
+        _exact(dlogits, torch.float32, (s.N, s.E), "dlogits"), _stream(stream)), name)
+
+
+def moe_route_full_softmax_grad(logits, topk_ids, dtopk_w, shape: Shape, dlogits, stream=None):
+    """dlogits fp32 [N, E] of moe_route_full_softmax."""
+    _route_logits_grad("moe_route_full_softmax_grad", logits, topk_ids, dtopk_w, shape, dlogits,
+                       stream)
+
+
+def moe_route_sigmoid_bias_grad(logits, topk_ids, dtopk_w, shape: Shape, dlogits, stream=None):
+    """dlogits fp32 [N, E] of moe_route_sigmoid_bias."""
+    _route_logits_grad("moe_route_sigmoid_bias_grad", logits, topk_ids, dtopk_w, shape, dlogits,
+                       stream)
+
+
+GATES = {"none": 0, "channel": 1, "token": 2}  # moe_gate
+
+
+@dataclass(frozen=True)
+class NormShape:
+    """N rows of width H at the boundary of two blocks (moe_norm_shape)."""
+    N: int
+    H: int
+    post: bool = True            # RMS norm after the block
+    pre: bool = True             # RMS norm before the next one
+    gate: str = "none"           # "none", "channel" (fp32 [H]) or "token" (fp32 [N])
+    stream: str = "bf16"         # residual stream: "bf16" or "fp32"
+    eps: float = 1e-6
+    residual_scale: float = 1.0
+
+    def c(self) -> MoeNormShape:
+        if self.gate not in GATES:
+            raise ValueError(f"gate must be one of {sorted(GATES)}")
+        if self.stream not in ("bf16", "fp32"):
+            raise ValueError("stream must be bf16 or fp32")
+        return MoeNormShape(self.N, self.H, int(bool(self.post)), int(bool(self.pre)),
+                            GATES[self.gate], int(self.stream == "fp32"), self.eps,
+                            self.residual_scale)
+
+    @property
+    def stream_dtype(self):
+        return torch.float32 if self.stream == "fp32" else torch.bfloat16
+
+    def gate_shape(self):
+        return (self.N,) if self.gate == "token" else (self.H,)
+
+
+def moe_norm_workspace_bytes(shape: NormShape) -> int:
+    return int(load().moe_norm_workspace_bytes(ctypes.byref(shape.c())))
+
+
+def norm_workspace(shape: NormShape, device="cuda") -> torch.Tensor:
+    n = moe_norm_workspace_bytes(shape)
+    if n == 0:
+        raise MoeError(1, "moe_norm_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_block_norm(y, residual, w_post, gate, w_pre, shape: NormShape, s, x, rstd_post=None,
+                   rstd_pre=None, stream=None):
+    """s = residual_scale * residual + gate * norm(y) w_post; x = norm(s) w_pre."""
+    n = shape
+    nh, h, f32, st = (n.N, n.H), (n.H,), torch.float32, n.stream_dtype
+    _check(load().moe_block_norm(
+        _exact(y, torch.bfloat16, nh, "y"), _exact(residual, st, nh, "residual"),
+        _exact(w_post, f32, h, "w_post"), _exact(gate, f32, n.gate_shape(), "gate"),
+        _exact(w_pre, f32, h, "w_pre"), ctypes.byref(n.c()), _exact(s, st, nh, "s"),
+        _exact(x, torch.bfloat16, nh, "x"), _exact(rstd_post, f32, (n.N,), "rstd_post"),
+        _exact(rstd_pre, f32, (n.N,), "rstd_pre"), _stream(stream)), "moe_block_norm")
+
+
+def moe_block_norm_grad(ds, dx, y, s, w_post, gate, w_pre, rstd_post, rstd_pre,
+                        shape: NormShape, dy, dresidual, dw_post, dgate, dw_pre, ws,
+                        accumulate=False, stream=None):
+    """Gradient of moe_block_norm from ds and dx; ws of norm_workspace(shape)."""
+    n = shape
+    nh, h, f32, st = (n.N, n.H), (n.H,), torch.float32, n.stream_dtype
+    bf = torch.bfloat16
+    _check(load().moe_block_norm_grad(
+        _exact(ds, st, nh, "ds"), _exact(dx, bf, nh, "dx"), _exact(y, bf, nh, "y"),
+        _exact(s, st, nh, "s"), _exact(w_post, f32, h, "w_post"),
+        _exact(gate, f32, n.gate_shape(), "gate"), _exact(w_pre, f32, h, "w_pre"),
+        _exact(rstd_post, f32, (n.N,), "rstd_post"), _exact(rstd_pre, f32, (n.N,), "rstd_pre"),
+        ctypes.byref(n.c()), _exact(dy, bf, nh, "dy"), _exact(dresidual, st, nh, "dresidual"),
+        _exact(dw_post, f32, h, "dw_post"), _exact(dgate, f32, n.gate_shape(), "dgate"),
+        _exact(dw_pre, f32, h, "dw_pre"), int(bool(accumulate)), *_ws(ws), _stream(stream)),
+        "moe_block_norm_grad")
 
 
 def moe_selftest_wait_timeout(ws, limit_cycles: int, stream=None):
