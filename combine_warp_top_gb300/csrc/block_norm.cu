@@ -25,6 +25,7 @@
 #include "../../include/moe_train.h"
 #include "api_checks.cuh"
 #include "moe_internal.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -45,6 +46,7 @@ struct NormArgs {
     float* rstd_pre;
     int N, V;                // V = H / 8
     int post, pre, gate_kind;
+    int wide;                // fp32 stream tensors start on 32-byte boundaries
     float eps, alpha, inv_h;
 };
 
@@ -64,293 +66,561 @@ struct NormGradArgs {
     float* partial;          // [grid][2][H]: sums of g yh (gated per token), of dx sh
     int N, V;
     int post, pre, gate_kind;
+    int wide;
     float alpha, inv_h;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Pairs of fp32 values: one instruction of the packed fp32 pipe for two elements.
+using f2 = float2;
+__device__ __forceinline__ unsigned long long bits2(f2 v) {
+    return *reinterpret_cast<unsigned long long*>(&v);
+}
+__device__ __forceinline__ f2 from_bits2(unsigned long long v) {
+    return *reinterpret_cast<f2*>(&v);
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return from_bits2(d);
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+    return from_bits2(d);
+}
+__device__ __forceinline__ f2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float across(f2 v) { return v.x + v.y; }
+
+// 8 consecutive values of an input as they are in memory: one 16-byte word of
+// bf16, or two of fp32.
+template <bool kF32>
+struct Raw {
+    uint4 w[kF32 ? 2 : 1];
+};
+template <bool kF32>
+__device__ __forceinline__ void unpack(const Raw<kF32>& r, f2 (&f)[4]) {
+    if (kF32) {
+        const uint4 a = r.w[0], b = r.w[kF32 ? 1 : 0];
+        f[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+        f[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+        f[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+        f[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+    } else {
+        const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < 4; ++i)
+            f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+__device__ __forceinline__ uint4 pack_bf16(const f2 (&f)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f[i].x, f[i].y);
         w[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 8 consecutive values of a stream tensor (vector index v), streamed past L1.
+// Vector v of a row, past L1 (each is read or written once).
 template <bool kF32>
-__device__ __forceinline__ void load_stream(const void* p, long long v, float (&f)[8]) {
-    if (kF32) {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(p) + 2 * v);
-        const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 2 * v + 1);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+__device__ __forceinline__ Raw<kF32> load_global(const char* row, uint32_t v) {
+    Raw<kF32> r;
+    const uint4* q = reinterpret_cast<const uint4*>(row + v * (kF32 ? 32u : 16u));
+    r.w[0] = __ldcs(q);
+    if (kF32) r.w[kF32 ? 1 : 0] = __ldcs(q + 1);
+    return r;
+}
+// wide: one 32-byte store of an fp32 vector, so that a warp writes whole lines
+// (two 16-byte ones write every sector by halves: 1.3 times slower on rows of
+// fp32 where the stores bound the kernel).
+template <bool kF32>
+__device__ __forceinline__ void store_global(char* row, uint32_t v, const f2 (&f)[4], int wide) {
+    char* at = row + v * (kF32 ? 32u : 16u);
+    if (!kF32) {
+        __stcs(reinterpret_cast<uint4*>(at), pack_bf16(f));
+    } else if (wide) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at),
+                     "f"(f[0].x), "f"(f[0].y), "f"(f[1].x), "f"(f[1].y), "f"(f[2].x),
+                     "f"(f[2].y), "f"(f[3].x), "f"(f[3].y)
+                     : "memory");
     } else {
-        unpack8(__ldcs(reinterpret_cast<const uint4*>(p) + v), f);
+        float4* o = reinterpret_cast<float4*>(at);
+        __stcs(o, make_float4(f[0].x, f[0].y, f[1].x, f[1].y));
+        __stcs(o + 1, make_float4(f[2].x, f[2].y, f[3].x, f[3].y));
     }
 }
-template <bool kF32>
-__device__ __forceinline__ void store_stream(void* p, long long v, const float (&f)[8]) {
-    if (kF32) {
-        float4* o = reinterpret_cast<float4*>(p) + 2 * v;
-        __stcs(o, make_float4(f[0], f[1], f[2], f[3]));
-        __stcs(o + 1, make_float4(f[4], f[5], f[6], f[7]));
-    } else {
-        __stcs(reinterpret_cast<uint4*>(p) + v, pack8(f));
-    }
-}
-// 8 values of a per-channel vector (null: ones), kept in L1.
-__device__ __forceinline__ void load_channel(const float* p, int v, float (&f)[8]) {
+// 8 values of a per-channel vector (null: ones).
+__device__ __forceinline__ void load_channel(const float* p, int v, f2 (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = both(1.0f);
     if (p) {
         const float4 a = __ldg(reinterpret_cast<const float4*>(p) + 2 * v);
         const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 2 * v + 1);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = 1.0f;
+        f[0] = make_float2(a.x, a.y);
+        f[1] = make_float2(a.z, a.w);
+        f[2] = make_float2(b.x, b.y);
+        f[3] = make_float2(b.z, b.w);
     }
 }
-
-__device__ __forceinline__ float warp_sum(float v) {
+// The block's scale of a channel: gate per channel times the weight after it.
+__device__ __forceinline__ void load_scale(const float* gate, const float* w_post, int v,
+                                           f2 (&f)[4]) {
+    f2 g[4];
+    load_channel(w_post, v, f);
+    load_channel(gate, v, g);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], g[i]);
+}
+
+// The inputs of the next rows of a block on their way into shared memory with
+// 16-byte cp.async, into slots that only the warp reads: a row in flight costs no
+// registers and no block barrier.  A stage holds words of 16 bytes for every
+// thread, `pitch` bytes between a thread's words.  bf16: a thread copies its own
+// word.  fp32: a warp copies its 64 words in order (so that it asks for whole
+// lines), each to the thread that owns it.
+template <bool kF32>
+__device__ __forceinline__ void ring_copy(uint32_t stage, uint32_t pitch, const char* row,
+                                          uint32_t thread, uint32_t v, uint32_t V) {
+    if (!kF32) {
+        if (v < V) ptx::cp_async_16(stage + thread * 16u, row + v * 16u, 16);
+    } else {
+        const uint32_t lane = thread & 31u;
+#pragma unroll
+        for (uint32_t i = 0; i < 2; ++i) {
+            const uint32_t g = lane + 32u * i;  // the warp's word
+            if (v - lane + (g >> 1) < V)
+                ptx::cp_async_16(stage + (g & 1u) * pitch + (thread - lane + (g >> 1)) * 16u,
+                                 row + ((v - lane) * 2u + g) * 16u, 16);
+        }
+    }
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+template <bool kF32>
+__device__ __forceinline__ Raw<kF32> ring_read(uint32_t slot, uint32_t pitch) {
+    Raw<kF32> r;
+    r.w[0] = lds16(slot);
+    if (kF32) r.w[kF32 ? 1 : 0] = lds16(slot + pitch);
+    return r;
+}
+__device__ __forceinline__ void ring_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kAhead>
+__device__ __forceinline__ void ring_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+    __syncwarp();  // what the warp's other lanes have copied is there too
+}
+
+// Rows are shared out to groups of kLanes threads: 8, 16 or 32 lanes of a warp
+// for short rows, or (kLanes = 0) a whole block.
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// Sum over the threads of a row: a warp, or the whole block through `part`
-// (32 floats; calls in a row use different ones).
-template <bool kWarpRow>
+// Sum over a row's threads, a block's through `part` (32 floats; calls in a row
+// use different ones).
+template <int kLanes>
 __device__ __forceinline__ float row_sum(float v, float* part) {
-    v = warp_sum(v);
-    if (kWarpRow) return v;
+    v = lanes_sum(v, kLanes ? kLanes : 32);
+    if (kLanes) return v;
     const int warps = blockDim.x >> 5;
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     float t = (int)(threadIdx.x & 31) < warps ? part[threadIdx.x & 31] : 0.0f;
-    return warp_sum(t);
+    return lanes_sum(t, 32);
 }
 
-// kV: vectors of 8 a thread holds; kWarpRow: a warp a row (a block holds
-// blockDim / 32 rows), else a block a row.
-template <int kV, bool kWarpRow, bool kF32>
-__global__ void __launch_bounds__(kWarpRow ? 32 * kRowWarps : 1024)
+// Sums of four values over a warp in 6 shuffles: the first two steps halve the
+// values a lane holds as well as the lanes.  Lane 8 i ends with value i's sum
+// (as do its 7 neighbours).
+__device__ __forceinline__ float warp_sum4(const float (&v)[4]) {
+    const int lane = threadIdx.x & 31;
+    const bool hi = lane & 16, hi8 = lane & 8;
+    const float x0 = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+    const float x1 = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
+    const float x = (hi8 ? x1 : x0) + __shfl_xor_sync(0xffffffffu, hi8 ? x0 : x1, 8);
+    return lanes_sum(x, 8);
+}
+// Four sums over a row's threads (part: 128 floats, as for row_sum).
+template <int kLanes>
+__device__ __forceinline__ void row_sum4(float (&v)[4], float4* part) {
+    if (kLanes == 8 || kLanes == 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lanes_sum(v[i], kLanes);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    float x = warp_sum4(v);
+    if (kLanes == 0) {
+        const int warps = blockDim.x >> 5;
+        if ((lane & 7) == 0) reinterpret_cast<float*>(part + (threadIdx.x >> 5))[lane >> 3] = x;
+        __syncthreads();
+        const float4 t = lane < warps ? part[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float u[4] = {t.x, t.y, t.z, t.w};
+        x = warp_sum4(u);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, x, 8 * i);
+}
+
+// The rows of this thread's group: its first, the step to its next, and how many
+// rows ahead of the group the first of its warp (or block) is, which bounds the
+// loop so that a warp's groups leave it together.
+struct Rows {
+    int first, step, lead;
+};
+template <int kLanes>
+__device__ __forceinline__ Rows my_rows() {
+    if (kLanes == 0) return {(int)blockIdx.x, (int)gridDim.x, 0};
+    constexpr int kGroups = 32 * kRowWarps / (kLanes ? kLanes : 32);
+    const int group = threadIdx.x / (kLanes ? kLanes : 32);
+    const int in_warp = (threadIdx.x & 31) / (kLanes ? kLanes : 32);
+    return {(int)blockIdx.x * kGroups + group, (int)gridDim.x * kGroups, in_warp};
+}
+
+// kV: vectors of 8 a thread holds.  kStages: rows of inputs in a block's ring
+// (groups of a warp load straight to registers).  kKeep: the per-channel vectors
+// stay in registers over the block's rows (a thread keeps its columns); else they
+// come from L1 for every row.  kFull: y, both norms and s are all there, so
+// nothing is tested for.
+template <int kV, int kLanes, bool kF32, int kStages, bool kKeep, bool kFull>
+__global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
     block_norm_kernel(const NormArgs a) {
-    __shared__ float part[2][32];
-    const int lanes = kWarpRow ? 32 : blockDim.x;
-    const int tid = kWarpRow ? (threadIdx.x & 31) : threadIdx.x;
-    const long long row = kWarpRow
-                              ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)
-                              : (long long)blockIdx.x;
-    if (row >= a.N) return;  // a whole warp, or (one row a block) nobody
-    const long long base = row * a.V;
-    float z[kV][8], s[kV][8];
-    float sum = 0.0f;
+    extern __shared__ uint4 ring[];
+    __shared__ float part[2][2][32];
+    constexpr bool kRing = kLanes == 0;
+    constexpr int kWordsR = kF32 ? 2 : 1, kPerV = 1 + kWordsR;
+    constexpr uint32_t kRowR = kF32 ? 32 : 16;  // bytes of a stream vector
+    const uint32_t lanes = kLanes ? kLanes : blockDim.x;
+    const uint32_t tid = kLanes ? threadIdx.x % lanes : threadIdx.x;
+    const uint32_t V = a.V;
+    const Rows rows = my_rows<kLanes>();
+    const uint32_t pitch = blockDim.x * 16, stage_bytes = pitch * kV * kPerV;
+    const uint32_t ring0 = kRing ? ptx::smem_u32(ring) : 0u;
+    const bool has_y = kFull || a.y, post = kFull || a.post, pre = kFull || a.pre;
+
+    auto fetch = [&](int row, uint32_t stage) {
+        if (row < a.N) {
+            const char* y = reinterpret_cast<const char*>(a.y) + (size_t)row * V * 16;
+            const char* r = reinterpret_cast<const char*>(a.residual) + (size_t)row * V * kRowR;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int c = tid + i * lanes;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[i][j] = s[i][j] = 0.0f;
-        if (c < a.V) {
-            if (a.y) unpack8(__ldcs(reinterpret_cast<const uint4*>(a.y) + base + c), z[i]);
-            load_stream<kF32>(a.residual, base + c, s[i]);
-        }
-    }
-    float r_post = 1.0f;
-    if (a.post) {
-#pragma unroll
-        for (int i = 0; i < kV; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum += z[i][j] * z[i][j];
-        r_post = rsqrtf(row_sum<kWarpRow>(sum, part[0]) * a.inv_h + a.eps);
-        if (tid == 0 && a.rstd_post) a.rstd_post[row] = r_post;
-    }
-    const float token_gate = a.gate_kind == MOE_GATE_TOKEN ? a.gate[row] : 1.0f;
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int c = tid + i * lanes;
-        if (c < a.V) {
-            float w[8], g[8];
-            load_channel(a.post ? a.w_post : nullptr, c, w);
-            load_channel(a.gate_kind == MOE_GATE_CHANNEL ? a.gate : nullptr, c, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float t = a.post ? z[i][j] * r_post * w[j] : z[i][j];
-                s[i][j] = a.alpha * s[i][j] + (a.gate_kind == MOE_GATE_TOKEN ? token_gate : g[j]) * t;
-                sum += s[i][j] * s[i][j];
+            for (int i = 0; i < kV; ++i) {
+                const uint32_t c = tid + i * lanes, at = stage + i * kPerV * pitch;
+                if (has_y) ring_copy<false>(at, pitch, y, tid, c, V);
+                ring_copy<kF32>(at + pitch, pitch, r, tid, c, V);
             }
-            if (a.s) store_stream<kF32>(a.s, base + c, s[i]);
         }
+        ring_commit();
+    };
+    if (kRing)
+        for (int p = 0; p < kStages - 1; ++p)
+            fetch(rows.first + p * rows.step, ring0 + p * stage_bytes);
+
+    const float* gate_c = a.gate_kind == MOE_GATE_CHANNEL ? a.gate : nullptr;
+    const float* w_post = a.post ? a.w_post : nullptr;
+    f2 cw[kV][4], wp[kV][4];
+    auto channels = [&](int i) {
+        const uint32_t c = tid + i * lanes;
+        if (c < V) {
+            load_scale(gate_c, w_post, c, cw[i]);
+            load_channel(a.w_pre, c, wp[i]);
+        }
+    };
+    if (kKeep) {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) channels(i);
     }
-    if (!a.pre) return;
-    const float r_pre = rsqrtf(row_sum<kWarpRow>(sum, part[1]) * a.inv_h + a.eps);
-    if (tid == 0 && a.rstd_pre) a.rstd_pre[row] = r_pre;
+
+    int buf = 0, stage = 0;
+    for (int row = rows.first; row - rows.lead < a.N; row += rows.step, buf ^= 1) {
+        const bool live = kRing || row < a.N;
+        const float token_gate = a.gate_kind == MOE_GATE_TOKEN && live ? a.gate[row] : 1.0f;
+        const char* y_row = reinterpret_cast<const char*>(a.y) + (size_t)row * V * 16;
+        const char* r_row = reinterpret_cast<const char*>(a.residual) + (size_t)row * V * kRowR;
+        char* s_row = reinterpret_cast<char*>(a.s) + (size_t)row * V * kRowR;
+        char* x_row = reinterpret_cast<char*>(a.x) + (size_t)row * V * 16;
+        const uint32_t slot = ring0 + stage * stage_bytes + tid * 16;
+        if constexpr (kRing) {
+            __syncwarp();  // every lane has read what this overwrites
+            const int next = stage == 0 ? kStages - 1 : stage - 1;
+            fetch(row + (kStages - 1) * rows.step, ring0 + next * stage_bytes);
+            ring_wait<kStages - 1>();
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+        }
+        Raw<false> ry[kV];
+        Raw<kF32> rr[kV];
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int c = tid + i * lanes;
-        if (c < a.V) {
-            float w[8];
-            load_channel(a.w_pre, c, w);
+        for (int i = 0; i < kV; ++i) {
+            const uint32_t c = tid + i * lanes, at = slot + i * kPerV * pitch;
+            ry[i].w[0] = make_uint4(0, 0, 0, 0);
+            if (c < V && live) {
+                if (has_y)
+                    ry[i] = kRing ? ring_read<false>(at, pitch) : load_global<false>(y_row, c);
+                if (!kRing) rr[i] = load_global<kF32>(r_row, c);
+            }
+        }
+        float r_post = 1.0f;
+        if (post) {
+            f2 sum = both(0.0f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = s[i][j] * r_pre * w[j];
-            __stcs(reinterpret_cast<uint4*>(a.x) + base + c, pack8(w));
+            for (int i = 0; i < kV; ++i) {
+                f2 y[4];
+                unpack(ry[i], y);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum = fma2(y[j], y[j], sum);
+            }
+            r_post = rsqrtf(row_sum<kLanes>(across(sum), part[buf][0]) * a.inv_h + a.eps);
+            if (tid == 0 && live && a.rstd_post) a.rstd_post[row] = r_post;
+        }
+        f2 s[kV][4];
+        f2 sum = both(0.0f);
+        const f2 scale = both(r_post * token_gate), alpha = both(a.alpha);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const uint32_t c = tid + i * lanes;
+            if (c < V && live) {
+                if (!kKeep) channels(i);
+                if (kRing) rr[i] = ring_read<kF32>(slot + (i * kPerV + 1) * pitch, pitch);
+                f2 y[4];
+                unpack(ry[i], y);
+                unpack(rr[i], s[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = fma2(mul2(y[j], scale), cw[i][j], mul2(alpha, s[i][j]));
+                    sum = fma2(s[i][j], s[i][j], sum);
+                }
+                if (kFull || a.s) store_global<kF32>(s_row, c, s[i], a.wide);
+            }
+        }
+        if (!pre) continue;
+        const float r_pre = rsqrtf(row_sum<kLanes>(across(sum), part[buf][1]) * a.inv_h + a.eps);
+        if (tid == 0 && live && a.rstd_pre) a.rstd_pre[row] = r_pre;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const uint32_t c = tid + i * lanes;
+            if (c < V && live) {
+                f2 x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = mul2(mul2(s[i][j], both(r_pre)), wp[i][j]);
+                store_global<false>(x_row, c, x, 0);
+            }
         }
     }
 }
 
-template <int kV, bool kWarpRow, bool kF32>
-__global__ void __launch_bounds__(kWarpRow ? 32 * kRowWarps : 1024)
+// The gradient needs two sums over the row, of b sh (b = dx w_pre) for g and then
+// of g cw yh (cw = gate per channel * w_post) for dy.  The second is linear in g:
+//   sum g cw yh = sum cw yh ds + r_pre * (sum cw yh b - mean(b sh) * sum cw yh sh)
+// so all four sums are taken in one pass and reduced together, with one barrier
+// a row; the second pass reads the row again from the ring.  The row's factors
+// r_pre, r_post and its gate are taken out of the sums over columns.
+// kFull: dx, y, s, ds and dresidual are all there.
+template <int kV, int kLanes, bool kF32, int kStages, bool kKeep, bool kFull>
+__global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
     block_norm_grad_kernel(const NormGradArgs a) {
-    extern __shared__ float cols[];  // kWarpRow: [warps][2][H] sums of the block's warps
-    __shared__ float part[2][2][32];
-    const int lanes = kWarpRow ? 32 : blockDim.x;
-    const int tid = kWarpRow ? (threadIdx.x & 31) : threadIdx.x;
-    const int rows_at_once = kWarpRow ? (int)(blockDim.x >> 5) : 1;
-    const int sub = kWarpRow ? (int)(threadIdx.x >> 5) : 0;
-    float t_post[kV][8], t_pre[kV][8];
+    extern __shared__ uint4 ring[];
+    float* cols = reinterpret_cast<float*>(ring);  // groups of a warp: their column sums
+    __shared__ float4 part[2][32];
+    constexpr bool kRing = kLanes == 0;
+    constexpr int kWordsR = kF32 ? 2 : 1, kPerV = 2 + 2 * kWordsR;
+    constexpr uint32_t kRowR = kF32 ? 32 : 16;
+    const uint32_t lanes = kLanes ? kLanes : blockDim.x;
+    const uint32_t tid = kLanes ? threadIdx.x % lanes : threadIdx.x;
+    const uint32_t V = a.V;
+    const Rows rows = my_rows<kLanes>();
+    const uint32_t pitch = blockDim.x * 16, stage_bytes = pitch * kV * kPerV;
+    const uint32_t ring0 = kRing ? ptx::smem_u32(ring) : 0u;
+    const bool has_y = kFull || a.y, pre = kFull || a.pre, has_ds = kFull || a.ds;
+    f2 t_post[kV][4], t_pre[kV][4];
 #pragma unroll
     for (int i = 0; i < kV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t_post[i][j] = t_pre[i][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) t_post[i][j] = t_pre[i][j] = both(0.0f);
 
-    int buf = 0;
-    for (long long row = (long long)blockIdx.x * rows_at_once + sub; row < a.N;
-         row += (long long)gridDim.x * rows_at_once, buf ^= 1) {
-        const long long base = row * a.V;
-        float g[kV][8], b[kV][8], yh[kV][8], sh[kV][8];
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int c = tid + i * lanes;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) g[i][j] = b[i][j] = yh[i][j] = sh[i][j] = 0.0f;
-            if (c < a.V) {
-                if (a.pre) {
-                    unpack8(__ldcs(reinterpret_cast<const uint4*>(a.dx) + base + c), b[i]);
-                    load_stream<kF32>(a.s, base + c, sh[i]);
-                }
-                if (a.ds) load_stream<kF32>(a.ds, base + c, g[i]);
-                if (a.y) unpack8(__ldcs(reinterpret_cast<const uint4*>(a.y) + base + c), yh[i]);
-            }
-        }
-        if (a.pre) {
-            const float r = a.rstd_pre[row];
-            float sum = 0.0f;
+    // words of a vector in a stage: dx, y, then s and ds
+    auto fetch = [&](int row, uint32_t stage) {
+        if (row < a.N) {
+            const size_t at16 = (size_t)row * V * 16, at_r = (size_t)row * V * kRowR;
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                const int c = tid + i * lanes;
-                if (c < a.V) {
-                    float w[8];
-                    load_channel(a.w_pre, c, w);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        sh[i][j] *= r;
-                        t_pre[i][j] += b[i][j] * sh[i][j];
-                        b[i][j] *= w[j];
-                        sum += b[i][j] * sh[i][j];
-                    }
+                const uint32_t c = tid + i * lanes, at = stage + i * kPerV * pitch;
+                if (pre) {
+                    ring_copy<false>(at, pitch, reinterpret_cast<const char*>(a.dx) + at16, tid, c,
+                                     V);
+                    ring_copy<kF32>(at + 2 * pitch, pitch,
+                                    reinterpret_cast<const char*>(a.s) + at_r, tid, c, V);
                 }
+                if (has_ds)
+                    ring_copy<kF32>(at + (2 + kWordsR) * pitch, pitch,
+                                    reinterpret_cast<const char*>(a.ds) + at_r, tid, c, V);
+                if (has_y)
+                    ring_copy<false>(at + pitch, pitch,
+                                     reinterpret_cast<const char*>(a.y) + at16, tid, c, V);
             }
-            sum = row_sum<kWarpRow>(sum, part[buf][0]) * a.inv_h;
+        }
+        ring_commit();
+    };
+    if (kRing)
+        for (int p = 0; p < kStages - 1; ++p)
+            fetch(rows.first + p * rows.step, ring0 + p * stage_bytes);
+
+    const float* gate_c = a.gate_kind == MOE_GATE_CHANNEL ? a.gate : nullptr;
+    const float* w_post = a.post ? a.w_post : nullptr;
+    f2 cw[kV][4], wp[kV][4];
+    auto channels = [&](int i) {
+        const uint32_t c = tid + i * lanes;
+        if (c < V) {
+            load_scale(gate_c, w_post, c, cw[i]);
+            load_channel(a.w_pre, c, wp[i]);
+        }
+    };
+    if (kKeep) {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) channels(i);
+    }
+
+    int buf = 0, stage = 0;
+    for (int row = rows.first; row - rows.lead < a.N; row += rows.step, buf ^= 1) {
+        const bool live = kRing || row < a.N;
+        const float r_pre = pre && live ? a.rstd_pre[row] : 0.0f;
+        const float r_post = a.post && live ? a.rstd_post[row] : 1.0f;
+        const float token_gate = a.gate_kind == MOE_GATE_TOKEN && live ? a.gate[row] : 1.0f;
+        const size_t at16 = (size_t)row * V * 16, at_r = (size_t)row * V * kRowR;
+        const uint32_t slot = ring0 + stage * stage_bytes + tid * 16;
+        if constexpr (kRing) {
+            __syncwarp();  // every lane has read what this overwrites
+            const int next = stage == 0 ? kStages - 1 : stage - 1;
+            fetch(row + (kStages - 1) * rows.step, ring0 + next * stage_bytes);
+            ring_wait<kStages - 1>();
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+        }
+        Raw<false> rx[kV], ry[kV];
+        Raw<kF32> rs[kV], rd[kV];
+        auto read = [&](int i) {
+            const uint32_t c = tid + i * lanes, at = slot + i * kPerV * pitch;
+            if (!kFull) {
+                rx[i].w[0] = ry[i].w[0] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < kWordsR; ++j)
+                    rs[i].w[j] = rd[i].w[j] = make_uint4(0, 0, 0, 0);
+            }
+            if (pre) {
+                rx[i] = kRing ? ring_read<false>(at, pitch)
+                              : load_global<false>(
+                                    reinterpret_cast<const char*>(a.dx) + at16, c);
+                rs[i] = kRing ? ring_read<kF32>(at + 2 * pitch, pitch)
+                              : load_global<kF32>(reinterpret_cast<const char*>(a.s) + at_r, c);
+            }
+            if (has_ds)
+                rd[i] = kRing ? ring_read<kF32>(at + (2 + kWordsR) * pitch, pitch)
+                              : load_global<kF32>(reinterpret_cast<const char*>(a.ds) + at_r, c);
+            if (has_y)
+                ry[i] = kRing ? ring_read<false>(at + pitch, pitch)
+                              : load_global<false>(reinterpret_cast<const char*>(a.y) + at16, c);
+        };
+        if (!kRing) {
 #pragma unroll
             for (int i = 0; i < kV; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) g[i][j] += r * (b[i][j] - sh[i][j] * sum);
+                if (tid + i * lanes < V && live) read(i);
         }
-        if (a.dresidual) {
+        f2 acc[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const int c = tid + i * lanes;
-                if (c < a.V) {
-                    float o[8];
+        for (int i = 0; i < kV; ++i) {
+            if (tid + i * lanes < V && live) {
+                if (kRing) read(i);
+                if (!kKeep) channels(i);
+                f2 b[4], sv[4], y[4], d[4];
+                unpack(rx[i], b);
+                unpack(rs[i], sv);
+                unpack(ry[i], y);
+                unpack(rd[i], d);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = a.alpha * g[i][j];
-                    store_stream<kF32>(a.dresidual, base + c, o);
+                for (int j = 0; j < 4; ++j) {
+                    b[j] = mul2(b[j], both(r_pre));
+                    t_pre[i][j] = fma2(b[j], sv[j], t_pre[i][j]);
+                    b[j] = mul2(b[j], wp[i][j]);           // r_pre b
+                    const f2 q = mul2(y[j], cw[i][j]);     // cw yh / r_post
+                    acc[0] = fma2(b[j], sv[j], acc[0]);
+                    acc[1] = fma2(q, d[j], acc[1]);
+                    acc[2] = fma2(q, b[j], acc[2]);
+                    acc[3] = fma2(q, sv[j], acc[3]);
                 }
             }
         }
-        if (!a.y) continue;
-        const float r = a.post ? a.rstd_post[row] : 1.0f;
-        const float token_gate = a.gate_kind == MOE_GATE_TOKEN ? a.gate[row] : 1.0f;
-        // sum: of g yh w_post (without the token's gate, which is the row's own)
-        float sum = 0.0f;
+        float sum[4] = {across(acc[0]), across(acc[1]), across(acc[2]), across(acc[3])};
+        row_sum4<kLanes>(sum, part[buf]);
+        const float m = sum[0] * a.inv_h;              // mean of b sh
+        const float rm = -r_pre * r_pre * m;           // g = ds + r b + rm s
+        const float dot = r_post * (sum[1] + sum[2] + rm * sum[3]);
+        const float mean = a.post ? dot * a.inv_h : 0.0f;
+        const float tgr = token_gate * r_post, tm = -tgr * r_post * mean;
+        if (tid == 0 && live && a.dgate_token) a.dgate_token[row] = dot;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const int c = tid + i * lanes;
-            if (c < a.V) {
-                float w[8], ch[8];
-                load_channel(a.post ? a.w_post : nullptr, c, w);
-                load_channel(a.gate_kind == MOE_GATE_CHANNEL ? a.gate : nullptr, c, ch);
+            const uint32_t c = tid + i * lanes;
+            if (c < V && live) {
+                if (kRing) read(i);
+                if (!kKeep) channels(i);
+                f2 b[4], sv[4], g[4], o[4];
+                unpack(rx[i], b);
+                unpack(rs[i], sv);
+                unpack(rd[i], g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    yh[i][j] *= r;
-                    t_post[i][j] += token_gate * g[i][j] * yh[i][j];
-                    b[i][j] = ch[j] * g[i][j] * w[j];
-                    sum += b[i][j] * yh[i][j];
+                for (int j = 0; j < 4; ++j) {
+                    g[j] = fma2(mul2(b[j], both(r_pre)), wp[i][j], g[j]);
+                    g[j] = fma2(sv[j], both(rm), g[j]);
+                    o[j] = mul2(both(a.alpha), g[j]);
                 }
-            }
-        }
-        float mean = 0.0f;
-        if (a.post || a.dgate_token) {
-            sum = row_sum<kWarpRow>(sum, part[buf][1]);
-            mean = a.post ? sum * a.inv_h : 0.0f;
-            if (tid == 0 && a.dgate_token) a.dgate_token[row] = sum;
-        }
+                if (kFull || a.dresidual)
+                    store_global<kF32>(reinterpret_cast<char*>(a.dresidual) + at_r, c, o, a.wide);
+                if (has_y) {
+                    f2 y[4];
+                    unpack(ry[i], y);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int c = tid + i * lanes;
-            if (c < a.V) {
-                float o[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    o[j] = token_gate * r * (b[i][j] - yh[i][j] * mean);
-                __stcs(reinterpret_cast<uint4*>(a.dy) + base + c, pack8(o));
+                    for (int j = 0; j < 4; ++j) {
+                        const f2 t = mul2(g[j], both(tgr));  // gate g r_post
+                        t_post[i][j] = fma2(t, y[j], t_post[i][j]);
+                        o[j] = fma2(y[j], both(tm), mul2(cw[i][j], t));
+                    }
+                    store_global<false>(reinterpret_cast<char*>(a.dy) + at16, c, o, 0);
+                }
             }
         }
     }
 
-    // the block's column sums: g yh (times the token's gate), dx sh
-    const int H = a.V * 8;
+    // the block's column sums: gate g yh (the token's gate), dx sh
+    const uint32_t H = V * 8;
     float* out = a.partial + (size_t)blockIdx.x * 2 * H;
-    if (kWarpRow) {
-        float* mine = cols + (size_t)sub * 2 * H;
+    float* mine = kRing ? out : cols + (size_t)(threadIdx.x / lanes) * 2 * H;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int c = tid + i * lanes;
-            if (c < a.V) {
+    for (int i = 0; i < kV; ++i) {
+        const uint32_t c = tid + i * lanes;
+        if (c < V) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    mine[c * 8 + j] = t_post[i][j];
-                    mine[H + c * 8 + j] = t_pre[i][j];
-                }
+            for (int j = 0; j < 4; ++j) {
+                *reinterpret_cast<f2*>(mine + c * 8 + 2 * j) = t_post[i][j];
+                *reinterpret_cast<f2*>(mine + H + c * 8 + 2 * j) = t_pre[i][j];
             }
         }
+    }
+    if (!kRing) {
         __syncthreads();
-        for (int c = threadIdx.x; c < 2 * H; c += blockDim.x) {
+        const int groups = 32 * kRowWarps / (kLanes ? kLanes : 32);
+        for (uint32_t c = threadIdx.x; c < 2 * H; c += blockDim.x) {
             float v = 0.0f;
-            for (int w = 0; w < rows_at_once; ++w) v += cols[(size_t)w * 2 * H + c];
+            for (int w = 0; w < groups; ++w) v += cols[(size_t)w * 2 * H + c];
             out[c] = v;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int c = tid + i * lanes;
-            if (c < a.V) {
-                float4* o = reinterpret_cast<float4*>(out + c * 8);
-                o[0] = make_float4(t_post[i][0], t_post[i][1], t_post[i][2], t_post[i][3]);
-                o[1] = make_float4(t_post[i][4], t_post[i][5], t_post[i][6], t_post[i][7]);
-                o = reinterpret_cast<float4*>(out + H + c * 8);
-                o[0] = make_float4(t_pre[i][0], t_pre[i][1], t_pre[i][2], t_pre[i][3]);
-                o[1] = make_float4(t_pre[i][4], t_pre[i][5], t_pre[i][6], t_pre[i][7]);
-            }
         }
     }
 }
@@ -392,15 +662,51 @@ __global__ void __launch_bounds__(32 * kReduceRows)
 
 int row_threads(int V, int kv) { return ((V + kv - 1) / kv + 31) / 32 * 32; }
 
-// Blocks of the gradient: as many as are resident at 64 registers a thread (8 at
-// most, so that their partial sums stay few), or one for each row.
-int grad_blocks(const moe_norm_shape& s) {
-    const int V = s.H / 8;
-    const bool warp_row = V <= kWarpRowV;
-    const long long rows = warp_row ? (s.N + kRowWarps - 1LL) / kRowWarps : s.N;
-    const int fit = warp_row ? 8 : 1024 / row_threads(V, V <= 1024 ? 1 : 2);
-    const long long most = (long long)sm_count() * (fit < 8 ? fit : 8);
-    return (int)(rows < most ? (rows > 0 ? rows : 1) : most);
+// A launch of either kernel: its grid, block, lanes a row (0: the block), vectors a
+// thread, ring stages and shared memory.
+struct Plan {
+    int grid, block, lanes, kv, stages;
+    size_t smem;
+};
+
+// words: 16-byte words a thread and vector have in flight; kv: vectors a thread of
+// a block's row; most_blocks: resident on an SM (few in the gradient, so that their
+// partial sums stay few).  1024 threads are resident at 64 registers.
+Plan plan_for(int N, int V, int words, int kv, int most_blocks) {
+    Plan p;
+    if (V <= kWarpRowV) {
+        p.kv = V <= 32 ? 1 : 2;
+        p.lanes = V <= 8 ? 8 : V <= 16 ? 16 : 32;
+        p.block = 32 * kRowWarps;
+        p.stages = 0;
+        p.smem = 0;
+        const int rows = p.block / p.lanes;
+        const long long need = (N + rows - 1LL) / rows, most = 8LL * sm_count();
+        p.grid = (int)(need < most ? need : most);
+    } else {
+        p.kv = kv;
+        p.lanes = 0;
+        p.block = row_threads(V, kv);
+        int fit = 1024 / p.block < most_blocks ? 1024 / p.block : most_blocks;
+        if (fit < 1) fit = 1;
+        const size_t stage = (size_t)p.block * kv * words * 16;
+        const size_t room = (size_t)216 * 1024 / fit;
+        p.stages = stage * 3 <= room ? 3 : stage * 2 <= room ? 2 : 1;
+        p.smem = stage * p.stages;
+        const long long most = (long long)sm_count() * fit;
+        p.grid = (int)(N < most ? N : most);
+    }
+    if (p.grid < 1) p.grid = 1;
+    return p;
+}
+
+Plan forward_plan(const moe_norm_shape& s) {
+    return plan_for(s.N, s.H / 8, s.stream_type == MOE_TYPE_F32 ? 3 : 2, s.H <= 8192 ? 1 : 2, 16);
+}
+Plan grad_plan(const moe_norm_shape& s) {
+    Plan p = plan_for(s.N, s.H / 8, s.stream_type == MOE_TYPE_F32 ? 6 : 4, s.H <= 8192 ? 1 : 2, 8);
+    if (p.lanes) p.smem = (size_t)(p.block / p.lanes) * 2 * s.H * sizeof(float);
+    return p;
 }
 
 moe_status check_norm(const moe_norm_shape* s) {
@@ -412,37 +718,48 @@ moe_status check_norm(const moe_norm_shape* s) {
         return MOE_ERR_INVALID_ARG;
     if (!(s->eps >= 0.0f) || !(s->eps < 1e30f)) return MOE_ERR_INVALID_ARG;
     if (s->H % 8 != 0 || s->H > kMaxNormH) return MOE_ERR_UNSUPPORTED;
+    if (s->N > INT32_MAX - (1 << 20)) return MOE_ERR_UNSUPPORTED;  // row + the next rows' steps
     return MOE_OK;
 }
 
-template <bool kF32>
-void run_forward(const NormArgs& a, cudaStream_t st) {
-    const int V = a.V;
-    if (V <= kWarpRowV) {
-        const int blocks = (a.N + kRowWarps - 1) / kRowWarps, t = 32 * kRowWarps;
-        if (V <= 32) block_norm_kernel<1, true, kF32><<<blocks, t, 0, st>>>(a);
-        else block_norm_kernel<2, true, kF32><<<blocks, t, 0, st>>>(a);
-    } else if (V <= 1024) {
-        block_norm_kernel<1, false, kF32><<<a.N, row_threads(V, 1), 0, st>>>(a);
-    } else {
-        block_norm_kernel<2, false, kF32><<<a.N, row_threads(V, 2), 0, st>>>(a);
+template <typename Args>
+cudaError_t run(void (*kernel)(Args), const Args& a, const Plan& p, cudaStream_t st) {
+    if (p.smem > 40 * 1024) {  // with the static arrays, past the default 48 KB
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+        if (e != cudaSuccess) return e;
     }
+    kernel<<<p.grid, p.block, p.smem, st>>>(a);
+    return cudaGetLastError();
 }
 
-template <bool kF32>
-void run_grad(const NormGradArgs& a, int blocks, cudaStream_t st) {
-    const int V = a.V;
-    if (V <= kWarpRowV) {
-        const int t = 32 * kRowWarps;
-        const size_t smem = (size_t)kRowWarps * 2 * V * 8 * sizeof(float);
-        if (V <= 32) block_norm_grad_kernel<1, true, kF32><<<blocks, t, smem, st>>>(a);
-        else block_norm_grad_kernel<2, true, kF32><<<blocks, t, smem, st>>>(a);
-    } else if (V <= 1024) {
-        block_norm_grad_kernel<1, false, kF32><<<blocks, row_threads(V, 1), 0, st>>>(a);
-    } else {
-        block_norm_grad_kernel<2, false, kF32><<<blocks, row_threads(V, 2), 0, st>>>(a);
-    }
+template <bool kF32, bool kFull>
+cudaError_t run_forward(const NormArgs& a, const Plan& p, cudaStream_t st) {
+    if (p.lanes == 8) return run(block_norm_kernel<1, 8, kF32, 0, true, kFull>, a, p, st);
+    if (p.lanes == 16) return run(block_norm_kernel<1, 16, kF32, 0, true, kFull>, a, p, st);
+    if (p.lanes == 32)
+        return p.kv == 1 ? run(block_norm_kernel<1, 32, kF32, 0, true, kFull>, a, p, st)
+                         : run(block_norm_kernel<2, 32, kF32, 0, true, kFull>, a, p, st);
+    if (p.kv == 1) return run(block_norm_kernel<1, 0, kF32, 3, true, kFull>, a, p, st);
+    return p.stages == 3 ? run(block_norm_kernel<2, 0, kF32, 3, false, kFull>, a, p, st)
+                         : run(block_norm_kernel<2, 0, kF32, 2, false, kFull>, a, p, st);
 }
+
+template <bool kF32, bool kFull>
+cudaError_t run_grad(const NormGradArgs& a, const Plan& p, cudaStream_t st) {
+    if (p.lanes == 8) return run(block_norm_grad_kernel<1, 8, kF32, 0, true, kFull>, a, p, st);
+    if (p.lanes == 16) return run(block_norm_grad_kernel<1, 16, kF32, 0, true, kFull>, a, p, st);
+    if (p.lanes == 32)
+        return p.kv == 1 ? run(block_norm_grad_kernel<1, 32, kF32, 0, true, kFull>, a, p, st)
+                         : run(block_norm_grad_kernel<2, 32, kF32, 0, true, kFull>, a, p, st);
+    if (p.kv == 1)
+        return p.stages == 3 ? run(block_norm_grad_kernel<1, 0, kF32, 3, true, kFull>, a, p, st)
+                             : run(block_norm_grad_kernel<1, 0, kF32, 2, true, kFull>, a, p, st);
+    return p.stages >= 2 ? run(block_norm_grad_kernel<2, 0, kF32, 2, false, kFull>, a, p, st)
+                         : run(block_norm_grad_kernel<2, 0, kF32, 1, false, kFull>, a, p, st);
+}
+
+inline int aligned32(const void* p) { return ((uintptr_t)p & 31u) == 0; }
 
 }  // namespace
 }  // namespace moe
@@ -453,7 +770,7 @@ extern "C" {
 
 size_t moe_norm_workspace_bytes(const moe_norm_shape* shape) {
     if (check_norm(shape) != MOE_OK) return 0;
-    return align256((size_t)grad_blocks(*shape) * 2 * shape->H * sizeof(float));
+    return align256((size_t)grad_plan(*shape).grid * 2 * shape->H * sizeof(float));
 }
 
 moe_status moe_block_norm(const uint16_t* y, const void* residual, const float* w_post,
@@ -472,10 +789,14 @@ moe_status moe_block_norm(const uint16_t* y, const void* residual, const float* 
         return MOE_ERR_INVALID_ARG;
     const NormArgs a{y,         residual, w_post,      gate, w_pre, s,   x,
                      rstd_post, rstd_pre, shape->N,    shape->H / 8,     post, pre, shape->gate,
-                     shape->eps, shape->residual_scale, 1.0f / (float)shape->H};
-    if (shape->stream_type == MOE_TYPE_F32) run_forward<true>(a, as_stream(stream));
-    else run_forward<false>(a, as_stream(stream));
-    return cuda_status(cudaGetLastError());
+                     aligned32(s), shape->eps, shape->residual_scale, 1.0f / (float)shape->H};
+    const Plan p = forward_plan(*shape);
+    const bool f32 = shape->stream_type == MOE_TYPE_F32, full = y && post && pre && s;
+    cudaStream_t st = as_stream(stream);
+    return cuda_status(full ? (f32 ? run_forward<true, true>(a, p, st)
+                                   : run_forward<false, true>(a, p, st))
+                            : (f32 ? run_forward<true, false>(a, p, st)
+                                   : run_forward<false, false>(a, p, st)));
 }
 
 moe_status moe_block_norm_grad(const void* ds, const uint16_t* dx, const uint16_t* y,
@@ -514,16 +835,18 @@ moe_status moe_block_norm_grad(const void* ds, const uint16_t* dx, const uint16_
         return MOE_ERR_INVALID_ARG;
     const NormGradArgs a{ds, dx, y, s, w_post, gate, w_pre, rstd_post, rstd_pre, dy, dresidual,
                          by_token ? dgate : nullptr, static_cast<float*>(ws), shape->N,
-                         shape->H / 8, post, pre, shape->gate, shape->residual_scale,
-                         1.0f / (float)shape->H};
-    const int blocks = grad_blocks(*shape);
-    if (shape->stream_type == MOE_TYPE_F32) run_grad<true>(a, blocks, st);
-    else run_grad<false>(a, blocks, st);
-    MOE_TRY(cuda_status(cudaGetLastError()));
+                         shape->H / 8, post, pre, shape->gate, aligned32(dresidual),
+                         shape->residual_scale, 1.0f / (float)shape->H};
+    const Plan p = grad_plan(*shape);
+    const bool f32 = shape->stream_type == MOE_TYPE_F32, full = y && pre && ds && dresidual;
+    MOE_TRY(cuda_status(full ? (f32 ? run_grad<true, true>(a, p, st)
+                                    : run_grad<false, true>(a, p, st))
+                             : (f32 ? run_grad<true, false>(a, p, st)
+                                    : run_grad<false, false>(a, p, st))));
     if (dw_post || dw_pre || (dgate && by_channel)) {
         const dim3 grid((shape->H + 31) / 32, dw_pre ? 2 : 1);
         block_norm_reduce_kernel<<<grid, 32 * kReduceRows, 0, st>>>(
-            a.partial, blocks, shape->H, by_channel ? gate : nullptr, post ? w_post : nullptr,
+            a.partial, p.grid, shape->H, by_channel ? gate : nullptr, post ? w_post : nullptr,
             dw_post, by_channel ? dgate : nullptr, dw_pre, accumulate != 0);
         MOE_TRY(cuda_status(cudaGetLastError()));
     }

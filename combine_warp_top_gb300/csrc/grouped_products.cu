@@ -342,7 +342,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                   abort_flag, err))
                         break;
                 }
-                if (queue_publish(ctl, i, tile_counter, total, abort_flag, err) < 0) break;
+                if (queue_publish(ctl, i, tile_counter, total, abort_flag, err,
+                                  (int)(gridDim.x / 2)) < 0)
+                    break;
             }
         } else if (kW && warp == 3) {
             // ---------------- block ends (both CTAs) ----------------
@@ -534,10 +536,17 @@ moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap&
                   const GemmGroup& g, long long tiles, int K, int m_out, int n_out, void* out,
                   bool accumulate, cudaStream_t st) {
     if (tiles >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
-    if (cudaFuncSetAttribute(grouped_product_kernel<kMode, OutT>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kSmemBytes) != cudaSuccess)
-        return MOE_ERR_CUDA;
+    // the attribute holds for the process and device: set once for each
+    static bool set[64] = {false};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dev >= 64 || !set[dev]) {
+        if (cudaFuncSetAttribute(grouped_product_kernel<kMode, OutT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kSmemBytes) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        if (dev < 64) set[dev] = true;
+    }
     const long long pairs_max = sm_count() / 2;
     const long long pairs = tiles < pairs_max ? tiles : pairs_max;
     const int chain = sizeof(OutT) == 4 ? kChainBlocks : 1 << 30;

@@ -18,14 +18,16 @@ constexpr int kQ = 8;  // slots of the tile queues
 
 // Leader's scheduler thread: wait until queue slot i % kQ is free in both CTAs, take
 // the next tile from the counter (-1 once every tile is taken) and publish it
-// to both CTAs.  Returns the tile, or -2 if the wait gave up.
+// to both CTAs.  Returns the tile, or -2 if the wait gave up.  first: the pair's
+// first tile is its own index and the counter hands out the ones after the
+// `first` pairs (0: every tile comes from the counter).
 template <typename Ctl>
 __device__ __forceinline__ int queue_publish(Ctl* ctl, int i, int* counter, int total,
-                                             volatile int* abort, int* err) {
+                                             volatile int* abort, int* err, int first = 0) {
     const int slot = i % kQ;
     const uint32_t ph = (uint32_t)(i / kQ) & 1u;
     if (!wait_bar(smem_u32(&ctl->tq_empty[slot]), ph ^ 1u, abort, err)) return -2;
-    int t = atomicAdd(counter, 1);
+    int t = first > 0 && i == 0 ? (int)(blockIdx.x / 2) : first + atomicAdd(counter, 1);
     if (t >= total) t = -1;
     ctl->tile_q[slot] = t;
     st_shared_cluster(mapa_shared(smem_u32(&ctl->tile_q[slot]), 1), t);

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from dataclasses import dataclass
 
@@ -182,10 +183,16 @@ def _lay(layout, shape):
     return ctypes.byref(layout.c)
 
 
+# The current stream's handle without a torch.cuda.Stream object around it (3 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 # ---- shapes, layouts, buffers ----------------------------------------------------------
@@ -206,6 +213,11 @@ class Shape:
     # layout of the expert weights the calls take: "row_major" (nn.Linear) or
     # "packed" (moe_pack_weights); see moe_weight_layout
     weights: str = "row_major"
+
+    @functools.cached_property
+    def ref(self):
+        """The C struct by reference, made once for this shape."""
+        return ctypes.byref(self.c())
 
     def c(self) -> MoeShape:
         if self.gemm not in GEMM_KERNELS:
@@ -537,7 +549,18 @@ def _exact(t, dtype, shape, what):
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _ptr(t)
+    if not t.is_cuda:
+        raise ValueError("libmoe takes device tensors")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _bytes(ws):
+    """(address, size in bytes) of a workspace tensor."""
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous device tensor")
+    return ws.data_ptr(), ws.nbytes
 
 
 def _out_type(t, what):
@@ -565,8 +588,8 @@ def moe_grouped_gemm(rows, layout: Layout, shape: Shape, w, out, ws, stream=None
     ot, R = _out_type(out, "out"), shape.R
     _check(load().moe_grouped_gemm(
         _exact(rows, torch.bfloat16, (R, ci), "rows"), _lay(layout, shape),
-        ctypes.byref(shape.c()), ci, co, _exact(w, torch.bfloat16, w.shape, "w"),
-        _exact(out, out.dtype, (R, co), "out"), ot, *_ws(ws), _stream(stream)),
+        shape.ref, ci, co, _exact(w, torch.bfloat16, w.shape, "w"),
+        _exact(out, out.dtype, (R, co), "out"), ot, *_bytes(ws), _stream(stream)),
         "moe_grouped_gemm")
 
 
@@ -576,8 +599,8 @@ def moe_grouped_gemm_input_grad(dout, layout: Layout, shape: Shape, w, drows, ws
     ot, R = _out_type(drows, "drows"), shape.R
     _check(load().moe_grouped_gemm_input_grad(
         _exact(dout, torch.bfloat16, (R, co), "dout"), _lay(layout, shape),
-        ctypes.byref(shape.c()), ci, co, _exact(w, torch.bfloat16, w.shape, "w"),
-        _exact(drows, drows.dtype, (R, ci), "drows"), ot, *_ws(ws), _stream(stream)),
+        shape.ref, ci, co, _exact(w, torch.bfloat16, w.shape, "w"),
+        _exact(drows, drows.dtype, (R, ci), "drows"), ot, *_bytes(ws), _stream(stream)),
         "moe_grouped_gemm_input_grad")
 
 
@@ -590,8 +613,8 @@ def moe_grouped_gemm_weight_grad(dout, rows, layout: Layout, shape: Shape, dw, w
     _check(load().moe_grouped_gemm_weight_grad(
         _exact(dout, torch.bfloat16, (R, co), "dout"),
         _exact(rows, torch.bfloat16, (R, ci), "rows"), _lay(layout, shape),
-        ctypes.byref(shape.c()), ci, co, _exact(dw, dw.dtype, dw.shape, "dw"), ot,
-        int(bool(accumulate)), *_ws(ws), _stream(stream)), "moe_grouped_gemm_weight_grad")
+        shape.ref, ci, co, _exact(dw, dw.dtype, dw.shape, "dw"), ot,
+        int(bool(accumulate)), *_bytes(ws), _stream(stream)), "moe_grouped_gemm_weight_grad")
 
 
 def moe_swiglu(gu, topk_w, layout: Layout, shape: Shape, h, stream=None):
@@ -601,7 +624,7 @@ def moe_swiglu(gu, topk_w, layout: Layout, shape: Shape, h, stream=None):
     _check(load().moe_swiglu(
         _exact(gu, torch.bfloat16, (s.R, 2 * s.I), "gu"),
         _exact(topk_w, torch.float32, (s.N, s.k), "topk_w"), _lay(layout, s),
-        ctypes.byref(s.c()), _exact(h, torch.bfloat16, (s.R, s.I), "h"), _stream(stream)),
+        s.ref, _exact(h, torch.bfloat16, (s.R, s.I), "h"), _stream(stream)),
         "moe_swiglu")
 
 
@@ -612,7 +635,7 @@ def moe_swiglu_grad(dh, gu, topk_w, layout: Layout, shape: Shape, dgu, dtopk_w, 
         _exact(dh, torch.bfloat16, (s.R, s.I), "dh"),
         _exact(gu, torch.bfloat16, (s.R, 2 * s.I), "gu"),
         _exact(topk_w, torch.float32, (s.N, s.k), "topk_w"), _lay(layout, s),
-        ctypes.byref(s.c()), _exact(dgu, torch.bfloat16, (s.R, 2 * s.I), "dgu"),
+        s.ref, _exact(dgu, torch.bfloat16, (s.R, 2 * s.I), "dgu"),
         _exact(dtopk_w, torch.float32, (s.N, s.k), "dtopk_w"), _stream(stream)),
         "moe_swiglu_grad")
 
@@ -623,7 +646,7 @@ def moe_route_grad(topk_ids, topk_w, dtopk_w, shape: Shape, dlogits, stream=None
     _check(load().moe_route_grad(
         _exact(topk_ids, torch.int32, (s.N, s.k), "topk_ids"),
         _exact(topk_w, torch.float32, (s.N, s.k), "topk_w"),
-        _exact(dtopk_w, torch.float32, (s.N, s.k), "dtopk_w"), ctypes.byref(s.c()),
+        _exact(dtopk_w, torch.float32, (s.N, s.k), "dtopk_w"), s.ref,
         _exact(dlogits, torch.float32, (s.N, s.E), "dlogits"), _stream(stream)),
         "moe_route_grad")
 
@@ -633,7 +656,7 @@ def _route_logits_grad(name, logits, topk_ids, dtopk_w, shape, dlogits, stream):
     _check(getattr(load(), name)(
         _exact(logits, torch.float32, (s.N, s.E), "logits"),
         _exact(topk_ids, torch.int32, (s.N, s.k), "topk_ids"),
-        _exact(dtopk_w, torch.float32, (s.N, s.k), "dtopk_w"), ctypes.byref(s.c()),
+        _exact(dtopk_w, torch.float32, (s.N, s.k), "dtopk_w"), s.ref,
         _exact(dlogits, torch.float32, (s.N, s.E), "dlogits"), _stream(stream)), name)
 
 
@@ -664,6 +687,11 @@ class NormShape:
     eps: float = 1e-6
     residual_scale: float = 1.0
 
+    @functools.cached_property
+    def ref(self):
+        """The C struct by reference, made once for this shape."""
+        return ctypes.byref(self.c())
+
     def c(self) -> MoeNormShape:
         if self.gate not in GATES:
             raise ValueError(f"gate must be one of {sorted(GATES)}")
@@ -682,7 +710,7 @@ class NormShape:
 
 
 def moe_norm_workspace_bytes(shape: NormShape) -> int:
-    return int(load().moe_norm_workspace_bytes(ctypes.byref(shape.c())))
+    return int(load().moe_norm_workspace_bytes(shape.ref))
 
 
 def norm_workspace(shape: NormShape, device="cuda") -> torch.Tensor:
@@ -700,7 +728,7 @@ def moe_block_norm(y, residual, w_post, gate, w_pre, shape: NormShape, s, x, rst
     _check(load().moe_block_norm(
         _exact(y, torch.bfloat16, nh, "y"), _exact(residual, st, nh, "residual"),
         _exact(w_post, f32, h, "w_post"), _exact(gate, f32, n.gate_shape(), "gate"),
-        _exact(w_pre, f32, h, "w_pre"), ctypes.byref(n.c()), _exact(s, st, nh, "s"),
+        _exact(w_pre, f32, h, "w_pre"), n.ref, _exact(s, st, nh, "s"),
         _exact(x, torch.bfloat16, nh, "x"), _exact(rstd_post, f32, (n.N,), "rstd_post"),
         _exact(rstd_pre, f32, (n.N,), "rstd_pre"), _stream(stream)), "moe_block_norm")
 
@@ -717,9 +745,9 @@ def moe_block_norm_grad(ds, dx, y, s, w_post, gate, w_pre, rstd_post, rstd_pre,
         _exact(s, st, nh, "s"), _exact(w_post, f32, h, "w_post"),
         _exact(gate, f32, n.gate_shape(), "gate"), _exact(w_pre, f32, h, "w_pre"),
         _exact(rstd_post, f32, (n.N,), "rstd_post"), _exact(rstd_pre, f32, (n.N,), "rstd_pre"),
-        ctypes.byref(n.c()), _exact(dy, bf, nh, "dy"), _exact(dresidual, st, nh, "dresidual"),
+        n.ref, _exact(dy, bf, nh, "dy"), _exact(dresidual, st, nh, "dresidual"),
         _exact(dw_post, f32, h, "dw_post"), _exact(dgate, f32, n.gate_shape(), "dgate"),
-        _exact(dw_pre, f32, h, "dw_pre"), int(bool(accumulate)), *_ws(ws), _stream(stream)),
+        _exact(dw_pre, f32, h, "dw_pre"), int(bool(accumulate)), *_bytes(ws), _stream(stream)),
         "moe_block_norm_grad")
 
 
