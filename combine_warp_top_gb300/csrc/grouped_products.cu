@@ -39,7 +39,6 @@
 #include "../../include/moe_train.h"
 #include "api_checks.cuh"
 #include "moe_internal.cuh"
-#include "pair_queue.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -53,7 +52,6 @@ constexpr int BT = 256;    // rows and columns of a pair's tile
 constexpr int BH = 128;    // rows of A and of B that a CTA of the pair holds
 constexpr int BK = 64;
 constexpr int UMMA_K = 16;
-constexpr int kStages = 6;
 constexpr int kAccs = 2;
 constexpr int kTmemCols = BT * kAccs;
 constexpr int OP_BYTES = BH * BK * 2;   // one operand of one stage in one CTA
@@ -62,81 +60,244 @@ constexpr int STAGE_BYTES = 2 * OP_BYTES;
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
 constexpr int kEpilogueCols = BT / 2;  // columns of one epilogue warp
-// Registers a thread: 384 x 168 at launch = 128 x 72 + 256 x 208 + 2048 to spare.
-constexpr int kRegsOther = 72, kRegsEpilogue = 208;
-// Output staging of an epilogue warp: 32 rows of 64 bytes, 64-byte swizzle.
-constexpr int kSliceBytes = 64;
-constexpr int kStagingBytes = 32 * kSliceBytes;
+// Registers a thread: 384 x 168 at launch = 128 x 88 + 256 x 208.
+constexpr int kRegsOther = 88, kRegsEpilogue = 208;
+constexpr int kStages = 6;
+constexpr int kAhead = 2;  // tiles the scheduler publishes ahead of the leader's producer
+// Rows of 128 bytes of an epilogue warp's output staging; the experts' tables take
+// the room for more where they are in shared memory.
+constexpr int staging_rows(int mode) { return mode == kWeightsGrad ? 32 : 16; }
 constexpr int kChainBlocks = 8;  // k-blocks added up in one accumulator (fp32 outputs)
 
-struct Ctl {
-    uint64_t full[kStages];   // leader: both CTAs' operands of a stage are there
-    uint64_t empty[kStages];  // each CTA: its stage may be refilled
-    uint64_t land[kStages];   // each CTA: its copies of a segment's last block have landed
-    uint64_t tfull[kAccs];    // each CTA: accumulator ready
-    uint64_t tempty[kAccs];   // leader: accumulator drained by both CTAs
-    uint64_t done;            // leader: every issued MMA retired
-    uint64_t tq_full[kQ];     // tile queues: pair_queue.cuh
-    uint64_t tq_empty[kQ];
-    int tile_q[kQ];
-    uint64_t tq_taken[kQ];
-    uint64_t lq_full[kQ];
-    uint64_t lq_empty[kQ];
-    int local_q[kQ];
+// A tile: its expert (-1: no more tiles) and the expert's rows, its row and column
+// block, and the k-blocks of its contraction.  Decoded once by the scheduler and
+// handed to the other roles through the tile queues: the divisions and the search
+// for the expert would cost each role some 800 cycles a tile.
+struct __align__(16) Tile {
+    int e, off, cnt, kblocks;
+    int mb, nb, pad0, pad1;
+};
+constexpr int kQ = 8;  // slots of a tile queue
+
+struct Barriers {
+    Tile queue[kQ];             // each CTA: the tiles in order, from the leader's scheduler
+    Tile local[kQ];             // peer: the tiles its producer forwards to its other warps
+    uint64_t full[kStages];     // leader: both CTAs' operands of a stage are there
+    uint64_t empty[kStages];    // each CTA: its stage may be refilled
+    uint64_t land[kStages];     // each CTA: its copies of a segment's last block are there
+    uint64_t tfull[kAccs];      // each CTA: accumulator ready
+    uint64_t tempty[kAccs];     // leader: accumulator drained by both CTAs
+    uint64_t done;              // leader: every issued MMA retired
+    uint64_t q_full[kQ];        // each CTA: slot of queue written
+    uint64_t q_empty[kQ];       // leader: slot read by every reader of both CTAs
+    uint64_t q_taken[kQ];       // leader: its producer has taken the slot's tile
+    uint64_t l_full[kQ];        // peer: slot of local written
+    uint64_t l_empty[kQ];       // peer: slot of local read by its warps
     uint32_t tmem_base;
     int abort;
+};
+// The experts' tables, for the scheduler's search (not in a weights' gradient, where
+// every expert has the same number of tiles).
+struct Tables {
     int prefix[kMaxE + 1];
     int offs[kMaxE];
     int cnts[kMaxE];
 };
-
-constexpr size_t kCtlBytes = (sizeof(Ctl) + 15) & ~size_t(15);
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * STAGE_BYTES +
-                              (size_t)kEpilogueWarps * kStagingBytes + kCtlBytes;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of one block");
-
-// A tile: its expert, its row and column block, and the k-blocks of its contraction.
-struct Tile {
-    int e, mb, nb, kblocks;
+template <int kMode>
+struct Ctl : Barriers {
+    Tables tables;
 };
+template <>
+struct Ctl<kWeightsGrad> : Barriers {};
 
 template <int kMode>
-__device__ __forceinline__ Tile tile_of(const Ctl* ctl, int E, int MB, int NB, int KB, int tile) {
-    Tile t;
-    if (kMode == kWeightsGrad) {
-        t.e = tile / (MB * NB);
-        const int local = tile - t.e * MB * NB;
-        t.mb = local / NB;
-        t.nb = local - t.mb * NB;
-        t.kblocks = (ctl->cnts[t.e] + BK - 1) / BK;
-    } else {
-        decode_tile(ctl->prefix, E, NB, BT, BT, tile, t.e, t.mb, t.nb);
-        t.kblocks = KB;
+constexpr size_t smem_bytes() {
+    constexpr size_t n = 1024 + (size_t)kStages * STAGE_BYTES +
+                         (size_t)kEpilogueWarps * staging_rows(kMode) * 128 +
+                         ((sizeof(Ctl<kMode>) + 15) & ~size_t(15));
+    static_assert(n <= 227 * 1024, "shared memory of one block");
+    return n;
+}
+
+// Spin for about `cycles` SM clocks (lets copies in flight land on abort).
+__device__ __forceinline__ void spin(long long cycles) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < cycles) {
     }
+}
+
+__device__ __forceinline__ Tile read_slot(const Tile* p) {
+    const volatile int* q = reinterpret_cast<const volatile int*>(p);
+    Tile t;
+    t.e = q[0];
+    t.off = q[1];
+    t.cnt = q[2];
+    t.kblocks = q[3];
+    t.mb = q[4];
+    t.nb = q[5];
+    t.pad0 = t.pad1 = 0;
     return t;
 }
 
+// One thread takes tile i of the queue; false when there is none or the wait gave up.
+// In the leader every role reads the leader's queue.  In the peer only its producer
+// does and forwards each tile through the local queue, so that a tile crosses between
+// the CTAs once each way.
+__device__ __forceinline__ bool take(Barriers* c, int i, bool leader, volatile int* abort,
+                                     int* err, Tile& t) {
+    const int slot = i % kQ;
+    const uint32_t ph = (uint32_t)(i / kQ) & 1u, full = smem_u32(&c->q_full[slot]);
+    if (!(leader ? wait_bar(full, ph, abort, err) : wait_bar_cluster(full, ph, abort, err)))
+        return false;
+    t = read_slot(&c->queue[slot]);
+    const uint32_t empty = smem_u32(&c->q_empty[slot]);
+    if (leader)
+        mbar_arrive(empty);
+    else
+        mbar_arrive_remote(mapa_shared(empty, 0));
+    return t.e >= 0;
+}
+__device__ __forceinline__ bool take_local(Barriers* c, int i, volatile int* abort, int* err,
+                                           Tile& t) {
+    const int slot = i % kQ;
+    const uint32_t ph = (uint32_t)(i / kQ) & 1u;
+    if (!wait_bar(smem_u32(&c->l_full[slot]), ph, abort, err)) return false;
+    t = read_slot(&c->local[slot]);
+    mbar_arrive(smem_u32(&c->l_empty[slot]));
+    return t.e >= 0;
+}
+// Peer's producer: tile i (or its end) on to the peer's other warps.
+__device__ __forceinline__ bool forward(Barriers* c, int i, const Tile& t, volatile int* abort,
+                                        int* err) {
+    const int slot = i % kQ;
+    const uint32_t ph = (uint32_t)(i / kQ) & 1u;
+    if (!wait_bar(smem_u32(&c->l_empty[slot]), ph ^ 1u, abort, err)) return false;
+    c->local[slot] = t;
+    mbar_arrive(smem_u32(&c->l_full[slot]));
+    return true;
+}
+// Leader's scheduler: tile i (or the end) into both CTAs' queues.
+__device__ __forceinline__ bool publish(Barriers* c, int i, const Tile& t, volatile int* abort,
+                                        int* err) {
+    const int slot = i % kQ;
+    const uint32_t ph = (uint32_t)(i / kQ) & 1u, full = smem_u32(&c->q_full[slot]);
+    if (!wait_bar(smem_u32(&c->q_empty[slot]), ph ^ 1u, abort, err)) return false;
+    c->queue[slot] = t;
+    mbar_arrive(full);
+    const uint32_t bar = mapa_shared(full, 1), at = mapa_shared(smem_u32(&c->queue[slot]), 1);
+    mbar_expect_tx_remote(bar, sizeof(Tile));
+    st_async4(at, bar, t.e, t.off, t.cnt, t.kblocks);
+    st_async4(at + 16, bar, t.mb, t.nb, 0, 0);
+    return true;
+}
+// The next tile of a whole warp.
+__device__ __forceinline__ bool warp_take(Barriers* c, int i, bool leader, volatile int* abort,
+                                          int* err, Tile& t) {
+    int more = 0;
+    if ((threadIdx.x & 31) == 0)
+        more = leader ? take(c, i, true, abort, err, t) : take_local(c, i, abort, err, t);
+    if (!__shfl_sync(0xffffffffu, more, 0)) return false;
+    t.e = __shfl_sync(0xffffffffu, t.e, 0);
+    t.off = __shfl_sync(0xffffffffu, t.off, 0);
+    t.cnt = __shfl_sync(0xffffffffu, t.cnt, 0);
+    t.kblocks = __shfl_sync(0xffffffffu, t.kblocks, 0);
+    t.mb = __shfl_sync(0xffffffffu, t.mb, 0);
+    t.nb = __shfl_sync(0xffffffffu, t.nb, 0);
+    return true;
+}
+
+// Expert e's segment; one that leaves the R rows is reported and taken as empty.
+__device__ __forceinline__ void segment(const int32_t* offsets, const int32_t* counts, int e,
+                                        int R, int* err, int* off, int* cnt) {
+    int o = offsets[e], c = counts[e];
+    if (o < 0 || c < 0 || c > R || o > R - c) {
+        set_error(err, MOE_ERR_INVALID_ARG);
+        o = c = 0;
+    }
+    *off = o;
+    *cnt = c;
+}
+
+// A warp's 32 rows x 128 columns of sums (lane r holds row r) to the output, by way
+// of shared memory: kRows rows of 128 bytes at a time, the 16-byte chunks of row r at
+// chunk ^ (r & 7), so that a store instruction writes 4 whole 128-byte lines.  rows,
+// cols: how many of them the output has (cols a multiple of 8, rows at p, n_out
+// apart).  accumulate (fp32): added in memory, one addition an element.
+template <int kRows, typename OutT>
+__device__ __forceinline__ void store_rows(uint8_t* staging, OutT* p, int n_out,
+                                           const uint32_t (&v)[kEpilogueCols / 32][32], int rows,
+                                           int cols, int accumulate) {
+    constexpr int kLine = 128 / (int)sizeof(OutT), kChunk = 16 / (int)sizeof(OutT);
+    const int lane = threadIdx.x & 31;
+    const int my = lane % kRows, r0 = lane >> 3, ch = lane & 7;
+    uint8_t* put = staging + my * 128;
+#pragma unroll
+    for (int c = 0; c < kEpilogueCols; c += kLine) {
+        if (c >= cols) break;
+#pragma unroll
+        for (int part = 0; part < 32; part += kRows) {
+            if (part >= rows) break;
+            __syncwarp();  // the chunks before have been read
+            if (kRows == 32 || lane / kRows * kRows == part) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int e = c + k * kChunk + (sizeof(OutT) == 4 ? j : 2 * j);
+                        o[j] = sizeof(OutT) == 4
+                                   ? v[e / 32][e % 32]
+                                   : pack2(__uint_as_float(v[e / 32][e % 32]),
+                                           __uint_as_float(v[e / 32][(e + 1) % 32]));
+                    }
+                    *reinterpret_cast<uint4*>(put + ((k ^ (my & 7)) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            __syncwarp();
+            const int col = c + ch * kChunk;
+            OutT* at = p + (long long)(part + r0) * n_out + col;
+#pragma unroll
+            for (int j = 0; j < kRows / 4; ++j, at += 4LL * n_out) {
+                const int r = j * 4 + r0;
+                const uint4 o = *reinterpret_cast<const uint4*>(staging + r * 128 +
+                                                                ((ch ^ (r & 7)) << 4));
+                if (part + r < rows && col < cols) {
+                    if (sizeof(OutT) == 4 && accumulate)
+                        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at),
+                                     "f"(__uint_as_float(o.x)), "f"(__uint_as_float(o.y)),
+                                     "f"(__uint_as_float(o.z)), "f"(__uint_as_float(o.w))
+                                     : "memory");
+                    else
+                        *reinterpret_cast<uint4*>(at) = o;
+                }
+            }
+        }
+    }
+}
+
 // kMode, and for kWeightsGrad K unused, m_out x n_out = C_out x C_in; otherwise
-// K the contraction and n_out the columns of out.  chain: k-blocks per
-// accumulator.
+// K the contraction and n_out the columns of out.
 template <int kMode, typename OutT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_product_kernel(const __grid_constant__ CUtensorMap tmA,
                            const __grid_constant__ CUtensorMap tmB,
-                           const __grid_constant__ CUtensorMap tmOut,
                            const int32_t* __restrict__ expert_offsets,
                            const int32_t* __restrict__ expert_counts, int E, int R, int K,
-                           int m_out, int n_out, OutT* __restrict__ out, int chain,
-                           int accumulate, int* err, int* tile_counter) {
+                           int m_out, int n_out, OutT* __restrict__ out, int accumulate,
+                           int* err, int* tile_counter) {
+    constexpr bool kW = kMode == kWeightsGrad;
+    constexpr int kStagingRows = staging_rows(kMode), kStagingBytes = kStagingRows * 128;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t* tiles = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
     const uint32_t tiles_addr = smem_u32(tiles);
     uint8_t* staging_area = tiles + (size_t)kStages * STAGE_BYTES;
-    Ctl* ctl = reinterpret_cast<Ctl*>(staging_area + (size_t)kEpilogueWarps * kStagingBytes);
+    Ctl<kMode>* ctl = reinterpret_cast<Ctl<kMode>*>(staging_area +
+                                                    (size_t)kEpilogueWarps * kStagingBytes);
     volatile int* abort_flag = &ctl->abort;
 
-    constexpr bool kW = kMode == kWeightsGrad;
+    constexpr bool kChained = sizeof(OutT) == 4;  // see kChainBlocks
     constexpr bool kMnA = kW;                 // the contraction runs along A's rows
     constexpr bool kMnB = kMode != kForward;  // and along B's
     // readers of a slot of the leader's queue: its producer, MMA thread,
@@ -151,18 +312,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int NB = (n_out + BT - 1) / BT;
     const int KB = (K + BK - 1) / BK;
 
-    for (int i = threadIdx.x; i < E; i += blockDim.x) {
-        int off = expert_offsets[i], cnt = expert_counts[i];
-        if (off < 0 || cnt < 0 || cnt > R || off > R - cnt) {
-            // a segment outside the rows is reported and left out
-            set_error(err, MOE_ERR_INVALID_ARG);
-            off = cnt = 0;
-        }
-        ctl->offs[i] = off;
-        ctl->cnts[i] = cnt;
+    if constexpr (!kW) {
+        Tables& tb = ctl->tables;
+        for (int i = threadIdx.x; i < E; i += blockDim.x)
+            segment(expert_offsets, expert_counts, i, R, err, &tb.offs[i], &tb.cnts[i]);
+        __syncthreads();
+        if (warp == 4) warp_mblk_prefix(tb.cnts, E, BT, tb.prefix);
     }
-    __syncthreads();
-    if (!kW && warp == 4) warp_mblk_prefix(ctl->cnts, E, BT, ctl->prefix);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&ctl->full[s]), kW ? 2 : 1);
@@ -175,11 +331,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         mbar_init(smem_u32(&ctl->done), 1);
         for (int q = 0; q < kQ; ++q) {
-            mbar_init(smem_u32(&ctl->tq_full[q]), 1);
-            mbar_init(smem_u32(&ctl->tq_empty[q]), kQueueReaders);
-            mbar_init(smem_u32(&ctl->tq_taken[q]), 1);
-            mbar_init(smem_u32(&ctl->lq_full[q]), 1);
-            mbar_init(smem_u32(&ctl->lq_empty[q]), kLocalReaders);
+            mbar_init(smem_u32(&ctl->q_full[q]), 1);
+            mbar_init(smem_u32(&ctl->q_empty[q]), kQueueReaders);
+            mbar_init(smem_u32(&ctl->q_taken[q]), 1);
+            mbar_init(smem_u32(&ctl->l_full[q]), 1);
+            mbar_init(smem_u32(&ctl->l_empty[q]), kLocalReaders);
         }
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -187,7 +343,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {
         prefetch_map(&tmA);
         prefetch_map(&tmB);
-        prefetch_map(&tmOut);
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(&ctl->tmem_base), kTmemCols);
@@ -198,8 +353,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();  // both CTAs' barriers exist before any remote signal
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
-    const int total = kW ? E * MB * NB : ctl->prefix[E] * NB;
-
+    int total;
+    if constexpr (kW)
+        total = E * MB * NB;
+    else
+        total = ctl->tables.prefix[E] * NB;
     if (warp < 4) {
         regs_shrink<kRegsOther>();
         if (warp == 0 && lane == 0) {
@@ -208,14 +366,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
-                int tile = queue_take(ctl, i, leader, abort_flag, err);
-                if (leader && tile != -2) mbar_arrive(smem_u32(&ctl->tq_taken[i % kQ]));
-                if (!leader && tile != -2 && !local_publish(ctl, i, tile, abort_flag, err))
-                    tile = -2;
-                if (tile < 0) break;
-                const Tile t = tile_of<kMode>(ctl, E, MB, NB, KB, tile);
-                const int off = ctl->offs[t.e];
-                const bool ragged = kW && (ctl->cnts[t.e] % UMMA_K) != 0;
+                Tile t = {};
+                t.e = -1;
+                bool more = take(ctl, i, leader, abort_flag, err, t);
+                if (leader && more) mbar_arrive(smem_u32(&ctl->q_taken[i % kQ]));
+                if (!leader && !forward(ctl, i, t, abort_flag, err)) more = false;
+                if (!more) break;
+                const int off = t.off;
+                const bool ragged = kW && (t.cnt % UMMA_K) != 0;
                 // this CTA's half of A's rows and of B's
                 const int a0 = t.mb * BT + (int)rank * BH;
                 const int b0 = t.nb * BT + (int)rank * BH;
@@ -278,12 +436,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t acc_phase = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
-                const int tile = queue_take(ctl, i, true, abort_flag, err);
-                if (tile < 0) break;
-                const Tile t = tile_of<kMode>(ctl, E, MB, NB, KB, tile);
+                Tile t = {};
+                if (!take(ctl, i, true, abort_flag, err, t)) break;
                 // K steps of the last block (a segment's end)
                 const int last_steps =
-                    kW ? (ctl->cnts[t.e] - (t.kblocks - 1) * BK + UMMA_K - 1) / UMMA_K
+                    kW ? (t.cnt - (t.kblocks - 1) * BK + UMMA_K - 1) / UMMA_K
                        : BK / UMMA_K;
                 int in_chain = 0;
                 for (int kb = 0; kb < t.kblocks; ++kb) {
@@ -320,7 +477,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (++in_chain == chain || kb == t.kblocks - 1) {
+                    ++in_chain;
+                    if ((kChained && in_chain == kChainBlocks) || kb == t.kblocks - 1) {
                         umma_commit_pair_multicast(smem_u32(&ctl->tfull[acc]), 0x3);
                         in_chain = 0;
                         if (++acc == kAccs) {
@@ -334,17 +492,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             wait_bar_drain(smem_u32(&ctl->done), 0);
         } else if (warp == 2 && leader && lane == 0) {
             // ---------------- tile scheduler (leader) ----------------
-            // index i is published once the producer has taken index i - 1
+            // The pair's first tile is its own index; the counter hands out the ones
+            // after the pairs'.  Tile i is published once the producer has taken tile
+            // i - kAhead.
+            const int pairs = (int)(gridDim.x / 2);
+            int e = -1, off = 0, cnt = 0;  // the last tile's expert
             for (int i = 0;; ++i) {
-                if (i > 0) {
-                    const int j = i - 1;
-                    if (!wait_bar(smem_u32(&ctl->tq_taken[j % kQ]), (uint32_t)(j / kQ) & 1u,
+                if (i >= kAhead) {
+                    const int j = i - kAhead;
+                    if (!wait_bar(smem_u32(&ctl->q_taken[j % kQ]), (uint32_t)(j / kQ) & 1u,
                                   abort_flag, err))
                         break;
                 }
-                if (queue_publish(ctl, i, tile_counter, total, abort_flag, err,
-                                  (int)(gridDim.x / 2)) < 0)
-                    break;
+                const int tile =
+                    i == 0 ? (int)(blockIdx.x / 2) : pairs + atomicAdd(tile_counter, 1);
+                Tile t = {};
+                t.e = -1;
+                if (tile < total) {
+                    if constexpr (kW) {
+                        t.e = tile / (MB * NB);
+                        const int local = tile - t.e * MB * NB;
+                        t.mb = local / NB;
+                        t.nb = local - t.mb * NB;
+                        if (t.e != e)
+                            segment(expert_offsets, expert_counts, t.e, R, err, &off, &cnt);
+                        t.kblocks = (cnt + BK - 1) / BK;
+                    } else {
+                        decode_tile(ctl->tables.prefix, E, NB, BT, BT, tile, t.e, t.mb, t.nb);
+                        off = ctl->tables.offs[t.e];
+                        cnt = ctl->tables.cnts[t.e];
+                        t.kblocks = KB;
+                    }
+                    e = t.e;
+                    t.off = off;
+                    t.cnt = cnt;
+                }
+                if (!publish(ctl, i, t, abort_flag, err) || t.e < 0) break;
             }
         } else if (kW && warp == 3) {
             // ---------------- block ends (both CTAs) ----------------
@@ -352,14 +535,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int stage = 0;
             uint32_t land_phase = 0;
             for (int i = 0;; ++i) {
-                int tile = 0;
-                if (lane == 0)
-                    tile = leader ? queue_take(ctl, i, true, abort_flag, err)
-                                  : local_take(ctl, i, abort_flag, err);
-                tile = __shfl_sync(0xffffffffu, tile, 0);
-                if (tile < 0) break;
-                const Tile t = tile_of<kMode>(ctl, E, MB, NB, KB, tile);
-                const int cnt = ctl->cnts[t.e];
+                Tile t = {};
+                if (!warp_take(ctl, i, leader, abort_flag, err, t)) break;
+                const int cnt = t.cnt;
                 if (t.kblocks == 0) continue;
                 const int last = (stage + t.kblocks - 1) % kStages;
                 stage = (stage + t.kblocks) % kStages;
@@ -381,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(full0 + (uint32_t)last * 8u);
+                if (lane == 0) mbar_arrive_remote_shared(full0 + (uint32_t)last * 8u);
             }
         }
     } else {
@@ -390,30 +568,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int q = warp & 3;               // TMEM lane quadrant
         const int half = (warp - 4) >> 2;     // 128 columns of the tile
         uint8_t* staging = staging_area + (size_t)(warp - 4) * kStagingBytes;
-        const uint32_t staging_addr = smem_u32(staging);
-        uint8_t* my_row = staging + lane * kSliceBytes;
-        const int sw = (lane >> 1) & 3;  // 64-byte swizzle of this lane's row
         const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[0]), 0);
-        constexpr int kSliceCols = kSliceBytes / (int)sizeof(OutT);
-        constexpr int kChunkElems = 16 / (int)sizeof(OutT);
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int i = 0;; ++i) {
-            int tile = 0;
-            if (lane == 0)
-                tile = leader ? queue_take(ctl, i, true, abort_flag, err)
-                              : local_take(ctl, i, abort_flag, err);
-            tile = __shfl_sync(0xffffffffu, tile, 0);
-            if (tile < 0) break;
-            const Tile t = tile_of<kMode>(ctl, E, MB, NB, KB, tile);
+            Tile t = {};
+            if (!warp_take(ctl, i, leader, abort_flag, err, t)) break;
             if (kW && t.kblocks == 0 && accumulate) continue;  // nothing to add
 
-            float sum[kEpilogueCols];
+            uint32_t sum[kEpilogueCols / 32][32];  // fp32 sums, as loaded from TMEM
             bool ok = true;
-            int chains = (t.kblocks + chain - 1) / chain;
-            if (chains == 0) {
+            const int chains = kChained ? (t.kblocks + kChainBlocks - 1) / kChainBlocks
+                                        : (t.kblocks > 0 ? 1 : 0);
+            if (kChained || (kW && chains == 0)) {
 #pragma unroll
-                for (int c = 0; c < kEpilogueCols; ++c) sum[c] = 0.f;
+                for (int c = 0; c < kEpilogueCols; ++c) sum[c / 32][c % 32] = 0u;
             }
             for (int n = 0; n < chains; ++n) {
                 int ready = 0;
@@ -428,21 +597,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) +
                                        (uint32_t)(acc * BT + half * kEpilogueCols);
 #pragma unroll
-                for (int c = 0; c < kEpilogueCols; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(tbase + c, v);
-                    tmem_wait_ld();
-                    if (n == 0) {
+                for (int c = 0; c < kEpilogueCols / 32; ++c) {
+                    if (kChained) {
+                        uint32_t v[32];
+                        tmem_ld32(tbase + c * 32, v);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) sum[c + j] = __uint_as_float(v[j]);
+                        for (int j = 0; j < 32; ++j)
+                            sum[c][j] = __float_as_uint(__uint_as_float(sum[c][j]) +
+                                                        __uint_as_float(v[j]));
                     } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) sum[c + j] += __uint_as_float(v[j]);
+                        tmem_ld32(tbase + c * 32, sum[c]);
                     }
                 }
+                if (!kChained) tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)acc * 8u);
+                if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
                 if (++acc == kAccs) {
                     acc = 0;
                     acc_phase ^= 1u;
@@ -450,67 +621,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
 
-            // first row and column of this warp's part, and how many rows it stores
-            const int row_tile = t.mb * BT + (int)rank * BH + q * 32;
-            const int row0 = kW ? row_tile : ctl->offs[t.e] + row_tile;
-            int rows_valid = (kW ? m_out : ctl->cnts[t.e]) - row_tile;
-            rows_valid = rows_valid < 0 ? 0 : (rows_valid > 32 ? 32 : rows_valid);
-            if (rows_valid == 0) continue;
-            const int col_base = t.nb * BT + half * kEpilogueCols;
-#pragma unroll
-            for (int c = 0; c < kEpilogueCols; c += kSliceCols) {
-                const int col0 = col_base + c;
-                if (col0 < n_out) {
-                    if (lane == 0) bulk_wait_read();
-                    __syncwarp();
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint4 o;
-                        uint32_t* op = reinterpret_cast<uint32_t*>(&o);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (sizeof(OutT) == 4)
-                                op[j] = __float_as_uint(sum[c + ch * kChunkElems + j]);
-                            else
-                                op[j] = pack2(sum[c + ch * kChunkElems + 2 * j],
-                                              sum[c + ch * kChunkElems + 2 * j + 1]);
-                        }
-                        *reinterpret_cast<uint4*>(my_row + ((ch ^ sw) << 4)) = o;
-                    }
-                    if (kW || rows_valid == 32) {
-                        fence_async_shared();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (!kW)
-                                tma_store_2d(&tmOut, staging_addr, col0, row0);
-                            else if (accumulate)
-                                tma_reduce_add_3d(&tmOut, staging_addr, col0, row0, t.e);
-                            else
-                                tma_store_3d(&tmOut, staging_addr, col0, row0, t.e);
-                            bulk_commit();
-                        }
-                    } else {
-                        // the segment ends inside these rows: the rows after it are
-                        // another expert's
-                        __syncwarp();
-                        const int ch = lane & 3, col = col0 + ch * kChunkElems;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int rr = j * 8 + (lane >> 2);
-                            if (rr < rows_valid && col < n_out) {
-                                const uint4 v = *reinterpret_cast<const uint4*>(
-                                    staging + rr * kSliceBytes + ((ch ^ ((rr >> 1) & 3)) << 4));
-                                *reinterpret_cast<uint4*>(out + (size_t)(row0 + rr) * n_out +
-                                                          col) = v;
-                            }
-                        }
-                        __syncwarp();
-                    }
-                }
-            }
+            // the first of this warp's rows and columns
+            const int row = t.mb * BT + (int)rank * BH + q * 32;
+            const int rows = (kW ? m_out : t.cnt) - row;
+            const int col = t.nb * BT + half * kEpilogueCols;
+            const long long first = kW ? (long long)t.e * m_out + row : (long long)t.off + row;
+            if (rows > 0 && col < n_out)
+                store_rows<kStagingRows>(staging, out + first * n_out + col, n_out, sum, rows, n_out - col,
+                           accumulate);
         }
-        if (lane == 0) bulk_wait_all();
-        __syncwarp();
     }
 
     tc_fence_before();
@@ -532,9 +651,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int kMode, typename OutT>
-moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
-                  const GemmGroup& g, long long tiles, int K, int m_out, int n_out, void* out,
-                  bool accumulate, cudaStream_t st) {
+moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const GemmGroup& g, long long tiles,
+                  int K, int m_out, int n_out, void* out, bool accumulate, cudaStream_t st) {
     if (tiles >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
     // the attribute holds for the process and device: set once for each
     static bool set[64] = {false};
@@ -543,17 +661,16 @@ moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap&
     if (dev >= 64 || !set[dev]) {
         if (cudaFuncSetAttribute(grouped_product_kernel<kMode, OutT>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)kSmemBytes) != cudaSuccess)
+                                 (int)smem_bytes<kMode>()) != cudaSuccess)
             return MOE_ERR_CUDA;
         if (dev < 64) set[dev] = true;
     }
     const long long pairs_max = sm_count() / 2;
     const long long pairs = tiles < pairs_max ? tiles : pairs_max;
-    const int chain = sizeof(OutT) == 4 ? kChainBlocks : 1 << 30;
     grouped_product_kernel<kMode, OutT>
-        <<<(int)(2 * (pairs > 0 ? pairs : 1)), kThreads, kSmemBytes, st>>>(
-            a, b, o, g.offsets, g.counts, g.E, (int)g.R, K, m_out, n_out,
-            reinterpret_cast<OutT*>(out), chain, accumulate ? 1 : 0, g.err, g.prefix + g.E + 1);
+        <<<(int)(2 * (pairs > 0 ? pairs : 1)), kThreads, smem_bytes<kMode>(), st>>>(
+            a, b, g.offsets, g.counts, g.E, (int)g.R, K, m_out, n_out,
+            reinterpret_cast<OutT*>(out), accumulate ? 1 : 0, g.err, g.prefix + g.E + 1);
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -565,47 +682,36 @@ bool map_bf16(CUtensorMap* m, const void* ptr, long long outer, long long rows, 
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-bool map_out(CUtensorMap* m, const void* ptr, long long outer, long long rows, long long cols,
-             bool f32) {
-    const uint64_t sizes[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)outer};
-    const uint32_t box[3] = {f32 ? 16u : 32u, 32, 1};
-    return map_tiled(m,
-                     f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                     f32 ? 4 : 2, outer > 0 ? 3 : 2, ptr, sizes, box, CU_TENSOR_MAP_SWIZZLE_64B);
-}
-
 moe_status launch_rows(const uint16_t* rows, const GemmGroup& g, int c_in, int c_out,
                        const uint16_t* w, void* out, bool out_f32, bool input_grad,
                        cudaStream_t st) {
     const int K = input_grad ? c_out : c_in, n_out = input_grad ? c_in : c_out;
-    CUtensorMap a, b, o;
+    CUtensorMap a, b;
     const bool ok = map_bf16(&a, rows, 0, g.R, K, BK, BH) &&
-                    map_bf16(&b, w, g.E, c_out, c_in, BK, input_grad ? BK : BH) &&
-                    map_out(&o, out, 0, g.R, n_out, out_f32);
+                    map_bf16(&b, w, g.E, c_out, c_in, BK, input_grad ? BK : BH);
     if (!ok) return MOE_ERR_UNSUPPORTED;
     const long long tiles = ((g.R + BT - 1) / BT + g.E) * ((n_out + BT - 1LL) / BT);
     if (input_grad)
-        return out_f32 ? launch<kRowsGrad, float>(a, b, o, g, tiles, K, 0, n_out, out, false, st)
-                       : launch<kRowsGrad, __nv_bfloat16>(a, b, o, g, tiles, K, 0, n_out, out,
+        return out_f32 ? launch<kRowsGrad, float>(a, b, g, tiles, K, 0, n_out, out, false, st)
+                       : launch<kRowsGrad, __nv_bfloat16>(a, b, g, tiles, K, 0, n_out, out,
                                                           false, st);
-    return out_f32 ? launch<kForward, float>(a, b, o, g, tiles, K, 0, n_out, out, false, st)
-                   : launch<kForward, __nv_bfloat16>(a, b, o, g, tiles, K, 0, n_out, out, false,
+    return out_f32 ? launch<kForward, float>(a, b, g, tiles, K, 0, n_out, out, false, st)
+                   : launch<kForward, __nv_bfloat16>(a, b, g, tiles, K, 0, n_out, out, false,
                                                      st);
 }
 
 moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const GemmGroup& g, int c_in,
                           int c_out, void* dw, bool out_f32, bool accumulate,
                           cudaStream_t st) {
-    CUtensorMap a, b, o;
+    CUtensorMap a, b;
     const bool ok = map_bf16(&a, dout, 0, g.R, c_out, 64, BK) &&
-                    map_bf16(&b, rows, 0, g.R, c_in, 64, BK) &&
-                    map_out(&o, dw, g.E, c_out, c_in, out_f32);
+                    map_bf16(&b, rows, 0, g.R, c_in, 64, BK);
     if (!ok) return MOE_ERR_UNSUPPORTED;
     const long long tiles =
         (long long)g.E * ((c_out + BT - 1) / BT) * ((c_in + BT - 1LL) / BT);
-    return out_f32 ? launch<kWeightsGrad, float>(a, b, o, g, tiles, 0, c_out, c_in, dw, accumulate,
+    return out_f32 ? launch<kWeightsGrad, float>(a, b, g, tiles, 0, c_out, c_in, dw, accumulate,
                                                  st)
-                   : launch<kWeightsGrad, __nv_bfloat16>(a, b, o, g, tiles, 0, c_out, c_in, dw,
+                   : launch<kWeightsGrad, __nv_bfloat16>(a, b, g, tiles, 0, c_out, c_in, dw,
                                                          accumulate, st);
 }
 

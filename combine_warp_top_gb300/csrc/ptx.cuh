@@ -148,6 +148,11 @@ __device__ __forceinline__ void bulk_commit() {
 __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
+// The same for all but the last kLeft committed groups.
+template <int kLeft>
+__device__ __forceinline__ void bulk_wait_read_but() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
 // Wait until every committed bulk store has completed.
 __device__ __forceinline__ void bulk_wait_all() {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -324,6 +329,39 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                  : "memory");
+}
+
+// The same with the default (CTA-scope) release, for an arrival that hands over no
+// memory written for the other CTA (the end of reads from TMEM or of a queue slot).
+// The cluster-scope release above fences everything the thread has in flight,
+// which took 2000 to 5000 cycles in warps of a block that was storing its tile.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// An arrival that hands over what the thread has written to its own CTA's shared
+// memory: a cluster-scope release of that memory alone.
+__device__ __forceinline__ void mbar_arrive_remote_shared(uint32_t cluster_addr) {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+
+// Hands 16 bytes to another CTA: an asynchronous store into its shared memory whose
+// bytes are counted on an mbarrier beside them (both shared::cluster addresses), so
+// that a wait on that barrier sees them; and the arrival that expects them there.
+__device__ __forceinline__ void mbar_expect_tx_remote(uint32_t cluster_bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar),
+                 "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void st_async4(uint32_t cluster_addr, uint32_t cluster_bar, int a, int b,
+                                          int c, int d) {
+    asm volatile(
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.s32 [%0], {%1, %2, %3, %4}, [%5];" ::
+            "r"(cluster_addr),
+        "r"(a), "r"(b), "r"(c), "r"(d), "r"(cluster_bar)
+        : "memory");
 }
 
 // 32-bit store into another CTA's shared memory (shared::cluster address).
