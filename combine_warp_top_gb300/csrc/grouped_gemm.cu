@@ -512,21 +512,22 @@ bool map_3d(CUtensorMap* m, const void* ptr, uint64_t E, uint64_t rows, uint64_t
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Any tiled map of 2 or 3 dimensions (innermost first) over a dense array.
-bool map_tiled(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, int rank, const void* ptr,
-               const uint64_t* sizes, const uint32_t* boxes, CUtensorMapSwizzle swizzle) {
+// Any tiled bf16 map (128-byte swizzle) of up to 4 dimensions, innermost first;
+// strides: bytes of dimensions 1 and up.
+bool map_tiled(CUtensorMap* m, int rank, const void* ptr, const uint64_t* sizes,
+               const uint64_t* strides, const uint32_t* boxes) {
     auto enc = encode_fn();
-    if (!enc || rank < 2 || rank > 3) return false;
-    cuuint64_t dims[3], strides[2];
-    cuuint32_t box[3], estr[3] = {1, 1, 1};
+    if (!enc || rank < 2 || rank > 4) return false;
+    cuuint64_t dims[4], str[3];
+    cuuint32_t box[4], estr[4] = {1, 1, 1, 1};
     for (int i = 0; i < rank; ++i) {
         dims[i] = sizes[i];
         box[i] = boxes[i];
+        if (i > 0) str[i - 1] = strides[i - 1];
     }
-    strides[0] = sizes[0] * (uint64_t)elem_bytes;
-    strides[1] = strides[0] * sizes[1];
-    return enc(m, type, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims,
+               str, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -12,7 +12,10 @@
 // rows of a matrix (W in the rows' gradient, both operands in the weights'
 // gradient) TMA brings boxes of 64 columns x 64 rows and the matrix and
 // instruction descriptors name the operand MN-major, so nothing is transposed
-// or copied.
+// or copied.  Where the matrix has whole groups of 64 columns its map has them as a
+// dimension and one copy brings both boxes of an operand: the producer thread needs
+// some 75 cycles for each copy, and four of them a k-block (512 cycles of MMA) would
+// leave it no time to catch up after a wait.
 //
 // The contraction of a weights' gradient ends inside a 64-row block where the
 // expert's segment ends.  The MMA stops at the next 16 rows, and the rows
@@ -107,8 +110,11 @@ template <int kMode>
 struct Ctl : Barriers {
     Tables tables;
 };
+constexpr int kMaxSorted = 512;  // what is left of shared memory holds
 template <>
-struct Ctl<kWeightsGrad> : Barriers {};
+struct Ctl<kWeightsGrad> : Barriers {
+    uint16_t order[kMaxSorted];  // experts by falling number of rows
+};
 
 template <int kMode>
 constexpr size_t smem_bytes() {
@@ -277,7 +283,8 @@ __device__ __forceinline__ void store_rows(uint8_t* staging, OutT* p, int n_out,
 }
 
 // kMode, and for kWeightsGrad K unused, m_out x n_out = C_out x C_in; otherwise
-// K the contraction and n_out the columns of out.
+// K the contraction and n_out the columns of out.  a_groups, b_groups: the map of an
+// MN-major operand has its groups of 64 columns as a dimension.
 template <int kMode, typename OutT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_product_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -285,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            const int32_t* __restrict__ expert_offsets,
                            const int32_t* __restrict__ expert_counts, int E, int R, int K,
                            int m_out, int n_out, OutT* __restrict__ out, int accumulate,
-                           int* err, int* tile_counter) {
+                           int a_groups, int b_groups, int* err, int* tile_counter) {
     constexpr bool kW = kMode == kWeightsGrad;
     constexpr int kStagingRows = staging_rows(kMode), kStagingBytes = kStagingRows * 128;
     extern __shared__ uint8_t smem_raw[];
@@ -318,6 +325,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             segment(expert_offsets, expert_counts, i, R, err, &tb.offs[i], &tb.cnts[i]);
         __syncthreads();
         if (warp == 4) warp_mblk_prefix(tb.cnts, E, BT, tb.prefix);
+    }
+    // A weights' gradient hands out the experts with the most rows first: their tiles
+    // take the longest, and the short ones fill the pairs up at the end (Zipf-skewed
+    // case of 262144 rows in 128 experts: 2190 us in the experts' order, 2040 so).
+    bool sorted = false;
+    if constexpr (kW) {
+        sorted = E <= kMaxSorted && E * MB * NB > (int)(gridDim.x / 2);
+        if (sorted && leader) {
+            int* cnts = reinterpret_cast<int*>(tiles);  // the operand ring, not in use yet
+            for (int i = threadIdx.x; i < E; i += blockDim.x) cnts[i] = expert_counts[i];
+            __syncthreads();
+            for (int i = threadIdx.x; i < E; i += blockDim.x) {
+                const int mine = cnts[i];
+                int before = 0;
+                for (int j = 0; j < E; ++j)
+                    before += cnts[j] > mine || (cnts[j] == mine && j < i) ? 1 : 0;
+                ctl->order[before] = (uint16_t)i;
+            }
+            fence_async_shared();  // before TMA writes there
+        }
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -362,6 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         regs_shrink<kRegsOther>();
         if (warp == 0 && lane == 0) {
             // ---------------- TMA producer (both CTAs) ----------------
+            const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -390,26 +418,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (ragged && kb == t.kblocks - 1) {
                             const uint32_t land = smem_u32(&ctl->land[stage]);
                             mbar_expect_tx(land, STAGE_BYTES);
-                            tma_load_2d(a_s, &tmA, land, a0, row);
-                            tma_load_2d(a_s + BOX_BYTES, &tmA, land, a0 + 64, row);
-                            tma_load_2d(b_s, &tmB, land, b0, row);
-                            tma_load_2d(b_s + BOX_BYTES, &tmB, land, b0 + 64, row);
+                            if (a_groups) {
+                                tma_load_3d(a_s, &tmA, land, 0, row, a0 / 64);
+                            } else {
+                                tma_load_2d(a_s, &tmA, land, a0, row);
+                                tma_load_2d(a_s + BOX_BYTES, &tmA, land, a0 + 64, row);
+                            }
+                            if (b_groups) {
+                                tma_load_3d(b_s, &tmB, land, 0, row, b0 / 64);
+                            } else {
+                                tma_load_2d(b_s, &tmB, land, b0, row);
+                                tma_load_2d(b_s + BOX_BYTES, &tmB, land, b0 + 64, row);
+                            }
                         } else {
-                            const uint32_t full = mapa_shared(full_local, 0);
+                            const uint32_t full = full0 + (uint32_t)stage * 8u;
                             if (leader) {
                                 mbar_arrive(full_local);
                                 mbar_expect_tx(full_local, 2 * STAGE_BYTES);
                             }
-                            tma_load_2d_pair(a_s, &tmA, full, a0, row);
-                            tma_load_2d_pair(a_s + BOX_BYTES, &tmA, full, a0 + 64, row);
-                            tma_load_2d_pair(b_s, &tmB, full, b0, row);
-                            tma_load_2d_pair(b_s + BOX_BYTES, &tmB, full, b0 + 64, row);
+                            if (a_groups) {
+                                tma_load_3d_pair(a_s, &tmA, full, 0, row, a0 / 64);
+                            } else {
+                                tma_load_2d_pair(a_s, &tmA, full, a0, row);
+                                tma_load_2d_pair(a_s + BOX_BYTES, &tmA, full, a0 + 64, row);
+                            }
+                            if (b_groups) {
+                                tma_load_3d_pair(b_s, &tmB, full, 0, row, b0 / 64);
+                            } else {
+                                tma_load_2d_pair(b_s, &tmB, full, b0, row);
+                                tma_load_2d_pair(b_s + BOX_BYTES, &tmB, full, b0 + 64, row);
+                            }
                         }
                     } else {
-                        const uint32_t full = mapa_shared(full_local, 0);
+                        const uint32_t full = full0 + (uint32_t)stage * 8u;
                         if (leader) mbar_expect_tx(full_local, 2 * STAGE_BYTES);
                         tma_load_2d_pair(a_s, &tmA, full, kb * BK, off + a0);
-                        if (kMnB) {
+                        if (kMnB && b_groups) {
+                            tma_load_4d_pair(b_s, &tmB, full, 0, kb * BK, b0 / 64, t.e);
+                        } else if (kMnB) {
                             tma_load_3d_pair(b_s, &tmB, full, b0, kb * BK, t.e);
                             tma_load_3d_pair(b_s + BOX_BYTES, &tmB, full, b0 + 64, kb * BK, t.e);
                         } else {
@@ -514,6 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int local = tile - t.e * MB * NB;
                         t.mb = local / NB;
                         t.nb = local - t.mb * NB;
+                        if (sorted) t.e = ctl->order[t.e];
                         if (t.e != e)
                             segment(expert_offsets, expert_counts, t.e, R, err, &off, &cnt);
                         t.kblocks = (cnt + BK - 1) / BK;
@@ -652,7 +699,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 template <int kMode, typename OutT>
 moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const GemmGroup& g, long long tiles,
-                  int K, int m_out, int n_out, void* out, bool accumulate, cudaStream_t st) {
+                  int K, int m_out, int n_out, void* out, bool accumulate, int a_groups,
+                  int b_groups, cudaStream_t st) {
     if (tiles >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
     // the attribute holds for the process and device: set once for each
     static bool set[64] = {false};
@@ -670,16 +718,29 @@ moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const GemmGroup& g
     grouped_product_kernel<kMode, OutT>
         <<<(int)(2 * (pairs > 0 ? pairs : 1)), kThreads, smem_bytes<kMode>(), st>>>(
             a, b, g.offsets, g.counts, g.E, (int)g.R, K, m_out, n_out,
-            reinterpret_cast<OutT*>(out), accumulate ? 1 : 0, g.err, g.prefix + g.E + 1);
+            reinterpret_cast<OutT*>(out), accumulate ? 1 : 0, a_groups, b_groups, g.err, g.prefix + g.E + 1);
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-bool map_bf16(CUtensorMap* m, const void* ptr, long long outer, long long rows, long long cols,
-              uint32_t box_cols, uint32_t box_rows) {
+// A [outer, rows, cols] matrix (outer 0: [rows, cols]) in boxes of 64 columns.
+bool map_rows(CUtensorMap* m, const void* ptr, long long outer, long long rows, long long cols,
+              uint32_t box_rows) {
     const uint64_t sizes[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)outer};
-    const uint32_t box[3] = {box_cols, box_rows, 1};
-    return map_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, outer > 0 ? 3 : 2, ptr, sizes, box,
-                     CU_TENSOR_MAP_SWIZZLE_128B);
+    const uint64_t strides[2] = {(uint64_t)cols * 2, (uint64_t)(cols * rows) * 2};
+    const uint32_t box[3] = {BK, box_rows, 1};
+    return map_tiled(m, outer > 0 ? 3 : 2, ptr, sizes, strides, box);
+}
+
+// The same as an MN-major operand: boxes of 64 rows, two groups of 64 columns at a
+// time where cols is a multiple of 64 (*groups), else one.
+bool map_mn(CUtensorMap* m, const void* ptr, long long outer, long long rows, long long cols,
+            int* groups) {
+    *groups = cols % 64 == 0;
+    if (!*groups) return map_rows(m, ptr, outer, rows, cols, BK);
+    const uint64_t sizes[4] = {64, (uint64_t)rows, (uint64_t)cols / 64, (uint64_t)outer};
+    const uint64_t strides[3] = {(uint64_t)cols * 2, 128, (uint64_t)(cols * rows) * 2};
+    const uint32_t box[4] = {64, BK, 2, 1};
+    return map_tiled(m, outer > 0 ? 4 : 3, ptr, sizes, strides, box);
 }
 
 moe_status launch_rows(const uint16_t* rows, const GemmGroup& g, int c_in, int c_out,
@@ -687,32 +748,33 @@ moe_status launch_rows(const uint16_t* rows, const GemmGroup& g, int c_in, int c
                        cudaStream_t st) {
     const int K = input_grad ? c_out : c_in, n_out = input_grad ? c_in : c_out;
     CUtensorMap a, b;
-    const bool ok = map_bf16(&a, rows, 0, g.R, K, BK, BH) &&
-                    map_bf16(&b, w, g.E, c_out, c_in, BK, input_grad ? BK : BH);
+    int groups = 0;
+    const bool ok = map_rows(&a, rows, 0, g.R, K, BH) &&
+                    (input_grad ? map_mn(&b, w, g.E, c_out, c_in, &groups)
+                                : map_rows(&b, w, g.E, c_out, c_in, BH));
     if (!ok) return MOE_ERR_UNSUPPORTED;
     const long long tiles = ((g.R + BT - 1) / BT + g.E) * ((n_out + BT - 1LL) / BT);
+    using bf16 = __nv_bfloat16;
     if (input_grad)
-        return out_f32 ? launch<kRowsGrad, float>(a, b, g, tiles, K, 0, n_out, out, false, st)
-                       : launch<kRowsGrad, __nv_bfloat16>(a, b, g, tiles, K, 0, n_out, out,
-                                                          false, st);
-    return out_f32 ? launch<kForward, float>(a, b, g, tiles, K, 0, n_out, out, false, st)
-                   : launch<kForward, __nv_bfloat16>(a, b, g, tiles, K, 0, n_out, out, false,
-                                                     st);
+        return out_f32
+                   ? launch<kRowsGrad, float>(a, b, g, tiles, K, 0, n_out, out, false, 0, groups, st)
+                   : launch<kRowsGrad, bf16>(a, b, g, tiles, K, 0, n_out, out, false, 0, groups, st);
+    return out_f32 ? launch<kForward, float>(a, b, g, tiles, K, 0, n_out, out, false, 0, 0, st)
+                   : launch<kForward, bf16>(a, b, g, tiles, K, 0, n_out, out, false, 0, 0, st);
 }
 
 moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const GemmGroup& g, int c_in,
-                          int c_out, void* dw, bool out_f32, bool accumulate,
-                          cudaStream_t st) {
+                          int c_out, void* dw, bool out_f32, bool accumulate, cudaStream_t st) {
     CUtensorMap a, b;
-    const bool ok = map_bf16(&a, dout, 0, g.R, c_out, 64, BK) &&
-                    map_bf16(&b, rows, 0, g.R, c_in, 64, BK);
-    if (!ok) return MOE_ERR_UNSUPPORTED;
+    int a_groups = 0, b_groups = 0;
+    if (!map_mn(&a, dout, 0, g.R, c_out, &a_groups) || !map_mn(&b, rows, 0, g.R, c_in, &b_groups))
+        return MOE_ERR_UNSUPPORTED;
     const long long tiles =
         (long long)g.E * ((c_out + BT - 1) / BT) * ((c_in + BT - 1LL) / BT);
     return out_f32 ? launch<kWeightsGrad, float>(a, b, g, tiles, 0, c_out, c_in, dw, accumulate,
-                                                 st)
+                                                 a_groups, b_groups, st)
                    : launch<kWeightsGrad, __nv_bfloat16>(a, b, g, tiles, 0, c_out, c_in, dw,
-                                                         accumulate, st);
+                                                         accumulate, a_groups, b_groups, st);
 }
 
 moe_status check_grouped(const moe_layout* layout, const moe_shape* shape, int32_t C_in,

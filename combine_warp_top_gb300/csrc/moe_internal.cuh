@@ -180,8 +180,8 @@ bool map_3d(CUtensorMap* m, const void* ptr, uint64_t E, uint64_t rows, uint64_t
 bool map_packed(CUtensorMap* m, CUtensorMap* second, const void* ptr, int E, int n_blocks, int K,
                 uint32_t box_rows);
 
-bool map_tiled(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, int rank, const void* ptr,
-               const uint64_t* sizes, const uint32_t* boxes, CUtensorMapSwizzle swizzle);
+bool map_tiled(CUtensorMap* m, int rank, const void* ptr, const uint64_t* sizes,
+               const uint64_t* strides, const uint32_t* boxes);
 
 // CTA-pair GEMMs (grouped_gemm_2sm.cu): 256-row tiles on tcgen05 cta_group::2.
 moe_status launch_gate_up_pair(const uint16_t* rows, const GemmGroup& g, int H, int I,

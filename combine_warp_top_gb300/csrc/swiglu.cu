@@ -13,10 +13,7 @@
 // over rows that the activation's gradient reads anyway.
 //
 // Memory bound: 3 (forward) or 5 (gradient) bf16 a column, each moved once in
-// 16-byte vectors; arithmetic in fp32, one rounding to bf16 on store.  A row is
-// handled by one warp (kRowWarps = 1), so the gradient's row sum is a fixed
-// shuffle tree, or by a block of 8 warps where there are too few rows to fill
-// the machine with one warp each.
+// 16-byte vectors; arithmetic in fp32, one rounding to bf16 on store.
 #include "../../include/moe_train.h"
 #include "api_checks.cuh"
 #include "moe_internal.cuh"
@@ -65,32 +62,45 @@ __device__ __forceinline__ long long pair_of_row(const int32_t* __restrict__ row
     return hit ? (long long)t * k + __ffs(hit) - 1 : -1;
 }
 
-template <int kRowWarps>
+// A warp takes kVecs x 32 vectors of 8 columns of a row, all their loads in flight
+// at once; `parts` such pieces make a row.
+template <int kVecs>
 __global__ void __launch_bounds__(kBlock)
     swiglu_kernel(const uint4* __restrict__ gu, const float* __restrict__ topk_w,
                   const int32_t* __restrict__ row_token, const int32_t* __restrict__ pair_row,
-                  int N, int k, long long R, int V, uint4* __restrict__ h) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kRows = kBlock / 32 / kRowWarps;
-    const int first = (warp % kRowWarps) * 32 + lane;
-    for (long long row = (long long)blockIdx.x * kRows + warp / kRowWarps; row < R;
-         row += (long long)gridDim.x * kRows) {
+                  int N, int k, long long pieces, int parts, int V, uint4* __restrict__ h) {
+    const int lane = threadIdx.x & 31;
+    const long long step = (long long)gridDim.x * (kBlock / 32);
+    for (long long p = (long long)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5); p < pieces;
+         p += step) {
+        const long long row = p / parts;
+        const int first = (int)(p - row * parts) * kVecs * 32 + lane;
+        const uint4* g = gu + row * 2 * V;
+        uint4 rg[kVecs], ru[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int c = first + i * 32;
+            if (c < V) {
+                rg[i] = __ldcs(g + c);
+                ru[i] = __ldcs(g + V + c);
+            }
+        }
         float w = 1.0f;
         if (topk_w) {
-            const long long p = pair_of_row(row_token, pair_row, N, k, row);
-            w = p >= 0 ? topk_w[p] : 0.0f;
+            const long long q = pair_of_row(row_token, pair_row, N, k, row);
+            w = q >= 0 ? topk_w[q] : 0.0f;
         }
-        const uint4* g = gu + row * 2 * V;
-        const uint4* u = g + V;
-        uint4* o = h + row * V;
-#pragma unroll 4
-        for (int c = first; c < V; c += 32 * kRowWarps) {
-            float a[8], b[8];
-            unpack8(__ldcs(g + c), a);
-            unpack8(__ldcs(u + c), b);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = w * (a[j] * sigmoid(a[j])) * b[j];
-            __stcs(o + c, pack8(a));
+        for (int i = 0; i < kVecs; ++i) {
+            const int c = first + i * 32;
+            if (c < V) {
+                float a[8], b[8];
+                unpack8(rg[i], a);
+                unpack8(ru[i], b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a[j] = w * (a[j] * sigmoid(a[j])) * b[j];
+                __stcs(h + row * V + c, pack8(a));
+            }
         }
     }
 }
@@ -150,9 +160,11 @@ __global__ void __launch_bounds__(kBlock)
     }
 }
 
-// One warp a row once that gives every SM at least 32 warps; below, the warps
-// of a block share a row.
-bool warp_per_row(long long R) { return R >= 32LL * sm_count(); }
+// The gradient gives a warp to a row (whose sum is then its own) when that gives
+// every SM at least 32 warps and a row is short; long rows leave too few warps in
+// the last wave, so a block takes them.
+constexpr int kWarpRowVecs = 512;
+bool warp_per_row(long long R, int V) { return V <= kWarpRowVecs && R >= 32LL * sm_count(); }
 
 int grid_for(long long blocks) {
     const long long most = 1LL << 30;
@@ -177,12 +189,20 @@ moe_status moe_swiglu(const uint16_t* gu, const float* topk_w, const moe_layout*
     const uint4* in = reinterpret_cast<const uint4*>(gu);
     uint4* out = reinterpret_cast<uint4*>(h);
     const int V = shape->I / 8;
-    if (warp_per_row(R))
-        swiglu_kernel<1><<<grid_for((R + 7) / 8), kBlock, 0, as_stream(stream)>>>(
-            in, topk_w, layout->row_token, layout->pair_row, shape->N, shape->k, R, V, out);
-    else
-        swiglu_kernel<8><<<grid_for(R), kBlock, 0, as_stream(stream)>>>(
-            in, topk_w, layout->row_token, layout->pair_row, shape->N, shape->k, R, V, out);
+    // the widest pieces that leave no more lanes idle than narrower ones
+    const auto wide = [V](int vecs) { return (V + 32 * vecs - 1) / (32 * vecs) * vecs; };
+    const int vecs = wide(4) == wide(1) ? 4 : wide(2) == wide(1) ? 2 : 1;
+    const int parts = (V + 32 * vecs - 1) / (32 * vecs);
+    const long long pieces = R * parts;
+    const int grid = grid_for((pieces + kBlock / 32 - 1) / (kBlock / 32));
+    const auto go = [&](auto kernel) {
+        kernel<<<grid, kBlock, 0, as_stream(stream)>>>(in, topk_w, layout->row_token,
+                                                       layout->pair_row, shape->N, shape->k,
+                                                       pieces, parts, V, out);
+    };
+    if (vecs == 4) go(swiglu_kernel<4>);
+    else if (vecs == 2) go(swiglu_kernel<2>);
+    else go(swiglu_kernel<1>);
     return cuda_status(cudaGetLastError());
 }
 
@@ -199,7 +219,7 @@ moe_status moe_swiglu_grad(const uint16_t* dh, const uint16_t* gu, const float* 
     const uint4* in = reinterpret_cast<const uint4*>(gu);
     uint4* out = reinterpret_cast<uint4*>(dgu);
     const int V = shape->I / 8;
-    if (warp_per_row(R))
+    if (warp_per_row(R, V))
         swiglu_grad_kernel<1><<<grid_for((R + 7) / 8), kBlock, 0, as_stream(stream)>>>(
             d, in, topk_w, layout->row_token, layout->pair_row, shape->N, shape->k, R, V, out,
             dtopk_w);
