@@ -48,52 +48,61 @@ __device__ __forceinline__ float sigmoid(float g) {
     return __fdividef(1.0f, 1.0f + __expf(-g));
 }
 
-// The (token, choice) pair of expert-major row i: the token from the layout,
-// the choice from the lane whose pair_row names the row.  Whole warp; -1 if the
-// layout names none.
+// The (token, choice) pair of an expert-major row: the token from the layout, the
+// choice from the lane whose pair_row names the row.  Run by whole warps, every kLanes
+// lanes for a row of their own (live: there is one); -1 if the layout names none.
+template <int kLanes>
 __device__ __forceinline__ long long pair_of_row(const int32_t* __restrict__ row_token,
                                                  const int32_t* __restrict__ pair_row, int N,
-                                                 int k, long long row) {
-    const int lane = threadIdx.x & 31;
-    const int t = row_token[row];
-    if ((unsigned)t >= (unsigned)N) return -1;
-    const bool mine = lane < k && pair_row[(long long)t * k + lane] == row;
-    const unsigned hit = __ballot_sync(0xffffffffu, mine);
-    return hit ? (long long)t * k + __ffs(hit) - 1 : -1;
+                                                 int k, long long row, bool live) {
+    const int lane = threadIdx.x & 31, sub = lane % kLanes;
+    const int t = live ? row_token[row] : -1;
+    const bool token = (unsigned)t < (unsigned)N;
+    long long pair = -1;
+    for (int j0 = 0; j0 < k; j0 += kLanes) {
+        const int j = j0 + sub;
+        const bool mine = token && j < k && pair_row[(long long)t * k + j] == row;
+        unsigned hit = __ballot_sync(0xffffffffu, mine);
+        if (kLanes < 32) hit = (hit >> (lane - sub)) & ((1u << kLanes % 32) - 1u);
+        if (hit) pair = (long long)t * k + j0 + __ffs(hit) - 1;
+    }
+    return pair;
 }
 
-// A warp takes kVecs x 32 vectors of 8 columns of a row, all their loads in flight
-// at once; `parts` such pieces make a row.
-template <int kVecs>
+// Pieces of a row: kLanes lanes take kVecs x kLanes vectors of 8 columns of it, all
+// their loads in flight at once; `parts` pieces make a row.
+template <int kLanes, int kVecs>
 __global__ void __launch_bounds__(kBlock)
     swiglu_kernel(const uint4* __restrict__ gu, const float* __restrict__ topk_w,
                   const int32_t* __restrict__ row_token, const int32_t* __restrict__ pair_row,
                   int N, int k, long long pieces, int parts, int V, uint4* __restrict__ h) {
-    const int lane = threadIdx.x & 31;
-    const long long step = (long long)gridDim.x * (kBlock / 32);
-    for (long long p = (long long)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5); p < pieces;
-         p += step) {
-        const long long row = p / parts;
-        const int first = (int)(p - row * parts) * kVecs * 32 + lane;
+    constexpr int kGroups = kBlock / kLanes;
+    const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    const int in_warp = (threadIdx.x & 31) / kLanes;  // a warp's groups leave together
+    const long long step = (long long)gridDim.x * kGroups;
+    for (long long p = (long long)blockIdx.x * kGroups + group; p - in_warp < pieces; p += step) {
+        const bool live = kLanes == 32 || p < pieces;
+        const long long row = live ? p / parts : 0;
+        const int first = (int)(p - row * parts) * kVecs * kLanes + sub;
         const uint4* g = gu + row * 2 * V;
         uint4 rg[kVecs], ru[kVecs];
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            const int c = first + i * 32;
-            if (c < V) {
+            const int c = first + i * kLanes;
+            if (live && c < V) {
                 rg[i] = __ldcs(g + c);
                 ru[i] = __ldcs(g + V + c);
             }
         }
         float w = 1.0f;
         if (topk_w) {
-            const long long q = pair_of_row(row_token, pair_row, N, k, row);
+            const long long q = pair_of_row<kLanes>(row_token, pair_row, N, k, row, live);
             w = q >= 0 ? topk_w[q] : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            const int c = first + i * 32;
-            if (c < V) {
+            const int c = first + i * kLanes;
+            if (live && c < V) {
                 float a[8], b[8];
                 unpack8(rg[i], a);
                 unpack8(ru[i], b);
@@ -105,66 +114,82 @@ __global__ void __launch_bounds__(kBlock)
     }
 }
 
-template <int kRowWarps>
-__global__ void __launch_bounds__(kBlock)
+// A row for kLanes lanes of a warp (8, 16 or 32), or (kLanes = 128 or 256) for a
+// block.  The first loads of a row are in flight while its pair is looked up.
+template <int kLanes>
+__global__ void __launch_bounds__(kLanes > 32 ? kLanes : kBlock)
     swiglu_grad_kernel(const uint4* __restrict__ dh, const uint4* __restrict__ gu,
                        const float* __restrict__ topk_w, const int32_t* __restrict__ row_token,
                        const int32_t* __restrict__ pair_row, int N, int k, long long R, int V,
                        uint4* __restrict__ dgu, float* __restrict__ dtopk_w) {
-    __shared__ float part[kBlock / 32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kRows = kBlock / 32 / kRowWarps;
-    const int first = (warp % kRowWarps) * 32 + lane;
-    for (long long row = (long long)blockIdx.x * kRows + warp / kRowWarps; row < R;
-         row += (long long)gridDim.x * kRows) {
+    constexpr bool kBlockRow = kLanes > 32;
+    constexpr int kLook = kBlockRow ? 32 : kLanes;  // lanes that look up a pair
+    constexpr int kVecs = 2, kGroups = kBlockRow ? 1 : kBlock / kLanes;
+    __shared__ float part[8];
+    const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    const int in_warp = kBlockRow ? 0 : (threadIdx.x & 31) / kLanes;
+    const long long step = (long long)gridDim.x * kGroups;
+    for (long long row = (long long)blockIdx.x * kGroups + group; row - in_warp < R; row += step) {
+        const bool live = kLanes >= 32 || row < R;
+        const uint4* d = dh + row * V;
+        const uint4* g = gu + row * 2 * V;
+        uint4* og = dgu + row * 2 * V;
+        uint4 rd[kVecs], rg[kVecs], ru[kVecs];
+        auto load = [&](int c0) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int c = c0 + i * kLanes;
+                if (live && c < V) {
+                    rd[i] = __ldcs(d + c);
+                    rg[i] = __ldcs(g + c);
+                    ru[i] = __ldcs(g + V + c);
+                }
+            }
+        };
+        load(sub);
         float w = 1.0f;
         long long p = -1;
         if (topk_w || dtopk_w) {
-            p = pair_of_row(row_token, pair_row, N, k, row);
+            p = pair_of_row<kLook>(row_token, pair_row, N, k, row, live);
             if (topk_w) w = p >= 0 ? topk_w[p] : 0.0f;
         }
-        const uint4* d = dh + row * V;
-        const uint4* g = gu + row * 2 * V;
-        const uint4* u = g + V;
-        uint4* og = dgu + row * 2 * V;
-        uint4* ou = og + V;
         float sum = 0.0f;
-#pragma unroll 2
-        for (int c = first; c < V; c += 32 * kRowWarps) {
-            float x[8], a[8], b[8];
-            unpack8(__ldcs(d + c), x);
-            unpack8(__ldcs(g + c), a);
-            unpack8(__ldcs(u + c), b);
+        for (int c0 = sub; c0 < V; c0 += kVecs * kLanes) {
+            if (c0 != sub) load(c0);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float s = sigmoid(a[j]), act = a[j] * s, y = w * x[j];
-                sum += x[j] * act * b[j];
-                b[j] = y * b[j] * (s * (1.0f + a[j] * (1.0f - s)));
-                a[j] = y * act;
+            for (int i = 0; i < kVecs; ++i) {
+                const int c = c0 + i * kLanes;
+                if (live && c < V) {
+                    float x[8], a[8], b[8];
+                    unpack8(rd[i], x);
+                    unpack8(rg[i], a);
+                    unpack8(ru[i], b);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float s = sigmoid(a[j]), act = a[j] * s, y = w * x[j];
+                        sum += x[j] * act * b[j];
+                        b[j] = y * b[j] * (s * (1.0f + a[j] * (1.0f - s)));
+                        a[j] = y * act;
+                    }
+                    __stcs(og + c, pack8(b));
+                    __stcs(og + V + c, pack8(a));
+                }
             }
-            __stcs(og + c, pack8(b));
-            __stcs(ou + c, pack8(a));
         }
         if (dtopk_w) {
 #pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (kRowWarps > 1) {
-                if (lane == 0) part[warp] = sum;
+            for (int o = kLook / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (kBlockRow) {
+                if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
                 __syncthreads();
                 sum = 0.0f;
-                for (int i = 0; i < kRowWarps; ++i) sum += part[i];
+                for (int i = 0; i < kLanes / 32; ++i) sum += part[i];
                 __syncthreads();
             }
-            if (warp % kRowWarps == 0 && lane == 0 && p >= 0) dtopk_w[p] = sum;
+            if (sub == 0 && p >= 0) dtopk_w[p] = sum;
         }
     }
 }
-
-// The gradient gives a warp to a row (whose sum is then its own) when that gives
-// every SM at least 32 warps and a row is short; long rows leave too few warps in
-// the last wave, so a block takes them.
-constexpr int kWarpRowVecs = 512;
-bool warp_per_row(long long R, int V) { return V <= kWarpRowVecs && R >= 32LL * sm_count(); }
 
 int grid_for(long long blocks) {
     const long long most = 1LL << 30;
@@ -189,20 +214,24 @@ moe_status moe_swiglu(const uint16_t* gu, const float* topk_w, const moe_layout*
     const uint4* in = reinterpret_cast<const uint4*>(gu);
     uint4* out = reinterpret_cast<uint4*>(h);
     const int V = shape->I / 8;
-    // the widest pieces that leave no more lanes idle than narrower ones
-    const auto wide = [V](int vecs) { return (V + 32 * vecs - 1) / (32 * vecs) * vecs; };
-    const int vecs = wide(4) == wide(1) ? 4 : wide(2) == wide(1) ? 2 : 1;
-    const int parts = (V + 32 * vecs - 1) / (32 * vecs);
-    const long long pieces = R * parts;
-    const int grid = grid_for((pieces + kBlock / 32 - 1) / (kBlock / 32));
+    // lanes of a piece: a warp, or as many as a short row has vectors; vectors a lane:
+    // the most that leave at most a fifth of the lanes idle in a row
+    const int lanes = V <= 8 ? 8 : V <= 16 ? 16 : 32;
+    const auto wide = [V, lanes](int vecs) { return (V + lanes * vecs - 1) / (lanes * vecs) * vecs; };
+    const int vecs = wide(4) * 4 <= wide(1) * 5 ? 4 : wide(2) * 4 <= wide(1) * 5 ? 2 : 1;
+    const int parts = (V + lanes * vecs - 1) / (lanes * vecs);
+    const long long pieces = R * parts, groups = kBlock / lanes;
+    const int grid = grid_for((pieces + groups - 1) / groups);
     const auto go = [&](auto kernel) {
         kernel<<<grid, kBlock, 0, as_stream(stream)>>>(in, topk_w, layout->row_token,
                                                        layout->pair_row, shape->N, shape->k,
                                                        pieces, parts, V, out);
     };
-    if (vecs == 4) go(swiglu_kernel<4>);
-    else if (vecs == 2) go(swiglu_kernel<2>);
-    else go(swiglu_kernel<1>);
+    if (lanes == 8) go(swiglu_kernel<8, 1>);
+    else if (lanes == 16) go(swiglu_kernel<16, 1>);
+    else if (vecs == 4) go(swiglu_kernel<32, 4>);
+    else if (vecs == 2) go(swiglu_kernel<32, 2>);
+    else go(swiglu_kernel<32, 1>);
     return cuda_status(cudaGetLastError());
 }
 
@@ -219,14 +248,19 @@ moe_status moe_swiglu_grad(const uint16_t* dh, const uint16_t* gu, const float* 
     const uint4* in = reinterpret_cast<const uint4*>(gu);
     uint4* out = reinterpret_cast<uint4*>(dgu);
     const int V = shape->I / 8;
-    if (warp_per_row(R, V))
-        swiglu_grad_kernel<1><<<grid_for((R + 7) / 8), kBlock, 0, as_stream(stream)>>>(
+    const auto go = [&](auto kernel, int block, long long groups) {
+        kernel<<<grid_for((R + groups - 1) / groups), block, 0, as_stream(stream)>>>(
             d, in, topk_w, layout->row_token, layout->pair_row, shape->N, shape->k, R, V, out,
             dtopk_w);
-    else
-        swiglu_grad_kernel<8><<<grid_for(R), kBlock, 0, as_stream(stream)>>>(
-            d, in, topk_w, layout->row_token, layout->pair_row, shape->N, shape->k, R, V, out,
-            dtopk_w);
+    };
+    // A warp (or the lanes of a short row) takes a row when that gives every SM at
+    // least 32 warps and a row is not long; long rows leave too few warps in the last
+    // wave, so a block of 4 or 8 warps takes them, whichever idles less.
+    if (V <= 8) go(swiglu_grad_kernel<8>, kBlock, kBlock / 8);
+    else if (V <= 16) go(swiglu_grad_kernel<16>, kBlock, kBlock / 16);
+    else if (V <= 512 && R >= 32LL * sm_count()) go(swiglu_grad_kernel<32>, kBlock, kBlock / 32);
+    else if ((V + 255) / 256 * 2 > (V + 127) / 128) go(swiglu_grad_kernel<128>, 128, 1);
+    else go(swiglu_grad_kernel<256>, 256, 1);
     return cuda_status(cudaGetLastError());
 }
 
