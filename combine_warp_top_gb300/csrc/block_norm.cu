@@ -289,27 +289,50 @@ __device__ __forceinline__ Rows my_rows() {
     return {(int)blockIdx.x * kGroups + group, (int)gridDim.x * kGroups, in_warp};
 }
 
-// kV: vectors of 8 a thread holds.  kStages: rows of inputs in a block's ring
-// (groups of a warp load straight to registers).  kKeep: the per-channel vectors
-// stay in registers over the block's rows (a thread keeps its columns); else they
-// come from L1 for every row.  kFull: y, both norms and s are all there, so
-// nothing is tested for.
-template <int kV, int kLanes, bool kF32, int kStages, bool kKeep, bool kFull>
-__global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
+// How a row's inputs reach the registers: loaded when the row begins, loaded into
+// registers one row ahead, or by a ring of kRing2 or kRing3 rows in shared memory.
+// Blocks of one row, 8192 x 4096: an fp32 stream takes 66 us from one row ahead in
+// registers and 80 us by the ring, a bf16 stream 51 and 45 us: its rows are half as
+// many bytes, so one row ahead is too few in flight, and fp32 pays for the ring with
+// twice the 16-byte copies and reads of shared memory.
+enum Feed { kNow = 0, kAhead = 1, kRing2 = 2, kRing3 = 3 };
+
+// kV: vectors of 8 a thread holds.  kKeep: the per-channel vectors stay in registers
+// over the rows (a thread keeps its columns); else they come from L1 for every row.
+// kFull: y, both norms and s are all there, so nothing is tested for.
+template <int kV, int kLanes, bool kF32, Feed kFeed, bool kKeep, bool kFull, int kThreads>
+__global__ void __launch_bounds__(kThreads)
     block_norm_kernel(const NormArgs a) {
     extern __shared__ uint4 ring[];
     __shared__ float part[2][2][32];
-    constexpr bool kRing = kLanes == 0;
-    constexpr int kWordsR = kF32 ? 2 : 1, kPerV = 1 + kWordsR;
+    constexpr bool kRing = kFeed >= kRing2;
+    constexpr int kStages = kRing ? kFeed : 1, kPerV = kF32 ? 3 : 2;
     constexpr uint32_t kRowR = kF32 ? 32 : 16;  // bytes of a stream vector
     const uint32_t lanes = kLanes ? kLanes : blockDim.x;
     const uint32_t tid = kLanes ? threadIdx.x % lanes : threadIdx.x;
     const uint32_t V = a.V;
     const Rows rows = my_rows<kLanes>();
-    const uint32_t pitch = blockDim.x * 16, stage_bytes = pitch * kV * kPerV;
-    const uint32_t ring0 = kRing ? ptx::smem_u32(ring) : 0u;
     const bool has_y = kFull || a.y, post = kFull || a.post, pre = kFull || a.pre;
 
+    Raw<false> ry[kV];
+    Raw<kF32> rr[kV];
+    auto load = [&](int row) {
+        const char* y = reinterpret_cast<const char*>(a.y) + (size_t)row * V * 16;
+        const char* r = reinterpret_cast<const char*>(a.residual) + (size_t)row * V * kRowR;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const uint32_t c = tid + i * lanes;
+            if (!kFull) ry[i].w[0] = make_uint4(0, 0, 0, 0);
+            if (c < V && row < a.N) {
+                if (has_y) ry[i] = load_global<false>(y, c);
+                rr[i] = load_global<kF32>(r, c);
+            }
+        }
+    };
+    if (kFeed == kAhead) load(rows.first);
+
+    const uint32_t pitch = blockDim.x * 16, stage_bytes = pitch * kV * kPerV;
+    const uint32_t ring0 = kRing ? ptx::smem_u32(ring) : 0u;
     auto fetch = [&](int row, uint32_t stage) {
         if (row < a.N) {
             const char* y = reinterpret_cast<const char*>(a.y) + (size_t)row * V * 16;
@@ -344,30 +367,23 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
 
     int buf = 0, stage = 0;
     for (int row = rows.first; row - rows.lead < a.N; row += rows.step, buf ^= 1) {
-        const bool live = kRing || row < a.N;
+        const bool live = kLanes == 0 || row < a.N;
         const float token_gate = a.gate_kind == MOE_GATE_TOKEN && live ? a.gate[row] : 1.0f;
-        const char* y_row = reinterpret_cast<const char*>(a.y) + (size_t)row * V * 16;
-        const char* r_row = reinterpret_cast<const char*>(a.residual) + (size_t)row * V * kRowR;
         char* s_row = reinterpret_cast<char*>(a.s) + (size_t)row * V * kRowR;
         char* x_row = reinterpret_cast<char*>(a.x) + (size_t)row * V * 16;
         const uint32_t slot = ring0 + stage * stage_bytes + tid * 16;
+        if (kFeed == kNow) load(row);
         if constexpr (kRing) {
             __syncwarp();  // every lane has read what this overwrites
             const int next = stage == 0 ? kStages - 1 : stage - 1;
             fetch(row + (kStages - 1) * rows.step, ring0 + next * stage_bytes);
             ring_wait<kStages - 1>();
             stage = stage + 1 == kStages ? 0 : stage + 1;
-        }
-        Raw<false> ry[kV];
-        Raw<kF32> rr[kV];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const uint32_t c = tid + i * lanes, at = slot + i * kPerV * pitch;
-            ry[i].w[0] = make_uint4(0, 0, 0, 0);
-            if (c < V && live) {
-                if (has_y)
-                    ry[i] = kRing ? ring_read<false>(at, pitch) : load_global<false>(y_row, c);
-                if (!kRing) rr[i] = load_global<kF32>(r_row, c);
+            for (int i = 0; i < kV; ++i) {
+                if (!kFull) ry[i].w[0] = make_uint4(0, 0, 0, 0);
+                if (tid + i * lanes < V && has_y)
+                    ry[i] = ring_read<false>(slot + i * kPerV * pitch, pitch);
             }
         }
         float r_post = 1.0f;
@@ -375,10 +391,12 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
             f2 sum = both(0.0f);
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                f2 y[4];
-                unpack(ry[i], y);
+                if (tid + i * lanes < V && live) {
+                    f2 y[4];
+                    unpack(ry[i], y);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sum = fma2(y[j], y[j], sum);
+                    for (int j = 0; j < 4; ++j) sum = fma2(y[j], y[j], sum);
+                }
             }
             r_post = rsqrtf(row_sum<kLanes>(across(sum), part[buf][0]) * a.inv_h + a.eps);
             if (tid == 0 && live && a.rstd_post) a.rstd_post[row] = r_post;
@@ -400,8 +418,15 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
                     s[i][j] = fma2(mul2(y[j], scale), cw[i][j], mul2(alpha, s[i][j]));
                     sum = fma2(s[i][j], s[i][j], sum);
                 }
-                if (kFull || a.s) store_global<kF32>(s_row, c, s[i], a.wide);
             }
+        }
+        // its registers are free: the next row comes in beside this row's second sum
+        // and stores (s may be the residual itself: another row of it)
+        if (kFeed == kAhead) load(row + rows.step);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const uint32_t c = tid + i * lanes;
+            if (c < V && live && (kFull || a.s)) store_global<kF32>(s_row, c, s[i], a.wide);
         }
         if (!pre) continue;
         const float r_pre = rsqrtf(row_sum<kLanes>(across(sum), part[buf][1]) * a.inv_h + a.eps);
@@ -669,7 +694,7 @@ struct Plan {
     size_t smem;
 };
 
-// words: 16-byte words a thread and vector have in flight; kv: vectors a thread of
+// words: 16-byte words of a vector in the ring (0: no ring); kv: vectors a thread of
 // a block's row; most_blocks: resident on an SM (few in the gradient, so that their
 // partial sums stay few).  1024 threads are resident at 64 registers.
 Plan plan_for(int N, int V, int words, int kv, int most_blocks) {
@@ -701,7 +726,9 @@ Plan plan_for(int N, int V, int words, int kv, int most_blocks) {
 }
 
 Plan forward_plan(const moe_norm_shape& s) {
-    return plan_for(s.N, s.H / 8, s.stream_type == MOE_TYPE_F32 ? 3 : 2, s.H <= 8192 ? 1 : 2, 16);
+    // the ring feeds blocks of one bf16 row of up to 8192
+    const bool ring = s.stream_type == MOE_TYPE_BF16 && s.H <= 8192;
+    return plan_for(s.N, s.H / 8, ring ? 2 : 0, s.H <= 8192 ? 1 : 2, 16);
 }
 Plan grad_plan(const moe_norm_shape& s) {
     Plan p = plan_for(s.N, s.H / 8, s.stream_type == MOE_TYPE_F32 ? 6 : 4, s.H <= 8192 ? 1 : 2, 8);
@@ -735,14 +762,16 @@ cudaError_t run(void (*kernel)(Args), const Args& a, const Plan& p, cudaStream_t
 
 template <bool kF32, bool kFull>
 cudaError_t run_forward(const NormArgs& a, const Plan& p, cudaStream_t st) {
-    if (p.lanes == 8) return run(block_norm_kernel<1, 8, kF32, 0, true, kFull>, a, p, st);
-    if (p.lanes == 16) return run(block_norm_kernel<1, 16, kF32, 0, true, kFull>, a, p, st);
+    constexpr int kW = 32 * kRowWarps;
+    constexpr Feed kF = kF32 ? kAhead : kRing3;
+    if (p.lanes == 8) return run(block_norm_kernel<1, 8, kF32, kAhead, true, kFull, kW>, a, p, st);
+    if (p.lanes == 16) return run(block_norm_kernel<1, 16, kF32, kAhead, true, kFull, kW>, a, p, st);
     if (p.lanes == 32)
-        return p.kv == 1 ? run(block_norm_kernel<1, 32, kF32, 0, true, kFull>, a, p, st)
-                         : run(block_norm_kernel<2, 32, kF32, 0, true, kFull>, a, p, st);
-    if (p.kv == 1) return run(block_norm_kernel<1, 0, kF32, 3, true, kFull>, a, p, st);
-    return p.stages == 3 ? run(block_norm_kernel<2, 0, kF32, 3, false, kFull>, a, p, st)
-                         : run(block_norm_kernel<2, 0, kF32, 2, false, kFull>, a, p, st);
+        return p.kv == 1 ? run(block_norm_kernel<1, 32, kF32, kNow, true, kFull, kW>, a, p, st)
+                         : run(block_norm_kernel<2, 32, kF32, kNow, true, kFull, kW>, a, p, st);
+    if (p.kv == 2)
+        return run(block_norm_kernel<2, 0, kF32, kAhead, false, kFull, 1024>, a, p, st);
+    return run(block_norm_kernel<1, 0, kF32, kF, true, kFull, 1024>, a, p, st);
 }
 
 template <bool kF32, bool kFull>
