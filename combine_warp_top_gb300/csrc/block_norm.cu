@@ -46,7 +46,6 @@ struct NormArgs {
     float* rstd_pre;
     int N, V;                // V = H / 8
     int post, pre, gate_kind;
-    int wide;                // fp32 stream tensors start on 32-byte boundaries
     float eps, alpha, inv_h;
 };
 
@@ -66,7 +65,6 @@ struct NormGradArgs {
     float* partial;          // [grid][2][H]: sums of g yh (gated per token), of dx sh
     int N, V;
     int post, pre, gate_kind;
-    int wide;
     float alpha, inv_h;
 };
 
@@ -122,53 +120,83 @@ __device__ __forceinline__ uint4 pack_bf16(const f2 (&f)[4]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Vector v of a row, past L1 (each is read or written once).
+// The 8 columns that a thread holds of a row, as two quads of 4.  bf16 streams: 8
+// consecutive columns, one 16-byte word of each bf16 tensor.  fp32 streams: the
+// quads of `L` neighbouring threads lie side by side, first all their first quads, then
+// the second, so that each 16-byte access of a warp to an fp32 tensor covers whole
+// lines (8 consecutive fp32 columns a thread would take them by half sectors: an L2
+// request for every half, and 8192 x 4096 backwards
+// 130 us, 94 so).
+struct Cols {
+    uint32_t c, a, b;  // vector of 8, quads
+    bool pa, pb;       // the row has them (pb implies pa)
+};
 template <bool kF32>
-__device__ __forceinline__ Raw<kF32> load_global(const char* row, uint32_t v) {
-    Raw<kF32> r;
-    const uint4* q = reinterpret_cast<const uint4*>(row + v * (kF32 ? 32u : 16u));
-    r.w[0] = __ldcs(q);
-    if (kF32) r.w[kF32 ? 1 : 0] = __ldcs(q + 1);
+__device__ __forceinline__ Cols cols_of(uint32_t c, uint32_t L, uint32_t V) {
+    if (!kF32) return {c, 2 * c, 2 * c + 1, c < V, c < V};
+    const uint32_t l = c % L, a = (c - l) * 2 + l;
+    return {c, a, a + L, a < 2 * V, a + L < 2 * V};
+}
+
+// A thread's columns of a tensor (kT32: fp32, else bf16) of a kernel on an fp32 stream
+// (kF32) or not, past L1 (each is read or written once).
+template <bool kT32, bool kF32>
+__device__ __forceinline__ Raw<kT32> load_cols(const char* row, const Cols& q) {
+    Raw<kT32> r;
+    if (kT32) {
+        const uint4* p = reinterpret_cast<const uint4*>(row);
+        r.w[0] = r.w[kT32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
+        if (q.pa) r.w[0] = __ldcs(p + q.a);
+        if (q.pb) r.w[kT32 ? 1 : 0] = __ldcs(p + q.b);
+    } else if (kF32) {
+        const uint2* p = reinterpret_cast<const uint2*>(row);
+        uint2 x = make_uint2(0, 0), y = x;
+        if (q.pa) x = __ldcs(p + q.a);
+        if (q.pb) y = __ldcs(p + q.b);
+        r.w[0] = make_uint4(x.x, x.y, y.x, y.y);
+    } else {
+        r.w[0] = __ldcs(reinterpret_cast<const uint4*>(row) + q.c);
+    }
     return r;
 }
-// wide: one 32-byte store of an fp32 vector, so that a warp writes whole lines
-// (two 16-byte ones write every sector by halves: 1.3 times slower on rows of
-// fp32 where the stores bound the kernel).
-template <bool kF32>
-__device__ __forceinline__ void store_global(char* row, uint32_t v, const f2 (&f)[4], int wide) {
-    char* at = row + v * (kF32 ? 32u : 16u);
-    if (!kF32) {
-        __stcs(reinterpret_cast<uint4*>(at), pack_bf16(f));
-    } else if (wide) {
-        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at),
-                     "f"(f[0].x), "f"(f[0].y), "f"(f[1].x), "f"(f[1].y), "f"(f[2].x),
-                     "f"(f[2].y), "f"(f[3].x), "f"(f[3].y)
-                     : "memory");
+template <bool kT32, bool kF32>
+__device__ __forceinline__ void store_cols(char* row, const Cols& q, const f2 (&f)[4]) {
+    if (kT32) {
+        float4* p = reinterpret_cast<float4*>(row);
+        if (q.pa) __stcs(p + q.a, make_float4(f[0].x, f[0].y, f[1].x, f[1].y));
+        if (q.pb) __stcs(p + q.b, make_float4(f[2].x, f[2].y, f[3].x, f[3].y));
     } else {
-        float4* o = reinterpret_cast<float4*>(at);
-        __stcs(o, make_float4(f[0].x, f[0].y, f[1].x, f[1].y));
-        __stcs(o + 1, make_float4(f[2].x, f[2].y, f[3].x, f[3].y));
+        const uint4 v = pack_bf16(f);
+        if (kF32) {
+            uint2* p = reinterpret_cast<uint2*>(row);
+            if (q.pa) __stcs(p + q.a, make_uint2(v.x, v.y));
+            if (q.pb) __stcs(p + q.b, make_uint2(v.z, v.w));
+        } else {
+            __stcs(reinterpret_cast<uint4*>(row) + q.c, v);
+        }
     }
 }
-// 8 values of a per-channel vector (null: ones).
-__device__ __forceinline__ void load_channel(const float* p, int v, f2 (&f)[4]) {
+// Those of a per-channel vector (null: ones).
+__device__ __forceinline__ void load_channel(const float* p, const Cols& q, f2 (&f)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = both(1.0f);
     if (p) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p) + 2 * v);
-        const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 2 * v + 1);
-        f[0] = make_float2(a.x, a.y);
-        f[1] = make_float2(a.z, a.w);
-        f[2] = make_float2(b.x, b.y);
-        f[3] = make_float2(b.z, b.w);
+        const float4* v = reinterpret_cast<const float4*>(p);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (q.pa) x = __ldg(v + q.a);
+        if (q.pb) y = __ldg(v + q.b);
+        f[0] = make_float2(x.x, x.y);
+        f[1] = make_float2(x.z, x.w);
+        f[2] = make_float2(y.x, y.y);
+        f[3] = make_float2(y.z, y.w);
     }
 }
 // The block's scale of a channel: gate per channel times the weight after it.
-__device__ __forceinline__ void load_scale(const float* gate, const float* w_post, int v,
+__device__ __forceinline__ void load_scale(const float* gate, const float* w_post, const Cols& q,
                                            f2 (&f)[4]) {
     f2 g[4];
-    load_channel(w_post, v, f);
-    load_channel(gate, v, g);
+    load_channel(w_post, q, f);
+    load_channel(gate, q, g);
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], g[i]);
 }
@@ -176,23 +204,17 @@ __device__ __forceinline__ void load_scale(const float* gate, const float* w_pos
 // The inputs of the next rows of a block on their way into shared memory with
 // 16-byte cp.async, into slots that only the warp reads: a row in flight costs no
 // registers and no block barrier.  A stage holds words of 16 bytes for every
-// thread, `pitch` bytes between a thread's words.  bf16: a thread copies its own
-// word.  fp32: a warp copies its 64 words in order (so that it asks for whole
-// lines), each to the thread that owns it.
-template <bool kF32>
-__device__ __forceinline__ void ring_copy(uint32_t stage, uint32_t pitch, const char* row,
-                                          uint32_t thread, uint32_t v, uint32_t V) {
-    if (!kF32) {
-        if (v < V) ptx::cp_async_16(stage + thread * 16u, row + v * 16u, 16);
-    } else {
-        const uint32_t lane = thread & 31u;
-#pragma unroll
-        for (uint32_t i = 0; i < 2; ++i) {
-            const uint32_t g = lane + 32u * i;  // the warp's word
-            if (v - lane + (g >> 1) < V)
-                ptx::cp_async_16(stage + (g & 1u) * pitch + (thread - lane + (g >> 1)) * 16u,
-                                 row + ((v - lane) * 2u + g) * 16u, 16);
-        }
+// thread, `pitch` bytes between a thread's words (slot: the thread's first).  A bf16
+// tensor's word is the thread's 8 consecutive columns, an fp32 tensor's two words
+// are its quads.
+template <bool kT32>
+__device__ __forceinline__ void ring_copy(uint32_t slot, uint32_t pitch, const char* row,
+                                          const Cols& q, uint32_t V) {
+    if (kT32) {
+        if (q.pa) ptx::cp_async_16(slot, row + q.a * 16u, 16);
+        if (q.pb) ptx::cp_async_16(slot + pitch, row + q.b * 16u, 16);
+    } else if (q.c < V) {
+        ptx::cp_async_16(slot, row + q.c * 16u, 16);
     }
 }
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
@@ -203,11 +225,29 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
                  : "memory");
     return v;
 }
-template <bool kF32>
-__device__ __forceinline__ Raw<kF32> ring_read(uint32_t slot, uint32_t pitch) {
-    Raw<kF32> r;
-    r.w[0] = lds16(slot);
-    if (kF32) r.w[kF32 ? 1 : 0] = lds16(slot + pitch);
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+// A thread's columns from the ring.  In a kernel on an fp32 stream a bf16 tensor's
+// quads are among the warp's 512 bytes.  Quads that the row does not have are zeros.
+template <bool kT32, bool kF32>
+__device__ __forceinline__ Raw<kT32> ring_read(uint32_t slot, uint32_t pitch, const Cols& q) {
+    Raw<kT32> r;
+    if (kT32) {
+        r.w[0] = r.w[kT32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
+        if (q.pa) r.w[0] = lds16(slot);
+        if (q.pb) r.w[kT32 ? 1 : 0] = lds16(slot + pitch);
+    } else if (kF32) {
+        const uint32_t l = threadIdx.x & 31u, at = slot - l * 16u + l * 8u;
+        uint2 x = make_uint2(0, 0), y = x;
+        if (q.pa) x = lds8(at);
+        if (q.pb) y = lds8(at + 256u);
+        r.w[0] = make_uint4(x.x, x.y, y.x, y.y);
+    } else {
+        r.w[0] = lds16(slot);
+    }
     return r;
 }
 __device__ __forceinline__ void ring_commit() {
@@ -291,10 +331,11 @@ __device__ __forceinline__ Rows my_rows() {
 
 // How a row's inputs reach the registers: loaded when the row begins, loaded into
 // registers one row ahead, or by a ring of kRing2 or kRing3 rows in shared memory.
-// Blocks of one row, 8192 x 4096: an fp32 stream takes 66 us from one row ahead in
-// registers and 80 us by the ring, a bf16 stream 51 and 45 us: its rows are half as
-// many bytes, so one row ahead is too few in flight, and fp32 pays for the ring with
-// twice the 16-byte copies and reads of shared memory.
+// One row ahead costs no traffic of shared memory but is little in flight.  It wins for
+// an fp32 stream where two rows' blocks or more share an SM (8192 x 4096: 65 us, by the
+// ring 70), and loses where one block has the SM (8192 x 5120: 97 us, by the ring 78)
+// and for a bf16 stream, whose rows are half as many bytes (8192 x 4096: 51 and 44 us),
+// but for rows of more than 8192 (2048 x 16384: 59 and 63 us).
 enum Feed { kNow = 0, kAhead = 1, kRing2 = 2, kRing3 = 3 };
 
 // kV: vectors of 8 a thread holds.  kKeep: the per-channel vectors stay in registers
@@ -314,6 +355,7 @@ __global__ void __launch_bounds__(kThreads)
     const Rows rows = my_rows<kLanes>();
     const bool has_y = kFull || a.y, post = kFull || a.post, pre = kFull || a.pre;
 
+    const auto cols = [&](int i) { return cols_of<kF32>(tid + i * lanes, kLanes ? kLanes : 32, V); };
     Raw<false> ry[kV];
     Raw<kF32> rr[kV];
     auto load = [&](int row) {
@@ -321,11 +363,11 @@ __global__ void __launch_bounds__(kThreads)
         const char* r = reinterpret_cast<const char*>(a.residual) + (size_t)row * V * kRowR;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const uint32_t c = tid + i * lanes;
+            const Cols q = cols(i);
             if (!kFull) ry[i].w[0] = make_uint4(0, 0, 0, 0);
-            if (c < V && row < a.N) {
-                if (has_y) ry[i] = load_global<false>(y, c);
-                rr[i] = load_global<kF32>(r, c);
+            if (q.pa && row < a.N) {
+                if (has_y) ry[i] = load_cols<false, kF32>(y, q);
+                rr[i] = load_cols<kF32, kF32>(r, q);
             }
         }
     };
@@ -339,9 +381,9 @@ __global__ void __launch_bounds__(kThreads)
             const char* r = reinterpret_cast<const char*>(a.residual) + (size_t)row * V * kRowR;
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                const uint32_t c = tid + i * lanes, at = stage + i * kPerV * pitch;
-                if (has_y) ring_copy<false>(at, pitch, y, tid, c, V);
-                ring_copy<kF32>(at + pitch, pitch, r, tid, c, V);
+                const uint32_t at = stage + i * kPerV * pitch + tid * 16;
+                if (has_y) ring_copy<false>(at, pitch, y, cols(i), V);
+                ring_copy<kF32>(at + pitch, pitch, r, cols(i), V);
             }
         }
         ring_commit();
@@ -354,10 +396,10 @@ __global__ void __launch_bounds__(kThreads)
     const float* w_post = a.post ? a.w_post : nullptr;
     f2 cw[kV][4], wp[kV][4];
     auto channels = [&](int i) {
-        const uint32_t c = tid + i * lanes;
-        if (c < V) {
-            load_scale(gate_c, w_post, c, cw[i]);
-            load_channel(a.w_pre, c, wp[i]);
+        const Cols q = cols(i);
+        if (q.pa) {
+            load_scale(gate_c, w_post, q, cw[i]);
+            load_channel(a.w_pre, q, wp[i]);
         }
     };
     if (kKeep) {
@@ -382,8 +424,8 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
                 if (!kFull) ry[i].w[0] = make_uint4(0, 0, 0, 0);
-                if (tid + i * lanes < V && has_y)
-                    ry[i] = ring_read<false>(slot + i * kPerV * pitch, pitch);
+                if (cols(i).pa && has_y)
+                    ry[i] = ring_read<false, kF32>(slot + i * kPerV * pitch, pitch, cols(i));
             }
         }
         float r_post = 1.0f;
@@ -391,7 +433,7 @@ __global__ void __launch_bounds__(kThreads)
             f2 sum = both(0.0f);
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                if (tid + i * lanes < V && live) {
+                if (cols(i).pa && live) {
                     f2 y[4];
                     unpack(ry[i], y);
 #pragma unroll
@@ -406,10 +448,10 @@ __global__ void __launch_bounds__(kThreads)
         const f2 scale = both(r_post * token_gate), alpha = both(a.alpha);
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const uint32_t c = tid + i * lanes;
-            if (c < V && live) {
+            if (cols(i).pa && live) {
                 if (!kKeep) channels(i);
-                if (kRing) rr[i] = ring_read<kF32>(slot + (i * kPerV + 1) * pitch, pitch);
+                if (kRing)
+                    rr[i] = ring_read<kF32, kF32>(slot + (i * kPerV + 1) * pitch, pitch, cols(i));
                 f2 y[4];
                 unpack(ry[i], y);
                 unpack(rr[i], s[i]);
@@ -425,20 +467,19 @@ __global__ void __launch_bounds__(kThreads)
         if (kFeed == kAhead) load(row + rows.step);
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const uint32_t c = tid + i * lanes;
-            if (c < V && live && (kFull || a.s)) store_global<kF32>(s_row, c, s[i], a.wide);
+            if (cols(i).pa && live && (kFull || a.s))
+                store_cols<kF32, kF32>(s_row, cols(i), s[i]);
         }
         if (!pre) continue;
         const float r_pre = rsqrtf(row_sum<kLanes>(across(sum), part[buf][1]) * a.inv_h + a.eps);
         if (tid == 0 && live && a.rstd_pre) a.rstd_pre[row] = r_pre;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const uint32_t c = tid + i * lanes;
-            if (c < V && live) {
+            if (cols(i).pa && live) {
                 f2 x[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = mul2(mul2(s[i][j], both(r_pre)), wp[i][j]);
-                store_global<false>(x_row, c, x, 0);
+                store_cols<false, kF32>(x_row, cols(i), x);
             }
         }
     }
@@ -455,7 +496,7 @@ template <int kV, int kLanes, bool kF32, int kStages, bool kKeep, bool kFull>
 __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
     block_norm_grad_kernel(const NormGradArgs a) {
     extern __shared__ uint4 ring[];
-    float* cols = reinterpret_cast<float*>(ring);  // groups of a warp: their column sums
+    float* group_sums = reinterpret_cast<float*>(ring);  // groups of a warp: column sums
     __shared__ float4 part[2][32];
     constexpr bool kRing = kLanes == 0;
     constexpr int kWordsR = kF32 ? 2 : 1, kPerV = 2 + 2 * kWordsR;
@@ -473,25 +514,26 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
 #pragma unroll
         for (int j = 0; j < 4; ++j) t_post[i][j] = t_pre[i][j] = both(0.0f);
 
+    const auto cols = [&](int i) { return cols_of<kF32>(tid + i * lanes, kLanes ? kLanes : 32, V); };
     // words of a vector in a stage: dx, y, then s and ds
     auto fetch = [&](int row, uint32_t stage) {
         if (row < a.N) {
             const size_t at16 = (size_t)row * V * 16, at_r = (size_t)row * V * kRowR;
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                const uint32_t c = tid + i * lanes, at = stage + i * kPerV * pitch;
+                const Cols q = cols(i);
+                const uint32_t at = stage + i * kPerV * pitch + tid * 16;
                 if (pre) {
-                    ring_copy<false>(at, pitch, reinterpret_cast<const char*>(a.dx) + at16, tid, c,
-                                     V);
+                    ring_copy<false>(at, pitch, reinterpret_cast<const char*>(a.dx) + at16, q, V);
                     ring_copy<kF32>(at + 2 * pitch, pitch,
-                                    reinterpret_cast<const char*>(a.s) + at_r, tid, c, V);
+                                    reinterpret_cast<const char*>(a.s) + at_r, q, V);
                 }
                 if (has_ds)
                     ring_copy<kF32>(at + (2 + kWordsR) * pitch, pitch,
-                                    reinterpret_cast<const char*>(a.ds) + at_r, tid, c, V);
+                                    reinterpret_cast<const char*>(a.ds) + at_r, q, V);
                 if (has_y)
                     ring_copy<false>(at + pitch, pitch,
-                                     reinterpret_cast<const char*>(a.y) + at16, tid, c, V);
+                                     reinterpret_cast<const char*>(a.y) + at16, q, V);
             }
         }
         ring_commit();
@@ -504,10 +546,10 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
     const float* w_post = a.post ? a.w_post : nullptr;
     f2 cw[kV][4], wp[kV][4];
     auto channels = [&](int i) {
-        const uint32_t c = tid + i * lanes;
-        if (c < V) {
-            load_scale(gate_c, w_post, c, cw[i]);
-            load_channel(a.w_pre, c, wp[i]);
+        const Cols q = cols(i);
+        if (q.pa) {
+            load_scale(gate_c, w_post, q, cw[i]);
+            load_channel(a.w_pre, q, wp[i]);
         }
     };
     if (kKeep) {
@@ -533,7 +575,12 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
         Raw<false> rx[kV], ry[kV];
         Raw<kF32> rs[kV], rd[kV];
         auto read = [&](int i) {
-            const uint32_t c = tid + i * lanes, at = slot + i * kPerV * pitch;
+            const Cols q = cols(i);
+            const uint32_t at = slot + i * kPerV * pitch;
+            const char* dx = reinterpret_cast<const char*>(a.dx) + at16;
+            const char* sv = reinterpret_cast<const char*>(a.s) + at_r;
+            const char* ds = reinterpret_cast<const char*>(a.ds) + at_r;
+            const char* y = reinterpret_cast<const char*>(a.y) + at16;
             if (!kFull) {
                 rx[i].w[0] = ry[i].w[0] = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -541,28 +588,26 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
                     rs[i].w[j] = rd[i].w[j] = make_uint4(0, 0, 0, 0);
             }
             if (pre) {
-                rx[i] = kRing ? ring_read<false>(at, pitch)
-                              : load_global<false>(
-                                    reinterpret_cast<const char*>(a.dx) + at16, c);
-                rs[i] = kRing ? ring_read<kF32>(at + 2 * pitch, pitch)
-                              : load_global<kF32>(reinterpret_cast<const char*>(a.s) + at_r, c);
+                rx[i] = kRing ? ring_read<false, kF32>(at, pitch, q) : load_cols<false, kF32>(dx, q);
+                rs[i] = kRing ? ring_read<kF32, kF32>(at + 2 * pitch, pitch, q)
+                              : load_cols<kF32, kF32>(sv, q);
             }
             if (has_ds)
-                rd[i] = kRing ? ring_read<kF32>(at + (2 + kWordsR) * pitch, pitch)
-                              : load_global<kF32>(reinterpret_cast<const char*>(a.ds) + at_r, c);
+                rd[i] = kRing ? ring_read<kF32, kF32>(at + (2 + kWordsR) * pitch, pitch, q)
+                              : load_cols<kF32, kF32>(ds, q);
             if (has_y)
-                ry[i] = kRing ? ring_read<false>(at + pitch, pitch)
-                              : load_global<false>(reinterpret_cast<const char*>(a.y) + at16, c);
+                ry[i] = kRing ? ring_read<false, kF32>(at + pitch, pitch, q)
+                              : load_cols<false, kF32>(y, q);
         };
         if (!kRing) {
 #pragma unroll
             for (int i = 0; i < kV; ++i)
-                if (tid + i * lanes < V && live) read(i);
+                if (cols(i).pa && live) read(i);
         }
         f2 acc[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            if (tid + i * lanes < V && live) {
+            if (cols(i).pa && live) {
                 if (kRing) read(i);
                 if (!kKeep) channels(i);
                 f2 b[4], sv[4], y[4], d[4];
@@ -593,8 +638,7 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
         if (tid == 0 && live && a.dgate_token) a.dgate_token[row] = dot;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const uint32_t c = tid + i * lanes;
-            if (c < V && live) {
+            if (cols(i).pa && live) {
                 if (kRing) read(i);
                 if (!kKeep) channels(i);
                 f2 b[4], sv[4], g[4], o[4];
@@ -608,7 +652,7 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
                     o[j] = mul2(both(a.alpha), g[j]);
                 }
                 if (kFull || a.dresidual)
-                    store_global<kF32>(reinterpret_cast<char*>(a.dresidual) + at_r, c, o, a.wide);
+                    store_cols<kF32, kF32>(reinterpret_cast<char*>(a.dresidual) + at_r, cols(i), o);
                 if (has_y) {
                     f2 y[4];
                     unpack(ry[i], y);
@@ -618,7 +662,7 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
                         t_post[i][j] = fma2(t, y[j], t_post[i][j]);
                         o[j] = fma2(y[j], both(tm), mul2(cw[i][j], t));
                     }
-                    store_global<false>(reinterpret_cast<char*>(a.dy) + at16, c, o, 0);
+                    store_cols<false, kF32>(reinterpret_cast<char*>(a.dy) + at16, cols(i), o);
                 }
             }
         }
@@ -627,15 +671,16 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
     // the block's column sums: gate g yh (the token's gate), dx sh
     const uint32_t H = V * 8;
     float* out = a.partial + (size_t)blockIdx.x * 2 * H;
-    float* mine = kRing ? out : cols + (size_t)(threadIdx.x / lanes) * 2 * H;
+    float* mine = kRing ? out : group_sums + (size_t)(threadIdx.x / lanes) * 2 * H;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
-        const uint32_t c = tid + i * lanes;
-        if (c < V) {
+        const Cols q = cols(i);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                *reinterpret_cast<f2*>(mine + c * 8 + 2 * j) = t_post[i][j];
-                *reinterpret_cast<f2*>(mine + H + c * 8 + 2 * j) = t_pre[i][j];
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t at = (j < 2 ? q.a : q.b) * 4 + j % 2 * 2;
+            if (j < 2 ? q.pa : q.pb) {
+                *reinterpret_cast<f2*>(mine + at) = t_post[i][j];
+                *reinterpret_cast<f2*>(mine + H + at) = t_pre[i][j];
             }
         }
     }
@@ -644,7 +689,7 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
         const int groups = 32 * kRowWarps / (kLanes ? kLanes : 32);
         for (uint32_t c = threadIdx.x; c < 2 * H; c += blockDim.x) {
             float v = 0.0f;
-            for (int w = 0; w < groups; ++w) v += cols[(size_t)w * 2 * H + c];
+            for (int w = 0; w < groups; ++w) v += group_sums[(size_t)w * 2 * H + c];
             out[c] = v;
         }
     }
@@ -659,6 +704,8 @@ __global__ void __launch_bounds__(32 * kReduceRows)
                              const float* __restrict__ gate, const float* __restrict__ w_post,
                              float* dw_post, float* dgate, float* dw_pre, int accumulate) {
     __shared__ float sums[kReduceRows][33];
+    // launched while the kernel that writes the partial sums still runs
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), r0 = threadIdx.x >> 5;
     const int which = blockIdx.y;
     float v = 0.0f;
@@ -716,7 +763,7 @@ Plan plan_for(int N, int V, int words, int kv, int most_blocks) {
         if (fit < 1) fit = 1;
         const size_t stage = (size_t)p.block * kv * words * 16;
         const size_t room = (size_t)216 * 1024 / fit;
-        p.stages = stage * 3 <= room ? 3 : stage * 2 <= room ? 2 : 1;
+        p.stages = words == 0 ? 0 : stage * 3 <= room ? 3 : stage * 2 <= room ? 2 : 1;
         p.smem = stage * p.stages;
         const long long most = (long long)sm_count() * fit;
         p.grid = (int)(N < most ? N : most);
@@ -726,9 +773,9 @@ Plan plan_for(int N, int V, int words, int kv, int most_blocks) {
 }
 
 Plan forward_plan(const moe_norm_shape& s) {
-    // the ring feeds blocks of one bf16 row of up to 8192
-    const bool ring = s.stream_type == MOE_TYPE_BF16 && s.H <= 8192;
-    return plan_for(s.N, s.H / 8, ring ? 2 : 0, s.H <= 8192 ? 1 : 2, 16);
+    const bool f32 = s.stream_type == MOE_TYPE_F32;
+    const int words = f32 ? (s.H > 4096 ? 3 : 0) : s.H <= 8192 ? 2 : 0;  // see Feed
+    return plan_for(s.N, s.H / 8, words, s.H <= 8192 ? 1 : 2, 16);
 }
 Plan grad_plan(const moe_norm_shape& s) {
     Plan p = plan_for(s.N, s.H / 8, s.stream_type == MOE_TYPE_F32 ? 6 : 4, s.H <= 8192 ? 1 : 2, 8);
@@ -763,15 +810,18 @@ cudaError_t run(void (*kernel)(Args), const Args& a, const Plan& p, cudaStream_t
 template <bool kF32, bool kFull>
 cudaError_t run_forward(const NormArgs& a, const Plan& p, cudaStream_t st) {
     constexpr int kW = 32 * kRowWarps;
-    constexpr Feed kF = kF32 ? kAhead : kRing3;
     if (p.lanes == 8) return run(block_norm_kernel<1, 8, kF32, kAhead, true, kFull, kW>, a, p, st);
     if (p.lanes == 16) return run(block_norm_kernel<1, 16, kF32, kAhead, true, kFull, kW>, a, p, st);
     if (p.lanes == 32)
         return p.kv == 1 ? run(block_norm_kernel<1, 32, kF32, kNow, true, kFull, kW>, a, p, st)
                          : run(block_norm_kernel<2, 32, kF32, kNow, true, kFull, kW>, a, p, st);
     if (p.kv == 2)
-        return run(block_norm_kernel<2, 0, kF32, kAhead, false, kFull, 1024>, a, p, st);
-    return run(block_norm_kernel<1, 0, kF32, kF, true, kFull, 1024>, a, p, st);
+        return p.stages == 0
+                   ? run(block_norm_kernel<2, 0, kF32, kAhead, false, kFull, 1024>, a, p, st)
+                   : run(block_norm_kernel<2, 0, kF32, kRing2, false, kFull, 1024>, a, p, st);
+    return p.stages == 0
+               ? run(block_norm_kernel<1, 0, kF32, kAhead, true, kFull, 1024>, a, p, st)
+               : run(block_norm_kernel<1, 0, kF32, kRing3, true, kFull, 1024>, a, p, st);
 }
 
 template <bool kF32, bool kFull>
@@ -787,8 +837,6 @@ cudaError_t run_grad(const NormGradArgs& a, const Plan& p, cudaStream_t st) {
     return p.stages >= 2 ? run(block_norm_grad_kernel<2, 0, kF32, 2, false, kFull>, a, p, st)
                          : run(block_norm_grad_kernel<2, 0, kF32, 1, false, kFull>, a, p, st);
 }
-
-inline int aligned32(const void* p) { return ((uintptr_t)p & 31u) == 0; }
 
 }  // namespace
 }  // namespace moe
@@ -818,7 +866,7 @@ moe_status moe_block_norm(const uint16_t* y, const void* residual, const float* 
         return MOE_ERR_INVALID_ARG;
     const NormArgs a{y,         residual, w_post,      gate, w_pre, s,   x,
                      rstd_post, rstd_pre, shape->N,    shape->H / 8,     post, pre, shape->gate,
-                     aligned32(s), shape->eps, shape->residual_scale, 1.0f / (float)shape->H};
+                     shape->eps, shape->residual_scale, 1.0f / (float)shape->H};
     const Plan p = forward_plan(*shape);
     const bool f32 = shape->stream_type == MOE_TYPE_F32, full = y && post && pre && s;
     cudaStream_t st = as_stream(stream);
@@ -864,8 +912,8 @@ moe_status moe_block_norm_grad(const void* ds, const uint16_t* dx, const uint16_
         return MOE_ERR_INVALID_ARG;
     const NormGradArgs a{ds, dx, y, s, w_post, gate, w_pre, rstd_post, rstd_pre, dy, dresidual,
                          by_token ? dgate : nullptr, static_cast<float*>(ws), shape->N,
-                         shape->H / 8, post, pre, shape->gate, aligned32(dresidual),
-                         shape->residual_scale, 1.0f / (float)shape->H};
+                         shape->H / 8, post, pre, shape->gate, shape->residual_scale,
+                         1.0f / (float)shape->H};
     const Plan p = grad_plan(*shape);
     const bool f32 = shape->stream_type == MOE_TYPE_F32, full = y && pre && ds && dresidual;
     MOE_TRY(cuda_status(full ? (f32 ? run_grad<true, true>(a, p, st)
@@ -873,11 +921,19 @@ moe_status moe_block_norm_grad(const void* ds, const uint16_t* dx, const uint16_
                              : (f32 ? run_grad<true, false>(a, p, st)
                                     : run_grad<false, false>(a, p, st))));
     if (dw_post || dw_pre || (dgate && by_channel)) {
-        const dim3 grid((shape->H + 31) / 32, dw_pre ? 2 : 1);
-        block_norm_reduce_kernel<<<grid, 32 * kReduceRows, 0, st>>>(
-            a.partial, p.grid, shape->H, by_channel ? gate : nullptr, post ? w_post : nullptr,
-            dw_post, by_channel ? dgate : nullptr, dw_pre, accumulate != 0);
-        MOE_TRY(cuda_status(cudaGetLastError()));
+        cudaLaunchAttribute early[1];
+        early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((shape->H + 31) / 32, dw_pre ? 2 : 1);
+        cfg.blockDim = dim3(32 * kReduceRows);
+        cfg.stream = st;
+        cfg.attrs = early;
+        cfg.numAttrs = 1;
+        MOE_TRY(cuda_status(cudaLaunchKernelEx(
+            &cfg, block_norm_reduce_kernel, (const float*)a.partial, p.grid, (int)shape->H,
+            by_channel ? gate : (const float*)nullptr, post ? w_post : (const float*)nullptr,
+            dw_post, by_channel ? dgate : (float*)nullptr, dw_pre, accumulate != 0 ? 1 : 0)));
     }
     return MOE_OK;
 }
