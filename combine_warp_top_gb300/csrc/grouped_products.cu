@@ -224,59 +224,59 @@ __device__ __forceinline__ void segment(const int32_t* offsets, const int32_t* c
     *cnt = c;
 }
 
-// A warp's 32 rows x 128 columns of sums (lane r holds row r) to the output, by way
-// of shared memory: kRows rows of 128 bytes at a time, the 16-byte chunks of row r at
-// chunk ^ (r & 7), so that a store instruction writes 4 whole 128-byte lines.  rows,
-// cols: how many of them the output has (cols a multiple of 8, rows at p, n_out
-// apart).  accumulate (fp32): added in memory, one addition an element.
+// 32 or 64 columns of an accumulator.
+__device__ __forceinline__ void tmem_ld_line(uint32_t at, uint32_t (&v)[32]) { tmem_ld32(at, v); }
+__device__ __forceinline__ void tmem_ld_line(uint32_t at, uint32_t (&v)[64]) {
+    tmem_ld32(at, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+    tmem_ld32(at + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+}
+
+// A warp's 32 rows of one 128-byte line each (lane r holds row r's values, fp32) to
+// the output, by way of shared memory: kRows rows at a time, the 16-byte chunks of row
+// r at chunk ^ (r & 7), so that a store instruction writes 4 whole lines.  rows, cols:
+// how many the output has from p on (cols a multiple of 8, rows n_out apart).
+// accumulate (fp32): added in memory, one addition an element.
 template <int kRows, typename OutT>
-__device__ __forceinline__ void store_rows(uint8_t* staging, OutT* p, int n_out,
-                                           const uint32_t (&v)[kEpilogueCols / 32][32], int rows,
-                                           int cols, int accumulate) {
-    constexpr int kLine = 128 / (int)sizeof(OutT), kChunk = 16 / (int)sizeof(OutT);
+__device__ __forceinline__ void store_lines(uint8_t* staging, OutT* p, int n_out,
+                                            const uint32_t (&v)[128 / sizeof(OutT)], int rows,
+                                            int cols, int accumulate) {
+    constexpr int kChunk = 16 / (int)sizeof(OutT);
     const int lane = threadIdx.x & 31;
     const int my = lane % kRows, r0 = lane >> 3, ch = lane & 7;
     uint8_t* put = staging + my * 128;
 #pragma unroll
-    for (int c = 0; c < kEpilogueCols; c += kLine) {
-        if (c >= cols) break;
+    for (int part = 0; part < 32; part += kRows) {
+        if (part >= rows) break;
+        __syncwarp();  // the lines before have been read
+        if (kRows == 32 || lane / kRows * kRows == part) {
 #pragma unroll
-        for (int part = 0; part < 32; part += kRows) {
-            if (part >= rows) break;
-            __syncwarp();  // the chunks before have been read
-            if (kRows == 32 || lane / kRows * kRows == part) {
+            for (int k = 0; k < 8; ++k) {
+                uint32_t o[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int e = c + k * kChunk + (sizeof(OutT) == 4 ? j : 2 * j);
-                        o[j] = sizeof(OutT) == 4
-                                   ? v[e / 32][e % 32]
-                                   : pack2(__uint_as_float(v[e / 32][e % 32]),
-                                           __uint_as_float(v[e / 32][(e + 1) % 32]));
-                    }
-                    *reinterpret_cast<uint4*>(put + ((k ^ (my & 7)) << 4)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
-                }
+                for (int j = 0; j < 4; ++j)
+                    o[j] = sizeof(OutT) == 4
+                               ? v[k * kChunk + j]
+                               : pack2(__uint_as_float(v[(k * kChunk + 2 * j) % (kChunk * 8)]),
+                                       __uint_as_float(v[(k * kChunk + 2 * j + 1) % (kChunk * 8)]));
+                *reinterpret_cast<uint4*>(put + ((k ^ (my & 7)) << 4)) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
             }
-            __syncwarp();
-            const int col = c + ch * kChunk;
-            OutT* at = p + (long long)(part + r0) * n_out + col;
+        }
+        __syncwarp();
+        OutT* at = p + (long long)(part + r0) * n_out + ch * kChunk;
 #pragma unroll
-            for (int j = 0; j < kRows / 4; ++j, at += 4LL * n_out) {
-                const int r = j * 4 + r0;
-                const uint4 o = *reinterpret_cast<const uint4*>(staging + r * 128 +
-                                                                ((ch ^ (r & 7)) << 4));
-                if (part + r < rows && col < cols) {
-                    if (sizeof(OutT) == 4 && accumulate)
-                        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at),
-                                     "f"(__uint_as_float(o.x)), "f"(__uint_as_float(o.y)),
-                                     "f"(__uint_as_float(o.z)), "f"(__uint_as_float(o.w))
-                                     : "memory");
-                    else
-                        *reinterpret_cast<uint4*>(at) = o;
-                }
+        for (int j = 0; j < kRows / 4; ++j, at += 4LL * n_out) {
+            const int r = j * 4 + r0;
+            const uint4 o =
+                *reinterpret_cast<const uint4*>(staging + r * 128 + ((ch ^ (r & 7)) << 4));
+            if (part + r < rows && ch * kChunk < cols) {
+                if (sizeof(OutT) == 4 && accumulate)
+                    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at),
+                                 "f"(__uint_as_float(o.x)), "f"(__uint_as_float(o.y)),
+                                 "f"(__uint_as_float(o.z)), "f"(__uint_as_float(o.w))
+                                 : "memory");
+                else
+                    *reinterpret_cast<uint4*>(at) = o;
             }
         }
     }
@@ -623,41 +623,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!warp_take(ctl, i, leader, abort_flag, err, t)) break;
             if (kW && t.kblocks == 0 && accumulate) continue;  // nothing to add
 
-            uint32_t sum[kEpilogueCols / 32][32];  // fp32 sums, as loaded from TMEM
-            bool ok = true;
-            const int chains = kChained ? (t.kblocks + kChainBlocks - 1) / kChainBlocks
-                                        : (t.kblocks > 0 ? 1 : 0);
-            if (kChained || (kW && chains == 0)) {
-#pragma unroll
-                for (int c = 0; c < kEpilogueCols; ++c) sum[c / 32][c % 32] = 0u;
-            }
-            for (int n = 0; n < chains; ++n) {
-                int ready = 0;
+            // this warp's part of the next accumulator, once it is ready
+            const auto ready = [&]() {
+                int ok = 0;
                 if (lane == 0)
-                    ready = wait_bar(smem_u32(&ctl->tfull[acc]), acc_phase, abort_flag, err);
-                ready = __shfl_sync(0xffffffffu, ready, 0);
-                if (!ready) {
-                    ok = false;
-                    break;
-                }
+                    ok = wait_bar(smem_u32(&ctl->tfull[acc]), acc_phase, abort_flag, err);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
                 tc_fence_after();
-                const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) +
-                                       (uint32_t)(acc * BT + half * kEpilogueCols);
-#pragma unroll
-                for (int c = 0; c < kEpilogueCols / 32; ++c) {
-                    if (kChained) {
-                        uint32_t v[32];
-                        tmem_ld32(tbase + c * 32, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            sum[c][j] = __float_as_uint(__uint_as_float(sum[c][j]) +
-                                                        __uint_as_float(v[j]));
-                    } else {
-                        tmem_ld32(tbase + c * 32, sum[c]);
-                    }
-                }
-                if (!kChained) tmem_wait_ld();
+                return ok != 0;
+            };
+            const auto part = [&]() {
+                return tmem + ((uint32_t)(q * 32) << 16) +
+                       (uint32_t)(acc * BT + half * kEpilogueCols);
+            };
+            // the accumulator has been read
+            const auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
@@ -665,17 +645,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     acc = 0;
                     acc_phase ^= 1u;
                 }
+            };
+            const int chains = kChained ? (t.kblocks + kChainBlocks - 1) / kChainBlocks
+                                        : (t.kblocks > 0 ? 1 : 0);
+            // fp32 outputs: the partial sums before the last
+            uint32_t sum[kChained ? kEpilogueCols / 32 : 1][32];
+            bool ok = true;
+            if (kChained && chains > 1) {
+#pragma unroll
+                for (int c = 0; c < kEpilogueCols; ++c) sum[c / 32][c % 32] = 0u;
+                for (int n = 0; ok && n < chains - 1; ++n) {
+                    if (!ready()) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = part();
+#pragma unroll
+                    for (int c = 0; c < kEpilogueCols / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(at + c * 32, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            sum[c][j] = __float_as_uint(__uint_as_float(sum[c][j]) +
+                                                        __uint_as_float(v[j]));
+                    }
+                    release();
+                }
             }
-            if (!ok) break;
+            if (!ok || (chains > 0 && !ready())) break;
 
-            // the first of this warp's rows and columns
+            // the last one (or zeros), stored line by line: the reads of a line from
+            // TMEM go on beside the stores of the one before
             const int row = t.mb * BT + (int)rank * BH + q * 32;
             const int rows = (kW ? m_out : t.cnt) - row;
             const int col = t.nb * BT + half * kEpilogueCols;
             const long long first = kW ? (long long)t.e * m_out + row : (long long)t.off + row;
-            if (rows > 0 && col < n_out)
-                store_rows<kStagingRows>(staging, out + first * n_out + col, n_out, sum, rows, n_out - col,
-                           accumulate);
+            OutT* to = out + first * n_out + col;
+            constexpr int kLine = 128 / (int)sizeof(OutT);
+            const uint32_t at = part();
+#pragma unroll
+            for (int c = 0; c < kEpilogueCols; c += kLine) {
+                uint32_t v[kLine];
+                if (chains > 0) {
+                    tmem_ld_line(at + c, v);
+                    tmem_wait_ld();
+                    if (kChained && chains > 1) {
+#pragma unroll
+                        for (int j = 0; j < kLine; ++j)
+                            v[j] = __float_as_uint(
+                                __uint_as_float(sum[kChained ? c / 32 : 0][j % 32]) +
+                                __uint_as_float(v[j]));
+                    }
+                    if (c == kEpilogueCols - kLine) release();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kLine; ++j) v[j] = 0u;
+                }
+                if (rows > 0 && col + c < n_out)
+                    store_lines<kStagingRows>(staging, to + c, n_out, v, rows, n_out - col - c,
+                                              accumulate);
+            }
         }
     }
 
