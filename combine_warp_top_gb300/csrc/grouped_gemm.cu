@@ -515,7 +515,7 @@ bool map_3d(CUtensorMap* m, const void* ptr, uint64_t E, uint64_t rows, uint64_t
 // Any tiled bf16 map (128-byte swizzle) of up to 4 dimensions, innermost first;
 // strides: bytes of dimensions 1 and up.
 bool map_tiled(CUtensorMap* m, int rank, const void* ptr, const uint64_t* sizes,
-               const uint64_t* strides, const uint32_t* boxes) {
+               const uint64_t* strides, const uint32_t* boxes, bool f32) {
     auto enc = encode_fn();
     if (!enc || rank < 2 || rank > 4) return false;
     cuuint64_t dims[4], str[3];
@@ -525,7 +525,9 @@ bool map_tiled(CUtensorMap* m, int rank, const void* ptr, const uint64_t* sizes,
         box[i] = boxes[i];
         if (i > 0) str[i - 1] = strides[i - 1];
     }
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims,
+    return enc(m,
+               f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+               (cuuint32_t)rank, const_cast<void*>(ptr), dims,
                str, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

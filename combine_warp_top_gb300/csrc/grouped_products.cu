@@ -231,53 +231,49 @@ __device__ __forceinline__ void tmem_ld_line(uint32_t at, uint32_t (&v)[64]) {
     tmem_ld32(at + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
 }
 
-// A warp's 32 rows of one 128-byte line each (lane r holds row r's values, fp32) to
-// the output, by way of shared memory: kRows rows at a time, the 16-byte chunks of row
-// r at chunk ^ (r & 7), so that a store instruction writes 4 whole lines.  rows, cols:
-// how many the output has from p on (cols a multiple of 8, rows n_out apart).
-// accumulate (fp32): added in memory, one addition an element.
-template <int kRows, typename OutT>
+// One row's 128-byte line of fp32 values (rounded to OutT) into shared memory, its
+// 16-byte chunks k at k ^ (row & 7): TMA's 128-byte swizzle, and no two of 8 rows'
+// stores in the same banks.
+template <typename OutT>
+__device__ __forceinline__ void put_line(uint8_t* staging, int row,
+                                         const uint32_t (&v)[128 / sizeof(OutT)]) {
+    constexpr int kChunk = 16 / (int)sizeof(OutT), kLine = kChunk * 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            o[j] = sizeof(OutT) == 4
+                       ? v[k * kChunk + j]
+                       : pack2(__uint_as_float(v[(k * kChunk + 2 * j) % kLine]),
+                               __uint_as_float(v[(k * kChunk + 2 * j + 1) % kLine]));
+        *reinterpret_cast<uint4*>(staging + row * 128 + ((k ^ (row & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// A warp's 32 lines (lane r holds row r's) to rows of the output, n_out apart, that may
+// end inside the tile, where another expert's begin: 16 rows at a time through shared
+// memory, then 4 whole lines by each store instruction.  rows, cols: how many the
+// output has from p on (cols a multiple of 8).
+template <typename OutT>
 __device__ __forceinline__ void store_lines(uint8_t* staging, OutT* p, int n_out,
                                             const uint32_t (&v)[128 / sizeof(OutT)], int rows,
-                                            int cols, int accumulate) {
+                                            int cols) {
     constexpr int kChunk = 16 / (int)sizeof(OutT);
-    const int lane = threadIdx.x & 31;
-    const int my = lane % kRows, r0 = lane >> 3, ch = lane & 7;
-    uint8_t* put = staging + my * 128;
+    const int lane = threadIdx.x & 31, r0 = lane >> 3, ch = lane & 7;
 #pragma unroll
-    for (int part = 0; part < 32; part += kRows) {
+    for (int part = 0; part < 32; part += 16) {
         if (part >= rows) break;
         __syncwarp();  // the lines before have been read
-        if (kRows == 32 || lane / kRows * kRows == part) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    o[j] = sizeof(OutT) == 4
-                               ? v[k * kChunk + j]
-                               : pack2(__uint_as_float(v[(k * kChunk + 2 * j) % (kChunk * 8)]),
-                                       __uint_as_float(v[(k * kChunk + 2 * j + 1) % (kChunk * 8)]));
-                *reinterpret_cast<uint4*>(put + ((k ^ (my & 7)) << 4)) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
-            }
-        }
+        if ((lane & 16) == part) put_line<OutT>(staging, lane & 15, v);
         __syncwarp();
         OutT* at = p + (long long)(part + r0) * n_out + ch * kChunk;
 #pragma unroll
-        for (int j = 0; j < kRows / 4; ++j, at += 4LL * n_out) {
-            const int r = j * 4 + r0;
+        for (int r = r0; r < 16 + r0; r += 4, at += 4LL * n_out) {
             const uint4 o =
                 *reinterpret_cast<const uint4*>(staging + r * 128 + ((ch ^ (r & 7)) << 4));
-            if (part + r < rows && ch * kChunk < cols) {
-                if (sizeof(OutT) == 4 && accumulate)
-                    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at),
-                                 "f"(__uint_as_float(o.x)), "f"(__uint_as_float(o.y)),
-                                 "f"(__uint_as_float(o.z)), "f"(__uint_as_float(o.w))
-                                 : "memory");
-                else
-                    *reinterpret_cast<uint4*>(at) = o;
-            }
+            if (part + r < rows && ch * kChunk < cols) *reinterpret_cast<uint4*>(at) = o;
         }
     }
 }
@@ -289,6 +285,7 @@ template <int kMode, typename OutT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_product_kernel(const __grid_constant__ CUtensorMap tmA,
                            const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmOut,
                            const int32_t* __restrict__ expert_offsets,
                            const int32_t* __restrict__ expert_counts, int E, int R, int K,
                            int m_out, int n_out, OutT* __restrict__ out, int accumulate,
@@ -370,6 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {
         prefetch_map(&tmA);
         prefetch_map(&tmB);
+        if (kW) prefetch_map(&tmOut);
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(&ctl->tmem_base), kTmemCols);
@@ -680,8 +678,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int row = t.mb * BT + (int)rank * BH + q * 32;
             const int rows = (kW ? m_out : t.cnt) - row;
             const int col = t.nb * BT + half * kEpilogueCols;
-            const long long first = kW ? (long long)t.e * m_out + row : (long long)t.off + row;
-            OutT* to = out + first * n_out + col;
             constexpr int kLine = 128 / (int)sizeof(OutT);
             const uint32_t at = part();
 #pragma unroll
@@ -702,10 +698,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < kLine; ++j) v[j] = 0u;
                 }
-                if (rows > 0 && col + c < n_out)
-                    store_lines<kStagingRows>(staging, to + c, n_out, v, rows, n_out - col - c,
-                                              accumulate);
+                if (rows <= 0 || col + c >= n_out) continue;
+                if (kW) {
+                    // lines past the matrix are clipped by its map
+                    if (lane == 0) bulk_wait_read();  // the line before has been read
+                    __syncwarp();
+                    put_line<OutT>(staging, lane, v);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (accumulate)
+                            tma_reduce_add_3d(&tmOut, smem_u32(staging), col + c, row, t.e);
+                        else
+                            tma_store_3d(&tmOut, smem_u32(staging), col + c, row, t.e);
+                        bulk_commit();
+                    }
+                } else {
+                    store_lines<OutT>(staging, out + ((long long)t.off + row) * n_out + col + c,
+                                      n_out, v, rows, n_out - col - c);
+                }
             }
+        }
+        if (kW) {
+            if (lane == 0) bulk_wait_all();
+            __syncwarp();
         }
     }
 
@@ -728,7 +744,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int kMode, typename OutT>
-moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const GemmGroup& g, long long tiles,
+moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+                  const GemmGroup& g, long long tiles,
                   int K, int m_out, int n_out, void* out, bool accumulate, int a_groups,
                   int b_groups, cudaStream_t st) {
     if (tiles >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
@@ -747,7 +764,7 @@ moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const GemmGroup& g
     const long long pairs = tiles < pairs_max ? tiles : pairs_max;
     grouped_product_kernel<kMode, OutT>
         <<<(int)(2 * (pairs > 0 ? pairs : 1)), kThreads, smem_bytes<kMode>(), st>>>(
-            a, b, g.offsets, g.counts, g.E, (int)g.R, K, m_out, n_out,
+            a, b, o, g.offsets, g.counts, g.E, (int)g.R, K, m_out, n_out,
             reinterpret_cast<OutT*>(out), accumulate ? 1 : 0, a_groups, b_groups, g.err, g.prefix + g.E + 1);
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -787,23 +804,29 @@ moe_status launch_rows(const uint16_t* rows, const GemmGroup& g, int c_in, int c
     using bf16 = __nv_bfloat16;
     if (input_grad)
         return out_f32
-                   ? launch<kRowsGrad, float>(a, b, g, tiles, K, 0, n_out, out, false, 0, groups, st)
-                   : launch<kRowsGrad, bf16>(a, b, g, tiles, K, 0, n_out, out, false, 0, groups, st);
-    return out_f32 ? launch<kForward, float>(a, b, g, tiles, K, 0, n_out, out, false, 0, 0, st)
-                   : launch<kForward, bf16>(a, b, g, tiles, K, 0, n_out, out, false, 0, 0, st);
+                   ? launch<kRowsGrad, float>(a, b, b, g, tiles, K, 0, n_out, out, false, 0, groups, st)
+                   : launch<kRowsGrad, bf16>(a, b, b, g, tiles, K, 0, n_out, out, false, 0, groups, st);
+    return out_f32 ? launch<kForward, float>(a, b, b, g, tiles, K, 0, n_out, out, false, 0, 0, st)
+                   : launch<kForward, bf16>(a, b, b, g, tiles, K, 0, n_out, out, false, 0, 0, st);
 }
 
 moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const GemmGroup& g, int c_in,
                           int c_out, void* dw, bool out_f32, bool accumulate, cudaStream_t st) {
-    CUtensorMap a, b;
+    CUtensorMap a, b, o;
     int a_groups = 0, b_groups = 0;
     if (!map_mn(&a, dout, 0, g.R, c_out, &a_groups) || !map_mn(&b, rows, 0, g.R, c_in, &b_groups))
         return MOE_ERR_UNSUPPORTED;
+    // dW in boxes of 32 lines of 128 bytes
+    const uint64_t es = out_f32 ? 4 : 2;
+    const uint64_t sizes[3] = {(uint64_t)c_in, (uint64_t)c_out, (uint64_t)g.E};
+    const uint64_t strides[2] = {(uint64_t)c_in * es, (uint64_t)c_in * c_out * es};
+    const uint32_t box[3] = {(uint32_t)(128 / es), 32, 1};
+    if (!map_tiled(&o, 3, dw, sizes, strides, box, out_f32)) return MOE_ERR_UNSUPPORTED;
     const long long tiles =
         (long long)g.E * ((c_out + BT - 1) / BT) * ((c_in + BT - 1LL) / BT);
-    return out_f32 ? launch<kWeightsGrad, float>(a, b, g, tiles, 0, c_out, c_in, dw, accumulate,
+    return out_f32 ? launch<kWeightsGrad, float>(a, b, o, g, tiles, 0, c_out, c_in, dw, accumulate,
                                                  a_groups, b_groups, st)
-                   : launch<kWeightsGrad, __nv_bfloat16>(a, b, g, tiles, 0, c_out, c_in, dw,
+                   : launch<kWeightsGrad, __nv_bfloat16>(a, b, o, g, tiles, 0, c_out, c_in, dw,
                                                          accumulate, a_groups, b_groups, st);
 }
 

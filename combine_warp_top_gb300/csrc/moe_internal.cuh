@@ -181,7 +181,7 @@ bool map_packed(CUtensorMap* m, CUtensorMap* second, const void* ptr, int E, int
                 uint32_t box_rows);
 
 bool map_tiled(CUtensorMap* m, int rank, const void* ptr, const uint64_t* sizes,
-               const uint64_t* strides, const uint32_t* boxes);
+               const uint64_t* strides, const uint32_t* boxes, bool f32 = false);
 
 // CTA-pair GEMMs (grouped_gemm_2sm.cu): 256-row tiles on tcgen05 cta_group::2.
 moe_status launch_gate_up_pair(const uint16_t* rows, const GemmGroup& g, int H, int I,
