@@ -67,9 +67,7 @@ constexpr int kEpilogueCols = BT / 2;  // columns of one epilogue warp
 constexpr int kRegsOther = 88, kRegsEpilogue = 208;
 constexpr int kStages = 6;
 constexpr int kAhead = 2;  // tiles the scheduler publishes ahead of the leader's producer
-// Rows of 128 bytes of an epilogue warp's output staging; the experts' tables take
-// the room for more where they are in shared memory.
-constexpr int staging_rows(int mode) { return mode == kWeightsGrad ? 32 : 16; }
+constexpr int kStagingBytes = 32 * 128;  // an epilogue warp's output: 32 lines
 constexpr int kChainBlocks = 8;  // k-blocks added up in one accumulator (fp32 outputs)
 
 // A tile: its expert (-1: no more tiles) and the expert's rows, its row and column
@@ -99,17 +97,8 @@ struct Barriers {
     uint32_t tmem_base;
     int abort;
 };
-// The experts' tables, for the scheduler's search (not in a weights' gradient, where
-// every expert has the same number of tiles).
-struct Tables {
-    int prefix[kMaxE + 1];
-    int offs[kMaxE];
-    int cnts[kMaxE];
-};
 template <int kMode>
-struct Ctl : Barriers {
-    Tables tables;
-};
+struct Ctl : Barriers {};
 constexpr int kMaxSorted = 512;  // what is left of shared memory holds
 template <>
 struct Ctl<kWeightsGrad> : Barriers {
@@ -119,7 +108,7 @@ struct Ctl<kWeightsGrad> : Barriers {
 template <int kMode>
 constexpr size_t smem_bytes() {
     constexpr size_t n = 1024 + (size_t)kStages * STAGE_BYTES +
-                         (size_t)kEpilogueWarps * staging_rows(kMode) * 128 +
+                         (size_t)kEpilogueWarps * kStagingBytes +
                          ((sizeof(Ctl<kMode>) + 15) & ~size_t(15));
     static_assert(n <= 227 * 1024, "shared memory of one block");
     return n;
@@ -212,6 +201,17 @@ __device__ __forceinline__ bool warp_take(Barriers* c, int i, bool leader, volat
     return true;
 }
 
+// Inclusive prefix sum over a warp.
+__device__ __forceinline__ int warp_prefix(int v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
 // Expert e's segment; one that leaves the R rows is reported and taken as empty.
 __device__ __forceinline__ void segment(const int32_t* offsets, const int32_t* counts, int e,
                                         int R, int* err, int* off, int* cnt) {
@@ -252,29 +252,18 @@ __device__ __forceinline__ void put_line(uint8_t* staging, int row,
     }
 }
 
-// A warp's 32 lines (lane r holds row r's) to rows of the output, n_out apart, that may
-// end inside the tile, where another expert's begin: 16 rows at a time through shared
-// memory, then 4 whole lines by each store instruction.  rows, cols: how many the
-// output has from p on (cols a multiple of 8).
+// The first `rows` of a warp's 32 lines in shared memory to rows of the output, n_out
+// apart, 4 whole lines by each store instruction.  cols: how many the output has from p
+// on (a multiple of 8).
 template <typename OutT>
-__device__ __forceinline__ void store_lines(uint8_t* staging, OutT* p, int n_out,
-                                            const uint32_t (&v)[128 / sizeof(OutT)], int rows,
+__device__ __forceinline__ void store_lines(const uint8_t* staging, OutT* p, int n_out, int rows,
                                             int cols) {
     constexpr int kChunk = 16 / (int)sizeof(OutT);
-    const int lane = threadIdx.x & 31, r0 = lane >> 3, ch = lane & 7;
-#pragma unroll
-    for (int part = 0; part < 32; part += 16) {
-        if (part >= rows) break;
-        __syncwarp();  // the lines before have been read
-        if ((lane & 16) == part) put_line<OutT>(staging, lane & 15, v);
-        __syncwarp();
-        OutT* at = p + (long long)(part + r0) * n_out + ch * kChunk;
-#pragma unroll
-        for (int r = r0; r < 16 + r0; r += 4, at += 4LL * n_out) {
-            const uint4 o =
+    const int lane = threadIdx.x & 31, ch = lane & 7;
+    for (int r = lane >> 3; r < rows; r += 4) {
+        if (ch * kChunk < cols)
+            *reinterpret_cast<uint4*>(p + (long long)r * n_out + ch * kChunk) =
                 *reinterpret_cast<const uint4*>(staging + r * 128 + ((ch ^ (r & 7)) << 4));
-            if (part + r < rows && ch * kChunk < cols) *reinterpret_cast<uint4*>(at) = o;
-        }
     }
 }
 
@@ -291,7 +280,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            int m_out, int n_out, OutT* __restrict__ out, int accumulate,
                            int a_groups, int b_groups, int* err, int* tile_counter) {
     constexpr bool kW = kMode == kWeightsGrad;
-    constexpr int kStagingRows = staging_rows(kMode), kStagingBytes = kStagingRows * 128;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t* tiles = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -316,13 +304,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int NB = (n_out + BT - 1) / BT;
     const int KB = (K + BK - 1) / BK;
 
-    if constexpr (!kW) {
-        Tables& tb = ctl->tables;
-        for (int i = threadIdx.x; i < E; i += blockDim.x)
-            segment(expert_offsets, expert_counts, i, R, err, &tb.offs[i], &tb.cnts[i]);
-        __syncthreads();
-        if (warp == 4) warp_mblk_prefix(tb.cnts, E, BT, tb.prefix);
-    }
     // A weights' gradient hands out the experts with the most rows first: their tiles
     // take the longest, and the short ones fill the pairs up at the end (Zipf-skewed
     // case of 262144 rows in 128 experts: 2190 us in the experts' order, 2040 so).
@@ -367,7 +348,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {
         prefetch_map(&tmA);
         prefetch_map(&tmB);
-        if (kW) prefetch_map(&tmOut);
+        prefetch_map(&tmOut);
+    }
+    // Products over rows: lane l of the scheduler holds the row blocks in its run of
+    // experts [l * per, (l + 1) * per) and up to its end.
+    const int per = (E + 31) / 32;
+    int blocks_end = 0, blocks_in = 0, total = E * MB * NB;
+    if (!kW && warp == 2 && leader) {
+        for (int j = 0; j < per; ++j) {
+            int off, cnt;
+            if (lane * per + j < E) {
+                segment(expert_offsets, expert_counts, lane * per + j, R, err, &off, &cnt);
+                blocks_in += (cnt + BT - 1) / BT;
+            }
+        }
+        blocks_end = warp_prefix(blocks_in);
+        total = __shfl_sync(0xffffffffu, blocks_end, 31) * NB;
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(&ctl->tmem_base), kTmemCols);
@@ -378,11 +374,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();  // both CTAs' barriers exist before any remote signal
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
-    int total;
-    if constexpr (kW)
-        total = E * MB * NB;
-    else
-        total = ctl->tables.prefix[E] * NB;
     if (warp < 4) {
         regs_shrink<kRegsOther>();
         if (warp == 0 && lane == 0) {
@@ -534,22 +525,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             umma_commit_pair_multicast(smem_u32(&ctl->done), 0x1);
             wait_bar_drain(smem_u32(&ctl->done), 0);
-        } else if (warp == 2 && leader && lane == 0) {
+        } else if (warp == 2 && leader) {
             // ---------------- tile scheduler (leader) ----------------
             // The pair's first tile is its own index; the counter hands out the ones
             // after the pairs'.  Tile i is published once the producer has taken tile
             // i - kAhead.
             const int pairs = (int)(gridDim.x / 2);
-            int e = -1, off = 0, cnt = 0;  // the last tile's expert
+            int e = -1, off = 0, cnt = 0;  // the last tile's expert (weights' gradient)
             for (int i = 0;; ++i) {
-                if (i >= kAhead) {
-                    const int j = i - kAhead;
-                    if (!wait_bar(smem_u32(&ctl->q_taken[j % kQ]), (uint32_t)(j / kQ) & 1u,
-                                  abort_flag, err))
-                        break;
+                int tile = -1;
+                if (lane == 0) {
+                    bool ok = true;
+                    if (i >= kAhead) {
+                        const int j = i - kAhead;
+                        ok = wait_bar(smem_u32(&ctl->q_taken[j % kQ]), (uint32_t)(j / kQ) & 1u,
+                                      abort_flag, err);
+                    }
+                    if (ok)
+                        tile = i == 0 ? (int)(blockIdx.x / 2) : pairs + atomicAdd(tile_counter, 1);
                 }
-                const int tile =
-                    i == 0 ? (int)(blockIdx.x / 2) : pairs + atomicAdd(tile_counter, 1);
+                tile = __shfl_sync(0xffffffffu, tile, 0);
+                if (tile < 0) break;
                 Tile t = {};
                 t.e = -1;
                 if (tile < total) {
@@ -561,18 +557,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (sorted) t.e = ctl->order[t.e];
                         if (t.e != e)
                             segment(expert_offsets, expert_counts, t.e, R, err, &off, &cnt);
+                        e = t.e;
+                        t.off = off;
+                        t.cnt = cnt;
                         t.kblocks = (cnt + BK - 1) / BK;
                     } else {
-                        decode_tile(ctl->tables.prefix, E, NB, BT, BT, tile, t.e, t.mb, t.nb);
-                        off = ctl->tables.offs[t.e];
-                        cnt = ctl->tables.cnts[t.e];
+                        // the run of experts that holds row block q, then the expert
+                        const int q = tile / NB;
+                        const int run = __ffs(__ballot_sync(0xffffffffu, blocks_end > q)) - 1;
+                        const int before =
+                            __shfl_sync(0xffffffffu, blocks_end - blocks_in, run);
+                        const int mine = run * per + lane;
+                        int o = 0, c = 0;
+                        if (lane < per && mine < E)
+                            segment(expert_offsets, expert_counts, mine, R, err, &o, &c);
+                        const int b = (c + BT - 1) / BT, end = before + warp_prefix(b);
+                        const int k = __ffs(__ballot_sync(0xffffffffu, end > q)) - 1;
+                        const int MBe = __shfl_sync(0xffffffffu, b, k);
+                        const int local = tile - NB * (__shfl_sync(0xffffffffu, end, k) - MBe);
+                        t.e = run * per + k;
+                        t.off = __shfl_sync(0xffffffffu, o, k);
+                        t.cnt = __shfl_sync(0xffffffffu, c, k);
                         t.kblocks = KB;
+                        // the expert's smaller operand is the one read again: its row
+                        // blocks side by side when they are fewer than its columns'
+                        if (MBe > NB) {
+                            t.mb = local / NB;
+                            t.nb = local - t.mb * NB;
+                        } else {
+                            t.nb = local / MBe;
+                            t.mb = local - t.nb * MBe;
+                        }
                     }
-                    e = t.e;
-                    t.off = off;
-                    t.cnt = cnt;
                 }
-                if (!publish(ctl, i, t, abort_flag, err) || t.e < 0) break;
+                int more = 0;
+                if (lane == 0) more = publish(ctl, i, t, abort_flag, err) && t.e >= 0;
+                if (!__shfl_sync(0xffffffffu, more, 0)) break;
             }
         } else if (kW && warp == 3) {
             // ---------------- block ends (both CTAs) ----------------
@@ -699,30 +719,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < kLine; ++j) v[j] = 0u;
                 }
                 if (rows <= 0 || col + c >= n_out) continue;
-                if (kW) {
-                    // lines past the matrix are clipped by its map
-                    if (lane == 0) bulk_wait_read();  // the line before has been read
-                    __syncwarp();
-                    put_line<OutT>(staging, lane, v);
+                if (lane == 0) bulk_wait_read();  // the line before has been read
+                __syncwarp();
+                put_line<OutT>(staging, lane, v);
+                if (kW || rows >= 32) {
+                    // columns (and rows of dW) past the matrix are clipped by its map
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        if (accumulate)
+                        if (!kW)
+                            tma_store_2d(&tmOut, smem_u32(staging), col + c, t.off + row);
+                        else if (accumulate)
                             tma_reduce_add_3d(&tmOut, smem_u32(staging), col + c, row, t.e);
                         else
                             tma_store_3d(&tmOut, smem_u32(staging), col + c, row, t.e);
                         bulk_commit();
                     }
                 } else {
+                    // the segment ends inside these rows: the ones after it are another
+                    // expert's
+                    __syncwarp();
                     store_lines<OutT>(staging, out + ((long long)t.off + row) * n_out + col + c,
-                                      n_out, v, rows, n_out - col - c);
+                                      n_out, rows, n_out - col - c);
                 }
             }
         }
-        if (kW) {
-            if (lane == 0) bulk_wait_all();
-            __syncwarp();
-        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
     }
 
     tc_fence_before();
@@ -790,38 +813,45 @@ bool map_mn(CUtensorMap* m, const void* ptr, long long outer, long long rows, lo
     return map_tiled(m, outer > 0 ? 4 : 3, ptr, sizes, strides, box);
 }
 
+// The output ([outer,] rows, cols) in boxes of 32 lines of 128 bytes.
+bool map_lines(CUtensorMap* m, const void* ptr, long long outer, long long rows, long long cols,
+               bool f32) {
+    const uint64_t es = f32 ? 4 : 2;
+    const uint64_t sizes[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)outer};
+    const uint64_t strides[2] = {(uint64_t)cols * es, (uint64_t)(cols * rows) * es};
+    const uint32_t box[3] = {(uint32_t)(128 / es), 32, 1};
+    return map_tiled(m, outer > 0 ? 3 : 2, ptr, sizes, strides, box, f32);
+}
+
 moe_status launch_rows(const uint16_t* rows, const GemmGroup& g, int c_in, int c_out,
                        const uint16_t* w, void* out, bool out_f32, bool input_grad,
                        cudaStream_t st) {
     const int K = input_grad ? c_out : c_in, n_out = input_grad ? c_in : c_out;
-    CUtensorMap a, b;
+    CUtensorMap a, b, o;
     int groups = 0;
     const bool ok = map_rows(&a, rows, 0, g.R, K, BH) &&
                     (input_grad ? map_mn(&b, w, g.E, c_out, c_in, &groups)
-                                : map_rows(&b, w, g.E, c_out, c_in, BH));
+                                : map_rows(&b, w, g.E, c_out, c_in, BH)) &&
+                    map_lines(&o, out, 0, g.R, n_out, out_f32);
     if (!ok) return MOE_ERR_UNSUPPORTED;
     const long long tiles = ((g.R + BT - 1) / BT + g.E) * ((n_out + BT - 1LL) / BT);
     using bf16 = __nv_bfloat16;
     if (input_grad)
         return out_f32
-                   ? launch<kRowsGrad, float>(a, b, b, g, tiles, K, 0, n_out, out, false, 0, groups, st)
-                   : launch<kRowsGrad, bf16>(a, b, b, g, tiles, K, 0, n_out, out, false, 0, groups, st);
-    return out_f32 ? launch<kForward, float>(a, b, b, g, tiles, K, 0, n_out, out, false, 0, 0, st)
-                   : launch<kForward, bf16>(a, b, b, g, tiles, K, 0, n_out, out, false, 0, 0, st);
+                   ? launch<kRowsGrad, float>(a, b, o, g, tiles, K, 0, n_out, out, false, 0, groups, st)
+                   : launch<kRowsGrad, bf16>(a, b, o, g, tiles, K, 0, n_out, out, false, 0, groups, st);
+    return out_f32 ? launch<kForward, float>(a, b, o, g, tiles, K, 0, n_out, out, false, 0, 0, st)
+                   : launch<kForward, bf16>(a, b, o, g, tiles, K, 0, n_out, out, false, 0, 0, st);
 }
 
 moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const GemmGroup& g, int c_in,
                           int c_out, void* dw, bool out_f32, bool accumulate, cudaStream_t st) {
     CUtensorMap a, b, o;
     int a_groups = 0, b_groups = 0;
-    if (!map_mn(&a, dout, 0, g.R, c_out, &a_groups) || !map_mn(&b, rows, 0, g.R, c_in, &b_groups))
+    if (!map_mn(&a, dout, 0, g.R, c_out, &a_groups) ||
+        !map_mn(&b, rows, 0, g.R, c_in, &b_groups) ||
+        !map_lines(&o, dw, g.E, c_out, c_in, out_f32))
         return MOE_ERR_UNSUPPORTED;
-    // dW in boxes of 32 lines of 128 bytes
-    const uint64_t es = out_f32 ? 4 : 2;
-    const uint64_t sizes[3] = {(uint64_t)c_in, (uint64_t)c_out, (uint64_t)g.E};
-    const uint64_t strides[2] = {(uint64_t)c_in * es, (uint64_t)c_in * c_out * es};
-    const uint32_t box[3] = {(uint32_t)(128 / es), 32, 1};
-    if (!map_tiled(&o, 3, dw, sizes, strides, box, out_f32)) return MOE_ERR_UNSUPPORTED;
     const long long tiles =
         (long long)g.E * ((c_out + BT - 1) / BT) * ((c_in + BT - 1LL) / BT);
     return out_f32 ? launch<kWeightsGrad, float>(a, b, o, g, tiles, 0, c_out, c_in, dw, accumulate,
