@@ -354,12 +354,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // experts [l * per, (l + 1) * per) and up to its end.
     const int per = (E + 31) / 32;
     int blocks_end = 0, blocks_in = 0, total = E * MB * NB;
+    int run_off = 0, run_cnt = 0;  // the run's last expert: the lane's own where per = 1
     if (!kW && warp == 2 && leader) {
         for (int j = 0; j < per; ++j) {
-            int off, cnt;
             if (lane * per + j < E) {
-                segment(expert_offsets, expert_counts, lane * per + j, R, err, &off, &cnt);
-                blocks_in += (cnt + BT - 1) / BT;
+                segment(expert_offsets, expert_counts, lane * per + j, R, err, &run_off, &run_cnt);
+                blocks_in += (run_cnt + BT - 1) / BT;
             }
         }
         blocks_end = warp_prefix(blocks_in);
@@ -564,13 +564,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     } else {
                         // the run of experts that holds row block q, then the expert
                         const int q = tile / NB;
-                        const int run = __ffs(__ballot_sync(0xffffffffu, blocks_end > q)) - 1;
-                        const int before =
-                            __shfl_sync(0xffffffffu, blocks_end - blocks_in, run);
-                        const int mine = run * per + lane;
-                        int o = 0, c = 0;
-                        if (lane < per && mine < E)
-                            segment(expert_offsets, expert_counts, mine, R, err, &o, &c);
+                        int run = 0, before = 0, o = run_off, c = run_cnt;
+                        if (per > 1) {
+                            run = __ffs(__ballot_sync(0xffffffffu, blocks_end > q)) - 1;
+                            before = __shfl_sync(0xffffffffu, blocks_end - blocks_in, run);
+                            const int mine = run * per + lane;
+                            o = c = 0;
+                            if (lane < per && mine < E)
+                                segment(expert_offsets, expert_counts, mine, R, err, &o, &c);
+                        }
                         const int b = (c + BT - 1) / BT, end = before + warp_prefix(b);
                         const int k = __ffs(__ballot_sync(0xffffffffu, end > q)) - 1;
                         const int MBe = __shfl_sync(0xffffffffu, b, k);
@@ -700,25 +702,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int col = t.nb * BT + half * kEpilogueCols;
             constexpr int kLine = 128 / (int)sizeof(OutT);
             const uint32_t at = part();
-#pragma unroll
-            for (int c = 0; c < kEpilogueCols; c += kLine) {
-                uint32_t v[kLine];
-                if (chains > 0) {
-                    tmem_ld_line(at + c, v);
-                    tmem_wait_ld();
-                    if (kChained && chains > 1) {
-#pragma unroll
-                        for (int j = 0; j < kLine; ++j)
-                            v[j] = __float_as_uint(
-                                __uint_as_float(sum[kChained ? c / 32 : 0][j % 32]) +
-                                __uint_as_float(v[j]));
-                    }
-                    if (c == kEpilogueCols - kLine) release();
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kLine; ++j) v[j] = 0u;
-                }
-                if (rows <= 0 || col + c >= n_out) continue;
+            const auto put = [&](int c, const uint32_t (&v)[kLine]) {
+                if (rows <= 0 || col + c >= n_out) return;
                 if (lane == 0) bulk_wait_read();  // the line before has been read
                 __syncwarp();
                 put_line<OutT>(staging, lane, v);
@@ -741,6 +726,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     store_lines<OutT>(staging, out + ((long long)t.off + row) * n_out + col + c,
                                       n_out, rows, n_out - col - c);
+                }
+            };
+            if (kChained && chains > 1) {
+#pragma unroll
+                for (int c = 0; c < kEpilogueCols; c += kLine) {
+                    uint32_t v[kLine];
+                    tmem_ld_line(at + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < kLine; ++j)
+                        v[j] = __float_as_uint(
+                            __uint_as_float(sum[kChained ? c / 32 : 0][j % 32]) +
+                            __uint_as_float(v[j]));
+                    if (c == kEpilogueCols - kLine) release();
+                    put(c, v);
+                }
+            } else {
+                // not unrolled: in a short call most of this is the fetch of its code
+#pragma unroll 1
+                for (int c = 0; c < kEpilogueCols; c += kLine) {
+                    uint32_t v[kLine];
+                    if (!kW || chains > 0) {
+                        tmem_ld_line(at + c, v);
+                        tmem_wait_ld();
+                        if (c == kEpilogueCols - kLine) release();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kLine; ++j) v[j] = 0u;
+                    }
+                    put(c, v);
                 }
             }
         }
