@@ -185,12 +185,13 @@ def _lay(layout, shape):
 
 # The current stream's handle without a torch.cuda.Stream object around it (3 us).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -539,21 +540,22 @@ MOE_TYPES = {torch.bfloat16: 0, torch.float32: 1}  # moe_type
 
 
 def _exact(t, dtype, shape, what):
-    """Pointer of a contiguous device tensor of exactly this type and shape
+    """Address of a contiguous device tensor of exactly this type and shape
     (None passes: the C call decides whether NULL is allowed)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what}: expected a torch tensor")
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{what}: expected a torch tensor") from None
     if t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError("libmoe takes device tensors")
-    if not t.is_contiguous():
-        raise ValueError("tensors must be contiguous")
-    return t.data_ptr()
+    raise ValueError("tensors must be contiguous")
 
 
 def _bytes(ws):
@@ -701,12 +703,16 @@ class NormShape:
                             GATES[self.gate], int(self.stream == "fp32"), self.eps,
                             self.residual_scale)
 
-    @property
+    @functools.cached_property
     def stream_dtype(self):
         return torch.float32 if self.stream == "fp32" else torch.bfloat16
 
-    def gate_shape(self):
+    @functools.cached_property
+    def _gate_shape(self):
         return (self.N,) if self.gate == "token" else (self.H,)
+
+    def gate_shape(self):
+        return self._gate_shape
 
 
 def moe_norm_workspace_bytes(shape: NormShape) -> int:
@@ -723,30 +729,29 @@ def norm_workspace(shape: NormShape, device="cuda") -> torch.Tensor:
 def moe_block_norm(y, residual, w_post, gate, w_pre, shape: NormShape, s, x, rstd_post=None,
                    rstd_pre=None, stream=None):
     """s = residual_scale * residual + gate * norm(y) w_post; x = norm(s) w_pre."""
-    n = shape
-    nh, h, f32, st = (n.N, n.H), (n.H,), torch.float32, n.stream_dtype
+    n, f32, bf, st = shape, torch.float32, torch.bfloat16, shape.stream_dtype
+    nh, rows, h = (n.N, n.H), (n.N,), (n.H,)
     _check(load().moe_block_norm(
-        _exact(y, torch.bfloat16, nh, "y"), _exact(residual, st, nh, "residual"),
-        _exact(w_post, f32, h, "w_post"), _exact(gate, f32, n.gate_shape(), "gate"),
-        _exact(w_pre, f32, h, "w_pre"), n.ref, _exact(s, st, nh, "s"),
-        _exact(x, torch.bfloat16, nh, "x"), _exact(rstd_post, f32, (n.N,), "rstd_post"),
-        _exact(rstd_pre, f32, (n.N,), "rstd_pre"), _stream(stream)), "moe_block_norm")
+        _exact(y, bf, nh, "y"), _exact(residual, st, nh, "residual"),
+        _exact(w_post, f32, h, "w_post"), _exact(gate, f32, n._gate_shape, "gate"),
+        _exact(w_pre, f32, h, "w_pre"), n.ref, _exact(s, st, nh, "s"), _exact(x, bf, nh, "x"),
+        _exact(rstd_post, f32, rows, "rstd_post"), _exact(rstd_pre, f32, rows, "rstd_pre"),
+        _stream(stream)), "moe_block_norm")
 
 
 def moe_block_norm_grad(ds, dx, y, s, w_post, gate, w_pre, rstd_post, rstd_pre,
                         shape: NormShape, dy, dresidual, dw_post, dgate, dw_pre, ws,
                         accumulate=False, stream=None):
     """Gradient of moe_block_norm from ds and dx; ws of norm_workspace(shape)."""
-    n = shape
-    nh, h, f32, st = (n.N, n.H), (n.H,), torch.float32, n.stream_dtype
-    bf = torch.bfloat16
+    n, f32, bf, st = shape, torch.float32, torch.bfloat16, shape.stream_dtype
+    nh, rows, h = (n.N, n.H), (n.N,), (n.H,)
     _check(load().moe_block_norm_grad(
         _exact(ds, st, nh, "ds"), _exact(dx, bf, nh, "dx"), _exact(y, bf, nh, "y"),
         _exact(s, st, nh, "s"), _exact(w_post, f32, h, "w_post"),
-        _exact(gate, f32, n.gate_shape(), "gate"), _exact(w_pre, f32, h, "w_pre"),
-        _exact(rstd_post, f32, (n.N,), "rstd_post"), _exact(rstd_pre, f32, (n.N,), "rstd_pre"),
+        _exact(gate, f32, n._gate_shape, "gate"), _exact(w_pre, f32, h, "w_pre"),
+        _exact(rstd_post, f32, rows, "rstd_post"), _exact(rstd_pre, f32, rows, "rstd_pre"),
         n.ref, _exact(dy, bf, nh, "dy"), _exact(dresidual, st, nh, "dresidual"),
-        _exact(dw_post, f32, h, "dw_post"), _exact(dgate, f32, n.gate_shape(), "dgate"),
+        _exact(dw_post, f32, h, "dw_post"), _exact(dgate, f32, n._gate_shape, "dgate"),
         _exact(dw_pre, f32, h, "dw_pre"), int(bool(accumulate)), *_bytes(ws), _stream(stream)),
         "moe_block_norm_grad")
 
