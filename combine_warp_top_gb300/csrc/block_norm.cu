@@ -17,11 +17,14 @@
 //   dgate = sum of g yh w_post over the rows (per channel) or columns (per token)
 //
 // Both are memory bound: forward reads y and the residual once and writes s and
-// x; the gradient reads ds, dx, y and s once and writes dy and dresidual.  A row
-// stays in registers between its two reductions.  All sums are fp32 in a fixed
-// order: columns by shuffle trees, rows of a column by the thread that owns the
-// column over its block's rows, then over the blocks' partial sums (in the
-// workspace) by a second kernel.
+// x; the gradient reads ds, dx, y and s once and writes dy and dresidual.  A block
+// keeps its columns over many rows, so per-channel vectors and column sums stay in
+// registers, and the next rows' inputs are under way during a row's sums.  8192 rows of
+// 4096: forward 44 us (bf16 stream, 6.1 TB/s) and 65 us (fp32, 6.1 TB/s), gradient
+// 72 us (5.6 TB/s, its issue slots two thirds full) and 94 us (6.4 TB/s).  All sums
+// are fp32 in a fixed order: columns by shuffle trees, rows of a column by the thread
+// that owns the column over its block's rows, then over the blocks' partial sums (in
+// the workspace) by a second kernel.
 #include "../../include/moe_train.h"
 #include "api_checks.cuh"
 #include "moe_internal.cuh"
@@ -125,8 +128,7 @@ __device__ __forceinline__ uint4 pack_bf16(const f2 (&f)[4]) {
 // quads of `L` neighbouring threads lie side by side, first all their first quads, then
 // the second, so that each 16-byte access of a warp to an fp32 tensor covers whole
 // lines (8 consecutive fp32 columns a thread would take them by half sectors: an L2
-// request for every half, and 8192 x 4096 backwards
-// 130 us, 94 so).
+// request for every half, and 8192 x 4096 backwards 130 us, 94 so).
 struct Cols {
     uint32_t c, a, b;  // vector of 8, quads
     bool pa, pb;       // the row has them (pb implies pa)

@@ -512,7 +512,7 @@ bool map_3d(CUtensorMap* m, const void* ptr, uint64_t E, uint64_t rows, uint64_t
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Any tiled bf16 map (128-byte swizzle) of up to 4 dimensions, innermost first;
+// Any tiled bf16 or fp32 map (128-byte swizzle) of up to 4 dimensions, innermost first;
 // strides: bytes of dimensions 1 and up.
 bool map_tiled(CUtensorMap* m, int rank, const void* ptr, const uint64_t* sizes,
                const uint64_t* strides, const uint32_t* boxes, bool f32) {

