@@ -54,7 +54,12 @@
 // - A tile costs each role some 800 cycles to decode: the scheduler does it for all.
 // - A decoding step streams the weights: 16 tokens of 6 of 64 experts of 2816 x 2048,
 //   98 us for 586 MB, 6.0 TB/s.  Smaller boxes for the few rows of A measured the same.
+// - Few tiles leave SMs idle: with a long contraction 2 or 4 pairs of a cluster share
+//   a tile's k-blocks, keep their sums in shared memory and add them up from there
+//   (4096 rows of one expert, 256 x 256 fp32 weights' gradient: 29 us with one pair,
+//   19 us with four; 1 row, 14336 x 3528: 67 and 35 us).
 // - 64 tokens: 7.6 us, the latencies of launch, first tile, loads and stores in a row.
+#include <limits.h>
 #include <stddef.h>
 
 #include "../../include/moe_train.h"
@@ -94,9 +99,13 @@ constexpr int kChainBlocks = 8;  // k-blocks added up in one accumulator (fp32 o
 // for the expert would cost each role some 800 cycles a tile.
 struct __align__(16) Tile {
     int e, off, cnt, kblocks;
-    int mb, nb, pad0, pad1;
+    int mb, nb;
+    // a split contraction: this pair's first k-block of rows' products (a weights'
+    // gradient's off and cnt are its own rows), and the expert's rows
+    int k0, all;
 };
 constexpr int kQ = 8;  // slots of a tile queue
+constexpr int kMaxSplits = 4;    // pairs of a cluster that share a tile's contraction
 
 struct Barriers {
     Tile queue[kQ];             // each CTA: the tiles in order, from the leader's scheduler
@@ -148,16 +157,18 @@ __device__ __forceinline__ Tile read_slot(const Tile* p) {
     t.kblocks = q[3];
     t.mb = q[4];
     t.nb = q[5];
-    t.pad0 = t.pad1 = 0;
+    t.k0 = q[6];
+    t.all = q[7];
     return t;
 }
 
 // One thread takes tile i of the queue; false when there is none or the wait gave up.
+// first: the cluster's rank of the pair's leader, here and below.
 // In the leader every role reads the leader's queue.  In the peer only its producer
 // does and forwards each tile through the local queue, so that a tile crosses between
 // the CTAs once each way.
-__device__ __forceinline__ bool take(Barriers* c, int i, bool leader, volatile int* abort,
-                                     int* err, Tile& t) {
+__device__ __forceinline__ bool take(Barriers* c, int i, bool leader, uint32_t first,
+                                     volatile int* abort, int* err, Tile& t) {
     const int slot = i % kQ;
     const uint32_t ph = (uint32_t)(i / kQ) & 1u, full = smem_u32(&c->q_full[slot]);
     if (!(leader ? wait_bar(full, ph, abort, err) : wait_bar_cluster(full, ph, abort, err)))
@@ -167,7 +178,7 @@ __device__ __forceinline__ bool take(Barriers* c, int i, bool leader, volatile i
     if (leader)
         mbar_arrive(empty);
     else
-        mbar_arrive_remote(mapa_shared(empty, 0));
+        mbar_arrive_remote(mapa_shared(empty, first));
     return t.e >= 0;
 }
 __device__ __forceinline__ bool take_local(Barriers* c, int i, volatile int* abort, int* err,
@@ -190,17 +201,18 @@ __device__ __forceinline__ bool forward(Barriers* c, int i, const Tile& t, volat
     return true;
 }
 // Leader's scheduler: tile i (or the end) into both CTAs' queues.
-__device__ __forceinline__ bool publish(Barriers* c, int i, const Tile& t, volatile int* abort,
-                                        int* err) {
+__device__ __forceinline__ bool publish(Barriers* c, int i, const Tile& t, uint32_t first,
+                                        volatile int* abort, int* err) {
     const int slot = i % kQ;
     const uint32_t ph = (uint32_t)(i / kQ) & 1u, full = smem_u32(&c->q_full[slot]);
     if (!wait_bar(smem_u32(&c->q_empty[slot]), ph ^ 1u, abort, err)) return false;
     c->queue[slot] = t;
     mbar_arrive(full);
-    const uint32_t bar = mapa_shared(full, 1), at = mapa_shared(smem_u32(&c->queue[slot]), 1);
+    const uint32_t bar = mapa_shared(full, first + 1);
+    const uint32_t at = mapa_shared(smem_u32(&c->queue[slot]), first + 1);
     mbar_expect_tx_remote(bar, sizeof(Tile));
     st_async4(at, bar, t.e, t.off, t.cnt, t.kblocks);
-    st_async4(at + 16, bar, t.mb, t.nb, 0, 0);
+    st_async4(at + 16, bar, t.mb, t.nb, t.k0, t.all);
     return true;
 }
 // The next tile of a whole warp.
@@ -208,7 +220,7 @@ __device__ __forceinline__ bool warp_take(Barriers* c, int i, bool leader, volat
                                           int* err, Tile& t) {
     int more = 0;
     if ((threadIdx.x & 31) == 0)
-        more = leader ? take(c, i, true, abort, err, t) : take_local(c, i, abort, err, t);
+        more = leader ? take(c, i, true, 0, abort, err, t) : take_local(c, i, abort, err, t);
     if (!__shfl_sync(0xffffffffu, more, 0)) return false;
     t.e = __shfl_sync(0xffffffffu, t.e, 0);
     t.off = __shfl_sync(0xffffffffu, t.off, 0);
@@ -216,6 +228,7 @@ __device__ __forceinline__ bool warp_take(Barriers* c, int i, bool leader, volat
     t.kblocks = __shfl_sync(0xffffffffu, t.kblocks, 0);
     t.mb = __shfl_sync(0xffffffffu, t.mb, 0);
     t.nb = __shfl_sync(0xffffffffu, t.nb, 0);
+    t.all = __shfl_sync(0xffffffffu, t.all, 0);
     return true;
 }
 
@@ -285,18 +298,93 @@ __device__ __forceinline__ void store_lines(const uint8_t* staging, OutT* p, int
     }
 }
 
+// Split contractions: a pair's sums of its tile stay in the two CTAs' operand rings as
+// 128 rows of 256 fp32 columns, 16-byte chunks k at k ^ (row & 7) (32 rows' stores of a
+// chunk in different banks).
+template <int kN>
+__device__ __forceinline__ void put_part(uint8_t* ring, int row, int col, const uint32_t (&v)[kN]) {
+#pragma unroll
+    for (int k = 0; k < kN / 4; ++k)
+        *reinterpret_cast<uint4*>(ring + row * (BT * 4) + (((col / 4 + k) ^ (row & 7)) << 4)) =
+            make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+}
+// Then each pair adds up all pairs' sums, in their order, of a share of the tile's
+// columns, its CTAs for their rows, and writes them out (the epilogue warps).  A thread
+// has 8 columns at a time of kRows rows, all their loads under way together: another
+// CTA's shared memory is some 200 ns away.
+template <bool kW, int kSplits, typename OutT>
+__device__ __forceinline__ void join_parts(uint32_t ring, uint32_t rank, int split, const Tile& t,
+                                           int m_out, int n_out, OutT* out, int accumulate) {
+    constexpr int kGroups = BT / kSplits / 8, kRows = 8 / kSplits;
+    constexpr int kStep = 32 * kEpilogueWarps / kGroups;  // rows of one load of the warps
+    if (kW && accumulate && t.all == 0) return;  // nothing to add
+    const int row0 = t.mb * BT + (int)rank * BH, left = (kW ? m_out : t.cnt) - row0;
+    const int rows = left < BH ? left : BH;
+    const int u = (int)threadIdx.x - 128;
+    const int c = split * (BT / kSplits) + u % kGroups * 8, col = t.nb * BT + c;
+    if (col >= n_out) return;
+    OutT* to = out + ((kW ? (long long)t.e * m_out : (long long)t.off) + row0) * n_out + col;
+    uint32_t from[kSplits];
+#pragma unroll
+    for (int p = 0; p < kSplits; ++p) from[p] = mapa_shared(ring, 2 * p + rank);
+    for (int r0 = u / kGroups; r0 < rows; r0 += kRows * kStep) {
+        float4 v[kRows][kSplits][2];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i * kStep;
+            const uint32_t at = (uint32_t)(r * (BT * 4)), ch = (uint32_t)c / 4, sw = r & 7;
+            if (r < rows) {
+#pragma unroll
+                for (int p = 0; p < kSplits; ++p) {
+                    v[i][p][0] = ld_cluster4(from[p] + at + ((ch ^ sw) << 4));
+                    v[i][p][1] = ld_cluster4(from[p] + at + (((ch + 1) ^ sw) << 4));
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i * kStep;
+            if (r >= rows) break;
+#pragma unroll
+            for (int p = 1; p < kSplits; ++p) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v[i][0][h].x += v[i][p][h].x;
+                    v[i][0][h].y += v[i][p][h].y;
+                    v[i][0][h].z += v[i][p][h].z;
+                    v[i][0][h].w += v[i][p][h].w;
+                }
+            }
+            const float4 x = v[i][0][0], y = v[i][0][1];
+            if constexpr (sizeof(OutT) == 4) {
+                float4* line = reinterpret_cast<float4*>(to + (long long)r * n_out);
+                if (accumulate) {
+                    const float4 a = line[0], b = line[1];
+                    line[0] = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+                    line[1] = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
+                } else {
+                    line[0] = x;
+                    line[1] = y;
+                }
+            } else {
+                *reinterpret_cast<uint4*>(to + (long long)r * n_out) = make_uint4(
+                    pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
+            }
+        }
+    }
+}
+
 // kMode, and for kWeightsGrad K unused, m_out x n_out = C_out x C_in; otherwise
 // K the contraction and n_out the columns of out.  a_groups, b_groups: the map of an
 // MN-major operand has its groups of 64 columns as a dimension.
-template <int kMode, typename OutT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    grouped_product_kernel(const __grid_constant__ CUtensorMap tmA,
-                           const __grid_constant__ CUtensorMap tmB,
-                           const __grid_constant__ CUtensorMap tmOut,
-                           const int32_t* __restrict__ expert_offsets,
-                           const int32_t* __restrict__ expert_counts, int E, int R, int K,
-                           int m_out, int n_out, OutT* __restrict__ out, int accumulate,
-                           int a_groups, int b_groups, int* err, int* tile_counter) {
+// kSplit: a cluster of several pairs has one tile, each pair a share of its
+// contraction, and the pairs' sums are joined at the end.
+template <int kMode, typename OutT, bool kSplit>
+__device__ __forceinline__ void grouped_product(
+    const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmOut,
+    const int32_t* __restrict__ expert_offsets, const int32_t* __restrict__ expert_counts, int E,
+    int R, int K, int m_out, int n_out, OutT* __restrict__ out, int accumulate, int a_groups,
+    int b_groups, int* err, int* tile_counter) {
     constexpr bool kW = kMode == kWeightsGrad;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -316,7 +404,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr int kQueueReaders = kLocalReaders + 3;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();  // 0 = leader
+    // the pair's leader is the even one of its two CTAs of the cluster
+    const uint32_t in_cluster = cluster_rank(), rank = in_cluster & 1u;
+    const uint32_t first = kSplit ? in_cluster & ~1u : 0u;
+    const int split = kSplit ? (int)(in_cluster >> 1) : 0;
+    const int splits = kSplit ? (int)(cluster_ctas() >> 1) : 1;
+    const uint16_t pair_mask = (uint16_t)(0x3u << first), leader_mask = (uint16_t)(0x1u << first);
     const bool leader = rank == 0;
     const int MB = (m_out + BT - 1) / BT;
     const int NB = (n_out + BT - 1) / BT;
@@ -326,7 +419,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // take the longest, and the short ones fill the pairs up at the end (Zipf-skewed
     // case of 262144 rows in 128 experts: 2190 us in the experts' order, 2040 so).
     bool sorted = false;
-    if constexpr (kW) {
+    if constexpr (kW && !kSplit) {
         sorted = E <= kMaxSorted && E * MB * NB > (int)(gridDim.x / 2);
         if (sorted && leader) {
             int* cnts = reinterpret_cast<int*>(tiles);  // the operand ring, not in use yet
@@ -378,6 +471,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         blocks_end = warp_prefix(blocks_in);
         total = __shfl_sync(0xffffffffu, blocks_end, 31) * NB;
+        // only a layout whose segments overlap has more tiles than the host allowed for
+        if (kSplit && blockIdx.x == 0 && lane == 0 && total > (int)gridDim.x / (2 * splits))
+            set_error(err, MOE_ERR_INVALID_ARG);
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(&ctl->tmem_base), kTmemCols);
@@ -388,18 +484,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();  // both CTAs' barriers exist before any remote signal
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
+    Tile joined = {};  // the tile of a split contraction (epilogue warps)
+    joined.e = -1;
     if (warp < 4) {
         regs_shrink<kRegsOther>();
         if (warp == 0 && lane == 0) {
             // ---------------- TMA producer (both CTAs) ----------------
-            const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
+            const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), first);
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
                 Tile t = {};
                 t.e = -1;
-                bool more = take(ctl, i, leader, abort_flag, err, t);
+                bool more = take(ctl, i, leader, first, abort_flag, err, t);
                 if (leader && more) mbar_arrive(smem_u32(&ctl->q_taken[i % kQ]));
                 if (!leader && !forward(ctl, i, t, abort_flag, err)) more = false;
                 if (!more) break;
@@ -454,15 +552,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     } else {
                         const uint32_t full = full0 + (uint32_t)stage * 8u;
+                        const int k = (kSplit ? t.k0 + kb : kb) * BK;
                         if (leader) mbar_expect_tx(full_local, 2 * STAGE_BYTES);
-                        tma_load_2d_pair(a_s, &tmA, full, kb * BK, off + a0);
+                        tma_load_2d_pair(a_s, &tmA, full, k, off + a0);
                         if (kMnB && b_groups) {
-                            tma_load_4d_pair(b_s, &tmB, full, 0, kb * BK, b0 / 64, t.e);
+                            tma_load_4d_pair(b_s, &tmB, full, 0, k, b0 / 64, t.e);
                         } else if (kMnB) {
-                            tma_load_3d_pair(b_s, &tmB, full, b0, kb * BK, t.e);
-                            tma_load_3d_pair(b_s + BOX_BYTES, &tmB, full, b0 + 64, kb * BK, t.e);
+                            tma_load_3d_pair(b_s, &tmB, full, b0, k, t.e);
+                            tma_load_3d_pair(b_s + BOX_BYTES, &tmB, full, b0 + 64, k, t.e);
                         } else {
-                            tma_load_3d_pair(b_s, &tmB, full, kb * BK, b0, t.e);
+                            tma_load_3d_pair(b_s, &tmB, full, k, b0, t.e);
                         }
                     }
                     if (++stage == kStages) {
@@ -486,7 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int i = 0; ok; ++i) {
                 Tile t = {};
-                if (!take(ctl, i, true, abort_flag, err, t)) break;
+                if (!take(ctl, i, true, first, abort_flag, err, t)) break;
                 // K steps of the last block (a segment's end)
                 const int last_steps =
                     kW ? (t.cnt - (t.kblocks - 1) * BK + UMMA_K - 1) / UMMA_K
@@ -521,14 +620,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             umma_bf16_pair(d, ad + kStepA * kk, bd + kStepB * kk, idesc,
                                            (in_chain | kk) != 0 ? 1u : 0u);
                     }
-                    umma_commit_pair_multicast(smem_u32(&ctl->empty[stage]), 0x3);
+                    umma_commit_pair_multicast(smem_u32(&ctl->empty[stage]), pair_mask);
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                     ++in_chain;
                     if ((kChained && in_chain == kChainBlocks) || kb == t.kblocks - 1) {
-                        umma_commit_pair_multicast(smem_u32(&ctl->tfull[acc]), 0x3);
+                        umma_commit_pair_multicast(smem_u32(&ctl->tfull[acc]), pair_mask);
                         in_chain = 0;
                         if (++acc == kAccs) {
                             acc = 0;
@@ -537,13 +636,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            umma_commit_pair_multicast(smem_u32(&ctl->done), 0x1);
+            umma_commit_pair_multicast(smem_u32(&ctl->done), leader_mask);
             wait_bar_drain(smem_u32(&ctl->done), 0);
         } else if (warp == 2 && leader) {
             // ---------------- tile scheduler (leader) ----------------
             // The pair's first tile is its own index; the counter hands out the ones
             // after the pairs'.  Tile i is published once the producer has taken tile
-            // i - kAhead.
+            // i - kAhead.  (A split contraction's tile is its cluster's index, the only one.)
             const int pairs = (int)(gridDim.x / 2);
             int e = -1, off = 0, cnt = 0;  // the last tile's expert (weights' gradient)
             for (int i = 0;; ++i) {
@@ -555,7 +654,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ok = wait_bar(smem_u32(&ctl->q_taken[j % kQ]), (uint32_t)(j / kQ) & 1u,
                                       abort_flag, err);
                     }
-                    if (ok)
+                    if (ok && kSplit)
+                        tile = i == 0 ? (int)blockIdx.x / (2 * splits) : INT_MAX;
+                    else if (ok)
                         tile = i == 0 ? (int)(blockIdx.x / 2) : pairs + atomicAdd(tile_counter, 1);
                 }
                 tile = __shfl_sync(0xffffffffu, tile, 0);
@@ -606,13 +707,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+                if (kSplit && t.e >= 0) {
+                    const int all = t.kblocks;
+                    t.k0 = (int)((long long)all * split / splits);
+                    t.kblocks = (int)((long long)all * (split + 1) / splits) - t.k0;
+                    t.all = t.cnt;
+                    if (kW) {
+                        const int end = (t.k0 + t.kblocks) * BK;
+                        t.off += t.k0 * BK;
+                        t.cnt = (t.cnt < end ? t.cnt : end) - t.k0 * BK;
+                    }
+                }
                 int more = 0;
-                if (lane == 0) more = publish(ctl, i, t, abort_flag, err) && t.e >= 0;
+                if (lane == 0) more = publish(ctl, i, t, first, abort_flag, err) && t.e >= 0;
                 if (!__shfl_sync(0xffffffffu, more, 0)) break;
             }
         } else if (kW && warp == 3) {
             // ---------------- block ends (both CTAs) ----------------
-            const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
+            const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), first);
             int stage = 0;
             uint32_t land_phase = 0;
             for (int i = 0;; ++i) {
@@ -649,13 +761,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int q = warp & 3;               // TMEM lane quadrant
         const int half = (warp - 4) >> 2;     // 128 columns of the tile
         uint8_t* staging = staging_area + (size_t)(warp - 4) * kStagingBytes;
-        const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[0]), 0);
+        const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[0]), first);
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int i = 0;; ++i) {
             Tile t = {};
             if (!warp_take(ctl, i, leader, abort_flag, err, t)) break;
-            if (kW && t.kblocks == 0 && accumulate) continue;  // nothing to add
+            if (!kSplit && kW && t.kblocks == 0 && accumulate) continue;  // nothing to add
+            if (kSplit) joined = t;
 
             // this warp's part of the next accumulator, once it is ready
             const auto ready = [&]() {
@@ -718,6 +831,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t at = part();
             const auto put = [&](int c, const uint32_t (&v)[kLine]) {
                 if (rows <= 0 || col + c >= n_out) return;
+                if constexpr (kSplit) {
+                    put_part<kLine>(tiles, q * 32 + lane, half * kEpilogueCols + c, v);
+                    return;
+                }
                 if (lane == 0) bulk_wait_read();  // the line before has been read
                 __syncwarp();
                 put_line<OutT>(staging, lane, v);
@@ -780,12 +897,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // no CTA leaves while its peer may still signal it
+    if constexpr (kSplit) {
+        if (joined.e >= 0 && splits == 2)
+            join_parts<kW, 2>(tiles_addr, rank, split, joined, m_out, n_out, out, accumulate);
+        else if (joined.e >= 0)
+            join_parts<kW, kMaxSplits>(tiles_addr, rank, split, joined, m_out, n_out, out,
+                                       accumulate);
+        __syncwarp();
+        cluster_sync();  // nor while its part is read
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, kTmemCols);
     }
     // the tile counter returns to zero for the next launch (the last pair out)
-    if (leader && threadIdx.x == 0) {
+    if (!kSplit && leader && threadIdx.x == 0) {
         __threadfence();
         const int before = atomicAdd(tile_counter + 1, 1);
         if (before == (int)(gridDim.x / 2) - 1) {
@@ -796,26 +922,111 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int kMode, typename OutT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    grouped_product_kernel(const __grid_constant__ CUtensorMap tmA,
+                           const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmOut,
+                           const int32_t* __restrict__ expert_offsets,
+                           const int32_t* __restrict__ expert_counts, int E, int R, int K,
+                           int m_out, int n_out, OutT* __restrict__ out, int accumulate,
+                           int a_groups, int b_groups, int* err, int* tile_counter) {
+    grouped_product<kMode, OutT, false>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R, K,
+                                        m_out, n_out, out, accumulate, a_groups, b_groups, err,
+                                        tile_counter);
+}
+// Launched with clusters of 2 * splits CTAs.
+template <int kMode, typename OutT>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_product_split_kernel(const __grid_constant__ CUtensorMap tmA,
+                                 const __grid_constant__ CUtensorMap tmB,
+                                 const __grid_constant__ CUtensorMap tmOut,
+                                 const int32_t* __restrict__ expert_offsets,
+                                 const int32_t* __restrict__ expert_counts, int E, int R, int K,
+                                 int m_out, int n_out, OutT* __restrict__ out, int accumulate,
+                                 int a_groups, int b_groups, int* err, int* tile_counter) {
+    grouped_product<kMode, OutT, true>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R, K,
+                                       m_out, n_out, out, accumulate, a_groups, b_groups, err,
+                                       tile_counter);
+}
+
+// Clusters of 2 * splits CTAs that the device holds at once.
+template <typename Kernel>
+int clusters_at_once(Kernel kernel, int splits, size_t smem) {
+    cudaLaunchAttribute cluster[1];
+    cluster[0].id = cudaLaunchAttributeClusterDimension;
+    cluster[0].val.clusterDim.x = 2 * splits;
+    cluster[0].val.clusterDim.y = cluster[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * splits);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = cluster;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
+
+template <int kMode, typename OutT>
 moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
-                  const GemmGroup& g, long long tiles,
+                  const GemmGroup& g, long long tiles, long long blocks,
                   int K, int m_out, int n_out, void* out, bool accumulate, int a_groups,
                   int b_groups, cudaStream_t st) {
     if (tiles >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
-    // the attribute holds for the process and device: set once for each
+    // the attributes hold for the process and device: set once for each
+    constexpr size_t smem = smem_bytes<kMode>();
+    const auto split_kernel = grouped_product_split_kernel<kMode, OutT>;
     static bool set[64] = {false};
+    static int at_once[64][2];  // clusters of 2 pairs and of 4
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-    if (dev >= 64 || !set[dev]) {
+    if (dev >= 64) return MOE_ERR_UNSUPPORTED;
+    if (!set[dev]) {
         if (cudaFuncSetAttribute(grouped_product_kernel<kMode, OutT>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem_bytes<kMode>()) != cudaSuccess)
+                                 (int)smem) != cudaSuccess ||
+            cudaFuncSetAttribute(split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem) != cudaSuccess)
             return MOE_ERR_CUDA;
-        if (dev < 64) set[dev] = true;
+        at_once[dev][0] = clusters_at_once(split_kernel, 2, smem);
+        at_once[dev][1] = clusters_at_once(split_kernel, kMaxSplits, smem);
+        set[dev] = true;
+    }
+    // Pairs that share a tile's contraction: as long as all clusters run side by side, and
+    // what a pair no longer has to do, some 0.3 us a k-block, is more than what the
+    // joining of the sums takes: 1 us for a few rows, 6 us for a tile's 256 (1 row, 4096 x
+    // 3528: 25 us with one pair a tile, 16 us with four; K = 512: 8.1 and 7.8 us with two;
+    // 256 x 256 sums of 1024 rows: 13.7 and 14.9 us with four, 4096 rows: 29 and 19 us).
+    const long long m = kMode == kWeightsGrad ? m_out : g.R;
+    const long long join_blocks = 4 + 16 * (m < BT ? m : BT) / BT;
+    int splits = 1;
+    if (tiles <= at_once[dev][1] && blocks * 3 > join_blocks * 4)
+        splits = kMaxSplits;
+    else if (tiles <= at_once[dev][0] && blocks > join_blocks * 2)
+        splits = 2;
+    if (splits > 1) {
+        cudaLaunchAttribute cluster[1];
+        cluster[0].id = cudaLaunchAttributeClusterDimension;
+        cluster[0].val.clusterDim.x = 2 * splits;
+        cluster[0].val.clusterDim.y = cluster[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(tiles * 2 * splits));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cfg.attrs = cluster;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, split_kernel, a, b, o,
+                                  (const int32_t*)g.offsets, (const int32_t*)g.counts, g.E,
+                                  (int)g.R, K, m_out, n_out, reinterpret_cast<OutT*>(out),
+                                  accumulate ? 1 : 0, a_groups, b_groups, g.err,
+                                  (int*)nullptr) == cudaSuccess
+                   ? MOE_OK
+                   : MOE_ERR_CUDA;
     }
     const long long pairs_max = sm_count() / 2;
     const long long pairs = tiles < pairs_max ? tiles : pairs_max;
     grouped_product_kernel<kMode, OutT>
-        <<<(int)(2 * (pairs > 0 ? pairs : 1)), kThreads, smem_bytes<kMode>(), st>>>(
+        <<<(int)(2 * (pairs > 0 ? pairs : 1)), kThreads, smem, st>>>(
             a, b, o, g.offsets, g.counts, g.E, (int)g.R, K, m_out, n_out,
             reinterpret_cast<OutT*>(out), accumulate ? 1 : 0, a_groups, b_groups, g.err, g.prefix + g.E + 1);
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -863,14 +1074,17 @@ moe_status launch_rows(const uint16_t* rows, const GemmGroup& g, int c_in, int c
                                 : map_rows(&b, w, g.E, c_out, c_in, BH)) &&
                     map_lines(&o, out, 0, g.R, n_out, out_f32);
     if (!ok) return MOE_ERR_UNSUPPORTED;
-    const long long tiles = ((g.R + BT - 1) / BT + g.E) * ((n_out + BT - 1LL) / BT);
+    // at most as many row blocks as experts with rows and whole blocks besides
+    const long long used = g.R < g.E ? g.R : g.E;
+    const long long tiles = (used + (g.R - used) / BT) * ((n_out + BT - 1LL) / BT);
+    const long long blocks = (K + BK - 1LL) / BK;
     using bf16 = __nv_bfloat16;
     if (input_grad)
         return out_f32
-                   ? launch<kRowsGrad, float>(a, b, o, g, tiles, K, 0, n_out, out, false, 0, groups, st)
-                   : launch<kRowsGrad, bf16>(a, b, o, g, tiles, K, 0, n_out, out, false, 0, groups, st);
-    return out_f32 ? launch<kForward, float>(a, b, o, g, tiles, K, 0, n_out, out, false, 0, 0, st)
-                   : launch<kForward, bf16>(a, b, o, g, tiles, K, 0, n_out, out, false, 0, 0, st);
+                   ? launch<kRowsGrad, float>(a, b, o, g, tiles, blocks, K, 0, n_out, out, false, 0, groups, st)
+                   : launch<kRowsGrad, bf16>(a, b, o, g, tiles, blocks, K, 0, n_out, out, false, 0, groups, st);
+    return out_f32 ? launch<kForward, float>(a, b, o, g, tiles, blocks, K, 0, n_out, out, false, 0, 0, st)
+                   : launch<kForward, bf16>(a, b, o, g, tiles, blocks, K, 0, n_out, out, false, 0, 0, st);
 }
 
 moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const GemmGroup& g, int c_in,
@@ -883,9 +1097,10 @@ moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const Gemm
         return MOE_ERR_UNSUPPORTED;
     const long long tiles =
         (long long)g.E * ((c_out + BT - 1) / BT) * ((c_in + BT - 1LL) / BT);
-    return out_f32 ? launch<kWeightsGrad, float>(a, b, o, g, tiles, 0, c_out, c_in, dw, accumulate,
+    const long long blocks = g.R / g.E / BK;  // of an expert, on average
+    return out_f32 ? launch<kWeightsGrad, float>(a, b, o, g, tiles, blocks, 0, c_out, c_in, dw, accumulate,
                                                  a_groups, b_groups, st)
-                   : launch<kWeightsGrad, __nv_bfloat16>(a, b, o, g, tiles, 0, c_out, c_in, dw,
+                   : launch<kWeightsGrad, __nv_bfloat16>(a, b, o, g, tiles, blocks, 0, c_out, c_in, dw,
                                                          accumulate, a_groups, b_groups, st);
 }
 

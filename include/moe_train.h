@@ -41,9 +41,12 @@ typedef enum {
  * accumulate != 0 adds to dw, which has to be fp32 then (MOE_ERR_UNSUPPORTED
  * otherwise); accumulate == 0 overwrites it, with zeros for an expert without
  * rows (and for every expert when N == 0).
+ * Where there are few tiles for the device's SMs, several of them share a long
+ * contraction and add up their fp32 sums in a fixed order; how many depends on N*k,
+ * E, C_in and C_out (and the device) only.
  * ws: workspace of moe_workspace_bytes(shape) bytes.  A layout whose segments
  * leave the N*k rows is reported there (moe_get_error) and those segments are
- * taken as empty. */
+ * taken as empty; segments that overlap may be reported, too. */
 moe_status moe_grouped_gemm(const uint16_t* rows, const moe_layout* layout,
                             const moe_shape* shape, int32_t C_in, int32_t C_out,
                             const uint16_t* w, void* out, int32_t out_type, void* ws,
@@ -103,8 +106,9 @@ typedef enum {
     MOE_GATE_TOKEN = 2    /* fp32 [N], one a row */
 } moe_gate;
 
-/* N rows of width H (a multiple of 8, at most 16384).  post, pre: whether there
- * is an RMS norm after the block and one before the next.  gate: a moe_gate.
+/* N rows (less than 2^31 - 2^20) of width H (a multiple of 8, at most 16384).
+ * post, pre: whether there is an RMS norm after the block and one before the
+ * next.  gate: a moe_gate.
  * stream_type: the moe_type of the residual stream and its gradients. */
 typedef struct {
     int32_t N, H;
