@@ -82,13 +82,18 @@ constexpr int kAccs = 2;
 constexpr int kTmemCols = BT * kAccs;
 constexpr int OP_BYTES = BH * BK * 2;   // one operand of one stage in one CTA
 constexpr int BOX_BYTES = OP_BYTES / 2;  // an MN-major box: 64 columns x 64 rows
-constexpr int STAGE_BYTES = 2 * OP_BYTES;
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
 constexpr int kEpilogueCols = BT / 2;  // columns of one epilogue warp
 // Registers a thread: 384 x 168 at launch = 128 x 88 + 256 x 208.
 constexpr int kRegsOther = 88, kRegsEpilogue = 208;
-constexpr int kStages = 6;
+// A tile of few rows: their number, which is the MMA's N (see kFew).
+constexpr int BF = 64;
+constexpr int FEW_BYTES = BF / 2 * BK * 2;  // that operand of one stage in one CTA
+template <bool kFew>
+constexpr int kStageBytes = kFew ? OP_BYTES + FEW_BYTES : 2 * OP_BYTES;
+template <bool kFew>
+constexpr int kStagesOf = kFew ? 9 : 6;
 constexpr int kAhead = 2;  // tiles the scheduler publishes ahead of the leader's producer
 constexpr int kStagingBytes = 32 * 128;  // an epilogue warp's output: 32 lines
 constexpr int kChainBlocks = 8;  // k-blocks added up in one accumulator (fp32 outputs)
@@ -105,14 +110,13 @@ struct __align__(16) Tile {
     int k0, all;
 };
 constexpr int kQ = 8;  // slots of a tile queue
+// Rows an expert, on average, up to which products take tiles of few rows.
+constexpr int kFewRows = 64;
 constexpr int kMaxSplits = 4;    // pairs of a cluster that share a tile's contraction
 
-struct Barriers {
+struct Queues {
     Tile queue[kQ];             // each CTA: the tiles in order, from the leader's scheduler
     Tile local[kQ];             // peer: the tiles its producer forwards to its other warps
-    uint64_t full[kStages];     // leader: both CTAs' operands of a stage are there
-    uint64_t empty[kStages];    // each CTA: its stage may be refilled
-    uint64_t land[kStages];     // each CTA: its copies of a segment's last block are there
     uint64_t tfull[kAccs];      // each CTA: accumulator ready
     uint64_t tempty[kAccs];     // leader: accumulator drained by both CTAs
     uint64_t done;              // leader: every issued MMA retired
@@ -124,19 +128,29 @@ struct Barriers {
     uint32_t tmem_base;
     int abort;
 };
-template <int kMode>
-struct Ctl : Barriers {};
+constexpr int kQueueBarriers = 2 * kAccs + 1 + 5 * kQ;
+static_assert(offsetof(Queues, tmem_base) - offsetof(Queues, tfull) ==
+                  kQueueBarriers * sizeof(uint64_t),
+              "the queues' barriers lie side by side");
+template <int kStages>
+struct Barriers : Queues {
+    uint64_t full[kStages];     // leader: both CTAs' operands of a stage are there
+    uint64_t empty[kStages];    // each CTA: its stage may be refilled
+    uint64_t land[kStages];     // each CTA: its copies of a segment's last block are there
+};
+template <int kMode, bool kFew>
+struct Ctl : Barriers<kStagesOf<kFew>> {};
 constexpr int kMaxSorted = 512;  // what is left of shared memory holds
 template <>
-struct Ctl<kWeightsGrad> : Barriers {
+struct Ctl<kWeightsGrad, false> : Barriers<kStagesOf<false>> {
     uint16_t order[kMaxSorted];  // experts by falling number of rows
 };
 
-template <int kMode>
+template <int kMode, bool kFew>
 constexpr size_t smem_bytes() {
-    constexpr size_t n = 1024 + (size_t)kStages * STAGE_BYTES +
+    constexpr size_t n = 1024 + (size_t)kStagesOf<kFew> * kStageBytes<kFew> +
                          (size_t)kEpilogueWarps * kStagingBytes +
-                         ((sizeof(Ctl<kMode>) + 15) & ~size_t(15));
+                         ((sizeof(Ctl<kMode, kFew>) + 15) & ~size_t(15));
     static_assert(n <= 227 * 1024, "shared memory of one block");
     return n;
 }
@@ -167,7 +181,7 @@ __device__ __forceinline__ Tile read_slot(const Tile* p) {
 // In the leader every role reads the leader's queue.  In the peer only its producer
 // does and forwards each tile through the local queue, so that a tile crosses between
 // the CTAs once each way.
-__device__ __forceinline__ bool take(Barriers* c, int i, bool leader, uint32_t first,
+__device__ __forceinline__ bool take(Queues* c, int i, bool leader, uint32_t first,
                                      volatile int* abort, int* err, Tile& t) {
     const int slot = i % kQ;
     const uint32_t ph = (uint32_t)(i / kQ) & 1u, full = smem_u32(&c->q_full[slot]);
@@ -181,7 +195,7 @@ __device__ __forceinline__ bool take(Barriers* c, int i, bool leader, uint32_t f
         mbar_arrive_remote(mapa_shared(empty, first));
     return t.e >= 0;
 }
-__device__ __forceinline__ bool take_local(Barriers* c, int i, volatile int* abort, int* err,
+__device__ __forceinline__ bool take_local(Queues* c, int i, volatile int* abort, int* err,
                                            Tile& t) {
     const int slot = i % kQ;
     const uint32_t ph = (uint32_t)(i / kQ) & 1u;
@@ -191,7 +205,7 @@ __device__ __forceinline__ bool take_local(Barriers* c, int i, volatile int* abo
     return t.e >= 0;
 }
 // Peer's producer: tile i (or its end) on to the peer's other warps.
-__device__ __forceinline__ bool forward(Barriers* c, int i, const Tile& t, volatile int* abort,
+__device__ __forceinline__ bool forward(Queues* c, int i, const Tile& t, volatile int* abort,
                                         int* err) {
     const int slot = i % kQ;
     const uint32_t ph = (uint32_t)(i / kQ) & 1u;
@@ -201,7 +215,7 @@ __device__ __forceinline__ bool forward(Barriers* c, int i, const Tile& t, volat
     return true;
 }
 // Leader's scheduler: tile i (or the end) into both CTAs' queues.
-__device__ __forceinline__ bool publish(Barriers* c, int i, const Tile& t, uint32_t first,
+__device__ __forceinline__ bool publish(Queues* c, int i, const Tile& t, uint32_t first,
                                         volatile int* abort, int* err) {
     const int slot = i % kQ;
     const uint32_t ph = (uint32_t)(i / kQ) & 1u, full = smem_u32(&c->q_full[slot]);
@@ -216,7 +230,7 @@ __device__ __forceinline__ bool publish(Barriers* c, int i, const Tile& t, uint3
     return true;
 }
 // The next tile of a whole warp.
-__device__ __forceinline__ bool warp_take(Barriers* c, int i, bool leader, volatile int* abort,
+__device__ __forceinline__ bool warp_take(Queues* c, int i, bool leader, volatile int* abort,
                                           int* err, Tile& t) {
     int more = 0;
     if ((threadIdx.x & 31) == 0)
@@ -377,27 +391,81 @@ __device__ __forceinline__ void join_parts(uint32_t ring, uint32_t rank, int spl
 // kMode, and for kWeightsGrad K unused, m_out x n_out = C_out x C_in; otherwise
 // K the contraction and n_out the columns of out.  a_groups, b_groups: the map of an
 // MN-major operand has its groups of 64 columns as a dimension.
+// Tiles of few rows: a warp's sums are 32 columns of the output (its TMEM lanes) by 32
+// rows, and leave by way of 32 lines of 128 bytes in shared memory, one a row.  One with
+// its pair's share of the contraction only has its lines in the ring instead.
+__device__ __forceinline__ void put_few(uint8_t* lines, int lane, const uint32_t (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) *reinterpret_cast<uint32_t*>(lines + j * 128 + lane * 4) = v[j];
+}
+template <typename OutT>
+__device__ __forceinline__ void store_few(OutT* to, const float4& v) {
+    if constexpr (sizeof(OutT) == 4)
+        *reinterpret_cast<float4*>(to) = v;
+    else
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+}
+// A tile of few rows of a warp: the first of its rows in the outputs, how many of its 32
+// there are, its first column.
+struct FewPart {
+    long long row;
+    int rows, col;
+};
+__device__ __forceinline__ FewPart few_part(const Tile& t, uint32_t rank) {
+    const int warp = (int)(threadIdx.x >> 5), at = t.mb * BF + ((warp - 4) >> 2) * 32;
+    return {(long long)t.off + at, t.cnt - at, t.nb * BT + (int)rank * BH + (warp & 3) * 32};
+}
+// The joining of a split one: the pairs take its rows in turn.
+template <int kSplits, typename OutT>
+__device__ __forceinline__ void join_few(uint32_t ring, uint32_t rank, int split, const Tile& t,
+                                         int n_out, OutT* out) {
+    const FewPart f = few_part(t, rank);
+    const int lane = threadIdx.x & 31, col = f.col + (lane & 7) * 4;
+    if (col >= n_out) return;
+    const uint32_t at = ring + ((threadIdx.x >> 5) - 4) * kStagingBytes + (lane & 7) * 16;
+    for (int r = (lane >> 3) * kSplits + split; r < 32 && r < f.rows; r += 4 * kSplits) {
+        float4 v[kSplits];
+#pragma unroll
+        for (int p = 0; p < kSplits; ++p) v[p] = ld_cluster4(mapa_shared(at, 2 * p + rank) + r * 128);
+#pragma unroll
+        for (int p = 1; p < kSplits; ++p) {
+            v[0].x += v[p].x;
+            v[0].y += v[p].y;
+            v[0].z += v[p].z;
+            v[0].w += v[p].w;
+        }
+        store_few(out + (f.row + r) * n_out + col, v[0]);
+    }
+}
+
+// kFew (products over rows): tiles of 256 columns of the output and BF rows, the matrix
+// being A and the rows B.  An MMA takes the same time for 1 row and for 128 of A, and 512
+// cycles a k-block for 256 of B, which is longer than the 32 KB of the matrix need to come
+// in; so it is a quarter of that, and the stages are 9.
 // kSplit: a cluster of several pairs has one tile, each pair a share of its
 // contraction, and the pairs' sums are joined at the end.
-template <int kMode, typename OutT, bool kSplit>
+template <int kMode, typename OutT, bool kFew, bool kSplit>
 __device__ __forceinline__ void grouped_product(
     const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmOut,
     const int32_t* __restrict__ expert_offsets, const int32_t* __restrict__ expert_counts, int E,
     int R, int K, int m_out, int n_out, OutT* __restrict__ out, int accumulate, int a_groups,
     int b_groups, int* err, int* tile_counter) {
     constexpr bool kW = kMode == kWeightsGrad;
+    static_assert(!kW || !kFew, "a weights' gradient has no tiles of few rows");
+    constexpr int kStages = kStagesOf<kFew>, STAGE_BYTES = kStageBytes<kFew>;
+    constexpr int kTileRows = kFew ? BF : BT;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t* tiles = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
     const uint32_t tiles_addr = smem_u32(tiles);
     uint8_t* staging_area = tiles + (size_t)kStages * STAGE_BYTES;
-    Ctl<kMode>* ctl = reinterpret_cast<Ctl<kMode>*>(staging_area +
+    auto* ctl = reinterpret_cast<Ctl<kMode, kFew>*>(staging_area +
                                                     (size_t)kEpilogueWarps * kStagingBytes);
     volatile int* abort_flag = &ctl->abort;
 
     constexpr bool kChained = sizeof(OutT) == 4;  // see kChainBlocks
-    constexpr bool kMnA = kW;                 // the contraction runs along A's rows
-    constexpr bool kMnB = kMode != kForward;  // and along B's
+    constexpr bool kMnA = kW;                 // the contraction runs along tmA's rows
+    constexpr bool kMnB = kMode != kForward;  // and along tmB's
     // readers of a slot of the leader's queue: its producer, MMA thread,
     // epilogue warps (and block-end warp), and the peer's producer
     constexpr int kLocalReaders = kEpilogueWarps + (kW ? 1 : 0);
@@ -435,27 +503,23 @@ __device__ __forceinline__ void grouped_product(
             fence_async_shared();  // before TMA writes there
         }
     }
-    // one barrier a thread, not 63 of them one after the other
-    constexpr int kBarriers = 3 * kStages + 2 * kAccs + 1 + 5 * kQ;
-    static_assert(kBarriers <= 64 && offsetof(Barriers, tmem_base) - offsetof(Barriers, full) ==
-                                         kBarriers * sizeof(uint64_t),
-                  "the barriers lie side by side");
+    // one or two barriers a thread, not 63 and more of them one after the other
+    static_assert(3 * kStages <= 64 && kQueueBarriers <= 64, "barriers of 64 threads");
     if (warp == 4 || warp == 5) {
-        const int i = threadIdx.x - 128;
-        const int q = i - (3 * kStages + 2 * kAccs + 1);  // past the stages' and accumulators'
+        const int i = threadIdx.x - 128, q = i - (2 * kAccs + 1);
         int count = 1;
-        if (kW && i < kStages) count = 2;                                       // full
-        if (i >= 3 * kStages + kAccs && i < 3 * kStages + 2 * kAccs) count = 2 * kEpilogueWarps;
-        if (q >= kQ && q < 2 * kQ) count = kQueueReaders;                       // q_empty
-        if (q >= 4 * kQ) count = kLocalReaders;                                 // l_empty
-        if (i < kBarriers) mbar_init(smem_u32(&ctl->full[0] + i), count);
+        if (i >= kAccs && i < 2 * kAccs) count = 2 * kEpilogueWarps;  // tempty
+        if (q >= kQ && q < 2 * kQ) count = kQueueReaders;             // q_empty
+        if (q >= 4 * kQ) count = kLocalReaders;                       // l_empty
+        if (i < kQueueBarriers) mbar_init(smem_u32(&ctl->tfull[0] + i), count);
+        if (i < 3 * kStages) mbar_init(smem_u32(&ctl->full[0] + i), kW && i < kStages ? 2 : 1);
         if (i == 63) ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0 && lane == 0) {
         prefetch_map(&tmA);
         prefetch_map(&tmB);
-        prefetch_map(&tmOut);
+        if (!kFew) prefetch_map(&tmOut);
     }
     // Products over rows: lane l of the scheduler holds the row blocks in its run of
     // experts [l * per, (l + 1) * per) and up to its end.
@@ -466,7 +530,7 @@ __device__ __forceinline__ void grouped_product(
         for (int j = 0; j < per; ++j) {
             if (lane * per + j < E) {
                 segment(expert_offsets, expert_counts, lane * per + j, R, err, &run_off, &run_cnt);
-                blocks_in += (run_cnt + BT - 1) / BT;
+                blocks_in += (run_cnt + kTileRows - 1) / kTileRows;
             }
         }
         blocks_end = warp_prefix(blocks_in);
@@ -553,15 +617,18 @@ __device__ __forceinline__ void grouped_product(
                     } else {
                         const uint32_t full = full0 + (uint32_t)stage * 8u;
                         const int k = (kSplit ? t.k0 + kb : kb) * BK;
+                        // the matrix is B, or A of a tile of few rows
+                        const uint32_t w_s = kFew ? a_s : b_s, r_s = kFew ? b_s : a_s;
                         if (leader) mbar_expect_tx(full_local, 2 * STAGE_BYTES);
-                        tma_load_2d_pair(a_s, &tmA, full, k, off + a0);
+                        tma_load_2d_pair(r_s, &tmA, full, k,
+                                         off + (kFew ? t.mb * BF + (int)rank * (BF / 2) : a0));
                         if (kMnB && b_groups) {
-                            tma_load_4d_pair(b_s, &tmB, full, 0, k, b0 / 64, t.e);
+                            tma_load_4d_pair(w_s, &tmB, full, 0, k, b0 / 64, t.e);
                         } else if (kMnB) {
-                            tma_load_3d_pair(b_s, &tmB, full, b0, k, t.e);
-                            tma_load_3d_pair(b_s + BOX_BYTES, &tmB, full, b0 + 64, k, t.e);
+                            tma_load_3d_pair(w_s, &tmB, full, b0, k, t.e);
+                            tma_load_3d_pair(w_s + BOX_BYTES, &tmB, full, b0 + 64, k, t.e);
                         } else {
-                            tma_load_3d_pair(b_s, &tmB, full, k, b0, t.e);
+                            tma_load_3d_pair(w_s, &tmB, full, k, b0, t.e);
                         }
                     }
                     if (++stage == kStages) {
@@ -574,10 +641,12 @@ __device__ __forceinline__ void grouped_product(
             if (*abort_flag) spin(4000000);
         } else if (warp == 1 && leader && lane == 0) {
             // ---------------- MMA issuer (leader only) ----------------
-            constexpr uint32_t idesc =
-                make_idesc(BT, BT) | (kMnA ? kIdescMnA : 0u) | (kMnB ? kIdescMnB : 0u);
+            constexpr bool kMajA = kFew ? kMnB : kMnA, kMajB = kFew ? kMnA : kMnB;
+            constexpr uint32_t idesc = make_idesc(BT, kTileRows) | (kMajA ? kIdescMnA : 0u) |
+                                       (kMajB ? kIdescMnB : 0u);
             // a K step of 16 inside a stage: 32 bytes of a K-major row, or 16 rows
-            constexpr uint64_t kStepA = kMnA ? 16 * 128 / 16 : 2, kStepB = kMnB ? 16 * 128 / 16 : 2;
+            constexpr uint64_t kStepA = kMajA ? 16 * 128 / 16 : 2;
+            constexpr uint64_t kStepB = kMajB ? 16 * 128 / 16 : 2;
             int stage = 0;
             uint32_t phase = 0;
             int acc = 0;
@@ -611,8 +680,8 @@ __device__ __forceinline__ void grouped_product(
                     const uint32_t d = tmem + (uint32_t)(acc * BT);
                     const uint32_t a_s = tiles_addr + stage * STAGE_BYTES;
                     const uint32_t b_s = a_s + OP_BYTES;
-                    const uint64_t ad = kMnA ? sw128_desc_mn(a_s, BOX_BYTES) : sw128_desc(a_s);
-                    const uint64_t bd = kMnB ? sw128_desc_mn(b_s, BOX_BYTES) : sw128_desc(b_s);
+                    const uint64_t ad = kMajA ? sw128_desc_mn(a_s, BOX_BYTES) : sw128_desc(a_s);
+                    const uint64_t bd = kMajB ? sw128_desc_mn(b_s, BOX_BYTES) : sw128_desc(b_s);
                     const int steps = kW && kb == t.kblocks - 1 ? last_steps : BK / UMMA_K;
 #pragma unroll
                     for (int kk = 0; kk < BK / UMMA_K; ++kk) {
@@ -688,7 +757,7 @@ __device__ __forceinline__ void grouped_product(
                             if (lane < per && mine < E)
                                 segment(expert_offsets, expert_counts, mine, R, err, &o, &c);
                         }
-                        const int b = (c + BT - 1) / BT, end = before + warp_prefix(b);
+                        const int b = (c + kTileRows - 1) / kTileRows, end = before + warp_prefix(b);
                         const int k = __ffs(__ballot_sync(0xffffffffu, end > q)) - 1;
                         const int MBe = __shfl_sync(0xffffffffu, b, k);
                         const int local = tile - NB * (__shfl_sync(0xffffffffu, end, k) - MBe);
@@ -759,7 +828,8 @@ __device__ __forceinline__ void grouped_product(
         // ---------------- epilogue (both CTAs): own 128 rows ----------------
         regs_grow<kRegsEpilogue>();
         const int q = warp & 3;               // TMEM lane quadrant
-        const int half = (warp - 4) >> 2;     // 128 columns of the tile
+        const int half = (warp - 4) >> 2;     // 128 columns of the tile, or 32 of its few rows
+        constexpr int kCols = kFew ? BF / 2 : kEpilogueCols;  // of the accumulator
         uint8_t* staging = staging_area + (size_t)(warp - 4) * kStagingBytes;
         const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[0]), first);
         int acc = 0;
@@ -781,7 +851,7 @@ __device__ __forceinline__ void grouped_product(
             };
             const auto part = [&]() {
                 return tmem + ((uint32_t)(q * 32) << 16) +
-                       (uint32_t)(acc * BT + half * kEpilogueCols);
+                       (uint32_t)(acc * BT + half * kCols);
             };
             // the accumulator has been read
             const auto release = [&]() {
@@ -796,11 +866,11 @@ __device__ __forceinline__ void grouped_product(
             const int chains = kChained ? (t.kblocks + kChainBlocks - 1) / kChainBlocks
                                         : (t.kblocks > 0 ? 1 : 0);
             // fp32 outputs: the partial sums before the last
-            uint32_t sum[kChained ? kEpilogueCols / 32 : 1][32];
+            uint32_t sum[kChained ? kCols / 32 : 1][32];
             bool ok = true;
             if (kChained && chains > 1) {
 #pragma unroll
-                for (int c = 0; c < kEpilogueCols; ++c) sum[c / 32][c % 32] = 0u;
+                for (int c = 0; c < kCols; ++c) sum[c / 32][c % 32] = 0u;
                 for (int n = 0; ok && n < chains - 1; ++n) {
                     if (!ready()) {
                         ok = false;
@@ -808,7 +878,7 @@ __device__ __forceinline__ void grouped_product(
                     }
                     const uint32_t at = part();
 #pragma unroll
-                    for (int c = 0; c < kEpilogueCols / 32; ++c) {
+                    for (int c = 0; c < kCols / 32; ++c) {
                         uint32_t v[32];
                         tmem_ld32(at + c * 32, v);
                         tmem_wait_ld();
@@ -821,6 +891,33 @@ __device__ __forceinline__ void grouped_product(
                 }
             }
             if (!ok || (chains > 0 && !ready())) break;
+            if constexpr (kFew) {
+                uint32_t v[32];
+                tmem_ld32(part(), v);
+                tmem_wait_ld();
+                release();
+                if (kChained && chains > 1) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = __float_as_uint(__uint_as_float(sum[0][j]) + __uint_as_float(v[j]));
+                }
+                const FewPart f = few_part(t, rank);
+                const int c = f.col + (lane & 7) * 4;
+                if (f.rows <= 0 || f.col >= n_out) continue;
+                if (kSplit) {
+                    put_few(tiles + (warp - 4) * kStagingBytes, lane, v);
+                    continue;
+                }
+                put_few(staging, lane, v);
+                __syncwarp();
+                for (int r = lane >> 3; r < 32 && r < f.rows; r += 4)
+                    if (c < n_out)
+                        store_few(out + (f.row + r) * n_out + c,
+                                  *reinterpret_cast<const float4*>(staging + r * 128 +
+                                                                   (lane & 7) * 16));
+                __syncwarp();
+                continue;
+            }
 
             // the last one (or zeros), stored line by line: the reads of a line from
             // TMEM go on beside the stores of the one before
@@ -898,7 +995,11 @@ __device__ __forceinline__ void grouped_product(
     __syncthreads();
     cluster_sync();  // no CTA leaves while its peer may still signal it
     if constexpr (kSplit) {
-        if (joined.e >= 0 && splits == 2)
+        if (kFew && joined.e >= 0 && splits == 2)
+            join_few<2>(tiles_addr, rank, split, joined, n_out, out);
+        else if (kFew && joined.e >= 0)
+            join_few<kMaxSplits>(tiles_addr, rank, split, joined, n_out, out);
+        else if (joined.e >= 0 && splits == 2)
             join_parts<kW, 2>(tiles_addr, rank, split, joined, m_out, n_out, out, accumulate);
         else if (joined.e >= 0)
             join_parts<kW, kMaxSplits>(tiles_addr, rank, split, joined, m_out, n_out, out,
@@ -921,7 +1022,7 @@ __device__ __forceinline__ void grouped_product(
     }
 }
 
-template <int kMode, typename OutT>
+template <int kMode, typename OutT, bool kFew>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_product_kernel(const __grid_constant__ CUtensorMap tmA,
                            const __grid_constant__ CUtensorMap tmB,
@@ -930,12 +1031,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            const int32_t* __restrict__ expert_counts, int E, int R, int K,
                            int m_out, int n_out, OutT* __restrict__ out, int accumulate,
                            int a_groups, int b_groups, int* err, int* tile_counter) {
-    grouped_product<kMode, OutT, false>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R, K,
+    grouped_product<kMode, OutT, kFew, false>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R, K,
                                         m_out, n_out, out, accumulate, a_groups, b_groups, err,
                                         tile_counter);
 }
 // Launched with clusters of 2 * splits CTAs.
-template <int kMode, typename OutT>
+template <int kMode, typename OutT, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_product_split_kernel(const __grid_constant__ CUtensorMap tmA,
                                  const __grid_constant__ CUtensorMap tmB,
@@ -944,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  const int32_t* __restrict__ expert_counts, int E, int R, int K,
                                  int m_out, int n_out, OutT* __restrict__ out, int accumulate,
                                  int a_groups, int b_groups, int* err, int* tile_counter) {
-    grouped_product<kMode, OutT, true>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R, K,
+    grouped_product<kMode, OutT, kFew, true>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R, K,
                                        m_out, n_out, out, accumulate, a_groups, b_groups, err,
                                        tile_counter);
 }
@@ -966,22 +1067,22 @@ int clusters_at_once(Kernel kernel, int splits, size_t smem) {
     return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
 }
 
-template <int kMode, typename OutT>
+template <int kMode, typename OutT, bool kFew = false>
 moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
                   const GemmGroup& g, long long tiles, long long blocks,
                   int K, int m_out, int n_out, void* out, bool accumulate, int a_groups,
                   int b_groups, cudaStream_t st) {
     if (tiles >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
     // the attributes hold for the process and device: set once for each
-    constexpr size_t smem = smem_bytes<kMode>();
-    const auto split_kernel = grouped_product_split_kernel<kMode, OutT>;
+    constexpr size_t smem = smem_bytes<kMode, kFew>();
+    const auto split_kernel = grouped_product_split_kernel<kMode, OutT, kFew>;
     static bool set[64] = {false};
     static int at_once[64][2];  // clusters of 2 pairs and of 4
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
     if (dev >= 64) return MOE_ERR_UNSUPPORTED;
     if (!set[dev]) {
-        if (cudaFuncSetAttribute(grouped_product_kernel<kMode, OutT>,
+        if (cudaFuncSetAttribute(grouped_product_kernel<kMode, OutT, kFew>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem) != cudaSuccess ||
             cudaFuncSetAttribute(split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -996,7 +1097,7 @@ moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap&
     // joining of the sums takes: 1 us for a few rows, 6 us for a tile's 256 (1 row, 4096 x
     // 3528: 25 us with one pair a tile, 16 us with four; K = 512: 8.1 and 7.8 us with two;
     // 256 x 256 sums of 1024 rows: 13.7 and 14.9 us with four, 4096 rows: 29 and 19 us).
-    const long long m = kMode == kWeightsGrad ? m_out : g.R;
+    const long long m = kMode == kWeightsGrad ? m_out : kFew ? 0 : g.R;
     const long long join_blocks = 4 + 16 * (m < BT ? m : BT) / BT;
     int splits = 1;
     if (tiles <= at_once[dev][1] && blocks * 3 > join_blocks * 4)
@@ -1025,7 +1126,7 @@ moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap&
     }
     const long long pairs_max = sm_count() / 2;
     const long long pairs = tiles < pairs_max ? tiles : pairs_max;
-    grouped_product_kernel<kMode, OutT>
+    grouped_product_kernel<kMode, OutT, kFew>
         <<<(int)(2 * (pairs > 0 ? pairs : 1)), kThreads, smem, st>>>(
             a, b, o, g.offsets, g.counts, g.E, (int)g.R, K, m_out, n_out,
             reinterpret_cast<OutT*>(out), accumulate ? 1 : 0, a_groups, b_groups, g.err, g.prefix + g.E + 1);
@@ -1069,22 +1170,28 @@ moe_status launch_rows(const uint16_t* rows, const GemmGroup& g, int c_in, int c
     const int K = input_grad ? c_out : c_in, n_out = input_grad ? c_in : c_out;
     CUtensorMap a, b, o;
     int groups = 0;
-    const bool ok = map_rows(&a, rows, 0, g.R, K, BH) &&
+    const long long used = g.R < g.E ? g.R : g.E;  // experts with rows, at most
+    const bool few = g.R <= kFewRows * used;
+    const bool ok = map_rows(&a, rows, 0, g.R, K, few ? BF / 2 : BH) &&
                     (input_grad ? map_mn(&b, w, g.E, c_out, c_in, &groups)
                                 : map_rows(&b, w, g.E, c_out, c_in, BH)) &&
-                    map_lines(&o, out, 0, g.R, n_out, out_f32);
+                    (few || map_lines(&o, out, 0, g.R, n_out, out_f32));
     if (!ok) return MOE_ERR_UNSUPPORTED;
+    if (few) o = a;  // not used
     // at most as many row blocks as experts with rows and whole blocks besides
-    const long long used = g.R < g.E ? g.R : g.E;
-    const long long tiles = (used + (g.R - used) / BT) * ((n_out + BT - 1LL) / BT);
+    const long long tiles = (used + (g.R - used) / (few ? BF : BT)) * ((n_out + BT - 1LL) / BT);
     const long long blocks = (K + BK - 1LL) / BK;
     using bf16 = __nv_bfloat16;
-    if (input_grad)
-        return out_f32
-                   ? launch<kRowsGrad, float>(a, b, o, g, tiles, blocks, K, 0, n_out, out, false, 0, groups, st)
-                   : launch<kRowsGrad, bf16>(a, b, o, g, tiles, blocks, K, 0, n_out, out, false, 0, groups, st);
-    return out_f32 ? launch<kForward, float>(a, b, o, g, tiles, blocks, K, 0, n_out, out, false, 0, 0, st)
-                   : launch<kForward, bf16>(a, b, o, g, tiles, blocks, K, 0, n_out, out, false, 0, 0, st);
+    const auto with = [&](auto launch) {
+        return launch(a, b, o, g, tiles, blocks, K, 0, n_out, out, false, 0, groups, st);
+    };
+    if (few)
+        return input_grad ? (out_f32 ? with(launch<kRowsGrad, float, true>)
+                                     : with(launch<kRowsGrad, bf16, true>))
+                          : (out_f32 ? with(launch<kForward, float, true>)
+                                     : with(launch<kForward, bf16, true>));
+    return input_grad ? (out_f32 ? with(launch<kRowsGrad, float>) : with(launch<kRowsGrad, bf16>))
+                      : (out_f32 ? with(launch<kForward, float>) : with(launch<kForward, bf16>));
 }
 
 moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const GemmGroup& g, int c_in,
