@@ -229,6 +229,21 @@ __device__ __forceinline__ bool publish(Queues* c, int i, const Tile& t, uint32_
     st_async4(at + 16, bar, t.mb, t.nb, t.k0, t.all);
     return true;
 }
+// The columns that the MMAs of the last column block take: where there are 128 at most,
+// as few as there are, in steps of what the two CTAs' halves of them can start at (16384 x
+// 1408 columns: 410 us with 256 in each, 399 us; 256 experts' 68 rows x 104: 199 and 154
+// us).  With more, boxes that overlap cost what the MMAs gain.  The rows of a tile are
+// the MMA's M, which is 256.
+__host__ __device__ __forceinline__ int last_columns(int n_out, bool groups) {
+    const int rest = n_out - (n_out - 1) / BT * BT, step = groups ? 2 * BK : 32;
+    return rest > BH ? BT : (rest + step - 1) / step * step;
+}
+// Of a CTA's half of the columns, those that its boxes of a K-major operand or of groups of
+// 64 columns bring in: all of them but where there is one column block.
+__host__ __device__ __forceinline__ int box_columns(int n_out, bool groups) {
+    return n_out > BT ? BH : last_columns(n_out, groups) / 2;
+}
+
 // The next tile of a whole warp.
 __device__ __forceinline__ bool warp_take(Queues* c, int i, bool leader, volatile int* abort,
                                           int* err, Tile& t) {
@@ -482,6 +497,7 @@ __device__ __forceinline__ void grouped_product(
     const int MB = (m_out + BT - 1) / BT;
     const int NB = (n_out + BT - 1) / BT;
     const int KB = (K + BK - 1) / BK;
+    const int n_last = kFew ? BT : last_columns(n_out, kMnB && b_groups);
 
     // A weights' gradient hands out the experts with the most rows first: their tiles
     // take the longest, and the short ones fill the pairs up at the end (Zipf-skewed
@@ -573,7 +589,14 @@ __device__ __forceinline__ void grouped_product(
                 const bool ragged = kW && (t.cnt % UMMA_K) != 0;
                 // this CTA's half of A's rows and of B's
                 const int a0 = t.mb * BT + (int)rank * BH;
-                const int b0 = t.nb * BT + (int)rank * BH;
+                const int half = (t.nb == NB - 1 ? n_last : BT) / 2;
+                const int b0 = t.nb * BT + (int)rank * half;
+                // boxes of 64 columns where those come one by one
+                const bool two = half > 64;
+                const uint32_t stage_tx =
+                    kFew ? STAGE_BYTES
+                         : OP_BYTES + (kMnB && !b_groups ? (two ? 2 : 1) * BOX_BYTES
+                                                         : box_columns(n_out, kMnB) * BK * 2);
                 for (int kb = 0; kb < t.kblocks; ++kb) {
                     if (!wait_bar(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, err)) {
                         ok = false;
@@ -586,7 +609,7 @@ __device__ __forceinline__ void grouped_product(
                         const int row = off + kb * BK;
                         if (ragged && kb == t.kblocks - 1) {
                             const uint32_t land = smem_u32(&ctl->land[stage]);
-                            mbar_expect_tx(land, STAGE_BYTES);
+                            mbar_expect_tx(land, stage_tx);
                             if (a_groups) {
                                 tma_load_3d(a_s, &tmA, land, 0, row, a0 / 64);
                             } else {
@@ -597,13 +620,13 @@ __device__ __forceinline__ void grouped_product(
                                 tma_load_3d(b_s, &tmB, land, 0, row, b0 / 64);
                             } else {
                                 tma_load_2d(b_s, &tmB, land, b0, row);
-                                tma_load_2d(b_s + BOX_BYTES, &tmB, land, b0 + 64, row);
+                                if (two) tma_load_2d(b_s + BOX_BYTES, &tmB, land, b0 + 64, row);
                             }
                         } else {
                             const uint32_t full = full0 + (uint32_t)stage * 8u;
                             if (leader) {
                                 mbar_arrive(full_local);
-                                mbar_expect_tx(full_local, 2 * STAGE_BYTES);
+                                mbar_expect_tx(full_local, 2 * stage_tx);
                             }
                             if (a_groups) {
                                 tma_load_3d_pair(a_s, &tmA, full, 0, row, a0 / 64);
@@ -615,7 +638,8 @@ __device__ __forceinline__ void grouped_product(
                                 tma_load_3d_pair(b_s, &tmB, full, 0, row, b0 / 64);
                             } else {
                                 tma_load_2d_pair(b_s, &tmB, full, b0, row);
-                                tma_load_2d_pair(b_s + BOX_BYTES, &tmB, full, b0 + 64, row);
+                                if (two)
+                                    tma_load_2d_pair(b_s + BOX_BYTES, &tmB, full, b0 + 64, row);
                             }
                         }
                     } else {
@@ -623,14 +647,15 @@ __device__ __forceinline__ void grouped_product(
                         const int k = (kSplit ? t.k0 + kb : kb) * BK;
                         // the matrix is B, or A of a tile of few rows
                         const uint32_t w_s = kFew ? a_s : b_s, r_s = kFew ? b_s : a_s;
-                        if (leader) mbar_expect_tx(full_local, 2 * STAGE_BYTES);
+                        if (leader) mbar_expect_tx(full_local, 2 * stage_tx);
                         tma_load_2d_pair(r_s, &tmA, full, k,
                                          off + (kFew ? t.mb * BF + (int)rank * (BF / 2) : a0));
                         if (kMnB && b_groups) {
                             tma_load_4d_pair(w_s, &tmB, full, 0, k, b0 / 64, t.e);
                         } else if (kMnB) {
                             tma_load_3d_pair(w_s, &tmB, full, b0, k, t.e);
-                            tma_load_3d_pair(w_s + BOX_BYTES, &tmB, full, b0 + 64, k, t.e);
+                            if (kFew || two)
+                                tma_load_3d_pair(w_s + BOX_BYTES, &tmB, full, b0 + 64, k, t.e);
                         } else {
                             tma_load_3d_pair(w_s, &tmB, full, k, b0, t.e);
                         }
@@ -646,8 +671,7 @@ __device__ __forceinline__ void grouped_product(
         } else if (warp == 1 && leader && elect_one()) {
             // ---------------- MMA issuer (leader only) ----------------
             constexpr bool kMajA = kFew ? kMnB : kMnA, kMajB = kFew ? kMnA : kMnB;
-            constexpr uint32_t idesc = make_idesc(BT, kTileRows) | (kMajA ? kIdescMnA : 0u) |
-                                       (kMajB ? kIdescMnB : 0u);
+            constexpr uint32_t kMajors = (kMajA ? kIdescMnA : 0u) | (kMajB ? kIdescMnB : 0u);
             // a K step of 16 inside a stage: 32 bytes of a K-major row, or 16 rows
             constexpr uint64_t kStepA = kMajA ? 16 * 128 / 16 : 2;
             constexpr uint64_t kStepB = kMajB ? 16 * 128 / 16 : 2;
@@ -663,6 +687,9 @@ __device__ __forceinline__ void grouped_product(
                 const int last_steps =
                     kW ? (t.cnt - (t.kblocks - 1) * BK + UMMA_K - 1) / UMMA_K
                        : BK / UMMA_K;
+                const uint32_t idesc =
+                    kMajors |
+                    (kFew ? make_idesc(BT, BF) : make_idesc(BT, t.nb == NB - 1 ? n_last : BT));
                 int in_chain = 0;
                 for (int kb = 0; kb < t.kblocks; ++kb) {
                     if (in_chain == 0) {
@@ -1146,15 +1173,15 @@ bool map_rows(CUtensorMap* m, const void* ptr, long long outer, long long rows, 
     return map_tiled(m, outer > 0 ? 3 : 2, ptr, sizes, strides, box);
 }
 
-// The same as an MN-major operand: boxes of 64 rows, two groups of 64 columns at a
-// time where cols is a multiple of 64 (*groups), else one.
+// The same as an MN-major operand: boxes of 64 rows, box_cols columns (64 or 128) at a
+// time where cols is a multiple of 64 (*groups), else 64.
 bool map_mn(CUtensorMap* m, const void* ptr, long long outer, long long rows, long long cols,
-            int* groups) {
+            int box_cols, int* groups) {
     *groups = cols % 64 == 0;
     if (!*groups) return map_rows(m, ptr, outer, rows, cols, BK);
     const uint64_t sizes[4] = {64, (uint64_t)rows, (uint64_t)cols / 64, (uint64_t)outer};
     const uint64_t strides[3] = {(uint64_t)cols * 2, 128, (uint64_t)(cols * rows) * 2};
-    const uint32_t box[4] = {64, BK, 2, 1};
+    const uint32_t box[4] = {64, BK, (uint32_t)box_cols / 64, 1};
     return map_tiled(m, outer > 0 ? 4 : 3, ptr, sizes, strides, box);
 }
 
@@ -1177,8 +1204,10 @@ moe_status launch_rows(const uint16_t* rows, const GemmGroup& g, int c_in, int c
     const long long used = g.R < g.E ? g.R : g.E;  // experts with rows, at most
     const bool few = g.R <= kFewRows * used;
     const bool ok = map_rows(&a, rows, 0, g.R, K, few ? BF / 2 : BH) &&
-                    (input_grad ? map_mn(&b, w, g.E, c_out, c_in, &groups)
-                                : map_rows(&b, w, g.E, c_out, c_in, BH)) &&
+                    (input_grad ? map_mn(&b, w, g.E, c_out, c_in, few ? BH : box_columns(n_out, true),
+                                         &groups)
+                                : map_rows(&b, w, g.E, c_out, c_in,
+                                           few ? BH : box_columns(n_out, false))) &&
                     (few || map_lines(&o, out, 0, g.R, n_out, out_f32));
     if (!ok) return MOE_ERR_UNSUPPORTED;
     if (few) o = a;  // not used
@@ -1202,8 +1231,8 @@ moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const Gemm
                           int c_out, void* dw, bool out_f32, bool accumulate, cudaStream_t st) {
     CUtensorMap a, b, o;
     int a_groups = 0, b_groups = 0;
-    if (!map_mn(&a, dout, 0, g.R, c_out, &a_groups) ||
-        !map_mn(&b, rows, 0, g.R, c_in, &b_groups) ||
+    if (!map_mn(&a, dout, 0, g.R, c_out, BH, &a_groups) ||
+        !map_mn(&b, rows, 0, g.R, c_in, box_columns(c_in, true), &b_groups) ||
         !map_lines(&o, dw, g.E, c_out, c_in, out_f32))
         return MOE_ERR_UNSUPPORTED;
     const long long tiles =

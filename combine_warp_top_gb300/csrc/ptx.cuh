@@ -280,7 +280,7 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t box_b
 // Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator (bits 4-5),
 // bf16 A (bits 7-9) and B (bits 10-12), both K-major, N >> 3 at bits 17-22,
 // M >> 4 at bits 24-28.
-constexpr uint32_t make_idesc(int M, int N) {
+__host__ __device__ constexpr uint32_t make_idesc(int M, int N) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
 }

@@ -120,3 +120,23 @@ def test_more_row_blocks_than_rows_allow_are_reported():
     moe.moe_grouped_gemm(rows, lay, shape, w, torch.zeros(2, 72, device="cuda"), ws)
     torch.cuda.synchronize()
     assert moe.moe_get_error(ws) == 1    # 4 blocks of 2 rows
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("width", [8, 40, 64, 104, 128, 136, 192, 264, 320, 360, 384, 392])
+def test_widths_of_the_last_column_block(width, dtype):
+    """Column blocks of 256 and what is left: from 8 columns to a whole block."""
+    counts = [300, 5, 270]
+    shape, lay, seg, rows, dout, w, ws = problem(counts, 200, width)
+    out = torch.full((shape.N, width), float("nan"), dtype=dtype, device="cuda")
+    moe.moe_grouped_gemm(rows, lay, shape, w, out, ws)
+    shape2, lay2, _, rows2, dout2, w2, ws2 = problem(counts, width, 200, seed=1)
+    drows = torch.full((shape.N, width), float("nan"), dtype=dtype, device="cuda")
+    dw = torch.full((3, 200, width), float("nan"), dtype=dtype, device="cuda")
+    moe.moe_grouped_gemm_input_grad(dout2, lay2, shape2, w2, drows, ws2)
+    moe.moe_grouped_gemm_weight_grad(dout2, rows2, lay2, shape2, dw, ws2)
+    assert moe.moe_get_error(ws) == 0 and moe.moe_get_error(ws2) == 0
+    for e, s in enumerate(seg):
+        check(out[s], rows[s].double(), w[e].double().T)
+        check(drows[s], dout2[s].double(), w2[e].double())
+        check(dw[e], dout2[s].double().T, rows2[s].double())
