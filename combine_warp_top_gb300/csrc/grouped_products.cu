@@ -33,16 +33,18 @@
 // nearest, in a fixed order: 4e-7 whatever the length, for 6 to 11% of the time
 // of a long contraction.
 //
-// Roles per CTA (384 threads): warp 0 loads by TMA into 6 stages; warp 1 owns TMEM
+// Roles per CTA (384 threads): warp 0 loads by TMA into 6 stages (9 in tiles of few rows); warp 1 owns TMEM
 // (two accumulators, one filled while the other is drained) and, in the leader,
 // issues the MMAs; warp 2 of the leader hands out tiles; warp 3 zeroes block ends
 // (weights' gradient); warps 4-11 drain the accumulators, two warps to each 32 rows
 // (128 columns each), with the registers that the others give up.  Every wait is
-// bounded.
+// bounded.  6 stages of 32 KB and 32 KB of outgoing lines fill the shared memory; 5 and
+// 4 stages measured slower.
 //
 // What bounds it, and what that led to (GB300, clock cycles of an SM):
-// - A k-block of a tile is 690 cycles of MMA (the rate that cuBLAS reaches, too),
-//   and long contractions run at that: 16384 x 14336 x 4096, 1030 us, 1870 TFLOP/s.
+// - Long contractions run at the tensor cores' rate: 16384 x 14336 x 4096, 1000 us,
+//   1920 TFLOP/s.  That takes an issuing lane that is done with a k-block (4 MMAs, a
+//   commit, a wait) before the MMAs are: see the election below.
 // - With few rows an expert the weights' gradient is the writing of dW.  A tile's
 //   128 KB (fp32) have to leave an SM in some 5000 cycles, which takes whole 128-byte
 //   lines (64-byte boxes: 22 bytes a cycle, 128-byte ones 26), by TMA (lines stored
@@ -53,12 +55,13 @@
 //   with those fences and 64-byte lines, 288 us now; floor 253 us.
 // - A tile costs each role some 800 cycles to decode: the scheduler does it for all.
 // - A decoding step streams the weights: 16 tokens of 6 of 64 experts of 2816 x 2048,
-//   98 us for 586 MB, 6.0 TB/s.  Smaller boxes for the few rows of A measured the same.
+//   88 us for 586 MB, 6.7 TB/s, with the matrix as A and 64 rows as B (kFew); 97 us with
+//   256 rows as A, whose MMAs take longer than the weights.
 // - Few tiles leave SMs idle: with a long contraction 2 or 4 pairs of a cluster share
 //   a tile's k-blocks, keep their sums in shared memory and add them up from there
 //   (4096 rows of one expert, 256 x 256 fp32 weights' gradient: 29 us with one pair,
-//   19 us with four; 1 row, 14336 x 3528: 67 and 35 us).
-// - 64 tokens: 7.6 us, the latencies of launch, first tile, loads and stores in a row.
+//   19 us with four; 1 row, 14336 x 3528 in tiles of few rows: 24 us with four).
+// - 64 tokens: 6.9 us, the latencies of launch, first tile, loads and stores in a row.
 #include <limits.h>
 #include <stddef.h>
 
@@ -110,7 +113,9 @@ struct __align__(16) Tile {
     int k0, all;
 };
 constexpr int kQ = 8;  // slots of a tile queue
-// Rows an expert, on average, up to which products take tiles of few rows.
+// Rows an expert, on average, up to which products take tiles of few rows: 128 rows each
+// of 64 experts of 2816 x 2048 take 134 us in two of those and 136 us in one of 256 rows,
+// 256 rows 209 and 146 us.
 constexpr int kFewRows = 64;
 constexpr int kMaxSplits = 4;    // pairs of a cluster that share a tile's contraction
 
@@ -456,7 +461,9 @@ __device__ __forceinline__ void join_few(uint32_t ring, uint32_t rank, int split
 // kFew (products over rows): tiles of 256 columns of the output and BF rows, the matrix
 // being A and the rows B.  An MMA takes the same time for 1 row and for 128 of A, and 512
 // cycles a k-block for 256 of B, which is longer than the 32 KB of the matrix need to come
-// in; so it is a quarter of that, and the stages are 9.
+// in; so it is a quarter of that, and the stages are 9.  64 experts of 2816 x 2048: 111 us
+// for 1 row each and 121 us for 64 (256 rows as A: 118 and 128 us); 512 x 512, 16 rows
+// each: 13.5 us (14.6 us).
 // kSplit: a cluster of several pairs has one tile, each pair a share of its
 // contraction, and the pairs' sums are joined at the end.
 template <int kMode, typename OutT, bool kFew, bool kSplit>

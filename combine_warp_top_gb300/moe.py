@@ -220,6 +220,10 @@ class Shape:
         """The C struct by reference, made once for this shape."""
         return ctypes.byref(self.c())
 
+    def __getstate__(self):
+        """The fields alone: copies and pickles make their own references."""
+        return {f.name: getattr(self, f.name) for f in dataclasses.fields(self)}
+
     def c(self) -> MoeShape:
         if self.gemm not in GEMM_KERNELS:
             raise ValueError(f"gemm must be one of {sorted(GEMM_KERNELS)}")
@@ -693,6 +697,10 @@ class NormShape:
     def ref(self):
         """The C struct by reference, made once for this shape."""
         return ctypes.byref(self.c())
+
+    def __getstate__(self):
+        """The fields alone: copies and pickles make their own references."""
+        return {f.name: getattr(self, f.name) for f in dataclasses.fields(self)}
 
     def c(self) -> MoeNormShape:
         if self.gate not in GATES:

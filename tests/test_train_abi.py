@@ -1,6 +1,8 @@
 """Host-side refusals of the training operators: answered without a GPU, before
 any launch."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -120,3 +122,12 @@ def test_binding_checks_types_and_shapes(lib):
         moe.moe_swiglu(y, None, lay, shape, y)
     with pytest.raises(ValueError, match="topk_ids: expected torch.int32"):
         moe.moe_route_grad(torch.empty(4, 2, dtype=torch.int64), v, v, shape, v)
+
+
+def test_shapes_copy_and_pickle_after_use():
+    for shape in (moe.Shape(4, 64, 8, 2, 1, 64, gemm="pair"),
+                  moe.NormShape(4, 64, gate="token", stream="fp32")):
+        before = moe.load() and shape.ref  # a call keeps the C struct
+        assert before is shape.ref
+        for other in (copy.copy(shape), copy.deepcopy(shape), pickle.loads(pickle.dumps(shape))):
+            assert other == shape and other.ref is not before
