@@ -556,9 +556,12 @@ __device__ __forceinline__ void grouped_product(
                 blocks_in += (run_cnt + kTileRows - 1) / kTileRows;
             }
         }
+        // Only a layout whose segments overlap has more blocks than R rows can fill: it gets
+        // no more, nor sums that wrap, and is reported where tiles are launched one by one.
+        if (blocks_in > 1 << 25) blocks_in = 1 << 25;
         blocks_end = warp_prefix(blocks_in);
-        total = __shfl_sync(0xffffffffu, blocks_end, 31) * NB;
-        // only a layout whose segments overlap has more tiles than the host allowed for
+        const int blocks = __shfl_sync(0xffffffffu, blocks_end, 31), most = R / kTileRows + E;
+        total = (blocks < most ? blocks : most) * NB;
         if (kSplit && blockIdx.x == 0 && lane == 0 && total > (int)gridDim.x / (2 * splits))
             set_error(err, MOE_ERR_INVALID_ARG);
     }

@@ -578,34 +578,35 @@ def _out_type(t, what):
     return MOE_TYPES[t.dtype]
 
 
-def _expert_matrices(w, shape: Shape, what):
-    """(C_out, C_in) of per-expert matrices [E, C_out, C_in]."""
+def _expert_matrices(w, dtype, shape: Shape, what):
+    """(address, C_out, C_in) of per-expert matrices [E, C_out, C_in]."""
     if not isinstance(w, torch.Tensor):
         raise TypeError(f"{what}: expected a torch tensor")
-    if w.dim() != 3 or w.shape[0] != shape.E:
-        raise ValueError(f"{what}: expected [E = {shape.E}, C_out, C_in], got {tuple(w.shape)}")
-    return w.shape[1], w.shape[2]
+    size = w.shape
+    if len(size) != 3 or size[0] != shape.E:
+        raise ValueError(f"{what}: expected [E = {shape.E}, C_out, C_in], got {tuple(size)}")
+    return _exact(w, dtype, size, what), size[1], size[2]
 
 
 def moe_grouped_gemm(rows, layout: Layout, shape: Shape, w, out, ws, stream=None):
     """out[i] = rows[i] W[e]^T for the N*k expert-major rows; w [E, C_out, C_in]
     bf16, out [N*k, C_out] bf16 or fp32."""
-    co, ci = _expert_matrices(w, shape, "w")
+    w_at, co, ci = _expert_matrices(w, torch.bfloat16, shape, "w")
     ot, R = _out_type(out, "out"), shape.R
     _check(load().moe_grouped_gemm(
         _exact(rows, torch.bfloat16, (R, ci), "rows"), _lay(layout, shape),
-        shape.ref, ci, co, _exact(w, torch.bfloat16, w.shape, "w"),
+        shape.ref, ci, co, w_at,
         _exact(out, out.dtype, (R, co), "out"), ot, *_bytes(ws), _stream(stream)),
         "moe_grouped_gemm")
 
 
 def moe_grouped_gemm_input_grad(dout, layout: Layout, shape: Shape, w, drows, ws, stream=None):
     """drows[i] = dout[i] W[e]; drows [N*k, C_in] bf16 or fp32."""
-    co, ci = _expert_matrices(w, shape, "w")
+    w_at, co, ci = _expert_matrices(w, torch.bfloat16, shape, "w")
     ot, R = _out_type(drows, "drows"), shape.R
     _check(load().moe_grouped_gemm_input_grad(
         _exact(dout, torch.bfloat16, (R, co), "dout"), _lay(layout, shape),
-        shape.ref, ci, co, _exact(w, torch.bfloat16, w.shape, "w"),
+        shape.ref, ci, co, w_at,
         _exact(drows, drows.dtype, (R, ci), "drows"), ot, *_bytes(ws), _stream(stream)),
         "moe_grouped_gemm_input_grad")
 
@@ -614,12 +615,12 @@ def moe_grouped_gemm_weight_grad(dout, rows, layout: Layout, shape: Shape, dw, w
                                  accumulate=False, stream=None):
     """dw[e] (+)= sum of dout[i]^T rows[i] over the expert's rows; dw
     [E, C_out, C_in] bf16 or fp32 (fp32 to accumulate)."""
-    co, ci = _expert_matrices(dw, shape, "dw")
     ot, R = _out_type(dw, "dw"), shape.R
+    dw_at, co, ci = _expert_matrices(dw, dw.dtype, shape, "dw")
     _check(load().moe_grouped_gemm_weight_grad(
         _exact(dout, torch.bfloat16, (R, co), "dout"),
         _exact(rows, torch.bfloat16, (R, ci), "rows"), _lay(layout, shape),
-        shape.ref, ci, co, _exact(dw, dw.dtype, dw.shape, "dw"), ot,
+        shape.ref, ci, co, dw_at, ot,
         int(bool(accumulate)), *_bytes(ws), _stream(stream)), "moe_grouped_gemm_weight_grad")
 
 
