@@ -817,13 +817,14 @@ cudaError_t run_forward(const NormArgs& a, const Plan& p, cudaStream_t st) {
     if (p.lanes == 32)
         return p.kv == 1 ? run(block_norm_kernel<1, 32, kF32, kNow, true, kFull, kW>, a, p, st)
                          : run(block_norm_kernel<2, 32, kF32, kNow, true, kFull, kW>, a, p, st);
-    if (p.kv == 2)
-        return p.stages == 0
-                   ? run(block_norm_kernel<2, 0, kF32, kAhead, false, kFull, 1024>, a, p, st)
-                   : run(block_norm_kernel<2, 0, kF32, kRing2, false, kFull, 1024>, a, p, st);
-    return p.stages == 0
-               ? run(block_norm_kernel<1, 0, kF32, kAhead, true, kFull, 1024>, a, p, st)
-               : run(block_norm_kernel<1, 0, kF32, kRing3, true, kFull, 1024>, a, p, st);
+    // forward_plan's rings fit: 3 rows of up to 1024 vectors on an SM, 2 of more
+    constexpr Feed kWide = kF32 ? kRing2 : kAhead;
+    if (p.kv == 2) return run(block_norm_kernel<2, 0, kF32, kWide, false, kFull, 1024>, a, p, st);
+    if constexpr (kF32) {
+        if (p.stages == 0)
+            return run(block_norm_kernel<1, 0, kF32, kAhead, true, kFull, 1024>, a, p, st);
+    }
+    return run(block_norm_kernel<1, 0, kF32, kRing3, true, kFull, 1024>, a, p, st);
 }
 
 template <bool kF32, bool kFull>
@@ -833,9 +834,13 @@ cudaError_t run_grad(const NormGradArgs& a, const Plan& p, cudaStream_t st) {
     if (p.lanes == 32)
         return p.kv == 1 ? run(block_norm_grad_kernel<1, 32, kF32, 0, true, kFull>, a, p, st)
                          : run(block_norm_grad_kernel<2, 32, kF32, 0, true, kFull>, a, p, st);
-    if (p.kv == 1)
-        return p.stages == 3 ? run(block_norm_grad_kernel<1, 0, kF32, 3, true, kFull>, a, p, st)
-                             : run(block_norm_grad_kernel<1, 0, kF32, 2, true, kFull>, a, p, st);
+    if (p.kv == 1) {
+        if constexpr (kF32) {  // 3 rows of a bf16 stream always fit
+            if (p.stages < 3)
+                return run(block_norm_grad_kernel<1, 0, kF32, 2, true, kFull>, a, p, st);
+        }
+        return run(block_norm_grad_kernel<1, 0, kF32, 3, true, kFull>, a, p, st);
+    }
     return p.stages >= 2 ? run(block_norm_grad_kernel<2, 0, kF32, 2, false, kFull>, a, p, st)
                          : run(block_norm_grad_kernel<2, 0, kF32, 1, false, kFull>, a, p, st);
 }
