@@ -34,6 +34,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxNormH = 16384;
+constexpr int kMaxRing = 216 * 1024;  // bytes of the rings of an SM's blocks
 constexpr int kRowWarps = 4;   // rows (warps) of a block where a warp takes a row
 constexpr int kWarpRowV = 64;  // up to this many vectors of 8 a row: H <= 512
 
@@ -764,7 +765,7 @@ Plan plan_for(int N, int V, int words, int kv, int most_blocks) {
         int fit = 1024 / p.block < most_blocks ? 1024 / p.block : most_blocks;
         if (fit < 1) fit = 1;
         const size_t stage = (size_t)p.block * kv * words * 16;
-        const size_t room = (size_t)216 * 1024 / fit;
+        const size_t room = (size_t)kMaxRing / fit;
         p.stages = words == 0 ? 0 : stage * 3 <= room ? 3 : stage * 2 <= room ? 2 : 1;
         p.smem = stage * p.stages;
         const long long most = (long long)sm_count() * fit;
@@ -798,51 +799,59 @@ moe_status check_norm(const moe_norm_shape* s) {
     return MOE_OK;
 }
 
-template <typename Args>
-cudaError_t run(void (*kernel)(Args), const Args& a, const Plan& p, cudaStream_t st) {
+template <auto kKernel, typename Args>
+cudaError_t run(const Args& a, const Plan& p, cudaStream_t st) {
     if (p.smem > 40 * 1024) {  // with the static arrays, past the default 48 KB
-        const cudaError_t e = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+        // the attribute holds for the process and device: set once for each
+        static bool set[64] = {false};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
+        if (dev >= 64 || !set[dev]) {
+            e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kMaxRing);
+            if (e != cudaSuccess) return e;
+            if (dev < 64) set[dev] = true;
+        }
     }
-    kernel<<<p.grid, p.block, p.smem, st>>>(a);
+    kKernel<<<p.grid, p.block, p.smem, st>>>(a);
     return cudaGetLastError();
 }
 
 template <bool kF32, bool kFull>
 cudaError_t run_forward(const NormArgs& a, const Plan& p, cudaStream_t st) {
     constexpr int kW = 32 * kRowWarps;
-    if (p.lanes == 8) return run(block_norm_kernel<1, 8, kF32, kAhead, true, kFull, kW>, a, p, st);
-    if (p.lanes == 16) return run(block_norm_kernel<1, 16, kF32, kAhead, true, kFull, kW>, a, p, st);
+    if (p.lanes == 8) return run<block_norm_kernel<1, 8, kF32, kAhead, true, kFull, kW>>(a, p, st);
+    if (p.lanes == 16) return run<block_norm_kernel<1, 16, kF32, kAhead, true, kFull, kW>>(a, p, st);
     if (p.lanes == 32)
-        return p.kv == 1 ? run(block_norm_kernel<1, 32, kF32, kNow, true, kFull, kW>, a, p, st)
-                         : run(block_norm_kernel<2, 32, kF32, kNow, true, kFull, kW>, a, p, st);
+        return p.kv == 1 ? run<block_norm_kernel<1, 32, kF32, kNow, true, kFull, kW>>(a, p, st)
+                         : run<block_norm_kernel<2, 32, kF32, kNow, true, kFull, kW>>(a, p, st);
     // forward_plan's rings fit: 3 rows of up to 1024 vectors on an SM, 2 of more
     constexpr Feed kWide = kF32 ? kRing2 : kAhead;
-    if (p.kv == 2) return run(block_norm_kernel<2, 0, kF32, kWide, false, kFull, 1024>, a, p, st);
+    if (p.kv == 2) return run<block_norm_kernel<2, 0, kF32, kWide, false, kFull, 1024>>(a, p, st);
     if constexpr (kF32) {
         if (p.stages == 0)
-            return run(block_norm_kernel<1, 0, kF32, kAhead, true, kFull, 1024>, a, p, st);
+            return run<block_norm_kernel<1, 0, kF32, kAhead, true, kFull, 1024>>(a, p, st);
     }
-    return run(block_norm_kernel<1, 0, kF32, kRing3, true, kFull, 1024>, a, p, st);
+    return run<block_norm_kernel<1, 0, kF32, kRing3, true, kFull, 1024>>(a, p, st);
 }
 
 template <bool kF32, bool kFull>
 cudaError_t run_grad(const NormGradArgs& a, const Plan& p, cudaStream_t st) {
-    if (p.lanes == 8) return run(block_norm_grad_kernel<1, 8, kF32, 0, true, kFull>, a, p, st);
-    if (p.lanes == 16) return run(block_norm_grad_kernel<1, 16, kF32, 0, true, kFull>, a, p, st);
+    if (p.lanes == 8) return run<block_norm_grad_kernel<1, 8, kF32, 0, true, kFull>>(a, p, st);
+    if (p.lanes == 16) return run<block_norm_grad_kernel<1, 16, kF32, 0, true, kFull>>(a, p, st);
     if (p.lanes == 32)
-        return p.kv == 1 ? run(block_norm_grad_kernel<1, 32, kF32, 0, true, kFull>, a, p, st)
-                         : run(block_norm_grad_kernel<2, 32, kF32, 0, true, kFull>, a, p, st);
+        return p.kv == 1 ? run<block_norm_grad_kernel<1, 32, kF32, 0, true, kFull>>(a, p, st)
+                         : run<block_norm_grad_kernel<2, 32, kF32, 0, true, kFull>>(a, p, st);
     if (p.kv == 1) {
         if constexpr (kF32) {  // 3 rows of a bf16 stream always fit
             if (p.stages < 3)
-                return run(block_norm_grad_kernel<1, 0, kF32, 2, true, kFull>, a, p, st);
+                return run<block_norm_grad_kernel<1, 0, kF32, 2, true, kFull>>(a, p, st);
         }
-        return run(block_norm_grad_kernel<1, 0, kF32, 3, true, kFull>, a, p, st);
+        return run<block_norm_grad_kernel<1, 0, kF32, 3, true, kFull>>(a, p, st);
     }
-    return p.stages >= 2 ? run(block_norm_grad_kernel<2, 0, kF32, 2, false, kFull>, a, p, st)
-                         : run(block_norm_grad_kernel<2, 0, kF32, 1, false, kFull>, a, p, st);
+    return p.stages >= 2 ? run<block_norm_grad_kernel<2, 0, kF32, 2, false, kFull>>(a, p, st)
+                         : run<block_norm_grad_kernel<2, 0, kF32, 1, false, kFull>>(a, p, st);
 }
 
 }  // namespace
