@@ -62,7 +62,6 @@
 //   (4096 rows of one expert, 256 x 256 fp32 weights' gradient: 29 us with one pair,
 //   19 us with four; 1 row, 14336 x 3528 in tiles of few rows: 24 us with four).
 // - 64 tokens: 6.9 us, the latencies of launch, first tile, loads and stores in a row.
-#include <limits.h>
 #include <stddef.h>
 
 #include "../../include/moe_train.h"
@@ -112,7 +111,7 @@ struct __align__(16) Tile {
     // gradient's off and cnt are its own rows), and the expert's rows
     int k0, all;
 };
-constexpr int kQ = 8;  // slots of a tile queue
+constexpr int kQ = 6;  // slots of a tile queue
 // Rows an expert, on average, up to which products take tiles of few rows: 128 rows each
 // of 64 experts of 2816 x 2048 take 134 us in two of those and 136 us in one of 256 rows,
 // 256 rows 209 and 146 us.
@@ -120,7 +119,8 @@ constexpr int kFewRows = 64;
 constexpr int kMaxSplits = 4;    // pairs of a cluster that share a tile's contraction
 
 struct Queues {
-    Tile queue[kQ];             // each CTA: the tiles in order, from the leader's scheduler
+    Tile first;                 // each CTA: the pair's first tile, decoded by both CTAs
+    Tile queue[kQ];             // each CTA: the ones after it, from the leader's scheduler
     Tile local[kQ];             // peer: the tiles its producer forwards to its other warps
     uint64_t tfull[kAccs];      // each CTA: accumulator ready
     uint64_t tempty[kAccs];     // leader: accumulator drained by both CTAs
@@ -132,6 +132,7 @@ struct Queues {
     uint64_t l_empty[kQ];       // peer: slot of local read by its warps
     uint32_t tmem_base;
     int abort;
+    int only;                   // no pair has more than its first tile
 };
 constexpr int kQueueBarriers = 2 * kAccs + 1 + 5 * kQ;
 static_assert(offsetof(Queues, tmem_base) - offsetof(Queues, tfull) ==
@@ -181,6 +182,8 @@ __device__ __forceinline__ Tile read_slot(const Tile* p) {
     return t;
 }
 
+// The first tile of a pair does not go through the queue: where it is the only one, as
+// in most short calls, no role waits for another's decoding or for an end.
 // One thread takes tile i of the queue; false when there is none or the wait gave up.
 // first: the cluster's rank of the pair's leader, here and below.
 // In the leader every role reads the leader's queue.  In the peer only its producer
@@ -249,12 +252,17 @@ __host__ __device__ __forceinline__ int box_columns(int n_out, bool groups) {
     return n_out > BT ? BH : last_columns(n_out, groups) / 2;
 }
 
-// The next tile of a whole warp.
-__device__ __forceinline__ bool warp_take(Queues* c, int i, bool leader, volatile int* abort,
+// The n-th tile of a whole warp, or of one thread with the leader's queue.
+__device__ __forceinline__ bool warp_next(Queues* c, int n, bool leader, volatile int* abort,
                                           int* err, Tile& t) {
+    if (n == 0) {
+        t = read_slot(&c->first);
+        return t.e >= 0;
+    }
+    if (c->only) return false;
     int more = 0;
     if ((threadIdx.x & 31) == 0)
-        more = leader ? take(c, i, true, 0, abort, err, t) : take_local(c, i, abort, err, t);
+        more = leader ? take(c, n - 1, true, 0, abort, err, t) : take_local(c, n - 1, abort, err, t);
     if (!__shfl_sync(0xffffffffu, more, 0)) return false;
     t.e = __shfl_sync(0xffffffffu, t.e, 0);
     t.off = __shfl_sync(0xffffffffu, t.off, 0);
@@ -262,8 +270,15 @@ __device__ __forceinline__ bool warp_take(Queues* c, int i, bool leader, volatil
     t.kblocks = __shfl_sync(0xffffffffu, t.kblocks, 0);
     t.mb = __shfl_sync(0xffffffffu, t.mb, 0);
     t.nb = __shfl_sync(0xffffffffu, t.nb, 0);
-    t.all = __shfl_sync(0xffffffffu, t.all, 0);
     return true;
+}
+__device__ __forceinline__ bool next(Queues* c, int n, uint32_t first, volatile int* abort,
+                                     int* err, Tile& t) {
+    if (n == 0) {
+        t = read_slot(&c->first);
+        return t.e >= 0;
+    }
+    return !c->only && take(c, n - 1, true, first, abort, err, t);
 }
 
 // Inclusive prefix sum over a warp.
@@ -512,7 +527,7 @@ __device__ __forceinline__ void grouped_product(
     bool sorted = false;
     if constexpr (kW && !kSplit) {
         sorted = E <= kMaxSorted && E * MB * NB > (int)(gridDim.x / 2);
-        if (sorted && leader) {
+        if (sorted) {
             int* cnts = reinterpret_cast<int*>(tiles);  // the operand ring, not in use yet
             for (int i = threadIdx.x; i < E; i += blockDim.x) cnts[i] = expert_counts[i];
             __syncthreads();
@@ -524,6 +539,7 @@ __device__ __forceinline__ void grouped_product(
                 ctl->order[before] = (uint16_t)i;
             }
             fence_async_shared();  // before TMA writes there
+            __syncthreads();
         }
     }
     // one or two barriers a thread, not 63 and more of them one after the other
@@ -549,21 +565,93 @@ __device__ __forceinline__ void grouped_product(
     const int per = (E + 31) / 32;
     int blocks_end = 0, blocks_in = 0, total = E * MB * NB;
     int run_off = 0, run_cnt = 0;  // the run's last expert: the lane's own where per = 1
-    if (!kW && warp == 2 && leader) {
-        for (int j = 0; j < per; ++j) {
-            if (lane * per + j < E) {
-                segment(expert_offsets, expert_counts, lane * per + j, R, err, &run_off, &run_cnt);
-                blocks_in += (run_cnt + kTileRows - 1) / kTileRows;
+    int last_e = -1, last_off = 0, last_cnt = 0;  // the last tile's (weights' gradient)
+    // A tile by its number, decoded by a whole warp.
+    const auto decode = [&](int tile) {
+        Tile t = {};
+        t.e = -1;
+        if (tile >= total) return t;
+        if constexpr (kW) {
+            t.e = tile / (MB * NB);
+            const int local = tile - t.e * MB * NB;
+            t.mb = local / NB;
+            t.nb = local - t.mb * NB;
+            if constexpr (!kSplit) {
+                if (sorted) t.e = ctl->order[t.e];
+            }
+            if (t.e != last_e)
+                segment(expert_offsets, expert_counts, t.e, R, err, &last_off, &last_cnt);
+            last_e = t.e;
+            t.off = last_off;
+            t.cnt = last_cnt;
+            t.kblocks = (t.cnt + BK - 1) / BK;
+        } else {
+            // the run of experts that holds row block q, then the expert
+            const int q = tile / NB;
+            int run = 0, before = 0, o = run_off, c = run_cnt;
+            if (per > 1) {
+                run = __ffs(__ballot_sync(0xffffffffu, blocks_end > q)) - 1;
+                before = __shfl_sync(0xffffffffu, blocks_end - blocks_in, run);
+                const int mine = run * per + lane;
+                o = c = 0;
+                if (lane < per && mine < E)
+                    segment(expert_offsets, expert_counts, mine, R, err, &o, &c);
+            }
+            const int b = (c + kTileRows - 1) / kTileRows, end = before + warp_prefix(b);
+            const int k = __ffs(__ballot_sync(0xffffffffu, end > q)) - 1;
+            const int MBe = __shfl_sync(0xffffffffu, b, k);
+            const int local = tile - NB * (__shfl_sync(0xffffffffu, end, k) - MBe);
+            t.e = run * per + k;
+            t.off = __shfl_sync(0xffffffffu, o, k);
+            t.cnt = __shfl_sync(0xffffffffu, c, k);
+            t.kblocks = KB;
+            // the expert's smaller operand is the one read again: its row blocks side by
+            // side when they are fewer than its columns'
+            if (MBe > NB) {
+                t.mb = local / NB;
+                t.nb = local - t.mb * NB;
+            } else {
+                t.nb = local / MBe;
+                t.mb = local - t.nb * MBe;
             }
         }
-        // Only a layout whose segments overlap has more blocks than R rows can fill: it gets
-        // no more, nor sums that wrap, and is reported where tiles are launched one by one.
-        if (blocks_in > 1 << 25) blocks_in = 1 << 25;
-        blocks_end = warp_prefix(blocks_in);
-        const int blocks = __shfl_sync(0xffffffffu, blocks_end, 31), most = R / kTileRows + E;
-        total = (blocks < most ? blocks : most) * NB;
-        if (kSplit && blockIdx.x == 0 && lane == 0 && total > (int)gridDim.x / (2 * splits))
-            set_error(err, MOE_ERR_INVALID_ARG);
+        if (kSplit) {
+            const int all = t.kblocks;
+            t.k0 = (int)((long long)all * split / splits);
+            t.kblocks = (int)((long long)all * (split + 1) / splits) - t.k0;
+            t.all = t.cnt;
+            if (kW) {
+                const int end = (t.k0 + t.kblocks) * BK;
+                t.off += t.k0 * BK;
+                t.cnt = (t.cnt < end ? t.cnt : end) - t.k0 * BK;
+            }
+        }
+        return t;
+    };
+    if (warp == 2) {
+        if (!kW) {
+            for (int j = 0; j < per; ++j) {
+                if (lane * per + j < E) {
+                    segment(expert_offsets, expert_counts, lane * per + j, R, err, &run_off, &run_cnt);
+                    blocks_in += (run_cnt + kTileRows - 1) / kTileRows;
+                }
+            }
+            // Only a layout whose segments overlap has more blocks than R rows can fill: it
+            // gets no more, nor sums that wrap, and is reported where tiles are launched one
+            // by one.
+            if (blocks_in > 1 << 25) blocks_in = 1 << 25;
+            blocks_end = warp_prefix(blocks_in);
+            const int blocks = __shfl_sync(0xffffffffu, blocks_end, 31), most = R / kTileRows + E;
+            total = (blocks < most ? blocks : most) * NB;
+            if (kSplit && blockIdx.x == 0 && lane == 0 && total > (int)gridDim.x / (2 * splits))
+                set_error(err, MOE_ERR_INVALID_ARG);
+        }
+        // the pair's first tile is its own index (its cluster's, in split contractions)
+        const Tile t = decode((int)blockIdx.x / (2 * splits));
+        if (lane == 0) {
+            ctl->first = t;
+            ctl->only = kSplit || total <= (int)gridDim.x / 2;
+        }
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(&ctl->tmem_base), kTmemCols);
@@ -591,9 +679,16 @@ __device__ __forceinline__ void grouped_product(
             for (int i = 0; ok; ++i) {
                 Tile t = {};
                 t.e = -1;
-                bool more = take(ctl, i, leader, first, abort_flag, err, t);
-                if (leader && more) mbar_arrive(smem_u32(&ctl->q_taken[i % kQ]));
-                if (!leader && !forward(ctl, i, t, abort_flag, err)) more = false;
+                bool more;
+                if (i == 0) {
+                    t = read_slot(&ctl->first);
+                    more = t.e >= 0;
+                } else {
+                    if (ctl->only) break;
+                    more = take(ctl, i - 1, leader, first, abort_flag, err, t);
+                    if (leader && more) mbar_arrive(smem_u32(&ctl->q_taken[(i - 1) % kQ]));
+                    if (!leader && !forward(ctl, i - 1, t, abort_flag, err)) more = false;
+                }
                 if (!more) break;
                 const int off = t.off;
                 const bool ragged = kW && (t.cnt % UMMA_K) != 0;
@@ -692,7 +787,7 @@ __device__ __forceinline__ void grouped_product(
             bool ok = true;
             for (int i = 0; ok; ++i) {
                 Tile t = {};
-                if (!take(ctl, i, true, first, abort_flag, err, t)) break;
+                if (!next(ctl, i, first, abort_flag, err, t)) break;
                 // K steps of the last block (a segment's end)
                 const int last_steps =
                     kW ? (t.cnt - (t.kblocks - 1) * BK + UMMA_K - 1) / UMMA_K
@@ -748,13 +843,11 @@ __device__ __forceinline__ void grouped_product(
             }
             umma_commit_pair_multicast(smem_u32(&ctl->done), leader_mask);
             wait_bar_drain(smem_u32(&ctl->done), 0);
-        } else if (warp == 2 && leader) {
+        } else if (warp == 2 && leader && !ctl->only) {
             // ---------------- tile scheduler (leader) ----------------
-            // The pair's first tile is its own index; the counter hands out the ones
-            // after the pairs'.  Tile i is published once the producer has taken tile
-            // i - kAhead.  (A split contraction's tile is its cluster's index, the only one.)
+            // The counter hands out the tiles after the pairs' first ones.  Tile i of the
+            // queue is published once the producer has taken tile i - kAhead.
             const int pairs = (int)(gridDim.x / 2);
-            int e = -1, off = 0, cnt = 0;  // the last tile's expert (weights' gradient)
             for (int i = 0;; ++i) {
                 int tile = -1;
                 if (lane == 0) {
@@ -764,70 +857,11 @@ __device__ __forceinline__ void grouped_product(
                         ok = wait_bar(smem_u32(&ctl->q_taken[j % kQ]), (uint32_t)(j / kQ) & 1u,
                                       abort_flag, err);
                     }
-                    if (ok && kSplit)
-                        tile = i == 0 ? (int)blockIdx.x / (2 * splits) : INT_MAX;
-                    else if (ok)
-                        tile = i == 0 ? (int)(blockIdx.x / 2) : pairs + atomicAdd(tile_counter, 1);
+                    if (ok) tile = pairs + atomicAdd(tile_counter, 1);
                 }
                 tile = __shfl_sync(0xffffffffu, tile, 0);
                 if (tile < 0) break;
-                Tile t = {};
-                t.e = -1;
-                if (tile < total) {
-                    if constexpr (kW) {
-                        t.e = tile / (MB * NB);
-                        const int local = tile - t.e * MB * NB;
-                        t.mb = local / NB;
-                        t.nb = local - t.mb * NB;
-                        if (sorted) t.e = ctl->order[t.e];
-                        if (t.e != e)
-                            segment(expert_offsets, expert_counts, t.e, R, err, &off, &cnt);
-                        e = t.e;
-                        t.off = off;
-                        t.cnt = cnt;
-                        t.kblocks = (cnt + BK - 1) / BK;
-                    } else {
-                        // the run of experts that holds row block q, then the expert
-                        const int q = tile / NB;
-                        int run = 0, before = 0, o = run_off, c = run_cnt;
-                        if (per > 1) {
-                            run = __ffs(__ballot_sync(0xffffffffu, blocks_end > q)) - 1;
-                            before = __shfl_sync(0xffffffffu, blocks_end - blocks_in, run);
-                            const int mine = run * per + lane;
-                            o = c = 0;
-                            if (lane < per && mine < E)
-                                segment(expert_offsets, expert_counts, mine, R, err, &o, &c);
-                        }
-                        const int b = (c + kTileRows - 1) / kTileRows, end = before + warp_prefix(b);
-                        const int k = __ffs(__ballot_sync(0xffffffffu, end > q)) - 1;
-                        const int MBe = __shfl_sync(0xffffffffu, b, k);
-                        const int local = tile - NB * (__shfl_sync(0xffffffffu, end, k) - MBe);
-                        t.e = run * per + k;
-                        t.off = __shfl_sync(0xffffffffu, o, k);
-                        t.cnt = __shfl_sync(0xffffffffu, c, k);
-                        t.kblocks = KB;
-                        // the expert's smaller operand is the one read again: its row
-                        // blocks side by side when they are fewer than its columns'
-                        if (MBe > NB) {
-                            t.mb = local / NB;
-                            t.nb = local - t.mb * NB;
-                        } else {
-                            t.nb = local / MBe;
-                            t.mb = local - t.nb * MBe;
-                        }
-                    }
-                }
-                if (kSplit && t.e >= 0) {
-                    const int all = t.kblocks;
-                    t.k0 = (int)((long long)all * split / splits);
-                    t.kblocks = (int)((long long)all * (split + 1) / splits) - t.k0;
-                    t.all = t.cnt;
-                    if (kW) {
-                        const int end = (t.k0 + t.kblocks) * BK;
-                        t.off += t.k0 * BK;
-                        t.cnt = (t.cnt < end ? t.cnt : end) - t.k0 * BK;
-                    }
-                }
+                const Tile t = decode(tile);
                 int more = 0;
                 if (lane == 0) more = publish(ctl, i, t, first, abort_flag, err) && t.e >= 0;
                 if (!__shfl_sync(0xffffffffu, more, 0)) break;
@@ -839,7 +873,7 @@ __device__ __forceinline__ void grouped_product(
             uint32_t land_phase = 0;
             for (int i = 0;; ++i) {
                 Tile t = {};
-                if (!warp_take(ctl, i, leader, abort_flag, err, t)) break;
+                if (!warp_next(ctl, i, leader, abort_flag, err, t)) break;
                 const int cnt = t.cnt;
                 if (t.kblocks == 0) continue;
                 const int last = (stage + t.kblocks - 1) % kStages;
@@ -877,7 +911,7 @@ __device__ __forceinline__ void grouped_product(
         uint32_t acc_phase = 0;
         for (int i = 0;; ++i) {
             Tile t = {};
-            if (!warp_take(ctl, i, leader, abort_flag, err, t)) break;
+            if (!warp_next(ctl, i, leader, abort_flag, err, t)) break;
             if (!kSplit && kW && t.kblocks == 0 && accumulate) continue;  // nothing to add
             if (kSplit) joined = t;
 
@@ -1053,7 +1087,7 @@ __device__ __forceinline__ void grouped_product(
         tmem_dealloc_pair(tmem, kTmemCols);
     }
     // the tile counter returns to zero for the next launch (the last pair out)
-    if (!kSplit && leader && threadIdx.x == 0) {
+    if (!ctl->only && leader && threadIdx.x == 0) {
         __threadfence();
         const int before = atomicAdd(tile_counter + 1, 1);
         if (before == (int)(gridDim.x / 2) - 1) {
