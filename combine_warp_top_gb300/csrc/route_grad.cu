@@ -12,12 +12,15 @@
 // The selection itself is piecewise constant and passes no gradient, so outside
 // the full softmax the gradient is zero but for k entries a token.
 //
-// Memory bound: N * E fp32 written (and read, full softmax).  One warp a token:
-// lane j holds choice j; the row is put together in shared memory and leaves in
-// whole 16-byte vectors, so the scattered entries cost no extra global write.
-// The warp's row is all zeros between tokens: only the k entries are put back.
-// 32768 tokens of 256 experts, full softmax: 14 us for 69 MB (the bytes' time is 10 us,
-// launch and tail the rest); 4096 of 64: 2.6 us, a launch.
+// Memory bound: N * E fp32 written (and read, full softmax).  A warp, or 8 or 16 lanes of
+// one, take a token: lane j holds choice j; the row is put together in shared memory and
+// leaves in whole 16-byte vectors, so the scattered entries cost no extra global write.
+// The row is all zeros between tokens: only the k entries are put back.  With a warp for
+// every token the instructions for it (three sums over the lanes, the choices) take longer
+// than a short row's bytes.  32768 tokens, full softmax: of 256 experts 12.0 us (a warp each:
+// 13.4 us; the 69 MB take 10.2), of 128 7.4 us (8.1), of 64 4.2 us (7.9); softmax over the
+// selected, of 64 3.5 us (5.5).  4096 of 64: 2.0 us, a launch.  The next token's loads a
+// token ahead measured slower (15.9 us of 256).
 #include <math.h>
 
 #include "../../include/moe_train.h"
@@ -31,53 +34,58 @@ constexpr int kWarps = 4;
 
 enum Router { kSoftmax, kFullSoftmax, kSigmoid };
 
-__device__ __forceinline__ float warp_sum(float v) {
+template <int kLanes>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = kLanes / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int kLanes>
+__device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = kLanes / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
-// kPer: row elements a lane holds, in groups of kVec consecutive ones (4 when E
-// is a multiple of 4).  in: the weights (kSoftmax) or the logits.
-template <int kRouter, int kPer, int kVec>
+// kLanes lanes of a warp take a token, each kPer elements of its row, in groups of kVec
+// consecutive ones (4 when E is a multiple of 4).  in: the weights (kSoftmax) or the logits.
+template <int kRouter, int kLanes, int kPer, int kVec>
 __global__ void __launch_bounds__(32 * kWarps)
     route_grad_kernel(const float* __restrict__ in, const int32_t* __restrict__ ids,
                       const float* __restrict__ dw, int N, int E, int k,
                       float* __restrict__ dlogits) {
     extern __shared__ __align__(16) float rows[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kGroups = 32 * kWarps / kLanes;  // tokens of a block
+    const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const int pitch = (E + 3) & ~3;
-    float* row = rows + warp * pitch;
-    for (int c = lane; c < pitch; c += 32) row[c] = 0.0f;
+    float* row = rows + group * pitch;
+    for (int c = lane; c < pitch; c += kLanes) row[c] = 0.0f;
     __syncwarp();
-    for (long long t = (long long)blockIdx.x * kWarps + warp; t < N;
-         t += (long long)gridDim.x * kWarps) {
+    const int ahead = (threadIdx.x & 31) / kLanes;  // of the warp's first token
+    for (long long t = (long long)blockIdx.x * kGroups + group; t - ahead < N;
+         t += (long long)gridDim.x * kGroups) {
+        const bool live = t < N;
         float v[kPer];
         if (kRouter == kFullSoftmax) {
 #pragma unroll
             for (int i = 0; i < kPer / kVec; ++i) {
-                const int c = (i * 32 + lane) * kVec;
+                const int c = (i * kLanes + lane) * kVec;
                 if (kVec == 4) {
                     float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                    if (c < E) x = __ldcs(reinterpret_cast<const float4*>(in + t * E + c));
+                    if (c < E && live) x = __ldcs(reinterpret_cast<const float4*>(in + t * E + c));
                     v[i * kVec] = x.x;
                     v[i * kVec + 1 % kVec] = x.y;
                     v[i * kVec + 2 % kVec] = x.z;
                     v[i * kVec + 3 % kVec] = x.w;
                 } else {
-                    v[i] = c < E ? __ldcs(in + t * E + c) : -INFINITY;
+                    v[i] = c < E && live ? __ldcs(in + t * E + c) : -INFINITY;
                 }
             }
         }
         // choice j of the token in lane j; an id out of range takes no part
         int id = -1;
         float d = 0.0f, x = 0.0f, rest = 0.0f;  // rest: 1 - sigmoid
-        if (lane < k) {
+        if (lane < k && live) {
             id = ids[t * k + lane];
             if ((unsigned)id >= (unsigned)E) id = -1;
             d = dw[t * k + lane];
@@ -89,72 +97,78 @@ __global__ void __launch_bounds__(32 * kWarps)
             }
             if (id < 0) x = d = 0.0f;
         }
-        float dot = 0.0f, inv = 0.0f;
+        float inv = 0.0f;
         if (kRouter == kFullSoftmax) {
             float m = v[0];
 #pragma unroll
             for (int i = 1; i < kPer; ++i) m = fmaxf(m, v[i]);
-            m = warp_max(m);
+            m = lanes_max<kLanes>(m);
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 v[i] = expf(v[i] - m);
                 sum += v[i];
             }
-            inv = 1.0f / warp_sum(sum);
-            if (id >= 0) row[id] = d;
+            inv = 1.0f / lanes_sum<kLanes>(sum);
+        } else if (kRouter == kSigmoid) {
+            const float total = lanes_sum<kLanes>(x);
+            const float w = x / total;
+            const float own = d - lanes_sum<kLanes>(w * d);
+            d = own * w * rest;
         } else {
-            if (kRouter == kSigmoid) {
-                const float total = warp_sum(x);
-                const float w = x / total;
-                const float own = d - warp_sum(w * d);
-                d = own * w * rest;
-            } else {
-                d = x * (d - warp_sum(x * d));
-            }
-            if (id >= 0) row[id] = d;
+            d = x * (d - lanes_sum<kLanes>(x * d));
         }
+        if (id >= 0) row[id] = d;
         __syncwarp();
-        if (kRouter == kFullSoftmax) {
-            // p . d over the row: zero where nothing is selected
-#pragma unroll
-            for (int i = 0; i < kPer / kVec; ++i) {
-                const int c = (i * 32 + lane) * kVec;
-#pragma unroll
-                for (int j = 0; j < kVec; ++j)
-                    if (c < E) dot += v[i * kVec + j] * row[c + j];
-            }
-            dot = warp_sum(dot) * inv;
-        }
+        float o[kPer];
 #pragma unroll
         for (int i = 0; i < kPer / kVec; ++i) {
-            const int c = (i * 32 + lane) * kVec;
-            if (c < E) {
-                float o[kVec];
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    o[j] = row[c + j];
-                    if (kRouter == kFullSoftmax) o[j] = v[i * kVec + j] * inv * (o[j] - dot);
-                }
-                if (kVec == 4)
-                    __stcs(reinterpret_cast<float4*>(dlogits + t * E + c),
-                           make_float4(o[0], o[1 % kVec], o[2 % kVec], o[3 % kVec]));
-                else
-                    __stcs(dlogits + t * E + c, o[0]);
+            const int c = (i * kLanes + lane) * kVec;
+            if (kVec == 4) {
+                float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (c < E) r = *reinterpret_cast<const float4*>(row + c);
+                o[i * kVec] = r.x;
+                o[i * kVec + 1 % kVec] = r.y;
+                o[i * kVec + 2 % kVec] = r.z;
+                o[i * kVec + 3 % kVec] = r.w;
+            } else {
+                o[i] = c < E ? row[c] : 0.0f;
             }
         }
         __syncwarp();
         if (id >= 0) row[id] = 0.0f;
+        if (kRouter == kFullSoftmax) {
+            // p . d over the row: zero where nothing is selected
+            float dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) dot += v[i] * o[i];
+            dot = lanes_sum<kLanes>(dot) * inv;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) o[i] = v[i] * inv * (o[i] - dot);
+        }
+#pragma unroll
+        for (int i = 0; i < kPer / kVec; ++i) {
+            const int c = (i * kLanes + lane) * kVec;
+            if (c < E && live) {
+                if (kVec == 4)
+                    __stcs(reinterpret_cast<float4*>(dlogits + t * E + c),
+                           make_float4(o[i * kVec], o[i * kVec + 1 % kVec], o[i * kVec + 2 % kVec],
+                                       o[i * kVec + 3 % kVec]));
+                else
+                    __stcs(dlogits + t * E + c, o[i]);
+            }
+        }
         __syncwarp();
     }
 }
 
-template <int kRouter, int kPer, int kVec>
+template <int kRouter, int kLanes, int kPer, int kVec>
 cudaError_t launch_one(const float* in, const int32_t* ids, const float* dw, const moe_shape& s,
                        float* dlogits, cudaStream_t st) {
-    const long long blocks = (s.N + kWarps - 1) / kWarps, most = 16LL * sm_count();
-    const size_t smem = (size_t)kWarps * ((s.E + 3) & ~3) * sizeof(float);
-    route_grad_kernel<kRouter, kPer, kVec>
+    constexpr int kGroups = 32 * kWarps / kLanes;
+    const long long blocks = (s.N + kGroups - 1LL) / kGroups, most = 16LL * sm_count();
+    const size_t smem = (size_t)kGroups * ((s.E + 3) & ~3) * sizeof(float);
+    route_grad_kernel<kRouter, kLanes, kPer, kVec>
         <<<(int)(blocks < most ? blocks : most), 32 * kWarps, smem, st>>>(in, ids, dw, s.N, s.E,
                                                                           s.k, dlogits);
     return cudaGetLastError();
@@ -166,13 +180,17 @@ cudaError_t launch_router(const float* in, const int32_t* ids, const float* dw,
     const bool vec = s.E % 4 == 0 && ((uintptr_t)dlogits & 15) == 0 &&
                      (kRouter != kFullSoftmax || ((uintptr_t)in & 15) == 0);
     if (vec) {
-        if (s.E <= 128) return launch_one<kRouter, 4, 4>(in, ids, dw, s, dlogits, st);
-        if (s.E <= 256) return launch_one<kRouter, 8, 4>(in, ids, dw, s, dlogits, st);
-        if (s.E <= 512) return launch_one<kRouter, 16, 4>(in, ids, dw, s, dlogits, st);
-        return launch_one<kRouter, 32, 4>(in, ids, dw, s, dlogits, st);
+        if (s.E <= 64 && s.k <= 8) return launch_one<kRouter, 8, 8, 4>(in, ids, dw, s, dlogits, st);
+        if (s.E <= 128 && s.k <= 16)
+            return launch_one<kRouter, 16, 8, 4>(in, ids, dw, s, dlogits, st);
+        if (s.E <= 256 && s.k <= 16)
+            return launch_one<kRouter, 16, 16, 4>(in, ids, dw, s, dlogits, st);
+        if (s.E <= 256) return launch_one<kRouter, 32, 8, 4>(in, ids, dw, s, dlogits, st);
+        if (s.E <= 512) return launch_one<kRouter, 32, 16, 4>(in, ids, dw, s, dlogits, st);
+        return launch_one<kRouter, 32, 32, 4>(in, ids, dw, s, dlogits, st);
     }
-    if (s.E <= 256) return launch_one<kRouter, 8, 1>(in, ids, dw, s, dlogits, st);
-    return launch_one<kRouter, 32, 1>(in, ids, dw, s, dlogits, st);
+    if (s.E <= 256) return launch_one<kRouter, 32, 8, 1>(in, ids, dw, s, dlogits, st);
+    return launch_one<kRouter, 32, 32, 1>(in, ids, dw, s, dlogits, st);
 }
 
 }  // namespace

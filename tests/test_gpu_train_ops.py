@@ -203,6 +203,50 @@ def test_route_grad_unaligned_rows():
     assert (out - want).abs().max() <= 2e-6 * want.abs().max()
 
 
+@pytest.mark.parametrize("router", ["softmax", "full_softmax", "sigmoid_bias"])
+@pytest.mark.parametrize("N,E,k", [(9, 48, 1), (131, 64, 8), (77, 64, 9), (63, 100, 16),
+                                   (50, 128, 17), (66, 252, 16), (35, 256, 17), (4097, 128, 6)])
+def test_route_grad_of_several_tokens_a_warp(router, N, E, k):
+    test_route_grad(router, N, E, k)
+
+
+@pytest.mark.parametrize("router", ["softmax", "full_softmax", "sigmoid_bias"])
+def test_route_grad_ids_out_of_range_take_no_part(router):
+    """One choice of some tokens is no expert: the others' gradients are those of the choices
+    that are left, and nothing is written outside the rows."""
+    shape, logits, ids, w = route(router, 37, 24, 3)
+    dw = normal(gen(8), 37, 3)
+    bad = torch.zeros(37, 3, dtype=torch.bool, device="cuda")
+    bad[::2, 1] = True
+    broken = torch.where(bad, torch.tensor([-1, 24, 1 << 30], device="cuda").int()[None], ids)
+    guard = torch.full((39, 24), 5.0, device="cuda")
+    out = guard[1:38]
+    if router == "softmax":
+        moe.moe_route_grad(broken, w, dw, shape, out)
+    else:
+        getattr(moe, CALLS[router])(logits, broken, dw, shape, out)
+    assert (guard[0] == 5).all() and (guard[38] == 5).all() and torch.isfinite(out).all()
+    # as if that choice had no weight: zero where it was, the others among themselves
+    i, keep = ids.long(), (~bad).double()
+    L, d = logits.double(), dw.double() * keep
+    if router == "softmax":
+        wk = w.double() * keep
+        g = wk * (d - (wk * d).sum(1, keepdim=True))
+        want = torch.zeros_like(L).scatter_(1, i, g * keep)
+    elif router == "full_softmax":
+        p = torch.softmax(L, 1)
+        dd = torch.zeros_like(L).scatter_(1, i, d)
+        want = p * (dd - (p * dd).sum(1, keepdim=True))
+    else:
+        s = torch.sigmoid(L.gather(1, i)) * keep
+        wk = s / s.sum(1, keepdim=True)
+        g = wk * (d - (wk * d).sum(1, keepdim=True)) * (1 - torch.sigmoid(L.gather(1, i)))
+        want = torch.zeros_like(L).scatter_(1, i, g * keep)
+    # terms of at most |dw| and their sum, as in test_route_grad
+    bound = 6e-6 * (dw.double().abs().sum(1, keepdim=True) * 2)
+    assert ((out.double() - want).abs() <= bound).all()
+
+
 # ---- block norms -------------------------------------------------------------------------
 
 EPS, ALPHA = 1e-5, 0.75
