@@ -81,6 +81,32 @@ struct NvtxRange {
     NvtxRange(const NvtxRange&) = delete;
     NvtxRange& operator=(const NvtxRange&) = delete;
 };
+// Launches a kernel whose blocks call after_previous(), in clusters of `cluster` blocks
+// (0: as the kernel says).
+template <typename... P, typename... A>
+inline cudaError_t launch_chained_clusters(void (*kernel)(P...), int cluster, dim3 grid, int block,
+                                           size_t smem, cudaStream_t st, const A&... args) {
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+template <typename... P, typename... A>
+inline cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int block, size_t smem,
+                                  cudaStream_t st, const A&... args) {
+    return launch_chained_clusters(kernel, 0, grid, block, smem, st, args...);
+}
+
 #define MOE_RANGE() const NvtxRange _moe_nvtx_range(__func__)
 
 #define MOE_TRY(expr)                     \

@@ -186,8 +186,8 @@ __device__ __forceinline__ void load_channel(const float* p, const Cols& q, f2 (
     if (p) {
         const float4* v = reinterpret_cast<const float4*>(p);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-        if (q.pa) x = __ldg(v + q.a);
-        if (q.pb) y = __ldg(v + q.b);
+        if (q.pa) x = v[q.a];
+        if (q.pb) y = v[q.b];
         f[0] = make_float2(x.x, x.y);
         f[1] = make_float2(x.z, x.w);
         f[2] = make_float2(y.x, y.y);
@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t V = a.V;
     const Rows rows = my_rows<kLanes>();
     const bool has_y = kFull || a.y, post = kFull || a.post, pre = kFull || a.pre;
+    after_previous();
 
     const auto cols = [&](int i) { return cols_of<kF32>(tid + i * lanes, kLanes ? kLanes : 32, V); };
     Raw<false> ry[kV];
@@ -511,6 +512,7 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
     const uint32_t pitch = blockDim.x * 16, stage_bytes = pitch * kV * kPerV;
     const uint32_t ring0 = kRing ? ptx::smem_u32(ring) : 0u;
     const bool has_y = kFull || a.y, pre = kFull || a.pre, has_ds = kFull || a.ds;
+    after_previous();
     f2 t_post[kV][4], t_pre[kV][4];
 #pragma unroll
     for (int i = 0; i < kV; ++i)
@@ -703,12 +705,11 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
 // dw_post = gate T, dgate = w_post T.
 constexpr int kReduceRows = 32;
 __global__ void __launch_bounds__(32 * kReduceRows)
-    block_norm_reduce_kernel(const float* __restrict__ partial, int blocks, int H,
-                             const float* __restrict__ gate, const float* __restrict__ w_post,
+    block_norm_reduce_kernel(const float* partial, int blocks, int H,
+                             const float* gate, const float* w_post,
                              float* dw_post, float* dgate, float* dw_pre, int accumulate) {
     __shared__ float sums[kReduceRows][33];
-    // launched while the kernel that writes the partial sums still runs
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), r0 = threadIdx.x >> 5;
     const int which = blockIdx.y;
     float v = 0.0f;
@@ -814,8 +815,7 @@ cudaError_t run(const Args& a, const Plan& p, cudaStream_t st) {
             if (dev < 64) set[dev] = true;
         }
     }
-    kKernel<<<p.grid, p.block, p.smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_chained(kKernel, p.grid, p.block, p.smem, st, a);
 }
 
 template <bool kF32, bool kFull>
@@ -937,19 +937,11 @@ moe_status moe_block_norm_grad(const void* ds, const uint16_t* dx, const uint16_
                              : (f32 ? run_grad<true, false>(a, p, st)
                                     : run_grad<false, false>(a, p, st))));
     if (dw_post || dw_pre || (dgate && by_channel)) {
-        cudaLaunchAttribute early[1];
-        early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        early[0].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((shape->H + 31) / 32, dw_pre ? 2 : 1);
-        cfg.blockDim = dim3(32 * kReduceRows);
-        cfg.stream = st;
-        cfg.attrs = early;
-        cfg.numAttrs = 1;
-        MOE_TRY(cuda_status(cudaLaunchKernelEx(
-            &cfg, block_norm_reduce_kernel, (const float*)a.partial, p.grid, (int)shape->H,
-            by_channel ? gate : (const float*)nullptr, post ? w_post : (const float*)nullptr,
-            dw_post, by_channel ? dgate : (float*)nullptr, dw_pre, accumulate != 0 ? 1 : 0)));
+        MOE_TRY(cuda_status(launch_chained(
+            block_norm_reduce_kernel, dim3((shape->H + 31) / 32, dw_pre ? 2 : 1), 32 * kReduceRows,
+            0, st, a.partial, p.grid, shape->H, by_channel ? gate : nullptr,
+            post ? w_post : nullptr, dw_post, by_channel ? dgate : nullptr, dw_pre,
+            accumulate != 0 ? 1 : 0)));
     }
     return MOE_OK;
 }

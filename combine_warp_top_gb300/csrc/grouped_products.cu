@@ -55,13 +55,13 @@
 //   with those fences and 64-byte lines, 288 us now; floor 253 us.
 // - A tile costs each role some 800 cycles to decode: the scheduler does it for all.
 // - A decoding step streams the weights: 16 tokens of 6 of 64 experts of 2816 x 2048,
-//   88 us for 586 MB, 6.7 TB/s, with the matrix as A and 64 rows as B (kFew); 97 us with
+//   86 us for 586 MB, 6.8 TB/s, with the matrix as A and 64 rows as B (kFew); 97 us with
 //   256 rows as A, whose MMAs take longer than the weights.
 // - Few tiles leave SMs idle: with a long contraction 2 or 4 pairs of a cluster share
 //   a tile's k-blocks, keep their sums in shared memory and add them up from there
 //   (4096 rows of one expert, 256 x 256 fp32 weights' gradient: 29 us with one pair,
 //   19 us with four; 1 row, 14336 x 3528 in tiles of few rows: 24 us with four).
-// - 64 tokens of 8 experts, 128 to 512: 5.2 us, of them 1.1 the experts' counts and the
+// - 64 tokens of 8 experts, 128 to 512: 5.0 us in a row of such calls; alone 5.2, of them 1.1 the experts' counts and the
 //   first tile, 0.4 the meeting of the CTAs, 0.9 loads, 0.6 MMAs, 0.5 stores, 0.7 the end.
 #include <stddef.h>
 
@@ -485,8 +485,8 @@ __device__ __forceinline__ void join_few(uint32_t ring, uint32_t rank, int split
 template <int kMode, typename OutT, bool kFew, bool kSplit>
 __device__ __forceinline__ void grouped_product(
     const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmOut,
-    const int32_t* __restrict__ expert_offsets, const int32_t* __restrict__ expert_counts, int E,
-    int R, int K, int m_out, int n_out, OutT* __restrict__ out, int accumulate, int a_groups,
+    const int32_t* expert_offsets, const int32_t* expert_counts, int E,
+    int R, int K, int m_out, int n_out, OutT* out, int accumulate, int a_groups,
     int b_groups, int* err, int* tile_counter) {
     constexpr bool kW = kMode == kWeightsGrad;
     static_assert(!kW || !kFew, "a weights' gradient has no tiles of few rows");
@@ -522,6 +522,29 @@ __device__ __forceinline__ void grouped_product(
     const int KB = (K + BK - 1) / BK;
     const int n_last = kFew ? BT : last_columns(n_out, kMnB && b_groups);
 
+    // one or two barriers a thread, not 63 and more of them one after the other
+    static_assert(3 * kStages <= 64 && kQueueBarriers <= 64, "barriers of 64 threads");
+    if (warp == 4 || warp == 5) {
+        const int i = threadIdx.x - 128, q = i - (2 * kAccs + 1);
+        int count = 1;
+        if (i >= kAccs && i < 2 * kAccs) count = 2 * kEpilogueWarps;  // tempty
+        if (q >= kQ && q < 2 * kQ) count = kQueueReaders;             // q_empty
+        if (q >= 4 * kQ) count = kLocalReaders;                       // l_empty
+        if (i < kQueueBarriers) mbar_init(smem_u32(&ctl->tfull[0] + i), count);
+        if (i < 3 * kStages) mbar_init(smem_u32(&ctl->full[0] + i), kW && i < kStages ? 2 : 1);
+        if (i == 63) ctl->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_map(&tmA);
+        prefetch_map(&tmB);
+        if (!kFew) prefetch_map(&tmOut);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&ctl->tmem_base), kTmemCols);
+        tmem_relinquish_pair();
+    }
+    after_previous();
     // A weights' gradient hands out the experts with the most rows first: their tiles
     // take the longest, and the short ones fill the pairs up at the end (Zipf-skewed
     // case of 262144 rows in 128 experts: 2190 us in the experts' order, 2040 so).
@@ -542,24 +565,6 @@ __device__ __forceinline__ void grouped_product(
             fence_async_shared();  // before TMA writes there
             __syncthreads();
         }
-    }
-    // one or two barriers a thread, not 63 and more of them one after the other
-    static_assert(3 * kStages <= 64 && kQueueBarriers <= 64, "barriers of 64 threads");
-    if (warp == 4 || warp == 5) {
-        const int i = threadIdx.x - 128, q = i - (2 * kAccs + 1);
-        int count = 1;
-        if (i >= kAccs && i < 2 * kAccs) count = 2 * kEpilogueWarps;  // tempty
-        if (q >= kQ && q < 2 * kQ) count = kQueueReaders;             // q_empty
-        if (q >= 4 * kQ) count = kLocalReaders;                       // l_empty
-        if (i < kQueueBarriers) mbar_init(smem_u32(&ctl->tfull[0] + i), count);
-        if (i < 3 * kStages) mbar_init(smem_u32(&ctl->full[0] + i), kW && i < kStages ? 2 : 1);
-        if (i == 63) ctl->abort = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == 0 && lane == 0) {
-        prefetch_map(&tmA);
-        prefetch_map(&tmB);
-        if (!kFew) prefetch_map(&tmOut);
     }
     // Products over rows: lane l of the scheduler holds the row blocks in its run of
     // experts [l * per, (l + 1) * per) and up to its end.
@@ -653,10 +658,6 @@ __device__ __forceinline__ void grouped_product(
             ctl->first = t;
             ctl->only = kSplit || total <= (int)gridDim.x / 2;
         }
-    }
-    if (warp == 1) {
-        tmem_alloc_pair(smem_u32(&ctl->tmem_base), kTmemCols);
-        tmem_relinquish_pair();
     }
     tc_fence_before();
     __syncthreads();
@@ -1103,9 +1104,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_product_kernel(const __grid_constant__ CUtensorMap tmA,
                            const __grid_constant__ CUtensorMap tmB,
                            const __grid_constant__ CUtensorMap tmOut,
-                           const int32_t* __restrict__ expert_offsets,
-                           const int32_t* __restrict__ expert_counts, int E, int R, int K,
-                           int m_out, int n_out, OutT* __restrict__ out, int accumulate,
+                           const int32_t* expert_offsets,
+                           const int32_t* expert_counts, int E, int R, int K,
+                           int m_out, int n_out, OutT* out, int accumulate,
                            int a_groups, int b_groups, int* err, int* tile_counter) {
     grouped_product<kMode, OutT, kFew, false>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R, K,
                                         m_out, n_out, out, accumulate, a_groups, b_groups, err,
@@ -1117,9 +1118,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     grouped_product_split_kernel(const __grid_constant__ CUtensorMap tmA,
                                  const __grid_constant__ CUtensorMap tmB,
                                  const __grid_constant__ CUtensorMap tmOut,
-                                 const int32_t* __restrict__ expert_offsets,
-                                 const int32_t* __restrict__ expert_counts, int E, int R, int K,
-                                 int m_out, int n_out, OutT* __restrict__ out, int accumulate,
+                                 const int32_t* expert_offsets,
+                                 const int32_t* expert_counts, int E, int R, int K,
+                                 int m_out, int n_out, OutT* out, int accumulate,
                                  int a_groups, int b_groups, int* err, int* tile_counter) {
     grouped_product<kMode, OutT, kFew, true>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R, K,
                                        m_out, n_out, out, accumulate, a_groups, b_groups, err,
@@ -1180,33 +1181,18 @@ moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap&
         splits = kMaxSplits;
     else if (tiles <= at_once[dev][0] && blocks > join_blocks * 2)
         splits = 2;
-    if (splits > 1) {
-        cudaLaunchAttribute cluster[1];
-        cluster[0].id = cudaLaunchAttributeClusterDimension;
-        cluster[0].val.clusterDim.x = 2 * splits;
-        cluster[0].val.clusterDim.y = cluster[0].val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(tiles * 2 * splits));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = st;
-        cfg.attrs = cluster;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, split_kernel, a, b, o,
-                                  (const int32_t*)g.offsets, (const int32_t*)g.counts, g.E,
-                                  (int)g.R, K, m_out, n_out, reinterpret_cast<OutT*>(out),
-                                  accumulate ? 1 : 0, a_groups, b_groups, g.err,
-                                  (int*)nullptr) == cudaSuccess
-                   ? MOE_OK
-                   : MOE_ERR_CUDA;
-    }
+    if (splits > 1)
+        return cuda_status(launch_chained_clusters(
+            split_kernel, 2 * splits, (int)(tiles * 2 * splits), kThreads, smem, st, a, b, o,
+            g.offsets, g.counts, g.E, (int)g.R, K, m_out, n_out, reinterpret_cast<OutT*>(out),
+            accumulate ? 1 : 0, a_groups, b_groups, g.err, (int*)nullptr));
     const long long pairs_max = sm_count() / 2;
     const long long pairs = tiles < pairs_max ? tiles : pairs_max;
-    grouped_product_kernel<kMode, OutT, kFew>
-        <<<(int)(2 * (pairs > 0 ? pairs : 1)), kThreads, smem, st>>>(
-            a, b, o, g.offsets, g.counts, g.E, (int)g.R, K, m_out, n_out,
-            reinterpret_cast<OutT*>(out), accumulate ? 1 : 0, a_groups, b_groups, g.err, g.prefix + g.E + 1);
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return cuda_status(launch_chained(
+        grouped_product_kernel<kMode, OutT, kFew>, (int)(2 * (pairs > 0 ? pairs : 1)), kThreads,
+        smem, st, a, b, o, g.offsets, g.counts, g.E, (int)g.R, K, m_out, n_out,
+        reinterpret_cast<OutT*>(out), accumulate ? 1 : 0, a_groups, b_groups, g.err,
+        g.prefix + g.E + 1));
 }
 
 // A [outer, rows, cols] matrix (outer 0: [rows, cols]) in boxes of 64 columns.

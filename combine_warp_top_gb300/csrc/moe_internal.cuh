@@ -75,6 +75,17 @@ __device__ __forceinline__ void warp_mblk_prefix(const int* cnts, int E, int bm,
     if (lane == 31) prefix[E] = incl;
 }
 
+// The blocks of a kernel launched by launch_chained start while the kernel before it on the
+// stream still runs; what they do before this touches no memory that another kernel writes,
+// and no load of such a kernel is a read-only one (the data may change after its start).
+// Every block calls it, so that a kernel's end is the end of all kernels before it.
+// What it gives, kernels back to back: block norm of 4096 x 7168 63.5 -> 60.0 us, its
+// gradient of 8192 x 4096 75.4 -> 72.6 us, router gradient of 32768 x 256 12.8 -> 11.2 us.
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Device-side status recording: the first error sticks.
 __device__ __forceinline__ void set_error(int* err, int code) {
     if (err) atomicCAS(err, 0, code);

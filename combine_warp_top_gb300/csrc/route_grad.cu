@@ -18,7 +18,7 @@
 // The row is all zeros between tokens: only the k entries are put back.  With a warp for
 // every token the instructions for it (three sums over the lanes, the choices) take longer
 // than a short row's bytes.  32768 tokens, full softmax: of 256 experts 12.0 us (a warp each:
-// 13.4 us; the 69 MB take 10.2), of 128 7.4 us (8.1), of 64 4.2 us (7.9); softmax over the
+// 13.4 us; the 69 MB take 10.2; back to back 11.1), of 128 7.4 us (8.1), of 64 4.2 us (7.9); softmax over the
 // selected, of 64 3.5 us (5.5).  4096 of 64: 2.0 us, a launch.  The next token's loads a
 // token ahead measured slower (15.9 us of 256).
 #include <math.h>
@@ -51,15 +51,16 @@ __device__ __forceinline__ float lanes_max(float v) {
 // consecutive ones (4 when E is a multiple of 4).  in: the weights (kSoftmax) or the logits.
 template <int kRouter, int kLanes, int kPer, int kVec>
 __global__ void __launch_bounds__(32 * kWarps)
-    route_grad_kernel(const float* __restrict__ in, const int32_t* __restrict__ ids,
-                      const float* __restrict__ dw, int N, int E, int k,
-                      float* __restrict__ dlogits) {
+    route_grad_kernel(const float* in, const int32_t* ids,
+                      const float* dw, int N, int E, int k,
+                      float* dlogits) {
     extern __shared__ __align__(16) float rows[];
     constexpr int kGroups = 32 * kWarps / kLanes;  // tokens of a block
     const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const int pitch = (E + 3) & ~3;
     float* row = rows + group * pitch;
     for (int c = lane; c < pitch; c += kLanes) row[c] = 0.0f;
+    after_previous();
     __syncwarp();
     const int ahead = (threadIdx.x & 31) / kLanes;  // of the warp's first token
     for (long long t = (long long)blockIdx.x * kGroups + group; t - ahead < N;
@@ -168,10 +169,9 @@ cudaError_t launch_one(const float* in, const int32_t* ids, const float* dw, con
     constexpr int kGroups = 32 * kWarps / kLanes;
     const long long blocks = (s.N + kGroups - 1LL) / kGroups, most = 16LL * sm_count();
     const size_t smem = (size_t)kGroups * ((s.E + 3) & ~3) * sizeof(float);
-    route_grad_kernel<kRouter, kLanes, kPer, kVec>
-        <<<(int)(blocks < most ? blocks : most), 32 * kWarps, smem, st>>>(in, ids, dw, s.N, s.E,
-                                                                          s.k, dlogits);
-    return cudaGetLastError();
+    return launch_chained(route_grad_kernel<kRouter, kLanes, kPer, kVec>,
+                          (int)(blocks < most ? blocks : most), 32 * kWarps, smem, st, in, ids, dw,
+                          s.N, s.E, s.k, dlogits);
 }
 
 template <int kRouter>

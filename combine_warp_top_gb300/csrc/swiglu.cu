@@ -56,8 +56,8 @@ __device__ __forceinline__ float sigmoid(float g) {
 // choice from the lane whose pair_row names the row.  Run by whole warps, every kLanes
 // lanes for a row of their own (live: there is one); -1 if the layout names none.
 template <int kLanes>
-__device__ __forceinline__ long long pair_of_row(const int32_t* __restrict__ row_token,
-                                                 const int32_t* __restrict__ pair_row, int N,
+__device__ __forceinline__ long long pair_of_row(const int32_t* row_token,
+                                                 const int32_t* pair_row, int N,
                                                  int k, long long row, bool live) {
     const int lane = threadIdx.x & 31, sub = lane % kLanes;
     const int t = live ? row_token[row] : -1;
@@ -77,13 +77,14 @@ __device__ __forceinline__ long long pair_of_row(const int32_t* __restrict__ row
 // their loads in flight at once; `parts` pieces make a row.
 template <int kLanes, int kVecs>
 __global__ void __launch_bounds__(kBlock)
-    swiglu_kernel(const uint4* __restrict__ gu, const float* __restrict__ topk_w,
-                  const int32_t* __restrict__ row_token, const int32_t* __restrict__ pair_row,
-                  int N, int k, long long pieces, int parts, int V, uint4* __restrict__ h) {
+    swiglu_kernel(const uint4* gu, const float* topk_w,
+                  const int32_t* row_token, const int32_t* pair_row,
+                  int N, int k, long long pieces, int parts, int V, uint4* h) {
     constexpr int kGroups = kBlock / kLanes;
     const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
     const int in_warp = (threadIdx.x & 31) / kLanes;  // a warp's groups leave together
     const long long step = (long long)gridDim.x * kGroups;
+    after_previous();
     for (long long p = (long long)blockIdx.x * kGroups + group; p - in_warp < pieces; p += step) {
         const bool live = kLanes == 32 || p < pieces;
         const long long row = live ? p / parts : 0;
@@ -122,10 +123,10 @@ __global__ void __launch_bounds__(kBlock)
 // block.  The first loads of a row are in flight while its pair is looked up.
 template <int kLanes>
 __global__ void __launch_bounds__(kLanes > 32 ? kLanes : kBlock)
-    swiglu_grad_kernel(const uint4* __restrict__ dh, const uint4* __restrict__ gu,
-                       const float* __restrict__ topk_w, const int32_t* __restrict__ row_token,
-                       const int32_t* __restrict__ pair_row, int N, int k, long long R, int V,
-                       uint4* __restrict__ dgu, float* __restrict__ dtopk_w) {
+    swiglu_grad_kernel(const uint4* dh, const uint4* gu,
+                       const float* topk_w, const int32_t* row_token,
+                       const int32_t* pair_row, int N, int k, long long R, int V,
+                       uint4* dgu, float* dtopk_w) {
     constexpr bool kBlockRow = kLanes > 32;
     constexpr int kLook = kBlockRow ? 32 : kLanes;  // lanes that look up a pair
     constexpr int kVecs = 2, kGroups = kBlockRow ? 1 : kBlock / kLanes;
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(kLanes > 32 ? kLanes : kBlock)
     const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
     const int in_warp = kBlockRow ? 0 : (threadIdx.x & 31) / kLanes;
     const long long step = (long long)gridDim.x * kGroups;
+    after_previous();
     for (long long row = (long long)blockIdx.x * kGroups + group; row - in_warp < R; row += step) {
         const bool live = kLanes >= 32 || row < R;
         const uint4* d = dh + row * V;
@@ -227,16 +229,15 @@ moe_status moe_swiglu(const uint16_t* gu, const float* topk_w, const moe_layout*
     const long long pieces = R * parts, groups = kBlock / lanes;
     const int grid = grid_for((pieces + groups - 1) / groups);
     const auto go = [&](auto kernel) {
-        kernel<<<grid, kBlock, 0, as_stream(stream)>>>(in, topk_w, layout->row_token,
-                                                       layout->pair_row, shape->N, shape->k,
-                                                       pieces, parts, V, out);
+        return launch_chained(kernel, grid, kBlock, 0, as_stream(stream), in, topk_w,
+                              layout->row_token, layout->pair_row, shape->N, shape->k, pieces,
+                              parts, V, out);
     };
-    if (lanes == 8) go(swiglu_kernel<8, 1>);
-    else if (lanes == 16) go(swiglu_kernel<16, 1>);
-    else if (vecs == 4) go(swiglu_kernel<32, 4>);
-    else if (vecs == 2) go(swiglu_kernel<32, 2>);
-    else go(swiglu_kernel<32, 1>);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(lanes == 8    ? go(swiglu_kernel<8, 1>)
+                       : lanes == 16 ? go(swiglu_kernel<16, 1>)
+                       : vecs == 4   ? go(swiglu_kernel<32, 4>)
+                       : vecs == 2   ? go(swiglu_kernel<32, 2>)
+                                     : go(swiglu_kernel<32, 1>));
 }
 
 moe_status moe_swiglu_grad(const uint16_t* dh, const uint16_t* gu, const float* topk_w,
@@ -253,19 +254,19 @@ moe_status moe_swiglu_grad(const uint16_t* dh, const uint16_t* gu, const float* 
     uint4* out = reinterpret_cast<uint4*>(dgu);
     const int V = shape->I / 8;
     const auto go = [&](auto kernel, int block, long long groups) {
-        kernel<<<grid_for((R + groups - 1) / groups), block, 0, as_stream(stream)>>>(
-            d, in, topk_w, layout->row_token, layout->pair_row, shape->N, shape->k, R, V, out,
-            dtopk_w);
+        return launch_chained(kernel, grid_for((R + groups - 1) / groups), block, 0,
+                              as_stream(stream), d, in, topk_w, layout->row_token, layout->pair_row,
+                              shape->N, shape->k, R, V, out, dtopk_w);
     };
     // A warp (or the lanes of a short row) takes a row when that gives every SM at
     // least 32 warps and a row is not long; long rows leave too few warps in the last
     // wave, so a block of 4 or 8 warps takes them, whichever idles less.
-    if (V <= 8) go(swiglu_grad_kernel<8>, kBlock, kBlock / 8);
-    else if (V <= 16) go(swiglu_grad_kernel<16>, kBlock, kBlock / 16);
-    else if (V <= 512 && R >= 32LL * sm_count()) go(swiglu_grad_kernel<32>, kBlock, kBlock / 32);
-    else if ((V + 255) / 256 * 2 > (V + 127) / 128) go(swiglu_grad_kernel<128>, 128, 1);
-    else go(swiglu_grad_kernel<256>, 256, 1);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(
+        V <= 8    ? go(swiglu_grad_kernel<8>, kBlock, kBlock / 8)
+        : V <= 16 ? go(swiglu_grad_kernel<16>, kBlock, kBlock / 16)
+        : V <= 512 && R >= 32LL * sm_count()         ? go(swiglu_grad_kernel<32>, kBlock, kBlock / 32)
+        : (V + 255) / 256 * 2 > (V + 127) / 128 ? go(swiglu_grad_kernel<128>, 128, 1)
+                                                : go(swiglu_grad_kernel<256>, 256, 1));
 }
 
 }  // extern "C"

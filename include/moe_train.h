@@ -7,6 +7,9 @@
  * checked on the host before anything is launched, nothing allocated.
  * No call here uses atomics whose order could change a result: every output is
  * the same from run to run on one GPU model.
+ * The kernels are launched with programmatic stream serialization: their blocks
+ * may start while the kernel before them on the stream ends, and wait for it
+ * before they touch memory.
  */
 #ifndef MOE_TRAIN_H
 #define MOE_TRAIN_H
