@@ -61,8 +61,9 @@
 //   a tile's k-blocks, keep their sums in shared memory and add them up from there
 //   (4096 rows of one expert, 256 x 256 fp32 weights' gradient: 29 us with one pair,
 //   19 us with four; 1 row, 14336 x 3528 in tiles of few rows: 24 us with four).
-// - 64 tokens of 8 experts, 128 to 512: 5.0 us in a row of such calls; alone 5.2, of them 1.1 the experts' counts and the
-//   first tile, 0.4 the meeting of the CTAs, 0.9 loads, 0.6 MMAs, 0.5 stores, 0.7 the end.
+// - 64 tokens of 8 experts, 128 to 512: 5.0 us in a row of such calls; alone 5.2, of
+//   them 1.1 the experts' counts and the first tile, 0.4 the meeting of the CTAs, 0.9
+//   loads, 0.6 MMAs, 0.5 stores, 0.7 the end.
 #include <stddef.h>
 
 #include "../../include/moe_train.h"
