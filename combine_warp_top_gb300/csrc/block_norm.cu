@@ -359,7 +359,9 @@ __global__ void __launch_bounds__(kThreads)
     const bool has_y = kFull || a.y, post = kFull || a.post, pre = kFull || a.pre;
     after_previous();
 
-    const auto cols = [&](int i) { return cols_of<kF32>(tid + i * lanes, kLanes ? kLanes : 32, V); };
+    const auto cols = [&](int i) {
+        return cols_of<kF32>(tid + i * lanes, kLanes ? kLanes : 32, V);
+    };
     Raw<false> ry[kV];
     Raw<kF32> rr[kV];
     auto load = [&](int row) {
@@ -519,7 +521,9 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
 #pragma unroll
         for (int j = 0; j < 4; ++j) t_post[i][j] = t_pre[i][j] = both(0.0f);
 
-    const auto cols = [&](int i) { return cols_of<kF32>(tid + i * lanes, kLanes ? kLanes : 32, V); };
+    const auto cols = [&](int i) {
+        return cols_of<kF32>(tid + i * lanes, kLanes ? kLanes : 32, V);
+    };
     // words of a vector in a stage: dx, y, then s and ds
     auto fetch = [&](int row, uint32_t stage) {
         if (row < a.N) {
@@ -593,7 +597,8 @@ __global__ void __launch_bounds__(kLanes ? 32 * kRowWarps : 1024)
                     rs[i].w[j] = rd[i].w[j] = make_uint4(0, 0, 0, 0);
             }
             if (pre) {
-                rx[i] = kRing ? ring_read<false, kF32>(at, pitch, q) : load_cols<false, kF32>(dx, q);
+                rx[i] = kRing ? ring_read<false, kF32>(at, pitch, q)
+                              : load_cols<false, kF32>(dx, q);
                 rs[i] = kRing ? ring_read<kF32, kF32>(at + 2 * pitch, pitch, q)
                               : load_cols<kF32, kF32>(sv, q);
             }
@@ -822,7 +827,8 @@ template <bool kF32, bool kFull>
 cudaError_t run_forward(const NormArgs& a, const Plan& p, cudaStream_t st) {
     constexpr int kW = 32 * kRowWarps;
     if (p.lanes == 8) return run<block_norm_kernel<1, 8, kF32, kAhead, true, kFull, kW>>(a, p, st);
-    if (p.lanes == 16) return run<block_norm_kernel<1, 16, kF32, kAhead, true, kFull, kW>>(a, p, st);
+    if (p.lanes == 16)
+        return run<block_norm_kernel<1, 16, kF32, kAhead, true, kFull, kW>>(a, p, st);
     if (p.lanes == 32)
         return p.kv == 1 ? run<block_norm_kernel<1, 32, kF32, kNow, true, kFull, kW>>(a, p, st)
                          : run<block_norm_kernel<2, 32, kF32, kNow, true, kFull, kW>>(a, p, st);
@@ -902,7 +908,8 @@ moe_status moe_block_norm_grad(const void* ds, const uint16_t* dx, const uint16_
     MOE_TRY(check_norm(shape));
     if (!ws || ws_bytes < moe_norm_workspace_bytes(shape)) return MOE_ERR_WORKSPACE;
     const bool post = shape->post != 0, pre = shape->pre != 0;
-    const bool by_channel = shape->gate == MOE_GATE_CHANNEL, by_token = shape->gate == MOE_GATE_TOKEN;
+    const bool by_channel = shape->gate == MOE_GATE_CHANNEL;
+    const bool by_token = shape->gate == MOE_GATE_TOKEN;
     // gradients of what the block does not have
     if ((dw_post && !post) || (dw_pre && !pre) || (dgate && shape->gate == MOE_GATE_NONE))
         return MOE_ERR_INVALID_ARG;

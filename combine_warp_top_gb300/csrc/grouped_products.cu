@@ -33,9 +33,9 @@
 // nearest, in a fixed order: 4e-7 whatever the length, for 6 to 11% of the time
 // of a long contraction.
 //
-// Roles per CTA (384 threads): warp 0 loads by TMA into 6 stages (9 in tiles of few rows); warp 1 owns TMEM
-// (two accumulators, one filled while the other is drained) and, in the leader,
-// issues the MMAs; warp 2 of the leader hands out tiles; warp 3 zeroes block ends
+// Roles per CTA (384 threads): warp 0 loads by TMA into 6 stages (9 in tiles of few rows);
+// warp 1 owns TMEM (two accumulators, one filled while the other is drained) and, in the
+// leader, issues the MMAs; warp 2 of the leader hands out tiles; warp 3 zeroes block ends
 // (weights' gradient); warps 4-11 drain the accumulators, two warps to each 32 rows
 // (128 columns each), with the registers that the others give up.  Every wait is
 // bounded.  6 stages of 32 KB and 32 KB of outgoing lines fill the shared memory; 5 and
@@ -264,7 +264,8 @@ __device__ __forceinline__ bool warp_next(Queues* c, int n, bool leader, volatil
     if (c->only) return false;
     int more = 0;
     if ((threadIdx.x & 31) == 0)
-        more = leader ? take(c, n - 1, true, 0, abort, err, t) : take_local(c, n - 1, abort, err, t);
+        more = leader ? take(c, n - 1, true, 0, abort, err, t)
+                      : take_local(c, n - 1, abort, err, t);
     if (!__shfl_sync(0xffffffffu, more, 0)) return false;
     t.e = __shfl_sync(0xffffffffu, t.e, 0);
     t.off = __shfl_sync(0xffffffffu, t.off, 0);
@@ -463,7 +464,8 @@ __device__ __forceinline__ void join_few(uint32_t ring, uint32_t rank, int split
     for (int r = (lane >> 3) * kSplits + split; r < 32 && r < f.rows; r += 4 * kSplits) {
         float4 v[kSplits];
 #pragma unroll
-        for (int p = 0; p < kSplits; ++p) v[p] = ld_cluster4(mapa_shared(at, 2 * p + rank) + r * 128);
+        for (int p = 0; p < kSplits; ++p)
+            v[p] = ld_cluster4(mapa_shared(at, 2 * p + rank) + r * 128);
 #pragma unroll
         for (int p = 1; p < kSplits; ++p) {
             v[0].x += v[p].x;
@@ -639,7 +641,8 @@ __device__ __forceinline__ void grouped_product(
         if (!kW) {
             for (int j = 0; j < per; ++j) {
                 if (lane * per + j < E) {
-                    segment(expert_offsets, expert_counts, lane * per + j, R, err, &run_off, &run_cnt);
+                    segment(expert_offsets, expert_counts, lane * per + j, R, err, &run_off,
+                            &run_cnt);
                     blocks_in += (run_cnt + kTileRows - 1) / kTileRows;
                 }
             }
@@ -1109,9 +1112,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            const int32_t* expert_counts, int E, int R, int K,
                            int m_out, int n_out, OutT* out, int accumulate,
                            int a_groups, int b_groups, int* err, int* tile_counter) {
-    grouped_product<kMode, OutT, kFew, false>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R, K,
-                                        m_out, n_out, out, accumulate, a_groups, b_groups, err,
-                                        tile_counter);
+    grouped_product<kMode, OutT, kFew, false>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R,
+                                              K, m_out, n_out, out, accumulate, a_groups, b_groups,
+                                              err, tile_counter);
 }
 // Launched with clusters of 2 * splits CTAs.
 template <int kMode, typename OutT, bool kFew>
@@ -1123,9 +1126,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  const int32_t* expert_counts, int E, int R, int K,
                                  int m_out, int n_out, OutT* out, int accumulate,
                                  int a_groups, int b_groups, int* err, int* tile_counter) {
-    grouped_product<kMode, OutT, kFew, true>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R, K,
-                                       m_out, n_out, out, accumulate, a_groups, b_groups, err,
-                                       tile_counter);
+    grouped_product<kMode, OutT, kFew, true>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R,
+                                             K, m_out, n_out, out, accumulate, a_groups, b_groups,
+                                             err, tile_counter);
 }
 
 // Clusters of 2 * splits CTAs that the device holds at once.
@@ -1236,8 +1239,8 @@ moe_status launch_rows(const uint16_t* rows, const GemmGroup& g, int c_in, int c
     const long long used = g.R < g.E ? g.R : g.E;  // experts with rows, at most
     const bool few = g.R <= kFewRows * used;
     const bool ok = map_rows(&a, rows, 0, g.R, K, few ? BF / 2 : BH) &&
-                    (input_grad ? map_mn(&b, w, g.E, c_out, c_in, few ? BH : box_columns(n_out, true),
-                                         &groups)
+                    (input_grad ? map_mn(&b, w, g.E, c_out, c_in,
+                                         few ? BH : box_columns(n_out, true), &groups)
                                 : map_rows(&b, w, g.E, c_out, c_in,
                                            few ? BH : box_columns(n_out, false))) &&
                     (few || map_lines(&o, out, 0, g.R, n_out, out_f32));
@@ -1270,10 +1273,11 @@ moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const Gemm
     const long long tiles =
         (long long)g.E * ((c_out + BT - 1) / BT) * ((c_in + BT - 1LL) / BT);
     const long long blocks = g.R / g.E / BK;  // of an expert, on average
-    return out_f32 ? launch<kWeightsGrad, float>(a, b, o, g, tiles, blocks, 0, c_out, c_in, dw, accumulate,
-                                                 a_groups, b_groups, st)
-                   : launch<kWeightsGrad, __nv_bfloat16>(a, b, o, g, tiles, blocks, 0, c_out, c_in, dw,
-                                                         accumulate, a_groups, b_groups, st);
+    const auto with = [&](auto launch) {
+        return launch(a, b, o, g, tiles, blocks, 0, c_out, c_in, dw, accumulate, a_groups, b_groups,
+                      st);
+    };
+    return out_f32 ? with(launch<kWeightsGrad, float>) : with(launch<kWeightsGrad, __nv_bfloat16>);
 }
 
 moe_status check_grouped(const moe_layout* layout, const moe_shape* shape, int32_t C_in,

@@ -223,7 +223,9 @@ moe_status moe_swiglu(const uint16_t* gu, const float* topk_w, const moe_layout*
     // lanes of a piece: a warp, or as many as a short row has vectors; vectors a lane:
     // the most that leave at most a fifth of the lanes idle in a row
     const int lanes = V <= 8 ? 8 : V <= 16 ? 16 : 32;
-    const auto wide = [V, lanes](int vecs) { return (V + lanes * vecs - 1) / (lanes * vecs) * vecs; };
+    const auto wide = [V, lanes](int vecs) {
+        return (V + lanes * vecs - 1) / (lanes * vecs) * vecs;
+    };
     const int vecs = wide(4) * 4 <= wide(1) * 5 ? 4 : wide(2) * 4 <= wide(1) * 5 ? 2 : 1;
     const int parts = (V + lanes * vecs - 1) / (lanes * vecs);
     const long long pieces = R * parts, groups = kBlock / lanes;
@@ -262,9 +264,9 @@ moe_status moe_swiglu_grad(const uint16_t* dh, const uint16_t* gu, const float* 
     // least 32 warps and a row is not long; long rows leave too few warps in the last
     // wave, so a block of 4 or 8 warps takes them, whichever idles less.
     return cuda_status(
-        V <= 8    ? go(swiglu_grad_kernel<8>, kBlock, kBlock / 8)
-        : V <= 16 ? go(swiglu_grad_kernel<16>, kBlock, kBlock / 16)
-        : V <= 512 && R >= 32LL * sm_count()         ? go(swiglu_grad_kernel<32>, kBlock, kBlock / 32)
+        V <= 8                                  ? go(swiglu_grad_kernel<8>, kBlock, kBlock / 8)
+        : V <= 16                               ? go(swiglu_grad_kernel<16>, kBlock, kBlock / 16)
+        : V <= 512 && R >= 32LL * sm_count()    ? go(swiglu_grad_kernel<32>, kBlock, kBlock / 32)
         : (V + 255) / 256 * 2 > (V + 127) / 128 ? go(swiglu_grad_kernel<128>, 128, 1)
                                                 : go(swiglu_grad_kernel<256>, 256, 1));
 }
