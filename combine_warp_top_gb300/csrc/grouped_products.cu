@@ -55,13 +55,13 @@
 //   with those fences and 64-byte lines, 288 us now; floor 253 us.
 // - A tile costs each role some 800 cycles to decode: the scheduler does it for all.
 // - A decoding step streams the weights: 16 tokens of 6 of 64 experts of 2816 x 2048,
-//   86 us for 586 MB, 6.8 TB/s, with the matrix as A and 64 rows as B (kFew); 97 us with
+//   87 us for 586 MB, 6.7 TB/s, with the matrix as A and 64 rows as B (kFew); 97 us with
 //   256 rows as A, whose MMAs take longer than the weights.
 // - Few tiles leave SMs idle: with a long contraction 2 or 4 pairs of a cluster share
 //   a tile's k-blocks, keep their sums in shared memory and add them up from there
 //   (4096 rows of one expert, 256 x 256 fp32 weights' gradient: 29 us with one pair,
 //   19 us with four; 1 row, 14336 x 3528 in tiles of few rows: 24 us with four).
-// - 64 tokens of 8 experts, 128 to 512: 5.0 us in a row of such calls; alone 5.2, of
+// - 64 tokens of 8 experts, 128 to 512: 5.2 us, of
 //   them 1.1 the experts' counts and the first tile, 0.4 the meeting of the CTAs, 0.9
 //   loads, 0.6 MMAs, 0.5 stores, 0.7 the end.
 #include <stddef.h>

@@ -18,7 +18,7 @@
 // The row is all zeros between tokens: only the k entries are put back.  With a warp for
 // every token the instructions for it (three sums over the lanes, the choices) take longer
 // than a short row's bytes.  32768 tokens, full softmax: of 256 experts 12.0 us (a warp each:
-// 13.4 us; the 69 MB take 10.2; kernels started early: 11.1), of 128 7.4 us (8.1), of 64 4.2
+// 13.4 us; the 69 MB take 10.2; back to back 10.8), of 128 7.4 us (8.1), of 64 4.2
 // us (7.9); softmax over the selected, of 64 3.5 us (5.5).  4096 of 64: 1.9 us, a launch.
 // The next token's loads a token ahead measured slower (15.9 us of 256).
 #include <math.h>

@@ -8,8 +8,8 @@
  * No call here uses atomics whose order could change a result: every output is
  * the same from run to run on one GPU model.
  * The kernels are launched with programmatic stream serialization: their blocks
- * may start while the kernel before them on the stream ends, and wait for it
- * before they touch memory.
+ * may start when those of the kernel before them on the stream are through, and
+ * wait for its writes before they touch memory.
  */
 #ifndef MOE_TRAIN_H
 #define MOE_TRAIN_H

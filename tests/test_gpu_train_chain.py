@@ -1,6 +1,6 @@
 """Calls one after the other on a stream, each reading what the one before has just written:
-a kernel's blocks may start while the kernel before it still runs, so the results have to be,
-bit for bit, those of calls that are waited for one by one."""
+a kernel's blocks may start before the writes of the kernel before it have landed, so the
+results have to be, bit for bit, those of calls that are waited for one by one."""
 import pytest
 import torch
 
