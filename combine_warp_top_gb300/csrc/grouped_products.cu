@@ -27,11 +27,14 @@
 // Precision: the tensor core adds into its fp32 accumulator with truncation,
 // which over a contraction of 4096 random bf16 products is a relative error of
 // 4e-6 (measured; 1e-6 over 1024, 2e-7 over 256; grows with the length), all of it
-// towards zero.  That is far below the rounding of a bf16 output, but not of an
-// fp32 one: fp32 outputs take at most kChainBlocks k-blocks (512 terms) into
-// one accumulator and add those partial sums in fp32 registers, rounding to
-// nearest, in a fixed order: 4e-7 whatever the length, for 6 to 11% of the time
-// of a long contraction.
+// towards zero; of terms of one sign it is 1.4e-9 a term (4.4e-5 over 32768, 1.2e-2
+// over 8 million).  So an accumulator takes at most kChainBlocks k-blocks, and those
+// partial sums are added in fp32 registers, rounding to nearest, in a fixed order.
+// fp32 outputs: 512 terms, 4e-7 whatever the length, for 6 to 11% of the time of a long
+// contraction.  bf16 outputs: 32768 terms, which lose a hundredth of the output's own
+// rounding (2^-8); a contraction of more than that takes as long as in one chain (16384
+// x 14336 x 4096 in chains of 4096 terms: 1158 us, in one 1161 us, side by side), and a
+// shorter one is one chain.
 //
 // Roles per CTA (384 threads): warp 0 loads by TMA into 6 stages (9 in tiles of few rows);
 // warp 1 owns TMEM (two accumulators, one filled while the other is drained) and, in the
@@ -100,7 +103,9 @@ template <bool kFew>
 constexpr int kStagesOf = kFew ? 9 : 6;
 constexpr int kAhead = 2;  // tiles the scheduler publishes ahead of the leader's producer
 constexpr int kStagingBytes = 32 * 128;  // an epilogue warp's output: 32 lines
-constexpr int kChainBlocks = 8;  // k-blocks added up in one accumulator (fp32 outputs)
+// k-blocks added up in one accumulator, see "Precision" above
+template <typename OutT>
+constexpr int kChainBlocks = sizeof(OutT) == 4 ? 8 : 512;
 
 // A tile: its expert (-1: no more tiles) and the expert's rows, its row and column
 // block, and the k-blocks of its contraction.  Decoded once by the scheduler and
@@ -504,7 +509,7 @@ __device__ __forceinline__ void grouped_product(
                                                     (size_t)kEpilogueWarps * kStagingBytes);
     volatile int* abort_flag = &ctl->abort;
 
-    constexpr bool kChained = sizeof(OutT) == 4;  // see kChainBlocks
+    constexpr int kChain = kChainBlocks<OutT>;
     constexpr bool kMnA = kW;                 // the contraction runs along tmA's rows
     constexpr bool kMnB = kMode != kForward;  // and along tmB's
     // readers of a slot of the leader's queue: its producer, MMA thread,
@@ -837,7 +842,7 @@ __device__ __forceinline__ void grouped_product(
                         phase ^= 1u;
                     }
                     ++in_chain;
-                    if ((kChained && in_chain == kChainBlocks) || kb == t.kblocks - 1) {
+                    if (in_chain == kChain || kb == t.kblocks - 1) {
                         umma_commit_pair_multicast(smem_u32(&ctl->tfull[acc]), pair_mask);
                         in_chain = 0;
                         if (++acc == kAccs) {
@@ -944,15 +949,17 @@ __device__ __forceinline__ void grouped_product(
                     acc_phase ^= 1u;
                 }
             };
-            const int chains = kChained ? (t.kblocks + kChainBlocks - 1) / kChainBlocks
-                                        : (t.kblocks > 0 ? 1 : 0);
-            // fp32 outputs: the partial sums before the last
-            uint32_t sum[kChained ? kCols / 32 : 1][32];
+            const int chains = (t.kblocks + kChain - 1) / kChain;
+            // the partial sums before the last, or all of them: with a line of 64 bf16
+            // columns beside them they would not fit the registers
+            constexpr bool kAllSummed = sizeof(OutT) == 2 && !kFew;
+            const int summed = chains > 1 ? chains - (kAllSummed ? 0 : 1) : 0;
+            uint32_t sum[kCols / 32][32];
             bool ok = true;
-            if (kChained && chains > 1) {
+            if (summed > 0) {
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) sum[c / 32][c % 32] = 0u;
-                for (int n = 0; ok && n < chains - 1; ++n) {
+                for (int n = 0; ok && n < summed; ++n) {
                     if (!ready()) {
                         ok = false;
                         break;
@@ -971,13 +978,13 @@ __device__ __forceinline__ void grouped_product(
                     release();
                 }
             }
-            if (!ok || (chains > 0 && !ready())) break;
+            if (!ok || (summed < chains && !ready())) break;
             if constexpr (kFew) {
                 uint32_t v[32];
                 tmem_ld32(part(), v);
                 tmem_wait_ld();
                 release();
-                if (kChained && chains > 1) {
+                if (chains > 1) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         v[j] = __float_as_uint(__uint_as_float(sum[0][j]) + __uint_as_float(v[j]));
@@ -1037,18 +1044,22 @@ __device__ __forceinline__ void grouped_product(
                                       n_out, rows, n_out - col - c);
                 }
             };
-            if (kChained && chains > 1) {
+            if (chains > 1) {
 #pragma unroll
                 for (int c = 0; c < kEpilogueCols; c += kLine) {
                     uint32_t v[kLine];
-                    tmem_ld_line(at + c, v);
-                    tmem_wait_ld();
+                    if constexpr (kAllSummed) {
 #pragma unroll
-                    for (int j = 0; j < kLine; ++j)
-                        v[j] = __float_as_uint(
-                            __uint_as_float(sum[kChained ? c / 32 : 0][j % 32]) +
-                            __uint_as_float(v[j]));
-                    if (c == kEpilogueCols - kLine) release();
+                        for (int j = 0; j < kLine; ++j) v[j] = sum[(c + j) / 32][j % 32];
+                    } else {
+                        tmem_ld_line(at + c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < kLine; ++j)
+                            v[j] = __float_as_uint(__uint_as_float(sum[c / 32][j % 32]) +
+                                                   __uint_as_float(v[j]));
+                        if (c == kEpilogueCols - kLine) release();
+                    }
                     put(c, v);
                 }
             } else {
