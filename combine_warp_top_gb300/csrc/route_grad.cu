@@ -7,7 +7,11 @@
 //   sigmoid, renormalised          dlogit[e_j] = s_j (1 - s_j) / S
 //                                                * (d_j - sum_i w_i d_i),
 //     s_j = sigmoid(logit[e_j]), S = sum_i s_i, w_j = s_j / S (the selection bias
-//     takes no part in the weights and has no gradient)
+//     takes no part in the weights and has no gradient).  The scores are taken times
+//     exp(-m), m = min(0, the largest selected logit), which leaves the weights as they
+//     are: s_j exp(-m) = exp(l_j - m) / (1 + exp(l_j)) for l_j <= 0, so that they do not
+//     all underflow where every selected logit is far below zero (fp32 scores are zero
+//     from -104 on, and 0 / 0 would be the weight).
 //
 // The selection itself is piecewise constant and passes no gradient, so outside
 // the full softmax the gradient is zero but for k entries a token.
@@ -20,7 +24,10 @@
 // than a short row's bytes.  32768 tokens, full softmax: of 256 experts 12.0 us (a warp each:
 // 13.4 us; the 69 MB take 10.2; back to back 10.8), of 128 7.4 us (8.1), of 64 4.2
 // us (7.9); softmax over the selected, of 64 3.5 us (5.5).  4096 of 64: 1.9 us, a launch.
+// Sigmoid, of 256 10.9 us, of 64 4.3: it writes as much as the softmax over the selected
+// (5.8 and 2.8 us beside it) and reads k logits a token from 32-byte sectors of their own.
 // The next token's loads a token ahead measured slower (15.9 us of 256).
+#include <float.h>
 #include <math.h>
 
 #include "../../include/moe_train.h"
@@ -91,12 +98,15 @@ __global__ void __launch_bounds__(32 * kWarps)
             if ((unsigned)id >= (unsigned)E) id = -1;
             d = dw[t * k + lane];
             if (kRouter == kSoftmax) x = in[t * k + lane];
-            if (kRouter == kSigmoid && id >= 0) {
-                const float l = in[t * E + id];
-                x = 1.0f / (1.0f + expf(-l));
-                rest = 1.0f / (1.0f + expf(l));
-            }
+            if (kRouter == kSigmoid && id >= 0) x = in[t * E + id];
             if (id < 0) x = d = 0.0f;
+        }
+        if (kRouter == kSigmoid) {
+            // (a lane without a choice takes no part in the maximum)
+            const float l = x, top = lanes_max<kLanes>(id < 0 ? -FLT_MAX : fmaxf(l, -FLT_MAX));
+            const float e = expf(-fabsf(l)), inv = 1.0f / (1.0f + e);
+            x = id < 0 ? 0.0f : l > 0.0f ? inv : expf(l - fminf(top, 0.0f)) * inv;
+            rest = l > 0.0f ? e * inv : inv;
         }
         float inv = 0.0f;
         if (kRouter == kFullSoftmax) {
@@ -113,7 +123,7 @@ __global__ void __launch_bounds__(32 * kWarps)
             inv = 1.0f / lanes_sum<kLanes>(sum);
         } else if (kRouter == kSigmoid) {
             const float total = lanes_sum<kLanes>(x);
-            const float w = x / total;
+            const float w = total == 0.0f ? 0.0f : x / total;  // 0: no choice of the token counts
             const float own = d - lanes_sum<kLanes>(w * d);
             d = own * w * rest;
         } else {
