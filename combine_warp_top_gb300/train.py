@@ -76,8 +76,8 @@ class MoETrainBlock:
         self.topk_w, self.dtopk_w = (torch.empty(N, k, **f32) for _ in range(2))
         self.ones = torch.ones(N, k, **f32)
         self.rstd_pre, self.rstd_post = (torch.empty(N, **f32) for _ in range(2))
-        self.out, self.d_stream = (torch.empty(N, H, **f32) for _ in range(2))
-        self.residual = None
+        # the residual stream as the block has taken it in, as it has left it, its gradient
+        self.stream, self.out, self.d_stream = (torch.empty(N, H, **f32) for _ in range(3))
         self.refresh()
 
     def refresh(self):
@@ -87,11 +87,12 @@ class MoETrainBlock:
 
     def forward(self, residual):
         """residual fp32 [N, H]; returns the next residual stream, fp32 [N, H] (a buffer
-        of the block, overwritten by the next call).  Keeps what backward() needs."""
+        of the block, overwritten by the next call).  Keeps what backward() needs of this
+        call, a copy of the residual among it, which the norm that reads it writes on its
+        way: the tensor given may be the block's own output, and may change afterwards."""
         s, p, lay, ws = self.shape, self.params, self.layout, self.ws
-        self.residual = residual
-        moe.moe_block_norm(None, residual, None, None, p["w_pre"], self.pre, None, self.x, None,
-                           self.rstd_pre)
+        moe.moe_block_norm(None, residual, None, None, p["w_pre"], self.pre, self.stream, self.x,
+                           None, self.rstd_pre)
         moe.moe_grouped_gemm(self.x, self.dense_layout, self.dense, self.w["w_router"].unsqueeze(0),
                              self.logits_all, self.dense_ws)
         self.logits.copy_(self.logits_all[:, :s.E])
@@ -102,7 +103,7 @@ class MoETrainBlock:
         moe.moe_swiglu(self.gu, self.topk_w, lay, s, self.h)
         moe.moe_grouped_gemm(self.h, lay, s, self.w["w_down"], self.y_rows, ws)
         moe.moe_combine(self.y_rows, self.ones, lay, s, None, None, self.y)
-        moe.moe_block_norm(self.y, residual, p["w_post"], p["gate"], None, self.post, self.out,
+        moe.moe_block_norm(self.y, self.stream, p["w_post"], p["gate"], None, self.post, self.out,
                            None, self.rstd_post)
         return self.out
 
@@ -111,7 +112,7 @@ class MoETrainBlock:
         the gradient of the residual stream, fp32 [N, H] (a buffer of the block)."""
         s, p, g, lay, ws = self.shape, self.params, self.grads, self.layout, self.ws
         acc = dict(accumulate=accumulate)
-        moe.moe_block_norm_grad(d_out, None, self.y, self.out, p["w_post"], p["gate"], None,
+        moe.moe_block_norm_grad(d_out, None, self.y, None, p["w_post"], p["gate"], None,
                                 self.rstd_post, None, self.post, self.dy, self.d_stream,
                                 g["w_post"], g["gate"], None, self.ws_post, **acc)
         # the combine's gradient: each row of an expert gets its token's
@@ -135,7 +136,7 @@ class MoETrainBlock:
                                         self.dense_ws)
         torch.add(self.dx_experts, self.dx_router, out=self.dx)
         # s of this norm is the residual itself, so its gradient adds to the stream's
-        moe.moe_block_norm_grad(self.d_stream, self.dx, None, self.residual, None, None,
+        moe.moe_block_norm_grad(self.d_stream, self.dx, None, self.stream, None, None,
                                 p["w_pre"], None, self.rstd_pre, self.pre, None, self.d_stream,
                                 None, None, g["w_pre"], self.ws_pre, **acc)
         return self.d_stream
