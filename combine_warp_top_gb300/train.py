@@ -64,7 +64,7 @@ class MoETrainBlock:
         self.dense_layout["expert_counts"].fill_(N)
         self.dense_layout["expert_offsets"].copy_(torch.tensor([0, N], dtype=torch.int32))
         self.ws, self.dense_ws = moe.workspace(s, device), moe.workspace(self.dense, device)
-        self.ws_pre, self.ws_post = moe.norm_workspace(self.pre), moe.norm_workspace(self.post)
+        self.ws_pre, self.ws_post = (moe.norm_workspace(n, device) for n in (self.pre, self.post))
         R = s.R
         self.x, self.y, self.dy, self.dx = (torch.empty(N, H, **bf) for _ in range(4))
         self.rows, self.y_rows, self.d_rows = (torch.empty(R, H, **bf) for _ in range(3))
