@@ -4,6 +4,8 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include <atomic>
+
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -81,6 +83,25 @@ struct NvtxRange {
     NvtxRange(const NvtxRange&) = delete;
     NvtxRange& operator=(const NvtxRange&) = delete;
 };
+
+// Whether what a call sets up once for each device (function attributes, figures kept
+// beside this) is set up.  Several host threads may make their first call together: each
+// of them then does the set-up, to the same end, and a thread that sees another's finish()
+// sees what that one has stored before.
+constexpr int kMaxDevices = 64;
+class OncePerDevice {
+  public:
+    bool done(int dev) const {
+        return dev < kMaxDevices && done_[dev].load(std::memory_order_acquire);
+    }
+    void finish(int dev) {
+        if (dev < kMaxDevices) done_[dev].store(true, std::memory_order_release);
+    }
+
+  private:
+    std::atomic<bool> done_[kMaxDevices] = {};
+};
+
 // Launches a kernel whose blocks call after_previous(), in clusters of `cluster` blocks
 // (0: as the kernel says).
 template <typename... P, typename... A>

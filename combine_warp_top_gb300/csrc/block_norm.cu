@@ -809,15 +809,15 @@ template <auto kKernel, typename Args>
 cudaError_t run(const Args& a, const Plan& p, cudaStream_t st) {
     if (p.smem > 40 * 1024) {  // with the static arrays, past the default 48 KB
         // the attribute holds for the process and device: set once for each
-        static bool set[64] = {false};
+        static OncePerDevice set;
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
-        if (dev >= 64 || !set[dev]) {
+        if (!set.done(dev)) {
             e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kMaxRing);
             if (e != cudaSuccess) return e;
-            if (dev < 64) set[dev] = true;
+            set.finish(dev);
         }
     }
     return launch_chained(kKernel, p.grid, p.block, p.smem, st, a);

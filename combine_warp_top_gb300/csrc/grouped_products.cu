@@ -1142,7 +1142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              err, tile_counter);
 }
 
-// Clusters of 2 * splits CTAs that the device holds at once.
+// Clusters of 2 * splits CTAs that the device holds at once; -1: the query failed.
 template <typename Kernel>
 int clusters_at_once(Kernel kernel, int splits, size_t smem) {
     cudaLaunchAttribute cluster[1];
@@ -1156,7 +1156,7 @@ int clusters_at_once(Kernel kernel, int splits, size_t smem) {
     cfg.attrs = cluster;
     cfg.numAttrs = 1;
     int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : -1;
 }
 
 template <int kMode, typename OutT, bool kFew = false>
@@ -1168,22 +1168,27 @@ moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap&
     // the attributes hold for the process and device: set once for each
     constexpr size_t smem = smem_bytes<kMode, kFew>();
     const auto split_kernel = grouped_product_split_kernel<kMode, OutT, kFew>;
-    static bool set[64] = {false};
-    static int at_once[64][2];  // clusters of 2 pairs and of 4
+    static OncePerDevice set;
+    static std::atomic<int> held[kMaxDevices][2];  // clusters of 2 pairs and of 4, on each device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-    if (dev >= 64) return MOE_ERR_UNSUPPORTED;
-    if (!set[dev]) {
+    if (dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
+    if (!set.done(dev)) {
         if (cudaFuncSetAttribute(grouped_product_kernel<kMode, OutT, kFew>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem) != cudaSuccess ||
             cudaFuncSetAttribute(split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem) != cudaSuccess)
             return MOE_ERR_CUDA;
-        at_once[dev][0] = clusters_at_once(split_kernel, 2, smem);
-        at_once[dev][1] = clusters_at_once(split_kernel, kMaxSplits, smem);
-        set[dev] = true;
+        const int two = clusters_at_once(split_kernel, 2, smem);
+        const int four = clusters_at_once(split_kernel, kMaxSplits, smem);
+        if (two < 0 || four < 0) return MOE_ERR_CUDA;
+        held[dev][0].store(two, std::memory_order_relaxed);
+        held[dev][1].store(four, std::memory_order_relaxed);
+        set.finish(dev);
     }
+    const int at_once[2] = {held[dev][0].load(std::memory_order_relaxed),
+                            held[dev][1].load(std::memory_order_relaxed)};
     // Pairs that share a tile's contraction: as long as all clusters run side by side, and
     // what a pair no longer has to do, some 0.3 us a k-block, is more than what the
     // joining of the sums takes: 1 us for a few rows, 6 us for a tile's 256 (1 row, 4096 x
@@ -1192,9 +1197,9 @@ moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap&
     const long long m = kMode == kWeightsGrad ? m_out : kFew ? 0 : g.R;
     const long long join_blocks = 4 + 16 * (m < BT ? m : BT) / BT;
     int splits = 1;
-    if (tiles <= at_once[dev][1] && blocks * 3 > join_blocks * 4)
+    if (tiles <= at_once[1] && blocks * 3 > join_blocks * 4)
         splits = kMaxSplits;
-    else if (tiles <= at_once[dev][0] && blocks > join_blocks * 2)
+    else if (tiles <= at_once[0] && blocks > join_blocks * 2)
         splits = 2;
     if (splits > 1)
         return cuda_status(launch_chained_clusters(
