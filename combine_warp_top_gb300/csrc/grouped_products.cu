@@ -168,6 +168,12 @@ constexpr size_t smem_bytes() {
     return n;
 }
 
+// Limit of a wait that lasts as long as a tile's contraction does: a k-block takes some 500
+// cycles, so 4 million of them are past kWaitLimit by themselves.
+__device__ __forceinline__ long long tile_limit(int kblocks) {
+    return kWaitLimit + 2048LL * kblocks;
+}
+
 // Spin for about `cycles` SM clocks (lets copies in flight land on abort).
 __device__ __forceinline__ void spin(long long cycles) {
     const long long t0 = clock64();
@@ -859,6 +865,7 @@ __device__ __forceinline__ void grouped_product(
             // The counter hands out the tiles after the pairs' first ones.  Tile i of the
             // queue is published once the producer has taken tile i - kAhead.
             const int pairs = (int)(gridDim.x / 2);
+            int longest = ctl->first.kblocks;  // of the tiles handed out
             for (int i = 0;; ++i) {
                 int tile = -1;
                 if (lane == 0) {
@@ -866,13 +873,14 @@ __device__ __forceinline__ void grouped_product(
                     if (i >= kAhead) {
                         const int j = i - kAhead;
                         ok = wait_bar(smem_u32(&ctl->q_taken[j % kQ]), (uint32_t)(j / kQ) & 1u,
-                                      abort_flag, err);
+                                      abort_flag, err, tile_limit(longest));
                     }
                     if (ok) tile = pairs + atomicAdd(tile_counter, 1);
                 }
                 tile = __shfl_sync(0xffffffffu, tile, 0);
                 if (tile < 0) break;
                 const Tile t = decode(tile);
+                longest = t.kblocks > longest ? t.kblocks : longest;
                 int more = 0;
                 if (lane == 0) more = publish(ctl, i, t, first, abort_flag, err) && t.e >= 0;
                 if (!__shfl_sync(0xffffffffu, more, 0)) break;
@@ -893,7 +901,7 @@ __device__ __forceinline__ void grouped_product(
                 int landed = 0;
                 if (lane == 0)
                     landed = wait_bar(smem_u32(&ctl->land[last]), (land_phase >> last) & 1u,
-                                      abort_flag, err);
+                                      abort_flag, err, tile_limit(t.kblocks));
                 landed = __shfl_sync(0xffffffffu, landed, 0);
                 if (!landed) break;
                 land_phase ^= 1u << last;

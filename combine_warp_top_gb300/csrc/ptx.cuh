@@ -44,15 +44,15 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Bounded wait.  Gives up when another role has aborted, or after kWaitLimit
+// Bounded wait.  Gives up when another role has aborted, or after `limit`
 // cycles, in which case it records the timeout and raises the abort flag.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort,
-                                         int* err) {
+                                         int* err, long long limit = kWaitLimit) {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (!mbar_try_wait(bar, parity)) {
         if (*abort) return false;
-        if (clock64() - t0 > kWaitLimit) {
+        if (clock64() - t0 > limit) {
             *abort = 1;
             set_error(err, MOE_ERR_TIMEOUT);
             return false;
