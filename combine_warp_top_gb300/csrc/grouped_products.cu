@@ -168,6 +168,11 @@ constexpr size_t smem_bytes() {
     return n;
 }
 
+// Blocks of `size` that n takes: widths go up to 2^31 - 8, where n + size - 1 is no int.
+__host__ __device__ __forceinline__ int blocks_of(int n, int size) {
+    return (int)(((unsigned)n + (unsigned)size - 1u) / (unsigned)size);
+}
+
 // Limit of a wait that lasts as long as a tile's contraction does: a k-block takes some 500
 // cycles, so 4 million of them are past kWaitLimit by themselves.
 __device__ __forceinline__ long long tile_limit(int kblocks) {
@@ -531,9 +536,9 @@ __device__ __forceinline__ void grouped_product(
     const int splits = kSplit ? (int)(cluster_ctas() >> 1) : 1;
     const uint16_t pair_mask = (uint16_t)(0x3u << first), leader_mask = (uint16_t)(0x1u << first);
     const bool leader = rank == 0;
-    const int MB = (m_out + BT - 1) / BT;
-    const int NB = (n_out + BT - 1) / BT;
-    const int KB = (K + BK - 1) / BK;
+    const int MB = blocks_of(m_out, BT);
+    const int NB = blocks_of(n_out, BT);
+    const int KB = blocks_of(K, BK);
     const int n_last = kFew ? BT : last_columns(n_out, kMnB && b_groups);
 
     // one or two barriers a thread, not 63 and more of them one after the other
@@ -604,7 +609,7 @@ __device__ __forceinline__ void grouped_product(
             last_e = t.e;
             t.off = last_off;
             t.cnt = last_cnt;
-            t.kblocks = (t.cnt + BK - 1) / BK;
+            t.kblocks = blocks_of(t.cnt, BK);
         } else {
             // the run of experts that holds row block q, then the expert
             const int q = tile / NB;
@@ -617,7 +622,7 @@ __device__ __forceinline__ void grouped_product(
                 if (lane < per && mine < E)
                     segment(expert_offsets, expert_counts, mine, R, err, &o, &c);
             }
-            const int b = (c + kTileRows - 1) / kTileRows, end = before + warp_prefix(b);
+            const int b = blocks_of(c, kTileRows), end = before + warp_prefix(b);
             const int k = __ffs(__ballot_sync(0xffffffffu, end > q)) - 1;
             const int MBe = __shfl_sync(0xffffffffu, b, k);
             const int local = tile - NB * (__shfl_sync(0xffffffffu, end, k) - MBe);
@@ -654,7 +659,7 @@ __device__ __forceinline__ void grouped_product(
                 if (lane * per + j < E) {
                     segment(expert_offsets, expert_counts, lane * per + j, R, err, &run_off,
                             &run_cnt);
-                    blocks_in += (run_cnt + kTileRows - 1) / kTileRows;
+                    blocks_in += blocks_of(run_cnt, kTileRows);
                 }
             }
             // Only a layout whose segments overlap has more blocks than R rows can fill: it
@@ -1271,8 +1276,8 @@ moe_status launch_rows(const uint16_t* rows, const GemmGroup& g, int c_in, int c
     if (!ok) return MOE_ERR_UNSUPPORTED;
     if (few) o = a;  // not used
     // at most as many row blocks as experts with rows and whole blocks besides
-    const long long tiles = (used + (g.R - used) / (few ? BF : BT)) * ((n_out + BT - 1LL) / BT);
-    const long long blocks = (K + BK - 1LL) / BK;
+    const long long tiles = (used + (g.R - used) / (few ? BF : BT)) * blocks_of(n_out, BT);
+    const long long blocks = blocks_of(K, BK);
     using bf16 = __nv_bfloat16;
     const auto with = [&](auto launch) {
         return launch(a, b, o, g, tiles, blocks, K, 0, n_out, out, false, 0, groups, st);
@@ -1295,7 +1300,7 @@ moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const Gemm
         !map_lines(&o, dw, g.E, c_out, c_in, out_f32))
         return MOE_ERR_UNSUPPORTED;
     const long long tiles =
-        (long long)g.E * ((c_out + BT - 1) / BT) * ((c_in + BT - 1LL) / BT);
+        (long long)g.E * blocks_of(c_out, BT) * blocks_of(c_in, BT);
     const long long blocks = g.R / g.E / BK;  // of an expert, on average
     const auto with = [&](auto launch) {
         return launch(a, b, o, g, tiles, blocks, 0, c_out, c_in, dw, accumulate, a_groups, b_groups,
@@ -1311,6 +1316,8 @@ moe_status check_grouped(const moe_layout* layout, const moe_shape* shape, int32
     MOE_TRY(check_ws(shape, ws, ws_bytes));
     if (C_in <= 0 || C_out <= 0) return MOE_ERR_INVALID_ARG;
     if (C_in % 8 != 0 || C_out % 8 != 0) return MOE_ERR_UNSUPPORTED;
+    // a row block's coordinates, past the last row included, are 32 bits
+    if ((long long)shape->N * shape->k > INT32_MAX - (1 << 20)) return MOE_ERR_UNSUPPORTED;
     if (out_type != MOE_TYPE_BF16 && out_type != MOE_TYPE_F32) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }

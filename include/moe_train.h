@@ -36,8 +36,8 @@ typedef enum {
  *                                               dout[i, :]^T rows[i, :]
  * rows bf16 [N*k, C_in], dout bf16 [N*k, C_out], w bf16 [E, C_out, C_in]; out
  * [N*k, C_out], drows [N*k, C_in] and dw [E, C_out, C_in] of out_type, a
- * moe_type.  C_in and C_out are multiples of 8; shape gives N, k and E (its H
- * and I are not read).  Products are bf16 with fp32 accumulation on the tensor
+ * moe_type.  C_in and C_out are multiples of 8, N*k is less than 2^31 - 2^20
+ * (MOE_ERR_UNSUPPORTED); shape gives N, k and E (its H and I are not read).  Products are bf16 with fp32 accumulation on the tensor
  * cores; an fp32 output is summed from partial sums of 512 terms, added in
  * order and rounded to nearest.  A row's values touch no other row's and no
  * other expert's output.
