@@ -1314,6 +1314,7 @@ moe_status check_grouped(const moe_layout* layout, const moe_shape* shape, int32
     MOE_TRY(check_shape(shape));
     MOE_TRY(check_layout(layout, shape));
     MOE_TRY(check_ws(shape, ws, ws_bytes));
+    if (((uintptr_t)ws & 3u) != 0) return MOE_ERR_INVALID_ARG;  // its words are counted in
     if (C_in <= 0 || C_out <= 0) return MOE_ERR_INVALID_ARG;
     if (C_in % 8 != 0 || C_out % 8 != 0) return MOE_ERR_UNSUPPORTED;
     // a row block's coordinates, past the last row included, are 32 bits

@@ -47,7 +47,7 @@ typedef enum {
  * Where there are few tiles for the device's SMs, several of them share a long
  * contraction and add up their fp32 sums in a fixed order; how many depends on N*k,
  * E, C_in and C_out (and the device) only.
- * ws: workspace of moe_workspace_bytes(shape) bytes.  A layout whose segments
+ * ws: workspace of moe_workspace_bytes(shape) bytes, on a 4-byte boundary.  A layout whose segments
  * leave the N*k rows is reported there (moe_get_error) and those segments are
  * taken as empty; segments that overlap may be reported, too. */
 moe_status moe_grouped_gemm(const uint16_t* rows, const moe_layout* layout,

@@ -34,3 +34,10 @@ def test_more_rows_than_their_blocks_can_be_counted(lib, N, k):
     assert all(status == UNSUPPORTED for status in calls(lib, shape, rows=None))
     shape = moe.Shape((2 ** 31 - 2 ** 20 - 1) // k, 64, 8, k, 2, 64)
     assert all(status == INVALID for status in calls(lib, shape, rows=None))
+
+
+def test_workspace_off_its_words(lib):
+    """The tile counters and the error word are 32-bit atomics."""
+    shape = moe.Shape(64, 64, 8, 2, 2, 64)
+    for at in (0x10001, 0x10002, 0x10003):
+        assert all(status == INVALID for status in calls(lib, shape, ws=ctypes.c_void_p(at)))
