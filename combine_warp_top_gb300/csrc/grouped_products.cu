@@ -442,9 +442,6 @@ __device__ __forceinline__ void join_parts(uint32_t ring, uint32_t rank, int spl
     }
 }
 
-// kMode, and for kWeightsGrad K unused, m_out x n_out = C_out x C_in; otherwise
-// K the contraction and n_out the columns of out.  a_groups, b_groups: the map of an
-// MN-major operand has its groups of 64 columns as a dimension.
 // Tiles of few rows: a warp's sums are 32 columns of the output (its TMEM lanes) by 32
 // rows, and leave by way of 32 lines of 128 bytes in shared memory, one a row.  One with
 // its pair's share of the contraction only has its lines in the ring instead.
@@ -501,6 +498,9 @@ __device__ __forceinline__ void join_few(uint32_t ring, uint32_t rank, int split
 // each: 13.5 us (14.6 us).
 // kSplit: a cluster of several pairs has one tile, each pair a share of its
 // contraction, and the pairs' sums are joined at the end.
+// kWeightsGrad: K unused, m_out x n_out = C_out x C_in; otherwise K the contraction and
+// n_out the columns of out.  a_groups, b_groups: the map of an MN-major operand has its
+// groups of 64 columns as a dimension.
 template <int kMode, typename OutT, bool kFew, bool kSplit>
 __device__ __forceinline__ void grouped_product(
     const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmOut,

@@ -46,8 +46,11 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// exp and divide of the hardware: about 1e-6 relative, far below bf16's 4e-3
-// (and the routing weight's sum of many such terms averages it further down)
+// exp and divide of the hardware.  The exponential is good to 2 + 1.2 |g| units of 2^-23
+// (CUDA's bound): 2e-6 relative at |g| = 12, 1.2e-5 at 85, against the 4e-3 of a bf16 output.
+// The routing weight's gradient is an fp32 sum of such terms, a row's, and is as good as
+// the largest of them, which are those of gates near zero and above, where s is off by
+// exp(-g) of that.  Below g = -87.3 the quotient is 0, which is off by less than 2^-126.
 __device__ __forceinline__ float sigmoid(float g) {
     return __fdividef(1.0f, 1.0f + __expf(-g));
 }

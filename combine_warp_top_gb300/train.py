@@ -29,6 +29,13 @@ class MoETrainBlock:
     first), w_down [E, H, I], w_pre, w_post, gate [H]; grads: the same, filled by
     backward() (added to when accumulate=True).  The expert and router products run
     on bf16 copies made by refresh(), which a step calls after it has changed params.
+
+    What is rounded to bf16 on the way: every operand of a product, the router's
+    matrix and its logits' gradient among them, for the tensor cores take no more (the
+    logits themselves, the routing weights, all parameters' gradients and the residual
+    stream with its gradient stay fp32); and the two parts of dx and their sum, the
+    experts' and the router's, because the norm before the block takes its dx in bf16, as
+    it gives x.  Each is 2^-8 at most, as at the block's other activations.
     """
 
     def __init__(self, N, H, E, k, I, residual_scale=1.0, eps=1e-6, seed=0, device="cuda"):

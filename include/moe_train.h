@@ -37,19 +37,20 @@ typedef enum {
  * rows bf16 [N*k, C_in], dout bf16 [N*k, C_out], w bf16 [E, C_out, C_in]; out
  * [N*k, C_out], drows [N*k, C_in] and dw [E, C_out, C_in] of out_type, a
  * moe_type.  C_in and C_out are multiples of 8, N*k is less than 2^31 - 2^20
- * (MOE_ERR_UNSUPPORTED); shape gives N, k and E (its H and I are not read).  Products are bf16 with fp32 accumulation on the tensor
- * cores; an fp32 output is summed from partial sums of 512 terms, added in
- * order and rounded to nearest.  A row's values touch no other row's and no
- * other expert's output.
+ * (MOE_ERR_UNSUPPORTED).  shape gives N, k and E; it has to be one that the calls
+ * of moe.h take, but its other fields size nothing here.  Products are bf16 with
+ * fp32 accumulation on the tensor cores: an output is summed from partial sums of
+ * 512 terms (fp32) or 32768 (bf16), added in order and rounded to nearest.  A row's
+ * values touch no other row's and no other expert's output.
  * accumulate != 0 adds to dw, which has to be fp32 then (MOE_ERR_UNSUPPORTED
  * otherwise); accumulate == 0 overwrites it, with zeros for an expert without
  * rows (and for every expert when N == 0).
  * Where there are few tiles for the device's SMs, several of them share a long
  * contraction and add up their fp32 sums in a fixed order; how many depends on N*k,
  * E, C_in and C_out (and the device) only.
- * ws: workspace of moe_workspace_bytes(shape) bytes, on a 4-byte boundary.  A layout whose segments
- * leave the N*k rows is reported there (moe_get_error) and those segments are
- * taken as empty; segments that overlap may be reported, too. */
+ * ws: workspace of moe_workspace_bytes(shape) bytes, on a 4-byte boundary.  A layout
+ * whose segments leave the N*k rows is reported there (moe_get_error) and those
+ * segments are taken as empty; segments that overlap may be reported, too. */
 moe_status moe_grouped_gemm(const uint16_t* rows, const moe_layout* layout,
                             const moe_shape* shape, int32_t C_in, int32_t C_out,
                             const uint16_t* w, void* out, int32_t out_type, void* ws,
@@ -92,7 +93,9 @@ moe_status moe_swiglu_grad(const uint16_t* dh, const uint16_t* gu, const float* 
  *                                selection only and has no gradient)
  * The selection passes no gradient: outside the full softmax the entries of the
  * experts not selected are zero (written, not left).  Ids out of range take no
- * part.  Only moe_shape's N, E and k are read. */
+ * part.  Of the shape, which has to be one that the calls of moe.h take, N, E and k
+ * are used.  The sigmoid router's gradient is finite for any finite logits, also where
+ * the selected scores are all too small for fp32. */
 moe_status moe_route_grad(const int32_t* topk_ids, const float* topk_w, const float* dtopk_w,
                           const moe_shape* shape, float* dlogits, void* stream);
 moe_status moe_route_full_softmax_grad(const float* logits, const int32_t* topk_ids,
