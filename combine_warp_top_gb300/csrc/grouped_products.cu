@@ -32,9 +32,8 @@
 // partial sums are added in fp32 registers, rounding to nearest, in a fixed order.
 // fp32 outputs: 512 terms, 4e-7 whatever the length, for 6 to 11% of the time of a long
 // contraction.  bf16 outputs: 32768 terms, which lose a hundredth of the output's own
-// rounding (2^-8); a contraction of more than that takes as long as in one chain (16384
-// x 14336 x 4096 in chains of 4096 terms: 1158 us, in one 1161 us, side by side), and a
-// shorter one is one chain.
+// rounding (2^-8); a shorter contraction is one chain.  262144 skewed rows' weights'
+// gradient with the code for it: 2064 us, without 2050.
 //
 // Roles per CTA (384 threads): warp 0 loads by TMA into 6 stages (9 in tiles of few rows);
 // warp 1 owns TMEM (two accumulators, one filled while the other is drained) and, in the
@@ -501,7 +500,8 @@ __device__ __forceinline__ void join_few(uint32_t ring, uint32_t rank, int split
 // kWeightsGrad: K unused, m_out x n_out = C_out x C_in; otherwise K the contraction and
 // n_out the columns of out.  a_groups, b_groups: the map of an MN-major operand has its
 // groups of 64 columns as a dimension.
-template <int kMode, typename OutT, bool kFew, bool kSplit>
+// kLong (bf16 outputs in tiles of 256 rows): a contraction may take more than one chain.
+template <int kMode, typename OutT, bool kFew, bool kSplit, bool kLong>
 __device__ __forceinline__ void grouped_product(
     const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmOut,
     const int32_t* expert_offsets, const int32_t* expert_counts, int E,
@@ -521,6 +521,10 @@ __device__ __forceinline__ void grouped_product(
     volatile int* abort_flag = &ctl->abort;
 
     constexpr int kChain = kChainBlocks<OutT>;
+    // the partial sums before the last are added to it in registers; else (kLong) in TMEM:
+    // beside a line of 64 bf16 columns 128 sums would not fit the registers
+    constexpr bool kSums = sizeof(OutT) == 4 || kFew;
+    static_assert(!kSums || !kLong, "these take any length");
     constexpr bool kMnA = kW;                 // the contraction runs along tmA's rows
     constexpr bool kMnB = kMode != kForward;  // and along tmB's
     // readers of a slot of the leader's queue: its producer, MMA thread,
@@ -853,7 +857,7 @@ __device__ __forceinline__ void grouped_product(
                         phase ^= 1u;
                     }
                     ++in_chain;
-                    if (in_chain == kChain || kb == t.kblocks - 1) {
+                    if (((kSums || kLong) && in_chain == kChain) || kb == t.kblocks - 1) {
                         umma_commit_pair_multicast(smem_u32(&ctl->tfull[acc]), pair_mask);
                         in_chain = 0;
                         if (++acc == kAccs) {
@@ -962,17 +966,14 @@ __device__ __forceinline__ void grouped_product(
                     acc_phase ^= 1u;
                 }
             };
-            const int chains = (t.kblocks + kChain - 1) / kChain;
-            // the partial sums before the last, or all of them: with a line of 64 bf16
-            // columns beside them they would not fit the registers
-            constexpr bool kAllSummed = sizeof(OutT) == 2 && !kFew;
-            const int summed = chains > 1 ? chains - (kAllSummed ? 0 : 1) : 0;
-            uint32_t sum[kCols / 32][32];
+            const int chains = kSums ? (t.kblocks + kChain - 1) / kChain
+                                     : (t.kblocks > 0 ? 1 : 0);
+            uint32_t sum[kSums ? kCols / 32 : 1][32];
             bool ok = true;
-            if (summed > 0) {
+            if (kSums && chains > 1) {
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) sum[c / 32][c % 32] = 0u;
-                for (int n = 0; ok && n < summed; ++n) {
+                for (int n = 0; ok && n < chains - 1; ++n) {
                     if (!ready()) {
                         ok = false;
                         break;
@@ -991,13 +992,48 @@ __device__ __forceinline__ void grouped_product(
                     release();
                 }
             }
-            if (!ok || (summed < chains && !ready())) break;
+            if (!ok || (chains > 0 && !ready())) break;
+            if constexpr (kLong) {
+                // adds the chains before the last to it, where the lines below read it
+                if (t.kblocks > kChain) {
+                    uint32_t before[kCols / 32][32] = {};
+                    for (int k = t.kblocks; ok && k > kChain; k -= kChain) {
+                        const uint32_t from = part();
+#pragma unroll
+                        for (int c = 0; c < kCols / 32; ++c) {
+                            uint32_t v[32];
+                            tmem_ld32(from + c * 32, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                before[c][j] = __float_as_uint(__uint_as_float(before[c][j]) +
+                                                               __uint_as_float(v[j]));
+                        }
+                        release();
+                        ok = ready();
+                    }
+                    if (!ok) break;
+                    const uint32_t last = part();
+#pragma unroll
+                    for (int c = 0; c < kCols / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(last + c * 32, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = __float_as_uint(__uint_as_float(before[c][j]) +
+                                                   __uint_as_float(v[j]));
+                        tmem_st32(last + c * 32, v);
+                    }
+                    tmem_wait_st();
+                }
+            }
             if constexpr (kFew) {
                 uint32_t v[32];
                 tmem_ld32(part(), v);
                 tmem_wait_ld();
                 release();
-                if (chains > 1) {
+                if (kSums && chains > 1) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         v[j] = __float_as_uint(__uint_as_float(sum[0][j]) + __uint_as_float(v[j]));
@@ -1057,22 +1093,18 @@ __device__ __forceinline__ void grouped_product(
                                       n_out, rows, n_out - col - c);
                 }
             };
-            if (chains > 1) {
+            if (kSums && chains > 1) {
 #pragma unroll
                 for (int c = 0; c < kEpilogueCols; c += kLine) {
                     uint32_t v[kLine];
-                    if constexpr (kAllSummed) {
+                    tmem_ld_line(at + c, v);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < kLine; ++j) v[j] = sum[(c + j) / 32][j % 32];
-                    } else {
-                        tmem_ld_line(at + c, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < kLine; ++j)
-                            v[j] = __float_as_uint(__uint_as_float(sum[c / 32][j % 32]) +
-                                                   __uint_as_float(v[j]));
-                        if (c == kEpilogueCols - kLine) release();
-                    }
+                    for (int j = 0; j < kLine; ++j)
+                        v[j] = __float_as_uint(
+                            __uint_as_float(sum[kSums ? c / 32 : 0][j % 32]) +
+                            __uint_as_float(v[j]));
+                    if (c == kEpilogueCols - kLine) release();
                     put(c, v);
                 }
             } else {
@@ -1127,7 +1159,7 @@ __device__ __forceinline__ void grouped_product(
     }
 }
 
-template <int kMode, typename OutT, bool kFew>
+template <int kMode, typename OutT, bool kFew, bool kLong>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_product_kernel(const __grid_constant__ CUtensorMap tmA,
                            const __grid_constant__ CUtensorMap tmB,
@@ -1136,12 +1168,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            const int32_t* expert_counts, int E, int R, int K,
                            int m_out, int n_out, OutT* out, int accumulate,
                            int a_groups, int b_groups, int* err, int* tile_counter) {
-    grouped_product<kMode, OutT, kFew, false>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R,
-                                              K, m_out, n_out, out, accumulate, a_groups, b_groups,
-                                              err, tile_counter);
+    grouped_product<kMode, OutT, kFew, false, kLong>(tmA, tmB, tmOut, expert_offsets, expert_counts,
+                                                     E, R, K, m_out, n_out, out, accumulate,
+                                                     a_groups, b_groups, err, tile_counter);
 }
 // Launched with clusters of 2 * splits CTAs.
-template <int kMode, typename OutT, bool kFew>
+template <int kMode, typename OutT, bool kFew, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_product_split_kernel(const __grid_constant__ CUtensorMap tmA,
                                  const __grid_constant__ CUtensorMap tmB,
@@ -1150,9 +1182,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  const int32_t* expert_counts, int E, int R, int K,
                                  int m_out, int n_out, OutT* out, int accumulate,
                                  int a_groups, int b_groups, int* err, int* tile_counter) {
-    grouped_product<kMode, OutT, kFew, true>(tmA, tmB, tmOut, expert_offsets, expert_counts, E, R,
-                                             K, m_out, n_out, out, accumulate, a_groups, b_groups,
-                                             err, tile_counter);
+    grouped_product<kMode, OutT, kFew, true, kLong>(tmA, tmB, tmOut, expert_offsets, expert_counts, E,
+                                                    R, K, m_out, n_out, out, accumulate, a_groups,
+                                                    b_groups, err, tile_counter);
 }
 
 // Clusters of 2 * splits CTAs that the device holds at once; -1: the query failed.
@@ -1172,22 +1204,22 @@ int clusters_at_once(Kernel kernel, int splits, size_t smem) {
     return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : -1;
 }
 
-template <int kMode, typename OutT, bool kFew = false>
-moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+template <int kMode, typename OutT, bool kFew, bool kLong>
+moe_status launch_form(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
                   const GemmGroup& g, long long tiles, long long blocks,
                   int K, int m_out, int n_out, void* out, bool accumulate, int a_groups,
                   int b_groups, cudaStream_t st) {
     if (tiles >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
     // the attributes hold for the process and device: set once for each
     constexpr size_t smem = smem_bytes<kMode, kFew>();
-    const auto split_kernel = grouped_product_split_kernel<kMode, OutT, kFew>;
+    const auto split_kernel = grouped_product_split_kernel<kMode, OutT, kFew, kLong>;
     static OncePerDevice set;
     static std::atomic<int> held[kMaxDevices][2];  // clusters of 2 pairs and of 4, on each device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
     if (dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
     if (!set.done(dev)) {
-        if (cudaFuncSetAttribute(grouped_product_kernel<kMode, OutT, kFew>,
+        if (cudaFuncSetAttribute(grouped_product_kernel<kMode, OutT, kFew, kLong>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem) != cudaSuccess ||
             cudaFuncSetAttribute(split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1222,10 +1254,29 @@ moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap&
     const long long pairs_max = sm_count() / 2;
     const long long pairs = tiles < pairs_max ? tiles : pairs_max;
     return cuda_status(launch_chained(
-        grouped_product_kernel<kMode, OutT, kFew>, (int)(2 * (pairs > 0 ? pairs : 1)), kThreads,
+        grouped_product_kernel<kMode, OutT, kFew, kLong>, (int)(2 * (pairs > 0 ? pairs : 1)), kThreads,
         smem, st, a, b, o, g.offsets, g.counts, g.E, (int)g.R, K, m_out, n_out,
         reinterpret_cast<OutT*>(out), accumulate ? 1 : 0, a_groups, b_groups, g.err,
         g.prefix + g.E + 1));
+}
+
+// terms: the longest contraction that there may be.
+template <int kMode, typename OutT, bool kFew = false>
+moe_status launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+                  const GemmGroup& g, long long tiles, long long blocks, long long terms,
+                  int K, int m_out, int n_out, void* out, bool accumulate, int a_groups,
+                  int b_groups, cudaStream_t st) {
+    const auto with = [&](auto form) {
+        return form(a, b, o, g, tiles, blocks, K, m_out, n_out, out, accumulate, a_groups, b_groups,
+                    st);
+    };
+    // bf16 outputs of what is surely one chain go without the code for more: 800 rows of 8
+    // experts, 512 x 512, 7.9 us, 8.3 us with it
+    if constexpr (sizeof(OutT) == 2 && !kFew) {
+        if (terms > (long long)kChainBlocks<OutT> * BK)
+            return with(launch_form<kMode, OutT, kFew, true>);
+    }
+    return with(launch_form<kMode, OutT, kFew, false>);
 }
 
 // A [outer, rows, cols] matrix (outer 0: [rows, cols]) in boxes of 64 columns.
@@ -1280,7 +1331,7 @@ moe_status launch_rows(const uint16_t* rows, const GemmGroup& g, int c_in, int c
     const long long blocks = blocks_of(K, BK);
     using bf16 = __nv_bfloat16;
     const auto with = [&](auto launch) {
-        return launch(a, b, o, g, tiles, blocks, K, 0, n_out, out, false, 0, groups, st);
+        return launch(a, b, o, g, tiles, blocks, K, K, 0, n_out, out, false, 0, groups, st);
     };
     if (few)
         return input_grad ? (out_f32 ? with(launch<kRowsGrad, float, true>)
@@ -1303,8 +1354,8 @@ moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const Gemm
         (long long)g.E * blocks_of(c_out, BT) * blocks_of(c_in, BT);
     const long long blocks = g.R / g.E / BK;  // of an expert, on average
     const auto with = [&](auto launch) {
-        return launch(a, b, o, g, tiles, blocks, 0, c_out, c_in, dw, accumulate, a_groups, b_groups,
-                      st);
+        return launch(a, b, o, g, tiles, blocks, g.R, 0, c_out, c_in, dw, accumulate, a_groups,
+                      b_groups, st);
     };
     return out_f32 ? with(launch<kWeightsGrad, float>) : with(launch<kWeightsGrad, __nv_bfloat16>);
 }
