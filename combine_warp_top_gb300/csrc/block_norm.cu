@@ -21,7 +21,10 @@
 // keeps its columns over many rows, so per-channel vectors and column sums stay in
 // registers, and the next rows' inputs are under way during a row's sums.  8192 rows of
 // 4096: forward 44 us (bf16 stream, 6.1 TB/s) and 65 us (fp32, 6.1 TB/s), gradient
-// 72 us (5.6 TB/s, its issue slots two thirds full) and 94 us (6.4 TB/s).  All sums
+// 72 us (5.6 TB/s; 68 us without the column sums' kernel) and 94 us (6.4 TB/s).  What
+// the bf16 gradient waits for is the latency between a row's sums and the next: two
+// blocks share an SM at 4096 columns, one from 4104 on (4680 rows of 7168: 79 us for the
+// same bytes), and above 8192 the 64 registers of 1024 threads spill (131 us).  All sums
 // are fp32 in a fixed order: columns by shuffle trees, rows of a column by the thread
 // that owns the column over its block's rows, then over the blocks' partial sums (in
 // the workspace) by a second kernel.

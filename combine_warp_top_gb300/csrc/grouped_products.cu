@@ -44,8 +44,9 @@
 // 4 stages measured slower.
 //
 // What bounds it, and what that led to (GB300, clock cycles of an SM):
-// - Long contractions run at the tensor cores' rate: 16384 x 14336 x 4096, 1000 us,
-//   1920 TFLOP/s.  That takes an issuing lane that is done with a k-block (4 MMAs, a
+// - Long contractions run at the tensor cores' rate: 16384 x 14336 x 4096, 1021 us
+//   (1885 TFLOP/s) at 2070 MHz, 1165 to 1219 us once the power cap lowers the clock
+//   (cuBLAS's own rate falls from 1936 to 1715 TFLOP/s).  That takes an issuing lane that is done with a k-block (4 MMAs, a
 //   commit, a wait) before the MMAs are: see the election below.
 // - With few rows an expert the weights' gradient is the writing of dW.  A tile's
 //   128 KB (fp32) have to leave an SM in some 5000 cycles, which takes whole 128-byte
@@ -54,15 +55,17 @@
 //   CTA's barrier with cluster-scope release waits for every store in flight, 2000
 //   to 5000 cycles a tile, so none of them is on that path; the block-end warp's
 //   releases shared memory alone.  64 experts x 384 rows, 2816 x 2048, fp32: 370 us
-//   with those fences and 64-byte lines, 288 us now; floor 253 us.
+//   with those fences and 64-byte lines, 288 us now (298 to 309 under the power cap);
+//   floor 253 us.
 // - A tile costs each role some 800 cycles to decode: the scheduler does it for all.
 // - A decoding step streams the weights: 16 tokens of 6 of 64 experts of 2816 x 2048,
-//   87 us for 586 MB, 6.7 TB/s, with the matrix as A and 64 rows as B (kFew); 97 us with
+//   88 us for 586 MB, 6.7 TB/s, with the matrix as A and 64 rows as B (kFew); 97 us with
 //   256 rows as A, whose MMAs take longer than the weights.
 // - Few tiles leave SMs idle: with a long contraction 2 or 4 pairs of a cluster share
 //   a tile's k-blocks, keep their sums in shared memory and add them up from there
 //   (4096 rows of one expert, 256 x 256 fp32 weights' gradient: 29 us with one pair,
-//   19 us with four; 1 row, 14336 x 3528 in tiles of few rows: 24 us with four).
+//   19 us with four; 1 row, 14336 x 3528 in tiles of few rows: 24 us with four
+//   a call, 21.7 us in a graph).
 // - 64 tokens of 8 experts, 128 to 512: 5.2 us, of
 //   them 1.1 the experts' counts and the first tile, 0.4 the meeting of the CTAs, 0.9
 //   loads, 0.6 MMAs, 0.5 stores, 0.7 the end.
