@@ -130,9 +130,9 @@ inline cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int block, si
 
 #define MOE_RANGE() const NvtxRange _moe_nvtx_range(__func__)
 
-#define MOE_TRY(expr)                     \
-    do {                                  \
-        const moe_status _st = (expr);    \
+#define MOE_TRY(...)                        \
+    do {                                    \
+        const moe_status _st = (__VA_ARGS__); \
         if (_st != MOE_OK) return _st;    \
     } while (0)
 

@@ -1,0 +1,694 @@
+// Orthogonalised momentum of per-expert matrices: the update of the Muon optimiser.  With g
+// the gradient and b the momentum of one [M, N] matrix:
+//
+//   b' = beta b + g,   u = g + beta b' (Nesterov) or b',   X = u / (|u|_F + eps)
+//   steps times:  G = X X^T,  S = p1 G + p2 G^2,  X = p0 X + S X
+//
+// with the quintic p = (3.4445, -4.7750, 2.0315), which takes every singular value of X
+// towards 1.  A tall matrix (M > N) runs on X^T X and X S instead, so that G is always the
+// smaller square; nothing is transposed, the tensor maps name the operands MN-major.
+#include <stddef.h>
+
+#include <cuda_fp16.h>
+
+#include "../../include/moe_train.h"
+#include "api_checks.cuh"
+#include "moe_internal.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+
+constexpr float kP0 = 3.4445f, kP1 = -4.7750f, kP2 = 2.0315f;
+
+constexpr int BT = 256;   // rows and columns of a pair's tile
+constexpr int BH = 128;   // rows of A and of B that a CTA of the pair holds
+constexpr int BK = 64;
+constexpr int UMMA_K = 16;
+constexpr int kStages = 5;
+constexpr int kAccs = 2;
+constexpr int kTmemCols = BT * kAccs;
+constexpr int OP_BYTES = BH * BK * 2;
+constexpr int BOX_BYTES = OP_BYTES / 2;
+constexpr int STAGE_BYTES = 2 * OP_BYTES;
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarps = 8;
+constexpr int kLine = 64;                 // columns of a line of 128 bytes
+constexpr int kLinesBytes = 32 * 128;     // 32 of them
+constexpr int kStagingBytes = 2 * kLinesBytes;  // of an epilogue warp
+// Registers a thread: 384 x 168 at launch = 128 x 88 + 256 x 208.
+constexpr int kRegsOther = 88, kRegsEpilogue = 208;
+constexpr int kMaxDim = 65536;
+// G and S are kept times 2^12, X times 2^p with 2^p about the root of its longer side, so
+// that entries far below the largest are normal fp16 numbers.
+constexpr float kSquareScale = 4096.0f;
+
+// The three products of a step, and the last one of all.
+enum Form { kGram, kSquare, kStep, kLast };
+
+struct Ctl {
+    uint64_t full[kStages];    // leader: both CTAs' operands of a stage are there
+    uint64_t empty[kStages];   // each CTA: its stage may be refilled
+    uint64_t tfull[kAccs];     // each CTA: accumulator ready
+    uint64_t tempty[kAccs];    // leader: accumulator drained by both CTAs
+    uint64_t lines[kEpilogueWarps];  // each CTA: a warp's lines have come in
+    uint64_t done;             // leader: every issued MMA retired
+    uint32_t tmem_base;
+    int abort;
+};
+constexpr int kBarriers = 2 * kStages + 2 * kAccs + kEpilogueWarps + 1;
+constexpr size_t kSmem = 1024 + (size_t)kStages * STAGE_BYTES +
+                         (size_t)kEpilogueWarps * kStagingBytes + ((sizeof(Ctl) + 15) & ~size_t(15));
+static_assert(kSmem <= 227 * 1024, "shared memory of one block");
+
+struct Dims {
+    int E, K, m, n;  // products: contraction, rows and columns of an output
+};
+
+__host__ __device__ __forceinline__ int blocks_of(int n, int size) { return (n + size - 1) / size; }
+
+// Columns that the MMAs of the last column block take, where there are 128 at most.
+__host__ __device__ __forceinline__ int last_columns(int n) {
+    const int rest = n - (n - 1) / BT * BT;
+    return rest > BH ? BT : (rest + 31) / 32 * 32;
+}
+
+struct Tile {
+    int e, mb, nb;
+};
+
+// kSym: the tiles on and above the diagonal, column by column.  Else 8 row blocks by all
+// column blocks at a time, so that what runs side by side shares operands in L2.
+template <bool kSym>
+__device__ __forceinline__ Tile decode(long long tile, int per_matrix, int MB, int NB) {
+    Tile t;
+    t.e = (int)(tile / per_matrix);
+    const int i = (int)(tile - (long long)t.e * per_matrix);
+    if (kSym) {
+        int c = (int)((sqrtf(8.0f * (float)i + 1.0f) - 1.0f) * 0.5f);
+        while (c * (c + 1) / 2 > i) --c;
+        while ((c + 1) * (c + 2) / 2 <= i) ++c;
+        t.nb = c;
+        t.mb = i - c * (c + 1) / 2;
+    } else {
+        const int g = i / (8 * NB), first = g * 8, rows = MB - first < 8 ? MB - first : 8;
+        const int in = i - g * 8 * NB;
+        t.nb = in / rows;
+        t.mb = first + in - t.nb * rows;
+    }
+    return t;
+}
+
+__device__ __forceinline__ void umma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                              uint32_t accumulate) {
+    umma_bf16_pair(d, a, b, idesc, accumulate);  // kind::f16, the types are idesc's
+}
+// fp16 operands, fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// A warp's 32 x 64 part of an output, of the same tiles of the inputs that lie in its lines,
+// and out by TMA.  v: the lane's row of the accumulator.
+//   kGram    G = acc * 2^(12 - 2p), and its mirror image
+//   kSquare  S = p1 G + p2 acc * 2^-12, likewise
+//   kStep    x = p0 (hi + lo) + acc * 2^-12, into hi and lo
+//   kLast    the same times 2^-p, bf16
+template <Form kForm>
+__device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLine], float alpha,
+                                        float beta) {
+    const int lane = threadIdx.x & 31;
+    uint8_t* second = lines + kLinesBytes;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        uint4* at = reinterpret_cast<uint4*>(lines + lane * 128 + ((k ^ (lane & 7)) << 4));
+        uint4* lo_at = reinterpret_cast<uint4*>(second + lane * 128 + ((k ^ (lane & 7)) << 4));
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = alpha * __uint_as_float(v[k * 8 + j]);
+        if (kForm != kGram) {
+            const uint4 h = *at;
+            const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+            uint32_t l[4] = {};
+            if (kForm != kSquare) {
+                const uint4 o = *lo_at;
+                l[0] = o.x, l[1] = o.y, l[2] = o.z, l[3] = o.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float2 x = unpack_half2(w[j]);
+                if (kForm != kSquare) {
+                    const float2 y = unpack_half2(l[j]);
+                    x.x += y.x;
+                    x.y += y.y;
+                }
+                f[2 * j] = fmaf(beta, x.x, f[2 * j]);
+                f[2 * j + 1] = fmaf(beta, x.y, f[2 * j + 1]);
+            }
+        }
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            o[j] = kForm == kLast ? pack2(f[2 * j], f[2 * j + 1])
+                                  : pack_half2(f[2 * j], f[2 * j + 1]);
+        *at = make_uint4(o[0], o[1], o[2], o[3]);
+        if (kForm == kStep) {
+            uint32_t r[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = unpack_half2(o[j]);
+                r[j] = pack_half2(f[2 * j] - x.x, f[2 * j + 1] - x.y);
+            }
+            *lo_at = make_uint4(r[0], r[1], r[2], r[3]);
+        }
+        if (kForm == kGram || kForm == kSquare) {
+            // column c of the part is row c of its mirror image: 64 rows of 32
+            uint16_t* mirror = reinterpret_cast<uint16_t*>(second);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                mirror[(k * 8 + j) * 32 + lane] = (uint16_t)(o[j / 2] >> (j % 2 * 16));
+        }
+    }
+}
+
+// in, in2: G, or X's two halves (kStep, kLast); out, out2: the output and its mirror image or
+// X's second half.
+template <Form kForm, bool kMnA, bool kMnB>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    muon_product_kernel(const __grid_constant__ CUtensorMap tmA,
+                        const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmIn,
+                        const __grid_constant__ CUtensorMap tmIn2,
+                        const __grid_constant__ CUtensorMap tmOut,
+                        const __grid_constant__ CUtensorMap tmOut2, Dims d, float alpha,
+                        float beta, int* err) {
+    constexpr bool kSym = kForm == kGram || kForm == kSquare;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t* tiles = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+    const uint32_t tiles_addr = smem_u32(tiles);
+    uint8_t* staging_area = tiles + (size_t)kStages * STAGE_BYTES;
+    auto* ctl = reinterpret_cast<Ctl*>(staging_area + (size_t)kEpilogueWarps * kStagingBytes);
+    volatile int* abort_flag = &ctl->abort;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    const int MB = blocks_of(d.m, BT), NB = blocks_of(d.n, BT), KB = blocks_of(d.K, BK);
+    const int per_matrix = kSym ? NB * (NB + 1) / 2 : MB * NB;
+    const long long total = (long long)d.E * per_matrix;
+    const int pairs = (int)(gridDim.x / 2);
+    const int n_last = last_columns(d.n);
+
+    if (warp == 4) {
+        if (lane < kBarriers) {
+            const int tempty = 2 * kStages + kAccs;
+            mbar_init(smem_u32(&ctl->full[0] + lane),
+                      lane >= tempty && lane < tempty + kAccs ? 2 * kEpilogueWarps : 1);
+        }
+        if (lane == 31) ctl->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_map(&tmA);
+        prefetch_map(&tmB);
+        prefetch_map(&tmOut);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&ctl->tmem_base), kTmemCols);
+        tmem_relinquish_pair();
+    }
+    after_previous();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before any remote signal
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    if (warp < 4) {
+        regs_shrink<kRegsOther>();
+        if (warp == 0 && elect_one()) {
+            // ---------------- TMA producer (both CTAs) ----------------
+            const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (long long i = blockIdx.x / 2; ok && i < total; i += pairs) {
+                const Tile t = decode<kSym>(i, per_matrix, MB, NB);
+                const int half = (t.nb == NB - 1 ? n_last : BT) / 2;
+                const int a0 = t.mb * BT + (int)rank * BH, b0 = t.nb * BT + (int)rank * half;
+                const bool two = half > 64;
+                const uint32_t tx = OP_BYTES + (kMnB && !two ? BOX_BYTES : OP_BYTES);
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!wait_bar(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = full0 + (uint32_t)stage * 8u;
+                    const uint32_t a_s = tiles_addr + stage * STAGE_BYTES, b_s = a_s + OP_BYTES;
+                    const int k = kb * BK;
+                    if (leader) mbar_expect_tx(smem_u32(&ctl->full[stage]), 2 * tx);
+                    if (kMnA) {
+                        tma_load_3d_pair(a_s, &tmA, full, a0, k, t.e);
+                        tma_load_3d_pair(a_s + BOX_BYTES, &tmA, full, a0 + 64, k, t.e);
+                    } else {
+                        tma_load_3d_pair(a_s, &tmA, full, k, a0, t.e);
+                    }
+                    if (kMnB) {
+                        tma_load_3d_pair(b_s, &tmB, full, b0, k, t.e);
+                        if (two) tma_load_3d_pair(b_s + BOX_BYTES, &tmB, full, b0 + 64, k, t.e);
+                    } else {
+                        tma_load_3d_pair(b_s, &tmB, full, k, b0, t.e);
+                    }
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // a wait has given up: let the copies in flight land before the CTA exits
+            if (*abort_flag) {
+                const long long t0 = clock64();
+                while (clock64() - t0 < 4000000) {
+                }
+            }
+        } else if (warp == 1 && leader && elect_one()) {
+            // ---------------- MMA issuer (leader only) ----------------
+            constexpr uint32_t kMajors = (kMnA ? kIdescMnA : 0u) | (kMnB ? kIdescMnB : 0u);
+            constexpr uint64_t kStepA = kMnA ? 16 * 128 / 16 : 2;
+            constexpr uint64_t kStepB = kMnB ? 16 * 128 / 16 : 2;
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (long long i = blockIdx.x / 2; ok && i < total; i += pairs) {
+                const Tile t = decode<kSym>(i, per_matrix, MB, NB);
+                const uint32_t idesc = kMajors | idesc_f16(BT, t.nb == NB - 1 ? n_last : BT);
+                if (!wait_bar(smem_u32(&ctl->tempty[acc]), acc_phase ^ 1u, abort_flag, err)) break;
+                tc_fence_after();
+                const uint32_t to = tmem + (uint32_t)(acc * BT);
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!wait_bar(smem_u32(&ctl->full[stage]), phase, abort_flag, err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a_s = tiles_addr + stage * STAGE_BYTES, b_s = a_s + OP_BYTES;
+                    const uint64_t ad = kMnA ? sw128_desc_mn(a_s, BOX_BYTES) : sw128_desc(a_s);
+                    const uint64_t bd = kMnB ? sw128_desc_mn(b_s, BOX_BYTES) : sw128_desc(b_s);
+#pragma unroll
+                    for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                        umma_f16_pair(to, ad + kStepA * kk, bd + kStepB * kk, idesc,
+                                      (kb | kk) != 0 ? 1u : 0u);
+                    umma_commit_pair_multicast(smem_u32(&ctl->empty[stage]), 0x3);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                umma_commit_pair_multicast(smem_u32(&ctl->tfull[acc]), 0x3);
+                if (++acc == kAccs) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            umma_commit_pair_multicast(smem_u32(&ctl->done), 0x1);
+            wait_bar_drain(smem_u32(&ctl->done), 0);
+        }
+    } else {
+        // ---------------- epilogue (both CTAs): own 128 rows ----------------
+        regs_grow<kRegsEpilogue>();
+        const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quadrant, 128 columns
+        uint8_t* lines = staging_area + (size_t)(warp - 4) * kStagingBytes;
+        const uint32_t lines_addr = smem_u32(lines), bar = smem_u32(&ctl->lines[warp - 4]);
+        const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[0]), 0);
+        int acc = 0;
+        uint32_t acc_phase = 0, lines_phase = 0;
+        for (long long i = blockIdx.x / 2; i < total; i += pairs) {
+            const Tile t = decode<kSym>(i, per_matrix, MB, NB);
+            const int row = t.mb * BT + (int)rank * BH + q * 32;
+            const int col = t.nb * BT + half * (BT / 2);
+            // lines of 64 columns that there are
+            const int have = row >= d.m || col >= d.n ? 0 : d.n - col > kLine ? 2 : 1;
+            const auto fetch = [&](int c) {
+                if (kForm == kGram || lane != 0) return;
+                bulk_wait_read();  // what went out from there has been read
+                mbar_expect_tx(bar, kForm == kSquare ? kLinesBytes : 2 * kLinesBytes);
+                tma_load_3d(lines_addr, &tmIn, bar, col + c * kLine, row, t.e);
+                if (kForm != kSquare)
+                    tma_load_3d(lines_addr + kLinesBytes, &tmIn2, bar, col + c * kLine, row, t.e);
+            };
+            if (have > 0) fetch(0);
+            int ok = 0;
+            if (lane == 0)
+                ok = wait_bar(smem_u32(&ctl->tfull[acc]), acc_phase, abort_flag, err);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            tc_fence_after();
+            if (!ok) break;
+            const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BT + half * 128);
+            const auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
+            };
+            if (have == 0) release();
+#pragma unroll 1
+            for (int c = 0; c < have; ++c) {
+                uint32_t v[kLine];
+                tmem_ld32(at + c * kLine, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+                tmem_ld32(at + c * kLine + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+                tmem_wait_ld();
+                if (c == have - 1) release();
+                if (kForm == kGram) {
+                    if (lane == 0) bulk_wait_read();
+                } else {
+                    if (!wait_bar(bar, lines_phase, abort_flag, err)) ok = 0;
+                    lines_phase ^= 1u;
+                }
+                if (!__all_sync(0xffffffffu, ok)) break;
+                combine<kForm>(lines, v, alpha, beta);
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&tmOut, lines_addr, col + c * kLine, row, t.e);
+                    if (kForm == kStep)
+                        tma_store_3d(&tmOut2, lines_addr + kLinesBytes, col + c * kLine, row, t.e);
+                    if (kSym && t.mb != t.nb)
+                        tma_store_3d(&tmOut2, lines_addr + kLinesBytes, row, col + c * kLine, t.e);
+                    bulk_commit();
+                }
+                if (c + 1 < have) fetch(c + 1);
+            }
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (++acc == kAccs) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while its peer may still signal it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// ---- momentum, norm, scale ----------------------------------------------------------------
+
+constexpr int kBlock = 256;
+constexpr int kChunk = kBlock * 8 * 4;  // elements of a block's round
+constexpr int kMaxParts = 64;           // blocks of a matrix
+
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+// u of a matrix's 8 elements at p, from the new momentum.
+template <typename G>
+__device__ __forceinline__ void update8(const G* grad, const float* buf, bool nesterov, float beta,
+                                        float (&u)[8]) {
+    if (!buf) {
+        load8(grad, u);
+        return;
+    }
+    load8(buf, u);
+    if (nesterov) {
+        float g[8];
+        load8(grad, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = fmaf(beta, u[j], g[j]);
+    }
+}
+
+// The new momentum and the sums of squares of u, one of each block (blockIdx.y: the matrix).
+// Squares of values from 2^64 on leave fp32: those are summed times 2^-128 besides.
+template <typename G>
+__global__ void __launch_bounds__(kBlock)
+    muon_momentum_kernel(const G* grad, const float* buf, float* new_buf, long long size,
+                         bool nesterov, float beta, double2* parts) {
+    after_previous();
+    const long long at = (long long)blockIdx.y * size;
+    double sum = 0.0, big = 0.0;
+    for (long long i = ((long long)blockIdx.x * kBlock + threadIdx.x) * 8; i < size;
+         i += (long long)gridDim.x * kBlock * 8) {
+        float g[8], u[8];
+        load8(grad + at + i, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = g[j];
+        if (buf) {
+            float b[8];
+            load8(buf + at + i, b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                b[j] = fmaf(beta, b[j], g[j]);
+                u[j] = nesterov ? fmaf(beta, b[j], g[j]) : b[j];
+            }
+            float4* to = reinterpret_cast<float4*>(new_buf + at + i);
+            to[0] = make_float4(b[0], b[1], b[2], b[3]);
+            to[1] = make_float4(b[4], b[5], b[6], b[7]);
+        }
+        float s = 0.0f, t = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float small = u[j] * 0x1p-64f;
+            s = fmaf(u[j], u[j], s);
+            t = fmaf(small, small, t);
+        }
+        sum += s;
+        big += t;
+    }
+    __shared__ double2 warps[kBlock / 32];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        big += __shfl_xor_sync(0xffffffffu, big, o);
+    }
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = make_double2(sum, big);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kBlock / 32; ++w) {
+            sum += warps[w].x;
+            big += warps[w].y;
+        }
+        parts[(long long)blockIdx.y * gridDim.x + blockIdx.x] = make_double2(sum, big);
+    }
+}
+
+// X = u 2^p / (|u| + eps) as hi + lo.
+template <typename G>
+__global__ void __launch_bounds__(kBlock)
+    muon_scale_kernel(const G* grad, const float* buf, long long size, bool nesterov, float beta,
+                      float eps, int p, const double2* parts, int n_parts, __half* hi, __half* lo) {
+    after_previous();
+    __shared__ float factors[2];
+    const long long at = (long long)blockIdx.y * size;
+    if (threadIdx.x == 0) {
+        double sum = 0.0, big = 0.0;
+        for (int i = 0; i < n_parts; ++i) {
+            const double2 v = parts[(long long)blockIdx.y * n_parts + i];
+            sum += v.x;
+            big += v.y;
+        }
+        // in two factors: one alone may be too small for fp32
+        if (!(sum < 1e300)) sum = big * 0x1p128;
+        int ex = 0;
+        const double f = frexp(1.0 / (sqrt(sum) + (double)eps), &ex);
+        factors[0] = (float)ldexp(f, ex / 2);
+        factors[1] = (float)ldexp(1.0, ex - ex / 2 + p);
+    }
+    __syncthreads();
+    const float f0 = factors[0], f1 = factors[1];
+    for (long long i = ((long long)blockIdx.x * kBlock + threadIdx.x) * 8; i < size;
+         i += (long long)gridDim.x * kBlock * 8) {
+        float u[8];
+        update8(grad + at + i, buf ? buf + at + i : nullptr, nesterov, beta, u);
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float a = u[2 * j] * f0 * f1, b = u[2 * j + 1] * f0 * f1;
+            h[j] = pack_half2(a, b);
+            const float2 r = unpack_half2(h[j]);
+            l[j] = pack_half2(a - r.x, b - r.y);
+        }
+        *reinterpret_cast<uint4*>(hi + at + i) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(lo + at + i) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------------
+
+struct Work {
+    size_t parts, gram, square, hi, lo, total;
+};
+Work work_of(const moe_muon_shape& s) {
+    const size_t n = (size_t)s.E * s.M * s.N;
+    const size_t m = s.M < s.N ? s.M : s.N, sq = (size_t)s.E * m * m;
+    Work w;
+    size_t o = 256;  // the error word
+    w.parts = o;  o = align256(o + (size_t)s.E * kMaxParts * sizeof(double2));
+    w.gram = o;   o = align256(o + sq * 2);
+    w.square = o; o = align256(o + sq * 2);
+    w.hi = o;     o = align256(o + n * 2);
+    w.lo = o;     o = align256(o + n * 2);
+    w.total = o;
+    return w;
+}
+
+bool map_matrices(CUtensorMap* m, const void* ptr, int E, int rows, int cols, uint32_t box_cols,
+                  uint32_t box_rows, MapType type) {
+    const uint64_t sizes[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)E};
+    const uint64_t strides[2] = {(uint64_t)cols * 2, (uint64_t)cols * rows * 2};
+    const uint32_t box[3] = {box_cols, box_rows, 1};
+    return map_typed(m, 3, ptr, sizes, strides, box, type, box_cols * 2 == 128);
+}
+
+template <Form kForm, bool kMnA, bool kMnB>
+moe_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in,
+                          const CUtensorMap& in2, const CUtensorMap& out, const CUtensorMap& out2,
+                          const Dims& d, float alpha, float beta, int* err, cudaStream_t st) {
+    const auto kernel = muon_product_kernel<kForm, kMnA, kMnB>;
+    static OncePerDevice set;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    if (!set.done(dev)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kSmem) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        set.finish(dev);
+    }
+    const long long MB = blocks_of(d.m, BT), NB = blocks_of(d.n, BT);
+    const long long tiles =
+        d.E * (kForm == kGram || kForm == kSquare ? NB * (NB + 1) / 2 : MB * NB);
+    const long long most = sm_count() / 2;
+    return cuda_status(launch_chained(kernel, (int)(2 * (tiles < most ? tiles : most)), kThreads,
+                                      kSmem, st, a, b, in, in2, out, out2, d, alpha, beta, err));
+}
+
+template <typename G>
+moe_status launch_prepare(const G* grad, const float* buf, float* new_buf, const moe_muon_shape& s,
+                          int p, double2* parts, __half* hi, __half* lo, cudaStream_t st) {
+    const long long size = (long long)s.M * s.N, rounds = (size + kChunk - 1) / kChunk;
+    const int blocks = (int)(rounds < kMaxParts ? rounds : kMaxParts);
+    const bool nesterov = s.nesterov != 0;
+    MOE_TRY(cuda_status(launch_chained(muon_momentum_kernel<G>, dim3(blocks, s.E), kBlock, 0, st,
+                                       grad, buf, new_buf, size, nesterov, s.momentum, parts)));
+    return cuda_status(launch_chained(muon_scale_kernel<G>, dim3(blocks, s.E), kBlock, 0, st, grad,
+                                      (const float*)new_buf, size, nesterov, s.momentum, s.eps, p,
+                                      (const double2*)parts, blocks, hi, lo));
+}
+
+bool valid(const moe_muon_shape* s) {
+    return s && s->E > 0 && s->M > 0 && s->N > 0 && s->steps > 0 && s->steps <= 64 &&
+           s->momentum >= 0.0f && s->momentum < 1.0f && s->eps >= 1e-12f && s->eps <= 1.0f &&
+           (s->grad_type == MOE_TYPE_BF16 || s->grad_type == MOE_TYPE_F32);
+}
+bool supported(const moe_muon_shape* s) {
+    return s->M % 8 == 0 && s->N % 8 == 0 && s->M <= kMaxDim && s->N <= kMaxDim &&
+           s->E <= kMaxE;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_muon_workspace_bytes(const moe_muon_shape* shape) {
+    return valid(shape) && supported(shape) ? work_of(*shape).total : 0;
+}
+
+moe_status moe_muon_update(const void* grad, const float* momentum, const moe_muon_shape* shape,
+                           uint16_t* update, float* new_momentum, void* ws, size_t ws_bytes,
+                           void* stream) {
+    MOE_RANGE();
+    if (!valid(shape)) return MOE_ERR_INVALID_ARG;
+    if (!supported(shape)) return MOE_ERR_UNSUPPORTED;
+    const moe_muon_shape& s = *shape;
+    const Work w = work_of(s);
+    if (!ws || ws_bytes < w.total) return MOE_ERR_WORKSPACE;
+    if (!grad || !update || (momentum == nullptr) != (new_momentum == nullptr))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(grad, momentum, update, new_momentum, ws)) return MOE_ERR_INVALID_ARG;
+    const cudaStream_t st = as_stream(stream);
+    const bool tall = s.M > s.N;
+    const int m = tall ? s.N : s.M, longer = tall ? s.M : s.N;
+    int p = 0;
+    while ((1LL << (2 * p + 1)) < longer) ++p;  // 2^p about the root of the longer side
+    auto* gram = ws_ptr<__half>(ws, w.gram);
+    auto* square = ws_ptr<__half>(ws, w.square);
+    auto* hi = ws_ptr<__half>(ws, w.hi);
+    auto* lo = ws_ptr<__half>(ws, w.lo);
+    auto* parts = ws_ptr<double2>(ws, w.parts);
+    int* err = ws_ptr<int>(ws, 0);
+    MOE_TRY(s.grad_type == MOE_TYPE_F32
+                ? launch_prepare(static_cast<const float*>(grad), momentum, new_momentum, s, p,
+                                 parts, hi, lo, st)
+                : launch_prepare(static_cast<const __nv_bfloat16*>(grad), momentum, new_momentum,
+                                 s, p, parts, hi, lo, st));
+    // operands: rows with their contraction along them (k) or columns (mn); lines and their
+    // mirror image
+    CUtensorMap x_k, x_mn, g_k, s_k, g_lines, g_mirror, s_lines, s_mirror, hi_lines, lo_lines, out;
+    const auto map = [&](CUtensorMap* t, const void* ptr, int rows, int cols, uint32_t bc,
+                         uint32_t br) {
+        return map_matrices(t, ptr, s.E, rows, cols, bc, br, kMapF16);
+    };
+    if (!map(&x_k, hi, s.M, s.N, 64, BH) || !map(&x_mn, hi, s.M, s.N, 64, BK) ||
+        !map(&g_k, gram, m, m, 64, BH) || !map(&s_k, square, m, m, 64, BH) ||
+        !map(&g_lines, gram, m, m, 64, 32) || !map(&g_mirror, gram, m, m, 32, 64) ||
+        !map(&s_lines, square, m, m, 64, 32) || !map(&s_mirror, square, m, m, 32, 64) ||
+        !map(&hi_lines, hi, s.M, s.N, 64, 32) || !map(&lo_lines, lo, s.M, s.N, 64, 32) ||
+        !map_matrices(&out, update, s.E, s.M, s.N, 64, 32, kMapBF16))
+        return MOE_ERR_UNSUPPORTED;
+    const float scale = ldexpf(1.0f, -2 * p) * kSquareScale, back = 1.0f / kSquareScale;
+    const Dims gd = {s.E, longer, m, m}, sd = {s.E, m, m, m}, xd = {s.E, m, s.M, s.N};
+    for (int i = 0; i < s.steps; ++i) {
+        MOE_TRY(tall ? launch_product<kGram, true, true>(x_mn, x_mn, g_lines, g_lines, g_lines,
+                                                         g_mirror, gd, scale, 0.0f, err, st)
+                     : launch_product<kGram, false, false>(x_k, x_k, g_lines, g_lines, g_lines,
+                                                           g_mirror, gd, scale, 0.0f, err, st));
+        MOE_TRY(launch_product<kSquare, false, false>(g_k, g_k, g_lines, g_lines, s_lines,
+                                                      s_mirror, sd, kP2 * back, kP1, err, st));
+        const bool last = i == s.steps - 1;
+        const float unscale = last ? ldexpf(1.0f, -p) : 1.0f;
+        const float alpha = back * unscale, beta = kP0 * unscale;
+        if (last)
+            MOE_TRY(tall ? launch_product<kLast, false, false>(x_k, s_k, hi_lines, lo_lines, out,
+                                                               out, xd, alpha, beta, err, st)
+                         : launch_product<kLast, false, true>(s_k, x_mn, hi_lines, lo_lines, out,
+                                                              out, xd, alpha, beta, err, st));
+        else
+            MOE_TRY(tall ? launch_product<kStep, false, false>(x_k, s_k, hi_lines, lo_lines,
+                                                               hi_lines, lo_lines, xd, alpha, beta,
+                                                               err, st)
+                         : launch_product<kStep, false, true>(s_k, x_mn, hi_lines, lo_lines,
+                                                              hi_lines, lo_lines, xd, alpha, beta,
+                                                              err, st));
+    }
+    return MOE_OK;
+}
+
+}  // extern "C"

@@ -43,6 +43,11 @@ class MoeNormShape(ctypes.Structure):
         [("eps", ctypes.c_float), ("residual_scale", ctypes.c_float)]
 
 
+class MoeMuonShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("E", "M", "N", "steps", "nesterov", "grad_type")] + \
+        [("momentum", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -62,7 +67,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     P, S, I32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
     shp, lay = ctypes.POINTER(MoeShape), ctypes.POINTER(MoeLayout)
-    nrm = ctypes.POINTER(MoeNormShape)
+    nrm, muon = ctypes.POINTER(MoeNormShape), ctypes.POINTER(MoeMuonShape)
     sigs = {
         "moe_workspace_bytes": (S, [shp]),
         "moe_packed_gate_up_bytes": (S, [shp]),
@@ -104,6 +109,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_block_norm": (I32, [P, P, P, P, P, nrm, P, P, P, P, P]),
         "moe_block_norm_grad": (I32, [P, P, P, P, P, P, P, P, P, nrm, P, P, P, P, P, I32, P, S,
                                       P]),
+        "moe_muon_workspace_bytes": (S, [muon]),
+        "moe_muon_update": (I32, [P, P, muon, P, P, P, S, P]),
         "moe_selftest_wait_timeout": (I32, [P, ctypes.c_int64, P]),
         "moe_get_error": (I32, [P, P]),
         "moe_status_str": (ctypes.c_char_p, [I32]),
@@ -763,6 +770,58 @@ def moe_block_norm_grad(ds, dx, y, s, w_post, gate, w_pre, rstd_post, rstd_pre,
         _exact(dw_post, f32, h, "dw_post"), _exact(dgate, f32, n._gate_shape, "dgate"),
         _exact(dw_pre, f32, h, "dw_pre"), int(bool(accumulate)), *_bytes(ws), _stream(stream)),
         "moe_block_norm_grad")
+
+
+@dataclass(frozen=True)
+class MuonShape:
+    """E matrices [M, N] with an orthogonalised momentum (moe_muon_shape)."""
+    E: int
+    M: int
+    N: int
+    steps: int = 5
+    momentum: float = 0.95
+    nesterov: bool = True
+    eps: float = 1e-7
+
+    @functools.cached_property
+    def _refs(self):
+        """The C struct by reference for each type of gradient."""
+        return {t: ctypes.byref(self.c(t)) for t in MOE_TYPES}
+
+    def __getstate__(self):
+        """The fields alone: copies and pickles make their own references."""
+        return {f.name: getattr(self, f.name) for f in dataclasses.fields(self)}
+
+    def c(self, grad_dtype=torch.float32) -> MoeMuonShape:
+        return MoeMuonShape(self.E, self.M, self.N, self.steps, int(bool(self.nesterov)),
+                            MOE_TYPES[grad_dtype], self.momentum, self.eps)
+
+
+def moe_muon_workspace_bytes(shape: MuonShape) -> int:
+    return int(load().moe_muon_workspace_bytes(ctypes.byref(shape.c())))
+
+
+def muon_workspace(shape: MuonShape, device="cuda") -> torch.Tensor:
+    n = moe_muon_workspace_bytes(shape)
+    if n == 0:
+        raise MoeError(1, "moe_muon_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def moe_muon_update(grad, momentum, shape: MuonShape, update, ws, new_momentum=None, stream=None):
+    """update bf16 [E, M, N] = the orthogonalised momentum of grad (bf16 or fp32) and momentum
+    (fp32, or None); new_momentum (None: momentum itself) receives the next one."""
+    s, size = shape, (shape.E, shape.M, shape.N)
+    _out_type(grad, "grad")
+    if new_momentum is None:
+        new_momentum = momentum
+    _check(load().moe_muon_update(
+        _exact(grad, grad.dtype, size, "grad"), _exact(momentum, torch.float32, size, "momentum"),
+        s._refs[grad.dtype], _exact(update, torch.bfloat16, size, "update"),
+        _exact(new_momentum, torch.float32, size, "new_momentum"), *_bytes(ws), _stream(stream)),
+        "moe_muon_update")
 
 
 def moe_selftest_wait_timeout(ws, limit_cycles: int, stream=None):

@@ -159,6 +159,37 @@ moe_status moe_block_norm_grad(const void* ds, const uint16_t* dx, const uint16_
                                float* dw_post, float* dgate, float* dw_pre, int32_t accumulate,
                                void* ws, size_t ws_bytes, void* stream);
 
+/* Orthogonalised momentum of E matrices [M, N], the update of the Muon optimiser.
+ * M and N are multiples of 8, at most 65536; 1 <= steps <= 64; 0 <= momentum < 1;
+ * 1e-12 <= eps <= 1.  grad_type: the moe_type of the gradient. */
+typedef struct {
+    int32_t E, M, N;
+    int32_t steps;
+    int32_t nesterov;
+    int32_t grad_type;
+    float momentum;
+    float eps;
+} moe_muon_shape;
+
+/* Bytes of device workspace of moe_muon_update (0 if the shape is invalid): two 16-bit
+ * copies of the matrices and two of their smaller squares.  Its first 256 bytes hold the
+ * error word (moe_get_error) and have to be zero at first. */
+size_t moe_muon_workspace_bytes(const moe_muon_shape* shape);
+
+/* For each matrix, with g its gradient (bf16 or fp32) and b its momentum (fp32):
+ *   b' = momentum * b + g
+ *   u  = g + momentum * b' with nesterov, else b'          (g itself without a momentum)
+ *   X  = u / (|u| + eps), |u| the Frobenius norm
+ *   steps times: G = X X^T, X = 3.4445 X + (-4.7750 G + 2.0315 G^2) X
+ * update, bf16 [E, M, N], receives X, whose singular values lie between about 0.7 and
+ * 1.2 where those of u are not far below its norm; new_momentum, fp32 [E, M, N], b' (may
+ * be momentum itself; both NULL: no momentum).  The products take X, G and the sum in
+ * brackets rounded to fp16, X in its place in the sum as two of them (22 bits); their
+ * sums are fp32.  A matrix with an infinity or a NaN in u makes its own update NaN, no other's. */
+moe_status moe_muon_update(const void* grad, const float* momentum, const moe_muon_shape* shape,
+                           uint16_t* update, float* new_momentum, void* ws, size_t ws_bytes,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif
