@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kBlock)
 // ---- host ---------------------------------------------------------------------------------
 
 struct Work {
-    size_t parts, gram, square, hi, lo, total;
+    size_t parts, gram, square, hi[2], lo, total;
 };
 Work work_of(const moe_muon_shape& s) {
     const size_t n = (size_t)s.E * s.M * s.N;
@@ -551,7 +551,7 @@ Work work_of(const moe_muon_shape& s) {
     w.parts = o;  o = align256(o + (size_t)s.E * kMaxParts * sizeof(double2));
     w.gram = o;   o = align256(o + sq * 2);
     w.square = o; o = align256(o + sq * 2);
-    w.hi = o;     o = align256(o + n * 2);
+    for (size_t& hi : w.hi) hi = o, o = align256(o + n * 2);
     w.lo = o;     o = align256(o + n * 2);
     w.total = o;
     return w;
@@ -640,53 +640,59 @@ moe_status moe_muon_update(const void* grad, const float* momentum, const moe_mu
     while ((1LL << (2 * p + 1)) < longer) ++p;  // 2^p about the root of the longer side
     auto* gram = ws_ptr<__half>(ws, w.gram);
     auto* square = ws_ptr<__half>(ws, w.square);
-    auto* hi = ws_ptr<__half>(ws, w.hi);
+    // a step's X is an operand of all tiles of the next one: they write to the other copy
+    __half* hi[2] = {ws_ptr<__half>(ws, w.hi[0]), ws_ptr<__half>(ws, w.hi[1])};
     auto* lo = ws_ptr<__half>(ws, w.lo);
     auto* parts = ws_ptr<double2>(ws, w.parts);
     int* err = ws_ptr<int>(ws, 0);
     MOE_TRY(s.grad_type == MOE_TYPE_F32
                 ? launch_prepare(static_cast<const float*>(grad), momentum, new_momentum, s, p,
-                                 parts, hi, lo, st)
+                                 parts, hi[0], lo, st)
                 : launch_prepare(static_cast<const __nv_bfloat16*>(grad), momentum, new_momentum,
-                                 s, p, parts, hi, lo, st));
+                                 s, p, parts, hi[0], lo, st));
     // operands: rows with their contraction along them (k) or columns (mn); lines and their
     // mirror image
-    CUtensorMap x_k, x_mn, g_k, s_k, g_lines, g_mirror, s_lines, s_mirror, hi_lines, lo_lines, out;
+    CUtensorMap x_k[2], x_mn[2], hi_lines[2], lo_lines, g_k, s_k, g_lines, g_mirror, s_lines,
+        s_mirror, out;
     const auto map = [&](CUtensorMap* t, const void* ptr, int rows, int cols, uint32_t bc,
                          uint32_t br) {
         return map_matrices(t, ptr, s.E, rows, cols, bc, br, kMapF16);
     };
-    if (!map(&x_k, hi, s.M, s.N, 64, BH) || !map(&x_mn, hi, s.M, s.N, 64, BK) ||
-        !map(&g_k, gram, m, m, 64, BH) || !map(&s_k, square, m, m, 64, BH) ||
-        !map(&g_lines, gram, m, m, 64, 32) || !map(&g_mirror, gram, m, m, 32, 64) ||
-        !map(&s_lines, square, m, m, 64, 32) || !map(&s_mirror, square, m, m, 32, 64) ||
-        !map(&hi_lines, hi, s.M, s.N, 64, 32) || !map(&lo_lines, lo, s.M, s.N, 64, 32) ||
-        !map_matrices(&out, update, s.E, s.M, s.N, 64, 32, kMapBF16))
-        return MOE_ERR_UNSUPPORTED;
+    bool ok = map(&g_k, gram, m, m, 64, BH) && map(&s_k, square, m, m, 64, BH) &&
+              map(&g_lines, gram, m, m, 64, 32) && map(&g_mirror, gram, m, m, 32, 64) &&
+              map(&s_lines, square, m, m, 64, 32) && map(&s_mirror, square, m, m, 32, 64) &&
+              map(&lo_lines, lo, s.M, s.N, 64, 32) &&
+              map_matrices(&out, update, s.E, s.M, s.N, 64, 32, kMapBF16);
+    for (int i = 0; i < 2; ++i)
+        ok = ok && map(&x_k[i], hi[i], s.M, s.N, 64, BH) && map(&x_mn[i], hi[i], s.M, s.N, 64, BK) &&
+             map(&hi_lines[i], hi[i], s.M, s.N, 64, 32);
+    if (!ok) return MOE_ERR_UNSUPPORTED;
     const float scale = ldexpf(1.0f, -2 * p) * kSquareScale, back = 1.0f / kSquareScale;
     const Dims gd = {s.E, longer, m, m}, sd = {s.E, m, m, m}, xd = {s.E, m, s.M, s.N};
     for (int i = 0; i < s.steps; ++i) {
-        MOE_TRY(tall ? launch_product<kGram, true, true>(x_mn, x_mn, g_lines, g_lines, g_lines,
-                                                         g_mirror, gd, scale, 0.0f, err, st)
-                     : launch_product<kGram, false, false>(x_k, x_k, g_lines, g_lines, g_lines,
-                                                           g_mirror, gd, scale, 0.0f, err, st));
+        const int now = i % 2;
+        MOE_TRY(tall ? launch_product<kGram, true, true>(x_mn[now], x_mn[now], g_lines, g_lines,
+                                                         g_lines, g_mirror, gd, scale, 0.0f, err,
+                                                         st)
+                     : launch_product<kGram, false, false>(x_k[now], x_k[now], g_lines, g_lines,
+                                                           g_lines, g_mirror, gd, scale, 0.0f, err,
+                                                           st));
         MOE_TRY(launch_product<kSquare, false, false>(g_k, g_k, g_lines, g_lines, s_lines,
                                                       s_mirror, sd, kP2 * back, kP1, err, st));
         const bool last = i == s.steps - 1;
         const float unscale = last ? ldexpf(1.0f, -p) : 1.0f;
-        const float alpha = back * unscale, beta = kP0 * unscale;
+        const CUtensorMap &a = tall ? x_k[now] : s_k, &b = tall ? s_k : x_mn[now];
+        const CUtensorMap &to = last ? out : hi_lines[1 - now], &to2 = last ? out : lo_lines;
+        const auto step = [&](auto launch) {
+            return launch(a, b, hi_lines[now], lo_lines, to, to2, xd, back * unscale, kP0 * unscale,
+                          err, st);
+        };
         if (last)
-            MOE_TRY(tall ? launch_product<kLast, false, false>(x_k, s_k, hi_lines, lo_lines, out,
-                                                               out, xd, alpha, beta, err, st)
-                         : launch_product<kLast, false, true>(s_k, x_mn, hi_lines, lo_lines, out,
-                                                              out, xd, alpha, beta, err, st));
+            MOE_TRY(tall ? step(launch_product<kLast, false, false>)
+                         : step(launch_product<kLast, false, true>));
         else
-            MOE_TRY(tall ? launch_product<kStep, false, false>(x_k, s_k, hi_lines, lo_lines,
-                                                               hi_lines, lo_lines, xd, alpha, beta,
-                                                               err, st)
-                         : launch_product<kStep, false, true>(s_k, x_mn, hi_lines, lo_lines,
-                                                              hi_lines, lo_lines, xd, alpha, beta,
-                                                              err, st));
+            MOE_TRY(tall ? step(launch_product<kStep, false, false>)
+                         : step(launch_product<kStep, false, true>));
     }
     return MOE_OK;
 }

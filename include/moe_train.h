@@ -171,8 +171,8 @@ typedef struct {
     float eps;
 } moe_muon_shape;
 
-/* Bytes of device workspace of moe_muon_update (0 if the shape is invalid): two 16-bit
- * copies of the matrices and two of their smaller squares.  Its first 256 bytes hold the
+/* Bytes of device workspace of moe_muon_update (0 if the shape is invalid): three
+ * 16-bit copies of the matrices and two of their smaller squares.  Its first 256 bytes hold the
  * error word (moe_get_error) and have to be zero at first. */
 size_t moe_muon_workspace_bytes(const moe_muon_shape* shape);
 

@@ -106,6 +106,17 @@ def test_singular_values_and_scale():
         check(grad * 2.0 ** k, None, scaled, a, None)
 
 
+@pytest.mark.parametrize("E,M,N", [(4, 2048, 1408), (2, 1536, 4096)])
+def test_tiles_in_turn(E, M, N):
+    """More tiles of a matrix than run at once: none may read what another has written."""
+    shape = moe.MuonShape(E, M, N)
+    grad = normal(11, E, M, N)
+    out, _ = run(grad, None, shape)
+    check(grad, None, shape, out, None)
+    again, _ = run(grad, None, shape)
+    assert torch.equal(out, again)
+
+
 def test_zero_and_non_finite_matrices():
     """A zero matrix has a zero update; an infinity or a NaN stays in its matrix."""
     E, M, N = 4, 72, 264
