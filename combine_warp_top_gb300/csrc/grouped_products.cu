@@ -73,6 +73,7 @@
 
 #include "../../include/moe_train.h"
 #include "api_checks.cuh"
+#include "gate.cuh"
 #include "moe_internal.cuh"
 #include "ptx.cuh"
 
@@ -81,7 +82,9 @@ namespace {
 
 using namespace ptx;
 
-enum Mode { kForward, kRowsGrad, kWeightsGrad };
+// kGated, kGatedGrad: the products before and behind an expert's gate, with the gate (or its
+// gradient) in their epilogue.  A tile of kGated is 128 gate columns and the same up columns.
+enum Mode { kForward, kRowsGrad, kWeightsGrad, kGated, kGatedGrad };
 
 constexpr int BT = 256;    // rows and columns of a pair's tile
 constexpr int BH = 128;    // rows of A and of B that a CTA of the pair holds
@@ -101,10 +104,13 @@ constexpr int BF = 64;
 constexpr int FEW_BYTES = BF / 2 * BK * 2;  // that operand of one stage in one CTA
 template <bool kFew>
 constexpr int kStageBytes = kFew ? OP_BYTES + FEW_BYTES : 2 * OP_BYTES;
-template <bool kFew>
-constexpr int kStagesOf = kFew ? 9 : 6;
+template <int kMode, bool kFew>
+constexpr int kStagesOf = kFew ? 9 : kMode == kGatedGrad ? 5 : 6;
 constexpr int kAhead = 2;  // tiles the scheduler publishes ahead of the leader's producer
 constexpr int kStagingBytes = 32 * 128;  // an epilogue warp's output: 32 lines
+// kGatedGrad: 32 lines of gate columns and 32 of up columns come in there and go out again
+template <int kMode>
+constexpr int kStagingOf = (kMode == kGatedGrad ? 2 : 1) * kStagingBytes;
 // k-blocks added up in one accumulator, see "Precision" above
 template <typename OutT>
 constexpr int kChainBlocks = sizeof(OutT) == 4 ? 8 : 512;
@@ -154,17 +160,21 @@ struct Barriers : Queues {
     uint64_t land[kStages];     // each CTA: its copies of a segment's last block are there
 };
 template <int kMode, bool kFew>
-struct Ctl : Barriers<kStagesOf<kFew>> {};
+struct Ctl : Barriers<kStagesOf<kMode, kFew>> {};
 constexpr int kMaxSorted = 512;  // what is left of shared memory holds
 template <>
-struct Ctl<kWeightsGrad, false> : Barriers<kStagesOf<false>> {
+struct Ctl<kWeightsGrad, false> : Barriers<kStagesOf<kWeightsGrad, false>> {
     uint16_t order[kMaxSorted];  // experts by falling number of rows
+};
+template <>
+struct Ctl<kGatedGrad, false> : Barriers<kStagesOf<kGatedGrad, false>> {
+    uint64_t lines[kEpilogueWarps];  // each CTA: a warp's lines have come in
 };
 
 template <int kMode, bool kFew>
 constexpr size_t smem_bytes() {
-    constexpr size_t n = 1024 + (size_t)kStagesOf<kFew> * kStageBytes<kFew> +
-                         (size_t)kEpilogueWarps * kStagingBytes +
+    constexpr size_t n = 1024 + (size_t)kStagesOf<kMode, kFew> * kStageBytes<kFew> +
+                         (size_t)kEpilogueWarps * kStagingOf<kMode> +
                          ((sizeof(Ctl<kMode, kFew>) + 15) & ~size_t(15));
     static_assert(n <= 227 * 1024, "shared memory of one block");
     return n;
@@ -492,6 +502,140 @@ __device__ __forceinline__ void join_few(uint32_t ring, uint32_t rank, int split
     }
 }
 
+// ---- the gate in the epilogue ---------------------------------------------------------------
+
+// Lines (32 rows x 64 bf16 columns) out: by TMA where all 32 rows are the segment's, else by
+// the warp's own stores.  to: the first row's first column, `pitch` apart; cols: how many there
+// are from it on.
+__device__ __forceinline__ void lines_out(const CUtensorMap* map, const uint8_t* lines, int c0,
+                                          int c1, int c2, bool three, uint16_t* to, int pitch,
+                                          int rows, int cols) {
+    const int lane = threadIdx.x & 31;
+    if (rows >= 32) {
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            if (three)
+                tma_store_3d(map, smem_u32(lines), c0, c1, c2);
+            else
+                tma_store_2d(map, smem_u32(lines), c0, c1);
+            bulk_commit();
+        }
+    } else {
+        __syncwarp();
+        store_lines<__nv_bfloat16>(lines, reinterpret_cast<__nv_bfloat16*>(to), pitch, rows, cols);
+        __syncwarp();
+    }
+}
+
+// kGated: 32 rows of 64 gate columns at g_at and of their up columns at u_at.  h leaves as
+// w SiLU(g) u of the fp32 sums, g and u rounded to bf16 where they are wanted.
+template <typename Release>
+__device__ __forceinline__ void gated_out(const CUtensorMap& tmGu, const CUtensorMap& tmH,
+                                          const Gate& gate, uint8_t* staging, uint32_t g_at,
+                                          uint32_t u_at, long long row, int rows, int col, int I,
+                                          float w, Release release) {
+    const int lane = threadIdx.x & 31;
+    uint32_t g[64], u[64];
+    tmem_ld_line(g_at, g);
+    tmem_ld_line(u_at, u);
+    tmem_wait_ld();
+    release();
+    if (rows <= 0 || col >= I) return;
+    const auto put = [&](const uint32_t (&v)[64]) {
+        if (lane == 0) bulk_wait_read();  // the lines before have been read
+        __syncwarp();
+        put_line<__nv_bfloat16>(staging, lane, v);
+    };
+    if (gate.gu) {
+        uint16_t* to = gate.gu + row * 2 * I + col;
+        put(g);
+        lines_out(&tmGu, staging, col, 0, (int)row, true, to, 2 * I, rows, I - col);
+        put(u);
+        lines_out(&tmGu, staging, col, 1, (int)row, true, to + I, 2 * I, rows, I - col);
+    }
+#pragma unroll
+    for (int j = 0; j < 64; ++j) {
+        const float a = __uint_as_float(g[j]);
+        g[j] = __float_as_uint(w * (a * sigmoid(a)) * __uint_as_float(u[j]));
+    }
+    put(g);
+    lines_out(&tmH, staging, col, (int)row, 0, false, gate.h + row * I + col, I, rows, I - col);
+}
+
+// kGated in tiles of few rows: a warp has the sums of 32 gate or up columns (its TMEM lanes)
+// by 32 rows.  The two warps of the same columns lay them down as lines of a row each, and
+// take 16 of the rows each.  in, out: their two barriers of 64 threads.
+__device__ __forceinline__ void named_sync(int id) {
+    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ void named_arrive(int id) {
+    asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ void gated_few_out(const Gate& gate, uint8_t* staging_area, int q,
+                                              int half, const uint32_t (&v)[32], long long row,
+                                              int rows, int col, int I, float w, int in, int out) {
+    const int lane = threadIdx.x & 31;
+    uint8_t* mine = staging_area + (size_t)(half * 4 + q) * kStagingBytes;
+    put_few(mine, lane, v);
+    named_sync(in);
+    const uint8_t* gs = staging_area + (size_t)(half * 4 + (q & 1)) * kStagingBytes;
+    const uint8_t* us = gs + 2 * kStagingBytes;
+    const int c = (lane & 7) * 4;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const int r = (q >> 1) * 16 + i * 4 + (lane >> 3);
+        const float wr = __shfl_sync(0xffffffffu, w, r);
+        if (r >= rows || col + c >= I) continue;
+        const float4 g = *reinterpret_cast<const float4*>(gs + r * 128 + c * 4);
+        const float4 u = *reinterpret_cast<const float4*>(us + r * 128 + c * 4);
+        const long long at = (row + r) * I + col + c;
+        if (gate.gu) {
+            uint16_t* to = gate.gu + at + (row + r) * I;
+            *reinterpret_cast<uint2*>(to) = make_uint2(pack2(g.x, g.y), pack2(g.z, g.w));
+            *reinterpret_cast<uint2*>(to + I) = make_uint2(pack2(u.x, u.y), pack2(u.z, u.w));
+        }
+        *reinterpret_cast<uint2*>(gate.h + at) =
+            make_uint2(pack2(wr * (g.x * sigmoid(g.x)) * u.x, wr * (g.y * sigmoid(g.y)) * u.y),
+                       pack2(wr * (g.z * sigmoid(g.z)) * u.z, wr * (g.w * sigmoid(g.w)) * u.w));
+    }
+    named_sync(out);
+}
+
+// kGatedGrad: dh's 32 rows of 64 columns in v, their g and u in the lines; dg and du take
+// their place.  Returns this lane's row's sum of dh SiLU(g) u.
+__device__ __forceinline__ float gated_grad_lines(uint8_t* lines, const uint32_t (&v)[64], float w) {
+    const int lane = threadIdx.x & 31;
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        uint4* g_at = reinterpret_cast<uint4*>(lines + lane * 128 + ((k ^ (lane & 7)) << 4));
+        uint4* u_at = g_at + kStagingBytes / 16;
+        const uint4 gv = *g_at, uv = *u_at;
+        const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w}, u[4] = {uv.x, uv.y, uv.z, uv.w};
+        uint32_t dg[4], du[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a[2], b[2];
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const float x = __uint_as_float(v[k * 8 + 2 * j + o]);
+                const float gg = __uint_as_float(o ? g[j] & 0xffff0000u : g[j] << 16);
+                const float uu = __uint_as_float(o ? u[j] & 0xffff0000u : u[j] << 16);
+                const float s = sigmoid(gg), act = gg * s, y = w * x;
+                sum += x * act * uu;
+                a[o] = y * uu * (s * (1.0f + gg * (1.0f - s)));
+                b[o] = y * act;
+            }
+            dg[j] = pack2(a[0], a[1]);
+            du[j] = pack2(b[0], b[1]);
+        }
+        *g_at = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+        *u_at = make_uint4(du[0], du[1], du[2], du[3]);
+    }
+    return sum;
+}
+
 // kFew (products over rows): tiles of 256 columns of the output and BF rows, the matrix
 // being A and the rows B.  An MMA takes the same time for 1 row and for 128 of A, and 512
 // cycles a k-block for 256 of B, which is longer than the 32 KB of the matrix need to come
@@ -509,10 +653,13 @@ __device__ __forceinline__ void grouped_product(
     const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmOut,
     const int32_t* expert_offsets, const int32_t* expert_counts, int E,
     int R, int K, int m_out, int n_out, OutT* out, int accumulate, int a_groups,
-    int b_groups, int* err, int* tile_counter) {
+    int b_groups, int* err, int* tile_counter, const CUtensorMap& tmGu, const Gate& gate) {
     constexpr bool kW = kMode == kWeightsGrad;
+    constexpr bool kGate = kMode == kGated || kMode == kGatedGrad;
+    static_assert(!kGate || (!kSplit && !kLong && sizeof(OutT) == 2), "the gate's forms");
+    static_assert(kMode != kGatedGrad || !kFew, "a gate's gradient has no tiles of few rows");
     static_assert(!kW || !kFew, "a weights' gradient has no tiles of few rows");
-    constexpr int kStages = kStagesOf<kFew>, STAGE_BYTES = kStageBytes<kFew>;
+    constexpr int kStages = kStagesOf<kMode, kFew>, STAGE_BYTES = kStageBytes<kFew>;
     constexpr int kTileRows = kFew ? BF : BT;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -520,7 +667,7 @@ __device__ __forceinline__ void grouped_product(
     const uint32_t tiles_addr = smem_u32(tiles);
     uint8_t* staging_area = tiles + (size_t)kStages * STAGE_BYTES;
     auto* ctl = reinterpret_cast<Ctl<kMode, kFew>*>(staging_area +
-                                                    (size_t)kEpilogueWarps * kStagingBytes);
+                                                    (size_t)kEpilogueWarps * kStagingOf<kMode>);
     volatile int* abort_flag = &ctl->abort;
 
     constexpr int kChain = kChainBlocks<OutT>;
@@ -529,7 +676,7 @@ __device__ __forceinline__ void grouped_product(
     constexpr bool kSums = sizeof(OutT) == 4 || kFew;
     static_assert(!kSums || !kLong, "these take any length");
     constexpr bool kMnA = kW;                 // the contraction runs along tmA's rows
-    constexpr bool kMnB = kMode != kForward;  // and along tmB's
+    constexpr bool kMnB = kMode != kForward && kMode != kGated;  // and along tmB's
     // readers of a slot of the leader's queue: its producer, MMA thread,
     // epilogue warps (and block-end warp), and the peer's producer
     constexpr int kLocalReaders = kEpilogueWarps + (kW ? 1 : 0);
@@ -544,9 +691,9 @@ __device__ __forceinline__ void grouped_product(
     const uint16_t pair_mask = (uint16_t)(0x3u << first), leader_mask = (uint16_t)(0x1u << first);
     const bool leader = rank == 0;
     const int MB = blocks_of(m_out, BT);
-    const int NB = blocks_of(n_out, BT);
+    const int NB = blocks_of(n_out, kMode == kGated ? BT / 2 : BT);
     const int KB = blocks_of(K, BK);
-    const int n_last = kFew ? BT : last_columns(n_out, kMnB && b_groups);
+    const int n_last = kFew || kMode == kGated ? BT : last_columns(n_out, kMnB && b_groups);
 
     // one or two barriers a thread, not 63 and more of them one after the other
     static_assert(3 * kStages <= 64 && kQueueBarriers <= 64, "barriers of 64 threads");
@@ -559,6 +706,8 @@ __device__ __forceinline__ void grouped_product(
         if (i < kQueueBarriers) mbar_init(smem_u32(&ctl->tfull[0] + i), count);
         if (i < 3 * kStages) mbar_init(smem_u32(&ctl->full[0] + i), kW && i < kStages ? 2 : 1);
         if (i == 63) ctl->abort = 0;
+        if constexpr (kMode == kGatedGrad)
+            if (i < kEpilogueWarps) mbar_init(smem_u32(&ctl->lines[i]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0 && lane == 0) {
@@ -728,7 +877,7 @@ __device__ __forceinline__ void grouped_product(
                 // boxes of 64 columns where those come one by one
                 const bool two = half > 64;
                 const uint32_t stage_tx =
-                    kFew ? STAGE_BYTES
+                    kFew || kMode == kGated ? STAGE_BYTES
                          : OP_BYTES + (kMnB && !b_groups ? (two ? 2 : 1) * BOX_BYTES
                                                          : box_columns(n_out, kMnB) * BK * 2);
                 for (int kb = 0; kb < t.kblocks; ++kb) {
@@ -784,7 +933,15 @@ __device__ __forceinline__ void grouped_product(
                         if (leader) mbar_expect_tx(full_local, 2 * stage_tx);
                         tma_load_2d_pair(r_s, &tmA, full, k,
                                          off + (kFew ? t.mb * BF + (int)rank * (BF / 2) : a0));
-                        if (kMnB && b_groups) {
+                        if (kMode == kGated && kFew) {
+                            // each CTA has 64 gate columns and their up columns
+                            const int c0 = t.nb * BH + (int)rank * 64;
+                            tma_load_4d_pair(w_s, &tmB, full, k, c0, 0, t.e);
+                            tma_load_4d_pair(w_s + BOX_BYTES, &tmB, full, k, c0, 1, t.e);
+                        } else if (kMode == kGated) {
+                            // one CTA brings the gate columns, one the up columns
+                            tma_load_4d_pair(w_s, &tmB, full, k, t.nb * BH, (int)rank, t.e);
+                        } else if (kMnB && b_groups) {
                             tma_load_4d_pair(w_s, &tmB, full, 0, k, b0 / 64, t.e);
                         } else if (kMnB) {
                             tma_load_3d_pair(w_s, &tmB, full, b0, k, t.e);
@@ -936,10 +1093,10 @@ __device__ __forceinline__ void grouped_product(
         const int q = warp & 3;               // TMEM lane quadrant
         const int half = (warp - 4) >> 2;     // 128 columns of the tile, or 32 of its few rows
         constexpr int kCols = kFew ? BF / 2 : kEpilogueCols;  // of the accumulator
-        uint8_t* staging = staging_area + (size_t)(warp - 4) * kStagingBytes;
+        uint8_t* staging = staging_area + (size_t)(warp - 4) * kStagingOf<kMode>;
         const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[0]), first);
         int acc = 0;
-        uint32_t acc_phase = 0;
+        uint32_t acc_phase = 0, lines_phase = 0;
         for (int i = 0;; ++i) {
             Tile t = {};
             if (!warp_next(ctl, i, leader, abort_flag, err, t)) break;
@@ -969,6 +1126,86 @@ __device__ __forceinline__ void grouped_product(
                     acc_phase ^= 1u;
                 }
             };
+            if constexpr (kMode == kGated && kFew) {
+                const int left = t.cnt - t.mb * BF - half * 32, rows = left < 32 ? left : 32;
+                const long long row = (long long)t.off + t.mb * BF + half * 32;
+                const float w = lane < rows ? row_weight(gate, row + lane) : 0.0f;
+                const int in = 1 + half * 2 + (q & 1), out_id = in + 4;
+                if (!ready()) {
+                    // the warp of the other half of these columns may be waiting already
+                    named_arrive(in);
+                    named_arrive(out_id);
+                    break;
+                }
+                uint32_t v[32];
+                tmem_ld32(part(), v);
+                tmem_wait_ld();
+                release();
+                gated_few_out(gate, staging_area, q, half, v, row, rows,
+                              t.nb * BH + (int)rank * 64 + (q & 1) * 32, n_out, w, in, out_id);
+                continue;
+            } else if constexpr (kMode == kGated) {
+                const int at_row = t.mb * BT + (int)rank * BH + q * 32, rows = t.cnt - at_row;
+                const long long row = (long long)t.off + at_row;
+                const float w = lane < rows ? row_weight(gate, row + lane) : 0.0f;
+                if (!ready()) break;
+                const uint32_t g_at = tmem + ((uint32_t)(q * 32) << 16) +
+                                      (uint32_t)(acc * BT + half * 64);
+                gated_out(tmGu, tmOut, gate, staging, g_at, g_at + BT / 2, row, rows,
+                          t.nb * BH + half * 64, n_out, w, release);
+                continue;
+            } else if constexpr (kMode == kGatedGrad) {
+                const int at_row = t.mb * BT + (int)rank * BH + q * 32, rows = t.cnt - at_row;
+                const int col = t.nb * BT + half * kEpilogueCols;
+                const long long row = (long long)t.off + at_row;
+                const int have = rows <= 0 || col >= n_out ? 0 : n_out - col > 64 ? 2 : 1;
+                const uint32_t bar = smem_u32(&ctl->lines[warp - 4]);
+                const auto fetch = [&](int c) {
+                    if (lane != 0) return;
+                    bulk_wait_read();  // what went out from there has been read
+                    mbar_expect_tx(bar, 2 * kStagingBytes);
+                    tma_load_3d(smem_u32(staging), &tmGu, bar, col + c * 64, 0, (int)row);
+                    tma_load_3d(smem_u32(staging) + kStagingBytes, &tmGu, bar, col + c * 64, 1,
+                                (int)row);
+                };
+                if (have > 0) fetch(0);
+                const float w = lane < rows ? row_weight(gate, row + lane) : 0.0f;
+                if (!ready()) break;
+                const uint32_t at = part();
+                if (have == 0) {
+                    release();
+                    continue;
+                }
+                float sum = 0.0f;
+                int ok = 1;
+#pragma unroll 1
+                for (int c = 0; c < have; ++c) {
+                    uint32_t v[64];
+                    tmem_ld_line(at + c * 64, v);
+                    tmem_wait_ld();
+                    if (c == have - 1) release();
+                    if (!wait_bar(bar, lines_phase, abort_flag, err)) ok = 0;
+                    lines_phase ^= 1u;
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    sum += gated_grad_lines(staging, v, w);
+                    const int left = n_out - col - c * 64;
+                    uint16_t* to = gate.gu + row * 2 * n_out + col + c * 64;
+                    lines_out(&tmOut, staging, col + c * 64, 0, (int)row, true, to, 2 * n_out,
+                              rows, left);
+                    lines_out(&tmOut, staging + kStagingBytes, col + c * 64, 1, (int)row, true,
+                              to + n_out, 2 * n_out, rows, left);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (c + 1 < have) fetch(c + 1);
+                }
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (gate.parts && lane < rows)
+                    gate.parts[(long long)(col / kEpilogueCols) * R + row + lane] = sum;
+                fence_async_shared();
+                __syncwarp();
+                continue;
+            }
+
             const int chains = kSums ? (t.kblocks + kChain - 1) / kChain
                                      : (t.kblocks > 0 ? 1 : 0);
             uint32_t sum[kSums ? kCols / 32 : 1][32];
@@ -1173,7 +1410,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            int a_groups, int b_groups, int* err, int* tile_counter) {
     grouped_product<kMode, OutT, kFew, false, kLong>(tmA, tmB, tmOut, expert_offsets, expert_counts,
                                                      E, R, K, m_out, n_out, out, accumulate,
-                                                     a_groups, b_groups, err, tile_counter);
+                                                     a_groups, b_groups, err, tile_counter, tmOut,
+                                                     Gate{});
 }
 // Launched with clusters of 2 * splits CTAs.
 template <int kMode, typename OutT, bool kFew, bool kLong>
@@ -1187,7 +1425,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  int a_groups, int b_groups, int* err, int* tile_counter) {
     grouped_product<kMode, OutT, kFew, true, kLong>(tmA, tmB, tmOut, expert_offsets, expert_counts, E,
                                                     R, K, m_out, n_out, out, accumulate, a_groups,
-                                                    b_groups, err, tile_counter);
+                                                    b_groups, err, tile_counter, tmOut, Gate{});
+}
+// tmGu: gu as gate and up columns, [N*k][2][I]; tmOut: h, or the gradient of gu likewise.
+template <int kMode, bool kFew>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gated_product_kernel(const __grid_constant__ CUtensorMap tmA,
+                         const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmOut,
+                         const __grid_constant__ CUtensorMap tmGu, const Gate gate,
+                         const int32_t* expert_offsets, const int32_t* expert_counts, int E, int R,
+                         int K, int I, int b_groups, int* err, int* tile_counter) {
+    grouped_product<kMode, __nv_bfloat16, kFew, false, false>(
+        tmA, tmB, tmOut, expert_offsets, expert_counts, E, R, K, 0, I,
+        reinterpret_cast<__nv_bfloat16*>(gate.h), 0, 0, b_groups, err, tile_counter, tmGu, gate);
+}
+
+// dtopk_w of each pair: its row's sums of all 128-column parts, in their order.  A pair whose
+// row no expert has keeps what is there; only where the experts have fewer rows than there are
+// does a row look for its own.
+__global__ void __launch_bounds__(256)
+    gate_weight_grad_kernel(const float* parts, int n_parts, const int32_t* expert_offsets,
+                            const int32_t* expert_counts, int E, const int32_t* pair_row,
+                            long long R, float* dtopk_w) {
+    __shared__ unsigned long long had[8];
+    after_previous();
+    long long rows = 0;
+    for (int e = threadIdx.x; e < E; e += 256) rows += expert_counts[e];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, o);
+    if ((threadIdx.x & 31) == 0) had[threadIdx.x >> 5] = (unsigned long long)rows;
+    __syncthreads();
+    rows = 0;
+    for (int w = 0; w < 8; ++w) rows += (long long)had[w];
+    const long long pair = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (pair >= R) return;
+    const int row = pair_row[pair];
+    if (row < 0 || row >= R) return;
+    bool mine = rows >= R;
+    for (int e = 0; !mine && e < E; ++e) {
+        const int off = expert_offsets[e];
+        mine = row >= off && row - off < expert_counts[e];
+    }
+    if (!mine) return;
+    float sum = 0.0f;
+    for (int p = 0; p < n_parts; ++p) sum += parts[p * R + row];
+    dtopk_w[pair] = sum;
 }
 
 // Clusters of 2 * splits CTAs that the device holds at once; -1: the query failed.
@@ -1363,6 +1646,80 @@ moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const Gemm
     return out_f32 ? with(launch<kWeightsGrad, float>) : with(launch<kWeightsGrad, __nv_bfloat16>);
 }
 
+// gu (or its gradient) [N*k, 2*I] as [N*k][2][I], in boxes of 32 rows of 64 columns of a half.
+bool map_gu(CUtensorMap* m, const void* ptr, long long R, int I) {
+    const uint64_t sizes[3] = {(uint64_t)I, 2, (uint64_t)R};
+    const uint64_t strides[2] = {(uint64_t)I * 2, (uint64_t)I * 4};
+    const uint32_t box[3] = {64, 1, 32};
+    return map_tiled(m, 3, ptr, sizes, strides, box);
+}
+
+template <int kMode, bool kFew>
+moe_status launch_gated(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+                        const CUtensorMap& gu, const Gate& gate, const GemmGroup& g,
+                        long long tiles, int K, int I, int b_groups, cudaStream_t st) {
+    if (tiles >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
+    constexpr size_t smem = smem_bytes<kMode, kFew>();
+    static OncePerDevice set;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    if (!set.done(dev)) {
+        if (cudaFuncSetAttribute(gated_product_kernel<kMode, kFew>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        set.finish(dev);
+    }
+    const long long pairs_max = sm_count() / 2;
+    const long long pairs = tiles < pairs_max ? tiles : pairs_max;
+    return cuda_status(launch_chained(gated_product_kernel<kMode, kFew>,
+                                      (int)(2 * (pairs > 0 ? pairs : 1)), kThreads, smem, st, a, b,
+                                      o, gu, gate, g.offsets, g.counts, g.E, (int)g.R, K, I,
+                                      b_groups, g.err, g.prefix + g.E + 1));
+}
+
+moe_status launch_gated_forward(const uint16_t* rows, const GemmGroup& g, int c_in, int I,
+                                const uint16_t* w, const Gate& gate, cudaStream_t st) {
+    CUtensorMap a, b, o, gu;
+    const long long used = g.R < g.E ? g.R : g.E;  // experts with rows, at most
+    const bool few = g.R <= kFewRows * used;
+    const uint64_t sizes[4] = {(uint64_t)c_in, (uint64_t)I, 2, (uint64_t)g.E};
+    const uint64_t strides[3] = {(uint64_t)c_in * 2, (uint64_t)c_in * I * 2,
+                                 (uint64_t)c_in * I * 4};
+    const uint32_t box[4] = {BK, (uint32_t)(few ? 64 : BH), 1, 1};
+    if (!map_rows(&a, rows, 0, g.R, c_in, few ? BF / 2 : BH) ||
+        !map_tiled(&b, 4, w, sizes, strides, box) || !map_lines(&o, gate.h, 0, g.R, I, false))
+        return MOE_ERR_UNSUPPORTED;
+    gu = o;
+    if (gate.gu && !map_gu(&gu, gate.gu, g.R, I)) return MOE_ERR_UNSUPPORTED;
+    const long long tiles = (used + (g.R - used) / (few ? BF : BT)) * blocks_of(I, BT / 2);
+    return few ? launch_gated<kGated, true>(a, b, o, gu, gate, g, tiles, c_in, I, 0, st)
+               : launch_gated<kGated, false>(a, b, o, gu, gate, g, tiles, c_in, I, 0, st);
+}
+
+moe_status launch_gated_grad(const uint16_t* dout, const GemmGroup& g, int c_out, int I,
+                             const uint16_t* w, const uint16_t* gu_in, const Gate& gate,
+                             float* dtopk_w, cudaStream_t st) {
+    CUtensorMap a, b, o, gu;
+    int groups = 0;
+    if (!map_rows(&a, dout, 0, g.R, c_out, BH) ||
+        !map_mn(&b, w, g.E, c_out, I, box_columns(I, true), &groups) ||
+        !map_gu(&gu, gu_in, g.R, I) || !map_gu(&o, gate.gu, g.R, I))
+        return MOE_ERR_UNSUPPORTED;
+    const long long used = g.R < g.E ? g.R : g.E;
+    const long long tiles = (used + (g.R - used) / BT) * blocks_of(I, BT);
+    MOE_TRY(launch_gated<kGatedGrad, false>(a, b, o, gu, gate, g, tiles, c_out, I, groups, st));
+    if (!dtopk_w) return MOE_OK;
+    return cuda_status(launch_chained(gate_weight_grad_kernel, (int)((g.R + 255) / 256), 256, 0, st,
+                                      (const float*)gate.parts, blocks_of(I, kEpilogueCols),
+                                      g.offsets, g.counts, g.E, gate.pair_row, g.R, dtopk_w));
+}
+
+// Contractions up to this are one chain of an accumulator (see "Precision").
+constexpr int kMaxGateTerms = kChainBlocks<__nv_bfloat16> * BK;
+
+size_t gated_parts_offset(const moe_shape& s) { return workspace_layout(s).total; }
+
 moe_status check_grouped(const moe_layout* layout, const moe_shape* shape, int32_t C_in,
                          int32_t C_out, int32_t out_type, void* ws, size_t ws_bytes) {
     MOE_TRY(check_shape(shape));
@@ -1408,6 +1765,45 @@ moe_status moe_grouped_gemm_input_grad(const uint16_t* dout, const moe_layout* l
     if (!aligned16(dout, w, drows)) return MOE_ERR_INVALID_ARG;
     return launch_rows(dout, routed_group(*layout, *shape, ws), C_in, C_out, w, drows,
                        out_type == MOE_TYPE_F32, true, as_stream(stream));
+}
+
+size_t moe_gated_workspace_bytes(const moe_shape* shape) {
+    if (check_shape(shape) != MOE_OK) return 0;
+    return gated_parts_offset(*shape) +
+           align256((size_t)shape->N * shape->k * blocks_of(shape->I, kEpilogueCols) * 4);
+}
+
+moe_status moe_gated_gemm(const uint16_t* rows, const moe_layout* layout, const moe_shape* shape,
+                          int32_t C_in, const uint16_t* w_gate_up, const float* topk_w,
+                          uint16_t* gu, uint16_t* h, void* ws, size_t ws_bytes, void* stream) {
+    MOE_RANGE();
+    MOE_TRY(check_grouped(layout, shape, C_in, 8, MOE_TYPE_BF16, ws, ws_bytes));
+    if (C_in > kMaxGateTerms) return MOE_ERR_UNSUPPORTED;
+    if (shape->N == 0) return MOE_OK;
+    if (!rows || !w_gate_up || !h) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(rows, w_gate_up, gu, h)) return MOE_ERR_INVALID_ARG;
+    const Gate gate = {topk_w, layout->row_token, layout->pair_row, shape->N, shape->k,
+                       h,      gu,                nullptr};
+    return launch_gated_forward(rows, routed_group(*layout, *shape, ws), C_in, shape->I, w_gate_up,
+                                gate, as_stream(stream));
+}
+
+moe_status moe_gated_gemm_grad(const uint16_t* dout, const moe_layout* layout,
+                               const moe_shape* shape, int32_t C_out, const uint16_t* w_down,
+                               const float* topk_w, const uint16_t* gu, uint16_t* dgu,
+                               float* dtopk_w, void* ws, size_t ws_bytes, void* stream) {
+    MOE_RANGE();
+    MOE_TRY(check_grouped(layout, shape, 8, C_out, MOE_TYPE_BF16, ws, ws_bytes));
+    if (ws_bytes < moe_gated_workspace_bytes(shape)) return MOE_ERR_WORKSPACE;
+    if (C_out > kMaxGateTerms) return MOE_ERR_UNSUPPORTED;
+    if (shape->N == 0) return MOE_OK;
+    if (!dout || !w_down || !gu || !dgu) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(dout, w_down, gu, dgu)) return MOE_ERR_INVALID_ARG;
+    float* parts = dtopk_w ? ws_ptr<float>(ws, gated_parts_offset(*shape)) : nullptr;
+    const Gate gate = {topk_w,  layout->row_token, layout->pair_row, shape->N, shape->k,
+                       nullptr, dgu,               parts};
+    return launch_gated_grad(dout, routed_group(*layout, *shape, ws), C_out, shape->I, w_down, gu,
+                             gate, dtopk_w, as_stream(stream));
 }
 
 moe_status moe_grouped_gemm_weight_grad(const uint16_t* dout, const uint16_t* rows,

@@ -102,6 +102,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_grouped_gemm_weight_grad": (I32, [P, P, lay, shp, I32, I32, P, I32, I32, P, S, P]),
         "moe_swiglu": (I32, [P, P, lay, shp, P, P]),
         "moe_swiglu_grad": (I32, [P, P, P, lay, shp, P, P, P]),
+        "moe_gated_workspace_bytes": (S, [shp]),
+        "moe_gated_gemm": (I32, [P, lay, shp, I32, P, P, P, P, P, S, P]),
+        "moe_gated_gemm_grad": (I32, [P, lay, shp, I32, P, P, P, P, P, P, S, P]),
         "moe_route_grad": (I32, [P, P, P, shp, P, P]),
         "moe_route_full_softmax_grad": (I32, [P, P, P, shp, P, P]),
         "moe_route_sigmoid_bias_grad": (I32, [P, P, P, shp, P, P]),
@@ -652,6 +655,48 @@ def moe_swiglu_grad(dh, gu, topk_w, layout: Layout, shape: Shape, dgu, dtopk_w, 
         s.ref, _exact(dgu, torch.bfloat16, (s.R, 2 * s.I), "dgu"),
         _exact(dtopk_w, torch.float32, (s.N, s.k), "dtopk_w"), _stream(stream)),
         "moe_swiglu_grad")
+
+
+def moe_gated_workspace_bytes(shape: Shape) -> int:
+    return int(load().moe_gated_workspace_bytes(shape.ref))
+
+
+def gated_workspace(shape: Shape, device="cuda") -> torch.Tensor:
+    n = moe_gated_workspace_bytes(shape)
+    if n == 0:
+        raise MoeError(1, "moe_gated_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:moe_workspace_bytes(shape)].zero_()
+    return ws
+
+
+def moe_gated_gemm(rows, layout: Layout, shape: Shape, w_gate_up, topk_w, gu, h, ws, stream=None):
+    """[g | u] = rows[i] Wgu[e]^T and h[i] = w_i SiLU(g) u in one kernel; w_gate_up
+    [E, 2*I, C_in] bf16, gu [N*k, 2*I] bf16 (None: not wanted), h [N*k, I] bf16."""
+    s, bf = shape, torch.bfloat16
+    w_at, co, ci = _expert_matrices(w_gate_up, bf, s, "w_gate_up")
+    if co != 2 * s.I:
+        raise ValueError(f"w_gate_up: expected 2*I = {2 * s.I} rows, got {co}")
+    _check(load().moe_gated_gemm(
+        _exact(rows, bf, (s.R, ci), "rows"), _lay(layout, s), s.ref, ci, w_at,
+        _exact(topk_w, torch.float32, (s.N, s.k), "topk_w"), _exact(gu, bf, (s.R, 2 * s.I), "gu"),
+        _exact(h, bf, (s.R, s.I), "h"), *_bytes(ws), _stream(stream)), "moe_gated_gemm")
+
+
+def moe_gated_gemm_grad(dout, layout: Layout, shape: Shape, w_down, topk_w, gu, dgu, dtopk_w, ws,
+                        stream=None):
+    """dgu [N*k, 2*I] (may be gu) and dtopk_w fp32 [N, k] (None: not wanted) from
+    dh = dout[i] Wd[e], w_down [E, C_out, I] bf16; ws of gated_workspace(shape)."""
+    s, bf = shape, torch.bfloat16
+    w_at, co, ci = _expert_matrices(w_down, bf, s, "w_down")
+    if ci != s.I:
+        raise ValueError(f"w_down: expected I = {s.I} columns, got {ci}")
+    _check(load().moe_gated_gemm_grad(
+        _exact(dout, bf, (s.R, co), "dout"), _lay(layout, s), s.ref, co, w_at,
+        _exact(topk_w, torch.float32, (s.N, s.k), "topk_w"), _exact(gu, bf, (s.R, 2 * s.I), "gu"),
+        _exact(dgu, bf, (s.R, 2 * s.I), "dgu"),
+        _exact(dtopk_w, torch.float32, (s.N, s.k), "dtopk_w"), *_bytes(ws), _stream(stream)),
+        "moe_gated_gemm_grad")
 
 
 def moe_route_grad(topk_ids, topk_w, dtopk_w, shape: Shape, dlogits, stream=None):

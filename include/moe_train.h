@@ -84,6 +84,31 @@ moe_status moe_swiglu_grad(const uint16_t* dh, const uint16_t* gu, const float* 
                            const moe_layout* layout, const moe_shape* shape, uint16_t* dgu,
                            float* dtopk_w, void* stream);
 
+/* An expert's gated feed-forward block up to its down product, in one kernel, and back:
+ *   moe_gated_gemm       [g | u] = rows[i, :] Wgu[e]^T
+ *                        h[i, :]  = bf16( w_i * SiLU(g) * u )
+ *   moe_gated_gemm_grad  dh = dout[i, :] Wd[e]
+ *                        dgu[i, :] = bf16( w_i * dh * u * SiLU'(g) ), bf16( w_i * dh * SiLU(g) )
+ *                        dtopk_w[t, j] = sum over the columns of dh * SiLU(g) * u
+ * with the rows, segments and w_i of the calls above: moe_grouped_gemm and moe_swiglu in one,
+ * moe_grouped_gemm_input_grad and moe_swiglu_grad in one, but g, u and dh go from one to the
+ * other in fp32.  rows bf16 [N*k, C_in], w_gate_up bf16 [E, 2*I, C_in] (gate rows first), h
+ * bf16 [N*k, I]; gu bf16 [N*k, 2*I] receives g and u for the gradient (NULL: not wanted).
+ * dout bf16 [N*k, C_out], w_down bf16 [E, C_out, I], dgu bf16 [N*k, 2*I] (may be gu itself),
+ * dtopk_w fp32 [N, k] (NULL: not wanted).  topk_w may be NULL (weights of one).  shape gives
+ * N, k, E and I; C_in and C_out are multiples of 8, at most 32768.
+ * ws: workspace of moe_gated_workspace_bytes(shape) bytes (moe_gated_gemm: of
+ * moe_workspace_bytes(shape)), on a 4-byte boundary, its first moe_workspace_bytes(shape)
+ * bytes zero at first. */
+size_t moe_gated_workspace_bytes(const moe_shape* shape);
+moe_status moe_gated_gemm(const uint16_t* rows, const moe_layout* layout, const moe_shape* shape,
+                          int32_t C_in, const uint16_t* w_gate_up, const float* topk_w,
+                          uint16_t* gu, uint16_t* h, void* ws, size_t ws_bytes, void* stream);
+moe_status moe_gated_gemm_grad(const uint16_t* dout, const moe_layout* layout,
+                               const moe_shape* shape, int32_t C_out, const uint16_t* w_down,
+                               const float* topk_w, const uint16_t* gu, uint16_t* dgu,
+                               float* dtopk_w, void* ws, size_t ws_bytes, void* stream);
+
 /* Gradient of the router's logits, fp32 [N, E], from that of the routing
  * weights, dtopk_w fp32 [N, k], one call per router of moe.h:
  *   moe_route_grad               of moe_route (softmax over the selected k);
