@@ -1,4 +1,4 @@
-"""Python binding of libmoe (include/moe.h, include/moe_train.h): argument marshalling only.
+"""Python binding of libmoe (include/moe.h, moe_train.h, moe_w4.h): argument marshalling only.
 
 Every function below has the name of the C entry point it calls and takes
 torch CUDA tensors in place of device pointers.  All arithmetic runs in the
@@ -48,6 +48,10 @@ class MoeMuonShape(ctypes.Structure):
         [("momentum", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class MoeW4Matrix(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("C_out", "C_in", "group", "gated")]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -68,6 +72,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     P, S, I32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
     shp, lay = ctypes.POINTER(MoeShape), ctypes.POINTER(MoeLayout)
     nrm, muon = ctypes.POINTER(MoeNormShape), ctypes.POINTER(MoeMuonShape)
+    w4m = ctypes.POINTER(MoeW4Matrix)
     sigs = {
         "moe_workspace_bytes": (S, [shp]),
         "moe_packed_gate_up_bytes": (S, [shp]),
@@ -114,6 +119,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                       P]),
         "moe_muon_workspace_bytes": (S, [muon]),
         "moe_muon_update": (I32, [P, P, muon, P, P, P, S, P]),
+        "moe_w4_quantize": (I32, [P, ctypes.c_int64, I32, I32, P, P, P]),
+        "moe_w4_packed_bytes": (S, [w4m, I32]),
+        "moe_w4_pack": (I32, [P, P, w4m, I32, P, P]),
+        "moe_w4_workspace_bytes": (S, [shp]),
+        "moe_w4_gemm": (I32, [P, lay, shp, w4m, P, P, I32, P, S, P]),
+        "moe_w4_gated_gemm": (I32, [P, lay, shp, w4m, P, P, P, P, S, P]),
         "moe_selftest_wait_timeout": (I32, [P, ctypes.c_int64, P]),
         "moe_get_error": (I32, [P, P]),
         "moe_status_str": (ctypes.c_char_p, [I32]),
@@ -867,6 +878,105 @@ def moe_muon_update(grad, momentum, shape: MuonShape, update, ws, new_momentum=N
         s._refs[grad.dtype], _exact(update, torch.bfloat16, size, "update"),
         _exact(new_momentum, torch.float32, size, "new_momentum"), *_bytes(ws), _stream(stream)),
         "moe_muon_update")
+
+
+# ---- experts with 4-bit weights (include/moe_w4.h) --------------------------------------
+
+class W4Matrices:
+    """E packed matrices of 4-bit weights [C_out, C_in] that share a scale by groups, or
+    stacked gate and up ones [2*C_out, C_in] (gated); made by pack_w4 or quantize_w4."""
+
+    def __init__(self, E: int, C_out: int, C_in: int, group: int, gated: bool, device="cuda"):
+        self.E, self.C_out, self.C_in, self.group, self.gated = E, C_out, C_in, group, bool(gated)
+        self.ref = ctypes.byref(MoeW4Matrix(C_out, C_in, group, int(self.gated)))
+        n = int(load().moe_w4_packed_bytes(self.ref, E))
+        if n == 0:
+            raise MoeError(1, "moe_w4_packed_bytes")
+        self.data = torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_w4_quantize(w, q, scales, stream=None):
+    """q uint8 [..., C_in / 2] and scales bf16 [..., C_in / group] of bf16 weights
+    w [..., C_in], a scale for each group; the group is that of the scales' size."""
+    if not isinstance(w, torch.Tensor) or not isinstance(scales, torch.Tensor):
+        raise TypeError("w, scales: expected torch tensors")
+    ci, groups = w.shape[-1], scales.shape[-1]
+    if groups == 0 or ci % groups != 0:
+        raise ValueError(f"scales: {groups} groups do not share {ci} columns")
+    _check(load().moe_w4_quantize(
+        _exact(w, torch.bfloat16, w.shape, "w"), w.numel() // ci if ci else 0, ci, ci // groups,
+        _exact(q, torch.uint8, (*w.shape[:-1], ci // 2), "q"),
+        _exact(scales, torch.bfloat16, (*w.shape[:-1], groups), "scales"), _stream(stream)),
+        "moe_w4_quantize")
+
+
+def moe_w4_pack(q, scales, w4: W4Matrices, stream=None):
+    """q uint8 [E, rows, C_in / 2] (weight 2i in the low four bits of byte i) and scales bf16
+    [E, rows, C_in / group] into w4; rows: C_out, or 2*C_out (gate rows first) of a gated."""
+    rows = w4.C_out * (2 if w4.gated else 1)
+    _check(load().moe_w4_pack(
+        _exact(q, torch.uint8, (w4.E, rows, w4.C_in // 2), "q"),
+        _exact(scales, torch.bfloat16, (w4.E, rows, w4.C_in // w4.group), "scales"),
+        w4.ref, w4.E, _exact(w4.data, torch.uint8, w4.data.shape, "w4"), _stream(stream)),
+        "moe_w4_pack")
+
+
+def pack_w4(q, scales, gated=False, stream=None) -> W4Matrices:
+    """Weights quantised elsewhere, packed for the products."""
+    if q.dim() != 3 or scales.dim() != 3 or scales.shape[2] == 0 or (gated and q.shape[1] % 2):
+        raise ValueError("q and scales: expected [E, rows, C_in / 2] and [E, rows, C_in / group]")
+    E, rows, ci = q.shape[0], q.shape[1], q.shape[2] * 2
+    w4 = W4Matrices(E, rows // 2 if gated else rows, ci, ci // scales.shape[2], gated, q.device)
+    moe_w4_pack(q, scales, w4, stream)
+    return w4
+
+
+def quantize_w4(w, group=128, gated=False, stream=None) -> W4Matrices:
+    """bf16 matrices [E, rows, C_in], quantised by groups and packed."""
+    E, rows, ci = w.shape
+    q = torch.empty(E, rows, ci // 2, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(E, rows, ci // group, dtype=torch.bfloat16, device=w.device)
+    moe_w4_quantize(w, q, scales, stream)
+    return pack_w4(q, scales, gated, stream)
+
+
+def moe_w4_workspace_bytes(shape: Shape) -> int:
+    return int(load().moe_w4_workspace_bytes(shape.ref))
+
+
+def w4_workspace(shape: Shape, device="cuda") -> torch.Tensor:
+    n = moe_w4_workspace_bytes(shape)
+    if n == 0:
+        raise MoeError(1, "moe_w4_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _w4(w4, shape: Shape, gated):
+    if not isinstance(w4, W4Matrices):
+        raise TypeError("w4: expected W4Matrices")
+    if w4.E != shape.E or w4.gated != gated:
+        raise ValueError(f"w4: expected {'gated' if gated else 'plain'} matrices of E = {shape.E}")
+    return w4.data.data_ptr()
+
+
+def moe_w4_gemm(rows, layout: Layout, shape: Shape, w4: W4Matrices, out, ws, stream=None):
+    """out[i] = rows[i] W[e]^T; out [N*k, C_out] bf16 or fp32; ws of w4_workspace(shape)."""
+    at, ot, R = _w4(w4, shape, False), _out_type(out, "out"), shape.R
+    _check(load().moe_w4_gemm(
+        _exact(rows, torch.bfloat16, (R, w4.C_in), "rows"), _lay(layout, shape), shape.ref,
+        w4.ref, at, _exact(out, out.dtype, (R, w4.C_out), "out"), ot, *_bytes(ws),
+        _stream(stream)), "moe_w4_gemm")
+
+
+def moe_w4_gated_gemm(rows, layout: Layout, shape: Shape, w4: W4Matrices, topk_w, h, ws,
+                      stream=None):
+    """h[i] = w_i SiLU(g) u of [g | u] = rows[i] W[e]^T; h [N*k, C_out] bf16."""
+    at, R = _w4(w4, shape, True), shape.R
+    _check(load().moe_w4_gated_gemm(
+        _exact(rows, torch.bfloat16, (R, w4.C_in), "rows"), _lay(layout, shape), shape.ref,
+        w4.ref, at, _exact(topk_w, torch.float32, (shape.N, shape.k), "topk_w"),
+        _exact(h, torch.bfloat16, (R, w4.C_out), "h"), *_bytes(ws), _stream(stream)),
+        "moe_w4_gated_gemm")
 
 
 def moe_selftest_wait_timeout(ws, limit_cycles: int, stream=None):
