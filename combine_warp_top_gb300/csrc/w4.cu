@@ -6,14 +6,17 @@
 // gate rows and I up rows, and h = w_i SiLU(g) u leaves instead of y.
 //
 // Memory bound: every weight is read once, 4 bits and its share of a scale.  So the packed
-// layout (pack_kernel) is the order in which the kernel reads: tiles of 256 matrix rows, in
-// chunks of 128 weights of each row, one chunk of a tile a contiguous piece of 17 to 18 KB that
-// one bulk copy brings into a ring of shared memory, the scales beside the weights.  The rows'
-// chunks come by TMA boxes of 8 rows.  A chunk's work: a warp has 32 rows of the matrix, whose
-// weights become bf16 operands of mma.sync m16n8k16 in registers (q | 0x4300 is the number 128 +
-// q, less 136: exact), the rows being its 8 columns; a group's products are summed in fp32 and
-// then scaled once, in fp32.  tcgen05 would need the weights as bf16 in shared memory, four
-// times the bytes that arrive, for MMAs of 8 columns.
+// layout (w4_pack_kernel) is the order in which the kernel reads: tiles of 128 matrix rows in
+// chunks of 128 weights of each, one chunk of a tile a contiguous piece of 8 to 9 KB that one
+// bulk copy brings into a ring of shared memory, the scales beside the weights.  The rows'
+// chunks come by TMA boxes of 8 rows.
+//
+// The matrix is the MMA's A and the rows are its B (tcgen05, M = 128, N = 16 to 64).  A thread
+// has one row of the matrix: it widens the row's weights to bf16 in registers (q | 0x4300 is
+// the number 128 + q, less 136: exact) and stores them into TMEM, from where the MMA takes A:
+// shared memory sees the 4-bit form only.  A group's sums are fp32 in TMEM; the thread reads
+// its row's, scales them once and adds them to its own sums, in fp32, while the MMAs of the
+// next 64 weights run.
 #include <stddef.h>
 
 #include "../../include/moe_train.h"
@@ -28,19 +31,20 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kSlabRows = 32;      // matrix rows of a warp
-constexpr int kSlabs = 8;          // warps' slabs of a tile
-constexpr int kChunk = 128;        // weights of a row in a chunk
+constexpr int kSlabRows = 32;  // matrix rows of a warp
+constexpr int kSlabs = 4;      // warps of a tile
+constexpr int kTileRows = kSlabRows * kSlabs;
+constexpr int kChunk = 128;    // weights of a row in a chunk
 constexpr int kNibbleBytes = kSlabRows * kChunk / 2;
 constexpr int kConsumers = kSlabs * 32;
 constexpr int kThreads = kConsumers + 32;
-constexpr int kMaxBlocks = 304;
+constexpr int kMaxBlocks = 608;
 
 __host__ __device__ __forceinline__ int ceil_div(long long a, int b) {
     return (int)((a + b - 1) / b);
 }
 // A slab's chunk: nibbles, then its scales.
-__host__ __device__ __forceinline__ int record_bytes(int group) {
+__host__ __device__ constexpr int record_bytes(int group) {
     return kNibbleBytes + kSlabRows * 2 * (kChunk / group);
 }
 
@@ -62,8 +66,7 @@ Matrix matrix_of(const moe_w4_matrix& m) {
     return d;
 }
 
-// Byte offset of a tile's chunk within an expert's packed matrix; the slabs of a tile's chunk
-// lie side by side.
+// The slabs of a tile's chunk lie side by side, the chunks of a tile one after the other.
 __host__ __device__ __forceinline__ int tile_slabs(const Matrix& m, int tile) {
     return m.slabs - tile * kSlabs < kSlabs ? m.slabs - tile * kSlabs : kSlabs;
 }
@@ -71,44 +74,36 @@ __host__ __device__ __forceinline__ long long chunk_at(const Matrix& m, int tile
     return ((long long)tile * kSlabs * m.chunks + (long long)chunk * tile_slabs(m, tile)) * m.record;
 }
 
-// The matrix row of a slab's row r (0..31), or -1.  A lane of the MMA holds rows l / 4 and l / 4
-// + 8 of two 16-row operands: those four are neighbours in the output, or two gate columns and
-// their up columns (`up`: whether it is one of these).
+// The output column of a slab's row r (0..31), or -1; up: whether the row is of the up matrix
+// (gated: 16 gate rows, then their 16 up rows).
 __device__ __forceinline__ int matrix_row(const Matrix& m, int slab, int r, bool* up) {
-    const int g = r & 7, which = r >> 3;  // which: 0, 1 first operand, 2, 3 second
-    int o;
-    if (m.gated) {
-        o = slab * 16 + 2 * g + (which & 1);
-        *up = which >= 2;
-    } else {
-        o = slab * 32 + 4 * g + which;
-        *up = false;
-    }
+    *up = m.gated && r >= 16;
+    const int o = m.gated ? slab * 16 + (r & 15) : slab * 32 + r;
     return o < m.rows ? o : -1;
-}
-
-// Weight j (0..3) of MMA step s (0..3) that the lanes l with l % 4 == c hold, within a half
-// chunk of 64: 16 neighbours a lane, or 8 of each group of 32.
-__device__ __forceinline__ int weight_of(int group, int c, int s, int j) {
-    return group == 32 ? (s >> 1) * 32 + c * 8 + (s & 1) * 4 + j : c * 16 + s * 4 + j;
 }
 
 // ---- the product ---------------------------------------------------------------------------
 
-template <int kNT>
-constexpr int kStagesOf = kNT == 1 ? 5 : kNT == 2 ? 4 : kNT == 4 ? 3 : 5;
-template <int kNT>
-constexpr int kBlocksPerSm = kNT <= 4 ? 2 : 1;
-constexpr int kMaxRecord = kNibbleBytes + kSlabRows * 2 * 4;
-constexpr int kWeightBytes = kSlabs * kMaxRecord;
-// the rows' boxes of a stage: two halves of 64 columns, 8 * kNT rows of 128 bytes
-template <int kNT>
-constexpr int kRowBytes = 2 * kNT * 1024;
-template <int kNT>
-constexpr size_t smem_bytes(int E) {
-    return 1024 + (size_t)kStagesOf<kNT> * (kWeightBytes + kRowBytes<kNT>) +
-           (size_t)(E + 1) * sizeof(long long);
-}
+// kN: rows of a pass at most (the MMA's N, in steps of 16).
+// A's two buffers of 64 weights a row, 32 columns each, and the sums of the groups that end in
+// one or the other.
+template <int kN, int kGroup>
+struct Form {
+    static constexpr int kHalfGroups = kGroup == 32 ? 2 : 1;  // sums of 64 weights
+    static constexpr int kSums = 64;                          // their first column
+    static constexpr int kUsed = kSums + 2 * kHalfGroups * kN;
+    static constexpr int kTmem = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    // of an SM; a thread with 32 sums takes the registers of three
+    static constexpr int kBlocks = kTmem == 512 ? 1 : kTmem == 256 ? 2 : kN == 16 ? 4 : 3;
+    static constexpr int kRecord = record_bytes(kGroup);
+    static constexpr int kWeightBytes = kSlabs * kRecord;
+    static constexpr int kRowBytes = 2 * kN * 128;  // two halves of 64 columns
+    // 4 blocks of an SM have 56 KB each, 3 have 74, 2 have 113
+    static constexpr int kStages = kBlocks == 4 ? (kGroup > 32 ? 4 : 3) : kN <= 32 ? 4 : 4;
+    static size_t smem(int E) {
+        return 1024 + (size_t)kStages * (kWeightBytes + kRowBytes) + (size_t)(E + 1) * 4;
+    }
+};
 
 struct Args {
     const uint8_t* packed;
@@ -134,54 +129,75 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
+// D[tmem] (+)= A[tmem] * B[smem]^T, bf16 inputs, fp32 accumulate, one CTA.
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
-// Eight nibbles to an operand: nibble r and nibble r + 4 are the halves of register r.
-__device__ __forceinline__ void widen(uint32_t w, uint32_t (&a)[4]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// (w & mask) | bits: one instruction, which takes two constants from registers only.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(mask), "r"(bits));
+    return v;
+}
+// Eight nibbles to four pairs: nibble r and nibble r + 4 are the halves of register r.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t* a) {
     const __nv_bfloat162 bias = __float2bfloat162_rn(136.0f);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const uint32_t v = ((w >> (4 * r)) & 0x000f000fu) | 0x43004300u;
+        const uint32_t v = and_or(w >> (4 * r), 0x000f000fu, 0x43004300u);
         const __nv_bfloat162 x = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), bias);
         a[r] = *reinterpret_cast<const uint32_t*>(&x);
     }
 }
 
-// A run of chunks of one tile for up to 8 * kNT rows of an expert.
+// A run of chunks of one tile for up to kN rows of an expert.
 struct Piece {
     int e, tile, first_row, rows;  // rows from first_row of the expert's on
     int chunk0, chunk1;            // of the tile's chunks
     long long start;               // the tile's first unit
 };
 
-// Units are chunks: expert by expert, tile by tile, the passes over 8 * kNT rows each side by
-// side (they read the same weights), chunk by chunk.
-template <int kNT>
-__device__ __forceinline__ Piece piece_at(const Args& a, const long long* prefix, long long u,
+// Units are chunks: expert by expert, tile by tile, the passes over kN rows each side by side
+// (they read the same weights), chunk by chunk.  prefix: passes before each expert.
+template <int kN>
+__device__ __forceinline__ Piece piece_at(const Args& a, const int* prefix, long long u,
                                           long long end) {
-    int lo = 0, hi = a.E;  // prefix[lo] <= u < prefix[hi]
+    const long long per_pass = (long long)a.m.tiles * a.m.chunks;
+    const int q = (int)(u / per_pass);
+    int lo = 0, hi = a.E;  // prefix[lo] <= q < prefix[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= u) lo = mid;
+        if (prefix[mid] <= q) lo = mid;
         else hi = mid;
     }
     Piece p;
     p.e = lo;
-    const long long local = u - prefix[lo];
-    const int cnt = a.counts[lo], passes = ceil_div(cnt, 8 * kNT);
+    const long long local = u - prefix[lo] * per_pass;
+    const int cnt = a.counts[lo], passes = prefix[lo + 1] - prefix[lo];
     const long long run = local / a.m.chunks;  // tile * passes + pass
     p.chunk0 = (int)(local - run * a.m.chunks);
     p.tile = (int)(run / passes);
     const int pass = (int)(run - (long long)p.tile * passes);
-    p.first_row = pass * 8 * kNT;
-    p.rows = cnt - p.first_row < 8 * kNT ? cnt - p.first_row : 8 * kNT;
+    p.first_row = pass * kN;
+    p.rows = cnt - p.first_row < kN ? cnt - p.first_row : kN;
     p.start = u - p.chunk0;
     const long long left = end - u;
     p.chunk1 = left < a.m.chunks - p.chunk0 ? p.chunk0 + (int)left : a.m.chunks;
@@ -193,45 +209,98 @@ __device__ __forceinline__ long long share(long long total, int b, int blocks) {
     return total * b / blocks;
 }
 
-template <int kNT>
-struct Sums {
-    float v[kNT][2][4];
-};
-
-// The sums of a tile's slab to their output.  w: the routing weights of rows `lane` and lane + 32.
-template <int kNT, bool kGated>
+// The sums of a tile's slab to their output.
+template <int kN, bool kGated>
 __device__ __forceinline__ void write_out(const Args& a, const Piece& p, int slab,
-                                          const Sums<kNT>& s, const float (&w)[2]) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+                                          const float (&s)[kN]) {
+    const int lane = threadIdx.x & 31;
     const long long row0 = (long long)a.offsets[p.e] + p.first_row;
+    if (kGated) {
+        // lanes l and l + 16 have the gate and the up column of the same output: the first
+        // takes the even rows, the second the odd ones
+        const bool upper = lane >= 16;
+        const int o = slab * 16 + (lane & 15);
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
+        for (int n = 0; n < kN; n += 2) {
+            if (n >= p.rows) break;
+            const float got = __shfl_xor_sync(0xffffffffu, upper ? s[n] : s[n + 1], 16);
+            const float g = upper ? got : s[n], u = upper ? s[n + 1] : got;
+            const int mine = n + upper;
+            if (mine >= p.rows || o >= a.m.rows) continue;
+            const long long row = row0 + mine;
+            const __nv_bfloat16 h = __float2bfloat16_rn(row_weight(a.gate, row) * (g * sigmoid(g)) * u);
+            a.gate.h[row * a.m.rows + o] = *reinterpret_cast<const uint16_t*>(&h);
+        }
+        return;
+    }
+    const int o = slab * 32 + lane;
+    if (o >= a.m.rows) return;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int n = nt * 8 + c * 2 + j;
-            const float wn = __shfl_sync(0xffffffffu, w[nt / 4], n & 31);
-            if (n >= p.rows) continue;
-            // the lane's four matrix rows for this row
-            const float v0 = s.v[nt][0][j], v1 = s.v[nt][0][2 + j];
-            const float v2 = s.v[nt][1][j], v3 = s.v[nt][1][2 + j];
-            const long long at = (row0 + n) * a.m.rows;
-            if (kGated) {
-                const int o = slab * 16 + 2 * g;
-                if (o < a.m.rows)
-                    *reinterpret_cast<uint32_t*>(a.gate.h + at + o) =
-                        pack2(wn * (v0 * sigmoid(v0)) * v2, wn * (v1 * sigmoid(v1)) * v3);
-            } else {
-                const int o = slab * 32 + 4 * g;
-                if (o >= a.m.rows) continue;
-                if (a.out_f32)
-                    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + o) =
-                        make_float4(v0, v1, v2, v3);
-                else
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + o) =
-                        make_uint2(pack2(v0, v1), pack2(v2, v3));
-            }
+    for (int n = 0; n < kN; ++n) {
+        if (n >= p.rows) break;
+        const long long at = (row0 + n) * a.m.rows + o;
+        if (a.out_f32)
+            static_cast<float*>(a.out)[at] = s[n];
+        else
+            static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(s[n]);
+    }
+}
+
+// wait_bar with a hint that the thread may be suspended for: a warp that polls takes issue
+// slots from those that widen.
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          int* err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(100000u)
+            : "memory");
+        if (ok) return true;
+        if (*abort) return false;
+        if (clock64() - t0 > kWaitLimit) {
+            *abort = 1;
+            set_error(err, MOE_ERR_TIMEOUT);
+            return false;
         }
     }
+}
+
+__device__ __forceinline__ uint4 ld_shared4(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+// The lane's row's bf16 scales of a chunk.
+__device__ __forceinline__ void load_scales(uint32_t at, float (&s)[1]) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    s[0] = __uint_as_float((uint32_t)v << 16);
+}
+__device__ __forceinline__ void load_scales(uint32_t at, float (&s)[2]) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    s[0] = __uint_as_float(v << 16);
+    s[1] = __uint_as_float(v & 0xffff0000u);
+}
+__device__ __forceinline__ void load_scales(uint32_t at, float (&s)[4]) {
+    uint32_t v, w;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(v), "=r"(w)
+                 : "r"(at)
+                 : "memory");
+    s[0] = __uint_as_float(v << 16);
+    s[1] = __uint_as_float(v & 0xffff0000u);
+    s[2] = __uint_as_float(w << 16);
+    s[3] = __uint_as_float(w & 0xffff0000u);
 }
 
 __device__ __forceinline__ void consumers_sync() {
@@ -241,236 +310,326 @@ __device__ __forceinline__ void consumers_sync() {
 // Each block takes an equal share of the units, whatever tiles they belong to.  A tile that
 // several blocks share: each leaves its sums in a slot of the workspace, and the one that comes
 // last adds them up in the order of the blocks and writes the tile out.  Nobody waits.
-template <int kNT, int kGroup, bool kGated>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm<kNT>)
+//
+// A half is 64 weights of a row.  A warp widens half v while the MMAs of the two before it run,
+// waits for those of half v - 2, whose buffer of A it takes, and reads the sums that they have
+// ended: an arrival for half v says that A is there and that the place of its sums is free.
+template <int kN, int kGroup, bool kGated>
+__global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
     w4_kernel(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__ Args a) {
-    constexpr int kStages = kStagesOf<kNT>;
-    constexpr int kStageBytes = kWeightBytes + kRowBytes<kNT>;
+    using F = Form<kN, kGroup>;
+    constexpr int kStages = F::kStages;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[kStages], empty[kStages];
-    __shared__ long long run_sums[kThreads / 32];
+    __shared__ uint64_t full[kStages], empty[kStages], a_ready[2], mma_done[2];
+    __shared__ int run_sums[kThreads / 32];
+    __shared__ uint32_t tmem_word;
     __shared__ int abort_word, arrived;
-    uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    long long* prefix = reinterpret_cast<long long*>(ring + (size_t)kStages * kStageBytes);
+    uint8_t* rows_ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* ring = rows_ring + (size_t)kStages * F::kRowBytes;
+    int* prefix = reinterpret_cast<int*>(ring + (size_t)kStages * F::kWeightBytes);
     volatile int* abort_flag = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&full[i]), 1);
-            mbar_init(smem_u32(&empty[i]), kSlabs);
+            mbar_init(smem_u32(&empty[i]), kSlabs + 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&a_ready[i]), kSlabs);
+            mbar_init(smem_u32(&mma_done[i]), 1);
         }
         abort_word = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (threadIdx.x == kConsumers) prefetch_map(&tmRows);
+    if (warp == kSlabs) {
+        if (lane == 0) prefetch_map(&tmRows);
+        tmem_alloc(smem_u32(&tmem_word), F::kTmem);
+        tmem_relinquish();
+    }
     after_previous();
-    // prefix[e]: units before expert e; each thread sums a run of experts
+    // prefix[e]: passes before expert e; each thread sums a run of experts
     const int per = ceil_div(a.E, kThreads), e0 = threadIdx.x * per;
-    const long long pass_units = (long long)a.m.tiles * a.m.chunks;
-    long long mine = 0;
-    const auto units = [&](int e) -> long long {
+    int mine = 0;
+    const auto passes = [&](int e) {
         const int off = a.offsets[e], cnt = a.counts[e];
         if (off < 0 || cnt < 0 || cnt > a.R || off > a.R - cnt) {
             set_error(a.err, MOE_ERR_INVALID_ARG);
             return 0;
         }
-        return ceil_div(cnt, 8 * kNT) * pass_units;
+        return ceil_div(cnt, kN);
     };
-    for (int e = e0; e < e0 + per && e < a.E; ++e) mine += units(e);
-    long long incl = mine;
+    for (int e = e0; e < e0 + per && e < a.E; ++e) mine += passes(e);
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
     }
     if (lane == 31) run_sums[warp] = incl;
     __syncthreads();
-    long long before = incl - mine;
-    for (int i = 0; i < warp; ++i) before += run_sums[i];
+    int before = incl - mine, all_passes = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < warp) before += run_sums[i];
+        all_passes += run_sums[i];
+    }
     for (int e = e0; e < e0 + per && e < a.E; ++e) {
         prefix[e] = before;
-        before += units(e);
+        before += passes(e);
     }
-    long long total = 0;
-    for (int i = 0; i < kThreads / 32; ++i) total += run_sums[i];
-    if (threadIdx.x == 0) prefix[a.E] = total;
+    if (threadIdx.x == 0) prefix[a.E] = all_passes;
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_word;
+    const long long total = (long long)all_passes * a.m.tiles * a.m.chunks;
     // no block without a unit: those of a tile are all that arrive at its counter
     const int blocks = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
     const int block = (int)blockIdx.x;
-    if (block >= blocks) return;
-    const long long first = share(total, block, blocks), last = share(total, block + 1, blocks);
+    long long first = 0, last = 0;
+    if (block < blocks) {
+        first = share(total, block, blocks);
+        last = share(total, block + 1, blocks);
+    }
 
-    if (warp == kSlabs) {
-        // ---------------- producer ----------------
-        if (lane != 0) return;
-        int stage = 0;
-        uint32_t phase = 0;
-        for (long long u = first; u < last;) {
-            const Piece p = piece_at<kNT>(a, prefix, u, last);
-            const uint8_t* from = a.packed + (long long)p.e * a.expert_bytes;
-            const int slabs = tile_slabs(a.m, p.tile), boxes = ceil_div(p.rows, 8);
-            const int row = a.offsets[p.e] + p.first_row;
-            const uint32_t weights = (uint32_t)(slabs * a.m.record);
-            for (int c = p.chunk0; c < p.chunk1; ++c) {
-                if (!wait_bar(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, a.err)) {
-                    // let the copies in flight land before the block exits
-                    const long long t0 = clock64();
-                    while (clock64() - t0 < 4000000) {
+    if (warp == kSlabs && elect_one()) {
+        // ---------------- copies and MMAs ----------------
+        // These instructions go before those of the warps that share a scheduler with this
+        // one: what can be is computed once for a piece.
+        Piece lp = {};
+        long long lu = first;
+        int lc = 0, load_slot = 0, boxes = 0, row = 0;
+        uint32_t load_phase = 1, weights = 0;
+        const uint8_t* from = nullptr;
+        bool ok = true;
+        // the next chunk, if there is one, into the slot of the one kStages before it
+        const auto load = [&]() {
+            if (lu >= last) return;
+            if (lc == lp.chunk1) {
+                lp = piece_at<kN>(a, prefix, lu, last);
+                lc = lp.chunk0;
+                boxes = ceil_div(lp.rows, 8);
+                row = a.offsets[lp.e] + lp.first_row;
+                weights = (uint32_t)(tile_slabs(a.m, lp.tile) * F::kRecord);
+                from = a.packed + (long long)lp.e * a.expert_bytes + chunk_at(a.m, lp.tile, lc);
+            }
+            if (!wait_long(smem_u32(&empty[load_slot]), load_phase, abort_flag, a.err)) {
+                ok = false;
+                return;
+            }
+            const uint32_t bar = smem_u32(&full[load_slot]);
+            mbar_expect_tx(bar, weights + (uint32_t)(boxes * 2048));
+            bulk_load(smem_u32(ring) + (uint32_t)(load_slot * F::kWeightBytes), from, weights, bar);
+            const uint32_t to = smem_u32(rows_ring) + (uint32_t)(load_slot * F::kRowBytes);
+#pragma unroll
+            for (int b = 0; b < kN / 8; ++b) {
+                if (b >= boxes) break;
+                tma_load_2d(to + b * 1024, &tmRows, bar, lc * kChunk, row + b * 8);
+                tma_load_2d(to + kN * 128 + b * 1024, &tmRows, bar, lc * kChunk + 64, row + b * 8);
+            }
+            from += weights;
+            ++lc;
+            ++lu;
+            if (++load_slot == kStages) {
+                load_slot = 0;
+                load_phase ^= 1u;
+            }
+        };
+        for (int i = 0; i < kStages - 2; ++i) load();
+        const uint64_t b0 = sw128_desc(smem_u32(rows_ring));
+        uint32_t it = 0, phase = 0;
+        int slot = 0;
+        for (long long u = first; ok && u < last;) {
+            const Piece p = piece_at<kN>(a, prefix, u, last);
+            const uint32_t idesc = make_idesc(kTileRows, ceil_div(p.rows, 16) * 16);
+            u += p.chunk1 - p.chunk0;
+            for (int left = p.chunk1 - p.chunk0; left > 0; --left, ++it) {
+                load();
+                if (!ok || !wait_long(smem_u32(&full[slot]), phase, abort_flag, a.err)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!wait_long(smem_u32(&a_ready[h]), it & 1u, abort_flag, a.err)) {
+                        ok = false;
+                        break;
                     }
-                    return;
+                    tc_fence_after();
+                    const uint64_t b = b0 + (uint64_t)((slot * F::kRowBytes + h * kN * 128) >> 4);
+                    const uint32_t buf = kGroup == 128 ? it & 1u : (uint32_t)h;
+                    const uint32_t d = tmem + F::kSums + buf * (uint32_t)(F::kHalfGroups * kN);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const bool starts = kGroup == 32   ? kk % 2 == 0
+                                            : kGroup == 64 ? kk == 0
+                                                           : kk == 0 && h == 0;
+                        umma_bf16_ta(d + (kGroup == 32 ? kk / 2 * kN : 0),
+                                     tmem + (uint32_t)(h * 32 + kk * 8), b + 2 * kk, idesc,
+                                     starts ? 0u : 1u);
+                    }
+                    umma_commit(smem_u32(&mma_done[h]));
                 }
-                const uint32_t bar = smem_u32(&full[stage]);
-                const uint32_t to = smem_u32(ring) + (uint32_t)(stage * kStageBytes);
-                mbar_expect_tx(bar, weights + (uint32_t)(boxes * 2048));
-                bulk_load(to + kRowBytes<kNT>, from + chunk_at(a.m, p.tile, c), weights, bar);
-                for (int b = 0; b < boxes; ++b) {
-                    tma_load_2d(to + b * 1024, &tmRows, bar, c * kChunk, row + b * 8);
-                    tma_load_2d(to + (kNT + b) * 1024, &tmRows, bar, c * kChunk + 64, row + b * 8);
-                }
-                if (++stage == kStages) {
-                    stage = 0;
+                if (!ok) break;
+                umma_commit(smem_u32(&empty[slot]));
+                if (++slot == kStages) {
+                    slot = 0;
                     phase ^= 1u;
                 }
             }
-            u += p.chunk1 - p.chunk0;
         }
-        return;
-    }
-    // ---------------- consumers ----------------
-    // One whose wait gives up goes on without its products: the others' barriers need it.
-    bool alive = true;
-    int stage = 0;
-    uint32_t phase = 0;
-    const int n = lane >> 2, c4 = lane & 3;
-    for (long long u = first; u < last;) {
-        const Piece p = piece_at<kNT>(a, prefix, u, last);
-        const bool has = warp < tile_slabs(a.m, p.tile);
-        const int slab = p.tile * kSlabs + warp, boxes = ceil_div(p.rows, 8);
-        float w[2] = {0.0f, 0.0f};
-        if (kGated) {
-            const long long row = (long long)a.offsets[p.e] + p.first_row;
-            if (lane < p.rows) w[0] = row_weight(a.gate, row + lane);
-            if (kNT > 4 && lane + 32 < p.rows) w[1] = row_weight(a.gate, row + lane + 32);
+        // a wait has given up: let the copies and MMAs in flight end before the block does
+        if (!ok || *abort_flag) {
+            const long long t0 = clock64();
+            while (clock64() - t0 < 4000000) {
+            }
         }
-        Sums<kNT> sums = {};
-        for (int c = p.chunk0; c < p.chunk1; ++c) {
-            if (alive && !wait_bar(smem_u32(&full[stage]), phase, abort_flag, a.err)) alive = false;
-            alive = __all_sync(0xffffffffu, alive);
-            if (has && alive) {
-                const uint8_t* rows = ring + (size_t)stage * kStageBytes;
-                const uint8_t* rec = rows + kRowBytes<kNT> + warp * a.m.record;
-                float part[kNT][2][4];
+    } else if (warp < kSlabs) {
+        // ---------------- weights and sums ----------------
+        // One whose wait gives up goes on (with what is in memory: the call reports it), for
+        // the others' barriers need it; its later waits return at once.
+        constexpr int kGroups = kChunk / kGroup;
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        // (a tile's last slabs may not be there: what the ring holds in their place gives rows of
+        // sums that go nowhere)
+        const uint32_t rec0 = smem_u32(ring) + (uint32_t)(warp * F::kRecord) + lane * 16;
+        const uint32_t rec_scales = smem_u32(ring) + (uint32_t)(warp * F::kRecord) + kNibbleBytes +
+                                    lane * (uint32_t)(kGroups * 2);
+        int it = 0, slot = 0;
+        uint32_t phase = 0;
+        for (long long u = first; u < last;) {
+            const Piece p = piece_at<kN>(a, prefix, u, last);
+            const bool has = warp < tile_slabs(a.m, p.tile);
+            const int slab = p.tile * kSlabs + warp;
+            const int columns = kN == 16 ? 16 : ceil_div(p.rows, 16) * 16;
+            float sums[kN];
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint32_t q[2][4];
+            for (int n = 0; n < kN; ++n) sums[n] = 0.0f;
+            float scale[kGroups], old[kGroups];  // the chunk's, the one's before
+            // adds `by` times the sums at column `at` of the groups' sums
+            const auto drain = [&](uint32_t at, float by) {
+                constexpr int kPer = kN < 64 ? 16 : 32;  // read side by side
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(
-                            rec + (hh * 2 + mt) * 512 + lane * 16);
-                        q[mt][0] = v.x, q[mt][1] = v.y, q[mt][2] = v.z, q[mt][3] = v.w;
+                for (int n0 = 0; n0 < kN; n0 += kPer) {
+                    if (n0 >= columns) break;
+                    uint32_t v[kPer / 16][16];
+#pragma unroll
+                    for (int j = 0; j < kPer / 16; ++j)
+                        if (n0 + j * 16 < columns)
+                            tmem_ld16(tmem + lanes + F::kSums + at + n0 + j * 16, v[j]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j)
+                        if (n0 + j / 16 * 16 < columns)
+                            sums[n0 + j] = fmaf(by, __uint_as_float(v[j / 16][j % 16]), sums[n0 + j]);
+                }
+            };
+            // the sums that half h of chunk number i has ended, s the chunk's scales
+            const auto drain_half = [&](int i, int h, const float (&s)[kGroups]) {
+                if constexpr (kGroup == 32) {
+                    drain(h * 2 * kN, s[h * 2]);
+                    drain(h * 2 * kN + kN, s[h * 2 + 1]);
+                } else if constexpr (kGroup == 64) {
+                    drain(h * kN, s[h]);
+                } else {
+                    if (h == 1) drain((i & 1) * kN, s[0]);
+                }
+            };
+            for (int c = p.chunk0; c < p.chunk1; ++c, ++it) {
+                wait_long(smem_u32(&full[slot]), phase, abort_flag, a.err);
+                const uint32_t rec = rec0 + (uint32_t)(slot * F::kWeightBytes);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t x[32];
+#pragma unroll
+                    for (int piece = 0; piece < 2; ++piece) {
+                        const uint4 v = ld_shared4(rec + (h * 2 + piece) * 512);
+                        widen(v.x, x + piece * 16);
+                        widen(v.y, x + piece * 16 + 4);
+                        widen(v.z, x + piece * 16 + 8);
+                        widen(v.w, x + piece * 16 + 12);
                     }
+                    if (h == 0) {
 #pragma unroll
-                    for (int sp = 0; sp < 2; ++sp) {
-                        uint32_t x[2][2][4];  // steps 2 sp and 2 sp + 1, both operands
-#pragma unroll
-                        for (int s = 0; s < 2; ++s)
-#pragma unroll
-                            for (int mt = 0; mt < 2; ++mt) widen(q[mt][sp * 2 + s], x[s][mt]);
-                        constexpr int kPairs = kChunk / kGroup;  // groups of a chunk
-                        const bool starts = kPairs == 4 || (kPairs == 2 && sp == 0) ||
-                                            (kPairs == 1 && sp == 0 && hh == 0);
-                        const bool ends = kPairs == 4 || (kPairs == 2 && sp == 1) ||
-                                          (kPairs == 1 && sp == 1 && hh == 1);
-                        const int gi = kPairs == 4 ? hh * 2 + sp : kPairs == 2 ? hh : 0;
-                        float4 scale;
-                        if (ends) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(
-                                rec + kNibbleBytes + gi * 64 + n * 8);
-                            scale = make_float4(__uint_as_float(v.x << 16),
-                                                __uint_as_float(v.x & 0xffff0000u),
-                                                __uint_as_float(v.y << 16),
-                                                __uint_as_float(v.y & 0xffff0000u));
-                        }
-                        const int piece = kGroup == 32 ? sp * 4 + c4 : c4 * 2 + sp;
-                        const uint8_t* at = rows + hh * kNT * 1024 + n * 128 + ((piece ^ n) << 4);
-#pragma unroll
-                        for (int nt = 0; nt < kNT; ++nt) {
-                            if (nt < boxes) {
-                                const uint4 b = *reinterpret_cast<const uint4*>(at + nt * 1024);
-                                if (starts) {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        part[nt][0][i] = part[nt][1][i] = 0.0f;
-                                }
-                                mma_16816(part[nt][0], x[0][0], b.x, b.y);
-                                mma_16816(part[nt][1], x[0][1], b.x, b.y);
-                                mma_16816(part[nt][0], x[1][0], b.z, b.w);
-                                mma_16816(part[nt][1], x[1][1], b.z, b.w);
-                                if (ends) {
-                                    float (&t)[2][4] = sums.v[nt];
-#pragma unroll
-                                    for (int i = 0; i < 2; ++i) {
-                                        t[0][i] = fmaf(scale.x, part[nt][0][i], t[0][i]);
-                                        t[0][2 + i] = fmaf(scale.y, part[nt][0][2 + i], t[0][2 + i]);
-                                        t[1][i] = fmaf(scale.z, part[nt][1][i], t[1][i]);
-                                        t[1][2 + i] = fmaf(scale.w, part[nt][1][2 + i], t[1][2 + i]);
-                                    }
-                                }
-                            }
-                        }
+                        for (int g = 0; g < kGroups; ++g) old[g] = scale[g];
+                        load_scales(rec_scales + (uint32_t)(slot * F::kWeightBytes), scale);
                     }
+                    // the buffer's MMAs of the chunk before
+                    wait_long(smem_u32(&mma_done[h]), (uint32_t)(it - 1) & 1u, abort_flag, a.err);
+                    tc_fence_after();
+                    tmem_st32(tmem + lanes + (uint32_t)(h * 32), x);
+                    // this half's MMAs write where the sums of two halves ago are; with groups
+                    // of 128, where those of two chunks ago were
+                    if (kGroup < 128 && c > p.chunk0) drain_half(it - 1, h, old);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&a_ready[h]));
+                        if (h == 1) mbar_arrive(smem_u32(&empty[slot]));
+                    }
+                    if (kGroup == 128 && c > p.chunk0) drain_half(it - 1, h, old);
+                }
+                if (++slot == kStages) {
+                    slot = 0;
+                    phase ^= 1u;
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&empty[stage]));
-            if (++stage == kStages) {
-                stage = 0;
-                phase ^= 1u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                wait_long(smem_u32(&mma_done[h]), (uint32_t)(it - 1) & 1u, abort_flag, a.err);
+                tc_fence_after();
+                drain_half(it - 1, h, scale);
+            }
+            tc_fence_before();
+            u += p.chunk1 - p.chunk0;
+            if (p.chunk0 == 0 && p.chunk1 == a.m.chunks) {
+                if (has) write_out<kN, kGated>(a, p, slab, sums);
+                continue;
+            }
+            // a tile of several blocks: those with units of [p.start, p.start + chunks)
+            constexpr long long kSlot = (long long)kConsumers * kN;
+            const long long tile_end = p.start + a.m.chunks;
+            int owner = block, after = block;  // the first of them, the last
+            while (share(total, owner, blocks) > p.start) --owner;
+            while (share(total, after + 1, blocks) < tile_end) ++after;
+            const auto slot_of = [&](int b) {
+                const int s = b == owner && share(total, b, blocks) != p.start ? 1 : 0;
+                return a.parts + ((long long)b * 2 + s) * kSlot + threadIdx.x;
+            };
+            float* to = slot_of(block);
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+                if (n < p.rows) __stcg(to + n * kConsumers, sums[n]);
+            __threadfence();
+            consumers_sync();
+            if (threadIdx.x == 0) {
+                arrived = atomicAdd(a.counters + owner, 1);
+                if (arrived == after - owner) a.counters[owner] = 0;  // for the next call
+                __threadfence();
+            }
+            consumers_sync();
+            const bool finish = arrived == after - owner;
+            consumers_sync();  // read before the next tile's
+            if (finish && has) {
+                __threadfence();
+#pragma unroll
+                for (int n = 0; n < kN; ++n) sums[n] = 0.0f;
+                for (int b = owner; b <= after; ++b) {
+                    const float* from = slot_of(b);
+#pragma unroll
+                    for (int n = 0; n < kN; ++n)
+                        if (n < p.rows) sums[n] += __ldcg(from + n * kConsumers);
+                }
+                write_out<kN, kGated>(a, p, slab, sums);
             }
         }
-        u += p.chunk1 - p.chunk0;
-        if (p.chunk0 == 0 && p.chunk1 == a.m.chunks) {
-            if (has) write_out<kNT, kGated>(a, p, slab, sums, w);
-            continue;
-        }
-        // a tile of several blocks: those with units of [p.start, p.start + chunks)
-        constexpr long long kSlot = (long long)kConsumers * kNT * 8;
-        const long long tile_end = p.start + a.m.chunks;
-        int owner = block, after = block;  // the first of them, the last
-        while (share(total, owner, blocks) > p.start) --owner;
-        while (share(total, after + 1, blocks) < tile_end) ++after;
-        const auto slot = [&](int b) {
-            const int s = b == owner && share(total, b, blocks) != p.start ? 1 : 0;
-            return a.parts + ((long long)b * 2 + s) * kSlot + warp * (kNT * 8 * 32) + lane;
-        };
-        float* to = slot(block);
-#pragma unroll
-        for (int i = 0; i < kNT * 8; ++i)
-            if (i / 8 < boxes) __stcg(to + i * 32, sums.v[i / 8][i / 4 % 2][i % 4]);
-        __threadfence();
-        consumers_sync();
-        if (threadIdx.x == 0) {
-            const int before_me = atomicAdd(a.counters + owner, 1);
-            arrived = before_me;
-            if (before_me == after - owner) a.counters[owner] = 0;  // the last: for the next call
-            __threadfence();
-        }
-        consumers_sync();
-        const bool finish = arrived == after - owner;
-        consumers_sync();  // read before the next tile's
-        if (finish && has) {
-            __threadfence();
-            Sums<kNT> all = {};
-            for (int b = owner; b <= after; ++b) {
-                const float* from = slot(b);
-#pragma unroll
-                for (int i = 0; i < kNT * 8; ++i)
-                    if (i / 8 < boxes) all.v[i / 8][i / 4 % 2][i % 4] += __ldcg(from + i * 32);
-            }
-            write_out<kNT, kGated>(a, p, slab, all, w);
-        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kSlabs) {
+        tc_fence_after();
+        tmem_dealloc(tmem, F::kTmem);
     }
 }
 
@@ -510,7 +669,8 @@ __global__ void __launch_bounds__(kBlock)
     if (i % lanes == 0) scales[i / lanes] = *reinterpret_cast<const uint16_t*>(&s);
 }
 
-// 16 bytes of the packed form a thread: 32 nibbles of a lane, or 8 scales.  Rows and columns
+// 16 bytes of the packed form a thread: 32 weights of a row (bytes' nibbles r and r + 4 of a
+// word are neighbours), or 8 scales.  Rows and columns
 // that the matrix does not have are weights of zero (nibble 8, scale 0).
 __global__ void __launch_bounds__(kBlock)
     w4_pack_kernel(const uint8_t* q, const uint16_t* scales, Matrix m, long long pieces,
@@ -532,31 +692,24 @@ __global__ void __launch_bounds__(kBlock)
         uint32_t o[4] = {};
         bool up;
         if (at < nibble_pieces) {
-            const int hh = at >> 6, mt = at >> 5 & 1, lane = at & 31;
+            const int r = matrix_row(m, slab, at & 31, &up);
+            const uint8_t* from = q + ((e * all_rows + (up ? m.rows : 0) + r) * (long long)m.C_in) / 2;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int r = matrix_row(m, slab, mt * 16 + half * 8 + (lane >> 2), &up);
-                const uint8_t* from =
-                    q + ((e * all_rows + (up ? m.rows : 0) + r) * (long long)m.C_in) / 2;
+            for (int w = 0; w < 4; ++w) {
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int k = chunk * kChunk + hh * 64 + weight_of(m.group, lane & 3, s, j);
-                        uint32_t v = 8;
-                        if (r >= 0 && k < m.C_in) v = (uint32_t)(from[k >> 1] >> (k % 2 * 4)) & 15u;
-                        // register half + 2 (j / 2) of the operand, its low or high half
-                        o[s] |= v << (4 * (half + 2 * (j >> 1) + 4 * (j & 1)));
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    const int k = chunk * kChunk + (at >> 5) * 32 + w * 8 + j;
+                    uint32_t v = 8;
+                    if (r >= 0 && k < m.C_in) v = (uint32_t)(from[k >> 1] >> (k % 2 * 4)) & 15u;
+                    o[w] |= v << (4 * (j / 2 + 4 * (j % 2)));
                 }
             }
         } else {
-            const int first = (at - nibble_pieces) * 8;  // scale of [group][row / 4 of the lane][4]
+            const int per_row = kChunk / m.group, first = (at - nibble_pieces) * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int s = first + j, gi = s >> 5, g = s >> 2 & 7, which = s & 3;
-                const int r = matrix_row(m, slab, which * 8 + g, &up);
-                const int grp = chunk * (kChunk / m.group) + gi;
+                const int r = matrix_row(m, slab, (first + j) / per_row, &up);
+                const int grp = chunk * per_row + (first + j) % per_row;
                 uint32_t v = 0;
                 if (r >= 0 && grp < groups)
                     v = scales[(e * all_rows + (up ? m.rows : 0) + r) * (long long)groups + grp];
@@ -569,12 +722,12 @@ __global__ void __launch_bounds__(kBlock)
 
 // ---- host -----------------------------------------------------------------------------------
 
-// Boxes of 8 rows of a pass: enough for most experts' rows at once when they are spread as by
-// chance around their average.
-int boxes_of(long long R, int E) {
+// Rows of a pass: enough for most experts' rows at once when they are spread as by chance
+// around their average.
+int pass_rows(long long R, int E) {
     const long long used = R < E ? R : E;
     const double mean = used > 0 ? (double)R / (double)used : 0.0;
-    return mean <= 4.0 ? 1 : mean <= 10.0 ? 2 : mean <= 24.0 ? 4 : 8;
+    return mean <= 10.0 ? 16 : mean <= 22.0 ? 32 : 64;
 }
 
 struct W4Work {
@@ -584,8 +737,8 @@ W4Work w4_work(const moe_shape& s) {
     W4Work w;
     w.counters = workspace_layout(s).total;
     w.parts = w.counters + align256(kMaxBlocks * sizeof(int));
-    w.total = w.parts + (size_t)kMaxBlocks * 2 * kConsumers * 8 * sizeof(float) *
-                            boxes_of((long long)s.N * s.k, s.E);
+    w.total = w.parts + (size_t)kMaxBlocks * 2 * kConsumers * sizeof(float) *
+                            pass_rows((long long)s.N * s.k, s.E);
     return w;
 }
 
@@ -600,39 +753,41 @@ long long packed_bytes(const moe_w4_matrix& m, int E) {
     return (long long)E * d.slabs * d.chunks * d.record;
 }
 
-template <int kNT, int kGroup, bool kGated>
-moe_status launch_as(const CUtensorMap& rows, const Args& a, long long units, cudaStream_t st) {
-    const auto kernel = w4_kernel<kNT, kGroup, kGated>;
+template <int kN, int kGroup, bool kGated>
+moe_status launch_as(const CUtensorMap& rows, const Args& a, long long used, cudaStream_t st) {
+    using F = Form<kN, kGroup>;
+    const auto kernel = w4_kernel<kN, kGroup, kGated>;
     static OncePerDevice set;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
     if (!set.done(dev)) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem_bytes<kNT>(kMaxE)) != cudaSuccess)
+                                 (int)F::smem(kMaxE)) != cudaSuccess)
             return MOE_ERR_CUDA;
         set.finish(dev);
     }
-    long long blocks = (long long)sm_count() * kBlocksPerSm<kNT>;
+    const long long units = (used + (a.R - used) / kN) * a.m.tiles * a.m.chunks;
+    long long blocks = (long long)sm_count() * F::kBlocks;
     if (blocks > kMaxBlocks) blocks = kMaxBlocks;
     if (blocks > units) blocks = units;
-    return cuda_status(
-        launch_chained(kernel, (int)blocks, kThreads, smem_bytes<kNT>(a.E), st, rows, a));
+    return cuda_status(launch_chained(kernel, (int)blocks, kThreads, F::smem(a.E), st, rows, a));
 }
 
-template <int kNT>
-moe_status launch_w4(const CUtensorMap& rows, const Args& a, long long units, cudaStream_t st) {
-    const bool gated = a.m.gated != 0;
-    switch (a.m.group) {
-        case 32:
-            return gated ? launch_as<kNT, 32, true>(rows, a, units, st)
-                         : launch_as<kNT, 32, false>(rows, a, units, st);
-        case 64:
-            return gated ? launch_as<kNT, 64, true>(rows, a, units, st)
-                         : launch_as<kNT, 64, false>(rows, a, units, st);
-        default:
-            return gated ? launch_as<kNT, 128, true>(rows, a, units, st)
-                         : launch_as<kNT, 128, false>(rows, a, units, st);
-    }
+// Groups of 32 in passes of 64 rows would take all of TMEM for one block: 32 rows, two blocks.
+template <int kGroup, bool kGated>
+moe_status launch_rows_of(int pass, const CUtensorMap& rows, const Args& a, long long used,
+                          cudaStream_t st) {
+    if (pass == 16) return launch_as<16, kGroup, kGated>(rows, a, used, st);
+    if (pass == 32 || kGroup == 32) return launch_as<32, kGroup, kGated>(rows, a, used, st);
+    return launch_as<kGroup == 32 ? 32 : 64, kGroup, kGated>(rows, a, used, st);
+}
+
+template <bool kGated>
+moe_status launch_w4(int pass, const CUtensorMap& rows, const Args& a, long long used,
+                     cudaStream_t st) {
+    return a.m.group == 32   ? launch_rows_of<32, kGated>(pass, rows, a, used, st)
+           : a.m.group == 64 ? launch_rows_of<64, kGated>(pass, rows, a, used, st)
+                             : launch_rows_of<128, kGated>(pass, rows, a, used, st);
 }
 
 moe_status w4_product(const uint16_t* rows, const moe_layout* layout, const moe_shape* shape,
@@ -671,14 +826,10 @@ moe_status w4_product(const uint16_t* rows, const moe_layout* layout, const moe_
     const uint64_t strides[1] = {(uint64_t)matrix->C_in * 2};
     const uint32_t box[2] = {64, 8};
     if (!map_tiled(&map, 2, rows, sizes, strides, box)) return MOE_ERR_UNSUPPORTED;
-    const int nt = boxes_of(R, g.E);
-    const long long used = R < g.E ? R : g.E;
-    const long long units = (used + (R - used) / (8 * nt)) * a.m.tiles * a.m.chunks;
-    const cudaStream_t st = as_stream(stream);
-    return nt == 1   ? launch_w4<1>(map, a, units, st)
-           : nt == 2 ? launch_w4<2>(map, a, units, st)
-           : nt == 4 ? launch_w4<4>(map, a, units, st)
-                     : launch_w4<8>(map, a, units, st);
+    const long long used = R < g.E ? R : g.E;  // experts with rows, at most
+    const int pass = pass_rows(R, g.E);
+    return gated ? launch_w4<true>(pass, map, a, used, as_stream(stream))
+                 : launch_w4<false>(pass, map, a, used, as_stream(stream));
 }
 
 }  // namespace
