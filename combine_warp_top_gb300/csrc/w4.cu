@@ -6,8 +6,8 @@
 // gate rows and I up rows, and h = w_i SiLU(g) u leaves instead of y.
 //
 // Memory bound: every weight is read once, 4 bits and its share of a scale.  So the packed
-// layout (w4_pack_kernel) is the order in which the kernel reads: tiles of 128 matrix rows in
-// chunks of 128 weights of each, one chunk of a tile a contiguous piece of 8 to 9 KB that one
+// layout (w4_pack_kernel) is the order in which the kernel reads: tiles of 256 matrix rows in
+// chunks of 128 weights of each, one chunk of a tile a contiguous piece of 17 to 18 KB that one
 // bulk copy brings into a ring of shared memory, the scales beside the weights.  The rows'
 // chunks come by TMA boxes of 8 rows.
 //
@@ -32,13 +32,13 @@ namespace {
 using namespace ptx;
 
 constexpr int kSlabRows = 32;  // matrix rows of a warp
-constexpr int kSlabs = 4;      // warps of a tile
-constexpr int kTileRows = kSlabRows * kSlabs;
+constexpr int kSlabs = 8;      // warps of a tile
 constexpr int kChunk = 128;    // weights of a row in a chunk
 constexpr int kNibbleBytes = kSlabRows * kChunk / 2;
 constexpr int kConsumers = kSlabs * 32;
-constexpr int kThreads = kConsumers + 32;
-constexpr int kMaxBlocks = 608;
+constexpr int kThreads = kConsumers + 64;  // and a warp for the MMAs, one for the copies
+constexpr int kMmaRows = 128;  // of an MMA: a tile has two
+constexpr int kMaxBlocks = 304;
 
 __host__ __device__ __forceinline__ int ceil_div(long long a, int b) {
     return (int)((a + b - 1) / b);
@@ -85,24 +85,26 @@ __device__ __forceinline__ int matrix_row(const Matrix& m, int slab, int r, bool
 // ---- the product ---------------------------------------------------------------------------
 
 // kN: rows of a pass at most (the MMA's N, in steps of 16).
-// A's two buffers of 64 weights a row, 32 columns each, and the sums of the groups that end in
-// one or the other.
+// TMEM: A's two buffers of 64 weights a row, 32 columns each, of both MMAs' rows, then the sums
+// of the groups that end in one buffer or the other.
 template <int kN, int kGroup>
 struct Form {
     static constexpr int kHalfGroups = kGroup == 32 ? 2 : 1;  // sums of 64 weights
-    static constexpr int kSums = 64;                          // their first column
-    static constexpr int kUsed = kSums + 2 * kHalfGroups * kN;
-    static constexpr int kTmem = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-    // of an SM; a thread with 32 sums takes the registers of three
-    static constexpr int kBlocks = kTmem == 512 ? 1 : kTmem == 256 ? 2 : kN == 16 ? 4 : 3;
+    static constexpr int kSumColumns = 2 * kHalfGroups * kN;  // of 128 rows
+    static constexpr int kSums = 128;                         // their first column
+    static constexpr int kUsed = kSums + 2 * kSumColumns;
+    static constexpr int kTmem = kUsed <= 256 ? 256 : 512;
+    static constexpr int kBlocks = 512 / kTmem;  // of an SM
     static constexpr int kRecord = record_bytes(kGroup);
     static constexpr int kWeightBytes = kSlabs * kRecord;
     static constexpr int kRowBytes = 2 * kN * 128;  // two halves of 64 columns
-    // 4 blocks of an SM have 56 KB each, 3 have 74, 2 have 113
-    static constexpr int kStages = kBlocks == 4 ? (kGroup > 32 ? 4 : 3) : kN <= 32 ? 4 : 4;
+    static constexpr int kStages = kBlocks == 2 ? (kN == 16 && kGroup > 32 ? 5 : 4) : 6;
     static size_t smem(int E) {
         return 1024 + (size_t)kStages * (kWeightBytes + kRowBytes) + (size_t)(E + 1) * 4;
     }
+    static_assert(kBlocks * (2048 + kStages * (kWeightBytes + kRowBytes) + (kMaxE + 1) * 4 + 1024) <=
+                      228 * 1024,
+                  "shared memory of an SM");
 };
 
 struct Args {
@@ -157,6 +159,16 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(mask), "r"(bits));
     return v;
 }
+__device__ __forceinline__ void tmem_st_a(uint32_t at, const uint32_t (&x)[32]) { tmem_st32(at, x); }
+__device__ __forceinline__ void tmem_st_a(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 // Eight nibbles to four pairs: nibble r and nibble r + 4 are the halves of register r.
 __device__ __forceinline__ void widen(uint32_t w, uint32_t* a) {
     const __nv_bfloat162 bias = __float2bfloat162_rn(136.0f);
@@ -209,10 +221,10 @@ __device__ __forceinline__ long long share(long long total, int b, int blocks) {
     return total * b / blocks;
 }
 
-// The sums of a tile's slab to their output.
+// The sums of a tile's slab to their output.  weights: of the rows (gated).
 template <int kN, bool kGated>
 __device__ __forceinline__ void write_out(const Args& a, const Piece& p, int slab,
-                                          const float (&s)[kN]) {
+                                          const float (&s)[kN], const float* weights) {
     const int lane = threadIdx.x & 31;
     const long long row0 = (long long)a.offsets[p.e] + p.first_row;
     if (kGated) {
@@ -228,7 +240,7 @@ __device__ __forceinline__ void write_out(const Args& a, const Piece& p, int sla
             const int mine = n + upper;
             if (mine >= p.rows || o >= a.m.rows) continue;
             const long long row = row0 + mine;
-            const __nv_bfloat16 h = __float2bfloat16_rn(row_weight(a.gate, row) * (g * sigmoid(g)) * u);
+            const __nv_bfloat16 h = __float2bfloat16_rn(weights[mine] * (g * sigmoid(g)) * u);
             a.gate.h[row * a.m.rows + o] = *reinterpret_cast<const uint16_t*>(&h);
         }
         return;
@@ -246,22 +258,13 @@ __device__ __forceinline__ void write_out(const Args& a, const Piece& p, int sla
     }
 }
 
-// wait_bar with a hint that the thread may be suspended for: a warp that polls takes issue
-// slots from those that widen.
-__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort,
-                                          int* err) {
-    if (mbar_try_wait(bar, parity)) return true;
+// wait_bar out of line, which sleeps between its looks: a warp that polls takes issue slots
+// from those that widen.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort,
+                                       int* err) {
     const long long t0 = clock64();
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(100000u)
-            : "memory");
-        if (ok) return true;
+    while (!mbar_try_wait(bar, parity)) {
+        __nanosleep(20);
         if (*abort) return false;
         if (clock64() - t0 > kWaitLimit) {
             *abort = 1;
@@ -269,6 +272,22 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatil
             return false;
         }
     }
+    return true;
+}
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort,
+                                         int* err) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, err);
+}
+__device__ __forceinline__ void linger() {
+    const long long t0 = clock64();
+    while (clock64() - t0 < 4000000) {
+    }
+}
+// A whole warp's wait.
+__device__ __forceinline__ void wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          int* err) {
+    if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) wait_slow(bar, parity, abort, err);
+    __syncwarp();
 }
 
 __device__ __forceinline__ uint4 ld_shared4(uint32_t at) {
@@ -324,6 +343,8 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
     __shared__ int run_sums[kThreads / 32];
     __shared__ uint32_t tmem_word;
     __shared__ int abort_word, arrived;
+    constexpr int kRowSlots = kStages + 2;
+    __shared__ float row_weights[kGated ? kRowSlots : 1][kN];
     uint8_t* rows_ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* ring = rows_ring + (size_t)kStages * F::kRowBytes;
     int* prefix = reinterpret_cast<int*>(ring + (size_t)kStages * F::kWeightBytes);
@@ -392,66 +413,82 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
         last = share(total, block + 1, blocks);
     }
 
-    if (warp == kSlabs && elect_one()) {
-        // ---------------- copies and MMAs ----------------
-        // These instructions go before those of the warps that share a scheduler with this
-        // one: what can be is computed once for a piece.
+    if (warp == kSlabs + 1) {
+        // ---------------- copies ----------------
         Piece lp = {};
         long long lu = first;
-        int lc = 0, load_slot = 0, boxes = 0, row = 0;
+        int load_slot = 0, boxes = 0, row = 0;
         uint32_t load_phase = 1, weights = 0;
         const uint8_t* from = nullptr;
-        bool ok = true;
-        // the next chunk, if there is one, into the slot of the one kStages before it
-        const auto load = [&]() {
-            if (lu >= last) return;
-            if (lc == lp.chunk1) {
-                lp = piece_at<kN>(a, prefix, lu, last);
-                lc = lp.chunk0;
-                boxes = ceil_div(lp.rows, 8);
-                row = a.offsets[lp.e] + lp.first_row;
-                weights = (uint32_t)(tile_slabs(a.m, lp.tile) * F::kRecord);
-                from = a.packed + (long long)lp.e * a.expert_bytes + chunk_at(a.m, lp.tile, lc);
-            }
-            if (!wait_long(smem_u32(&empty[load_slot]), load_phase, abort_flag, a.err)) {
-                ok = false;
-                return;
-            }
-            const uint32_t bar = smem_u32(&full[load_slot]);
-            mbar_expect_tx(bar, weights + (uint32_t)(boxes * 2048));
-            bulk_load(smem_u32(ring) + (uint32_t)(load_slot * F::kWeightBytes), from, weights, bar);
-            const uint32_t to = smem_u32(rows_ring) + (uint32_t)(load_slot * F::kRowBytes);
+        int pieces = 0;
+        const bool one = elect_one();
+        while (lu < last) {
+            lp = piece_at<kN>(a, prefix, lu, last);
+            boxes = ceil_div(lp.rows, 8);
+            row = a.offsets[lp.e] + lp.first_row;
+            weights = (uint32_t)(tile_slabs(a.m, lp.tile) * F::kRecord);
+            from = a.packed + (long long)lp.e * a.expert_bytes + chunk_at(a.m, lp.tile, lp.chunk0);
+            if (kGated) {
+                // three loads one after the other, here in nobody's way: those that read them
+                // are kRowSlots - 2 pieces behind at most, for these have a chunk at least
 #pragma unroll
-            for (int b = 0; b < kN / 8; ++b) {
-                if (b >= boxes) break;
-                tma_load_2d(to + b * 1024, &tmRows, bar, lc * kChunk, row + b * 8);
-                tma_load_2d(to + kN * 128 + b * 1024, &tmRows, bar, lc * kChunk + 64, row + b * 8);
+                for (int n = 0; n < kN; n += 32)
+                    if (n + lane < lp.rows)
+                        row_weights[pieces % kRowSlots][n + lane] =
+                            row_weight(a.gate, (long long)row + n + lane);
+                __syncwarp();
             }
-            from += weights;
-            ++lc;
-            ++lu;
-            if (++load_slot == kStages) {
-                load_slot = 0;
-                load_phase ^= 1u;
+            ++pieces;
+            int given_up = 0;
+            if (one) {
+                for (int c = lp.chunk0; c < lp.chunk1; ++c) {
+                    if (!wait_one(smem_u32(&empty[load_slot]), load_phase, abort_flag, a.err)) {
+                        given_up = 1;
+                        break;
+                    }
+                    const uint32_t bar = smem_u32(&full[load_slot]);
+                    mbar_expect_tx(bar, weights + (uint32_t)(boxes * 2048));
+                    bulk_load(smem_u32(ring) + (uint32_t)(load_slot * F::kWeightBytes), from,
+                              weights, bar);
+                    const uint32_t to = smem_u32(rows_ring) + (uint32_t)(load_slot * F::kRowBytes);
+#pragma unroll
+                    for (int b = 0; b < kN / 8; ++b) {
+                        if (b >= boxes) break;
+                        tma_load_2d(to + b * 1024, &tmRows, bar, c * kChunk, row + b * 8);
+                        tma_load_2d(to + kN * 128 + b * 1024, &tmRows, bar, c * kChunk + 64,
+                                    row + b * 8);
+                    }
+                    from += weights;
+                    if (++load_slot == kStages) {
+                        load_slot = 0;
+                        load_phase ^= 1u;
+                    }
+                }
             }
-        };
-        for (int i = 0; i < kStages - 2; ++i) load();
+            if (__any_sync(0xffffffffu, given_up)) break;
+            lu += lp.chunk1 - lp.chunk0;
+        }
+        // a wait has given up: let the copies in flight land before the block ends
+        if (*abort_flag) linger();
+    } else if (warp == kSlabs && elect_one()) {
+        // ---------------- MMAs ----------------
+        bool ok = true;
         const uint64_t b0 = sw128_desc(smem_u32(rows_ring));
         uint32_t it = 0, phase = 0;
         int slot = 0;
         for (long long u = first; ok && u < last;) {
             const Piece p = piece_at<kN>(a, prefix, u, last);
-            const uint32_t idesc = make_idesc(kTileRows, ceil_div(p.rows, 16) * 16);
+            const uint32_t idesc = make_idesc(kMmaRows, ceil_div(p.rows, 16) * 16);
+            const bool upper = tile_slabs(a.m, p.tile) > kSlabs / 2;  // any slab of the second MMA's
             u += p.chunk1 - p.chunk0;
             for (int left = p.chunk1 - p.chunk0; left > 0; --left, ++it) {
-                load();
-                if (!ok || !wait_long(smem_u32(&full[slot]), phase, abort_flag, a.err)) {
+                if (!wait_one(smem_u32(&full[slot]), phase, abort_flag, a.err)) {
                     ok = false;
                     break;
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (!wait_long(smem_u32(&a_ready[h]), it & 1u, abort_flag, a.err)) {
+                    if (!wait_one(smem_u32(&a_ready[h]), it & 1u, abort_flag, a.err)) {
                         ok = false;
                         break;
                     }
@@ -460,13 +497,17 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
                     const uint32_t buf = kGroup == 128 ? it & 1u : (uint32_t)h;
                     const uint32_t d = tmem + F::kSums + buf * (uint32_t)(F::kHalfGroups * kN);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const bool starts = kGroup == 32   ? kk % 2 == 0
-                                            : kGroup == 64 ? kk == 0
-                                                           : kk == 0 && h == 0;
-                        umma_bf16_ta(d + (kGroup == 32 ? kk / 2 * kN : 0),
-                                     tmem + (uint32_t)(h * 32 + kk * 8), b + 2 * kk, idesc,
-                                     starts ? 0u : 1u);
+                    for (int t = 0; t < 2; ++t) {
+                        if (t == 1 && !upper) break;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const bool starts = kGroup == 32   ? kk % 2 == 0
+                                                : kGroup == 64 ? kk == 0
+                                                               : kk == 0 && h == 0;
+                            umma_bf16_ta(d + (uint32_t)(t * F::kSumColumns + (kGroup == 32 ? kk / 2 * kN : 0)),
+                                         tmem + (uint32_t)(t * 64 + h * 32 + kk * 8), b + 2 * kk,
+                                         idesc, starts ? 0u : 1u);
+                        }
                     }
                     umma_commit(smem_u32(&mma_done[h]));
                 }
@@ -478,27 +519,25 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
                 }
             }
         }
-        // a wait has given up: let the copies and MMAs in flight end before the block does
-        if (!ok || *abort_flag) {
-            const long long t0 = clock64();
-            while (clock64() - t0 < 4000000) {
-            }
-        }
+        if (*abort_flag) linger();  // likewise the MMAs
     } else if (warp < kSlabs) {
         // ---------------- weights and sums ----------------
         // One whose wait gives up goes on (with what is in memory: the call reports it), for
         // the others' barriers need it; its later waits return at once.
         constexpr int kGroups = kChunk / kGroup;
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t a_at = tmem + lanes + (uint32_t)((warp >> 2) * 64);
+        const uint32_t sums_at = tmem + lanes + (uint32_t)(F::kSums + (warp >> 2) * F::kSumColumns);
         // (a tile's last slabs may not be there: what the ring holds in their place gives rows of
         // sums that go nowhere)
         const uint32_t rec0 = smem_u32(ring) + (uint32_t)(warp * F::kRecord) + lane * 16;
         const uint32_t rec_scales = smem_u32(ring) + (uint32_t)(warp * F::kRecord) + kNibbleBytes +
                                     lane * (uint32_t)(kGroups * 2);
-        int it = 0, slot = 0;
+        int it = 0, slot = 0, pieces = 0;
         uint32_t phase = 0;
-        for (long long u = first; u < last;) {
+        for (long long u = first; u < last; ++pieces) {
             const Piece p = piece_at<kN>(a, prefix, u, last);
+            const float* weights = row_weights[kGated ? pieces % kRowSlots : 0];
             const bool has = warp < tile_slabs(a.m, p.tile);
             const int slab = p.tile * kSlabs + warp;
             const int columns = kN == 16 ? 16 : ceil_div(p.rows, 16) * 16;
@@ -516,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
 #pragma unroll
                     for (int j = 0; j < kPer / 16; ++j)
                         if (n0 + j * 16 < columns)
-                            tmem_ld16(tmem + lanes + F::kSums + at + n0 + j * 16, v[j]);
+                            tmem_ld16(sums_at + at + n0 + j * 16, v[j]);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < kPer; ++j)
@@ -536,28 +575,36 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
                 }
             };
             for (int c = p.chunk0; c < p.chunk1; ++c, ++it) {
-                wait_long(smem_u32(&full[slot]), phase, abort_flag, a.err);
+                wait_warp(smem_u32(&full[slot]), phase, abort_flag, a.err);
                 const uint32_t rec = rec0 + (uint32_t)(slot * F::kWeightBytes);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t x[32];
-#pragma unroll
-                    for (int piece = 0; piece < 2; ++piece) {
+                    // 32 weights at a time of a row where the registers are its sums'
+                    constexpr int kPieces = kN == 16 ? 2 : 1;
+                    uint32_t x[16 * kPieces];
+                    const auto widen_piece = [&](int piece) {
                         const uint4 v = ld_shared4(rec + (h * 2 + piece) * 512);
-                        widen(v.x, x + piece * 16);
-                        widen(v.y, x + piece * 16 + 4);
-                        widen(v.z, x + piece * 16 + 8);
-                        widen(v.w, x + piece * 16 + 12);
-                    }
+                        uint32_t* to = x + piece % kPieces * 16;
+                        widen(v.x, to);
+                        widen(v.y, to + 4);
+                        widen(v.z, to + 8);
+                        widen(v.w, to + 12);
+                    };
+                    widen_piece(0);
+                    if (kPieces == 2) widen_piece(1);
                     if (h == 0) {
 #pragma unroll
                         for (int g = 0; g < kGroups; ++g) old[g] = scale[g];
                         load_scales(rec_scales + (uint32_t)(slot * F::kWeightBytes), scale);
                     }
                     // the buffer's MMAs of the chunk before
-                    wait_long(smem_u32(&mma_done[h]), (uint32_t)(it - 1) & 1u, abort_flag, a.err);
+                    wait_warp(smem_u32(&mma_done[h]), (uint32_t)(it - 1) & 1u, abort_flag, a.err);
                     tc_fence_after();
-                    tmem_st32(tmem + lanes + (uint32_t)(h * 32), x);
+                    tmem_st_a(a_at + (uint32_t)(h * 32), x);
+                    if (kPieces == 1) {
+                        widen_piece(1);
+                        tmem_st_a(a_at + (uint32_t)(h * 32 + 16), x);
+                    }
                     // this half's MMAs write where the sums of two halves ago are; with groups
                     // of 128, where those of two chunks ago were
                     if (kGroup < 128 && c > p.chunk0) drain_half(it - 1, h, old);
@@ -577,14 +624,14 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                wait_long(smem_u32(&mma_done[h]), (uint32_t)(it - 1) & 1u, abort_flag, a.err);
+                wait_warp(smem_u32(&mma_done[h]), (uint32_t)(it - 1) & 1u, abort_flag, a.err);
                 tc_fence_after();
                 drain_half(it - 1, h, scale);
             }
             tc_fence_before();
             u += p.chunk1 - p.chunk0;
             if (p.chunk0 == 0 && p.chunk1 == a.m.chunks) {
-                if (has) write_out<kN, kGated>(a, p, slab, sums);
+                if (has) write_out<kN, kGated>(a, p, slab, sums, weights);
                 continue;
             }
             // a tile of several blocks: those with units of [p.start, p.start + chunks)
@@ -621,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
                     for (int n = 0; n < kN; ++n)
                         if (n < p.rows) sums[n] += __ldcg(from + n * kConsumers);
                 }
-                write_out<kN, kGated>(a, p, slab, sums);
+                write_out<kN, kGated>(a, p, slab, sums, weights);
             }
         }
     }
