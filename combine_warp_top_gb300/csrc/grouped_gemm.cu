@@ -515,7 +515,7 @@ bool map_3d(CUtensorMap* m, const void* ptr, uint64_t E, uint64_t rows, uint64_t
 // Any tiled bf16 or fp32 map (128-byte swizzle) of up to 4 dimensions, innermost first;
 // strides: bytes of dimensions 1 and up.
 bool map_typed(CUtensorMap* m, int rank, const void* ptr, const uint64_t* sizes,
-               const uint64_t* strides, const uint32_t* boxes, MapType type, bool swizzle) {
+               const uint64_t* strides, const uint32_t* boxes, MapType type, int swizzle) {
     auto enc = encode_fn();
     if (!enc || rank < 2 || rank > 4) return false;
     cuuint64_t dims[4], str[3];
@@ -531,14 +531,16 @@ bool map_typed(CUtensorMap* m, int rank, const void* ptr, const uint64_t* sizes,
                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                (cuuint32_t)rank, const_cast<void*>(ptr), dims,
                str, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+               : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                               : CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool map_tiled(CUtensorMap* m, int rank, const void* ptr, const uint64_t* sizes,
                const uint64_t* strides, const uint32_t* boxes, bool f32) {
-    return map_typed(m, rank, ptr, sizes, strides, boxes, f32 ? kMapF32 : kMapBF16, true);
+    return map_typed(m, rank, ptr, sizes, strides, boxes, f32 ? kMapF32 : kMapBF16, 128);
 }
 
 // Map over packed weights (E experts x n_blocks n-blocks x ceil(K/64) k-blocks

@@ -108,7 +108,8 @@ template <int kMode, bool kFew>
 constexpr int kStagesOf = kFew ? 9 : kMode == kGatedGrad ? 5 : 6;
 constexpr int kAhead = 2;  // tiles the scheduler publishes ahead of the leader's producer
 constexpr int kStagingBytes = 32 * 128;  // an epilogue warp's output: 32 lines
-// kGatedGrad: 32 lines of gate columns and 32 of up columns come in there and go out again
+// kGatedGrad: 32 half lines of gate columns and 32 of up columns come in there and go out again,
+// twice: the next ones come in while these are worked on
 template <int kMode>
 constexpr int kStagingOf = (kMode == kGatedGrad ? 2 : 1) * kStagingBytes;
 // k-blocks added up in one accumulator, see "Precision" above
@@ -161,6 +162,8 @@ struct Barriers : Queues {
 };
 template <int kMode, bool kFew>
 struct Ctl : Barriers<kStagesOf<kMode, kFew>> {};
+constexpr int kGateCols = 32;             // kGatedGrad: columns of a half line of 64 bytes
+constexpr int kHalfLines = 32 * kGateCols * 2;  // bytes of 32 rows' half lines
 constexpr int kMaxSorted = 512;  // what is left of shared memory holds
 template <>
 struct Ctl<kWeightsGrad, false> : Barriers<kStagesOf<kWeightsGrad, false>> {
@@ -602,15 +605,16 @@ __device__ __forceinline__ void gated_few_out(const Gate& gate, uint8_t* staging
     named_sync(out);
 }
 
-// kGatedGrad: dh's 32 rows of 64 columns in v, their g and u in the lines; dg and du take
-// their place.  Returns this lane's row's sum of dh SiLU(g) u.
-__device__ __forceinline__ float gated_grad_lines(uint8_t* lines, const uint32_t (&v)[64], float w) {
+// kGatedGrad: dh's 32 rows of 32 columns in v, their g and u in the half lines; dg and du take
+// their place.  16-byte chunk k of row r is at k ^ (r / 2 % 4): TMA's 64-byte swizzle.  Returns
+// this lane's row's sum of dh SiLU(g) u.
+__device__ __forceinline__ float gated_grad_lines(uint8_t* lines, const uint32_t (&v)[32], float w) {
     const int lane = threadIdx.x & 31;
     float sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        uint4* g_at = reinterpret_cast<uint4*>(lines + lane * 128 + ((k ^ (lane & 7)) << 4));
-        uint4* u_at = g_at + kStagingBytes / 16;
+    for (int k = 0; k < 4; ++k) {
+        uint4* g_at = reinterpret_cast<uint4*>(lines + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4));
+        uint4* u_at = g_at + kHalfLines / 16;
         const uint4 gv = *g_at, uv = *u_at;
         const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w}, u[4] = {uv.x, uv.y, uv.z, uv.w};
         uint32_t dg[4], du[4];
@@ -634,6 +638,119 @@ __device__ __forceinline__ float gated_grad_lines(uint8_t* lines, const uint32_t
         *u_at = make_uint4(du[0], du[1], du[2], du[3]);
     }
     return sum;
+}
+// The first `rows` of 32 half lines to rows of gu's gradient, `pitch` apart; cols: how many
+// columns there are from `to` on.
+__device__ __forceinline__ void store_half_lines(const uint8_t* lines, uint16_t* to, int pitch,
+                                                 int rows, int cols) {
+    const int lane = threadIdx.x & 31, k = lane & 3;
+    for (int r = lane >> 2; r < rows; r += 8)
+        if (k * 8 < cols)
+            *reinterpret_cast<uint4*>(to + (long long)r * pitch + k * 8) =
+                *reinterpret_cast<const uint4*>(lines + r * 64 + ((k ^ (r >> 1 & 3)) << 4));
+}
+
+// One warp's part of a tile of kGatedGrad: its 32 rows (of which the segment has `rows`), from
+// column `col` on `have` half lines of 32 columns.
+struct GradPart {
+    long long row;
+    int rows, col, have;
+};
+__device__ __forceinline__ GradPart grad_part(const Tile& t, uint32_t rank, int n_out) {
+    const int warp = (int)(threadIdx.x >> 5), half = (warp - 4) >> 2;
+    GradPart p;
+    const int at = t.mb * BT + (int)rank * BH + (warp & 3) * 32;
+    p.row = (long long)t.off + at;
+    p.rows = t.cnt - at;
+    p.col = t.nb * BT + half * kEpilogueCols;
+    const int left = n_out - p.col < kEpilogueCols ? n_out - p.col : kEpilogueCols;
+    p.have = p.rows <= 0 || left <= 0 ? 0 : (left + kGateCols - 1) / kGateCols;
+    return p;
+}
+// Its epilogue warps' loop.  A half line's inputs are asked for one half line ahead, the next
+// tile's first ones during this tile's last, with the rows' weights of that tile (three loads
+// one after the other), so that only the call's first tile waits for them.
+template <typename Take, typename Ready, typename Release>
+__device__ __forceinline__ void gated_grad_tiles(const CUtensorMap& tmGu, const CUtensorMap& tmOut,
+                                                 const Gate& gate, uint8_t* staging, uint32_t bar,
+                                                 uint32_t rank, int R, int n_out,
+                                                 volatile int* abort, int* err, Take take_tile,
+                                                 Ready ready, Release release) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t staging_at = smem_u32(staging);
+    uint32_t phase = 0;
+    int buf = 0;
+    Tile t = {};
+    if (!take_tile(0, t)) return;
+    GradPart p = grad_part(t, rank, n_out);
+    const auto fetch = [&](const GradPart& q, int c, int b) {
+        if (lane != 0) return;
+        bulk_wait_read();  // what went out from there has been read
+        const uint32_t to = staging_at + (uint32_t)(b * 2 * kHalfLines);
+        mbar_expect_tx(bar, 2 * kHalfLines);
+        tma_load_3d(to, &tmGu, bar, q.col + c * kGateCols, 0, (int)q.row);
+        tma_load_3d(to + kHalfLines, &tmGu, bar, q.col + c * kGateCols, 1, (int)q.row);
+    };
+    if (p.have > 0) fetch(p, 0, 0);
+    float w = lane < p.rows ? row_weight(gate, p.row + lane) : 0.0f;
+    for (int i = 1;; ++i) {
+        uint32_t at;
+        if (!ready(&at)) return;
+        Tile next = {};
+        GradPart np = {};
+        bool more = false, taken = false;
+        float next_w = 0.0f;
+        const auto look_ahead = [&](int b) {
+            taken = true;
+            more = take_tile(i, next);
+            if (!more) return;
+            np = grad_part(next, rank, n_out);
+            if (np.have > 0) fetch(np, 0, b);
+            if (lane < np.rows) next_w = row_weight(gate, np.row + lane);
+        };
+        if (p.have == 0) release();
+        float sum = 0.0f;
+        int ok = 1;
+#pragma unroll 1
+        for (int c = 0; c < p.have; ++c, buf ^= 1) {
+            uint32_t v[32];
+            tmem_ld32(at + c * kGateCols, v);
+            tmem_wait_ld();
+            if (c == p.have - 1) release();
+            if (!wait_bar(bar, phase, abort, err)) ok = 0;
+            phase ^= 1u;
+            if (!__all_sync(0xffffffffu, ok)) return;
+            if (c + 1 < p.have) fetch(p, c + 1, buf ^ 1);
+            uint8_t* lines = staging + buf * 2 * kHalfLines;
+            sum += gated_grad_lines(lines, v, w);
+            const int col = p.col + c * kGateCols;
+            fence_async_shared();
+            __syncwarp();
+            if (p.rows >= 32) {
+                if (lane == 0) {
+                    const uint32_t from = staging_at + (uint32_t)(buf * 2 * kHalfLines);
+                    tma_store_3d(&tmOut, from, col, 0, (int)p.row);
+                    tma_store_3d(&tmOut, from + kHalfLines, col, 1, (int)p.row);
+                    bulk_commit();
+                }
+            } else {
+                // the segment ends inside these rows: the ones after it are another expert's
+                uint16_t* to = gate.gu + p.row * 2 * n_out + col;
+                store_half_lines(lines, to, 2 * n_out, p.rows, n_out - col);
+                store_half_lines(lines + kHalfLines, to + n_out, 2 * n_out, p.rows, n_out - col);
+                fence_async_shared();
+                __syncwarp();
+            }
+            if (c == p.have - 1) look_ahead(buf ^ 1);
+        }
+        if (!taken) look_ahead(buf);
+        if (gate.parts && lane < p.rows && p.have > 0)
+            gate.parts[(long long)(p.col / kEpilogueCols) * R + p.row + lane] = sum;
+        if (!more) return;
+        t = next;
+        p = np;
+        w = next_w;
+    }
 }
 
 // kFew (products over rows): tiles of 256 columns of the output and BF rows, the matrix
@@ -1096,7 +1213,33 @@ __device__ __forceinline__ void grouped_product(
         uint8_t* staging = staging_area + (size_t)(warp - 4) * kStagingOf<kMode>;
         const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[0]), first);
         int acc = 0;
-        uint32_t acc_phase = 0, lines_phase = 0;
+        uint32_t acc_phase = 0;
+        if constexpr (kMode == kGatedGrad) {
+            const auto take_tile = [&](int i, Tile& t) {
+                return warp_next(ctl, i, leader, abort_flag, err, t);
+            };
+            // this warp's columns of the next accumulator, once it is ready
+            const auto ready = [&](uint32_t* at) {
+                int ok = 0;
+                if (lane == 0)
+                    ok = wait_bar(smem_u32(&ctl->tfull[acc]), acc_phase, abort_flag, err);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                tc_fence_after();
+                *at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BT + half * kCols);
+                return ok != 0;
+            };
+            const auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
+                if (++acc == kAccs) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            };
+            gated_grad_tiles(tmGu, tmOut, gate, staging, smem_u32(&ctl->lines[warp - 4]), rank, R,
+                             n_out, abort_flag, err, take_tile, ready, release);
+        } else
         for (int i = 0;; ++i) {
             Tile t = {};
             if (!warp_next(ctl, i, leader, abort_flag, err, t)) break;
@@ -1153,56 +1296,6 @@ __device__ __forceinline__ void grouped_product(
                                       (uint32_t)(acc * BT + half * 64);
                 gated_out(tmGu, tmOut, gate, staging, g_at, g_at + BT / 2, row, rows,
                           t.nb * BH + half * 64, n_out, w, release);
-                continue;
-            } else if constexpr (kMode == kGatedGrad) {
-                const int at_row = t.mb * BT + (int)rank * BH + q * 32, rows = t.cnt - at_row;
-                const int col = t.nb * BT + half * kEpilogueCols;
-                const long long row = (long long)t.off + at_row;
-                const int have = rows <= 0 || col >= n_out ? 0 : n_out - col > 64 ? 2 : 1;
-                const uint32_t bar = smem_u32(&ctl->lines[warp - 4]);
-                const auto fetch = [&](int c) {
-                    if (lane != 0) return;
-                    bulk_wait_read();  // what went out from there has been read
-                    mbar_expect_tx(bar, 2 * kStagingBytes);
-                    tma_load_3d(smem_u32(staging), &tmGu, bar, col + c * 64, 0, (int)row);
-                    tma_load_3d(smem_u32(staging) + kStagingBytes, &tmGu, bar, col + c * 64, 1,
-                                (int)row);
-                };
-                if (have > 0) fetch(0);
-                const float w = lane < rows ? row_weight(gate, row + lane) : 0.0f;
-                if (!ready()) break;
-                const uint32_t at = part();
-                if (have == 0) {
-                    release();
-                    continue;
-                }
-                float sum = 0.0f;
-                int ok = 1;
-#pragma unroll 1
-                for (int c = 0; c < have; ++c) {
-                    uint32_t v[64];
-                    tmem_ld_line(at + c * 64, v);
-                    tmem_wait_ld();
-                    if (c == have - 1) release();
-                    if (!wait_bar(bar, lines_phase, abort_flag, err)) ok = 0;
-                    lines_phase ^= 1u;
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    sum += gated_grad_lines(staging, v, w);
-                    const int left = n_out - col - c * 64;
-                    uint16_t* to = gate.gu + row * 2 * n_out + col + c * 64;
-                    lines_out(&tmOut, staging, col + c * 64, 0, (int)row, true, to, 2 * n_out,
-                              rows, left);
-                    lines_out(&tmOut, staging + kStagingBytes, col + c * 64, 1, (int)row, true,
-                              to + n_out, 2 * n_out, rows, left);
-                    fence_async_shared();
-                    __syncwarp();
-                    if (c + 1 < have) fetch(c + 1);
-                }
-                if (!__all_sync(0xffffffffu, ok)) break;
-                if (gate.parts && lane < rows)
-                    gate.parts[(long long)(col / kEpilogueCols) * R + row + lane] = sum;
-                fence_async_shared();
-                __syncwarp();
                 continue;
             }
 
@@ -1646,12 +1739,13 @@ moe_status launch_weights(const uint16_t* dout, const uint16_t* rows, const Gemm
     return out_f32 ? with(launch<kWeightsGrad, float>) : with(launch<kWeightsGrad, __nv_bfloat16>);
 }
 
-// gu (or its gradient) [N*k, 2*I] as [N*k][2][I], in boxes of 32 rows of 64 columns of a half.
-bool map_gu(CUtensorMap* m, const void* ptr, long long R, int I) {
+// gu (or its gradient) [N*k, 2*I] as [N*k][2][I], in boxes of 32 rows of 64 or 32 columns of a
+// half.
+bool map_gu(CUtensorMap* m, const void* ptr, long long R, int I, int columns) {
     const uint64_t sizes[3] = {(uint64_t)I, 2, (uint64_t)R};
     const uint64_t strides[2] = {(uint64_t)I * 2, (uint64_t)I * 4};
-    const uint32_t box[3] = {64, 1, 32};
-    return map_tiled(m, 3, ptr, sizes, strides, box);
+    const uint32_t box[3] = {(uint32_t)columns, 1, 32};
+    return map_typed(m, 3, ptr, sizes, strides, box, kMapBF16, columns * 2);
 }
 
 template <int kMode, bool kFew>
@@ -1691,7 +1785,7 @@ moe_status launch_gated_forward(const uint16_t* rows, const GemmGroup& g, int c_
         !map_tiled(&b, 4, w, sizes, strides, box) || !map_lines(&o, gate.h, 0, g.R, I, false))
         return MOE_ERR_UNSUPPORTED;
     gu = o;
-    if (gate.gu && !map_gu(&gu, gate.gu, g.R, I)) return MOE_ERR_UNSUPPORTED;
+    if (gate.gu && !map_gu(&gu, gate.gu, g.R, I, 64)) return MOE_ERR_UNSUPPORTED;
     const long long tiles = (used + (g.R - used) / (few ? BF : BT)) * blocks_of(I, BT / 2);
     return few ? launch_gated<kGated, true>(a, b, o, gu, gate, g, tiles, c_in, I, 0, st)
                : launch_gated<kGated, false>(a, b, o, gu, gate, g, tiles, c_in, I, 0, st);
@@ -1704,7 +1798,7 @@ moe_status launch_gated_grad(const uint16_t* dout, const GemmGroup& g, int c_out
     int groups = 0;
     if (!map_rows(&a, dout, 0, g.R, c_out, BH) ||
         !map_mn(&b, w, g.E, c_out, I, box_columns(I, true), &groups) ||
-        !map_gu(&gu, gu_in, g.R, I) || !map_gu(&o, gate.gu, g.R, I))
+        !map_gu(&gu, gu_in, g.R, I, kGateCols) || !map_gu(&o, gate.gu, g.R, I, kGateCols))
         return MOE_ERR_UNSUPPORTED;
     const long long used = g.R < g.E ? g.R : g.E;
     const long long tiles = (used + (g.R - used) / BT) * blocks_of(I, BT);

@@ -194,10 +194,11 @@ bool map_3d(CUtensorMap* m, const void* ptr, uint64_t E, uint64_t rows, uint64_t
 bool map_packed(CUtensorMap* m, CUtensorMap* second, const void* ptr, int E, int n_blocks, int K,
                 uint32_t box_rows);
 
-// The same of any rank from 2 to 4, element type and swizzle (none: boxes of other widths).
+// The same of any rank from 2 to 4, element type and swizzle (128 or 64 bytes, the
+// width of a box; 0: none).
 enum MapType { kMapBF16, kMapF32, kMapF16 };
 bool map_typed(CUtensorMap* m, int rank, const void* ptr, const uint64_t* sizes,
-               const uint64_t* strides, const uint32_t* boxes, MapType type, bool swizzle);
+               const uint64_t* strides, const uint32_t* boxes, MapType type, int swizzle);
 bool map_tiled(CUtensorMap* m, int rank, const void* ptr, const uint64_t* sizes,
                const uint64_t* strides, const uint32_t* boxes, bool f32 = false);
 

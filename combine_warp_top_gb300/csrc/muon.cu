@@ -33,13 +33,14 @@ constexpr int kTmemCols = BT * kAccs;
 constexpr int OP_BYTES = BH * BK * 2;
 constexpr int BOX_BYTES = OP_BYTES / 2;
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
-constexpr int kThreads = 384;
-constexpr int kEpilogueWarps = 8;
 constexpr int kLine = 64;                 // columns of a line of 128 bytes
 constexpr int kLinesBytes = 32 * 128;     // 32 of them
-constexpr int kStagingBytes = 2 * kLinesBytes;  // of an epilogue warp
-// Registers a thread: 384 x 168 at launch = 128 x 88 + 256 x 208.
-constexpr int kRegsOther = 88, kRegsEpilogue = 208;
+// Epilogue warps (kWarps): 4, with all 256 columns of 32 rows each and two buffers for the lines
+// of two inputs or outputs, or 8 with 128 columns and one buffer.  With two the next line's
+// inputs come in while a line is worked on: 64 matrices of 2048 x 1408, 4369 us with 8, 4195
+// with 4.  A tile that nothing runs beside is done sooner by 8: 8 of 1024 x 1024, 421 and 384 us.
+constexpr int kMaxWarps = 8;
+constexpr int kStagingBytes = 4 * 4 * kLinesBytes;  // of all of them
 constexpr int kMaxDim = 65536;
 // G and S are kept times 2^12, X times 2^p with 2^p about the root of its longer side, so
 // that entries far below the largest are normal fp16 numbers.
@@ -53,14 +54,14 @@ struct Ctl {
     uint64_t empty[kStages];   // each CTA: its stage may be refilled
     uint64_t tfull[kAccs];     // each CTA: accumulator ready
     uint64_t tempty[kAccs];    // leader: accumulator drained by both CTAs
-    uint64_t lines[kEpilogueWarps];  // each CTA: a warp's lines have come in
+    uint64_t lines[kMaxWarps];  // each CTA: a warp's lines have come in
     uint64_t done;             // leader: every issued MMA retired
     uint32_t tmem_base;
     int abort;
 };
-constexpr int kBarriers = 2 * kStages + 2 * kAccs + kEpilogueWarps + 1;
+constexpr int kBarriers = 2 * kStages + 2 * kAccs + kMaxWarps + 1;
 constexpr size_t kSmem = 1024 + (size_t)kStages * STAGE_BYTES +
-                         (size_t)kEpilogueWarps * kStagingBytes + ((sizeof(Ctl) + 15) & ~size_t(15));
+                         (size_t)kStagingBytes + ((sizeof(Ctl) + 15) & ~size_t(15));
 static_assert(kSmem <= 227 * 1024, "shared memory of one block");
 
 struct Dims {
@@ -183,8 +184,8 @@ __device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLin
 
 // in, in2: G, or X's two halves (kStep, kLast); out, out2: the output and its mirror image or
 // X's second half.
-template <Form kForm, bool kMnA, bool kMnB>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <Form kForm, bool kMnA, bool kMnB, int kWarps>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1)
     muon_product_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmIn,
@@ -193,12 +194,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tmOut2, Dims d, float alpha,
                         float beta, int* err) {
     constexpr bool kSym = kForm == kGram || kForm == kSquare;
+    constexpr bool kTwo = kWarps == 4;             // two buffers
+    constexpr int kColumns = BT * 4 / kWarps;      // of an epilogue warp
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t* tiles = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
     const uint32_t tiles_addr = smem_u32(tiles);
     uint8_t* staging_area = tiles + (size_t)kStages * STAGE_BYTES;
-    auto* ctl = reinterpret_cast<Ctl*>(staging_area + (size_t)kEpilogueWarps * kStagingBytes);
+    auto* ctl = reinterpret_cast<Ctl*>(staging_area + (size_t)kStagingBytes);
     volatile int* abort_flag = &ctl->abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -214,7 +217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane < kBarriers) {
             const int tempty = 2 * kStages + kAccs;
             mbar_init(smem_u32(&ctl->full[0] + lane),
-                      lane >= tempty && lane < tempty + kAccs ? 2 * kEpilogueWarps : 1);
+                      lane >= tempty && lane < tempty + kAccs ? 2 * kWarps : 1);
         }
         if (lane == 31) ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -235,7 +238,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
     if (warp < 4) {
-        regs_shrink<kRegsOther>();
         if (warp == 0 && elect_one()) {
             // ---------------- TMA producer (both CTAs) ----------------
             const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
@@ -326,35 +328,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------- epilogue (both CTAs): own 128 rows ----------------
-        regs_grow<kRegsEpilogue>();
-        const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quadrant, 128 columns
-        uint8_t* lines = staging_area + (size_t)(warp - 4) * kStagingBytes;
+        const int q = warp & 3, part = (warp - 4) >> 2;  // TMEM lane quadrant, columns
+        uint8_t* lines = staging_area + (size_t)(warp - 4) * (kStagingBytes / kWarps);
         const uint32_t lines_addr = smem_u32(lines), bar = smem_u32(&ctl->lines[warp - 4]);
         const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[0]), 0);
-        int acc = 0;
+        int acc = 0, buf = 0;
         uint32_t acc_phase = 0, lines_phase = 0;
         for (long long i = blockIdx.x / 2; i < total; i += pairs) {
             const Tile t = decode<kSym>(i, per_matrix, MB, NB);
-            const int row = t.mb * BT + (int)rank * BH + q * 32;
-            const int col = t.nb * BT + half * (BT / 2);
+            const int row = t.mb * BT + (int)rank * BH + q * 32, col = t.nb * BT + part * kColumns;
             // lines of 64 columns that there are
-            const int have = row >= d.m || col >= d.n ? 0 : d.n - col > kLine ? 2 : 1;
-            const auto fetch = [&](int c) {
+            const int left = d.n - col < kColumns ? d.n - col : kColumns;
+            const int have = row >= d.m || left <= 0 ? 0 : (left + kLine - 1) / kLine;
+            // the inputs' lines c into buffer b, once what went out from there has been read
+            const auto fetch = [&](int c, int b) {
                 if (kForm == kGram || lane != 0) return;
-                bulk_wait_read();  // what went out from there has been read
+                bulk_wait_read();
+                const uint32_t to = lines_addr + (uint32_t)(b * 2 * kLinesBytes);
                 mbar_expect_tx(bar, kForm == kSquare ? kLinesBytes : 2 * kLinesBytes);
-                tma_load_3d(lines_addr, &tmIn, bar, col + c * kLine, row, t.e);
+                tma_load_3d(to, &tmIn, bar, col + c * kLine, row, t.e);
                 if (kForm != kSquare)
-                    tma_load_3d(lines_addr + kLinesBytes, &tmIn2, bar, col + c * kLine, row, t.e);
+                    tma_load_3d(to + kLinesBytes, &tmIn2, bar, col + c * kLine, row, t.e);
             };
-            if (have > 0) fetch(0);
+            if (have > 0) fetch(0, buf);
             int ok = 0;
             if (lane == 0)
                 ok = wait_bar(smem_u32(&ctl->tfull[acc]), acc_phase, abort_flag, err);
             ok = __shfl_sync(0xffffffffu, ok, 0);
             tc_fence_after();
             if (!ok) break;
-            const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BT + half * 128);
+            const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BT + part * kColumns);
             const auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();
@@ -369,24 +372,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tmem_wait_ld();
                 if (c == have - 1) release();
                 if (kForm == kGram) {
-                    if (lane == 0) bulk_wait_read();
+                    if (lane == 0) {  // the buffer's last lines have been read
+                        if (kTwo) bulk_wait_read_but_one();
+                        else bulk_wait_read();
+                    }
                 } else {
                     if (!wait_bar(bar, lines_phase, abort_flag, err)) ok = 0;
                     lines_phase ^= 1u;
                 }
                 if (!__all_sync(0xffffffffu, ok)) break;
-                combine<kForm>(lines, v, alpha, beta);
+                if (kTwo && c + 1 < have) fetch(c + 1, buf ^ 1);
+                uint8_t* mine = lines + buf * 2 * kLinesBytes;
+                combine<kForm>(mine, v, alpha, beta);
                 fence_async_shared();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_3d(&tmOut, lines_addr, col + c * kLine, row, t.e);
+                    const uint32_t from = smem_u32(mine);
+                    tma_store_3d(&tmOut, from, col + c * kLine, row, t.e);
                     if (kForm == kStep)
-                        tma_store_3d(&tmOut2, lines_addr + kLinesBytes, col + c * kLine, row, t.e);
+                        tma_store_3d(&tmOut2, from + kLinesBytes, col + c * kLine, row, t.e);
                     if (kSym && t.mb != t.nb)
-                        tma_store_3d(&tmOut2, lines_addr + kLinesBytes, row, col + c * kLine, t.e);
+                        tma_store_3d(&tmOut2, from + kLinesBytes, row, col + c * kLine, t.e);
                     bulk_commit();
                 }
-                if (c + 1 < have) fetch(c + 1);
+                if (!kTwo && c + 1 < have) fetch(c + 1, buf);
+                if (kTwo) buf ^= 1;
             }
             if (!__all_sync(0xffffffffu, ok)) break;
             if (++acc == kAccs) {
@@ -410,7 +420,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 constexpr int kBlock = 256;
 constexpr int kChunk = kBlock * 8 * 4;  // elements of a block's round
-constexpr int kMaxParts = 64;           // blocks of a matrix
+constexpr int kMaxParts = 256;          // blocks of a matrix
+constexpr int kAhead = 2;               // vectors of a thread that are loaded together
 
 __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
     const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
@@ -452,33 +463,46 @@ __global__ void __launch_bounds__(kBlock)
     after_previous();
     const long long at = (long long)blockIdx.y * size;
     double sum = 0.0, big = 0.0;
-    for (long long i = ((long long)blockIdx.x * kBlock + threadIdx.x) * 8; i < size;
-         i += (long long)gridDim.x * kBlock * 8) {
-        float g[8], u[8];
-        load8(grad + at + i, g);
+    const long long step = (long long)gridDim.x * kBlock * 8;
+    for (long long i0 = ((long long)blockIdx.x * kBlock + threadIdx.x) * 8; i0 < size;
+         i0 += kAhead * step) {
+        // all loads of kAhead vectors before the first is worked on
+        float g[kAhead][8], b[kAhead][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = g[j];
-        if (buf) {
-            float b[8];
-            load8(buf + at + i, b);
+        for (int v = 0; v < kAhead; ++v) {
+            const long long i = i0 + v * step;
+            if (i < size) {
+                load8(grad + at + i, g[v]);
+                if (buf) load8(buf + at + i, b[v]);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < kAhead; ++v) {
+            const long long i = i0 + v * step;
+            if (i >= size) break;
+            float u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = g[v][j];
+            if (buf) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    b[v][j] = fmaf(beta, b[v][j], g[v][j]);
+                    u[j] = nesterov ? fmaf(beta, b[v][j], g[v][j]) : b[v][j];
+                }
+                float4* to = reinterpret_cast<float4*>(new_buf + at + i);
+                to[0] = make_float4(b[v][0], b[v][1], b[v][2], b[v][3]);
+                to[1] = make_float4(b[v][4], b[v][5], b[v][6], b[v][7]);
+            }
+            float s = 0.0f, t = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                b[j] = fmaf(beta, b[j], g[j]);
-                u[j] = nesterov ? fmaf(beta, b[j], g[j]) : b[j];
+                const float small = u[j] * 0x1p-64f;
+                s = fmaf(u[j], u[j], s);
+                t = fmaf(small, small, t);
             }
-            float4* to = reinterpret_cast<float4*>(new_buf + at + i);
-            to[0] = make_float4(b[0], b[1], b[2], b[3]);
-            to[1] = make_float4(b[4], b[5], b[6], b[7]);
+            sum += s;
+            big += t;
         }
-        float s = 0.0f, t = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float small = u[j] * 0x1p-64f;
-            s = fmaf(u[j], u[j], s);
-            t = fmaf(small, small, t);
-        }
-        sum += s;
-        big += t;
     }
     __shared__ double2 warps[kBlock / 32];
 #pragma unroll
@@ -505,19 +529,26 @@ __global__ void __launch_bounds__(kBlock)
     after_previous();
     __shared__ float factors[2];
     const long long at = (long long)blockIdx.y * size;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x < 32) {
         double sum = 0.0, big = 0.0;
-        for (int i = 0; i < n_parts; ++i) {
+        for (int i = threadIdx.x; i < n_parts; i += 32) {
             const double2 v = parts[(long long)blockIdx.y * n_parts + i];
             sum += v.x;
             big += v.y;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            big += __shfl_xor_sync(0xffffffffu, big, o);
         }
         // in two factors: one alone may be too small for fp32
         if (!(sum < 1e300)) sum = big * 0x1p128;
         int ex = 0;
         const double f = frexp(1.0 / (sqrt(sum) + (double)eps), &ex);
-        factors[0] = (float)ldexp(f, ex / 2);
-        factors[1] = (float)ldexp(1.0, ex - ex / 2 + p);
+        if (threadIdx.x == 0) {
+            factors[0] = (float)ldexp(f, ex / 2);
+            factors[1] = (float)ldexp(1.0, ex - ex / 2 + p);
+        }
     }
     __syncthreads();
     const float f0 = factors[0], f1 = factors[1];
@@ -562,14 +593,15 @@ bool map_matrices(CUtensorMap* m, const void* ptr, int E, int rows, int cols, ui
     const uint64_t sizes[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)E};
     const uint64_t strides[2] = {(uint64_t)cols * 2, (uint64_t)cols * rows * 2};
     const uint32_t box[3] = {box_cols, box_rows, 1};
-    return map_typed(m, 3, ptr, sizes, strides, box, type, box_cols * 2 == 128);
+    return map_typed(m, 3, ptr, sizes, strides, box, type, box_cols * 2 == 128 ? 128 : 0);
 }
 
-template <Form kForm, bool kMnA, bool kMnB>
-moe_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in,
-                          const CUtensorMap& in2, const CUtensorMap& out, const CUtensorMap& out2,
-                          const Dims& d, float alpha, float beta, int* err, cudaStream_t st) {
-    const auto kernel = muon_product_kernel<kForm, kMnA, kMnB>;
+template <Form kForm, bool kMnA, bool kMnB, int kWarps>
+moe_status launch_form(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in,
+                       const CUtensorMap& in2, const CUtensorMap& out, const CUtensorMap& out2,
+                       const Dims& d, float alpha, float beta, int* err, long long pairs,
+                       cudaStream_t st) {
+    const auto kernel = muon_product_kernel<kForm, kMnA, kMnB, kWarps>;
     static OncePerDevice set;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
@@ -579,19 +611,33 @@ moe_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUte
             return MOE_ERR_CUDA;
         set.finish(dev);
     }
+    return cuda_status(launch_chained(kernel, (int)(2 * pairs), 128 + 32 * kWarps, kSmem, st, a, b,
+                                      in, in2, out, out2, d, alpha, beta, err));
+}
+template <Form kForm, bool kMnA, bool kMnB>
+moe_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in,
+                          const CUtensorMap& in2, const CUtensorMap& out, const CUtensorMap& out2,
+                          const Dims& d, float alpha, float beta, int* err, cudaStream_t st) {
     const long long MB = blocks_of(d.m, BT), NB = blocks_of(d.n, BT);
     const long long tiles =
         d.E * (kForm == kGram || kForm == kSquare ? NB * (NB + 1) / 2 : MB * NB);
     const long long most = sm_count() / 2;
-    return cuda_status(launch_chained(kernel, (int)(2 * (tiles < most ? tiles : most)), kThreads,
-                                      kSmem, st, a, b, in, in2, out, out2, d, alpha, beta, err));
+    // 8 warps where a pair has no more than two tiles
+    return tiles > 2 * most
+               ? launch_form<kForm, kMnA, kMnB, 4>(a, b, in, in2, out, out2, d, alpha, beta, err,
+                                                   most, st)
+               : launch_form<kForm, kMnA, kMnB, 8>(a, b, in, in2, out, out2, d, alpha, beta, err,
+                                                   tiles < most ? tiles : most, st);
 }
 
 template <typename G>
 moe_status launch_prepare(const G* grad, const float* buf, float* new_buf, const moe_muon_shape& s,
                           int p, double2* parts, __half* hi, __half* lo, cudaStream_t st) {
     const long long size = (long long)s.M * s.N, rounds = (size + kChunk - 1) / kChunk;
-    const int blocks = (int)(rounds < kMaxParts ? rounds : kMaxParts);
+    // some 16 blocks an SM in all, each matrix the same number
+    const long long share = 16LL * sm_count() / s.E + 1;
+    const long long most = share < kMaxParts ? share : kMaxParts;
+    const int blocks = (int)(rounds < most ? rounds : most);
     const bool nesterov = s.nesterov != 0;
     MOE_TRY(cuda_status(launch_chained(muon_momentum_kernel<G>, dim3(blocks, s.E), kBlock, 0, st,
                                        grad, buf, new_buf, size, nesterov, s.momentum, parts)));
