@@ -30,11 +30,15 @@ __device__ __forceinline__ float row_weight(const Gate& g, long long row) {
     return hit < 0 ? 0.0f : g.topk_w[first + hit];
 }
 
-// exp and divide of the hardware: 2 + 1.2 |g| units of 2^-23 (CUDA's bound), 2e-6 relative at
-// |g| = 12, against 2^-8 of a bf16 output.  Below g = -87.3 the quotient is 0, off by less
-// than 2^-126.
+// 1 / (1 + 2^(-g log2 e)) by the hardware's exponential and reciprocal, without the scaling
+// that the library's functions give denormal results: a sigmoid below 2^-126 is 0.  The
+// product -g log2 e is rounded to fp32, which makes the power off by |g| 2^-24 (and 2^-22 for
+// ex2.approx, 2^-23 for rcp.approx): 1e-6 relative at |g| = 12, against 2^-8 of a bf16 output.
 __device__ __forceinline__ float sigmoid(float g) {
-    return __fdividef(1.0f, 1.0f + __expf(-g));
+    float p, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + p));
+    return s;
 }
 
 }  // namespace moe

@@ -1562,6 +1562,7 @@ __global__ void __launch_bounds__(256)
     }
     if (!mine) return;
     float sum = 0.0f;
+#pragma unroll 8
     for (int p = 0; p < n_parts; ++p) sum += parts[p * R + row];
     dtopk_w[pair] = sum;
 }

@@ -685,9 +685,9 @@ def moe_gated_gemm(rows, layout: Layout, shape: Shape, w_gate_up, topk_w, gu, h,
     """[g | u] = rows[i] Wgu[e]^T and h[i] = w_i SiLU(g) u in one kernel; w_gate_up
     [E, 2*I, C_in] bf16, gu [N*k, 2*I] bf16 (None: not wanted), h [N*k, I] bf16."""
     s, bf = shape, torch.bfloat16
+    if isinstance(w_gate_up, torch.Tensor) and w_gate_up.shape[1:2] != (2 * s.I,):
+        raise ValueError(f"w_gate_up: expected 2*I = {2 * s.I} rows, got {tuple(w_gate_up.shape)}")
     w_at, co, ci = _expert_matrices(w_gate_up, bf, s, "w_gate_up")
-    if co != 2 * s.I:
-        raise ValueError(f"w_gate_up: expected 2*I = {2 * s.I} rows, got {co}")
     _check(load().moe_gated_gemm(
         _exact(rows, bf, (s.R, ci), "rows"), _lay(layout, s), s.ref, ci, w_at,
         _exact(topk_w, torch.float32, (s.N, s.k), "topk_w"), _exact(gu, bf, (s.R, 2 * s.I), "gu"),
@@ -699,9 +699,9 @@ def moe_gated_gemm_grad(dout, layout: Layout, shape: Shape, w_down, topk_w, gu, 
     """dgu [N*k, 2*I] (may be gu) and dtopk_w fp32 [N, k] (None: not wanted) from
     dh = dout[i] Wd[e], w_down [E, C_out, I] bf16; ws of gated_workspace(shape)."""
     s, bf = shape, torch.bfloat16
+    if isinstance(w_down, torch.Tensor) and w_down.shape[2:] != (s.I,):
+        raise ValueError(f"w_down: expected I = {s.I} columns, got {tuple(w_down.shape)}")
     w_at, co, ci = _expert_matrices(w_down, bf, s, "w_down")
-    if ci != s.I:
-        raise ValueError(f"w_down: expected I = {s.I} columns, got {ci}")
     _check(load().moe_gated_gemm_grad(
         _exact(dout, bf, (s.R, co), "dout"), _lay(layout, s), s.ref, co, w_at,
         _exact(topk_w, torch.float32, (s.N, s.k), "topk_w"), _exact(gu, bf, (s.R, 2 * s.I), "gu"),
@@ -1018,14 +1018,32 @@ class MoELayer:
     [E] or None."""
 
     def __init__(self, shape: Shape, w_gate, w_up, w_down, placement=None, device="cuda",
-                 shared=None, fuse_combine=False, pack=True):
+                 shared=None, fuse_combine=False, pack=True, w4=None):
         """shared: optional (w_gate_s [I_s, H], w_up_s [I_s, H], w_down_s [H, I_s])
         of a shared expert run on every token.  fuse_combine: run the down GEMM
         with the combine in its epilogue (moe_ffn_down_combine, fp32
         accumulator) instead of moe_ffn_down + moe_combine.  pack: copy
         row-major weights once into the packed layout (moe_pack_weights) and
         run the layer on that copy (the layer's shape becomes "packed"); the
-        results are bit-identical, the weight stream faster."""
+        results are bit-identical, the weight stream faster.  w4: run the routed
+        experts on 4-bit weights (moe_w4_gated_gemm, moe_w4_gemm), made for decoding
+        steps: a group size (32, 64 or 128) to quantise the given row-major weights
+        with, or the (gate and up, down) W4Matrices themselves (the weight arguments
+        None); the layer's shape is row-major then."""
+        if w4 is not None:
+            if fuse_combine or shape.gemm == "fused" or shape.weights != "row_major":
+                raise ValueError("4-bit experts run their own two products on row-major shapes")
+            if not isinstance(w4, (tuple, list)):
+                w4 = (quantize_w4(torch.cat([w_gate, w_up], 1), w4, gated=True),
+                      quantize_w4(w_down, w4))
+            for m, gated, size in ((w4[0], True, (shape.I, shape.H)),
+                                   (w4[1], False, (shape.H, shape.I))):
+                _w4(m, shape, gated)
+                if (m.C_out, m.C_in) != size:
+                    raise ValueError(f"w4: expected matrices of {size}, got {(m.C_out, m.C_in)}")
+            w_gate = w_up = w_down = None
+            pack = False
+        self.w4 = w4
         if fuse_combine and shared is not None:
             raise ValueError("the combine fused into the down GEMM adds no shared expert")
         if fuse_combine and shape.gemm == "fused":
@@ -1051,12 +1069,14 @@ class MoELayer:
         self.layout = Layout(shape, device)
         rows_d = shape.R_d_max if shape.dedup else shape.R
         # plain rows gathered inside the gate/up GEMM need no dispatch buffer
-        self.fused_dispatch = moe_layer_skips_dispatch(shape)
+        self.fused_dispatch = moe_layer_skips_dispatch(shape) and w4 is None
         # the expert FFN as one kernel (h on chip), unless the combine is to go
         # into the down GEMM's epilogue
-        self.fused_ffn = moe_layer_fuses_ffn(shape) and not fuse_combine
+        self.fused_ffn = moe_layer_fuses_ffn(shape) and not fuse_combine and w4 is None
         self.xd = torch.empty(1 if self.fused_dispatch else max(rows_d, 1), H, **bf)
-        self.xe = None  # the dedup expansion happens inside the gate/up GEMM
+        # the dedup expansion happens inside the gate/up GEMM, but for 4-bit experts
+        self.xe = (torch.empty(max(shape.R, 1), H, **bf) if w4 is not None and shape.dedup
+                   else None)
         self.h = torch.empty(max(shape.R, 1), I, **bf)
         self.y = torch.empty(max(shape.R, 1), H, **bf)
         # the dedup combine keeps its partial rows in registers (moe_combine with
@@ -1065,11 +1085,11 @@ class MoELayer:
         self.out = torch.empty(max(N, 1), H, **bf)
         self.acc = (torch.empty(max(N, 1), H, dtype=torch.float32, device=device)
                     if fuse_combine else None)
-        self.ws = workspace(shape, device)
+        self.ws = workspace(shape, device) if w4 is None else w4_workspace(shape, device)
 
     def forward(self, logits, x, residual=None, out=None, stream=None):
         out = self.out if out is None else out
-        if self.shared is not None or self.fuse_combine:
+        if self.shared is not None or self.fuse_combine or self.w4 is not None:
             return self.forward_stages(logits, x, residual, out, stream)
         moe_layer_forward(logits, x, self.placement, self.w_gate, self.w_up, self.w_down,
                           residual, self.shape, self.topk_ids, self.topk_w, self.layout,
@@ -1136,6 +1156,8 @@ class MoELayer:
         elif name == "down_combine":
             moe_ffn_down_combine(self.h, self.topk_w, self.layout, s, self.w_down, residual,
                                  self.acc, out, self.ws, st)
+        elif name == "down" and self.w4 is not None:
+            moe_w4_gemm(self.h, self.layout, s, self.w4[1], self.y, self.ws, st)
         elif name == "down":
             moe_ffn_down(self.h, self.layout, s, self.w_down, self.y, self.ws, st)
         elif name == "shared":
@@ -1167,7 +1189,14 @@ class MoELayer:
         by the GEMM's gather warps; plain rows gathered from x when the
         dispatch is fused, else read from the dispatched rows."""
         s, lay = self.shape, self.layout
-        if s.dedup:
+        if self.w4 is not None:
+            rows = self.xd
+            if s.dedup:
+                moe_expand(self.xd, lay, s, self.xe, st)
+                rows = self.xe
+            # the combine weighs the rows
+            moe_w4_gated_gemm(rows, lay, s, self.w4[0], None, self.h, self.ws, st)
+        elif s.dedup:
             moe_ffn_gate_up_gather(self.xd, lay["expand_src"], lay, s, self.w_gate, self.w_up,
                                    self.h, self.ws, st)
         elif self.fused_dispatch:
@@ -1188,6 +1217,8 @@ class MoELayer:
         # fused combine: GEMM + finish (the accumulator memset is a copy-engine op)
         down_combine = 2 if self.fuse_combine else 1 + 1
         gate_up = 0 if self.fused_ffn else 1  # the fused FFN is one launch with the down
+        if self.w4 is not None and s.dedup:
+            gate_up += 1  # the expansion
         return 1 + layout_launches(s) + dispatch + gate_up + down_combine + shared
 
     def forward_host(self, logits_h, x_h, residual_h, out_h, dev_inputs=None, stream=None):

@@ -12,9 +12,12 @@ h between an expert's two products (moe_swiglu), so the combine is a plain sum o
 token's k rows and each row's gradient is its token's: the dispatch and the combine
 of the forward pass serve the backward pass with their roles exchanged.
 
-    python -m combine_warp_top_gb300.train     # a few steps on a toy regression
+    python -m combine_warp_top_gb300.train          # a few steps on a toy regression
+    python -m combine_warp_top_gb300.train --muon   # with the fused gate and Muon
 """
 from __future__ import annotations
+
+import sys
 
 import torch
 
@@ -38,7 +41,12 @@ class MoETrainBlock:
     it gives x.  Each is 2^-8 at most, as at the block's other activations.
     """
 
-    def __init__(self, N, H, E, k, I, residual_scale=1.0, eps=1e-6, seed=0, device="cuda"):
+    def __init__(self, N, H, E, k, I, residual_scale=1.0, eps=1e-6, seed=0, device="cuda",
+                 fuse_gate=False):
+        """fuse_gate: the gate and its gradient inside the products before and behind them
+        (moe_gated_gemm, moe_gated_gemm_grad): less memory traffic, and g, u and dh are not
+        rounded to bf16 on their way."""
+        self.fuse_gate = bool(fuse_gate)
         self.shape = s = moe.Shape(N, H, E, k, 1, I)
         # the router is a product of one group: all N rows, one matrix
         self.dense = moe.Shape(N, H, 1, 1, 1, I)
@@ -70,13 +78,15 @@ class MoETrainBlock:
         self.dense_layout = moe.Layout(self.dense, device)
         self.dense_layout["expert_counts"].fill_(N)
         self.dense_layout["expert_offsets"].copy_(torch.tensor([0, N], dtype=torch.int32))
-        self.ws, self.dense_ws = moe.workspace(s, device), moe.workspace(self.dense, device)
+        self.ws = (moe.gated_workspace if fuse_gate else moe.workspace)(s, device)
+        self.dense_ws = moe.workspace(self.dense, device)
         self.ws_pre, self.ws_post = (moe.norm_workspace(n, device) for n in (self.pre, self.post))
         R = s.R
         self.x, self.y, self.dy, self.dx = (torch.empty(N, H, **bf) for _ in range(4))
         self.rows, self.y_rows, self.d_rows = (torch.empty(R, H, **bf) for _ in range(3))
         self.gu, self.dgu = (torch.empty(R, 2 * I, **bf) for _ in range(2))
-        self.h, self.dh = (torch.empty(R, I, **bf) for _ in range(2))
+        self.h = torch.empty(R, I, **bf)
+        self.dh = None if fuse_gate else torch.empty(R, I, **bf)
         self.logits, self.dlogits = (torch.empty(N, E, **f32) for _ in range(2))
         self.dx_router, self.dx_experts = (torch.empty(N, H, **bf) for _ in range(2))
         self.ids = torch.empty(N, k, dtype=torch.int32, device=device)
@@ -85,6 +95,7 @@ class MoETrainBlock:
         self.rstd_pre, self.rstd_post = (torch.empty(N, **f32) for _ in range(2))
         # the residual stream as the block has taken it in, as it has left it, its gradient
         self.stream, self.out, self.d_stream = (torch.empty(N, H, **f32) for _ in range(3))
+        self.momenta = None  # of muon()
         self.refresh()
 
     def refresh(self):
@@ -106,8 +117,12 @@ class MoETrainBlock:
         moe.moe_route(self.logits, s, self.ids, self.topk_w)
         moe.moe_dispatch_layout(self.ids, None, s, lay, ws)
         moe.moe_dispatch(self.x, lay, s, self.rows)
-        moe.moe_grouped_gemm(self.rows, lay, s, self.w["w_gate_up"], self.gu, ws)
-        moe.moe_swiglu(self.gu, self.topk_w, lay, s, self.h)
+        if self.fuse_gate:
+            moe.moe_gated_gemm(self.rows, lay, s, self.w["w_gate_up"], self.topk_w, self.gu, self.h,
+                               ws)
+        else:
+            moe.moe_grouped_gemm(self.rows, lay, s, self.w["w_gate_up"], self.gu, ws)
+            moe.moe_swiglu(self.gu, self.topk_w, lay, s, self.h)
         moe.moe_grouped_gemm(self.h, lay, s, self.w["w_down"], self.y_rows, ws)
         moe.moe_combine(self.y_rows, self.ones, lay, s, None, None, self.y)
         moe.moe_block_norm(self.y, self.stream, p["w_post"], p["gate"], None, self.post, self.out,
@@ -125,8 +140,12 @@ class MoETrainBlock:
         # the combine's gradient: each row of an expert gets its token's
         moe.moe_dispatch(self.dy, lay, s, self.d_rows)
         moe.moe_grouped_gemm_weight_grad(self.d_rows, self.h, lay, s, g["w_down"], ws, **acc)
-        moe.moe_grouped_gemm_input_grad(self.d_rows, lay, s, self.w["w_down"], self.dh, ws)
-        moe.moe_swiglu_grad(self.dh, self.gu, self.topk_w, lay, s, self.dgu, self.dtopk_w)
+        if self.fuse_gate:
+            moe.moe_gated_gemm_grad(self.d_rows, lay, s, self.w["w_down"], self.topk_w, self.gu,
+                                    self.dgu, self.dtopk_w, ws)
+        else:
+            moe.moe_grouped_gemm_input_grad(self.d_rows, lay, s, self.w["w_down"], self.dh, ws)
+            moe.moe_swiglu_grad(self.dh, self.gu, self.topk_w, lay, s, self.dgu, self.dtopk_w)
         moe.moe_grouped_gemm_weight_grad(self.dgu, self.rows, lay, s, g["w_gate_up"], ws, **acc)
         moe.moe_grouped_gemm_input_grad(self.dgu, lay, s, self.w["w_gate_up"], self.d_rows, ws)
         # the dispatch's gradient: a token gets the sum of its rows'
@@ -155,19 +174,48 @@ class MoETrainBlock:
         self.refresh()
 
 
-def main(steps=60, N=512, H=256, E=8, k=2, I=512):
-    """Fits the block to a fixed random target and prints the loss."""
+    def muon(self, lr, momentum=0.95, nesterov=True, weight_decay=0.0, sgd_lr=None):
+        """A step of the Muon optimiser on the experts' matrices (gate and up ones apart), a
+        plain gradient step of sgd_lr (None: lr) on the router and the norms.  An
+        orthogonalised [M, N] matrix has entries of about max(M, N) ** -0.5; times 0.2 of the
+        root they are the size of an Adam step, so that lr and weight_decay mean the same."""
+        s, p, g = self.shape, self.params, self.grads
+        matrices = dict(w_gate_up=(2 * s.E, s.I, s.H), w_down=(s.E, s.H, s.I))
+        if self.momenta is None:
+            self.momenta = {n: torch.zeros_like(p[n]) for n in matrices}
+            self.updates = {n: torch.empty_like(self.w[n]) for n in matrices}
+            need = max(moe.moe_muon_workspace_bytes(moe.MuonShape(*m)) for m in matrices.values())
+            self.muon_ws = torch.empty(need, dtype=torch.uint8, device=p["w_down"].device)
+            self.muon_ws[:256].zero_()
+        for n, (E, M, N) in matrices.items():
+            shape = moe.MuonShape(E, M, N, momentum=momentum, nesterov=nesterov)
+            moe.moe_muon_update(g[n].view(E, M, N), self.momenta[n].view(E, M, N), shape,
+                                self.updates[n].view(E, M, N), self.muon_ws)
+            p[n].mul_(1.0 - lr * weight_decay).add_(self.updates[n],
+                                                    alpha=-lr * 0.2 * max(M, N) ** 0.5)
+        for n in p:
+            if n not in matrices:
+                p[n].sub_(g[n], alpha=lr if sgd_lr is None else sgd_lr)
+        self.refresh()
+
+
+def main(steps=60, N=512, H=256, E=8, k=2, I=512, optimizer="sgd"):
+    """Fits the block to a fixed random target and prints the loss.  optimizer "muon": with
+    the fused gate and the experts' matrices by Muon."""
     gen = torch.Generator(device="cuda")
     gen.manual_seed(1)
     x = torch.randn(N, H, generator=gen, device="cuda")
     target = torch.randn(N, H, generator=gen, device="cuda")
-    block = MoETrainBlock(N, H, E, k, I)
+    block = MoETrainBlock(N, H, E, k, I, fuse_gate=optimizer == "muon")
     losses = []
     for step in range(steps):
         err = block.forward(x) - target
         losses.append(err.square().mean().item())
         block.backward(err * (2.0 / N))
-        block.sgd(0.05)
+        if optimizer == "muon":
+            block.muon(0.02, sgd_lr=0.05)
+        else:
+            block.sgd(0.05)
         if step % 10 == 0 or step == steps - 1:
             print(f"step {step:3d}  loss {losses[-1]:.4f}", flush=True)
     assert moe.moe_get_error(block.ws) == 0 and moe.moe_get_error(block.dense_ws) == 0
@@ -175,4 +223,4 @@ def main(steps=60, N=512, H=256, E=8, k=2, I=512):
 
 
 if __name__ == "__main__":
-    main()
+    main(optimizer="muon" if "--muon" in sys.argv[1:] else "sgd")
