@@ -648,18 +648,19 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
 #pragma unroll
             for (int n = 0; n < kN; ++n)
                 if (n < p.rows) __stcg(to + n * kConsumers, sums[n]);
-            __threadfence();
             consumers_sync();
             if (threadIdx.x == 0) {
-                arrived = atomicAdd(a.counters + owner, 1);
-                if (arrived == after - owner) a.counters[owner] = 0;  // for the next call
+                // one thread's fences stand for all: the barriers order the others' accesses
+                // before and after them
                 __threadfence();
+                const int before_me = atomicAdd(a.counters + owner, 1);
+                if (before_me == after - owner) a.counters[owner] = 0;  // for the next call
+                __threadfence();
+                arrived = before_me;
             }
             consumers_sync();
-            const bool finish = arrived == after - owner;
-            consumers_sync();  // read before the next tile's
-            if (finish && has) {
-                __threadfence();
+            // (written again behind the next such tile's first barrier, after all have read it)
+            if (arrived == after - owner && has) {
 #pragma unroll
                 for (int n = 0; n < kN; ++n) sums[n] = 0.0f;
                 for (int b = owner; b <= after; ++b) {
