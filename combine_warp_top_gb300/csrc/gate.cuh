@@ -13,7 +13,8 @@ struct Gate {
     const int32_t* pair_row;   // [N*k]
     int N, k;
     uint16_t* h;    // forward: [N*k, I]
-    uint16_t* gu;   // forward: [N*k, 2*I] (NULL: not wanted); gradient: its gradient
+    uint16_t* gu;   // forward: [N*k, 2*I] (NULL: not wanted); gradient: dgu
+    const uint16_t* gu_in;  // gradient: gu
     float* parts;   // gradient: [ceil(I / 128), N*k] sums of dh SiLU(g) u (NULL: not wanted)
 };
 

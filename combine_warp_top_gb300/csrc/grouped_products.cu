@@ -97,8 +97,12 @@ constexpr int BOX_BYTES = OP_BYTES / 2;  // an MN-major box: 64 columns x 64 row
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
 constexpr int kEpilogueCols = BT / 2;  // columns of one epilogue warp
-// Registers a thread: 384 x 168 at launch = 128 x 88 + 256 x 208.
-constexpr int kRegsOther = 88, kRegsEpilogue = 208;
+// Registers a thread: 384 x 168 at launch = 128 x 88 + 256 x 208, or 128 x 56 + 256 x 224
+// where an epilogue thread keeps 128 sums beside what it does with them.
+template <int kMode>
+constexpr int kRegsOther = kMode == kGatedGrad ? 56 : 88;
+template <int kMode>
+constexpr int kRegsEpilogue = kMode == kGatedGrad ? 224 : 208;
 // A tile of few rows: their number, which is the MMA's N (see kFew).
 constexpr int BF = 64;
 constexpr int FEW_BYTES = BF / 2 * BK * 2;  // that operand of one stage in one CTA
@@ -164,6 +168,7 @@ template <int kMode, bool kFew>
 struct Ctl : Barriers<kStagesOf<kMode, kFew>> {};
 constexpr int kGateCols = 32;             // kGatedGrad: columns of a half line of 64 bytes
 constexpr int kHalfLines = 32 * kGateCols * 2;  // bytes of 32 rows' half lines
+constexpr int kGradChain = kChainBlocks<float>; // its k-blocks of an accumulator
 constexpr int kMaxSorted = 512;  // what is left of shared memory holds
 template <>
 struct Ctl<kWeightsGrad, false> : Barriers<kStagesOf<kWeightsGrad, false>> {
@@ -171,9 +176,10 @@ struct Ctl<kWeightsGrad, false> : Barriers<kStagesOf<kWeightsGrad, false>> {
 };
 template <>
 struct Ctl<kGatedGrad, false> : Barriers<kStagesOf<kGatedGrad, false>> {
-    uint64_t lines[kEpilogueWarps];  // each CTA: a warp's lines have come in
+    uint64_t lines[kEpilogueWarps];  // each CTA: a warp's half lines have come in
+    uint64_t w_full[2], w_empty[2];  // each CTA: its rows' weights are there, have been read
+    float weights[2][BH];            // of two tiles in turn
 };
-
 template <int kMode, bool kFew>
 constexpr size_t smem_bytes() {
     constexpr size_t n = 1024 + (size_t)kStagesOf<kMode, kFew> * kStageBytes<kFew> +
@@ -605,12 +611,38 @@ __device__ __forceinline__ void gated_few_out(const Gate& gate, uint8_t* staging
     named_sync(out);
 }
 
-// kGatedGrad: dh's 32 rows of 32 columns in v, their g and u in the half lines; dg and du take
-// their place.  16-byte chunk k of row r is at k ^ (r / 2 % 4): TMA's 64-byte swizzle.  Returns
-// this lane's row's sum of dh SiLU(g) u.
-__device__ __forceinline__ float gated_grad_lines(uint8_t* lines, const uint32_t (&v)[32], float w) {
+// Two fp32 numbers in one instruction.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 f2_get(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// kGatedGrad: dh's 32 columns of a lane's row in v, their g and u in the half lines; dg and du
+// take their place.  16-byte chunk k of row r is at k ^ (r / 2 % 4): TMA's 64-byte swizzle.
+// Returns this lane's row's sums of dh SiLU(g) u, of the even and the odd columns.
+__device__ __forceinline__ F2 gated_grad_lines(uint8_t* lines, const uint32_t (&v)[32], float w) {
     const int lane = threadIdx.x & 31;
-    float sum = 0.0f;
+    const F2 ww = f2(w, w), one = f2(1.0f, 1.0f), minus = f2(-1.0f, -1.0f);
+    F2 sum = f2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         uint4* g_at = reinterpret_cast<uint4*>(lines + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4));
@@ -620,19 +652,18 @@ __device__ __forceinline__ float gated_grad_lines(uint8_t* lines, const uint32_t
         uint32_t dg[4], du[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float a[2], b[2];
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                const float x = __uint_as_float(v[k * 8 + 2 * j + o]);
-                const float gg = __uint_as_float(o ? g[j] & 0xffff0000u : g[j] << 16);
-                const float uu = __uint_as_float(o ? u[j] & 0xffff0000u : u[j] << 16);
-                const float s = sigmoid(gg), act = gg * s, y = w * x;
-                sum += x * act * uu;
-                a[o] = y * uu * (s * (1.0f + gg * (1.0f - s)));
-                b[o] = y * act;
-            }
-            dg[j] = pack2(a[0], a[1]);
-            du[j] = pack2(b[0], b[1]);
+            const float g0 = __uint_as_float(g[j] << 16), g1 = __uint_as_float(g[j] & 0xffff0000u);
+            const F2 gg = f2(g0, g1);
+            const F2 uu = f2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
+            const F2 x = f2(__uint_as_float(v[k * 8 + 2 * j]), __uint_as_float(v[k * 8 + 2 * j + 1]));
+            const F2 s = f2(sigmoid(g0), sigmoid(g1));
+            const F2 act = f2_mul(gg, s), y = f2_mul(ww, x);
+            sum = f2_fma(f2_mul(x, act), uu, sum);
+            // s (1 + g (1 - s)) = s + act (1 - s)
+            const F2 slope = f2_fma(act, f2_fma(s, minus, one), s);
+            const float2 a = f2_get(f2_mul(f2_mul(y, uu), slope)), b = f2_get(f2_mul(y, act));
+            dg[j] = pack2(a.x, a.y);
+            du[j] = pack2(b.x, b.y);
         }
         *g_at = make_uint4(dg[0], dg[1], dg[2], dg[3]);
         *u_at = make_uint4(du[0], du[1], du[2], du[3]);
@@ -667,22 +698,26 @@ __device__ __forceinline__ GradPart grad_part(const Tile& t, uint32_t rank, int 
     p.have = p.rows <= 0 || left <= 0 ? 0 : (left + kGateCols - 1) / kGateCols;
     return p;
 }
-// Its epilogue warps' loop.  A half line's inputs are asked for one half line ahead, the next
-// tile's first ones during this tile's last, with the rows' weights of that tile (three loads
-// one after the other), so that only the call's first tile waits for them.
-template <typename Take, typename Ready, typename Release>
+// Its epilogue warps' loop.  A half line's inputs are asked for one half line ahead, a tile's
+// first ones before its products are there; its rows' weights a warp of their own has looked up
+// (three loads one after the other, 3600 cycles).  What this does for a tile has to fit the two
+// chains that the MMAs are ahead, 8500 cycles: half of them the exponentials and reciprocals.
+template <typename Take, typename Ready, typename Release, typename Weight>
 __device__ __forceinline__ void gated_grad_tiles(const CUtensorMap& tmGu, const CUtensorMap& tmOut,
                                                  const Gate& gate, uint8_t* staging, uint32_t bar,
-                                                 uint32_t rank, int R, int n_out,
+                                                 uint32_t rank, int R, int n_out, int kblocks,
                                                  volatile int* abort, int* err, Take take_tile,
-                                                 Ready ready, Release release) {
+                                                 Ready ready, Release release, Weight weight) {
     const int lane = threadIdx.x & 31;
     const uint32_t staging_at = smem_u32(staging);
     uint32_t phase = 0;
     int buf = 0;
-    Tile t = {};
-    if (!take_tile(0, t)) return;
-    GradPart p = grad_part(t, rank, n_out);
+    GradPart p;
+    {
+        Tile t = {};
+        if (!take_tile(0, t)) return;
+        p = grad_part(t, rank, n_out);
+    }
     const auto fetch = [&](const GradPart& q, int c, int b) {
         if (lane != 0) return;
         bulk_wait_read();  // what went out from there has been read
@@ -692,37 +727,40 @@ __device__ __forceinline__ void gated_grad_tiles(const CUtensorMap& tmGu, const 
         tma_load_3d(to + kHalfLines, &tmGu, bar, q.col + c * kGateCols, 1, (int)q.row);
     };
     if (p.have > 0) fetch(p, 0, 0);
-    float w = lane < p.rows ? row_weight(gate, p.row + lane) : 0.0f;
     for (int i = 1;; ++i) {
-        uint32_t at;
-        if (!ready(&at)) return;
-        Tile next = {};
-        GradPart np = {};
-        bool more = false, taken = false;
-        float next_w = 0.0f;
-        const auto look_ahead = [&](int b) {
-            taken = true;
-            more = take_tile(i, next);
-            if (!more) return;
-            np = grad_part(next, rank, n_out);
-            if (np.have > 0) fetch(np, 0, b);
-            if (lane < np.rows) next_w = row_weight(gate, np.row + lane);
-        };
-        if (p.have == 0) release();
-        float sum = 0.0f;
-        int ok = 1;
+        // dh, the chains' partial sums added up in fp32 registers (the sums over a row of dh
+        // times what the gate gives are fp32 outputs), which frees the accumulators
+        uint32_t dh[kEpilogueCols / 32][32];
+#pragma unroll
+        for (int c = 0; c < kEpilogueCols; ++c) dh[c / 32][c % 32] = 0u;
 #pragma unroll 1
-        for (int c = 0; c < p.have; ++c, buf ^= 1) {
-            uint32_t v[32];
-            tmem_ld32(at + c * kGateCols, v);
-            tmem_wait_ld();
-            if (c == p.have - 1) release();
-            if (!wait_bar(bar, phase, abort, err)) ok = 0;
+        for (int k = 0; k < kblocks; k += kGradChain) {
+            uint32_t at;
+            if (!ready(&at)) return;
+#pragma unroll
+            for (int c = 0; c < kEpilogueCols / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld32(at + c * 32, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    dh[c][j] = __float_as_uint(__uint_as_float(dh[c][j]) + __uint_as_float(v[j]));
+            }
+            release();
+        }
+        float w;
+        if (!weight(i - 1, &w)) return;
+        F2 sum = f2(0.0f, 0.0f);
+        const F2 one = f2(1.0f, 1.0f);
+#pragma unroll
+        for (int c = 0; c < kEpilogueCols / kGateCols; ++c) {
+            if (c >= p.have) break;
+            const bool in = wait_bar(bar, phase, abort, err);
             phase ^= 1u;
-            if (!__all_sync(0xffffffffu, ok)) return;
+            if (!__all_sync(0xffffffffu, in)) return;
             if (c + 1 < p.have) fetch(p, c + 1, buf ^ 1);
             uint8_t* lines = staging + buf * 2 * kHalfLines;
-            sum += gated_grad_lines(lines, v, w);
+            sum = f2_fma(gated_grad_lines(lines, dh[c], w), one, sum);
             const int col = p.col + c * kGateCols;
             fence_async_shared();
             __syncwarp();
@@ -741,15 +779,16 @@ __device__ __forceinline__ void gated_grad_tiles(const CUtensorMap& tmGu, const 
                 fence_async_shared();
                 __syncwarp();
             }
-            if (c == p.have - 1) look_ahead(buf ^ 1);
+            buf ^= 1;
         }
-        if (!taken) look_ahead(buf);
         if (gate.parts && lane < p.rows && p.have > 0)
-            gate.parts[(long long)(p.col / kEpilogueCols) * R + p.row + lane] = sum;
-        if (!more) return;
-        t = next;
-        p = np;
-        w = next_w;
+            gate.parts[(long long)(p.col / kEpilogueCols) * R + p.row + lane] =
+                f2_get(sum).x + f2_get(sum).y;
+        // the next tile's first inputs while its products run
+        Tile t = {};
+        if (!take_tile(i, t)) return;
+        p = grad_part(t, rank, n_out);
+        if (p.have > 0) fetch(p, 0, buf);
     }
 }
 
@@ -787,7 +826,7 @@ __device__ __forceinline__ void grouped_product(
                                                     (size_t)kEpilogueWarps * kStagingOf<kMode>);
     volatile int* abort_flag = &ctl->abort;
 
-    constexpr int kChain = kChainBlocks<OutT>;
+    constexpr int kChain = kMode == kGatedGrad ? kGradChain : kChainBlocks<OutT>;
     // the partial sums before the last are added to it in registers; else (kLong) in TMEM:
     // beside a line of 64 bf16 columns 128 sums would not fit the registers
     constexpr bool kSums = sizeof(OutT) == 4 || kFew;
@@ -795,8 +834,8 @@ __device__ __forceinline__ void grouped_product(
     constexpr bool kMnA = kW;                 // the contraction runs along tmA's rows
     constexpr bool kMnB = kMode != kForward && kMode != kGated;  // and along tmB's
     // readers of a slot of the leader's queue: its producer, MMA thread,
-    // epilogue warps (and block-end warp), and the peer's producer
-    constexpr int kLocalReaders = kEpilogueWarps + (kW ? 1 : 0);
+    // epilogue warps (and block-end warp, or the one for rows' weights), and the peer's producer
+    constexpr int kLocalReaders = kEpilogueWarps + (kW || kMode == kGatedGrad ? 1 : 0);
     constexpr int kQueueReaders = kLocalReaders + 3;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -823,8 +862,11 @@ __device__ __forceinline__ void grouped_product(
         if (i < kQueueBarriers) mbar_init(smem_u32(&ctl->tfull[0] + i), count);
         if (i < 3 * kStages) mbar_init(smem_u32(&ctl->full[0] + i), kW && i < kStages ? 2 : 1);
         if (i == 63) ctl->abort = 0;
-        if constexpr (kMode == kGatedGrad)
+        if constexpr (kMode == kGatedGrad) {
             if (i < kEpilogueWarps) mbar_init(smem_u32(&ctl->lines[i]), 1);
+            if (i < 2) mbar_init(smem_u32(&ctl->w_full[i]), 1);
+            if (i < 2) mbar_init(smem_u32(&ctl->w_empty[i]), kEpilogueWarps);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0 && lane == 0) {
@@ -960,7 +1002,7 @@ __device__ __forceinline__ void grouped_product(
     Tile joined = {};  // the tile of a split contraction (epilogue warps)
     joined.e = -1;
     if (warp < 4) {
-        regs_shrink<kRegsOther>();
+        regs_shrink<kRegsOther<kMode>>();
         // One lane each of the producer and the MMA issuer, elected rather than lane 0: the
         // compiler then knows that the lane is alone and keeps the operands of copies and
         // MMAs in uniform registers (tiles of few rows: a k-block in 0.19 us,
@@ -1134,7 +1176,8 @@ __device__ __forceinline__ void grouped_product(
                         phase ^= 1u;
                     }
                     ++in_chain;
-                    if (((kSums || kLong) && in_chain == kChain) || kb == t.kblocks - 1) {
+                    if (((kSums || kLong || kMode == kGatedGrad) && in_chain == kChain) ||
+                        kb == t.kblocks - 1) {
                         umma_commit_pair_multicast(smem_u32(&ctl->tfull[acc]), pair_mask);
                         in_chain = 0;
                         if (++acc == kAccs) {
@@ -1171,6 +1214,28 @@ __device__ __forceinline__ void grouped_product(
                 if (lane == 0) more = publish(ctl, i, t, first, abort_flag, err) && t.e >= 0;
                 if (!__shfl_sync(0xffffffffu, more, 0)) break;
             }
+        } else if (kMode == kGatedGrad && warp == 3) {
+            if constexpr (kMode == kGatedGrad) {
+                // ---------------- rows' weights (both CTAs) ----------------
+                for (int i = 0;; ++i) {
+                    Tile t = {};
+                    if (!warp_next(ctl, i, leader, abort_flag, err, t)) break;
+                    const int b = i & 1, left = t.cnt - t.mb * BT - (int)rank * BH;
+                    const long long row = (long long)t.off + t.mb * BT + (int)rank * BH;
+                    float w[BH / 32];
+#pragma unroll
+                    for (int r = 0; r < BH / 32; ++r)
+                        w[r] = r * 32 + lane < left ? row_weight(gate, row + r * 32 + lane) : 0.0f;
+                    const bool free = wait_bar(smem_u32(&ctl->w_empty[b]),
+                                               ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_flag, err,
+                                               tile_limit(t.kblocks));
+                    if (!__all_sync(0xffffffffu, free)) break;
+#pragma unroll
+                    for (int r = 0; r < BH / 32; ++r) ctl->weights[b][r * 32 + lane] = w[r];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&ctl->w_full[b]));
+                }
+            }
         } else if (kW && warp == 3) {
             // ---------------- block ends (both CTAs) ----------------
             const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), first);
@@ -1206,7 +1271,7 @@ __device__ __forceinline__ void grouped_product(
         }
     } else {
         // ---------------- epilogue (both CTAs): own 128 rows ----------------
-        regs_grow<kRegsEpilogue>();
+        regs_grow<kRegsEpilogue<kMode>>();
         const int q = warp & 3;               // TMEM lane quadrant
         const int half = (warp - 4) >> 2;     // 128 columns of the tile, or 32 of its few rows
         constexpr int kCols = kFew ? BF / 2 : kEpilogueCols;  // of the accumulator
@@ -1237,8 +1302,19 @@ __device__ __forceinline__ void grouped_product(
                     acc_phase ^= 1u;
                 }
             };
+            // this lane's row's weight in tile i
+            const auto weight = [&](int i, float* w) {
+                const int b = i & 1;
+                const bool ok = wait_bar(smem_u32(&ctl->w_full[b]), (uint32_t)(i >> 1) & 1u,
+                                         abort_flag, err);
+                *w = ctl->weights[b][q * 32 + lane];
+                const bool all = __all_sync(0xffffffffu, ok);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->w_empty[b]));
+                return all;
+            };
             gated_grad_tiles(tmGu, tmOut, gate, staging, smem_u32(&ctl->lines[warp - 4]), rank, R,
-                             n_out, abort_flag, err, take_tile, ready, release);
+                             n_out, KB, abort_flag, err, take_tile, ready, release, weight);
         } else
         for (int i = 0;; ++i) {
             Tile t = {};
@@ -1793,13 +1869,13 @@ moe_status launch_gated_forward(const uint16_t* rows, const GemmGroup& g, int c_
 }
 
 moe_status launch_gated_grad(const uint16_t* dout, const GemmGroup& g, int c_out, int I,
-                             const uint16_t* w, const uint16_t* gu_in, const Gate& gate,
-                             float* dtopk_w, cudaStream_t st) {
+                             const uint16_t* w, const Gate& gate, float* dtopk_w,
+                             cudaStream_t st) {
     CUtensorMap a, b, o, gu;
     int groups = 0;
     if (!map_rows(&a, dout, 0, g.R, c_out, BH) ||
         !map_mn(&b, w, g.E, c_out, I, box_columns(I, true), &groups) ||
-        !map_gu(&gu, gu_in, g.R, I, kGateCols) || !map_gu(&o, gate.gu, g.R, I, kGateCols))
+        !map_gu(&gu, gate.gu_in, g.R, I, kGateCols) || !map_gu(&o, gate.gu, g.R, I, kGateCols))
         return MOE_ERR_UNSUPPORTED;
     const long long used = g.R < g.E ? g.R : g.E;
     const long long tiles = (used + (g.R - used) / BT) * blocks_of(I, BT);
@@ -1878,7 +1954,7 @@ moe_status moe_gated_gemm(const uint16_t* rows, const moe_layout* layout, const 
     if (!rows || !w_gate_up || !h) return MOE_ERR_INVALID_ARG;
     if (!aligned16(rows, w_gate_up, gu, h)) return MOE_ERR_INVALID_ARG;
     const Gate gate = {topk_w, layout->row_token, layout->pair_row, shape->N, shape->k,
-                       h,      gu,                nullptr};
+                       h,      gu,                nullptr,          nullptr};
     return launch_gated_forward(rows, routed_group(*layout, *shape, ws), C_in, shape->I, w_gate_up,
                                 gate, as_stream(stream));
 }
@@ -1896,9 +1972,9 @@ moe_status moe_gated_gemm_grad(const uint16_t* dout, const moe_layout* layout,
     if (!aligned16(dout, w_down, gu, dgu)) return MOE_ERR_INVALID_ARG;
     float* parts = dtopk_w ? ws_ptr<float>(ws, gated_parts_offset(*shape)) : nullptr;
     const Gate gate = {topk_w,  layout->row_token, layout->pair_row, shape->N, shape->k,
-                       nullptr, dgu,               parts};
-    return launch_gated_grad(dout, routed_group(*layout, *shape, ws), C_out, shape->I, w_down, gu,
-                             gate, dtopk_w, as_stream(stream));
+                       nullptr, dgu,               gu,               parts};
+    return launch_gated_grad(dout, routed_group(*layout, *shape, ws), C_out, shape->I, w_down, gate,
+                             dtopk_w, as_stream(stream));
 }
 
 moe_status moe_grouped_gemm_weight_grad(const uint16_t* dout, const uint16_t* rows,

@@ -33,14 +33,22 @@ constexpr int kTmemCols = BT * kAccs;
 constexpr int OP_BYTES = BH * BK * 2;
 constexpr int BOX_BYTES = OP_BYTES / 2;
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
-constexpr int kLine = 64;                 // columns of a line of 128 bytes
-constexpr int kLinesBytes = 32 * 128;     // 32 of them
-// Epilogue warps (kWarps): 4, with all 256 columns of 32 rows each and two buffers for the lines
-// of two inputs or outputs, or 8 with 128 columns and one buffer.  With two the next line's
-// inputs come in while a line is worked on: 64 matrices of 2048 x 1408, 4369 us with 8, 4195
-// with 4.  A tile that nothing runs beside is done sooner by 8: 8 of 1024 x 1024, 421 and 384 us.
+// Epilogue warps, kWarps: 4 with all 256 columns of 32 rows of a CTA's half tile each, or 8 with
+// 128.  Their rows come in and go out in lines of a quarter of those columns (64 or 32: 128 or
+// 64 bytes) through two buffers: the next ones' inputs are on their way while these are worked on.
+// Whole lines of 128 bytes are fewer rows for the copy engine, which is as busy with a tile's
+// operands as the MMAs are (16 of 2048 x 7168: 5950 us with 4 warps, 6100 with 8); a tile that no
+// other runs beside is done sooner by 8 (8 of 1024 x 1024: 437 and 359 us).  With one buffer 64 of
+// 2048 x 1408 took 4369 us, 4195 with two.
 constexpr int kMaxWarps = 8;
-constexpr int kStagingBytes = 4 * 4 * kLinesBytes;  // of all of them
+template <int kWarps>
+constexpr int kLine = 256 / kWarps;
+template <int kWarps>
+constexpr int kLinesBytes = 32 * kLine<kWarps> * 2;
+template <int kWarps>
+constexpr int kBufferBytes = 2 * kLinesBytes<kWarps>;  // lines of two inputs or outputs
+constexpr int kStagingBytes = kMaxWarps * 2 * kBufferBytes<kMaxWarps>;  // of all warps
+static_assert(kStagingBytes == 4 * 2 * kBufferBytes<4>, "the same for 4 warps");
 constexpr int kMaxDim = 65536;
 // G and S are kept times 2^12, X times 2^p with 2^p about the root of its longer side, so
 // that entries far below the largest are normal fp16 numbers.
@@ -119,21 +127,33 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t v) {
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-// A warp's 32 x 64 part of an output, of the same tiles of the inputs that lie in its lines,
-// and out by TMA.  v: the lane's row of the accumulator.
+// 32 or 64 columns of an accumulator.
+__device__ __forceinline__ void tmem_ld_columns(uint32_t at, uint32_t (&v)[32]) {
+    tmem_ld32(at, v);
+}
+__device__ __forceinline__ void tmem_ld_columns(uint32_t at, uint32_t (&v)[64]) {
+    tmem_ld32(at, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+    tmem_ld32(at + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+}
+
+// A line of a warp's 32 rows of an output, of the same columns of the inputs that lie in the
+// buffer, and out by TMA.  v: the lane's row of the accumulator.  16-byte chunk k of row r is at
+// k ^ (r % 8) of its 128 bytes or k ^ (r / 2 % 4) of its 64: TMA's swizzles; a mirror image has
+// none.
 //   kGram    G = acc * 2^(12 - 2p), and its mirror image
 //   kSquare  S = p1 G + p2 acc * 2^-12, likewise
 //   kStep    x = p0 (hi + lo) + acc * 2^-12, into hi and lo
 //   kLast    the same times 2^-p, bf16
-template <Form kForm>
-__device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLine], float alpha,
-                                        float beta) {
-    const int lane = threadIdx.x & 31;
-    uint8_t* second = lines + kLinesBytes;
+template <Form kForm, int kWarps>
+__device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLine<kWarps>],
+                                        float alpha, float beta) {
+    constexpr int kL = kLine<kWarps>;
+    const int lane = threadIdx.x & 31, flip = kL == 64 ? lane & 7 : lane >> 1 & 3;
+    uint8_t* second = lines + kLinesBytes<kWarps>;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        uint4* at = reinterpret_cast<uint4*>(lines + lane * 128 + ((k ^ (lane & 7)) << 4));
-        uint4* lo_at = reinterpret_cast<uint4*>(second + lane * 128 + ((k ^ (lane & 7)) << 4));
+    for (int k = 0; k < kL / 8; ++k) {
+        uint4* at = reinterpret_cast<uint4*>(lines + lane * (kL * 2) + ((k ^ flip) << 4));
+        uint4* lo_at = at + kLinesBytes<kWarps> / 16;
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = alpha * __uint_as_float(v[k * 8 + j]);
@@ -173,7 +193,7 @@ __device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLin
             *lo_at = make_uint4(r[0], r[1], r[2], r[3]);
         }
         if (kForm == kGram || kForm == kSquare) {
-            // column c of the part is row c of its mirror image: 64 rows of 32
+            // column c of the part is row c of its mirror image
             uint16_t* mirror = reinterpret_cast<uint16_t*>(second);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -194,8 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
                         const __grid_constant__ CUtensorMap tmOut2, Dims d, float alpha,
                         float beta, int* err) {
     constexpr bool kSym = kForm == kGram || kForm == kSquare;
-    constexpr bool kTwo = kWarps == 4;             // two buffers
-    constexpr int kColumns = BT * 4 / kWarps;      // of an epilogue warp
+    constexpr int kL = kLine<kWarps>, kColumns = 4 * kL;  // of a line, of an epilogue warp
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t* tiles = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -337,18 +356,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
         for (long long i = blockIdx.x / 2; i < total; i += pairs) {
             const Tile t = decode<kSym>(i, per_matrix, MB, NB);
             const int row = t.mb * BT + (int)rank * BH + q * 32, col = t.nb * BT + part * kColumns;
-            // lines of 64 columns that there are
+            // lines that there are
             const int left = d.n - col < kColumns ? d.n - col : kColumns;
-            const int have = row >= d.m || left <= 0 ? 0 : (left + kLine - 1) / kLine;
+            const int have = row >= d.m || left <= 0 ? 0 : (left + kL - 1) / kL;
             // the inputs' lines c into buffer b, once what went out from there has been read
             const auto fetch = [&](int c, int b) {
                 if (kForm == kGram || lane != 0) return;
                 bulk_wait_read();
-                const uint32_t to = lines_addr + (uint32_t)(b * 2 * kLinesBytes);
-                mbar_expect_tx(bar, kForm == kSquare ? kLinesBytes : 2 * kLinesBytes);
-                tma_load_3d(to, &tmIn, bar, col + c * kLine, row, t.e);
+                const uint32_t to = lines_addr + (uint32_t)(b * kBufferBytes<kWarps>);
+                mbar_expect_tx(bar, kForm == kSquare ? kLinesBytes<kWarps> : 2 * kLinesBytes<kWarps>);
+                tma_load_3d(to, &tmIn, bar, col + c * kL, row, t.e);
                 if (kForm != kSquare)
-                    tma_load_3d(to + kLinesBytes, &tmIn2, bar, col + c * kLine, row, t.e);
+                    tma_load_3d(to + kLinesBytes<kWarps>, &tmIn2, bar, col + c * kL, row, t.e);
             };
             if (have > 0) fetch(0, buf);
             int ok = 0;
@@ -366,37 +385,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
             if (have == 0) release();
 #pragma unroll 1
             for (int c = 0; c < have; ++c) {
-                uint32_t v[kLine];
-                tmem_ld32(at + c * kLine, reinterpret_cast<uint32_t(&)[32]>(v[0]));
-                tmem_ld32(at + c * kLine + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+                uint32_t v[kL];
+                tmem_ld_columns(at + c * kL, v);
                 tmem_wait_ld();
                 if (c == have - 1) release();
                 if (kForm == kGram) {
-                    if (lane == 0) {  // the buffer's last lines have been read
-                        if (kTwo) bulk_wait_read_but_one();
-                        else bulk_wait_read();
-                    }
+                    if (lane == 0) bulk_wait_read_but_one();  // the buffer's last lines
                 } else {
                     if (!wait_bar(bar, lines_phase, abort_flag, err)) ok = 0;
                     lines_phase ^= 1u;
                 }
                 if (!__all_sync(0xffffffffu, ok)) break;
-                if (kTwo && c + 1 < have) fetch(c + 1, buf ^ 1);
-                uint8_t* mine = lines + buf * 2 * kLinesBytes;
-                combine<kForm>(mine, v, alpha, beta);
+                if (c + 1 < have) fetch(c + 1, buf ^ 1);
+                uint8_t* mine = lines + buf * kBufferBytes<kWarps>;
+                combine<kForm, kWarps>(mine, v, alpha, beta);
                 fence_async_shared();
                 __syncwarp();
                 if (lane == 0) {
                     const uint32_t from = smem_u32(mine);
-                    tma_store_3d(&tmOut, from, col + c * kLine, row, t.e);
+                    tma_store_3d(&tmOut, from, col + c * kL, row, t.e);
                     if (kForm == kStep)
-                        tma_store_3d(&tmOut2, from + kLinesBytes, col + c * kLine, row, t.e);
+                        tma_store_3d(&tmOut2, from + kLinesBytes<kWarps>, col + c * kL, row, t.e);
                     if (kSym && t.mb != t.nb)
-                        tma_store_3d(&tmOut2, from + kLinesBytes, row, col + c * kLine, t.e);
+                        tma_store_3d(&tmOut2, from + kLinesBytes<kWarps>, row, col + c * kL, t.e);
                     bulk_commit();
                 }
-                if (!kTwo && c + 1 < have) fetch(c + 1, buf);
-                if (kTwo) buf ^= 1;
+                buf ^= 1;
             }
             if (!__all_sync(0xffffffffu, ok)) break;
             if (++acc == kAccs) {
@@ -589,16 +603,21 @@ Work work_of(const moe_muon_shape& s) {
 }
 
 bool map_matrices(CUtensorMap* m, const void* ptr, int E, int rows, int cols, uint32_t box_cols,
-                  uint32_t box_rows, MapType type) {
+                  uint32_t box_rows, MapType type, int swizzle) {
     const uint64_t sizes[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)E};
     const uint64_t strides[2] = {(uint64_t)cols * 2, (uint64_t)cols * rows * 2};
     const uint32_t box[3] = {box_cols, box_rows, 1};
-    return map_typed(m, 3, ptr, sizes, strides, box, type, box_cols * 2 == 128 ? 128 : 0);
+    return map_typed(m, 3, ptr, sizes, strides, box, type, swizzle);
 }
 
+// The outputs' (and their inputs') maps, in lines of 64 columns and of 32: of 32 rows, and mirror
+// images of 32 columns.
+struct LineMaps {
+    CUtensorMap g, g_mirror, s, s_mirror, hi[2], lo, out;
+};
+
 template <Form kForm, bool kMnA, bool kMnB, int kWarps>
-moe_status launch_form(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in,
-                       const CUtensorMap& in2, const CUtensorMap& out, const CUtensorMap& out2,
+moe_status launch_form(const CUtensorMap& a, const CUtensorMap& b, const LineMaps& l, int now,
                        const Dims& d, float alpha, float beta, int* err, long long pairs,
                        cudaStream_t st) {
     const auto kernel = muon_product_kernel<kForm, kMnA, kMnB, kWarps>;
@@ -611,23 +630,32 @@ moe_status launch_form(const CUtensorMap& a, const CUtensorMap& b, const CUtenso
             return MOE_ERR_CUDA;
         set.finish(dev);
     }
+    const CUtensorMap& in = kForm <= kSquare ? l.g : l.hi[now];
+    const CUtensorMap& in2 = kForm <= kSquare ? l.g : l.lo;
+    const CUtensorMap& out = kForm == kGram     ? l.g
+                             : kForm == kSquare ? l.s
+                             : kForm == kStep   ? l.hi[1 - now]
+                                                : l.out;
+    const CUtensorMap& out2 = kForm == kGram     ? l.g_mirror
+                              : kForm == kSquare ? l.s_mirror
+                              : kForm == kStep   ? l.lo
+                                                 : l.out;
     return cuda_status(launch_chained(kernel, (int)(2 * pairs), 128 + 32 * kWarps, kSmem, st, a, b,
                                       in, in2, out, out2, d, alpha, beta, err));
 }
 template <Form kForm, bool kMnA, bool kMnB>
-moe_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in,
-                          const CUtensorMap& in2, const CUtensorMap& out, const CUtensorMap& out2,
-                          const Dims& d, float alpha, float beta, int* err, cudaStream_t st) {
+moe_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const LineMaps (&l)[2],
+                          int now, const Dims& d, float alpha, float beta, int* err,
+                          cudaStream_t st) {
     const long long MB = blocks_of(d.m, BT), NB = blocks_of(d.n, BT);
     const long long tiles =
         d.E * (kForm == kGram || kForm == kSquare ? NB * (NB + 1) / 2 : MB * NB);
     const long long most = sm_count() / 2;
-    // 8 warps where a pair has no more than two tiles
-    return tiles > 2 * most
-               ? launch_form<kForm, kMnA, kMnB, 4>(a, b, in, in2, out, out2, d, alpha, beta, err,
-                                                   most, st)
-               : launch_form<kForm, kMnA, kMnB, 8>(a, b, in, in2, out, out2, d, alpha, beta, err,
-                                                   tiles < most ? tiles : most, st);
+    // 8 warps where a pair has no more than four tiles
+    return tiles > 4 * most ? launch_form<kForm, kMnA, kMnB, 4>(a, b, l[0], now, d, alpha, beta,
+                                                                err, most, st)
+                            : launch_form<kForm, kMnA, kMnB, 8>(a, b, l[1], now, d, alpha, beta,
+                                                                err, tiles < most ? tiles : most, st);
 }
 
 template <typename G>
@@ -696,42 +724,46 @@ moe_status moe_muon_update(const void* grad, const float* momentum, const moe_mu
                                  parts, hi[0], lo, st)
                 : launch_prepare(static_cast<const __nv_bfloat16*>(grad), momentum, new_momentum,
                                  s, p, parts, hi[0], lo, st));
-    // operands: rows with their contraction along them (k) or columns (mn); lines and their
-    // mirror image
-    CUtensorMap x_k[2], x_mn[2], hi_lines[2], lo_lines, g_k, s_k, g_lines, g_mirror, s_lines,
-        s_mirror, out;
-    const auto map = [&](CUtensorMap* t, const void* ptr, int rows, int cols, uint32_t bc,
-                         uint32_t br) {
-        return map_matrices(t, ptr, s.E, rows, cols, bc, br, kMapF16);
+    // operands: rows with their contraction along them (k) or columns (mn)
+    CUtensorMap x_k[2], x_mn[2], g_k, s_k;
+    LineMaps l[2];
+    const auto operand = [&](CUtensorMap* t, const void* ptr, int rows, int cols, uint32_t box_rows) {
+        return map_matrices(t, ptr, s.E, rows, cols, BK, box_rows, kMapF16, 128);
     };
-    bool ok = map(&g_k, gram, m, m, 64, BH) && map(&s_k, square, m, m, 64, BH) &&
-              map(&g_lines, gram, m, m, 64, 32) && map(&g_mirror, gram, m, m, 32, 64) &&
-              map(&s_lines, square, m, m, 64, 32) && map(&s_mirror, square, m, m, 32, 64) &&
-              map(&lo_lines, lo, s.M, s.N, 64, 32) &&
-              map_matrices(&out, update, s.E, s.M, s.N, 64, 32, kMapBF16);
+    bool ok = operand(&g_k, gram, m, m, BH) && operand(&s_k, square, m, m, BH);
     for (int i = 0; i < 2; ++i)
-        ok = ok && map(&x_k[i], hi[i], s.M, s.N, 64, BH) && map(&x_mn[i], hi[i], s.M, s.N, 64, BK) &&
-             map(&hi_lines[i], hi[i], s.M, s.N, 64, 32);
+        ok = ok && operand(&x_k[i], hi[i], s.M, s.N, BH) && operand(&x_mn[i], hi[i], s.M, s.N, BK);
+    for (int w = 0; w < 2; ++w) {
+        const uint32_t cols = w == 0 ? kLine<4> : kLine<8>;
+        const auto lines = [&](CUtensorMap* t, const void* ptr, int M, int N, MapType type) {
+            return map_matrices(t, ptr, s.E, M, N, cols, 32, type, (int)cols * 2);
+        };
+        const auto mirror = [&](CUtensorMap* t, const void* ptr) {
+            return map_matrices(t, ptr, s.E, m, m, 32, cols, kMapF16, 0);
+        };
+        ok = ok && lines(&l[w].g, gram, m, m, kMapF16) && lines(&l[w].s, square, m, m, kMapF16) &&
+             mirror(&l[w].g_mirror, gram) && mirror(&l[w].s_mirror, square) &&
+             lines(&l[w].hi[0], hi[0], s.M, s.N, kMapF16) &&
+             lines(&l[w].hi[1], hi[1], s.M, s.N, kMapF16) &&
+             lines(&l[w].lo, lo, s.M, s.N, kMapF16) &&
+             lines(&l[w].out, update, s.M, s.N, kMapBF16);
+    }
     if (!ok) return MOE_ERR_UNSUPPORTED;
     const float scale = ldexpf(1.0f, -2 * p) * kSquareScale, back = 1.0f / kSquareScale;
     const Dims gd = {s.E, longer, m, m}, sd = {s.E, m, m, m}, xd = {s.E, m, s.M, s.N};
     for (int i = 0; i < s.steps; ++i) {
         const int now = i % 2;
-        MOE_TRY(tall ? launch_product<kGram, true, true>(x_mn[now], x_mn[now], g_lines, g_lines,
-                                                         g_lines, g_mirror, gd, scale, 0.0f, err,
-                                                         st)
-                     : launch_product<kGram, false, false>(x_k[now], x_k[now], g_lines, g_lines,
-                                                           g_lines, g_mirror, gd, scale, 0.0f, err,
-                                                           st));
-        MOE_TRY(launch_product<kSquare, false, false>(g_k, g_k, g_lines, g_lines, s_lines,
-                                                      s_mirror, sd, kP2 * back, kP1, err, st));
+        MOE_TRY(tall ? launch_product<kGram, true, true>(x_mn[now], x_mn[now], l, now, gd, scale,
+                                                         0.0f, err, st)
+                     : launch_product<kGram, false, false>(x_k[now], x_k[now], l, now, gd, scale,
+                                                           0.0f, err, st));
+        MOE_TRY(launch_product<kSquare, false, false>(g_k, g_k, l, now, sd, kP2 * back, kP1, err,
+                                                      st));
         const bool last = i == s.steps - 1;
         const float unscale = last ? ldexpf(1.0f, -p) : 1.0f;
         const CUtensorMap &a = tall ? x_k[now] : s_k, &b = tall ? s_k : x_mn[now];
-        const CUtensorMap &to = last ? out : hi_lines[1 - now], &to2 = last ? out : lo_lines;
         const auto step = [&](auto launch) {
-            return launch(a, b, hi_lines[now], lo_lines, to, to2, xd, back * unscale, kP0 * unscale,
-                          err, st);
+            return launch(a, b, l, now, xd, back * unscale, kP0 * unscale, err, st);
         };
         if (last)
             MOE_TRY(tall ? step(launch_product<kLast, false, false>)

@@ -142,23 +142,6 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint64_t b_
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-
-// (w & mask) | bits: one instruction, which takes two constants from registers only.
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
-    uint32_t v;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(mask), "r"(bits));
-    return v;
-}
 __device__ __forceinline__ void tmem_st_a(uint32_t at, const uint32_t (&x)[32]) { tmem_st32(at, x); }
 __device__ __forceinline__ void tmem_st_a(uint32_t at, const uint32_t (&r)[16]) {
     asm volatile(
@@ -859,7 +842,7 @@ moe_status w4_product(const uint16_t* rows, const moe_layout* layout, const moe_
     a.m = matrix_of(*matrix);
     a.expert_bytes = (long long)a.m.slabs * a.m.chunks * a.m.record;
     a.gate = Gate{topk_w,  layout->row_token, layout->pair_row, shape->N, shape->k,
-                  gated ? static_cast<uint16_t*>(out) : nullptr, nullptr, nullptr};
+                  gated ? static_cast<uint16_t*>(out) : nullptr, nullptr, nullptr, nullptr};
     a.out = out;
     a.out_f32 = out_f32;
     a.offsets = g.offsets;
