@@ -118,7 +118,7 @@ struct Args {
     const int32_t* counts;
     int E, R;
     float* parts;    // partial sums: two slots a block
-    int* counters;   // arrivals at a tile, one of each block's
+    int* counters;   // arrivals at a slab of a tile, one of each block's warps
     int* err;
 };
 
@@ -163,18 +163,25 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t* a) {
     }
 }
 
+// The unit at which block b's share starts.
+__device__ __forceinline__ long long share(long long total, int b, int blocks) {
+    return total * b / blocks;
+}
+
 // A run of chunks of one tile for up to kN rows of an expert.
 struct Piece {
     int e, tile, first_row, rows;  // rows from first_row of the expert's on
     int chunk0, chunk1;            // of the tile's chunks
-    long long start;               // the tile's first unit
+    // the blocks that share the tile (after < 0: this one has all of it), and which of its two
+    // slots the first of them uses
+    int owner, after, owner_slot;
 };
 
 // Units are chunks: expert by expert, tile by tile, the passes over kN rows each side by side
 // (they read the same weights), chunk by chunk.  prefix: passes before each expert.
 template <int kN>
 __device__ __forceinline__ Piece piece_at(const Args& a, const int* prefix, long long u,
-                                          long long end) {
+                                          long long end, long long total, int block, int blocks) {
     const long long per_pass = (long long)a.m.tiles * a.m.chunks;
     const int q = (int)(u / per_pass);
     int lo = 0, hi = a.E;  // prefix[lo] <= q < prefix[hi]
@@ -193,15 +200,22 @@ __device__ __forceinline__ Piece piece_at(const Args& a, const int* prefix, long
     const int pass = (int)(run - (long long)p.tile * passes);
     p.first_row = pass * kN;
     p.rows = cnt - p.first_row < kN ? cnt - p.first_row : kN;
-    p.start = u - p.chunk0;
     const long long left = end - u;
     p.chunk1 = left < a.m.chunks - p.chunk0 ? p.chunk0 + (int)left : a.m.chunks;
+    p.owner = p.after = -1;
+    p.owner_slot = 0;
+    if (p.chunk0 > 0 || p.chunk1 < a.m.chunks) {
+        // a tile of several blocks: those with units of [start, start + chunks).  A block's first
+        // slot is for what it starts with, its second for a tile that it starts later.
+        const long long start = u - p.chunk0;
+        int o = block, f = block;
+        while (share(total, o, blocks) > start) --o;
+        while (share(total, f + 1, blocks) < start + a.m.chunks) ++f;
+        p.owner = o;
+        p.after = f;
+        p.owner_slot = share(total, o, blocks) != start;
+    }
     return p;
-}
-
-// The unit at which block b's share starts.
-__device__ __forceinline__ long long share(long long total, int b, int blocks) {
-    return total * b / blocks;
 }
 
 // The sums of a tile's slab to their output.  weights: of the rows (gated).
@@ -305,10 +319,6 @@ __device__ __forceinline__ void load_scales(uint32_t at, float (&s)[4]) {
     s[3] = __uint_as_float(w & 0xffff0000u);
 }
 
-__device__ __forceinline__ void consumers_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-}
-
 // Each block takes an equal share of the units, whatever tiles they belong to.  A tile that
 // several blocks share: each leaves its sums in a slot of the workspace, and the one that comes
 // last adds them up in the order of the blocks and writes the tile out.  Nobody waits.
@@ -325,9 +335,12 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
     __shared__ uint64_t full[kStages], empty[kStages], a_ready[2], mma_done[2];
     __shared__ int run_sums[kThreads / 32];
     __shared__ uint32_t tmem_word;
-    __shared__ int abort_word, arrived;
-    constexpr int kRowSlots = kStages + 2;
-    __shared__ float row_weights[kGated ? kRowSlots : 1][kN];
+    __shared__ int abort_word;
+    // the pieces on their way and their rows' weights: those that read them are kSlots - 2 pieces
+    // behind the copies at most, for a piece has a chunk at least
+    constexpr int kSlots = kStages + 2;
+    __shared__ Piece slots[kSlots];
+    __shared__ float row_weights[kGated ? kSlots : 1][kN];
     uint8_t* rows_ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* ring = rows_ring + (size_t)kStages * F::kRowBytes;
     int* prefix = reinterpret_cast<int*>(ring + (size_t)kStages * F::kWeightBytes);
@@ -406,21 +419,21 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
         int pieces = 0;
         const bool one = elect_one();
         while (lu < last) {
-            lp = piece_at<kN>(a, prefix, lu, last);
+            lp = piece_at<kN>(a, prefix, lu, last, total, block, blocks);
             boxes = ceil_div(lp.rows, 8);
             row = a.offsets[lp.e] + lp.first_row;
             weights = (uint32_t)(tile_slabs(a.m, lp.tile) * F::kRecord);
             from = a.packed + (long long)lp.e * a.expert_bytes + chunk_at(a.m, lp.tile, lp.chunk0);
             if (kGated) {
-                // three loads one after the other, here in nobody's way: those that read them
-                // are kRowSlots - 2 pieces behind at most, for these have a chunk at least
+                // three loads one after the other, here in nobody's way
 #pragma unroll
                 for (int n = 0; n < kN; n += 32)
                     if (n + lane < lp.rows)
-                        row_weights[pieces % kRowSlots][n + lane] =
+                        row_weights[pieces % kSlots][n + lane] =
                             row_weight(a.gate, (long long)row + n + lane);
-                __syncwarp();
             }
+            if (lane == 0) slots[pieces % kSlots] = lp;
+            __syncwarp();
             ++pieces;
             int given_up = 0;
             if (one) {
@@ -459,8 +472,11 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
         const uint64_t b0 = sw128_desc(smem_u32(rows_ring));
         uint32_t it = 0, phase = 0;
         int slot = 0;
-        for (long long u = first; ok && u < last;) {
-            const Piece p = piece_at<kN>(a, prefix, u, last);
+        int pieces = 0;
+        for (long long u = first; ok && u < last; ++pieces) {
+            // a piece is known when its first chunk is there
+            if (!wait_one(smem_u32(&full[slot]), phase, abort_flag, a.err)) break;
+            const Piece p = slots[pieces % kSlots];
             const uint32_t idesc = make_idesc(kMmaRows, ceil_div(p.rows, 16) * 16);
             const bool upper = tile_slabs(a.m, p.tile) > kSlabs / 2;  // any slab of the second MMA's
             u += p.chunk1 - p.chunk0;
@@ -505,8 +521,8 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
         if (*abort_flag) linger();  // likewise the MMAs
     } else if (warp < kSlabs) {
         // ---------------- weights and sums ----------------
-        // One whose wait gives up goes on (with what is in memory: the call reports it), for
-        // the others' barriers need it; its later waits return at once.
+        // One whose wait gives up goes on with what is in memory to the piece's end (the call
+        // reports it); its later waits return at once.
         constexpr int kGroups = kChunk / kGroup;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t a_at = tmem + lanes + (uint32_t)((warp >> 2) * 64);
@@ -519,8 +535,11 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
         int it = 0, slot = 0, pieces = 0;
         uint32_t phase = 0;
         for (long long u = first; u < last; ++pieces) {
-            const Piece p = piece_at<kN>(a, prefix, u, last);
-            const float* weights = row_weights[kGated ? pieces % kRowSlots : 0];
+            wait_warp(smem_u32(&full[slot]), phase, abort_flag, a.err);
+            // (a wait that gave up may leave no piece: the block is done then)
+            if (*abort_flag) break;
+            const Piece p = slots[pieces % kSlots];
+            const float* weights = row_weights[kGated ? pieces % kSlots : 0];
             const bool has = warp < tile_slabs(a.m, p.tile);
             const int slab = p.tile * kSlabs + warp;
             const int columns = kN == 16 ? 16 : ceil_div(p.rows, 16) * 16;
@@ -613,47 +632,42 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
             }
             tc_fence_before();
             u += p.chunk1 - p.chunk0;
-            if (p.chunk0 == 0 && p.chunk1 == a.m.chunks) {
-                if (has) write_out<kN, kGated>(a, p, slab, sums, weights);
+            if (!has) continue;
+            if (p.after < 0) {
+                write_out<kN, kGated>(a, p, slab, sums, weights);
                 continue;
             }
-            // a tile of several blocks: those with units of [p.start, p.start + chunks)
+            // this warp's slab is shared with the same warp of other blocks
             constexpr long long kSlot = (long long)kConsumers * kN;
-            const long long tile_end = p.start + a.m.chunks;
-            int owner = block, after = block;  // the first of them, the last
-            while (share(total, owner, blocks) > p.start) --owner;
-            while (share(total, after + 1, blocks) < tile_end) ++after;
             const auto slot_of = [&](int b) {
-                const int s = b == owner && share(total, b, blocks) != p.start ? 1 : 0;
-                return a.parts + ((long long)b * 2 + s) * kSlot + threadIdx.x;
+                return a.parts + ((long long)b * 2 + (b == p.owner ? p.owner_slot : 0)) * kSlot +
+                       threadIdx.x;
             };
             float* to = slot_of(block);
 #pragma unroll
             for (int n = 0; n < kN; ++n)
                 if (n < p.rows) __stcg(to + n * kConsumers, sums[n]);
-            consumers_sync();
-            if (threadIdx.x == 0) {
-                // one thread's fences stand for all: the barriers order the others' accesses
-                // before and after them
+            __syncwarp();
+            int arrived = 0;
+            if (lane == 0) {
+                // one lane's fences stand for the warp's accesses before and after them
+                int* counter = a.counters + p.owner * kSlabs + warp;
                 __threadfence();
-                const int before_me = atomicAdd(a.counters + owner, 1);
-                if (before_me == after - owner) a.counters[owner] = 0;  // for the next call
+                arrived = atomicAdd(counter, 1);
+                if (arrived == p.after - p.owner) *counter = 0;  // for the next call
                 __threadfence();
-                arrived = before_me;
             }
-            consumers_sync();
-            // (written again behind the next such tile's first barrier, after all have read it)
-            if (arrived == after - owner && has) {
+            arrived = __shfl_sync(0xffffffffu, arrived, 0);
+            if (arrived != p.after - p.owner) continue;
 #pragma unroll
-                for (int n = 0; n < kN; ++n) sums[n] = 0.0f;
-                for (int b = owner; b <= after; ++b) {
-                    const float* from = slot_of(b);
+            for (int n = 0; n < kN; ++n) sums[n] = 0.0f;
+            for (int b = p.owner; b <= p.after; ++b) {
+                const float* from = slot_of(b);
 #pragma unroll
-                    for (int n = 0; n < kN; ++n)
-                        if (n < p.rows) sums[n] += __ldcg(from + n * kConsumers);
-                }
-                write_out<kN, kGated>(a, p, slab, sums, weights);
+                for (int n = 0; n < kN; ++n)
+                    if (n < p.rows) sums[n] += __ldcg(from + n * kConsumers);
             }
+            write_out<kN, kGated>(a, p, slab, sums, weights);
         }
     }
     tc_fence_before();
@@ -767,7 +781,7 @@ struct W4Work {
 W4Work w4_work(const moe_shape& s) {
     W4Work w;
     w.counters = workspace_layout(s).total;
-    w.parts = w.counters + align256(kMaxBlocks * sizeof(int));
+    w.parts = w.counters + align256(kMaxBlocks * kSlabs * sizeof(int));
     w.total = w.parts + (size_t)kMaxBlocks * 2 * kConsumers * sizeof(float) *
                             pass_rows((long long)s.N * s.k, s.E);
     return w;
