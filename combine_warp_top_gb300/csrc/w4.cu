@@ -767,12 +767,14 @@ __global__ void __launch_bounds__(kBlock)
 
 // ---- host -----------------------------------------------------------------------------------
 
-// Rows of a pass: enough for most experts' rows at once when they are spread as by chance
-// around their average.
+// Rows of a pass, by the experts' average: 16 take the least time for a chunk, and an expert with
+// more of them than a pass has its weights widened once for each.  32 experts of 4096 x 2816, us
+// with 16, 32 and 64 rows a pass: 8 rows an expert 54, 55, 70; 12 rows 58, 57, 72; 24 rows 92, 61,
+// 80; 32 rows 110, 80, 83; 48 rows 144, 101, 88.
 int pass_rows(long long R, int E) {
     const long long used = R < E ? R : E;
     const double mean = used > 0 ? (double)R / (double)used : 0.0;
-    return mean <= 10.0 ? 16 : mean <= 22.0 ? 32 : 64;
+    return mean <= 11.0 ? 16 : mean <= 33.0 ? 32 : 64;
 }
 
 struct W4Work {
