@@ -7,6 +7,28 @@
 // with the quintic p = (3.4445, -4.7750, 2.0315), which takes every singular value of X
 // towards 1.  A tall matrix (M > N) runs on X^T X and X S instead, so that G is always the
 // smaller square; nothing is transposed, the tensor maps name the operands MN-major.
+//
+// What is rounded.  The products' operands are fp16 (11 bits), scaled so that none of their
+// numbers that matter is a denormal: X as an operand, G and S; their sums are fp32.  Every step
+// multiplies small singular values by 3.4445, and what a rounding has put in their place with
+// them, so X in its own place in the sum, p0 X, is kept in two fp16 halves (22 bits): rounded to
+// one, a gradient of rank 16 over noise would end 3.8e-2 of its norm from the 64-bit result, 5e-4
+// with two (bf16 operands and X: 0.3).  The output's rounding to bf16 is 1.7e-3, all together
+// 2.0e-3 to 2.4e-3.
+//
+// Three products a step, on 256 x 256 tiles of a CTA pair (tcgen05, two accumulators in TMEM, 5
+// stages of 32 KB).  G and S are symmetric: only tiles on and above the diagonal are made, each
+// stored a second time as its mirror image, so that a step is 3 m^2 n + m^3 operations instead of
+// 4 m^2 n + 2 m^3 (n the longer side, m the shorter).  The epilogue does the sums, so that S and X are written once.
+//
+// What bounds it (GB300): the MMAs, at the clock that the power cap leaves.  64 of 2048 x 1408:
+// 4240 us, of them 650 the two passes ahead of the products (HBM: 12 bytes an element each); G
+// 192 us (17700 cycles a tile, 17000 of them MMAs), S 140, X 359 (14500 cycles; 11700).  16 of
+// 2048 x 7168: 5900 us, 710 ahead, G 310, S 97, X 585; all 4 m^2 n + 2 m^3 operations at a
+// library product's sustained rate would be 6400 us.  8 of 512 x 128: 104 us, 17
+// launches of one or two tiles a pair, 6 us each.
+// One kernel for all products, whose tiles wait for those that they need by counters in global
+// memory, was no faster (4670 us; 125 us): a tile's end is seen by the next one 5 us later.
 #include <stddef.h>
 
 #include <cuda_fp16.h>

@@ -16,7 +16,20 @@
 // the number 128 + q, less 136: exact) and stores them into TMEM, from where the MMA takes A:
 // shared memory sees the 4-bit form only.  A group's sums are fp32 in TMEM; the thread reads
 // its row's, scales them once and adds them to its own sums, in fp32, while the MMAs of the
-// next 64 weights run.
+// next 64 weights run.  (mma.sync on weights widened in the same way: 129 tokens of the fourth
+// case below 213 us, 16 tokens of the second 379 us.)
+//
+// What bounds it (GB300), in a graph, and the bytes' floor:
+//   1 token of 8 of 256 experts, 2048 -> 7168          23.4 us    8.9
+//   16 tokens of the same layer, gate and up           317 us     227   (5.0 TB/s)
+//   64 tokens of 6 of 64 experts, 2048 -> 2 x 1408     56 us      29
+//   129 tokens of 2 of 8 experts, 14336 -> 4096        85 us      37
+// The integer pipe, in the long run: 7 operations (4 LOP3, 3 shifts) for 8 weights take it to
+// 62%, which with 20 warps an SM is all it gives; without the shifts the second case takes 271
+// us, without the subtractions no less, without widening 237.  Multiplications in the shifts'
+// place are slower (354 us), byte permutes the same.  A block's chunk takes 2000 cycles (two
+// blocks an SM), of which it waits 450.  In short calls the ends: 3500 cycles until a block has
+// found its first tile, 5400 to join a tile that blocks share.
 #include <stddef.h>
 
 #include "../../include/moe_train.h"
