@@ -12,9 +12,11 @@
 // numbers that matter is a denormal: X as an operand, G and S; their sums are fp32.  Every step
 // multiplies small singular values by 3.4445, and what a rounding has put in their place with
 // them, so X in its own place in the sum, p0 X, is kept in two fp16 halves (22 bits): rounded to
-// one, a gradient of rank 16 over noise would end 3.8e-2 of its norm from the 64-bit result, 5e-4
-// with two (bf16 operands and X: 0.3).  The output's rounding to bf16 is 1.7e-3, all together
-// 2.0e-3 to 2.4e-3.
+// one, a gradient of rank 16 over noise would end 3.8e-2 of its norm from the 64-bit result (bf16
+// operands and X: 0.3).  And S, near the end some -2.7 I and little beside it, goes apart: its
+// diagonal d, fp32, to p0, the rest into the product, whose roundings are then those of the
+// little.  Together 4e-4 to 1.4e-3 of the result's norm (with S whole up to 2.2e-3); the output's
+// own rounding to bf16 is 1.7e-3.
 //
 // Three products a step, on 256 x 256 tiles of a CTA pair (tcgen05, two accumulators in TMEM, 5
 // stages of 32 KB).  G and S are symmetric: only tiles on and above the diagonal are made, each
@@ -163,12 +165,16 @@ __device__ __forceinline__ void tmem_ld_columns(uint32_t at, uint32_t (&v)[64]) 
 // k ^ (r % 8) of its 128 bytes or k ^ (r / 2 % 4) of its 64: TMA's swizzles; a mirror image has
 // none.
 //   kGram    G = acc * 2^(12 - 2p), and its mirror image
-//   kSquare  S = p1 G + p2 acc * 2^-12, likewise
-//   kStep    x = p0 (hi + lo) + acc * 2^-12, into hi and lo
+//   kSquare  S = p1 G + p2 acc * 2^-12, likewise; kSpecial: with the column `at_diag` of this row
+//            taken out (into *diag), if it is one of these
+//   kStep    x = (p0 + d) (hi + lo) + acc * 2^-12, into hi and lo
 //   kLast    the same times 2^-p, bf16
-template <Form kForm, int kWarps>
+// with p0 + d as beta; kSpecial: with d by columns at `diag`, of which there are `left`, times
+// `unscale`.
+template <Form kForm, int kWarps, bool kSpecial>
 __device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLine<kWarps>],
-                                        float alpha, float beta) {
+                                        float alpha, float beta, float* diag, int at_diag, int left,
+                                        float unscale) {
     constexpr int kL = kLine<kWarps>;
     const int lane = threadIdx.x & 31, flip = kL == 64 ? lane & 7 : lane >> 1 & 3;
     uint8_t* second = lines + kLinesBytes<kWarps>;
@@ -187,6 +193,16 @@ __device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLin
                 const uint4 o = *lo_at;
                 l[0] = o.x, l[1] = o.y, l[2] = o.z, l[3] = o.w;
             }
+            float b[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[j] = beta;
+            if (kForm != kSquare && kSpecial && k * 8 < left) {
+                const float4 d0 = reinterpret_cast<const float4*>(diag + k * 8)[0];
+                const float4 d1 = reinterpret_cast<const float4*>(diag + k * 8)[1];
+                const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) b[j] = fmaf(unscale, d[j], beta);
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float2 x = unpack_half2(w[j]);
@@ -195,8 +211,17 @@ __device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLin
                     x.x += y.x;
                     x.y += y.y;
                 }
-                f[2 * j] = fmaf(beta, x.x, f[2 * j]);
-                f[2 * j + 1] = fmaf(beta, x.y, f[2 * j + 1]);
+                f[2 * j] = fmaf(b[2 * j], x.x, f[2 * j]);
+                f[2 * j + 1] = fmaf(b[2 * j + 1], x.y, f[2 * j + 1]);
+            }
+            if (kForm == kSquare && kSpecial) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (k * 8 + j == at_diag) {
+                        *diag = f[j] * (1.0f / kSquareScale);
+                        f[j] = 0.0f;
+                    }
+                }
             }
         }
         uint32_t o[4];
@@ -225,7 +250,8 @@ __device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLin
 }
 
 // in, in2: G, or X's two halves (kStep, kLast); out, out2: the output and its mirror image or
-// X's second half.
+// X's second half.  diag: S's diagonal, fp32 [E, m]: kSquare writes it and leaves zeros in its
+// place, kStep and kLast add it to p0.
 template <Form kForm, bool kMnA, bool kMnB, int kWarps>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1)
     muon_product_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -234,8 +260,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
                         const __grid_constant__ CUtensorMap tmIn2,
                         const __grid_constant__ CUtensorMap tmOut,
                         const __grid_constant__ CUtensorMap tmOut2, Dims d, float alpha,
-                        float beta, int* err) {
+                        float beta, float unscale, float* diag, int* err) {
     constexpr bool kSym = kForm == kGram || kForm == kSquare;
+    constexpr bool kWide = kMnB;  // kStep, kLast: S X (S's rows are X's), or else X S
     constexpr int kL = kLine<kWarps>, kColumns = 4 * kL;  // of a line, of an epilogue warp
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -392,6 +419,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
                     tma_load_3d(to + kLinesBytes<kWarps>, &tmIn2, bar, col + c * kL, row, t.e);
             };
             if (have > 0) fetch(0, buf);
+            float* diag_e = diag + (long long)t.e * (kForm >= kStep && !kWide ? d.n : d.m);
+            float row_beta = beta;
+            if (kForm >= kStep && kWide && row + lane < d.m)
+                row_beta = fmaf(unscale, diag_e[row + lane], beta);
             int ok = 0;
             if (lane == 0)
                 ok = wait_bar(smem_u32(&ctl->tfull[acc]), acc_phase, abort_flag, err);
@@ -420,7 +451,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
                 if (!__all_sync(0xffffffffu, ok)) break;
                 if (c + 1 < have) fetch(c + 1, buf ^ 1);
                 uint8_t* mine = lines + buf * kBufferBytes<kWarps>;
-                combine<kForm, kWarps>(mine, v, alpha, beta);
+                const int first = col + c * kL;
+                if (kForm == kSquare && t.mb == t.nb)
+                    combine<kForm, kWarps, true>(mine, v, alpha, beta, diag_e + row + lane,
+                                                 row + lane < d.m ? row + lane - first : -1, 0, 0.0f);
+                else if (kForm >= kStep && !kWide)
+                    combine<kForm, kWarps, true>(mine, v, alpha, beta, diag_e + first, 0,
+                                                 d.n - first, unscale);
+                else
+                    combine<kForm, kWarps, false>(mine, v, alpha, row_beta, nullptr, 0, 0, 0.0f);
                 fence_async_shared();
                 __syncwarp();
                 if (lane == 0) {
@@ -608,7 +647,7 @@ __global__ void __launch_bounds__(kBlock)
 // ---- host ---------------------------------------------------------------------------------
 
 struct Work {
-    size_t parts, gram, square, hi[2], lo, total;
+    size_t parts, diag, gram, square, hi[2], lo, total;
 };
 Work work_of(const moe_muon_shape& s) {
     const size_t n = (size_t)s.E * s.M * s.N;
@@ -616,6 +655,7 @@ Work work_of(const moe_muon_shape& s) {
     Work w;
     size_t o = 256;  // the error word
     w.parts = o;  o = align256(o + (size_t)s.E * kMaxParts * sizeof(double2));
+    w.diag = o;   o = align256(o + (size_t)s.E * m * 4);
     w.gram = o;   o = align256(o + sq * 2);
     w.square = o; o = align256(o + sq * 2);
     for (size_t& hi : w.hi) hi = o, o = align256(o + n * 2);
@@ -640,8 +680,8 @@ struct LineMaps {
 
 template <Form kForm, bool kMnA, bool kMnB, int kWarps>
 moe_status launch_form(const CUtensorMap& a, const CUtensorMap& b, const LineMaps& l, int now,
-                       const Dims& d, float alpha, float beta, int* err, long long pairs,
-                       cudaStream_t st) {
+                       const Dims& d, float alpha, float beta, float unscale, float* diag, int* err,
+                       long long pairs, cudaStream_t st) {
     const auto kernel = muon_product_kernel<kForm, kMnA, kMnB, kWarps>;
     static OncePerDevice set;
     int dev = 0;
@@ -663,21 +703,22 @@ moe_status launch_form(const CUtensorMap& a, const CUtensorMap& b, const LineMap
                               : kForm == kStep   ? l.lo
                                                  : l.out;
     return cuda_status(launch_chained(kernel, (int)(2 * pairs), 128 + 32 * kWarps, kSmem, st, a, b,
-                                      in, in2, out, out2, d, alpha, beta, err));
+                                      in, in2, out, out2, d, alpha, beta, unscale, diag, err));
 }
 template <Form kForm, bool kMnA, bool kMnB>
 moe_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const LineMaps (&l)[2],
-                          int now, const Dims& d, float alpha, float beta, int* err,
-                          cudaStream_t st) {
+                          int now, const Dims& d, float alpha, float beta, float unscale,
+                          float* diag, int* err, cudaStream_t st) {
     const long long MB = blocks_of(d.m, BT), NB = blocks_of(d.n, BT);
     const long long tiles =
         d.E * (kForm == kGram || kForm == kSquare ? NB * (NB + 1) / 2 : MB * NB);
     const long long most = sm_count() / 2;
     // 8 warps where a pair has no more than four tiles
     return tiles > 4 * most ? launch_form<kForm, kMnA, kMnB, 4>(a, b, l[0], now, d, alpha, beta,
-                                                                err, most, st)
+                                                                unscale, diag, err, most, st)
                             : launch_form<kForm, kMnA, kMnB, 8>(a, b, l[1], now, d, alpha, beta,
-                                                                err, tiles < most ? tiles : most, st);
+                                                                unscale, diag, err,
+                                                                tiles < most ? tiles : most, st);
 }
 
 template <typename G>
@@ -740,6 +781,7 @@ moe_status moe_muon_update(const void* grad, const float* momentum, const moe_mu
     __half* hi[2] = {ws_ptr<__half>(ws, w.hi[0]), ws_ptr<__half>(ws, w.hi[1])};
     auto* lo = ws_ptr<__half>(ws, w.lo);
     auto* parts = ws_ptr<double2>(ws, w.parts);
+    float* diag = ws_ptr<float>(ws, w.diag);
     int* err = ws_ptr<int>(ws, 0);
     MOE_TRY(s.grad_type == MOE_TYPE_F32
                 ? launch_prepare(static_cast<const float*>(grad), momentum, new_momentum, s, p,
@@ -776,16 +818,16 @@ moe_status moe_muon_update(const void* grad, const float* momentum, const moe_mu
     for (int i = 0; i < s.steps; ++i) {
         const int now = i % 2;
         MOE_TRY(tall ? launch_product<kGram, true, true>(x_mn[now], x_mn[now], l, now, gd, scale,
-                                                         0.0f, err, st)
+                                                         0.0f, 1.0f, diag, err, st)
                      : launch_product<kGram, false, false>(x_k[now], x_k[now], l, now, gd, scale,
-                                                           0.0f, err, st));
-        MOE_TRY(launch_product<kSquare, false, false>(g_k, g_k, l, now, sd, kP2 * back, kP1, err,
-                                                      st));
+                                                           0.0f, 1.0f, diag, err, st));
+        MOE_TRY(launch_product<kSquare, false, false>(g_k, g_k, l, now, sd, kP2 * back, kP1, 1.0f,
+                                                      diag, err, st));
         const bool last = i == s.steps - 1;
         const float unscale = last ? ldexpf(1.0f, -p) : 1.0f;
         const CUtensorMap &a = tall ? x_k[now] : s_k, &b = tall ? s_k : x_mn[now];
         const auto step = [&](auto launch) {
-            return launch(a, b, l, now, xd, back * unscale, kP0 * unscale, err, st);
+            return launch(a, b, l, now, xd, back * unscale, kP0 * unscale, unscale, diag, err, st);
         };
         if (last)
             MOE_TRY(tall ? step(launch_product<kLast, false, false>)

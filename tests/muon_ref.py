@@ -17,8 +17,8 @@ def momentum(g, b, beta, nesterov):
 
 
 def orthogonal(u, steps, eps, rounded=False):
-    """X of one matrix u [M, N] (float64).  rounded: G, S and X as an operand in fp16, scaled
-    as the operator scales them (G and S by 2^12, X by 2^p)."""
+    """X of one matrix u [M, N] (float64).  rounded: G, S without its diagonal and X as an
+    operand in fp16, scaled as the operator scales them (G and S by 2^12, X by 2^p)."""
     tall = u.shape[0] > u.shape[1]
     x = u.T if tall else u
     x = x / (torch.linalg.vector_norm(x) + eps)
@@ -31,6 +31,7 @@ def orthogonal(u, steps, eps, rounded=False):
     for _ in range(steps):
         xr = r(x, p)
         g = r(xr @ xr.T, 4096.0)
-        s = r(P1 * g + P2 * (g @ g), 4096.0)
-        x = P0 * x + s @ xr
+        s = P1 * g + P2 * (g @ g)
+        d = torch.diagonal(s).clone()
+        x = (P0 + d)[:, None] * x + r(s - torch.diag(d), 4096.0) @ xr
     return x.T if tall else x

@@ -1,7 +1,7 @@
 """Orthogonalised momentum against its definition in 64 bits.
 
-Tolerances.  The operator rounds G, S and X as an operand to fp16 and nothing else below fp32
-but the output.  What those roundings do to a result depends on the matrix (small singular
+Tolerances.  The operator rounds G, S without its diagonal and X as an operand to fp16 and nothing
+else below fp32 but the output.  What those roundings do to a result depends on the matrix (small singular
 values grow by 3.4445 a step, and so does what a rounding adds there), so it is computed: the
 same recurrence in 64 bits with these roundings is off by e from the one without, and the
 operator, whose own sums round otherwise in the last place and so round some numbers to the
