@@ -581,20 +581,27 @@ __device__ __forceinline__ void gated_out(const CUtensorMap& tmGu, const CUtenso
 
 // kGated in tiles of few rows: a warp has the sums of 32 gate or up columns (its TMEM lanes)
 // by 32 rows.  The two warps of the same columns lay them down as lines of a row each, and
-// take 16 of the rows each.  in, out: their two barriers of 64 threads.
+// take 16 of the rows each, between their two barriers of 64 threads.
 __device__ __forceinline__ void named_sync(int id) {
     asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
 }
 __device__ __forceinline__ void named_arrive(int id) {
     asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
 }
+__device__ __forceinline__ int few_barrier(int q, int half) { return 1 + half * 2 + (q & 1); }
+// A warp that takes no further tile, at the end or because a wait has given up: the other one may
+// still be at these barriers with a tile of before.
+__device__ __forceinline__ void gated_few_leave(int q, int half) {
+    named_arrive(few_barrier(q, half));
+    named_arrive(few_barrier(q, half) + 4);
+}
 __device__ __forceinline__ void gated_few_out(const Gate& gate, uint8_t* staging_area, int q,
                                               int half, const uint32_t (&v)[32], long long row,
-                                              int rows, int col, int I, float w, int in, int out) {
+                                              int rows, int col, int I, float w) {
     const int lane = threadIdx.x & 31;
     uint8_t* mine = staging_area + (size_t)(half * 4 + q) * kStagingBytes;
     put_few(mine, lane, v);
-    named_sync(in);
+    named_sync(few_barrier(q, half));
     const uint8_t* gs = staging_area + (size_t)(half * 4 + (q & 1)) * kStagingBytes;
     const uint8_t* us = gs + 2 * kStagingBytes;
     const int c = (lane & 7) * 4;
@@ -615,7 +622,7 @@ __device__ __forceinline__ void gated_few_out(const Gate& gate, uint8_t* staging
             make_uint2(pack2(wr * (g.x * sigmoid(g.x)) * u.x, wr * (g.y * sigmoid(g.y)) * u.y),
                        pack2(wr * (g.z * sigmoid(g.z)) * u.z, wr * (g.w * sigmoid(g.w)) * u.w));
     }
-    named_sync(out);
+    named_sync(few_barrier(q, half) + 4);
 }
 
 // Two fp32 numbers in one instruction.
@@ -1325,7 +1332,10 @@ __device__ __forceinline__ void grouped_product(
         } else
         for (int i = 0;; ++i) {
             Tile t = {};
-            if (!warp_next(ctl, i, leader, abort_flag, err, t)) break;
+            if (!warp_next(ctl, i, leader, abort_flag, err, t)) {
+                if constexpr (kMode == kGated && kFew) gated_few_leave(q, half);
+                break;
+            }
             if (!kSplit && kW && t.kblocks == 0 && accumulate) continue;  // nothing to add
             if (kSplit) joined = t;
 
@@ -1356,11 +1366,8 @@ __device__ __forceinline__ void grouped_product(
                 const int left = t.cnt - t.mb * BF - half * 32, rows = left < 32 ? left : 32;
                 const long long row = (long long)t.off + t.mb * BF + half * 32;
                 const float w = lane < rows ? row_weight(gate, row + lane) : 0.0f;
-                const int in = 1 + half * 2 + (q & 1), out_id = in + 4;
-                if (!ready()) {
-                    // the warp of the other half of these columns may be waiting already
-                    named_arrive(in);
-                    named_arrive(out_id);
+                if (!ready() || *abort_flag) {
+                    gated_few_leave(q, half);
                     break;
                 }
                 uint32_t v[32];
@@ -1368,7 +1375,7 @@ __device__ __forceinline__ void grouped_product(
                 tmem_wait_ld();
                 release();
                 gated_few_out(gate, staging_area, q, half, v, row, rows,
-                              t.nb * BH + (int)rank * 64 + (q & 1) * 32, n_out, w, in, out_id);
+                              t.nb * BH + (int)rank * 64 + (q & 1) * 32, n_out, w);
                 continue;
             } else if constexpr (kMode == kGated) {
                 const int at_row = t.mb * BT + (int)rank * BH + q * 32, rows = t.cnt - at_row;
@@ -1896,6 +1903,9 @@ moe_status launch_gated_grad(const uint16_t* dout, const GemmGroup& g, int c_out
 // Contractions up to this are one chain of an accumulator (see "Precision").
 constexpr int kMaxGateTerms = kChainBlocks<__nv_bfloat16> * BK;
 
+// Columns of gu, and so its rows' pitch, are 32 bits.
+constexpr int kMaxGateColumns = 1 << 28;
+
 size_t gated_parts_offset(const moe_shape& s) { return workspace_layout(s).total; }
 
 moe_status check_grouped(const moe_layout* layout, const moe_shape* shape, int32_t C_in,
@@ -1956,7 +1966,7 @@ moe_status moe_gated_gemm(const uint16_t* rows, const moe_layout* layout, const 
                           uint16_t* gu, uint16_t* h, void* ws, size_t ws_bytes, void* stream) {
     MOE_RANGE();
     MOE_TRY(check_grouped(layout, shape, C_in, 8, MOE_TYPE_BF16, ws, ws_bytes));
-    if (C_in > kMaxGateTerms) return MOE_ERR_UNSUPPORTED;
+    if (C_in > kMaxGateTerms || shape->I > kMaxGateColumns) return MOE_ERR_UNSUPPORTED;
     if (shape->N == 0) return MOE_OK;
     if (!rows || !w_gate_up || !h) return MOE_ERR_INVALID_ARG;
     if (!aligned16(rows, w_gate_up, gu, h)) return MOE_ERR_INVALID_ARG;
@@ -1973,7 +1983,7 @@ moe_status moe_gated_gemm_grad(const uint16_t* dout, const moe_layout* layout,
     MOE_RANGE();
     MOE_TRY(check_grouped(layout, shape, 8, C_out, MOE_TYPE_BF16, ws, ws_bytes));
     if (ws_bytes < moe_gated_workspace_bytes(shape)) return MOE_ERR_WORKSPACE;
-    if (C_out > kMaxGateTerms) return MOE_ERR_UNSUPPORTED;
+    if (C_out > kMaxGateTerms || shape->I > kMaxGateColumns) return MOE_ERR_UNSUPPORTED;
     if (shape->N == 0) return MOE_OK;
     if (!dout || !w_down || !gu || !dgu) return MOE_ERR_INVALID_ARG;
     if (!aligned16(dout, w_down, gu, dgu)) return MOE_ERR_INVALID_ARG;

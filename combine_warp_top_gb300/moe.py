@@ -888,11 +888,19 @@ class W4Matrices:
 
     def __init__(self, E: int, C_out: int, C_in: int, group: int, gated: bool, device="cuda"):
         self.E, self.C_out, self.C_in, self.group, self.gated = E, C_out, C_in, group, bool(gated)
-        self.ref = ctypes.byref(MoeW4Matrix(C_out, C_in, group, int(self.gated)))
         n = int(load().moe_w4_packed_bytes(self.ref, E))
         if n == 0:
             raise MoeError(1, "moe_w4_packed_bytes")
         self.data = torch.empty(n, dtype=torch.uint8, device=device)
+
+    @functools.cached_property
+    def ref(self):
+        """The C struct by reference, made once for these matrices."""
+        return ctypes.byref(MoeW4Matrix(self.C_out, self.C_in, self.group, int(self.gated)))
+
+    def __getstate__(self):
+        """All but the reference: copies and pickles make their own."""
+        return {n: v for n, v in vars(self).items() if n != "ref"}
 
 
 def moe_w4_quantize(w, q, scales, stream=None):

@@ -184,13 +184,17 @@ class MoETrainBlock:
         if self.momenta is None:
             self.momenta = {n: torch.zeros_like(p[n]) for n in matrices}
             self.updates = {n: torch.empty_like(self.w[n]) for n in matrices}
-            need = max(moe.moe_muon_workspace_bytes(moe.MuonShape(*m)) for m in matrices.values())
+            need = max(moe.moe_muon_workspace_bytes(moe.MuonShape(min(E, 1024), M, N))
+                       for E, M, N in matrices.values())
             self.muon_ws = torch.empty(need, dtype=torch.uint8, device=p["w_down"].device)
             self.muon_ws[:256].zero_()
         for n, (E, M, N) in matrices.items():
-            shape = moe.MuonShape(E, M, N, momentum=momentum, nesterov=nesterov)
-            moe.moe_muon_update(g[n].view(E, M, N), self.momenta[n].view(E, M, N), shape,
-                                self.updates[n].view(E, M, N), self.muon_ws)
+            grads, momenta, updates = (t.view(E, M, N) for t in (g[n], self.momenta[n],
+                                                                 self.updates[n]))
+            for e in range(0, E, 1024):  # as many as a call takes
+                part = slice(e, min(E, e + 1024))
+                shape = moe.MuonShape(part.stop - e, M, N, momentum=momentum, nesterov=nesterov)
+                moe.moe_muon_update(grads[part], momenta[part], shape, updates[part], self.muon_ws)
             p[n].mul_(1.0 - lr * weight_decay).add_(self.updates[n],
                                                     alpha=-lr * 0.2 * max(M, N) ** 0.5)
         for n in p:

@@ -96,7 +96,7 @@ moe_status moe_swiglu_grad(const uint16_t* dh, const uint16_t* gu, const float* 
  * bf16 [N*k, I]; gu bf16 [N*k, 2*I] receives g and u for the gradient (NULL: not wanted).
  * dout bf16 [N*k, C_out], w_down bf16 [E, C_out, I], dgu bf16 [N*k, 2*I] (may be gu itself),
  * dtopk_w fp32 [N, k] (NULL: not wanted).  topk_w may be NULL (weights of one).  shape gives
- * N, k, E and I; C_in and C_out are multiples of 8, at most 32768.
+ * N, k, E and I; C_in and C_out are multiples of 8, at most 32768, I is at most 2^28.
  * ws: workspace of moe_gated_workspace_bytes(shape) bytes (moe_gated_gemm: of
  * moe_workspace_bytes(shape)), on a 4-byte boundary, its first moe_workspace_bytes(shape)
  * bytes zero at first. */

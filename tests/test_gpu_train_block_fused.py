@@ -69,3 +69,20 @@ def test_muon_step():
 def test_training_runs():
     losses = train.main(steps=6, N=64, H=64, E=4, k=2, I=64, optimizer="muon")
     assert len(losses) == 6 and all(v == v for v in losses)
+
+
+def test_muon_of_more_matrices_than_a_call_takes():
+    block = train.MoETrainBlock(4, 8, 640, 1, 8, fuse_gate=True)
+    for n, g in block.grads.items():
+        g.copy_(torch.randn(g.shape, device="cuda"))
+    before = block.params["w_gate_up"].clone()
+    block.muon(1.0)
+    moved = (before - block.params["w_gate_up"]).view(-1, 8, 8) / (0.2 * 8 ** 0.5)
+    for e in (0, 1023, 1024, 1279):
+        u, _ = muon_ref.momentum(block.grads["w_gate_up"].view(-1, 8, 8)[e], torch.zeros(
+            8, 8, device="cuda"), 0.95, True)
+        want = muon_ref.orthogonal(u, 5, 1e-7)
+        off = (muon_ref.orthogonal(u, 5, 1e-7, rounded=True) - want).norm()
+        # as for the operator alone; 2^-22 for the step's two fp32 roundings and the way back
+        assert (moved[e] - want).norm() <= 2 * off + (2.0 ** -8 + 1e-3) * want.norm() + \
+            2.0 ** -22 * before.abs().max() * 8 / (0.2 * 8 ** 0.5)

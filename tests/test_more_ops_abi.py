@@ -49,6 +49,10 @@ def test_gated_refusals(lib):
     assert grad(dout=None) == INVALID and grad(gu=None) == INVALID and grad(dgu=ODD) == INVALID
     assert grad(co=-8) == INVALID and grad(co=12) == UNSUPPORTED and grad(co=40000) == UNSUPPORTED
     assert grad(n=base) == WORKSPACE
+    wide, Lw, sw = args(I=(1 << 28) + 8)
+    more = moe.moe_gated_workspace_bytes(sw)
+    assert fwd(lay=Lw, shape=wide, n=more) == UNSUPPORTED
+    assert grad(lay=Lw, shape=wide, n=more) == UNSUPPORTED
     none, L0, _ = args(N=0)
     assert fwd(rows=None, lay=L0, shape=none, w=None, h=None) == 0
     assert grad(dout=None, lay=L0, shape=none, w=None, gu=None, dgu=None) == 0
@@ -152,6 +156,9 @@ def test_w4_binding_and_layer(lib):
     def layer(shape=s, w4=(gated, plain), **kw):
         return moe.MoELayer(shape, None, None, None, device="cpu", w4=w4, **kw)
 
+    for other in (copy.copy(plain), copy.deepcopy(plain), pickle.loads(pickle.dumps(plain))):
+        assert (other.C_out, other.gated) == (128, False) and other.data.shape == plain.data.shape
+        assert other.ref is not plain.ref
     one = layer()
     assert one.stage_names() == ["route", "layout", "dispatch", "gate_up", "down", "combine"]
     assert one.kernel_launches_per_step() == 1 + 1 + 1 + 2 + 1
