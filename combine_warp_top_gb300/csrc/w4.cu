@@ -165,16 +165,27 @@ __device__ __forceinline__ void tmem_st_a(uint32_t at, const uint32_t (&r)[16]) 
         : "memory");
 }
 
-// Eight nibbles to four pairs: nibble r and nibble r + 4 are the halves of register r.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// Eight nibbles to four pairs of (q - 8) / 64: nibble r and nibble r + 4 are the halves of
+// register r.  The last eight bits of a bf16 that has no others set are its units of 2^-133
+// (subnormals and the binade above them are one line), so that a nibble is a number where it
+// stands, q or 16 q units, and one FMA makes it the weight, exact: no exponent to be put to it,
+// and one shift for both bytes.
 __device__ __forceinline__ void widen(uint32_t w, uint32_t* a) {
-    const __nv_bfloat162 bias = __float2bfloat162_rn(136.0f);
+    const uint32_t low = 0x7f007f00u, high = 0x7d007d00u, less = 0xbe00be00u;  // 2^127, 2^123, -1/8
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const uint32_t v = and_or(w >> (4 * r), 0x000f000fu, 0x43004300u);
-        const __nv_bfloat162 x = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), bias);
-        a[r] = *reinterpret_cast<const uint32_t*>(&x);
+    for (int r = 0; r < 4; r += 2) {
+        const uint32_t b = w >> (4 * r);
+        a[r] = fma_bf16x2(b & 0x000f000fu, low, less);
+        a[r + 1] = fma_bf16x2(b & 0x00f000f0u, high, less);
     }
 }
+constexpr float kWidened = 64.0f;  // the weights over what widen gives
 
 // The unit at which block b's share starts.
 __device__ __forceinline__ long long share(long long total, int b, int blocks) {
@@ -245,8 +256,9 @@ __device__ __forceinline__ void write_out(const Args& a, const Piece& p, int sla
 #pragma unroll
         for (int n = 0; n < kN; n += 2) {
             if (n >= p.rows) break;
-            const float got = __shfl_xor_sync(0xffffffffu, upper ? s[n] : s[n + 1], 16);
-            const float g = upper ? got : s[n], u = upper ? s[n + 1] : got;
+            const float mine_of = kWidened * (upper ? s[n + 1] : s[n]);
+            const float got = kWidened * __shfl_xor_sync(0xffffffffu, upper ? s[n] : s[n + 1], 16);
+            const float g = upper ? got : mine_of, u = upper ? mine_of : got;
             const int mine = n + upper;
             if (mine >= p.rows || o >= a.m.rows) continue;
             const long long row = row0 + mine;
@@ -262,9 +274,9 @@ __device__ __forceinline__ void write_out(const Args& a, const Piece& p, int sla
         if (n >= p.rows) break;
         const long long at = (row0 + n) * a.m.rows + o;
         if (a.out_f32)
-            static_cast<float*>(a.out)[at] = s[n];
+            static_cast<float*>(a.out)[at] = kWidened * s[n];
         else
-            static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(s[n]);
+            static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(kWidened * s[n]);
     }
 }
 
