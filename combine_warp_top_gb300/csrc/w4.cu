@@ -12,24 +12,24 @@
 // chunks come by TMA boxes of 8 rows.
 //
 // The matrix is the MMA's A and the rows are its B (tcgen05, M = 128, N = 16 to 64).  A thread
-// has one row of the matrix: it widens the row's weights to bf16 in registers (q | 0x4300 is
-// the number 128 + q, less 136: exact) and stores them into TMEM, from where the MMA takes A:
+// has one row of the matrix: it widens the row's weights to bf16 in registers (q - 8 over 64,
+// exact: see widen) and stores them into TMEM, from where the MMA takes A:
 // shared memory sees the 4-bit form only.  A group's sums are fp32 in TMEM; the thread reads
 // its row's, scales them once and adds them to its own sums, in fp32, while the MMAs of the
 // next 64 weights run.  (mma.sync on weights widened in the same way: 129 tokens of the fourth
 // case below 213 us, 16 tokens of the second 379 us.)
 //
 // What bounds it (GB300), in a graph, and the bytes' floor:
-//   1 token of 8 of 256 experts, 2048 -> 7168          23.4 us    8.9
-//   16 tokens of the same layer, gate and up           317 us     227   (5.0 TB/s)
-//   64 tokens of 6 of 64 experts, 2048 -> 2 x 1408     56 us      29
-//   129 tokens of 2 of 8 experts, 14336 -> 4096        85 us      37
-// The integer pipe, in the long run: 7 operations (4 LOP3, 3 shifts) for 8 weights take it to
-// 62%, which with 20 warps an SM is all it gives; without the shifts the second case takes 271
-// us, without the subtractions no less, without widening 237.  Multiplications in the shifts'
-// place are slower (354 us), byte permutes the same.  A block's chunk takes 2000 cycles (two
-// blocks an SM), of which it waits 450.  In short calls the ends: 3500 cycles until a block has
-// found its first tile, 5400 to join a tile that blocks share.
+//   1 token of 8 of 256 experts, 2048 -> 7168          22 us      8.9
+//   16 tokens of the same layer, gate and up           268 us     227   (5.9 TB/s)
+//   64 tokens of 6 of 64 experts, 2048 -> 2 x 1408     50 us      29
+//   129 tokens of 2 of 8 experts, 14336 -> 4096        76 us      37
+// In the long run the integer pipe: 5 operations (4 LOP3, a shift) for 8 weights; without the
+// shift the second case would take 246 us, without the groups' sums 256, without widening 234.
+// (Before widen used subnormals it had 7 operations and a subtraction for every pair: 317 us.  A
+// multiplication in the shift's place 292, a byte permute the same as it.)  In short calls the
+// ends: 3500 cycles until a block has found its first tile, 5400 to join a tile that blocks
+// share; and an expert of more rows than a pass has its weights widened for each.
 #include <stddef.h>
 
 #include "../../include/moe_train.h"
@@ -155,8 +155,7 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint64_t b_
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_a(uint32_t at, const uint32_t (&x)[32]) { tmem_st32(at, x); }
-__device__ __forceinline__ void tmem_st_a(uint32_t at, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
         "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
@@ -606,19 +605,16 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
                 const uint32_t rec = rec0 + (uint32_t)(slot * F::kWeightBytes);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    // 32 weights at a time of a row where the registers are its sums'
-                    constexpr int kPieces = kN == 16 ? 2 : 1;
-                    uint32_t x[16 * kPieces];
+                    // 32 weights of a row at a time
+                    uint32_t x[16];
                     const auto widen_piece = [&](int piece) {
                         const uint4 v = ld_shared4(rec + (h * 2 + piece) * 512);
-                        uint32_t* to = x + piece % kPieces * 16;
-                        widen(v.x, to);
-                        widen(v.y, to + 4);
-                        widen(v.z, to + 8);
-                        widen(v.w, to + 12);
+                        widen(v.x, x);
+                        widen(v.y, x + 4);
+                        widen(v.z, x + 8);
+                        widen(v.w, x + 12);
                     };
                     widen_piece(0);
-                    if (kPieces == 2) widen_piece(1);
                     if (h == 0) {
 #pragma unroll
                         for (int g = 0; g < kGroups; ++g) old[g] = scale[g];
@@ -627,11 +623,9 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
                     // the buffer's MMAs of the chunk before
                     wait_warp(smem_u32(&mma_done[h]), (uint32_t)(it - 1) & 1u, abort_flag, a.err);
                     tc_fence_after();
-                    tmem_st_a(a_at + (uint32_t)(h * 32), x);
-                    if (kPieces == 1) {
-                        widen_piece(1);
-                        tmem_st_a(a_at + (uint32_t)(h * 32 + 16), x);
-                    }
+                    tmem_st16(a_at + (uint32_t)(h * 32), x);
+                    widen_piece(1);
+                    tmem_st16(a_at + (uint32_t)(h * 32 + 16), x);
                     // this half's MMAs write where the sums of two halves ago are; with groups
                     // of 128, where those of two chunks ago were
                     if (kGroup < 128 && c > p.chunk0) drain_half(it - 1, h, old);
@@ -794,12 +788,12 @@ __global__ void __launch_bounds__(kBlock)
 
 // Rows of a pass, by the experts' average: 16 take the least time for a chunk, and an expert with
 // more of them than a pass has its weights widened once for each.  32 experts of 4096 x 2816, us
-// with 16, 32 and 64 rows a pass: 8 rows an expert 54, 55, 70; 12 rows 58, 57, 72; 24 rows 92, 61,
-// 80; 32 rows 110, 80, 83; 48 rows 144, 101, 88.
+// with 16, 32 and 64 rows a pass: 8 rows an expert 50, 51, 68; 12 rows 53, 53, 72; 24 rows 84, 58,
+// 82; 32 rows 101, 75, 85; 48 rows 130, 95, 90.
 int pass_rows(long long R, int E) {
     const long long used = R < E ? R : E;
     const double mean = used > 0 ? (double)R / (double)used : 0.0;
-    return mean <= 11.0 ? 16 : mean <= 33.0 ? 32 : 64;
+    return mean <= 12.0 ? 16 : mean <= 33.0 ? 32 : 64;
 }
 
 struct W4Work {
