@@ -21,14 +21,15 @@
 // Three products a step, on 256 x 256 tiles of a CTA pair (tcgen05, two accumulators in TMEM, 5
 // stages of 32 KB).  G and S are symmetric: only tiles on and above the diagonal are made, each
 // stored a second time as its mirror image, so that a step is 3 m^2 n + m^3 operations instead of
-// 4 m^2 n + 2 m^3 (n the longer side, m the shorter).  The epilogue does the sums, so that S and X are written once.
+// 4 m^2 n + 2 m^3 (n the longer side, m the shorter).  The epilogue does the sums, so that S and X are
+// written once.  Few and small matrices: tiles of 128 or 64 columns, all of them.
 //
 // What bounds it (GB300): the MMAs, at the clock that the power cap leaves.  64 of 2048 x 1408:
 // 4240 us, of them 650 the two passes ahead of the products (HBM: 12 bytes an element each); G
 // 192 us (17700 cycles a tile, 17000 of them MMAs), S 140, X 359 (14500 cycles; 11700).  16 of
 // 2048 x 7168: 5900 us, 710 ahead, G 310, S 97, X 585; all 4 m^2 n + 2 m^3 operations at a
-// library product's sustained rate would be 6400 us.  8 of 512 x 128: 104 us, 17
-// launches of one or two tiles a pair, 6 us each.
+// library product's sustained rate would be 6400 us.  8 of 512 x 128: 78 us, 17
+// launches of one tile a pair, 4.6 us each.
 // One kernel for all products, whose tiles wait for those that they need by counters in global
 // memory, was no faster (4670 us; 125 us): a tile's end is seen by the next one 5 us later.
 #include <stddef.h>
@@ -47,7 +48,7 @@ using namespace ptx;
 
 constexpr float kP0 = 3.4445f, kP1 = -4.7750f, kP2 = 2.0315f;
 
-constexpr int BT = 256;   // rows and columns of a pair's tile
+constexpr int BT = 256;   // rows and columns of a pair's tile (columns: or 128, 64)
 constexpr int BH = 128;   // rows of A and of B that a CTA of the pair holds
 constexpr int BK = 64;
 constexpr int UMMA_K = 16;
@@ -98,13 +99,14 @@ static_assert(kSmem <= 227 * 1024, "shared memory of one block");
 
 struct Dims {
     int E, K, m, n;  // products: contraction, rows and columns of an output
+    int wide;        // columns of a tile: BT, 128 or 64
 };
 
 __host__ __device__ __forceinline__ int blocks_of(int n, int size) { return (n + size - 1) / size; }
 
 // Columns that the MMAs of the last column block take, where there are 128 at most.
-__host__ __device__ __forceinline__ int last_columns(int n) {
-    const int rest = n - (n - 1) / BT * BT;
+__host__ __device__ __forceinline__ int last_columns(int n, int wide) {
+    const int rest = n - (n - 1) / wide * wide;
     return rest > BH ? BT : (rest + 31) / 32 * 32;
 }
 
@@ -112,14 +114,14 @@ struct Tile {
     int e, mb, nb;
 };
 
-// kSym: the tiles on and above the diagonal, column by column.  Else 8 row blocks by all
+// triangle: the tiles on and above the diagonal, column by column.  Else 8 row blocks by all
 // column blocks at a time, so that what runs side by side shares operands in L2.
-template <bool kSym>
-__device__ __forceinline__ Tile decode(long long tile, int per_matrix, int MB, int NB) {
+__device__ __forceinline__ Tile decode(long long tile, int per_matrix, int MB, int NB,
+                                       bool triangle) {
     Tile t;
     t.e = (int)(tile / per_matrix);
     const int i = (int)(tile - (long long)t.e * per_matrix);
-    if (kSym) {
+    if (triangle) {
         int c = (int)((sqrtf(8.0f * (float)i + 1.0f) - 1.0f) * 0.5f);
         while (c * (c + 1) / 2 > i) --c;
         while ((c + 1) * (c + 2) / 2 <= i) ++c;
@@ -171,7 +173,7 @@ __device__ __forceinline__ void tmem_ld_columns(uint32_t at, uint32_t (&v)[64]) 
 //   kLast    the same times 2^-p, bf16
 // with p0 + d as beta; kSpecial: with d by columns at `diag`, of which there are `left`, times
 // `unscale`.
-template <Form kForm, int kWarps, bool kSpecial>
+template <Form kForm, int kWarps, bool kSpecial, bool kMirrored>
 __device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLine<kWarps>],
                                         float alpha, float beta, float* diag, int at_diag, int left,
                                         float unscale) {
@@ -239,7 +241,7 @@ __device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLin
             }
             *lo_at = make_uint4(r[0], r[1], r[2], r[3]);
         }
-        if (kForm == kGram || kForm == kSquare) {
+        if (kMirrored) {
             // column c of the part is row c of its mirror image
             uint16_t* mirror = reinterpret_cast<uint16_t*>(second);
 #pragma unroll
@@ -252,8 +254,8 @@ __device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLin
 // Behind after_previous: lets the next kernel's blocks start on SMs that this one leaves idle or
 // is through with, where they set up their barriers and their TMEM and wait for this kernel's end.
 // All blocks have the kernel before behind them when they say so, so a kernel's start is still
-// the end of all but the one before it.  17 launches on each other's results, in a graph: 8 of
-// 512 x 128 117 -> 105 us, one of 1024 x 1024 176 -> 166, 8 of them 313 -> 300.  Products of many
+// the end of all but the one before it.  17 launches on each other's results, in a graph, on tiles
+// of 256 columns: 8 of 512 x 128 117 -> 105 us, one of 1024 x 1024 176 -> 166, 8 of them 313 -> 300.  Products of many
 // tiles a pair do without: 64 of 2048 x 1408 back to back 4750 -> 4830 to 4910 us with it.
 __device__ __forceinline__ void start_next() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -273,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
                         float beta, float unscale, float* diag, int* err) {
     constexpr bool kSym = kForm == kGram || kForm == kSquare;
     constexpr bool kWide = kMnB;  // kStep, kLast: S X (S's rows are X's), or else X S
-    constexpr int kL = kLine<kWarps>, kColumns = 4 * kL;  // of a line, of an epilogue warp
+    constexpr int kL = kLine<kWarps>;  // columns of a line
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t* tiles = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -285,11 +287,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
-    const int MB = blocks_of(d.m, BT), NB = blocks_of(d.n, BT), KB = blocks_of(d.K, BK);
-    const int per_matrix = kSym ? NB * (NB + 1) / 2 : MB * NB;
+    const int wide = kWarps == 4 ? BT : d.wide;
+    const bool triangle = kSym && wide == BT;
+    const int MB = blocks_of(d.m, BT), NB = blocks_of(d.n, wide), KB = blocks_of(d.K, BK);
+    const int per_matrix = triangle ? NB * (NB + 1) / 2 : MB * NB;
     const long long total = (long long)d.E * per_matrix;
     const int pairs = (int)(gridDim.x / 2);
-    const int n_last = last_columns(d.n);
+    const int n_last = last_columns(d.n, wide);
 
     if (warp == 4) {
         if (lane < kBarriers) {
@@ -324,9 +328,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
             uint32_t phase = 0;
             bool ok = true;
             for (long long i = blockIdx.x / 2; ok && i < total; i += pairs) {
-                const Tile t = decode<kSym>(i, per_matrix, MB, NB);
-                const int half = (t.nb == NB - 1 ? n_last : BT) / 2;
-                const int a0 = t.mb * BT + (int)rank * BH, b0 = t.nb * BT + (int)rank * half;
+                const Tile t = decode(i, per_matrix, MB, NB, triangle);
+                const int half = (t.nb == NB - 1 ? n_last : wide) / 2;
+                const int a0 = t.mb * BT + (int)rank * BH, b0 = t.nb * wide + (int)rank * half;
                 const bool two = half > 64;
                 const uint32_t tx = OP_BYTES + (kMnB && !two ? BOX_BYTES : OP_BYTES);
                 for (int kb = 0; kb < KB; ++kb) {
@@ -371,8 +375,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
             for (long long i = blockIdx.x / 2; ok && i < total; i += pairs) {
-                const Tile t = decode<kSym>(i, per_matrix, MB, NB);
-                const uint32_t idesc = kMajors | idesc_f16(BT, t.nb == NB - 1 ? n_last : BT);
+                const Tile t = decode(i, per_matrix, MB, NB, triangle);
+                const uint32_t idesc = kMajors | idesc_f16(BT, t.nb == NB - 1 ? n_last : wide);
                 if (!wait_bar(smem_u32(&ctl->tempty[acc]), acc_phase ^ 1u, abort_flag, err)) break;
                 tc_fence_after();
                 const uint32_t to = tmem + (uint32_t)(acc * BT);
@@ -408,16 +412,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
     } else {
         // ---------------- epilogue (both CTAs): own 128 rows ----------------
         const int q = warp & 3, part = (warp - 4) >> 2;  // TMEM lane quadrant, columns
+        const int columns = wide / (kWarps / 4);
         uint8_t* lines = staging_area + (size_t)(warp - 4) * (kStagingBytes / kWarps);
         const uint32_t lines_addr = smem_u32(lines), bar = smem_u32(&ctl->lines[warp - 4]);
         const uint32_t tempty0 = mapa_shared(smem_u32(&ctl->tempty[0]), 0);
         int acc = 0, buf = 0;
         uint32_t acc_phase = 0, lines_phase = 0;
         for (long long i = blockIdx.x / 2; i < total; i += pairs) {
-            const Tile t = decode<kSym>(i, per_matrix, MB, NB);
-            const int row = t.mb * BT + (int)rank * BH + q * 32, col = t.nb * BT + part * kColumns;
+            const Tile t = decode(i, per_matrix, MB, NB, triangle);
+            const int row = t.mb * BT + (int)rank * BH + q * 32, col = t.nb * wide + part * columns;
             // lines that there are
-            const int left = d.n - col < kColumns ? d.n - col : kColumns;
+            const int left = d.n - col < columns ? d.n - col : columns;
             const int have = row >= d.m || left <= 0 ? 0 : (left + kL - 1) / kL;
             // the inputs' lines c into buffer b, once what went out from there has been read
             const auto fetch = [&](int c, int b) {
@@ -440,7 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
             ok = __shfl_sync(0xffffffffu, ok, 0);
             tc_fence_after();
             if (!ok) break;
-            const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BT + part * kColumns);
+            const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BT + part * columns);
             const auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();
@@ -463,14 +468,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
                 if (c + 1 < have) fetch(c + 1, buf ^ 1);
                 uint8_t* mine = lines + buf * kBufferBytes<kWarps>;
                 const int first = col + c * kL;
-                if (kForm == kSquare && t.mb == t.nb)
-                    combine<kForm, kWarps, true>(mine, v, alpha, beta, diag_e + row + lane,
-                                                 row + lane < d.m ? row + lane - first : -1, 0, 0.0f);
+                const bool mirrored = triangle && t.mb != t.nb;
+                if (kForm == kSquare && first < row + 32 && row < first + kL)
+                    combine<kForm, kWarps, true, false>(mine, v, alpha, beta, diag_e + row + lane,
+                                                        row + lane < d.m ? row + lane - first : -1,
+                                                        0, 0.0f);
                 else if (kForm >= kStep && !kWide)
-                    combine<kForm, kWarps, true>(mine, v, alpha, beta, diag_e + first, 0,
-                                                 d.n - first, unscale);
+                    combine<kForm, kWarps, true, false>(mine, v, alpha, beta, diag_e + first, 0,
+                                                        d.n - first, unscale);
+                else if (kSym && mirrored)
+                    combine<kForm, kWarps, false, kSym>(mine, v, alpha, beta, nullptr, 0, 0, 0.0f);
                 else
-                    combine<kForm, kWarps, false>(mine, v, alpha, row_beta, nullptr, 0, 0, 0.0f);
+                    combine<kForm, kWarps, false, false>(mine, v, alpha, row_beta, nullptr, 0, 0, 0.0f);
                 fence_async_shared();
                 __syncwarp();
                 if (lane == 0) {
@@ -478,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + 32 * kWarps, 1
                     tma_store_3d(&tmOut, from, col + c * kL, row, t.e);
                     if (kForm == kStep)
                         tma_store_3d(&tmOut2, from + kLinesBytes<kWarps>, col + c * kL, row, t.e);
-                    if (kSym && t.mb != t.nb)
+                    if (mirrored)
                         tma_store_3d(&tmOut2, from + kLinesBytes<kWarps>, row, col + c * kL, t.e);
                     bulk_commit();
                 }
@@ -720,12 +729,21 @@ moe_status launch_form(const CUtensorMap& a, const CUtensorMap& b, const LineMap
 }
 template <Form kForm, bool kMnA, bool kMnB>
 moe_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const LineMaps (&l)[2],
-                          int now, const Dims& d, float alpha, float beta, float unscale,
-                          float* diag, int* err, cudaStream_t st) {
-    const long long MB = blocks_of(d.m, BT), NB = blocks_of(d.n, BT);
-    const long long tiles =
-        d.E * (kForm == kGram || kForm == kSquare ? NB * (NB + 1) / 2 : MB * NB);
-    const long long most = sm_count() / 2;
+                          int now, Dims d, float alpha, float beta, float unscale, float* diag,
+                          int* err, cudaStream_t st) {
+    constexpr bool kSym = kForm == kGram || kForm == kSquare;
+    const long long MB = blocks_of(d.m, BT), most = sm_count() / 2;
+    long long NB = blocks_of(d.n, BT);
+    // As narrow as lets all tiles run at once: the epilogue, a line of 32 columns after the other,
+    // is most of a short launch.  Symmetric products then make every tile.  With 256 columns, and
+    // so: 8 of 512 x 128 105, 78 us; one of 1024 x 1024 166, 115; 4 of 256 x 4096 207, 153; one of
+    // 1408 x 2048 211, 179.  Narrow tiles that run in turn gain nothing: one of 2048 x 2048 255, 281.
+    for (int wide = BT / 4; wide < BT && d.wide == BT; wide *= 2)
+        if (d.E * MB * blocks_of(d.n, wide) <= most) {
+            d.wide = wide;
+            NB = blocks_of(d.n, wide);
+        }
+    const long long tiles = d.E * (kSym && d.wide == BT ? NB * (NB + 1) / 2 : MB * NB);
     // 8 warps where a pair has no more than four tiles
     return tiles > 4 * most ? launch_form<kForm, kMnA, kMnB, 4>(a, b, l[0], now, d, alpha, beta,
                                                                 unscale, diag, err, most, st)
@@ -827,7 +845,7 @@ moe_status moe_muon_update(const void* grad, const float* momentum, const moe_mu
     }
     if (!ok) return MOE_ERR_UNSUPPORTED;
     const float scale = ldexpf(1.0f, -2 * p) * kSquareScale, back = 1.0f / kSquareScale;
-    const Dims gd = {s.E, longer, m, m}, sd = {s.E, m, m, m}, xd = {s.E, m, s.M, s.N};
+    const Dims gd = {s.E, longer, m, m, BT}, sd = {s.E, m, m, m, BT}, xd = {s.E, m, s.M, s.N, BT};
     for (int i = 0; i < s.steps; ++i) {
         const int now = i % 2;
         MOE_TRY(tall ? launch_product<kGram, true, true>(x_mn[now], x_mn[now], l, now, gd, scale,

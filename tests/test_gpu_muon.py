@@ -65,6 +65,18 @@ def test_sizes(E, M, N):
     check(grad, mom, shape, out, new)
 
 
+@pytest.mark.parametrize("E,M,N", [
+    (80, 8, 24), (80, 24, 8), (78, 40, 264), (78, 264, 40), (40, 264, 280), (30, 392, 520),
+    (30, 520, 392), (20, 264, 1032), (20, 1032, 264),
+])
+def test_sizes_of_many_matrices(E, M, N):
+    """Too many tiles for narrow ones: 256 columns, the symmetric products by half."""
+    shape = moe.MuonShape(E, M, N)
+    grad, mom = normal(1, E, M, N), normal(2, E, M, N, std=3.0)
+    out, new = run(grad, mom, shape)
+    check(grad, mom, shape, out, new)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("with_momentum,nesterov", [(True, True), (True, False), (False, True)])
 @pytest.mark.parametrize("M,N", [(96, 200), (200, 96)])
