@@ -22,41 +22,41 @@ DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
 def listed():
     return [
         # one decoding step of 16 sequences on the 64-expert layer: the matrices stream by
-        dict(name="gated forward decode 16", op="gated", dir="forward", N=16, k=6, E=64, H=2048,
+        dict(name="gated forward, decode 16", op="gated", dir="forward", N=16, k=6, E=64, H=2048,
              I=1408, keep=False, skew=0.0),
         # a microbatch of odd length of the same layer in training: gate and up columns are kept
-        dict(name="gated forward 4099 tokens", op="gated", dir="forward", N=4099, k=6, E=64,
+        dict(name="gated forward, 4099 tokens", op="gated", dir="forward", N=4099, k=6, E=64,
              H=2048, I=1408, keep=True, skew=0.0),
         # the Mixtral-shaped layer's full batch
-        dict(name="gated forward 8192 tokens", op="gated", dir="forward", N=8192, k=2, E=8,
+        dict(name="gated forward, 8192 tokens", op="gated", dir="forward", N=8192, k=2, E=8,
              H=4096, I=14336, keep=True, skew=0.0),
         # that microbatch of the 64-expert layer, backwards
-        dict(name="gated gradient 4099 tokens", op="gated", dir="grad", N=4099, k=6, E=64, H=2048,
+        dict(name="gated gradient, 4099 tokens", op="gated", dir="grad", N=4099, k=6, E=64, H=2048,
              I=1408, skew=0.0),
         # the Zipf-skewed layer's full batch, backwards: from a few rows to tens of thousands an
         # expert
-        dict(name="gated gradient 32768 tokens", op="gated", dir="grad", N=32768, k=8, E=128,
+        dict(name="gated gradient, 32768 tokens", op="gated", dir="grad", N=32768, k=8, E=128,
              H=4096, I=1536, skew=1.0),
         # the tiny layer's stacked gate and up matrices: launches count
-        dict(name="muon 8 of 512 x 128", op="muon", E=8, M=512, N=128, grad="fp32",
+        dict(name="muon, 8 of 512 x 128", op="muon", E=8, M=512, N=128, grad="fp32",
              momentum=True),
         # the 64-expert layer's down matrices
-        dict(name="muon 64 of 2048 x 1408", op="muon", E=64, M=2048, N=1408, grad="fp32",
+        dict(name="muon, 64 of 2048 x 1408", op="muon", E=64, M=2048, N=1408, grad="fp32",
              momentum=True),
         # 16 experts of the DeepSeek-V3-shaped layer: one matrix each
-        dict(name="muon 16 of 2048 x 7168", op="muon", E=16, M=2048, N=7168, grad="bf16",
+        dict(name="muon, 16 of 2048 x 7168", op="muon", E=16, M=2048, N=7168, grad="bf16",
              momentum=True),
         # one token of the DeepSeek-V3-shaped layer: 8 experts' down matrices
-        dict(name="w4 down 1 token", op="w4", gated=False, N=1, k=8, E=256, c_in=2048, c_out=7168,
+        dict(name="w4 down, 1 token", op="w4", gated=False, N=1, k=8, E=256, c_in=2048, c_out=7168,
              group=128, out="bf16", skew=0.0),
         # a decoding step of 16 sequences there: gate and up
-        dict(name="w4 gated 16 tokens", op="w4", gated=True, N=16, k=8, E=256, c_in=7168,
+        dict(name="w4 gated, 16 tokens", op="w4", gated=True, N=16, k=8, E=256, c_in=7168,
              c_out=2048, group=128, out="bf16", skew=0.0),
         # 64 sequences on the 64-expert layer, finer groups
-        dict(name="w4 gated 64 tokens", op="w4", gated=True, N=64, k=6, E=64, c_in=2048,
+        dict(name="w4 gated, 64 tokens", op="w4", gated=True, N=64, k=6, E=64, c_in=2048,
              c_out=1408, group=64, out="bf16", skew=0.0),
         # an odd, larger batch on the Mixtral-shaped layer: some 32 rows an expert
-        dict(name="w4 down 129 tokens", op="w4", gated=False, N=129, k=2, E=8, c_in=14336,
+        dict(name="w4 down, 129 tokens", op="w4", gated=False, N=129, k=2, E=8, c_in=14336,
              c_out=4096, group=128, out="fp32", skew=0.0),
     ]
 
