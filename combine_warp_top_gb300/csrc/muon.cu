@@ -550,7 +550,8 @@ __device__ __forceinline__ void update8(const G* grad, const float* buf, bool ne
 }
 
 // The new momentum and the sums of squares of u, one of each block (blockIdx.y: the matrix).
-// Squares of values from 2^64 on leave fp32: those are summed times 2^-128 besides.
+// Squares of values from 2^64 on, and sums of eight of them from some 2^62 on, leave fp32: all are
+// summed times 2^-132 besides, where eight squares of the largest fp32 number are below 2^127.
 template <typename G>
 __global__ void __launch_bounds__(kBlock)
     muon_momentum_kernel(const G* grad, const float* buf, float* new_buf, long long size,
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(kBlock)
             float s = 0.0f, t = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float small = u[j] * 0x1p-64f;
+                const float small = u[j] * 0x1p-66f;
                 s = fmaf(u[j], u[j], s);
                 t = fmaf(small, small, t);
             }
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kBlock)
             big += __shfl_xor_sync(0xffffffffu, big, o);
         }
         // in two factors: one alone may be too small for fp32
-        if (!(sum < 1e300)) sum = big * 0x1p128;
+        if (!(sum < 1e300)) sum = big * 0x1p132;
         int ex = 0;
         const double f = frexp(1.0 / (sqrt(sum) + (double)eps), &ex);
         if (threadIdx.x == 0) {
