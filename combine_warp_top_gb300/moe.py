@@ -888,15 +888,23 @@ class W4Matrices:
 
     def __init__(self, E: int, C_out: int, C_in: int, group: int, gated: bool, device="cuda"):
         self.E, self.C_out, self.C_in, self.group, self.gated = E, C_out, C_in, group, bool(gated)
-        n = int(load().moe_w4_packed_bytes(self.ref, E))
-        if n == 0:
+        if self.nbytes == 0:
             raise MoeError(1, "moe_w4_packed_bytes")
-        self.data = torch.empty(n, dtype=torch.uint8, device=device)
+        self.data = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
 
     @functools.cached_property
     def ref(self):
         """The C struct by reference, made once for these matrices."""
         return ctypes.byref(MoeW4Matrix(self.C_out, self.C_in, self.group, int(self.gated)))
+
+    @functools.cached_property
+    def nbytes(self) -> int:
+        """What the packed form of these matrices takes."""
+        return int(load().moe_w4_packed_bytes(self.ref, self.E))
+
+    def address(self):
+        """That of the packed form, once it is the device's and all there."""
+        return _exact(self.data, torch.uint8, (self.nbytes,), "w4")
 
     def __getstate__(self):
         """All but the reference: copies and pickles make their own."""
@@ -925,7 +933,7 @@ def moe_w4_pack(q, scales, w4: W4Matrices, stream=None):
     _check(load().moe_w4_pack(
         _exact(q, torch.uint8, (w4.E, rows, w4.C_in // 2), "q"),
         _exact(scales, torch.bfloat16, (w4.E, rows, w4.C_in // w4.group), "scales"),
-        w4.ref, w4.E, _exact(w4.data, torch.uint8, w4.data.shape, "w4"), _stream(stream)),
+        w4.ref, w4.E, w4.address(), _stream(stream)),
         "moe_w4_pack")
 
 
@@ -959,30 +967,31 @@ def w4_workspace(shape: Shape, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _w4(w4, shape: Shape, gated):
+def _check_w4(w4, shape: Shape, gated):
     if not isinstance(w4, W4Matrices):
         raise TypeError("w4: expected W4Matrices")
     if w4.E != shape.E or w4.gated != gated:
         raise ValueError(f"w4: expected {'gated' if gated else 'plain'} matrices of E = {shape.E}")
-    return w4.data.data_ptr()
 
 
 def moe_w4_gemm(rows, layout: Layout, shape: Shape, w4: W4Matrices, out, ws, stream=None):
     """out[i] = rows[i] W[e]^T; out [N*k, C_out] bf16 or fp32; ws of w4_workspace(shape)."""
-    at, ot, R = _w4(w4, shape, False), _out_type(out, "out"), shape.R
+    _check_w4(w4, shape, False)
+    ot, R = _out_type(out, "out"), shape.R
     _check(load().moe_w4_gemm(
         _exact(rows, torch.bfloat16, (R, w4.C_in), "rows"), _lay(layout, shape), shape.ref,
-        w4.ref, at, _exact(out, out.dtype, (R, w4.C_out), "out"), ot, *_bytes(ws),
+        w4.ref, w4.address(), _exact(out, out.dtype, (R, w4.C_out), "out"), ot, *_bytes(ws),
         _stream(stream)), "moe_w4_gemm")
 
 
 def moe_w4_gated_gemm(rows, layout: Layout, shape: Shape, w4: W4Matrices, topk_w, h, ws,
                       stream=None):
     """h[i] = w_i SiLU(g) u of [g | u] = rows[i] W[e]^T; h [N*k, C_out] bf16."""
-    at, R = _w4(w4, shape, True), shape.R
+    _check_w4(w4, shape, True)
+    R = shape.R
     _check(load().moe_w4_gated_gemm(
         _exact(rows, torch.bfloat16, (R, w4.C_in), "rows"), _lay(layout, shape), shape.ref,
-        w4.ref, at, _exact(topk_w, torch.float32, (shape.N, shape.k), "topk_w"),
+        w4.ref, w4.address(), _exact(topk_w, torch.float32, (shape.N, shape.k), "topk_w"),
         _exact(h, torch.bfloat16, (R, w4.C_out), "h"), *_bytes(ws), _stream(stream)),
         "moe_w4_gated_gemm")
 
@@ -1046,7 +1055,7 @@ class MoELayer:
                       quantize_w4(w_down, w4))
             for m, gated, size in ((w4[0], True, (shape.I, shape.H)),
                                    (w4[1], False, (shape.H, shape.I))):
-                _w4(m, shape, gated)
+                _check_w4(m, shape, gated)
                 if (m.C_out, m.C_in) != size:
                     raise ValueError(f"w4: expected matrices of {size}, got {(m.C_out, m.C_in)}")
             w_gate = w_up = w_down = None
