@@ -812,11 +812,19 @@ bool valid(const moe_w4_matrix* m) {
     return m && m->C_out > 0 && m->C_in > 0 &&
            (m->group == 32 || m->group == 64 || m->group == 128);
 }
-bool supported(const moe_w4_matrix* m) { return m->C_out % 8 == 0 && m->C_in % m->group == 0; }
+// Rows and columns, with what the last slab and chunk add to them and a gated matrix's two halves
+// as one, are 32 bits.
+constexpr int kMaxSide = 1 << 28;
+bool supported(const moe_w4_matrix* m) {
+    return m->C_out % 8 == 0 && m->C_in % m->group == 0 && m->C_out <= kMaxSide &&
+           m->C_in <= kMaxSide;
+}
 
+long long expert_bytes(const Matrix& d) { return (long long)d.slabs * d.chunks * d.record; }
+// 0: more than any memory has (and, from there on, more than 64 bits).
 long long packed_bytes(const moe_w4_matrix& m, int E) {
-    const Matrix d = matrix_of(m);
-    return (long long)E * d.slabs * d.chunks * d.record;
+    const long long one = expert_bytes(matrix_of(m));
+    return one > (1LL << 50) / E ? 0 : E * one;
 }
 
 template <int kN, int kGroup, bool kGated>
@@ -868,14 +876,15 @@ moe_status w4_product(const uint16_t* rows, const moe_layout* layout, const moe_
     if (!ws || ws_bytes < work.total) return MOE_ERR_WORKSPACE;
     if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
     const long long R = (long long)shape->N * shape->k;
-    if (R > INT32_MAX - (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (R > INT32_MAX - (1 << 20) || packed_bytes(*matrix, shape->E) == 0)
+        return MOE_ERR_UNSUPPORTED;
     if (R == 0) return MOE_OK;
     if (!rows || !packed || !out || !aligned16(rows, packed, out)) return MOE_ERR_INVALID_ARG;
     const GemmGroup g = routed_group(*layout, *shape, ws);
     Args a = {};
     a.packed = static_cast<const uint8_t*>(packed);
     a.m = matrix_of(*matrix);
-    a.expert_bytes = (long long)a.m.slabs * a.m.chunks * a.m.record;
+    a.expert_bytes = expert_bytes(a.m);
     a.gate = Gate{topk_w,  layout->row_token, layout->pair_row, shape->N, shape->k,
                   gated ? static_cast<uint16_t*>(out) : nullptr, nullptr, nullptr, nullptr};
     a.out = out;
@@ -934,8 +943,9 @@ moe_status moe_w4_pack(const uint8_t* q, const uint16_t* scales, const moe_w4_ma
     MOE_RANGE();
     if (!valid(matrix) || E <= 0) return MOE_ERR_INVALID_ARG;
     if (!supported(matrix) || E > kMaxE) return MOE_ERR_UNSUPPORTED;
-    if (!q || !scales || !packed || !aligned16(q, scales, packed)) return MOE_ERR_INVALID_ARG;
     const long long pieces = packed_bytes(*matrix, E) / 16;
+    if (pieces == 0) return MOE_ERR_UNSUPPORTED;
+    if (!q || !scales || !packed || !aligned16(q, scales, packed)) return MOE_ERR_INVALID_ARG;
     const long long blocks = (pieces + kBlock - 1) / kBlock, most = 1LL << 20;
     return cuda_status(launch_chained(w4_pack_kernel, (int)(blocks < most ? blocks : most), kBlock,
                                       0, as_stream(stream), q, scales, matrix_of(*matrix), pieces,

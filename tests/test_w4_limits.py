@@ -1,5 +1,6 @@
 """Refusals of the 4-bit products and of the helpers that make their weights: answered on the
 host, before anything is launched."""
+import ctypes
 import types
 
 import pytest
@@ -8,6 +9,8 @@ import torch
 from combine_warp_top_gb300 import build as libbuild
 from combine_warp_top_gb300 import moe
 
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+OK16 = ctypes.c_void_p(0x10000)  # never dereferenced on the host
 bf = torch.bfloat16
 
 
@@ -62,3 +65,34 @@ def test_packed_weights_are_checked_like_other_operands(lib, monkeypatch):
         w4.data = on_device(size, dtype=torch.uint8)
         product()
         assert calls.pop()
+
+
+@pytest.mark.parametrize("gated", [0, 1])
+@pytest.mark.parametrize("C_out,C_in", [
+    (1 << 30, 32), ((1 << 28) + 8, 128), (2 ** 31 - 8, 64), (8, (1 << 28) + 128),
+    (8, 2 ** 31 - 128), (1 << 28, 1 << 28), (1 << 27, 1 << 24),
+])
+def test_sides_past_those_that_are_counted_in_32_bits(lib, C_out, C_in, gated):
+    """Twice C_out from 2^30 on is negative, and so are the rows of a last slab and the weights of
+    a last chunk near 2^31: the largest sides are refused, as is more than 64 bits of bytes.  A call
+    that passes the check of its sizes stops at the missing weights."""
+    s = moe.Shape(4, 64, 1024, 2, 1, 64)
+    lay = ctypes.byref(moe.MoeLayout(*([0x20000] * len(moe.LAYOUT_FIELDS))))
+    n = moe.moe_w4_workspace_bytes(s)
+
+    def calls(C_out, C_in):
+        m = ctypes.byref(moe.MoeW4Matrix(C_out, C_in, 32, gated))
+        yield lib.moe_w4_pack(OK16, OK16, m, 1024, None, None)
+        if gated:
+            yield lib.moe_w4_gated_gemm(OK16, lay, s.ref, m, None, None, OK16, OK16, n, None)
+        else:
+            yield lib.moe_w4_gemm(OK16, lay, s.ref, m, None, OK16, 0, OK16, n, None)
+
+    m = ctypes.byref(moe.MoeW4Matrix(C_out, C_in, 32, gated))
+    assert lib.moe_w4_packed_bytes(m, 1024) == 0
+    assert list(calls(C_out, C_in)) == [UNSUPPORTED, UNSUPPORTED]
+    assert list(calls(1 << 28, 32)) == [INVALID, INVALID]
+    assert list(calls(8, 1 << 28)) == [INVALID, INVALID]
+    # one expert's may be as large as a gated block's
+    one = ctypes.byref(moe.MoeW4Matrix(1 << 28, 32, 32, gated))
+    assert lib.moe_w4_packed_bytes(one, 1) == (1 << 28) * (1 + gated) // 32 * (32 * 64 + 32 * 2 * 4)
