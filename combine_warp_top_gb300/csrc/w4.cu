@@ -389,8 +389,11 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
         tmem_relinquish();
     }
     after_previous();
-    // prefix[e]: passes before expert e; each thread sums a run of experts
+    // prefix[e]: passes before expert e; each thread sums a run of experts.  Only a layout whose
+    // segments overlap has more of them than `most`: it gets one more and is reported, so that the
+    // sums do not wrap.
     const int per = ceil_div(a.E, kThreads), e0 = threadIdx.x * per;
+    const int most = a.R / kN + a.E;
     int mine = 0;
     const auto passes = [&](int e) {
         const int off = a.offsets[e], cnt = a.counts[e];
@@ -400,25 +403,31 @@ __global__ void __launch_bounds__(kThreads, (Form<kN, kGroup>::kBlocks))
         }
         return ceil_div(cnt, kN);
     };
-    for (int e = e0; e < e0 + per && e < a.E; ++e) mine += passes(e);
+    const auto sum = [&](int x, int y) { return min(x + y, most + 1); };
+    for (int e = e0; e < e0 + per && e < a.E; ++e) mine = sum(mine, passes(e));
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        if (lane >= o) incl = sum(incl, v);
     }
     if (lane == 31) run_sums[warp] = incl;
+    int before = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 0) before = 0;
     __syncthreads();
-    int before = incl - mine, all_passes = 0;
+    int all_passes = 0;
     for (int i = 0; i < kThreads / 32; ++i) {
-        if (i < warp) before += run_sums[i];
-        all_passes += run_sums[i];
+        if (i < warp) before = sum(before, run_sums[i]);
+        all_passes = sum(all_passes, run_sums[i]);
     }
     for (int e = e0; e < e0 + per && e < a.E; ++e) {
         prefix[e] = before;
-        before += passes(e);
+        before = sum(before, passes(e));
     }
-    if (threadIdx.x == 0) prefix[a.E] = all_passes;
+    if (threadIdx.x == 0) {
+        prefix[a.E] = all_passes;
+        if (all_passes > most) set_error(a.err, MOE_ERR_INVALID_ARG);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

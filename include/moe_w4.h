@@ -50,7 +50,8 @@ moe_status moe_w4_pack(const uint8_t* q, const uint16_t* scales, const moe_w4_ma
  * 2^31 - 2^20.
  * ws: workspace of moe_w4_workspace_bytes(shape) bytes, 16-byte aligned, zero at first.  A
  * layout whose segments leave the N*k rows is reported there (moe_get_error) and those
- * segments are taken as empty.  After MOE_ERR_TIMEOUT it has to be zeroed again. */
+ * segments are taken as empty; one whose segments overlap may be reported, too, and leave rows
+ * without their products.  After MOE_ERR_TIMEOUT it has to be zeroed again. */
 size_t moe_w4_workspace_bytes(const moe_shape* shape);
 moe_status moe_w4_gemm(const uint16_t* rows, const moe_layout* layout, const moe_shape* shape,
                        const moe_w4_matrix* matrix, const void* packed, void* out,
