@@ -217,6 +217,20 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _hand_over(stream, *tensors):
+    """For tensors made here, on the current stream, and written or read on another one: that one
+    waits for what the current stream still does with their memory, which may have been another
+    tensor's, and their memory is no one else's before it is through with them."""
+    if stream is None:
+        return
+    current = torch.cuda.current_stream(tensors[0].device)
+    if stream.cuda_stream == current.cuda_stream:
+        return
+    stream.wait_stream(current)
+    for t in tensors:
+        t.record_stream(stream)
+
+
 # ---- shapes, layouts, buffers ----------------------------------------------------------
 
 @dataclass(frozen=True)
@@ -943,6 +957,7 @@ def pack_w4(q, scales, gated=False, stream=None) -> W4Matrices:
         raise ValueError("q and scales: expected [E, rows, C_in / 2] and [E, rows, C_in / group]")
     E, rows, ci = q.shape[0], q.shape[1], q.shape[2] * 2
     w4 = W4Matrices(E, rows // 2 if gated else rows, ci, ci // scales.shape[2], gated, q.device)
+    _hand_over(stream, w4.data)
     moe_w4_pack(q, scales, w4, stream)
     return w4
 
@@ -952,6 +967,7 @@ def quantize_w4(w, group=128, gated=False, stream=None) -> W4Matrices:
     E, rows, ci = w.shape
     q = torch.empty(E, rows, ci // 2, dtype=torch.uint8, device=w.device)
     scales = torch.empty(E, rows, ci // group, dtype=torch.bfloat16, device=w.device)
+    _hand_over(stream, q, scales)
     moe_w4_quantize(w, q, scales, stream)
     return pack_w4(q, scales, gated, stream)
 

@@ -41,3 +41,43 @@ def test_the_most_passes_that_a_layout_can_have(E, rows):
     counts[-1] = rows - sum(counts)
     c = Case(rows, E, 1, 256, 40, 64, False, seed=4, counts=counts)
     c.check(c.run())
+
+
+def test_weights_made_on_another_stream():
+    """The helpers' own memory: nothing that the current stream still does to what was there
+    before reaches them, and nothing gets it before the other stream is through."""
+    E, rows, c_in, group = 4, 520, 1024, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    w = torch.randn(E, rows, c_in, generator=g, device="cuda").to(bf)
+    want = moe.quantize_w4(w, group).data.clone()
+    q = torch.empty(E, rows, c_in // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(E, rows, c_in // group, dtype=bf, device="cuda")
+    moe.moe_w4_quantize(w, q, scales)
+    side = torch.cuda.Stream()
+    sizes = [q.nbytes, scales.nbytes, want.nbytes]
+    wait = 40_000_000  # cycles, 20 ms
+
+    def make(packing):
+        return (moe.pack_w4(q, scales, stream=side) if packing
+                else moe.quantize_w4(w, group, stream=side))
+
+    for packing in (False, True):
+        torch.cuda.synchronize()
+        # the memory is free and not yet written by the current stream
+        junk = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+        torch.cuda._sleep(wait)
+        for t in junk:
+            t.fill_(170)
+        del junk, t
+        w4 = make(packing)
+        torch.cuda.synchronize()
+        assert torch.equal(w4.data, want)
+        # the other stream is late
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(wait)
+        w4 = make(packing)
+        junk = [torch.full((n,), 170, dtype=torch.uint8, device="cuda") for n in sizes]
+        torch.cuda.synchronize()
+        assert torch.equal(w4.data, want)
+        del junk
