@@ -963,8 +963,13 @@ def pack_w4(q, scales, gated=False, stream=None) -> W4Matrices:
 
 
 def quantize_w4(w, group=128, gated=False, stream=None) -> W4Matrices:
-    """bf16 matrices [E, rows, C_in], quantised by groups and packed."""
+    """bf16 matrices [E, rows, C_in], quantised by groups (32, 64 or 128, of which C_in is a
+    multiple) and packed."""
     E, rows, ci = w.shape
+    # the calls below take the group from the scales' size: another would pass for one of these
+    if group not in (32, 64, 128) or ci % group != 0:
+        raise ValueError(f"group: expected 32, 64 or 128, of which {ci} columns are a multiple, "
+                         f"got {group}")
     q = torch.empty(E, rows, ci // 2, dtype=torch.uint8, device=w.device)
     scales = torch.empty(E, rows, ci // group, dtype=torch.bfloat16, device=w.device)
     _hand_over(stream, q, scales)

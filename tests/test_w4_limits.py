@@ -96,3 +96,18 @@ def test_sides_past_those_that_are_counted_in_32_bits(lib, C_out, C_in, gated):
     # one expert's may be as large as a gated block's
     one = ctypes.byref(moe.MoeW4Matrix(1 << 28, 32, 32, gated))
     assert lib.moe_w4_packed_bytes(one, 1) == (1 << 28) * (1 + gated) // 32 * (32 * 64 + 32 * 2 * 4)
+
+
+@pytest.mark.parametrize("C_in,group", [
+    (128, 96), (128, 48), (7168, 127), (64, 128), (160, 64), (96, 128), (128, 0), (128, -64),
+    (128, 16), (256, 256), (128, 64.5), (192, 128),
+])
+def test_groups_are_those_asked_for(lib, monkeypatch, C_in, group):
+    """No other group stands in for one that the products do not have, here or in a layer."""
+    monkeypatch.setattr(moe, "load", lambda: pytest.fail("reached the library"))
+    with pytest.raises(ValueError, match="group: expected 32, 64 or 128"):
+        moe.quantize_w4(torch.zeros(2, 8, C_in, dtype=bf), group)
+    s = moe.Shape(4, C_in, 2, 1, 1, 128)
+    gate, down = torch.zeros(2, 128, C_in, dtype=bf), torch.zeros(2, C_in, 128, dtype=bf)
+    with pytest.raises(ValueError, match="group: expected 32, 64 or 128"):
+        moe.MoELayer(s, gate, gate, down, device="cpu", w4=group)
