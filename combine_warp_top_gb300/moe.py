@@ -1111,12 +1111,14 @@ class MoELayer:
         # the expert FFN as one kernel (h on chip), unless the combine is to go
         # into the down GEMM's epilogue
         self.fused_ffn = moe_layer_fuses_ffn(shape) and not fuse_combine and w4 is None
-        self.xd = torch.empty(1 if self.fused_dispatch else max(rows_d, 1), H, **bf)
+        # 4-bit experts' products take their rows as they are, none of an empty batch
+        least = 1 if w4 is None else 0
+        self.xd = torch.empty(1 if self.fused_dispatch else max(rows_d, least), H, **bf)
         # the dedup expansion happens inside the gate/up GEMM, but for 4-bit experts
-        self.xe = (torch.empty(max(shape.R, 1), H, **bf) if w4 is not None and shape.dedup
+        self.xe = (torch.empty(shape.R, H, **bf) if w4 is not None and shape.dedup
                    else None)
-        self.h = torch.empty(max(shape.R, 1), I, **bf)
-        self.y = torch.empty(max(shape.R, 1), H, **bf)
+        self.h = torch.empty(max(shape.R, least), I, **bf)
+        self.y = torch.empty(max(shape.R, least), H, **bf)
         # the dedup combine keeps its partial rows in registers (moe_combine with
         # partial = NULL); a caller who wants them written passes its own buffer
         self.partial = None

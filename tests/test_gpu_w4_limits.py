@@ -81,3 +81,21 @@ def test_weights_made_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(w4.data, want)
         del junk
+
+
+@pytest.mark.parametrize("W,dedup,with_shared", [(1, False, False), (4, True, False), (1, False, True)])
+def test_layer_of_an_empty_batch_is_a_noop(W, dedup, with_shared):
+    E, H, I = 8, 128, 64
+    shape = moe.Shape(0, H, E, 2, W, I, dedup=dedup)
+    w = [torch.zeros(E, a, b, dtype=bf, device="cuda") for a, b in ((I, H), (I, H), (H, I))]
+    shared = [t[0].contiguous() for t in w] if with_shared else None
+    layer = moe.MoELayer(shape, *w, w4=64, shared=shared)
+    x = torch.empty(0, H, dtype=bf, device="cuda")
+    layer.out.fill_(7.0)
+    for res in (None, x):
+        out = layer.forward(torch.empty(0, E, device="cuda"), x, res)
+        torch.cuda.synchronize()
+        assert (out == 7.0).all()
+    layer.check_device_errors()
+    assert layer.kernel_launches_per_step() == 0
+    assert (layer.layout["expert_counts"] == 0).all()
