@@ -222,7 +222,8 @@ def main(steps=60, N=512, H=256, E=8, k=2, I=512, optimizer="sgd"):
             block.sgd(0.05)
         if step % 10 == 0 or step == steps - 1:
             print(f"step {step:3d}  loss {losses[-1]:.4f}", flush=True)
-    assert moe.moe_get_error(block.ws) == 0 and moe.moe_get_error(block.dense_ws) == 0
+    used = [block.ws, block.dense_ws] + ([block.muon_ws] if block.momenta is not None else [])
+    assert all(moe.moe_get_error(ws) == 0 for ws in used)
     return losses
 
 
