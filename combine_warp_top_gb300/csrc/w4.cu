@@ -796,9 +796,21 @@ __global__ void __launch_bounds__(kBlock)
 // ---- host -----------------------------------------------------------------------------------
 
 // Rows of a pass, by the experts' average: 16 take the least time for a chunk, and an expert with
-// more of them than a pass has its weights widened once for each.  32 experts of 4096 x 2816, us
-// with 16, 32 and 64 rows a pass: 8 rows an expert 50, 51, 68; 12 rows 53, 53, 72; 24 rows 84, 58,
-// 82; 32 rows 101, 75, 85; 48 rows 130, 95, 90.
+// more of them than a pass has its weights widened once for each.  So the changes lie where many
+// experts come to need a second pass: at the pass's own size where all have the same rows, before it
+// where rows are drawn at random, and later (with less between the two) where some experts have
+// several times the rows of others.  32 experts of 4096 x 2816, groups of 128, us in a graph with
+// 16 and with 32 rows a pass:
+//   rows an expert      8         12         14         16         20         24
+//   all the same     56, 56     56, 58     56, 58     58, 58     89, 60     89, 62
+//   at random        56, 56     58, 58     64, 59     72, 60     80, 61     89, 62
+//   uneven           58, 58     64, 58     65, 59     70, 62     76, 64     87, 67
+// and with 32 and with 64:
+//   rows an expert     28         32         36         40         44         48
+//   all the same     62, 72     64, 72     95, 78     95, 78     97, 80     95, 80
+//   at random        68, 76     76, 78     89, 78     93, 80     96, 82     97, 82
+//   uneven           72, 83     76, 87     81, 89     85, 91     89, 91     97, 93
+// (uneven: shares of 1 / sqrt(i)).  8 of 14336 x 4096 and 64 of 2048 x 2 x 1408, gated: the same.
 int pass_rows(long long R, int E) {
     const long long used = R < E ? R : E;
     const double mean = used > 0 ? (double)R / (double)used : 0.0;
