@@ -11,12 +11,13 @@
 // What is rounded.  The products' operands are fp16 (11 bits), scaled so that none of their
 // numbers that matter is a denormal: X as an operand, G and S; their sums are fp32.  Every step
 // multiplies small singular values by 3.4445, and what a rounding has put in their place with
-// them, so X in its own place in the sum, p0 X, is kept in two fp16 halves (22 bits): rounded to
-// one, a gradient of rank 16 over noise would end 3.8e-2 of its norm from the 64-bit result (bf16
-// operands and X: 0.3).  And S, near the end some -2.7 I and little beside it, goes apart: its
+// them, so X in its own place in the sum, p0 X, is kept in two fp16 halves (22 bits; the second one
+// times 2^11): rounded to one, a gradient of rank 16 over noise would end 3.8e-2 of its norm from
+// the 64-bit result (bf16 operands and X: 0.3).  And S, near the end some -2.7 I and little beside it, goes apart: its
 // diagonal d, fp32, to p0, the rest into the product, whose roundings are then those of the
-// little.  Together 4e-4 to 1.4e-3 of the result's norm (with S whole up to 2.2e-3); the output's
-// own rounding to bf16 is 1.7e-3.
+// little.  Together 4e-4 to 1.5e-3 of the result's norm (with S whole up to 2.2e-3); the output's
+// own rounding to bf16 is 1.7e-3.  The largest are gradients of rank 1: 264 x 264 1.5e-3, 8192 x 8192
+// 1.2e-3 (2.0e-3 with an unscaled second half, which is a denormal there).
 //
 // Three products a step, on 256 x 256 tiles of a CTA pair (tcgen05, two accumulators in TMEM, 5
 // stages of 32 KB).  G and S are symmetric: only tiles on and above the diagonal are made, each
@@ -78,6 +79,9 @@ constexpr int kMaxDim = 65536;
 // G and S are kept times 2^12, X times 2^p with 2^p about the root of its longer side, so
 // that entries far below the largest are normal fp16 numbers.
 constexpr float kSquareScale = 4096.0f;
+// X's second half is kept times 2^11, which makes it the size of the first: unscaled it would be a
+// denormal where X's entries are below 2^-3 (sides of hundreds), and X have fewer bits.
+constexpr float kLowScale = 2048.0f;
 
 // The three products of a step, and the last one of all.
 enum Form { kGram, kSquare, kStep, kLast };
@@ -169,7 +173,7 @@ __device__ __forceinline__ void tmem_ld_columns(uint32_t at, uint32_t (&v)[64]) 
 //   kGram    G = acc * 2^(12 - 2p), and its mirror image
 //   kSquare  S = p1 G + p2 acc * 2^-12, likewise; kSpecial: with the column `at_diag` of this row
 //            taken out (into *diag), if it is one of these
-//   kStep    x = (p0 + d) (hi + lo) + acc * 2^-12, into hi and lo
+//   kStep    x = (p0 + d) (hi + lo 2^-11) + acc * 2^-12, into hi and lo
 //   kLast    the same times 2^-p, bf16
 // with p0 + d as beta; kSpecial: with d by columns at `diag`, of which there are `left`, times
 // `unscale`.
@@ -210,8 +214,8 @@ __device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLin
                 float2 x = unpack_half2(w[j]);
                 if (kForm != kSquare) {
                     const float2 y = unpack_half2(l[j]);
-                    x.x += y.x;
-                    x.y += y.y;
+                    x.x = fmaf(1.0f / kLowScale, y.x, x.x);
+                    x.y = fmaf(1.0f / kLowScale, y.y, x.y);
                 }
                 f[2 * j] = fmaf(b[2 * j], x.x, f[2 * j]);
                 f[2 * j + 1] = fmaf(b[2 * j + 1], x.y, f[2 * j + 1]);
@@ -237,7 +241,7 @@ __device__ __forceinline__ void combine(uint8_t* lines, const uint32_t (&v)[kLin
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 x = unpack_half2(o[j]);
-                r[j] = pack_half2(f[2 * j] - x.x, f[2 * j + 1] - x.y);
+                r[j] = pack_half2(kLowScale * (f[2 * j] - x.x), kLowScale * (f[2 * j + 1] - x.y));
             }
             *lo_at = make_uint4(r[0], r[1], r[2], r[3]);
         }
@@ -618,7 +622,7 @@ __global__ void __launch_bounds__(kBlock)
     }
 }
 
-// X = u 2^p / (|u| + eps) as hi + lo.
+// X = u 2^p / (|u| + eps) as hi + lo 2^-11.
 template <typename G>
 __global__ void __launch_bounds__(kBlock)
     muon_scale_kernel(const G* grad, const float* buf, long long size, bool nesterov, float beta,
@@ -660,7 +664,7 @@ __global__ void __launch_bounds__(kBlock)
             const float a = u[2 * j] * f0 * f1, b = u[2 * j + 1] * f0 * f1;
             h[j] = pack_half2(a, b);
             const float2 r = unpack_half2(h[j]);
-            l[j] = pack_half2(a - r.x, b - r.y);
+            l[j] = pack_half2(kLowScale * (a - r.x), kLowScale * (b - r.y));
         }
         *reinterpret_cast<uint4*>(hi + at + i) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4*>(lo + at + i) = make_uint4(l[0], l[1], l[2], l[3]);

@@ -210,7 +210,8 @@ size_t moe_muon_workspace_bytes(const moe_muon_shape* shape);
  * 1.2 where those of u are not far below its norm; new_momentum, fp32 [E, M, N], b' (may
  * be momentum itself; both NULL: no momentum).  The products take X, G and the sum in
  * brackets without its diagonal rounded to fp16; X in its place in the sum is two of them
- * (22 bits), the diagonal and all sums are fp32.  A matrix with an infinity or a NaN in u makes its own update NaN, no other's. */
+ * (22 bits), the diagonal and all sums are fp32.  A matrix with an infinity or a NaN in u makes
+ * its own update NaN, no other's. */
 moe_status moe_muon_update(const void* grad, const float* momentum, const moe_muon_shape* shape,
                            uint16_t* update, float* new_momentum, void* ws, size_t ws_bytes,
                            void* stream);

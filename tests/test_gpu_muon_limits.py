@@ -40,3 +40,27 @@ def test_momentum_near_the_end_of_the_range():
     grad, mom = sign * 1e38, sign * 5e37
     out, new = run(grad, mom, shape)
     check(grad, mom, shape, out, new)
+
+
+@pytest.mark.parametrize("M,N", [(8, 24), (264, 1032), (1032, 264), (2048, 2048), (4096, 7168)])
+@pytest.mark.parametrize("spread", [1.0, 1e-3])
+def test_scaled_matrices_have_22_bits(M, N, spread):
+    """A workspace ends with X's first halves, two copies, and its second ones times 2^11; a call of
+    one step leaves those of u 2^p / (|u| + eps) there.  The second half is what the first leaves,
+    2^-11 of x at most, rounded to fp16: 2^-11 of that, or 2^-25 of its unit, 2^-11.  x itself is two
+    fp32 products with factors rounded to fp32: 2^-22.  spread: rows far below the others."""
+    shape = moe.MuonShape(2, M, N, steps=1)
+    grad = normal(4, 2, M, N)
+    grad[:, 1::2] *= spread
+    ws, out = moe.muon_workspace(shape), torch.empty(2, M, N, dtype=torch.bfloat16, device="cuda")
+    moe.moe_muon_update(grad, None, shape, out, ws)
+    part = (2 * 2 * M * N + 255) // 256 * 256
+    hi, lo = (ws[at:at + 2 * 2 * M * N].view(torch.float16).double().view(2, M, N)
+              for at in (ws.numel() - 3 * part, ws.numel() - part))
+    p = 0
+    while 1 << 2 * p + 1 < max(M, N):
+        p += 1
+    g = grad.double()
+    x = g * 2.0 ** p / (g.square().sum((1, 2), keepdim=True).sqrt() + shape.eps)
+    off = (hi + lo * 2.0 ** -11 - x).abs()
+    assert ((off - 2.0 ** -21 * x.abs() - 2.0 ** -36) <= 0).all()
