@@ -75,16 +75,17 @@ __device__ __forceinline__ void warp_mblk_prefix(const int* cnts, int E, int bm,
     if (lane == 31) prefix[E] = incl;
 }
 
-// The blocks of a kernel launched by launch_chained start when those of the kernel before
-// it on the stream are through, before their writes have all landed; what they do ahead of
-// this touches no memory that another kernel writes, and no load of such a kernel is a
-// read-only one (the data may change after its start).  Every block calls it, so that a
-// kernel's end is the end of all kernels before it.
+// The blocks of a kernel launched by launch_chained may start while the kernel before it on the
+// stream still runs: when its blocks are through, or when all of them have let the next kernel
+// start (launch_dependents).  This wait, for that kernel's end and its writes, is what orders memory:
+// what a block does ahead of it touches no memory that another kernel writes, and no load of such
+// a kernel is a read-only one (the data may change after its start).  Every block calls it, so that
+// a kernel's end is the end of all kernels before it.
 // Kernels back to back: block norm of 4096 x 7168 63.7 -> 61.0 us, its gradient of 8192 x
-// 4096 75.4 -> 72.7 us, router gradient of 32768 x 256 12.7 -> 10.8 us.  Letting the next
-// kernel's blocks start while this one's still run as well (launch_dependents) gives a
-// further 1 us to some of them and takes it elsewhere: norm gradients of 8192 x 2048 43 ->
-// 53 us, a training step of 64 experts (4096 tokens, 2048 wide) 1430 -> 1450 us.
+// 4096 75.4 -> 72.7 us, router gradient of 32768 x 256 12.7 -> 10.8 us.  launch_dependents gives a
+// further 1 us to some of the training step's kernels and takes it elsewhere (norm gradients of
+// 8192 x 2048 43 -> 53 us, a training step of 64 experts, 4096 tokens, 2048 wide 1430 -> 1450 us): none
+// of them has it.  Muon's short products have (muon.cu, start_next).
 __device__ __forceinline__ void after_previous() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }

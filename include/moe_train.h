@@ -8,8 +8,10 @@
  * No call here uses atomics whose order could change a result: every output is
  * the same from run to run on one GPU model.
  * The kernels are launched with programmatic stream serialization: their blocks
- * may start when those of the kernel before them on the stream are through, and
- * wait for its writes before they touch memory.
+ * may start before the kernel before them on the stream has ended, and wait for
+ * its end (griddepcontrol.wait) before they touch memory.  Those of moe_muon_update let the next
+ * such kernel on the stream, the caller's own too, start while they still compute: that wait, or a
+ * launch without the attribute, is what orders memory.
  */
 #ifndef MOE_TRAIN_H
 #define MOE_TRAIN_H

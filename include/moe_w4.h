@@ -34,7 +34,8 @@ moe_status moe_w4_quantize(const uint16_t* w, int64_t rows, int32_t C_in, int32_
 
 /* The order in which the products read E such matrices (q and scales as above, of any
  * origin), once for each set of weights: packed, moe_w4_packed_bytes bytes (0 if the matrix
- * is invalid), 4 bits a weight and its scales. */
+ * is invalid), 4 bits a weight and its scales.  256 gate and up matrices of 4096 x 7168 in groups
+ * of 128: 8.3 ms to quantise, 19 ms to pack (GB300). */
 size_t moe_w4_packed_bytes(const moe_w4_matrix* matrix, int32_t E);
 moe_status moe_w4_pack(const uint8_t* q, const uint16_t* scales, const moe_w4_matrix* matrix,
                        int32_t E, void* packed, void* stream);
@@ -46,8 +47,10 @@ moe_status moe_w4_pack(const uint8_t* q, const uint16_t* scales, const moe_w4_ma
  * rows bf16 [N*k, C_in]; out of out_type, a moe_type; w_i as in moe_swiglu (topk_w NULL:
  * ones).  Products of bf16 rows with the whole numbers q - 8 are summed in fp32 over a group
  * and scaled then, in fp32.  shape gives N, k and E; rows an expert has: any number, but it
- * is few that this is made for (64 at a time read the weights again).  N*k is less than
- * 2^31 - 2^20.
+ * is few that this is made for.  An expert's rows go through in passes of 16, 32 or 64 (of 32 at
+ * most with groups of 32), chosen once a call by the average of N*k rows over the experts, and
+ * every pass reads and widens the expert's weights again: from some hundred rows an expert on,
+ * products with bf16 weights are faster.  N*k is less than 2^31 - 2^20.
  * ws: workspace of moe_w4_workspace_bytes(shape) bytes, 16-byte aligned, zero at first.  A
  * layout whose segments leave the N*k rows is reported there (moe_get_error) and those
  * segments are taken as empty; one whose segments overlap may be reported, too, and leave rows
