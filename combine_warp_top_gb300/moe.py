@@ -367,6 +367,7 @@ def pack_weights(shape: Shape, w_gate, w_up, w_down, stream=None):
     dev = w_gate.device
     gu = torch.empty(moe_packed_gate_up_bytes(s) // 2, dtype=torch.bfloat16, device=dev)
     dn = torch.empty(moe_packed_down_bytes(s) // 2, dtype=torch.bfloat16, device=dev)
+    _hand_over(stream, gu, dn)
     moe_pack_weights(w_gate, w_up, w_down, s, gu, dn, stream)
     return gu, dn
 
