@@ -1267,12 +1267,13 @@ class MoELayer:
         run moe_layer_forward, copy the output device->host, all on one stream.
         Host tensors should be pinned for the copies to be asynchronous."""
         st = torch.cuda.current_stream() if stream is None else stream
-        if dev_inputs is None:
-            dev_inputs = (torch.empty_like(logits_h, device="cuda"),
-                          torch.empty_like(x_h, device="cuda"),
-                          None if residual_h is None else torch.empty_like(residual_h, device="cuda"))
-        L_d, x_d, r_d = dev_inputs
         with torch.cuda.stream(st):
+            if dev_inputs is None:  # memory of the stream that uses it
+                dev_inputs = (torch.empty_like(logits_h, device="cuda"),
+                              torch.empty_like(x_h, device="cuda"),
+                              None if residual_h is None
+                              else torch.empty_like(residual_h, device="cuda"))
+            L_d, x_d, r_d = dev_inputs
             L_d.copy_(logits_h, non_blocking=True)
             x_d.copy_(x_h, non_blocking=True)
             if residual_h is not None:

@@ -33,3 +33,34 @@ def test_weights_packed_on_another_stream():
     junk = [torch.full_like(t, 7.0) for t in want]
     torch.cuda.synchronize()
     assert all((t == 7.0).all() for t in junk)
+
+
+def test_host_step_on_another_stream():
+    """The inputs' device copies are the other stream's, too."""
+    N, H, E = 512, 256, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    w = [torch.randn(E, a, b, generator=g, device="cuda").mul_(0.05).bfloat16()
+         for a, b in ((384, H), (384, H), (H, 384))]
+    layer = moe.MoELayer(moe.Shape(N, H, E, 2, 1, 384), *w)
+    logits, x, res = (torch.randn(N, n, generator=g, device="cuda") for n in (E, H, H))
+    x, res = x.bfloat16(), res.bfloat16()
+    want = layer.forward(logits, x, res).cpu()
+    host = [t.cpu().pin_memory() for t in (logits, x, res)]
+    out = torch.empty(N, H, dtype=torch.bfloat16).pin_memory()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    junk = [torch.empty_like(t, device="cuda") for t in host]
+    torch.cuda._sleep(40_000_000)
+    for t in junk:
+        t.zero_()
+    del junk, t
+    layer.forward_host(*host, out, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+    layer.forward_host(*host, out.zero_(), stream=side)
+    junk = [torch.zeros_like(t, device="cuda") for t in host]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and all((t == 0).all() for t in junk)
