@@ -13,11 +13,11 @@
 // multiplies small singular values by 3.4445, and what a rounding has put in their place with
 // them, so X in its own place in the sum, p0 X, is kept in two fp16 halves (22 bits; the second one
 // times 2^11): rounded to one, a gradient of rank 16 over noise would end 3.8e-2 of its norm from
-// the 64-bit result (bf16 operands and X: 0.3).  And S, near the end some -2.7 I and little beside it, goes apart: its
-// diagonal d, fp32, to p0, the rest into the product, whose roundings are then those of the
-// little.  Together 4e-4 to 1.5e-3 of the result's norm (with S whole up to 2.2e-3); the output's
-// own rounding to bf16 is 1.7e-3.  The largest are gradients of rank 1: 264 x 264 1.5e-3, 8192 x 8192
-// 1.2e-3 (2.0e-3 with an unscaled second half, which is a denormal there).
+// the 64-bit result (bf16 operands and X: 0.3).  And S, near the end some -2.7 I and little beside
+// it, goes apart: its diagonal d, fp32, to p0, the rest into the product, whose roundings are then
+// those of the little.  Together 4e-4 to 1.5e-3 of the result's norm (with S whole up to 2.2e-3);
+// the output's own rounding to bf16 is 1.7e-3.  The largest are gradients of rank 1: 264 x 264
+// 1.5e-3, 8192 x 8192 1.2e-3 (2.0e-3 with an unscaled second half, which is a denormal there).
 //
 // Three products a step, on 256 x 256 tiles of a CTA pair (tcgen05, two accumulators in TMEM, 5
 // stages of 32 KB).  G and S are symmetric: only tiles on and above the diagonal are made, each

@@ -743,7 +743,8 @@ __global__ void __launch_bounds__(kBlock)
 }
 
 // Once for each set of weights, so neither of these is made fast: w4_quantize_kernel reads and
-// writes 2.3 TB/s, this one 0.4 TB/s (single bytes of rows); 256 matrices of 4096 x 7168 8.3 and 19 ms.
+// writes 2.3 TB/s, this one 0.4 TB/s (single bytes of rows); 256 matrices of 4096 x 7168 take 8.3
+// and 19 ms.
 // 16 bytes of the packed form a thread: 32 weights of a row (bytes' nibbles r and r + 4 of a
 // word are neighbours), or 8 scales.  Rows and columns
 // that the matrix does not have are weights of zero (nibble 8, scale 0).
@@ -812,7 +813,7 @@ __global__ void __launch_bounds__(kBlock)
 //   all the same     62, 72     64, 72     95, 78     95, 78     97, 80     95, 80
 //   at random        68, 76     76, 78     89, 78     93, 80     96, 82     97, 82
 //   uneven           72, 83     76, 87     81, 89     85, 91     89, 91     97, 93
-// (uneven: shares of 1 / sqrt(i)).  8 of 14336 x 4096 and 64 of 2048 x 2 x 1408, gated: the same.
+// (uneven: shares of 1 / sqrt(i)).  8 of 14336 x 4096 and 64 of 2048 x 2 x 1408, gated: alike.
 int pass_rows(long long R, int E) {
     const long long used = R < E ? R : E;
     const double mean = used > 0 ? (double)R / (double)used : 0.0;

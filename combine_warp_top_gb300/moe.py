@@ -1066,9 +1066,10 @@ class MoELayer:
         run the layer on that copy (the layer's shape becomes "packed"); the
         results are bit-identical, the weight stream faster.  w4: run the routed
         experts on 4-bit weights (moe_w4_gated_gemm, moe_w4_gemm), made for decoding
-        steps (from some hundred rows an expert on, bf16 weights are faster): a group size (32, 64 or 128) to quantise the given row-major weights
-        with, or the (gate and up, down) W4Matrices themselves (the weight arguments
-        None); the layer's shape is row-major then."""
+        steps (from some hundred rows an expert on, bf16 weights are faster): a group
+        size (32, 64 or 128) to quantise the given row-major weights with, or the (gate
+        and up, down) W4Matrices themselves (the weight arguments None); the layer's shape
+        is row-major then."""
         if w4 is not None:
             if fuse_combine or shape.gemm == "fused" or shape.weights != "row_major":
                 raise ValueError("4-bit experts run their own two products on row-major shapes")

@@ -9,9 +9,9 @@
  * the same from run to run on one GPU model.
  * The kernels are launched with programmatic stream serialization: their blocks
  * may start before the kernel before them on the stream has ended, and wait for
- * its end (griddepcontrol.wait) before they touch memory.  Those of moe_muon_update let the next
- * such kernel on the stream, the caller's own too, start while they still compute: that wait, or a
- * launch without the attribute, is what orders memory.
+ * its end (griddepcontrol.wait) before they touch memory.  Those of moe_muon_update
+ * let the next such kernel on the stream, the caller's own too, start while they
+ * still compute: that wait, or a launch without the attribute, is what orders memory.
  */
 #ifndef MOE_TRAIN_H
 #define MOE_TRAIN_H

@@ -17,8 +17,8 @@ extern "C" {
 
 /* Matrices of 4-bit weights: weight k of row o is scale[o, k / group] * (q[o, k] - 8), q in
  * 0..15, the scales bf16.  group: 32, 64 or 128, of which C_in is a multiple; C_out is a
- * multiple of 8; both are at most 2^28.  gated: the stacked gate and up matrices [2 * C_out, C_in], gate rows first;
- * else [C_out, C_in]. */
+ * multiple of 8; both are at most 2^28.  gated: the stacked gate and up matrices
+ * [2 * C_out, C_in], gate rows first; else [C_out, C_in]. */
 typedef struct {
     int32_t C_out, C_in;
     int32_t group;
